@@ -7,6 +7,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "decode.h"
 #include "gemm.h"
 #include "kernels.h"
 
@@ -83,6 +84,15 @@ int check_ptrs(std::initializer_list<const void*> req, std::initializer_list<con
   return MOE_OK;
 }
 
+// The same for calls without a workspace.
+int check_arrays(std::initializer_list<const void*> req) {
+  for (const void* p : req) {
+    if (!p) return MOE_ERR_ARG;
+    if (!al16(p)) return MOE_ERR_ALIGN;
+  }
+  return MOE_OK;
+}
+
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
 #define MOE_TRY(expr)             \
@@ -142,6 +152,24 @@ int route_tables(const moe_cfg& c, const WsLayout& L, void* ws, const float* log
   MOE_TRY_CUDA(launch_route(logits, c.T, c.E, c.k, c.renorm, topk_idx, topk_w, hist, L.nb_route, err, s));
   return build_tables(c, L, ws, topk_idx, counts, offsets, dest, row_token, row_slot, s);
 }
+
+// Limits of the calls for a few tokens.
+int check_decode_cfg(const moe_cfg* c) {
+  MOE_TRY(check_cfg(c));
+  return c->T <= MOE_DECODE_MAX_T ? MOE_OK : MOE_ERR_SHAPE;
+}
+int check_linear(int T, int n, int K) {
+  if (T < 1 || T > MOE_DECODE_MAX_T || n < 1 || n >= 0x7FFFFF00 || K < 64 || K % 64) return MOE_ERR_SHAPE;
+  return MOE_OK;
+}
+bool q4_group_ok(int group, int cols) {
+  return (group == 32 || group == 64 || group == 128) && cols > 0 && cols % group == 0;
+}
+int check_q4_mats(int mats, int rows, int cols, int group) {
+  if (mats < 1 || rows < 1 || rows >= 0x7FFFFF00 || !q4_group_ok(group, cols)) return MOE_ERR_SHAPE;
+  return MOE_OK;
+}
+bool y_type_ok(int y_type) { return y_type == MOE_Y_F32 || y_type == MOE_Y_BF16; }
 
 int fwd_gemms(const moe_cfg& c, const WsLayout& L, void* ws, const uint16_t* Xp, const uint16_t* x,
               const int32_t* offsets, const int32_t* row_slot, const float* topk_w, const uint16_t* W1,
@@ -505,6 +533,80 @@ int moe_layer_bwd(const moe_cfg* cfg, const uint16_t* dy, const float* logits, c
     MOE_TRY(launch_gemm(kDW13, a, s, persistent_grid()));
     MOE_TRY(launch_gemm(kDW2, a, s, persistent_grid()));
   }
+  return MOE_OK;
+}
+
+size_t moe_decode_workspace_bytes(const moe_cfg* cfg) {
+  return check_decode_cfg(cfg) == MOE_OK ? decode_workspace_bytes(*cfg) : 0;
+}
+
+int moe_decode_ws_init(const moe_cfg* cfg, void* ws, void* stream) {
+  MOE_TRY(check_decode_cfg(cfg));
+  MOE_TRY(check_ptrs({}, {}, ws));
+  return decode_ws_init(ws, static_cast<cudaStream_t>(stream));
+}
+
+int moe_decode_fwd(const moe_cfg* cfg, const float* logits, const uint16_t* x, const uint16_t* W1, const uint16_t* W3,
+                   const uint16_t* W2, void* y, int y_type, int32_t* topk_idx, float* topk_w, void* ws, void* stream) {
+  MOE_TRY(check_decode_cfg(cfg));
+  if (!y_type_ok(y_type)) return MOE_ERR_ARG;
+  MOE_TRY(check_ptrs({logits, x, W1, W3, W2, y, topk_idx, topk_w}, {}, ws));
+  const DecodeArgs a{*cfg, 0, logits, x, {W1, nullptr}, {W3, nullptr}, {W2, nullptr}, y, y_type, topk_idx, topk_w, ws};
+  return launch_decode(a, static_cast<cudaStream_t>(stream));
+}
+
+int moe_decode_q4_fwd(const moe_cfg* cfg, int group, const float* logits, const uint16_t* x, const uint8_t* W1q,
+                      const uint16_t* W1s, const uint8_t* W3q, const uint16_t* W3s, const uint8_t* W2q,
+                      const uint16_t* W2s, void* y, int y_type, int32_t* topk_idx, float* topk_w, void* ws,
+                      void* stream) {
+  MOE_TRY(check_decode_cfg(cfg));
+  if (!q4_group_ok(group, cfg->d_model) || !q4_group_ok(group, cfg->d_ff)) return MOE_ERR_SHAPE;
+  if (!y_type_ok(y_type)) return MOE_ERR_ARG;
+  MOE_TRY(check_ptrs({logits, x, W1q, W1s, W3q, W3s, W2q, W2s, y, topk_idx, topk_w}, {}, ws));
+  const DecodeArgs a{*cfg, group, logits, x, {W1q, W1s}, {W3q, W3s}, {W2q, W2s}, y, y_type, topk_idx, topk_w, ws};
+  return launch_decode(a, static_cast<cudaStream_t>(stream));
+}
+
+size_t moe_linear_workspace_bytes(int T, int n, int K) {
+  return check_linear(T, n, K) == MOE_OK ? linear_workspace_bytes(T, n, K) : 0;
+}
+
+int moe_linear_ws_init(int T, int n, int K, void* ws, void* stream) {
+  MOE_TRY(check_linear(T, n, K));
+  MOE_TRY(check_ptrs({}, {}, ws));
+  return decode_ws_init(ws, static_cast<cudaStream_t>(stream));
+}
+
+int moe_linear_fwd(int T, int n, int K, const uint16_t* x, const uint16_t* W, void* y, int y_type, void* ws,
+                   void* stream) {
+  MOE_TRY(check_linear(T, n, K));
+  if (!y_type_ok(y_type)) return MOE_ERR_ARG;
+  MOE_TRY(check_ptrs({x, W, y}, {}, ws));
+  return launch_linear(LinearArgs{T, n, K, 0, x, {W, nullptr}, y, y_type, ws}, static_cast<cudaStream_t>(stream));
+}
+
+int moe_linear_q4_fwd(int T, int n, int K, int group, const uint16_t* x, const uint8_t* Wq, const uint16_t* Ws,
+                      void* y, int y_type, void* ws, void* stream) {
+  MOE_TRY(check_linear(T, n, K));
+  if (!q4_group_ok(group, K)) return MOE_ERR_SHAPE;
+  if (!y_type_ok(y_type)) return MOE_ERR_ARG;
+  MOE_TRY(check_ptrs({x, Wq, Ws, y}, {}, ws));
+  return launch_linear(LinearArgs{T, n, K, group, x, {Wq, Ws}, y, y_type, ws}, static_cast<cudaStream_t>(stream));
+}
+
+int moe_q4_quantize(const uint16_t* W, uint8_t* codes, uint16_t* scales, int mats, int rows, int cols, int group,
+                    void* stream) {
+  MOE_TRY(check_q4_mats(mats, rows, cols, group));
+  MOE_TRY(check_arrays({W, codes, scales}));
+  MOE_TRY_CUDA(launch_q4_quantize(W, codes, scales, mats, rows, cols, group, static_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+int moe_q4_dequantize(const uint8_t* codes, const uint16_t* scales, uint16_t* W, int mats, int rows, int cols,
+                      int group, void* stream) {
+  MOE_TRY(check_q4_mats(mats, rows, cols, group));
+  MOE_TRY(check_arrays({W, codes, scales}));
+  MOE_TRY_CUDA(launch_q4_dequantize(codes, scales, W, mats, rows, cols, group, static_cast<cudaStream_t>(stream)));
   return MOE_OK;
 }
 

@@ -47,6 +47,11 @@ cudaError_t launch_dw_reduce(const float* partial, const int32_t* dest, int R, i
                              cudaStream_t s);
 cudaError_t launch_route_bwd(const float* logits, const int32_t* topk_idx, const float* topk_w, const float* dw,
                              int T, int E, int k, int renorm, float* dlogits, int* err, cudaStream_t s);
+// bf16 matrices [mats][rows][cols] to 4-bit codes and group scales (q4.cuh), and back.
+cudaError_t launch_q4_quantize(const uint16_t* W, uint8_t* codes, uint16_t* scales, int mats, int rows, int cols,
+                               int group, cudaStream_t s);
+cudaError_t launch_q4_dequantize(const uint8_t* codes, const uint16_t* scales, uint16_t* W, int mats, int rows,
+                                 int cols, int group, cudaStream_t s);
 int num_sms();
 // Makes sure the modules of moe_dispatch's kernels (histogram, scan, scatter,
 // row gather) are loaded on the current device.

@@ -63,6 +63,16 @@ _SIGS = {
     "moe_dispatch_bwd": ([_CFG, _P, _P, _P, _P, _P], _I),
     "moe_route_bwd": ([_CFG, _P, _P, _P, _P, _P, _P, _P], _I),
     "moe_layer_bwd": ([_CFG] + [_P] * 14 + [_I, _P], _I),
+    "moe_decode_workspace_bytes": ([_CFG], ctypes.c_size_t),
+    "moe_decode_ws_init": ([_CFG, _P, _P], _I),
+    "moe_decode_fwd": ([_CFG] + [_P] * 6 + [_I] + [_P] * 4, _I),
+    "moe_decode_q4_fwd": ([_CFG, _I] + [_P] * 9 + [_I] + [_P] * 4, _I),
+    "moe_linear_workspace_bytes": ([_I] * 3, ctypes.c_size_t),
+    "moe_linear_ws_init": ([_I] * 3 + [_P, _P], _I),
+    "moe_linear_fwd": ([_I] * 3 + [_P] * 3 + [_I, _P, _P], _I),
+    "moe_linear_q4_fwd": ([_I] * 4 + [_P] * 4 + [_I, _P, _P], _I),
+    "moe_q4_quantize": ([_P] * 3 + [_I] * 4 + [_P], _I),
+    "moe_q4_dequantize": ([_P] * 3 + [_I] * 4 + [_P], _I),
     "moe_get_device_error": ([_P, _P, ctypes.POINTER(_I), ctypes.POINTER(_I)], _I),
     "moe_num_sms": ([], _I),
     "moe_set_grid_limit": ([_I], _I),
@@ -89,7 +99,7 @@ _SIGS = {
 TRACE_KINDS = ["route", "hist", "scan", "scatter", "gather", "gemm1_swiglu", "gemm2_scale", "combine",
                "combine_bwd", "gemm_dh", "dw_reduce", "route_bwd", "gemm_dx", "dispatch_bwd", "gemm_dw13",
                "gemm_dw2", "megakernel", "megakernel_bwd",
-               "route_tables", "bwd_gemms"]
+               "route_tables", "bwd_gemms", "decode", "linear", "q4"]
 
 _lib = None
 
@@ -215,6 +225,99 @@ def moe_layer_bwd(cfg, dy, logits, x, W1, W3, W2, topk_idx, topk_w, ws, dx, dlog
     _call("moe_layer_bwd", _cfg(cfg), _ptr(dy), _ptr(logits), _ptr(x), _ptr(W1), _ptr(W3), _ptr(W2),
           _ptr(topk_idx), _ptr(topk_w), _ptr(ws), _ptr(dx), _ptr(dlogits), _ptr(dW1), _ptr(dW3), _ptr(dW2),
           int(which), _stream(stream))
+
+
+# ------------------------------------------------- the layer for a few tokens
+MOE_DECODE_MAX_T = 64  # most tokens (rows of x) of these calls
+MOE_Y_F32, MOE_Y_BF16 = 0, 1
+_Y_TYPES = {torch.float32: MOE_Y_F32, torch.bfloat16: MOE_Y_BF16}
+
+
+def _y_type(y) -> int:
+    """Code of y's type; another type becomes one that the library refuses."""
+    return _Y_TYPES.get(y.dtype, -1)
+
+
+def moe_decode_workspace_bytes(cfg) -> int:
+    return int(lib().moe_decode_workspace_bytes(_cfg(cfg)))
+
+
+def moe_decode_ws_init(cfg, ws, stream=None):
+    _call("moe_decode_ws_init", _cfg(cfg), _ptr(ws), _stream(stream))
+
+
+def moe_decode_fwd(cfg, logits, x, W1, W3, W2, y, topk_idx, topk_w, ws, stream=None):
+    """Whole layer forward for T <= 64 tokens; y [T, d] fp32 or bf16."""
+    _call("moe_decode_fwd", _cfg(cfg), _ptr(logits), _ptr(x), _ptr(W1), _ptr(W3), _ptr(W2), _ptr(y), _y_type(y),
+          _ptr(topk_idx), _ptr(topk_w), _ptr(ws), _stream(stream))
+
+
+def moe_decode_q4_fwd(cfg, group, logits, x, W1q, W1s, W3q, W3s, W2q, W2s, y, topk_idx, topk_w, ws, stream=None):
+    """The same with 4-bit weights (codes [E+S, rows, cols/2] uint8, scales as q4_empty gives them)."""
+    _call("moe_decode_q4_fwd", _cfg(cfg), int(group), _ptr(logits), _ptr(x), _ptr(W1q), _ptr(W1s), _ptr(W3q),
+          _ptr(W3s), _ptr(W2q), _ptr(W2s), _ptr(y), _y_type(y), _ptr(topk_idx), _ptr(topk_w), _ptr(ws),
+          _stream(stream))
+
+
+def moe_linear_workspace_bytes(T, n, K) -> int:
+    return int(lib().moe_linear_workspace_bytes(int(T), int(n), int(K)))
+
+
+def moe_linear_ws_init(T, n, K, ws, stream=None):
+    _call("moe_linear_ws_init", int(T), int(n), int(K), _ptr(ws), _stream(stream))
+
+
+def _linear_shape(x, y):
+    """(T, n, K) of y [T, n] = x [T, K] . W^T."""
+    if x.dim() != 2 or y.dim() != 2 or x.shape[0] != y.shape[0]:
+        raise ValueError(f"x [T, K] and y [T, n] expected, got {tuple(x.shape)} and {tuple(y.shape)}")
+    return x.shape[0], y.shape[1], x.shape[1]
+
+
+def moe_linear_fwd(x, W, y, ws, stream=None):
+    """y [T, n] = x [T, K] . W [n, K]^T for T <= 64 rows; y fp32 or bf16."""
+    T, n, K = _linear_shape(x, y)
+    if W.numel() != n * K:
+        raise ValueError(f"W of {n} x {K} weights expected, got {tuple(W.shape)}")
+    _call("moe_linear_fwd", T, n, K, _ptr(x), _ptr(W), _ptr(y), _y_type(y), _ptr(ws), _stream(stream))
+
+
+def moe_linear_q4_fwd(x, Wq, Ws, group, y, ws, stream=None):
+    """The same with a 4-bit W (codes Wq, scales Ws, groups of `group` columns)."""
+    T, n, K = _linear_shape(x, y)
+    _q4_check(Wq, Ws, 1, n, K, group)
+    _call("moe_linear_q4_fwd", T, n, K, int(group), _ptr(x), _ptr(Wq), _ptr(Ws), _ptr(y), _y_type(y), _ptr(ws),
+          _stream(stream))
+
+
+def _q4_check(codes, scales, mats, rows, cols, group):
+    want = mats * rows * cols // 2, mats * (cols // max(1, group)) * (-(-rows // 8) * 8)
+    if (codes.numel(), scales.numel()) != want:
+        raise ValueError(f"{want[0]} bytes of codes and {want[1]} scales expected, got {codes.numel()} and "
+                         f"{scales.numel()}")
+
+
+def q4_empty(mats, rows, cols, group, device="cuda"):
+    """Uninitialised 4-bit arrays of `mats` matrices [rows, cols]: codes [mats, rows, cols/2] uint8 and scales
+    [mats, cols/group, rows rounded up to 8] bf16."""
+    return (torch.empty(mats, rows, cols // 2, dtype=torch.uint8, device=device),
+            torch.empty(mats, cols // group, -(-rows // 8) * 8, dtype=torch.bfloat16, device=device))
+
+
+def moe_q4_quantize(W, codes, scales, group, stream=None):
+    """W [mats, rows, cols] (or [rows, cols]) bf16 -> 4-bit codes and scales of groups of `group` columns."""
+    rows, cols = W.shape[-2:]
+    mats = W.shape[0] if W.dim() == 3 else 1
+    _q4_check(codes, scales, mats, rows, cols, group)
+    _call("moe_q4_quantize", _ptr(W), _ptr(codes), _ptr(scales), mats, rows, cols, int(group), _stream(stream))
+
+
+def moe_q4_dequantize(codes, scales, W, group, stream=None):
+    """The bf16 values W [mats, rows, cols] (or [rows, cols]) that codes and scales stand for."""
+    rows, cols = W.shape[-2:]
+    mats = W.shape[0] if W.dim() == 3 else 1
+    _q4_check(codes, scales, mats, rows, cols, group)
+    _call("moe_q4_dequantize", _ptr(codes), _ptr(scales), _ptr(W), mats, rows, cols, int(group), _stream(stream))
 
 
 def moe_get_device_error(ws, stream=None):
@@ -399,4 +502,24 @@ def ws_view(ws: torch.Tensor, cfg: MoEConfig, name: str) -> torch.Tensor:
 def alloc_workspace(cfg: MoEConfig, device="cuda", stream=None) -> torch.Tensor:
     ws = torch.empty(moe_workspace_bytes(cfg), dtype=torch.uint8, device=device)
     moe_ws_init(cfg, ws, stream)
+    return ws
+
+
+def alloc_decode_workspace(cfg, device="cuda", stream=None) -> torch.Tensor:
+    """Workspace of moe_decode_fwd and moe_decode_q4_fwd, ready for use."""
+    n = moe_decode_workspace_bytes(cfg)
+    if n == 0:
+        raise MoeError("moe_decode_workspace_bytes", MOE_ERR_SHAPE)
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    moe_decode_ws_init(cfg, ws, stream)
+    return ws
+
+
+def alloc_linear_workspace(T, n, K, device="cuda", stream=None) -> torch.Tensor:
+    """Workspace of moe_linear_fwd and moe_linear_q4_fwd, ready for use."""
+    nbytes = moe_linear_workspace_bytes(T, n, K)
+    if nbytes == 0:
+        raise MoeError("moe_linear_workspace_bytes", MOE_ERR_SHAPE)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    moe_linear_ws_init(T, n, K, ws, stream)
     return ws

@@ -294,6 +294,80 @@ int moe_layer_bwd(const moe_cfg* cfg, const uint16_t* dy, const float* logits,
                   void* ws, float* dx, float* dlogits, float* dW1, float* dW3,
                   float* dW2, int which, void* stream);
 
+/* ------------------------------------------------- the layer for a few tokens
+ * Forward of the same layer for the tokens of one generation step, where the
+ * weights' bytes are all that counts: no activations are kept for a backward
+ * and the weights may be held in 4 bits.
+ *
+ * 4-bit weights: a matrix [rows, cols] is W[r, c] = s[c / G, r] * (q[r, c] - 8)
+ * with codes q in 0..15 and one bf16 scale s per group of G = 32, 64 or 128
+ * columns of a row.
+ *   codes  uint8 [rows, cols / 2]: the eight columns 8j..8j+7 share four bytes
+ *          (one little-endian 32-bit word); columns 8j+0, +2, +4, +6 are its
+ *          nibbles 0..3 (lowest first) and columns 8j+1, +3, +5, +7 its
+ *          nibbles 4..7.
+ *   scales bf16 [cols / G, pitch], pitch = rows rounded up to a multiple of 8.
+ * Several matrices of one shape follow each other in both arrays. */
+enum { MOE_Y_F32 = 0, MOE_Y_BF16 = 1 }; /* type of y */
+#define MOE_DECODE_MAX_T 64             /* most tokens (rows of x) of these calls */
+
+/* Workspace of moe_decode_fwd and moe_decode_q4_fwd (0 if cfg is outside their
+ * limits: those of moe_cfg and T <= MOE_DECODE_MAX_T).  Clear it once
+ * with moe_decode_ws_init; the calls leave its counters at 0.  Calls sharing a workspace must not run
+ * concurrently. */
+size_t moe_decode_workspace_bytes(const moe_cfg* cfg);
+int moe_decode_ws_init(const moe_cfg* cfg, void* ws, void* stream);
+
+/* Whole layer forward for T <= MOE_DECODE_MAX_T tokens: the router of moe_route
+ * (the same topk_idx and topk_w bits), then with e = topk_idx[t, j]
+ *   h[t, j] = topk_w[t, j] * silu(x_t . W1_e^T) * (x_t . W3_e^T)
+ *   y[t]    = sum_j h[t, j] . W2_e^T + sum_s h[t, s] . W2_(E+s)^T
+ * (shared experts with weight 1).  Layouts as moe_layer_fwd.  All sums are
+ * fp32; h enters the second product as the sum of two bf16 values (16
+ * significant bits); y [T, d] is rounded once to y_type.  Only the weights of
+ * experts that some token picked (and of the shared experts) are read.  A
+ * non-finite logit sets MOE_ERR_NONFINITE, as in moe_route, and leaves that
+ * token's outputs unspecified.  Bitwise reproducible.  Pointers 16-byte
+ * aligned, ws 256-byte. */
+int moe_decode_fwd(const moe_cfg* cfg, const float* logits, const uint16_t* x, const uint16_t* W1,
+                   const uint16_t* W3, const uint16_t* W2, void* y, int y_type, int32_t* topk_idx,
+                   float* topk_w, void* ws, void* stream);
+
+/* The same with 4-bit weights: W1q/W1s, W3q/W3s [E+S] matrices [f, d], W2q/W2s
+ * [E+S] matrices [d, f]; d_model and d_ff multiples of `group` (32, 64 or 128;
+ * MOE_ERR_SHAPE otherwise).  Codes multiply the bf16 activations exactly and
+ * each group's fp32 sum is scaled in fp32: no weight is rounded. */
+int moe_decode_q4_fwd(const moe_cfg* cfg, int group, const float* logits, const uint16_t* x,
+                      const uint8_t* W1q, const uint16_t* W1s, const uint8_t* W3q, const uint16_t* W3s,
+                      const uint8_t* W2q, const uint16_t* W2s, void* y, int y_type, int32_t* topk_idx,
+                      float* topk_w, void* ws, void* stream);
+
+/* y [T, n] = x [T, K] . W [n, K]^T for T <= MOE_DECODE_MAX_T rows (the gate
+ * projection that gives the layer's logits; dense layers beside it): bf16 x
+ * and W, fp32 sums, y fp32 or bf16.  Limits (MOE_ERR_SHAPE): T, n >= 1, K a
+ * positive multiple of 64, n < 2^31 - 256.  Workspace:
+ * moe_linear_workspace_bytes (0 outside the limits), cleared once with
+ * moe_linear_ws_init. */
+size_t moe_linear_workspace_bytes(int T, int n, int K);
+int moe_linear_ws_init(int T, int n, int K, void* ws, void* stream);
+int moe_linear_fwd(int T, int n, int K, const uint16_t* x, const uint16_t* W, void* y, int y_type,
+                   void* ws, void* stream);
+/* The same with a 4-bit W (K a multiple of `group` too). */
+int moe_linear_q4_fwd(int T, int n, int K, int group, const uint16_t* x, const uint8_t* Wq,
+                      const uint16_t* Ws, void* y, int y_type, void* ws, void* stream);
+
+/* bf16 matrices W [mats, rows, cols] to 4 bits: s = bf16(absmax / 7) of the
+ * group, q = 8 + rint(w / s) held to -8..7 (8 where s is 0 or not finite: a
+ * group that holds a NaN or an Inf comes back as NaN).  Scales of the padding
+ * rows are written as 0.  cols a positive multiple of group (32, 64 or 128),
+ * mats, rows >= 1, rows < 2^31 - 256. */
+int moe_q4_quantize(const uint16_t* W, uint8_t* codes, uint16_t* scales, int mats, int rows, int cols,
+                    int group, void* stream);
+/* And back: W = bf16(s * (q - 8)), one rounding (moe_layer_fwd on prompts then
+ * runs on the values, up to that rounding, that the 4-bit calls use). */
+int moe_q4_dequantize(const uint8_t* codes, const uint16_t* scales, uint16_t* W, int mats, int rows, int cols,
+                      int group, void* stream);
+
 /* Reads the device error word of `ws` into *code (MOE_OK or a negative
  * MOE_ERR_*) and *info (a code-specific detail, e.g. the token of a
  * non-finite logit or the task of a timed-out wait).  Synchronises
@@ -489,7 +563,10 @@ enum {
   MOE_K_MEGAKERNEL_BWD = 17, /* backward (input-gradient) MegaKernel */
   MOE_K_ROUTE_TABLES = 18, /* router + histogram + scan + scatter, one launch */
   MOE_K_BWD_GEMMS = 19,   /* dX, dW1/dW3 and dW2 interleaved in one launch */
-  MOE_K_COUNT = 20
+  MOE_K_DECODE = 20,      /* layer for a few tokens */
+  MOE_K_LINEAR = 21,      /* linear layer for a few tokens */
+  MOE_K_Q4 = 22,          /* to and from 4-bit weights */
+  MOE_K_COUNT = 23
 };
 /* Testing aid for failure detection (no device fault involved): the forward
  * MegaKernel claims task `ticket` but never runs or signals it, so the
