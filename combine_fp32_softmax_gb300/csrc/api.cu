@@ -551,7 +551,8 @@ int moe_decode_fwd(const moe_cfg* cfg, const float* logits, const uint16_t* x, c
   MOE_TRY(check_decode_cfg(cfg));
   if (!y_type_ok(y_type)) return MOE_ERR_ARG;
   MOE_TRY(check_ptrs({logits, x, W1, W3, W2, y, topk_idx, topk_w}, {}, ws));
-  const DecodeArgs a{*cfg, 0, logits, x, {W1, nullptr}, {W3, nullptr}, {W2, nullptr}, y, y_type, topk_idx, topk_w, ws};
+  const DecodeArgs a{*cfg, 0, logits, x, {W1, nullptr}, {W3, nullptr}, {W2, nullptr}, y, y_type, topk_idx, topk_w, ws,
+                     g_grid_limit};
   return launch_decode(a, static_cast<cudaStream_t>(stream));
 }
 
@@ -563,12 +564,13 @@ int moe_decode_q4_fwd(const moe_cfg* cfg, int group, const float* logits, const 
   if (!q4_group_ok(group, cfg->d_model) || !q4_group_ok(group, cfg->d_ff)) return MOE_ERR_SHAPE;
   if (!y_type_ok(y_type)) return MOE_ERR_ARG;
   MOE_TRY(check_ptrs({logits, x, W1q, W1s, W3q, W3s, W2q, W2s, y, topk_idx, topk_w}, {}, ws));
-  const DecodeArgs a{*cfg, group, logits, x, {W1q, W1s}, {W3q, W3s}, {W2q, W2s}, y, y_type, topk_idx, topk_w, ws};
+  const DecodeArgs a{*cfg, group, logits, x, {W1q, W1s}, {W3q, W3s}, {W2q, W2s}, y, y_type, topk_idx, topk_w, ws,
+                     g_grid_limit};
   return launch_decode(a, static_cast<cudaStream_t>(stream));
 }
 
 size_t moe_linear_workspace_bytes(int T, int n, int K) {
-  return check_linear(T, n, K) == MOE_OK ? linear_workspace_bytes(T, n, K) : 0;
+  return check_linear(T, n, K) == MOE_OK ? linear_workspace_bytes() : 0;
 }
 
 int moe_linear_ws_init(int T, int n, int K, void* ws, void* stream) {
@@ -582,7 +584,8 @@ int moe_linear_fwd(int T, int n, int K, const uint16_t* x, const uint16_t* W, vo
   MOE_TRY(check_linear(T, n, K));
   if (!y_type_ok(y_type)) return MOE_ERR_ARG;
   MOE_TRY(check_ptrs({x, W, y}, {}, ws));
-  return launch_linear(LinearArgs{T, n, K, 0, x, {W, nullptr}, y, y_type, ws}, static_cast<cudaStream_t>(stream));
+  return launch_linear(LinearArgs{T, n, K, 0, x, {W, nullptr}, y, y_type, ws, g_grid_limit},
+                       static_cast<cudaStream_t>(stream));
 }
 
 int moe_linear_q4_fwd(int T, int n, int K, int group, const uint16_t* x, const uint8_t* Wq, const uint16_t* Ws,
@@ -591,7 +594,8 @@ int moe_linear_q4_fwd(int T, int n, int K, int group, const uint16_t* x, const u
   if (!q4_group_ok(group, K)) return MOE_ERR_SHAPE;
   if (!y_type_ok(y_type)) return MOE_ERR_ARG;
   MOE_TRY(check_ptrs({x, Wq, Ws, y}, {}, ws));
-  return launch_linear(LinearArgs{T, n, K, group, x, {Wq, Ws}, y, y_type, ws}, static_cast<cudaStream_t>(stream));
+  return launch_linear(LinearArgs{T, n, K, group, x, {Wq, Ws}, y, y_type, ws, g_grid_limit},
+                       static_cast<cudaStream_t>(stream));
 }
 
 int moe_q4_quantize(const uint16_t* W, uint8_t* codes, uint16_t* scales, int mats, int rows, int cols, int group,

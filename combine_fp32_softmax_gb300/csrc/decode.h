@@ -26,6 +26,7 @@ struct DecodeArgs {
   int32_t* topk_idx;
   float* topk_w;
   void* ws;
+  int grid_limit;  // most CTAs, 0: no limit
 };
 
 struct LinearArgs {
@@ -35,10 +36,11 @@ struct LinearArgs {
   void* y;
   int y_type;
   void* ws;
+  int grid_limit;
 };
 
 size_t decode_workspace_bytes(const moe_cfg& c);
-size_t linear_workspace_bytes(int T, int n, int K);
+size_t linear_workspace_bytes();
 // Clears the error word and the counters of either workspace.
 int decode_ws_init(void* ws, cudaStream_t s);
 int launch_decode(const DecodeArgs& a, cudaStream_t s);

@@ -53,6 +53,7 @@
 #include "gemm.h"
 #include "kernels.h"
 #include "ptx.cuh"
+#include "tensor_map.h"
 #include "trace.h"
 
 namespace moe {
@@ -1179,42 +1180,6 @@ __device__ __forceinline__ void epilogue_drain(SharedState& ss, const EpiState& 
 }
 
 // ------------------------------------------------------------------ host
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  if (!fn) {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(ptr);
-  }
-  return fn;
-}
-
-// Row-major matrix [outer, inner] of bf16 (esize 2) or fp32 (esize 4) seen
-// as 2D boxes of box_outer rows x box_inner elements; out-of-range reads
-// fill zeros and out-of-range parts of a stored box are skipped.
-bool map2d_any(CUtensorMap* m, const void* base, int esize, uint64_t inner, uint64_t outer, uint32_t box_inner,
-               uint32_t box_outer, CUtensorMapSwizzle swz) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn || !base || inner == 0 || outer == 0) return false;
-  const cuuint64_t dims[2] = {inner, outer};
-  const cuuint64_t strides[1] = {inner * esize};
-  const cuuint32_t box[2] = {box_inner, box_outer};
-  const cuuint32_t estr[2] = {1, 1};
-  const CUtensorMapDataType dt = esize == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
-  return fn(m, dt, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-// Operand tiles: bf16, 64-element (128-byte) swizzled rows.
-bool map2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint32_t box_inner, uint32_t box_outer) {
-  return map2d_any(m, base, 2, inner, outer, box_inner, box_outer, CU_TENSOR_MAP_SWIZZLE_128B);
-}
 // MN-major operand tiles: a row-major bf16 matrix [rows, cols] (cols a
 // multiple of 64) seen as 3D {64 columns of a chunk, row, chunk} (strides
 // cols*2 and 128 bytes).  A box {64, 64 rows, chunks} lands in shared memory
