@@ -13,20 +13,24 @@
 //     W2 while the hidden values of this and other CTAs are still being made:
 //     the grid-wide dependency between the two products costs no bandwidth.
 //   - A second producer warp brings the activation columns of the same tiles
-//     (one bulk copy per row, gathered by the row's token) and is the one
+//     (16-byte asynchronous copies, rows gathered by token) and is the one
 //     that waits for the hidden values of all CTAs before the second product.
+//     One bulk copy per row instead took 1300 clocks a stage at 32 rows, twice
+//     what the weights of the stage need.
 //   - The tiles of all picked experts form one sequence of K blocks, cut into
 //     equal contiguous ranges, one per SM, so no SM idles whatever the number
-//     of experts, rows and tokens.  A tile cut by a range border is summed
-//     from per-range parts in range order by whichever warp finishes last:
-//     fixed order, no floating-point atomics.
-//   - Eight consumer warps multiply: weights are the 16-row operand of
+//     of experts, rows and tokens.  A tile cut by a range border belongs to
+//     the range it begins in.  The ranges it goes on in work on it first and
+//     leave their sums in the workspace; its owner comes to it last, long
+//     after, and adds them in range order: no floating-point atomics, and
+//     nobody waits in the middle of a range.
+//   - Sixteen consumer warps multiply: weights are the 16-row operand of
 //     mma.sync.m16n8k16, activations its 8 columns, so one token wastes
 //     tensor throughput that nothing else needs, and no shared-memory copy of
 //     converted 4-bit weights is made: codes become bf16 pairs in the
 //     registers that feed the instruction.  The warp-level instruction has
 //     the rate for it: a weight fragment arrives every 21 clocks per SM
-//     (bf16).  Each warp takes 16 rows of either box (W1 and W3 rows of the
+//     (bf16).  Each warp takes 8 rows of either box (W1 and W3 rows of the
 //     same hidden columns, so silu(a) * b stays in a thread) and one half of
 //     the stage's columns.
 #include <cuda_runtime.h>
@@ -46,14 +50,14 @@ namespace moe {
 
 namespace {
 
-constexpr int kMmaWarps = 8;             // 4 row groups x 2 halves of a stage's columns
-constexpr int kWeightWarp = kMmaWarps;   // producer of weight tiles
+constexpr int kRowGroups = 8;            // 8 rows of either box each
+constexpr int kMmaWarps = 2 * kRowGroups;   // row groups x halves of a stage's columns
+constexpr int kWeightWarp = kMmaWarps;      // producer of weight tiles
 constexpr int kColumnWarp = kMmaWarps + 1;  // producer of activation columns
-constexpr int kThreads = (kMmaWarps + 2) * 32;
-constexpr int kRowGroups = 4;
+constexpr int kWarps = kMmaWarps + 2;
+constexpr int kThreads = kWarps * 32;
 constexpr int kBoxRows = 64;             // rows of one weight box
 constexpr int kBoxBytes = kBoxRows * 128;
-constexpr int kMaxCols = 32;             // activation rows (MMA columns) of one tile
 constexpr int kMaxStages = 12;
 constexpr int kMaxTokens = MOE_DECODE_MAX_T;
 constexpr int kMaxPicks = kMaxTokens * 8;
@@ -64,7 +68,7 @@ constexpr int kMaxActive = 256 + 4;
 constexpr int kMaxWorkers = 256;
 
 // Counters in the error region (ints), all 0 between launches.
-constexpr int kCtrHidden = 8;   // consumer warps (upper half of the columns aside) done with the first product
+constexpr int kCtrHidden = 8;   // finishing warps (one per row group) done with the first product
 constexpr int kCtrOut = 9;      // ... with the second
 constexpr int kCtrExit = 10;    // CTAs done
 
@@ -76,6 +80,10 @@ struct Geo {
   static constexpr bool Q4 = G != 0;
   static constexpr int KB = Q4 ? 256 : 64;
   static constexpr int PITCH = Q4 ? 512 + 64 : 128 + 16;
+  // Activation rows (MMA columns) of a tile.  An expert with more has its
+  // weight tiles visited again, from L2.  32 rows of 512 bytes in several
+  // parts would leave no room for a ring.
+  static constexpr int COLS = Q4 ? 16 : 32;
   static constexpr int GROUPS = Q4 ? KB / (Q4 ? G : 1) : 0;   // scale rows of a stage
   static constexpr int SCALE_BYTES = GROUPS * kBoxRows * 2;   // of one box
 };
@@ -94,17 +102,19 @@ struct StreamParams {
   const uint16_t* x;
   int32_t* topk_idx;
   float* topk_w;
-  uint16_t* h;          // [2][Rs][f]: upper and lower bf16 part
+  uint16_t* h;          // [parts][Rs][f]
   float* o;             // [Rs][d]
-  float* part;          // parts of tiles cut by a range border: [workers][2][4 row groups][32][32]
-  int* arrive;          // [2][workers][4]
+  float* part;          // sums of the tile that a range begins in: [workers][row groups][16][32]
+  int* arrive;          // parts there, by the owning range: [2][workers][row groups]
   void* y;
   int* err;             // error word and counters
-  int y_type, workers, stages, stage_bytes, cols8, xbuf_bytes;  // cols8: activation rows of a stage, per part
+  int y_type, workers, stages, stage_bytes, xbuf_bytes;
+  int cols8, parts;     // activation rows of a stage; bf16 parts of a hidden value
 };
 
 struct alignas(16) Shared {
   uint64_t full_w[kMaxStages], full_x[kMaxStages], empty[kMaxStages];
+  uint64_t xfull[kRowGroups], xfree[kRowGroups];  // exchange of the column halves
   int abort;
   int nact, nblk;                  // work list entries, column blocks of 32 rows in all
   int e[kMaxActive];               // expert
@@ -130,9 +140,13 @@ constexpr int kSharedBytes = (sizeof(Shared) + 127) / 128 * 128;
 template <int EPL>
 __device__ __forceinline__ void route_tokens(const StreamParams& p, Shared& ss) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int t = warp; t < p.T; t += kThreads / 32) {
+  float ahead[EPL];  // the next token's logits
+  if (warp < p.T) row_load<EPL>(p.logits + static_cast<size_t>(warp) * p.E, p.E, lane, ahead);
+  for (int t = warp; t < p.T; t += kWarps) {
     RowSoftmax<EPL> r;
-    row_load<EPL>(p.logits + static_cast<size_t>(t) * p.E, p.E, lane, r.v);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) r.v[i] = ahead[i];
+    if (t + kWarps < p.T) row_load<EPL>(p.logits + static_cast<size_t>(t + kWarps) * p.E, p.E, lane, ahead);
     int idx;
     float w;
     route_token<EPL>(r, t, p.E, p.k, p.renorm, lane, p.err, idx, w);
@@ -148,6 +162,7 @@ __device__ __forceinline__ void route_tokens(const StreamParams& p, Shared& ss) 
   }
 }
 
+template <int COLS>
 __device__ void build_work_list(const StreamParams& p, Shared& ss) {
   const int tid = threadIdx.x, lane = tid & 31;
   for (int i = tid; i < 512; i += kThreads) (&ss.mask[0][0])[i] = 0;
@@ -170,7 +185,7 @@ __device__ void build_work_list(const StreamParams& p, Shared& ss) {
       n[j] = e < p.E ? __popc(ss.mask[e][0]) + __popc(ss.mask[e][1]) : 0;
       na += n[j] > 0;
       nr += n[j];
-      nb += (n[j] + kMaxCols - 1) / kMaxCols;
+      nb += (n[j] + COLS - 1) / COLS;
     }
     int ia = na, ir = nr, ib = nb;
 #pragma unroll
@@ -190,9 +205,9 @@ __device__ void build_work_list(const StreamParams& p, Shared& ss) {
       ss.blk0[ia] = ib;
       ++ia;
       ir += n[j];
-      ib += (n[j] + kMaxCols - 1) / kMaxCols;
+      ib += (n[j] + COLS - 1) / COLS;
     }
-    const int per = (p.T + kMaxCols - 1) / kMaxCols;
+    const int per = (p.T + COLS - 1) / COLS;
     if (lane < p.S) {
       ss.e[all_a + lane] = p.E + lane;
       ss.m[all_a + lane] = p.T;
@@ -243,24 +258,35 @@ struct Walk {
   const Product& pr;
   const Shared& ss;
   int workers, v;
-  long long units, u, u1;
+  int units, u, u1;
   int item, kb, a;
 
-  __device__ Walk(const Product& product, const Shared& shared, int nworkers)
-      : pr(product), ss(shared), workers(nworkers), v(static_cast<int>(blockIdx.x) - static_cast<int>(gridDim.x)) {
-    units = static_cast<long long>(ss.nblk) * pr.row_tiles * pr.kblocks;
-    workers = static_cast<int>(min(static_cast<long long>(workers), units));  // no range is empty
+  // A CTA takes the ranges blockIdx.x + i * gridDim.x in descending order:
+  // the owner of a cut tile waits for ranges after its own, so on a capped
+  // grid those come first.
+  __device__ Walk(const Product& product, const Shared& shared, int most) : pr(product), ss(shared) {
+    units = ss.nblk * pr.row_tiles * pr.kblocks;
+    workers = min(most, units);  // no range is empty
+    const int b = static_cast<int>(blockIdx.x), n = static_cast<int>(gridDim.x);
+    v = b < workers ? b + ((workers - 1 - b) / n + 1) * n : 0;
     u = u1 = 0;
     item = kb = a = 0;
   }
+  __device__ int begin_of(int worker) const {
+    return static_cast<int>(static_cast<long long>(units) * worker / workers);
+  }
+  // The range that holds K block `unit`.
+  __device__ int worker_of(int unit) const {
+    return static_cast<int>((static_cast<long long>(unit + 1) * workers - 1) / units);
+  }
   __device__ bool next(Segment& s) {
-    while (u >= u1) {
-      v += gridDim.x;
-      if (v >= workers) return false;
-      u = units * v / workers;
-      u1 = units * (v + 1) / workers;
-      item = static_cast<int>(u / pr.kblocks);
-      kb = static_cast<int>(u - static_cast<long long>(item) * pr.kblocks);
+    if (u >= u1) {
+      v -= static_cast<int>(gridDim.x);
+      if (v < 0) return false;
+      u = begin_of(v);
+      u1 = begin_of(v + 1);
+      item = u / pr.kblocks;
+      kb = u - item * pr.kblocks;
       int lo = 0, hi = ss.nact - 1;   // last entry with blk0 * row_tiles <= item
       while (lo < hi) {
         const int mid = (lo + hi + 1) / 2;
@@ -276,7 +302,7 @@ struct Walk {
     s.worker = v;
     s.item = item;
     s.kb0 = kb;
-    s.kb1 = static_cast<int>(min(static_cast<long long>(pr.kblocks), kb + (u1 - u)));
+    s.kb1 = min(pr.kblocks, kb + (u1 - u));
     s.a = a;
     s.rt = r / nblk;
     s.nb = r - s.rt * nblk;
@@ -285,8 +311,6 @@ struct Walk {
     ++item;
     return true;
   }
-  // The range that holds K block u.
-  __device__ int worker_of(long long unit) const { return static_cast<int>(((unit + 1) * workers - 1) / units); }
 };
 
 struct Ring {
@@ -307,8 +331,8 @@ __device__ bool drain_wait(uint64_t* bar, uint32_t parity) {
     if (globaltimer_ns() - t0 > kWaitLimitNs) return false;
   return true;
 }
-// After an abort: lets the copies that this producer issued land before the
-// CTA may leave its shared memory.
+// Lets the copies that this producer issued land before the CTA may leave
+// its shared memory (after an abort nobody else waits for them).
 struct Drain {
   uint32_t filled = 0, parity = 0;
   __device__ __forceinline__ void note(int stage, uint32_t phase) {
@@ -367,36 +391,44 @@ __device__ bool produce_weights(const StreamParams& p, int which, Shared& ss, ui
   return true;
 }
 
-// Columns: the rows of x by token (hidden, linear) or of h's two parts.
+// Columns: the rows of x by token (hidden, linear) or the parts of h.  16
+// bytes a lane; a lane's arrival on the stage's barrier follows its copies.
 template <int G, bool LAYER>
-__device__ bool produce_columns(const StreamParams& p, int which, Shared& ss, uint8_t* ring, Ring& rg, Drain& dr,
+__device__ bool produce_columns(const StreamParams& p, int which, Shared& ss, uint8_t* ring, Ring& rg,
                                 volatile int* abort) {
   using Ge = Geo<G>;
+  constexpr int LANES = Ge::KB / 8;         // lanes of a row
+  constexpr int ROWS = 32 / LANES;          // rows of an instruction
   const Product& pr = p.p[which];
   const int lane = threadIdx.x & 31;
   const bool hidden_in = LAYER && which == 1;
-  const size_t Rs = static_cast<size_t>(p.T) * (p.k + p.S);
+  const uint16_t* base = hidden_in ? p.h : p.x;
+  const int parts = hidden_in ? p.parts : 1;
+  const size_t part_step = static_cast<size_t>(p.T) * (p.k + p.S) * p.f;
+  const int col = (lane % LANES) * 8;
   Walk walk(pr, ss, p.workers);
   Segment s;
   while (walk.next(s)) {
-    const int m = min(kMaxCols, ss.m[s.a] - s.nb * kMaxCols);
-    const int r = ss.row0[s.a] + s.nb * kMaxCols + lane;
-    const uint16_t* src = nullptr;
-    if (lane < m) src = hidden_in ? p.h + static_cast<size_t>(r) * p.f : p.x + static_cast<size_t>(ss.row_token[r]) * pr.K;
+    const int m = min(Ge::COLS, ss.m[s.a] - s.nb * Ge::COLS);
+    const int r = ss.row0[s.a] + s.nb * Ge::COLS;
+    int mine = 0;  // row of `base` that this lane keeps for the warp
+    if (lane < m) mine = hidden_in ? r + lane : ss.row_token[r + lane];
     for (int kb = s.kb0; kb < s.kb1; ++kb) {
       const bool ok = mbar_wait(&ss.empty[rg.stage], rg.phase ^ 1, abort, p.err, (0x22 << 24) | which);
       if (!__all_sync(kFull, ok)) return false;
       uint64_t* bar = &ss.full_x[rg.stage];
-      const uint32_t bytes = min(Ge::KB, pr.K - kb * Ge::KB) * 2;
-      if (lane == 0) mbar_arrive_expect_tx(bar, bytes * m * (hidden_in ? 2 : 1));
-      dr.note(rg.stage, rg.phase);
-      __syncwarp();
-      if (lane < m) {
-        uint8_t* dst = ring + static_cast<size_t>(rg.stage) * p.stage_bytes + 2 * (kBoxBytes + Ge::SCALE_BYTES) +
-                       lane * Ge::PITCH;
-        bulk_load(dst, src + kb * Ge::KB, bytes, bar);
-        if (hidden_in) bulk_load(dst + p.cols8 * Ge::PITCH, src + Rs * p.f + kb * Ge::KB, bytes, bar);
+      const uint32_t dst = smem_u32(ring) + static_cast<uint32_t>(rg.stage) * p.stage_bytes +
+                           2 * (kBoxBytes + Ge::SCALE_BYTES) + (lane / LANES) * Ge::PITCH + col * 2;
+      const bool in = kb * Ge::KB + col < pr.K;
+      for (int i = 0; i < m; i += ROWS) {
+        const int at = i + lane / LANES;
+        const int row = __shfl_sync(kFull, mine, at & 31);
+        const uint16_t* src = base + static_cast<size_t>(row) * pr.K + kb * Ge::KB + col;
+        if (in && at < m)
+          for (int q = 0; q < parts; ++q)
+            cp_async16(dst + (q * p.cols8 + i) * Ge::PITCH, src + q * part_step);
       }
+      cp_async_arrive(bar);
       rg.step(p.stages);
     }
   }
@@ -404,117 +436,103 @@ __device__ bool produce_columns(const StreamParams& p, int which, Shared& ss, ui
 }
 
 // --------------------------------------------------------------- consumers
-// The hidden values enter the second product in two bf16 parts, 16
-// significant bits: one part would cost 2^-9 of each, more than all the fp32
-// sums together, and the tensor instructions of a second one are free beside
-// the weights' bytes.  The lower part is held times 2^8, so that it leaves
+// The hidden values enter the second product in bf16 parts that add up to
+// them: two (16 significant bits) for a bf16 y, three (24) for an fp32 y.
+// One part alone would cost 2^-9 of each value, as much as the rounding of a
+// bf16 y, and the tensor instructions of more parts are free beside the
+// weights' bytes.  The lower parts are held times 2^8, so that they leave
 // bf16's range no sooner than the upper one does.
 constexpr float kLowScale = 256.f;
 
-template <int PARTS, int NT>
-__device__ __forceinline__ float join_parts(const float (&s)[PARTS][2][NT][4], int box, int n, int i) {
-  if constexpr (PARTS == 2)
-    return fmaf(s[1][box][n][i], 1.f / kLowScale, s[0][box][n][i]);
+// Sums of the upper part, and of the lower ones together.
+template <int PARTS>
+constexpr int kSums = PARTS > 1 ? 2 : 1;
+
+template <int SUMS, int NT>
+__device__ __forceinline__ float join_parts(const float (&s)[SUMS][NT][4], int n, int i) {
+  if constexpr (SUMS == 2)
+    return fmaf(s[1][n][i], 1.f / kLowScale, s[0][n][i]);
   else
-    return s[0][box][n][i];
+    return s[0][n][i];
 }
 
-// One stage, this warp's 2 x 16 rows and half of the columns:
-// acc[box][n][..] += weights . columns.  Sums of a stage (bf16) or of a group
-// (4 bits) start from zero in the tensor core and are added to acc in fp32,
-// so the chain of additions inside the tensor core, which truncates, is short.
+// One stage, this warp's 8 rows of either box and half of the columns:
+// acc[n][..] += weights . columns.  The 16-row operand holds the first box's
+// rows on top and the second box's below.  Sums of a stage (bf16) or of a
+// group (4 bits) start from zero in the tensor core and are added to acc in
+// fp32, so the chain of additions inside the tensor core, which truncates, is
+// short.
 template <int G, int NT, int PARTS>
-__device__ __forceinline__ void multiply_stage(uint32_t st, int part_bytes, int kleft, int m, float (&acc)[2][NT][4]) {
+__device__ __forceinline__ void multiply_stage(uint32_t st, int part_bytes, int kleft, int m, float (&acc)[NT][4]) {
   using Ge = Geo<G>;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rgrp = warp & 3, half = warp >> 2;
+  const int rgrp = warp % kRowGroups, half = warp / kRowGroups;
   const uint32_t cols = st + 2 * (kBoxBytes + Ge::SCALE_BYTES);
-  // weight fragments: matrices (rows 0-7, 16 bytes c), (rows 8-15, c), (rows 0-7, c + 1), (rows 8-15, c + 1)
-  const uint32_t arow = st + (rgrp * 16 + ((lane >> 3) & 1) * 8 + (lane & 7)) * 128;
-  auto frag = [&](int box, int c, uint32_t (&a)[4]) {
-    ldmatrix_x4(arow + box * kBoxBytes + ((static_cast<uint32_t>(c + (lane >> 4)) ^ (lane & 7)) << 4), a);
+  // matrices (box 0, 16 bytes c), (box 1, c), (box 0, c + 1), (box 1, c + 1)
+  const uint32_t arow = st + ((lane >> 3) & 1) * kBoxBytes + (rgrp * 8 + (lane & 7)) * 128;
+  auto frag = [&](int c, uint32_t (&a)[4]) {
+    ldmatrix_x4(arow + ((static_cast<uint32_t>(c + (lane >> 4)) ^ (lane & 7)) << 4), a);
   };
   if constexpr (!Ge::Q4) {
-    float s[PARTS][2][NT][4] = {};
-    uint32_t a[2][2][4];
+    float s[kSums<PARTS>][NT][4] = {};
+    uint32_t a[2][4];
 #pragma unroll
-    for (int box = 0; box < 2; ++box)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) frag(box, half * 4 + 2 * i, a[box][i]);
+    for (int i = 0; i < 2; ++i) frag(half * 4 + 2 * i, a[i]);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int q = 0; q < PARTS; ++q) {
         uint32_t b[4];  // four matrices: 16 bytes c .. c + 3 of the 8 activation rows
         ldmatrix_x4(cols + q * part_bytes + (n * 8 + (lane & 7)) * Ge::PITCH + (half * 4 + (lane >> 3)) * 16, b);
-#pragma unroll
-        for (int box = 0; box < 2; ++box) {
-          mma_bf16(s[q][box][n], a[box][0][0], a[box][0][1], a[box][0][2], a[box][0][3], b[0], b[1]);
-          mma_bf16(s[q][box][n], a[box][1][0], a[box][1][1], a[box][1][2], a[box][1][3], b[2], b[3]);
-        }
+        mma_bf16(s[q > 0][n], a[0][0], a[0][1], a[0][2], a[0][3], b[0], b[1]);
+        mma_bf16(s[q > 0][n], a[1][0], a[1][1], a[1][2], a[1][3], b[2], b[3]);
       }
 #pragma unroll
-    for (int box = 0; box < 2; ++box)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[box][n][i] += join_parts<PARTS>(s, box, n, i);
+      for (int i = 0; i < 4; ++i) acc[n][i] += join_parts(s, n, i);
   } else {
     const int g = lane >> 2, t = lane & 3;
-    const uint32_t scales = st + 2 * kBoxBytes + (rgrp * 16 + g) * 2;
-    constexpr int SPAN = G < 64 ? 1 : 2;             // 32-column chunks that share a sum
+    const uint32_t scales = st + 2 * kBoxBytes + (rgrp * 8 + g) * 2;
     constexpr int CHUNKS = 4;                        // 32-column chunks of this warp's half
-    float s[PARTS][2][NT][4];
+    float s[kSums<PARTS>][NT][4];
 #pragma unroll
     for (int c2 = 0; c2 < CHUNKS; c2 += 2) {
       if (half * 128 + c2 * 32 >= kleft) break;      // columns past K (a multiple of 64)
-      uint32_t w[2][4];
-#pragma unroll
-      for (int box = 0; box < 2; ++box) frag(box, half * 4 + c2, w[box]);
+      uint32_t w[4];
+      frag(half * 4 + c2, w);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {                  // chunk c2 + i
         const int c = half * 4 + c2 + i;
-        if (i % SPAN == 0 && !(G == 128 && c2 != 0))
+        const bool group_begins = G == 32 || (i == 0 && (G == 64 || c2 == 0));
+        const bool group_ends = G == 32 || (i == 1 && (G == 64 || c2 == 2));
+        if (group_begins)
 #pragma unroll
-          for (int j = 0; j < PARTS * 2 * NT * 4; ++j) (&s[0][0][0][0])[j] = 0.f;
-        uint32_t a[2][8];                            // rows g and g + 8, pairs 0..3
+          for (int j = 0; j < kSums<PARTS> * NT * 4; ++j) (&s[0][0][0])[j] = 0.f;
+        uint32_t a[8];                               // pairs 0..3 of either box's row
 #pragma unroll
-        for (int box = 0; box < 2; ++box)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            a[box][2 * j] = q4_pair(w[box][2 * i], j);
-            a[box][2 * j + 1] = q4_pair(w[box][2 * i + 1], j);
-          }
+        for (int j = 0; j < 4; ++j) {
+          a[2 * j] = q4_pair(w[2 * i], j);
+          a[2 * j + 1] = q4_pair(w[2 * i + 1], j);
+        }
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int q = 0; q < PARTS; ++q) {
             uint32_t b[4] = {0, 0, 0, 0};
             if (n * 8 + g < m) lds128(cols + q * part_bytes + (n * 8 + g) * Ge::PITCH + c * 64 + t * 16, b);
-#pragma unroll
-            for (int box = 0; box < 2; ++box) {
-              mma_bf16(s[q][box][n], a[box][0], a[box][1], a[box][2], a[box][3], b[0], b[1]);
-              mma_bf16(s[q][box][n], a[box][4], a[box][5], a[box][6], a[box][7], b[2], b[3]);
-            }
+            mma_bf16(s[q > 0][n], a[0], a[1], a[2], a[3], b[0], b[1]);
+            mma_bf16(s[q > 0][n], a[4], a[5], a[6], a[7], b[2], b[3]);
           }
-        const bool group_ends = G == 32 || (G == 64 && i == 1) ||
-                                (G == 128 && i == 1 && (c2 == 2 || half * 128 + 64 >= kleft));
         if (group_ends) {
           const uint32_t sc = scales + (c * 32 / G) * (kBoxRows * 2);
+          const float f0 = lds_bf16(sc), f1 = lds_bf16(sc + Ge::SCALE_BYTES);
 #pragma unroll
-          for (int box = 0; box < 2; ++box) {
-            uint16_t lo, hi;
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(lo) : "r"(sc + box * Ge::SCALE_BYTES) : "memory");
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(hi) : "r"(sc + box * Ge::SCALE_BYTES + 16) : "memory");
-            const float f0 = __uint_as_float(static_cast<uint32_t>(lo) << 16);
-            const float f1 = __uint_as_float(static_cast<uint32_t>(hi) << 16);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              acc[box][n][0] = fmaf(f0, join_parts<PARTS>(s, box, n, 0), acc[box][n][0]);
-              acc[box][n][1] = fmaf(f0, join_parts<PARTS>(s, box, n, 1), acc[box][n][1]);
-              acc[box][n][2] = fmaf(f1, join_parts<PARTS>(s, box, n, 2), acc[box][n][2]);
-              acc[box][n][3] = fmaf(f1, join_parts<PARTS>(s, box, n, 3), acc[box][n][3]);
-            }
+          for (int n = 0; n < NT; ++n) {
+            acc[n][0] = fmaf(f0, join_parts(s, n, 0), acc[n][0]);
+            acc[n][1] = fmaf(f0, join_parts(s, n, 1), acc[n][1]);
+            acc[n][2] = fmaf(f1, join_parts(s, n, 2), acc[n][2]);
+            acc[n][3] = fmaf(f1, join_parts(s, n, 3), acc[n][3]);
           }
         }
       }
@@ -529,40 +547,41 @@ __device__ __forceinline__ void store_y(void* y, int y_type, size_t at, float v)
     static_cast<float*>(y)[at] = v;
 }
 
-// A finished tile's values, one thread's share: rows g and g + 8 of either
-// box, columns 2t and 2t + 1 of every 8.
-template <bool LAYER, int NT>
+// A finished tile's values, one thread's share: row g of either box, columns
+// 2t and 2t + 1 of every 8.
+template <int G, bool LAYER, int NT>
 __device__ __forceinline__ void finish_tile(const StreamParams& p, int which, const Shared& ss, const Segment& s,
-                                            const float (&acc)[2][NT][4]) {
-  const int lane = threadIdx.x & 31, rgrp = (threadIdx.x >> 5) & 3;
-  const int g = lane >> 2, t2 = (lane & 3) * 2;
-  const int m = min(kMaxCols, ss.m[s.a] - s.nb * kMaxCols), r0 = ss.row0[s.a] + s.nb * kMaxCols;
-  const size_t Rs = static_cast<size_t>(p.T) * (p.k + p.S);
+                                            const float (&acc)[NT][4]) {
+  const int lane = threadIdx.x & 31, rgrp = (threadIdx.x >> 5) % kRowGroups;
+  const int row = rgrp * 8 + (lane >> 2), t2 = (lane & 3) * 2;
+  const int m = min(Geo<G>::COLS, ss.m[s.a] - s.nb * Geo<G>::COLS), r0 = ss.row0[s.a] + s.nb * Geo<G>::COLS;
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int col = n * 8 + t2 + (i & 1), row = rgrp * 16 + g + (i >> 1) * 8;
+    for (int i = 0; i < 2; ++i) {
+      const int col = n * 8 + t2 + i;
       if (col >= m) continue;
       const int r = r0 + col;
       if (LAYER && which == 0) {
-        const float a = acc[0][n][i], b = acc[1][n][i];
+        const float a = acc[n][i], b = acc[n][2 + i];
         const float h = ss.row_w[r] * (a / (1.f + expf(-a)) * b);
-        // a value that rounds to infinity keeps that alone
-        const __nv_bfloat16 hi = __float2bfloat16_rn(h);
-        const float rest = (h - __bfloat162float(hi)) * kLowScale;
-        const __nv_bfloat16 lo = __float2bfloat16_rn(isfinite(rest) ? rest : 0.f);
-        const size_t at = static_cast<size_t>(r) * p.f + s.rt * kBoxRows + row;
-        p.h[at] = __bfloat16_as_ushort(hi);
-        p.h[Rs * p.f + at] = __bfloat16_as_ushort(lo);
+        const size_t part_step = static_cast<size_t>(p.T) * (p.k + p.S) * p.f;
+        uint16_t* to = p.h + static_cast<size_t>(r) * p.f + s.rt * kBoxRows + row;
+        float rest = h;
+        for (int q = 0; q < p.parts; ++q) {
+          const __nv_bfloat16 v = __float2bfloat16_rn(rest);
+          to[q * part_step] = __bfloat16_as_ushort(v);
+          rest = (rest - __bfloat162float(v)) * (q == 0 ? kLowScale : 1.f);
+          if (!isfinite(rest)) rest = 0.f;  // a value that rounds to infinity keeps that alone
+        }
       } else {
 #pragma unroll
         for (int box = 0; box < 2; ++box) {
           const int c = s.rt * 2 * kBoxRows + box * kBoxRows + row;
           if (LAYER) {
-            if (c < p.d) p.o[static_cast<size_t>(r) * p.d + c] = acc[box][n][i];
+            if (c < p.d) p.o[static_cast<size_t>(r) * p.d + c] = acc[n][2 * box + i];
           } else {
-            if (c < p.n) store_y(p.y, p.y_type, static_cast<size_t>(r) * p.n + c, acc[box][n][i]);
+            if (c < p.n) store_y(p.y, p.y_type, static_cast<size_t>(r) * p.n + c, acc[n][2 * box + i]);
           }
         }
       }
@@ -571,99 +590,98 @@ __device__ __forceinline__ void finish_tile(const StreamParams& p, int which, co
 
 struct Consumer {
   Ring rg;
-  bool ok = true;
-  bool shared_once = false;   // the exchange buffer was used before
+  uint32_t xphase = 0;  // exchange of the column halves
 };
 
 // Sums this warp's share of a segment and, on the lower column half's warp,
-// finishes the tile or leaves its part for the warp that does.
+// finishes the tile or leaves its part for the range that does.  False after
+// a wait that gave up.
 template <int G, bool LAYER, int NT, int PARTS>
-__device__ void consume_segment(const StreamParams& p, int which, Shared& ss, uint8_t* ring, float* xbuf, const Walk& walk,
+__device__ bool consume_segment(const StreamParams& p, int which, Shared& ss, uint8_t* ring, float* xbuf, const Walk& walk,
                                 const Segment& s, Consumer& cs, volatile int* abort) {
   using Ge = Geo<G>;
   const Product& pr = p.p[which];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rgrp = warp & 3, half = warp >> 2;
-  const int m = min(kMaxCols, ss.m[s.a] - s.nb * kMaxCols);
-  float acc[2][NT][4] = {};
+  const int rgrp = warp % kRowGroups, half = warp / kRowGroups;
+  const int m = min(Ge::COLS, ss.m[s.a] - s.nb * Ge::COLS);
+  constexpr int N = NT * 4;
+  float acc[NT][4] = {};
+  bool ok = true;
   for (int kb = s.kb0; kb < s.kb1; ++kb) {
-    // After an abort the walk goes on without waiting or reading, so that the
-    // named barriers below still meet.
-    if (cs.ok) {
-      const bool got = mbar_wait(&ss.full_w[cs.rg.stage], cs.rg.phase, abort, p.err, (0x23 << 24) | which) &&
-                       mbar_wait(&ss.full_x[cs.rg.stage], cs.rg.phase, abort, p.err, (0x24 << 24) | which);
-      cs.ok = __all_sync(kFull, got);
-    }
-    if (cs.ok) {
-      const uint32_t st = smem_u32(ring) + static_cast<uint32_t>(cs.rg.stage) * p.stage_bytes;
-      multiply_stage<G, NT, PARTS>(st, p.cols8 * Ge::PITCH, pr.K - kb * Ge::KB, m, acc);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ss.empty[cs.rg.stage]);
-    }
+    ok = mbar_wait(&ss.full_w[cs.rg.stage], cs.rg.phase, abort, p.err, (0x23 << 24) | which) &&
+         mbar_wait(&ss.full_x[cs.rg.stage], cs.rg.phase, abort, p.err, (0x24 << 24) | which);
+    if (!__all_sync(kFull, ok)) return false;
+    const uint32_t st = smem_u32(ring) + static_cast<uint32_t>(cs.rg.stage) * p.stage_bytes;
+    multiply_stage<G, NT, PARTS>(st, p.cols8 * Ge::PITCH, pr.K - kb * Ge::KB, m, acc);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ss.empty[cs.rg.stage]);
     cs.rg.step(p.stages);
   }
   // the two column halves
   float* xb = xbuf + rgrp * (p.xbuf_bytes / (kRowGroups * static_cast<int>(sizeof(float)))) + lane;
   if (half == 1) {
-    if (cs.shared_once) named_sync(5 + rgrp, 64);
-    cs.shared_once = true;
+    ok = mbar_wait(&ss.xfree[rgrp], cs.xphase ^ 1, abort, p.err, (0x27 << 24) | which);
+    cs.xphase ^= 1;
+    if (!__all_sync(kFull, ok)) return false;
 #pragma unroll
-    for (int i = 0; i < 2 * NT * 4; ++i) xb[i * 32] = (&acc[0][0][0])[i];
-    named_arrive(1 + rgrp, 64);
-    return;
-  }
-  named_sync(1 + rgrp, 64);
-#pragma unroll
-  for (int i = 0; i < 2 * NT * 4; ++i) (&acc[0][0][0])[i] += xb[i * 32];
-  named_arrive(5 + rgrp, 64);
-  if (!cs.ok) return;
-  if (s.kb0 != 0 || s.kb1 != pr.kblocks) {
-    // The ranges that hold K blocks of this tile; the first one's counter
-    // counts their parts.
-    const long long first = static_cast<long long>(s.item) * pr.kblocks;
-    const int v0 = walk.worker_of(first), v1 = walk.worker_of(first + pr.kblocks - 1);
-    constexpr int N = 2 * NT * 4;
-    auto slot = [&](int v, bool head) {  // a range's part: of the tile it begins in, or of the one it ends in
-      return p.part + ((static_cast<size_t>(v) * 2 + (head ? 0 : 1)) * kRowGroups + rgrp) * (32 * 32) + lane;
-    };
-    float* mine = slot(s.worker, s.kb0 != 0);
-#pragma unroll
-    for (int i = 0; i < N; ++i) __stcg(mine + i * 32, (&acc[0][0][0])[i]);
-    __threadfence();
+    for (int i = 0; i < N; ++i) xb[i * 32] = (&acc[0][0])[i];
     __syncwarp();
-    int* cnt = p.arrive + (static_cast<size_t>(which) * p.workers + v0) * kRowGroups + rgrp;
-    int last = 0;
+    if (lane == 0) mbar_arrive(&ss.xfull[rgrp]);
+    return true;
+  }
+  ok = mbar_wait(&ss.xfull[rgrp], cs.xphase, abort, p.err, (0x28 << 24) | which);
+  cs.xphase ^= 1;
+  if (!__all_sync(kFull, ok)) return false;
+#pragma unroll
+  for (int i = 0; i < N; ++i) (&acc[0][0])[i] += xb[i * 32];
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&ss.xfree[rgrp]);
+
+  const int first = s.item * pr.kblocks;
+  auto part = [&](int v) { return p.part + (static_cast<size_t>(v) * kRowGroups + rgrp) * (16 * 32) + lane; };
+  auto arrived = [&](int v) { return p.arrive + (static_cast<size_t>(which) * p.workers + v) * kRowGroups + rgrp; };
+  if (s.kb0 != 0) {  // the tile began in an earlier range
+    float* mine = part(s.worker);
+#pragma unroll
+    for (int i = 0; i < N; ++i) __stcg(mine + i * 32, (&acc[0][0])[i]);
+    __syncwarp();
+    if (lane == 0) red_release_gpu_add(arrived(walk.worker_of(first)), 1);
+    return true;
+  }
+  if (s.kb1 != pr.kblocks) {  // it goes on in later ranges, which began with it
+    const int v1 = walk.worker_of(first + pr.kblocks - 1);
+    int* cnt = arrived(s.worker);
     if (lane == 0) {
-      last = atomicAdd(cnt, 1) == v1 - v0;
-      if (last) *cnt = 0;
-      __threadfence();
+      ok = wait_count(cnt, v1 - s.worker, abort, p.err, (0x29 << 24) | which);
+      *cnt = 0;
     }
-    if (!__shfl_sync(kFull, last, 0)) return;
+    if (!__shfl_sync(kFull, ok, 0)) return false;
+    for (int v = s.worker + 1; v <= v1; ++v) {
+      const float* from = part(v);
 #pragma unroll
-    for (int i = 0; i < N; ++i) (&acc[0][0][0])[i] = 0.f;
-    for (int v = v0; v <= v1; ++v) {
-      const float* from = slot(v, v != v0);
-#pragma unroll
-      for (int i = 0; i < N; ++i) (&acc[0][0][0])[i] += __ldcg(from + i * 32);
+      for (int i = 0; i < N; ++i) (&acc[0][0])[i] += __ldcg(from + i * 32);
     }
   }
-  finish_tile<LAYER, NT>(p, which, ss, s, acc);
+  finish_tile<G, LAYER, NT>(p, which, ss, s, acc);
+  return true;
 }
 
 template <int G, bool LAYER, int PARTS>
-__device__ void consume(const StreamParams& p, int which, Shared& ss, uint8_t* ring, float* xbuf, Consumer& cs,
+__device__ bool consume(const StreamParams& p, int which, Shared& ss, uint8_t* ring, float* xbuf, Consumer& cs,
                         volatile int* abort) {
   Walk walk(p.p[which], ss, p.workers);
   Segment s;
-  while (walk.next(s)) {
-    const int m = min(kMaxCols, ss.m[s.a] - s.nb * kMaxCols);
+  bool ok = true;
+  while (ok && walk.next(s)) {
+    const int m = min(Geo<G>::COLS, ss.m[s.a] - s.nb * Geo<G>::COLS);
     if (m <= 8)
-      consume_segment<G, LAYER, 1, PARTS>(p, which, ss, ring, xbuf, walk, s, cs, abort);
+      ok = consume_segment<G, LAYER, 1, PARTS>(p, which, ss, ring, xbuf, walk, s, cs, abort);
     else if (m <= 16)
-      consume_segment<G, LAYER, 2, PARTS>(p, which, ss, ring, xbuf, walk, s, cs, abort);
-    else
-      consume_segment<G, LAYER, 4, PARTS>(p, which, ss, ring, xbuf, walk, s, cs, abort);
+      ok = consume_segment<G, LAYER, 2, PARTS>(p, which, ss, ring, xbuf, walk, s, cs, abort);
+    else if constexpr (Geo<G>::COLS > 16)
+      ok = consume_segment<G, LAYER, 4, PARTS>(p, which, ss, ring, xbuf, walk, s, cs, abort);
   }
+  return ok;
 }
 
 // y[t] = its slots' rows in slot order, then the shared experts', in fp32.
@@ -707,16 +725,20 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
   if (tid == 0) {
     for (int i = 0; i < p.stages; ++i) {
       mbar_init(&ss.full_w[i], 1);
-      mbar_init(&ss.full_x[i], 1);
+      mbar_init(&ss.full_x[i], 32);
       mbar_init(&ss.empty[i], kMmaWarps);
+    }
+    for (int i = 0; i < kRowGroups; ++i) {
+      mbar_init(&ss.xfull[i], 1);
+      mbar_init(&ss.xfree[i], 1);
     }
     ss.abort = 0;
     fence_mbar_init();
   }
   if (LAYER) {
-    build_work_list(p, ss);
+    build_work_list<Geo<G>::COLS>(p, ss);
   } else {
-    const int per = (p.T + kMaxCols - 1) / kMaxCols;
+    const int per = (p.T + Geo<G>::COLS - 1) / Geo<G>::COLS;
     if (tid < p.T) ss.row_token[tid] = static_cast<unsigned char>(tid);
     if (tid == 0) {
       ss.nact = 1;
@@ -737,50 +759,42 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
       Drain dr;
       bool ok = true;
       if (LAYER) ok = produce_weights<G>(p, 0, ss, ring, rg, dr, abort);
-      if (ok) ok = produce_weights<G>(p, 1, ss, ring, rg, dr, abort);
-      if (!ok) dr.wait(ss.full_w);
+      if (ok) produce_weights<G>(p, 1, ss, ring, rg, dr, abort);
+      dr.wait(ss.full_w);
     }
     __syncwarp();
   } else if (warp == kColumnWarp) {
     Ring rg;
-    Drain dr;
     bool ok = true;
     if (LAYER) {
-      ok = produce_columns<G, LAYER>(p, 0, ss, ring, rg, dr, abort);
+      ok = produce_columns<G, LAYER>(p, 0, ss, ring, rg, abort);
       if (ok) {  // every hidden value of every CTA
         if (lane == 0) ok = wait_count(p.err + kCtrHidden, arrivals, abort, p.err, 0x25 << 24);
         ok = __shfl_sync(kFull, ok, 0);
-        fence_proxy_async_global();
       }
     }
-    if (ok) ok = produce_columns<G, LAYER>(p, 1, ss, ring, rg, dr, abort);
-    if (!ok) dr.wait(ss.full_x);
+    if (ok) produce_columns<G, LAYER>(p, 1, ss, ring, rg, abort);
+    cp_async_wait_all();
   } else {
     Consumer cs;
+    bool ok;
     if (LAYER) {
-      consume<G, LAYER, 1>(p, 0, ss, ring, xbuf, cs, abort);
-      if (warp < kRowGroups) {  // publishes this warp's hidden values to other CTAs' bulk copies
-        fence_proxy_async_global();
-        __threadfence();
+      // Counted even after a wait that gave up, so that the counters come
+      // back to 0 and the other CTAs go on (the error word is set by then).
+      auto publish = [&](int counter) {
         __syncwarp();
-        if (lane == 0) red_release_gpu_add(p.err + kCtrHidden, 1);
-      }
-      consume<G, LAYER, 2>(p, 1, ss, ring, xbuf, cs, abort);
-      if (warp < kRowGroups) {
-        __threadfence();
-        __syncwarp();
-        if (lane == 0) red_release_gpu_add(p.err + kCtrOut, 1);
-      }
-      bool ok = true;
-      if (lane == 0) ok = wait_count(p.err + kCtrOut, arrivals, abort, p.err, 0x26 << 24);
-      if (__shfl_sync(kFull, ok, 0)) {
-        __threadfence();
-        sum_rows(p, ss);
-      }
+        if (warp < kRowGroups && lane == 0) red_release_gpu_add(p.err + counter, 1);
+      };
+      ok = consume<G, LAYER, 1>(p, 0, ss, ring, xbuf, cs, abort);
+      publish(kCtrHidden);
+      if (ok) ok = p.parts == 3 ? consume<G, LAYER, 3>(p, 1, ss, ring, xbuf, cs, abort)
+                                : consume<G, LAYER, 2>(p, 1, ss, ring, xbuf, cs, abort);
+      publish(kCtrOut);
+      if (lane == 0) ok = ok && wait_count(p.err + kCtrOut, arrivals, abort, p.err, 0x26 << 24);
+      if (__shfl_sync(kFull, ok, 0)) sum_rows(p, ss);
     } else {
       consume<G, LAYER, 1>(p, 1, ss, ring, xbuf, cs, abort);
     }
-    if (warp >= kRowGroups && cs.shared_once) named_sync(5 + (warp & 3), 64);  // the last arrival on it
   }
   if (LAYER) {  // the last CTA to pass its waits clears the counters
     __syncthreads();
@@ -810,8 +824,8 @@ Layout layout(size_t rows, size_t d, size_t f) {
     return at;
   };
   L.arrive = take(sizeof(int) * 2 * kMaxWorkers * kRowGroups);
-  L.part = take(sizeof(float) * kMaxWorkers * 2 * kRowGroups * 32 * 32);
-  L.h = take(2 * sizeof(uint16_t) * rows * f);
+  L.part = take(sizeof(float) * kMaxWorkers * kRowGroups * 16 * 32);
+  L.h = take(3 * sizeof(uint16_t) * rows * f);
   L.o = take(sizeof(float) * rows * d);
   L.total = o;
   return L;
@@ -854,10 +868,10 @@ constexpr int kSmemMax = 232448;  // 227 KB
 template <int G>
 size_t ring_shape(StreamParams& p, int parts) {
   using Ge = Geo<G>;
-  const int cols = std::min(p.T, kMaxCols);
+  const int cols = std::min(p.T, Ge::COLS);
   const int nt = cols <= 8 ? 1 : cols <= 16 ? 2 : 4;
   p.cols8 = nt * 8;  // rows that the widest tile's instructions read
-  p.xbuf_bytes = kRowGroups * 32 * 2 * nt * 4 * static_cast<int>(sizeof(float));
+  p.xbuf_bytes = kRowGroups * 32 * nt * 4 * static_cast<int>(sizeof(float));
   p.stage_bytes = static_cast<int>(align_up(2 * (kBoxBytes + Ge::SCALE_BYTES) + parts * p.cols8 * Ge::PITCH, 1024));
   const size_t fixed = kSharedBytes + p.xbuf_bytes + 1024;
   p.stages = std::min<int>(kMaxStages, static_cast<int>((kSmemMax - fixed) / p.stage_bytes));
@@ -882,7 +896,7 @@ int launch_stream(StreamParams& p, size_t smem, int grid_limit, cudaStream_t s) 
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = LAYER ? 1 : 0;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, stream_kernel<G, LAYER>, p) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -904,7 +918,8 @@ int decode_g(const DecodeArgs& a, cudaStream_t s) {
   p.part = reinterpret_cast<float*>(ws + L.part);
   p.arrive = reinterpret_cast<int*>(ws + L.arrive);
   p.y = a.y, p.y_type = a.y_type, p.err = reinterpret_cast<int*>(ws), p.workers = workers();
-  const size_t smem = ring_shape<G>(p, 2);
+  p.parts = a.y_type == MOE_Y_F32 ? 3 : 2;
+  const size_t smem = ring_shape<G>(p, p.parts);
   TraceScope trace_scope(MOE_K_DECODE, s);
   return launch_stream<G, true>(p, smem, a.grid_limit, s);
 }

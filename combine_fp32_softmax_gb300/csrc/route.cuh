@@ -99,7 +99,7 @@ __device__ __forceinline__ void route_token(RowSoftmax<EPL>& r, int t, int E, in
     if (lane == 0) record_error(err, MOE_ERR_NONFINITE_CODE, t);
     return;
   }
-  float psum = 0.f, my_p = 0.f;
+  float my_ex = 0.f;
   for (int j = 0; j < k; ++j) {
     // Best remaining entry of this lane: strictly greater keeps the lower
     // index on ties (entries are visited in increasing expert index).
@@ -117,20 +117,24 @@ __device__ __forceinline__ void route_token(RowSoftmax<EPL>& r, int t, int E, in
     const unsigned kbest = __reduce_max_sync(kFull, bk);
     const int bi = static_cast<int>(__reduce_min_sync(kFull, bk == kbest ? be : 0xffffffffu));
     const int owner = bi & 31, which = bi >> 5;
-    float p_local = 0.f;
+    float ex = 0.f;
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
-      if (lane == owner && i == which) {
-        key[i] = 0u;  // taken
-        p_local = r.ex[i] / r.s;
+      if (i == which) {
+        if (lane == owner) key[i] = 0u;  // taken
+        ex = r.ex[i];
       }
-    const float p = __shfl_sync(kFull, p_local, owner);
+    ex = __shfl_sync(kFull, ex, owner);
     if (lane == j) {
       my_idx = bi;
-      my_p = p;
+      my_ex = ex;
     }
-    psum += p;
   }
+  // one division per slot, all slots at once, outside the serial picks
+  const float my_p = my_ex / r.s;
+  float psum = 0.f;
+  if (renorm)
+    for (int j = 0; j < k; ++j) psum += __shfl_sync(kFull, my_p, j);
   my_w = renorm ? my_p / psum : my_p;
 }
 
