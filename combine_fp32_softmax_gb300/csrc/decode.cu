@@ -7,16 +7,25 @@
 // What bounds it: at 64 tokens the products need 8 flops per weight byte,
 // the tensor cores balance at 280, so the weights' bytes are the work.  The
 // kernel is built around keeping them coming:
-//   - A producer warp keeps a ring of shared-memory stages full of weight
-//     tiles (128 rows x 128 bytes, two TMA boxes of 64 rows), up to 200 KB in
-//     flight per SM.  It needs nothing but the routing, so it runs ahead into
-//     W2 while the hidden values of this and other CTAs are still being made:
+//   - A producer thread keeps a ring of shared-memory stages full of weight
+//     tiles (two TMA boxes of 128 rows x 128 bytes), 96 to 192 KB in flight
+//     per SM.  It needs nothing but the routing, so it runs ahead into W2
+//     while the hidden values of this and other CTAs are still being made:
 //     the grid-wide dependency between the two products costs no bandwidth.
-//   - A second producer warp brings the activation columns of the same tiles
-//     (16-byte asynchronous copies, rows gathered by token) and is the one
-//     that waits for the hidden values of all CTAs before the second product.
-//     One bulk copy per row instead took 1300 clocks a stage at 32 rows, twice
-//     what the weights of the stage need.
+//   - A second producer thread brings the activation rows of the same tiles
+//     and is the one that waits for the hidden values of all CTAs before the
+//     second product.  The first product multiplies every tile with all T
+//     tokens' rows of x, one box, and the epilogue picks the expert's: rows
+//     gathered one by one cost more time than the weights of their stage,
+//     while the tensor cores have the columns to spare.
+//   - tcgen05: the weights are the 128-row operand, the tokens its columns,
+//     so a handful of tokens costs the smallest instruction (N = 16).
+//     bf16 weights are read from the stage.  4-bit codes are turned into
+//     bf16 pairs by the warps that own the tile's rows, one thread a row, and
+//     go to tensor memory, from where the instruction takes them: written
+//     back to shared memory they would need four times the codes' bandwidth
+//     there, twice.  Each group of columns is summed from zero and scaled in
+//     fp32 on its way out, so no weight is rounded.
 //   - The tiles of all picked experts form one sequence of K blocks, cut into
 //     equal contiguous ranges, one per SM, so no SM idles whatever the number
 //     of experts, rows and tokens.  A tile cut by a range border belongs to
@@ -24,15 +33,6 @@
 //     leave their sums in the workspace; its owner comes to it last, long
 //     after, and adds them in range order: no floating-point atomics, and
 //     nobody waits in the middle of a range.
-//   - Sixteen consumer warps multiply: weights are the 16-row operand of
-//     mma.sync.m16n8k16, activations its 8 columns, so one token wastes
-//     tensor throughput that nothing else needs, and no shared-memory copy of
-//     converted 4-bit weights is made: codes become bf16 pairs in the
-//     registers that feed the instruction.  The warp-level instruction has
-//     the rate for it: a weight fragment arrives every 21 clocks per SM
-//     (bf16).  Each warp takes 8 rows of either box (W1 and W3 rows of the
-//     same hidden columns, so silu(a) * b stays in a thread) and one half of
-//     the stage's columns.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -50,15 +50,16 @@ namespace moe {
 
 namespace {
 
-constexpr int kRowGroups = 8;            // 8 rows of either box each
-constexpr int kMmaWarps = 2 * kRowGroups;   // row groups x halves of a stage's columns
-constexpr int kWeightWarp = kMmaWarps;      // producer of weight tiles
-constexpr int kColumnWarp = kMmaWarps + 1;  // producer of activation columns
-constexpr int kWarps = kMmaWarps + 2;
+constexpr int kRowWarps = 8;             // two sets of four: a set's warps cover the 128 rows of a tile
+constexpr int kWeightWarp = kRowWarps;   // producer of weight tiles
+constexpr int kColumnWarp = kRowWarps + 1;  // producer of activation rows
+constexpr int kMmaWarp = kRowWarps + 2;     // issues the tensor instructions, owns the tensor memory
+constexpr int kWarps = kRowWarps + 3;
 constexpr int kThreads = kWarps * 32;
-constexpr int kBoxRows = 64;             // rows of one weight box
-constexpr int kBoxBytes = kBoxRows * 128;
-constexpr int kMaxStages = 12;
+constexpr int kTileRows = 128;           // rows of one weight box: an accumulator's lanes
+constexpr int kBoxBytes = kTileRows * 128;
+constexpr int kTmemCols = 512;
+constexpr int kMaxStages = 8;
 constexpr int kMaxTokens = MOE_DECODE_MAX_T;
 constexpr int kMaxPicks = kMaxTokens * 8;
 constexpr int kMaxRows = kMaxTokens * 12;   // k <= 8 slots and 4 shared experts
@@ -68,30 +69,36 @@ constexpr int kMaxActive = 256 + 4;
 constexpr int kMaxWorkers = 256;
 
 // Counters in the error region (ints), all 0 between launches.
-constexpr int kCtrHidden = 8;   // finishing warps (one per row group) done with the first product
+constexpr int kCtrHidden = 8;   // row warps done with the first product
 constexpr int kCtrOut = 9;      // ... with the second
 constexpr int kCtrExit = 10;    // CTAs done
 
-// Columns of a stage and bytes between activation rows in it.  The padding
-// puts the 8 rows an instruction reads into different banks: ldmatrix reads
-// 16 bytes of each (bf16), 16-byte loads 64 bytes of two at a time (4 bits).
+// A stage: 128 bytes of 2 x 128 weight rows, the scales of those columns (4
+// bits) and the activation rows, 64 columns (128 bytes, swizzled) at a time.
+// G: columns of a scale group, 0 for bf16 weights.
 template <int G>
 struct Geo {
   static constexpr bool Q4 = G != 0;
-  static constexpr int KB = Q4 ? 256 : 64;
-  static constexpr int PITCH = Q4 ? 512 + 64 : 128 + 16;
-  // Activation rows (MMA columns) of a tile.  An expert with more has its
-  // weight tiles visited again, from L2.  32 rows of 512 bytes in several
-  // parts would leave no room for a ring.
-  static constexpr int COLS = Q4 ? 16 : 32;
-  static constexpr int GROUPS = Q4 ? KB / (Q4 ? G : 1) : 0;   // scale rows of a stage
-  static constexpr int SCALE_BYTES = GROUPS * kBoxRows * 2;   // of one box
+  static constexpr int KB = Q4 ? 256 : 64;                     // columns
+  static constexpr int ATOMS = KB / 64;
+  static constexpr int GROUPS = Q4 ? KB / (Q4 ? G : 1) : 0;    // scale rows
+  static constexpr int SCALE_BYTES = GROUPS * kTileRows * 2;   // of one box
+  static constexpr int WEIGHT_BYTES = 2 * (kBoxBytes + SCALE_BYTES);
+  // Tensor memory, 4 bits: two operand buffers of G / 2 words for either box,
+  // then two accumulators of each (one group each) of ACC columns.
+  [[maybe_unused]] static constexpr int A_COLS = G / 2;
+  [[maybe_unused]] static constexpr int ACC = (kTmemCols - 4 * A_COLS) / 4;
+  // Rows of h in one tile of the second product.  bf16 weights: all of them.
+  // 4 bits: what the accumulators hold; an expert with more rows has its
+  // weight tiles visited again, from L2.
+  __host__ __device__ static constexpr int h_rows(int parts) { return !Q4 ? 64 : parts == 2 ? 32 : 16; }
 };
 
 // One product of the launch: weight tiles of `row_step` output rows.
 struct Product {
-  CUtensorMap w0, w1;   // weight boxes: W1 and W3, or the two halves of a W2 tile
+  CUtensorMap w0, w1;   // weight boxes: W1 and W3, or (the same) the two halves of a W2 tile
   CUtensorMap s0, s1;   // their scales (4 bits)
+  CUtensorMap cols;     // activation rows
   int K, kblocks, rows, row_step, row_tiles;
 };
 
@@ -99,28 +106,35 @@ struct StreamParams {
   Product p[2];         // layer: hidden, out; linear form: the second only
   int T, d, f, E, k, S, renorm, n;
   const float* logits;
-  const uint16_t* x;
   int32_t* topk_idx;
   float* topk_w;
   uint16_t* h;          // [parts][Rs][f]
   float* o;             // [Rs][d]
-  float* part;          // sums of the tile that a range begins in: [workers][row groups][16][32]
-  int* arrive;          // parts there, by the owning range: [2][workers][row groups]
+  float* part;          // sums of the tile that a range begins in: [workers][2][64][128]
+  int* arrive;          // row warps that left theirs there, by the owning range: [2][workers][row warps]
   void* y;
   int* err;             // error word and counters
-  int y_type, workers, stages, stage_bytes, xbuf_bytes;
-  int cols8, parts;     // activation rows of a stage; bf16 parts of a hidden value
+  int y_type, workers, stages, stage_bytes;
+  int tcols;            // T rounded up to 16: columns of the first product and of the linear form
+  int parts;            // bf16 parts of a hidden value
+  int h_block;          // rows of h in one tile of the second product
+  int acc_cols, acc_bufs;  // bf16 weights: columns of an accumulator, accumulator pairs
 };
 
 struct alignas(16) Shared {
   uint64_t full_w[kMaxStages], full_x[kMaxStages], empty[kMaxStages];
-  uint64_t xfull[kRowGroups], xfree[kRowGroups];  // exchange of the column halves
+  uint64_t acc_full[2], acc_empty[2];   // bf16: accumulator pairs
+  uint64_t a_ready[2][2], d_full[2][2]; // 4 bits: [box][buffer]
+  uint64_t swap_ready, swap_done;       // 4 bits: both boxes' sums of a tile in tensor memory
+  uint64_t out_done;                    // every CTA's output rows are there
+  uint64_t drained;                     // tensor instructions all complete
+  uint32_t tmem;
   int abort;
-  int nact, nblk;                  // work list entries, column blocks of 32 rows in all
+  int nact, nblk;                  // work list entries, blocks of h rows in all
   int e[kMaxActive];               // expert
   int m[kMaxActive];               // its rows
   int row0[kMaxActive];            // its first row in h and o
-  int blk0[kMaxActive + 1];        // column blocks before it
+  int blk0[kMaxActive + 1];        // blocks of h rows before it
   unsigned mask[256][2];           // tokens that picked expert e
   float row_w[kMaxRows];
   float pick_w[kMaxPicks];
@@ -128,7 +142,6 @@ struct alignas(16) Shared {
   short pick_row[kMaxPicks];
   unsigned char row_token[kMaxRows];
 };
-
 constexpr int kSharedBytes = (sizeof(Shared) + 127) / 128 * 128;
 
 // ---------------------------------------------------------------- work list
@@ -162,7 +175,6 @@ __device__ __forceinline__ void route_tokens(const StreamParams& p, Shared& ss) 
   }
 }
 
-template <int COLS>
 __device__ void build_work_list(const StreamParams& p, Shared& ss) {
   const int tid = threadIdx.x, lane = tid & 31;
   for (int i = tid; i < 512; i += kThreads) (&ss.mask[0][0])[i] = 0;
@@ -177,7 +189,7 @@ __device__ void build_work_list(const StreamParams& p, Shared& ss) {
     route_tokens<8>(p, ss);
   __syncthreads();
   const int R = p.T * p.k;
-  if (tid < 32) {  // experts 8 lane .. 8 lane + 7: exclusive sums of entries, rows and column blocks
+  if (tid < 32) {  // experts 8 lane .. 8 lane + 7: exclusive sums of entries, rows and blocks of h rows
     int n[8], na = 0, nr = 0, nb = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -185,7 +197,7 @@ __device__ void build_work_list(const StreamParams& p, Shared& ss) {
       n[j] = e < p.E ? __popc(ss.mask[e][0]) + __popc(ss.mask[e][1]) : 0;
       na += n[j] > 0;
       nr += n[j];
-      nb += (n[j] + COLS - 1) / COLS;
+      nb += (n[j] + p.h_block - 1) / p.h_block;
     }
     int ia = na, ir = nr, ib = nb;
 #pragma unroll
@@ -205,9 +217,9 @@ __device__ void build_work_list(const StreamParams& p, Shared& ss) {
       ss.blk0[ia] = ib;
       ++ia;
       ir += n[j];
-      ib += (n[j] + COLS - 1) / COLS;
+      ib += (n[j] + p.h_block - 1) / p.h_block;
     }
-    const int per = (p.T + COLS - 1) / COLS;
+    const int per = (p.T + p.h_block - 1) / p.h_block;
     if (lane < p.S) {
       ss.e[all_a + lane] = p.E + lane;
       ss.m[all_a + lane] = p.T;
@@ -246,14 +258,15 @@ __device__ void build_work_list(const StreamParams& p, Shared& ss) {
 }
 
 // ------------------------------------------------------------------ ranges
-// The K blocks of a product, tile after tile (expert, row tile, column
-// block), cut into `workers` contiguous ranges.  Every role of a CTA walks
+// The K blocks of a product, tile after tile (expert, row tile, block
+// of h rows), cut into `workers` contiguous ranges.  Every role of a CTA walks
 // the same segments: the K blocks [kb0, kb1) of one tile.
 struct Segment {
   int worker, item, kb0, kb1;
-  int a, rt, nb;   // work list entry, row tile, column block
+  int a, rt, nb;   // work list entry, row tile, block of h rows (second product of the layer)
 };
 
+template <bool BLOCKS>  // more than one tile column wise: the layer's second product
 struct Walk {
   const Product& pr;
   const Shared& ss;
@@ -265,7 +278,7 @@ struct Walk {
   // the owner of a cut tile waits for ranges after its own, so on a capped
   // grid those come first.
   __device__ Walk(const Product& product, const Shared& shared, int most) : pr(product), ss(shared) {
-    units = ss.nblk * pr.row_tiles * pr.kblocks;
+    units = (BLOCKS ? ss.nblk : ss.nact) * pr.row_tiles * pr.kblocks;
     workers = min(most, units);  // no range is empty
     const int b = static_cast<int>(blockIdx.x), n = static_cast<int>(gridDim.x);
     v = b < workers ? b + ((workers - 1 - b) / n + 1) * n : 0;
@@ -287,25 +300,33 @@ struct Walk {
       u1 = begin_of(v + 1);
       item = u / pr.kblocks;
       kb = u - item * pr.kblocks;
-      int lo = 0, hi = ss.nact - 1;   // last entry with blk0 * row_tiles <= item
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (ss.blk0[mid] * pr.row_tiles <= item)
-          lo = mid;
-        else
-          hi = mid - 1;
+      if (BLOCKS) {
+        int lo = 0, hi = ss.nact - 1;   // last entry with blk0 * row_tiles <= item
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) / 2;
+          if (ss.blk0[mid] * pr.row_tiles <= item)
+            lo = mid;
+          else
+            hi = mid - 1;
+        }
+        a = lo;
       }
-      a = lo;
     }
-    while (item >= ss.blk0[a + 1] * pr.row_tiles) ++a;
-    const int nblk = ss.blk0[a + 1] - ss.blk0[a], r = item - ss.blk0[a] * pr.row_tiles;
+    if (BLOCKS) {
+      while (item >= ss.blk0[a + 1] * pr.row_tiles) ++a;
+      const int nblk = ss.blk0[a + 1] - ss.blk0[a], r = item - ss.blk0[a] * pr.row_tiles;
+      s.a = a;
+      s.rt = r / nblk;
+      s.nb = r - s.rt * nblk;
+    } else {
+      s.a = item / pr.row_tiles;
+      s.rt = item - s.a * pr.row_tiles;
+      s.nb = 0;
+    }
     s.worker = v;
     s.item = item;
     s.kb0 = kb;
     s.kb1 = min(pr.kblocks, kb + (u1 - u));
-    s.a = a;
-    s.rt = r / nblk;
-    s.nb = r - s.rt * nblk;
     u += s.kb1 - s.kb0;
     kb = 0;
     ++item;
@@ -347,43 +368,70 @@ struct Drain {
 
 // Waits until `target` arrivals are counted (bounded).
 __device__ bool wait_count(const int* c, int target, volatile int* abort, int* err, int where) {
-  const uint64_t t0 = globaltimer_ns();
-  while (ld_acquire_gpu(c) < target) {
+  uint64_t t0 = 0;
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (ld_acquire_gpu(c) >= target) return true;
     if (*abort) return false;
+    if (t0 == 0) t0 = globaltimer_ns();
     if (globaltimer_ns() - t0 > kWaitLimitNs) {
       record_error(err, MOE_ERR_TIMEOUT_CODE, where);
       *abort = 1;
       return false;
     }
   }
-  return true;
 }
 
+// Columns of a tile: all tokens (first product, linear form), or the parts of
+// its rows of h, each rounded up to 16.
+template <bool H>
+struct Columns {
+  int m;       // real ones: rows of the expert in this tile
+  int r0;      // its first row in h and o
+  int n16;     // 16-row boxes of one part
+  int n;       // columns of the tensor instruction
+  __device__ Columns(const StreamParams& p, const Shared& ss, const Segment& s) {
+    if (H) {
+      m = min(p.h_block, ss.m[s.a] - s.nb * p.h_block);
+      n16 = (m + 15) / 16;
+      n = 16 * n16 * p.parts;
+    } else {
+      m = ss.m[s.a];
+      n16 = p.tcols / 16;
+      n = p.tcols;
+    }
+    r0 = ss.row0[s.a] + s.nb * p.h_block;
+  }
+};
+
+// Everything below is written for one product: `which` picks its tensor maps,
+// H says that its columns are rows of h.
 // --------------------------------------------------------------- producers
-template <int G>
+template <int G, bool H>
 __device__ bool produce_weights(const StreamParams& p, int which, Shared& ss, uint8_t* ring, Ring& rg, Drain& dr,
                                 volatile int* abort) {
   using Ge = Geo<G>;
   const Product& pr = p.p[which];
-  Walk walk(pr, ss, p.workers);
+  Walk<H> walk(pr, ss, p.workers);
   Segment s;
   while (walk.next(s)) {
     const int row = ss.e[s.a] * pr.rows + s.rt * pr.row_step;
-    const int second = which == 0 ? row : row + kBoxRows;  // W3 beside W1, or the tile's other rows
+    const int beside = which == 0 ? 0 : kTileRows;  // W3 beside W1, or the tile's other rows
     for (int kb = s.kb0; kb < s.kb1; ++kb) {
       if (!mbar_wait(&ss.empty[rg.stage], rg.phase ^ 1, abort, p.err, (0x21 << 24) | which)) return false;
       uint8_t* st = ring + static_cast<size_t>(rg.stage) * p.stage_bytes;
       uint64_t* bar = &ss.full_w[rg.stage];
-      mbar_arrive_expect_tx(bar, 2 * (kBoxBytes + Ge::SCALE_BYTES));
+      mbar_arrive_expect_tx(bar, Ge::WEIGHT_BYTES);
       dr.note(rg.stage, rg.phase);
       const int col = kb * (Ge::Q4 ? 128 : 64);  // bytes or bf16
       tma_load_2d(st, &pr.w0, bar, col, row);
-      tma_load_2d(st + kBoxBytes, &pr.w1, bar, col, second);
+      tma_load_2d(st + kBoxBytes, &pr.w1, bar, col, row + beside);
       if constexpr (Ge::Q4) {
         uint8_t* sc = st + 2 * kBoxBytes;
         const int at = ss.e[s.a] * (pr.K / G) + kb * Ge::GROUPS, r0 = s.rt * pr.row_step;
         tma_load_2d(sc, &pr.s0, bar, r0, at);
-        tma_load_2d(sc + Ge::SCALE_BYTES, &pr.s1, bar, which == 0 ? r0 : r0 + kBoxRows, at);
+        tma_load_2d(sc + Ge::SCALE_BYTES, &pr.s1, bar, r0 + beside, at);
       }
       rg.step(p.stages);
     }
@@ -391,51 +439,122 @@ __device__ bool produce_weights(const StreamParams& p, int which, Shared& ss, ui
   return true;
 }
 
-// Columns: the rows of x by token (hidden, linear) or the parts of h.  16
-// bytes a lane; a lane's arrival on the stage's barrier follows its copies.
-template <int G, bool LAYER>
-__device__ bool produce_columns(const StreamParams& p, int which, Shared& ss, uint8_t* ring, Ring& rg,
+// Activation rows: 64 columns at a time, the parts of h below one another.
+template <int G, bool H>
+__device__ bool produce_columns(const StreamParams& p, int which, Shared& ss, uint8_t* ring, Ring& rg, Drain& dr,
                                 volatile int* abort) {
   using Ge = Geo<G>;
-  constexpr int LANES = Ge::KB / 8;         // lanes of a row
-  constexpr int ROWS = 32 / LANES;          // rows of an instruction
   const Product& pr = p.p[which];
-  const int lane = threadIdx.x & 31;
-  const bool hidden_in = LAYER && which == 1;
-  const uint16_t* base = hidden_in ? p.h : p.x;
-  const int parts = hidden_in ? p.parts : 1;
-  const size_t part_step = static_cast<size_t>(p.T) * (p.k + p.S) * p.f;
-  const int col = (lane % LANES) * 8;
-  Walk walk(pr, ss, p.workers);
+  const int Rs = p.T * (p.k + p.S);
+  Walk<H> walk(pr, ss, p.workers);
   Segment s;
   while (walk.next(s)) {
-    const int m = min(Ge::COLS, ss.m[s.a] - s.nb * Ge::COLS);
-    const int r = ss.row0[s.a] + s.nb * Ge::COLS;
-    int mine = 0;  // row of `base` that this lane keeps for the warp
-    if (lane < m) mine = hidden_in ? r + lane : ss.row_token[r + lane];
+    const Columns<H> c(p, ss, s);
     for (int kb = s.kb0; kb < s.kb1; ++kb) {
-      const bool ok = mbar_wait(&ss.empty[rg.stage], rg.phase ^ 1, abort, p.err, (0x22 << 24) | which);
-      if (!__all_sync(kFull, ok)) return false;
+      if (!mbar_wait(&ss.empty[rg.stage], rg.phase ^ 1, abort, p.err, (0x22 << 24) | which)) return false;
+      uint8_t* st = ring + static_cast<size_t>(rg.stage) * p.stage_bytes + Ge::WEIGHT_BYTES;
       uint64_t* bar = &ss.full_x[rg.stage];
-      const uint32_t dst = smem_u32(ring) + static_cast<uint32_t>(rg.stage) * p.stage_bytes +
-                           2 * (kBoxBytes + Ge::SCALE_BYTES) + (lane / LANES) * Ge::PITCH + col * 2;
-      const bool in = kb * Ge::KB + col < pr.K;
-      for (int i = 0; i < m; i += ROWS) {
-        const int at = i + lane / LANES;
-        const int row = __shfl_sync(kFull, mine, at & 31);
-        const uint16_t* src = base + static_cast<size_t>(row) * pr.K + kb * Ge::KB + col;
-        if (in && at < m)
-          for (int q = 0; q < parts; ++q)
-            cp_async16(dst + (q * p.cols8 + i) * Ge::PITCH, src + q * part_step);
+      mbar_arrive_expect_tx(bar, Ge::ATOMS * c.n * 128);
+      dr.note(rg.stage, rg.phase);
+#pragma unroll 1
+      for (int at = 0; at < Ge::ATOMS; ++at) {
+        uint8_t* dst = st + at * c.n * 128;
+        const int col = (kb * Ge::ATOMS + at) * 64;
+        if (!H) {
+          tma_load_2d(dst, &pr.cols, bar, col, 0);
+        } else {
+          for (int q = 0; q < p.parts; ++q)
+            for (int i = 0; i < c.n16; ++i)
+              tma_load_2d(dst + (q * c.n16 + i) * 2048, &pr.cols, bar, col, q * Rs + c.r0 + i * 16);
+        }
       }
-      cp_async_arrive(bar);
       rg.step(p.stages);
     }
   }
   return true;
 }
 
-// --------------------------------------------------------------- consumers
+// ----------------------------------------------------- tensor instructions
+// Positions in the row warps' buffers: bf16, segments; 4 bits, groups.
+struct Turn {
+  int buf = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void step(int bufs) {
+    if (++buf == bufs) {
+      buf = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+// Groups of a stage that lie inside K.
+template <int G>
+__device__ __forceinline__ int stage_groups(int K, int kb) {
+  return min(Geo<G>::KB, K - kb * Geo<G>::KB) / G;
+}
+
+template <int G, bool H>
+__device__ bool issue_mmas(const StreamParams& p, int which, Shared& ss, uint8_t* ring, Ring& rg, Turn& tn,
+                           volatile int* abort) {
+  using Ge = Geo<G>;
+  const Product& pr = p.p[which];
+  const uint32_t tmem = ss.tmem;
+  Walk<H> walk(pr, ss, p.workers);
+  Segment s;
+  while (walk.next(s)) {
+    const Columns<H> c(p, ss, s);
+    const uint32_t idesc = idesc_bf16_f32(kTileRows, c.n, 0, 0);
+    if constexpr (!Ge::Q4)
+      if (!mbar_wait(&ss.acc_empty[tn.buf], tn.phase ^ 1, abort, p.err, (0x31 << 24) | which)) return false;
+    for (int kb = s.kb0; kb < s.kb1; ++kb) {
+      const uint32_t st = smem_u32(ring) + static_cast<uint32_t>(rg.stage) * p.stage_bytes;
+      const uint32_t x = st + Ge::WEIGHT_BYTES;
+      if (!mbar_wait(&ss.full_x[rg.stage], rg.phase, abort, p.err, (0x24 << 24) | which)) return false;
+      if constexpr (!Ge::Q4) {
+        if (!mbar_wait(&ss.full_w[rg.stage], rg.phase, abort, p.err, (0x23 << 24) | which)) return false;
+        tc_fence_after();
+        const uint32_t acc = tmem + tn.buf * 2 * p.acc_cols;
+#pragma unroll
+        for (int k4 = 0; k4 < 4; ++k4) {
+          const uint64_t bd = smem_desc_sw128(x + k4 * 32, 16, 1024);
+          const uint32_t go_on = (kb != s.kb0 || k4 != 0) ? 1u : 0u;
+#pragma unroll
+          for (int box = 0; box < 2; ++box)
+            umma_bf16(acc + box * p.acc_cols, smem_desc_sw128(st + box * kBoxBytes + k4 * 32, 16, 1024), bd, idesc, go_on);
+        }
+        umma_commit(&ss.empty[rg.stage]);
+      } else {
+        const int groups = stage_groups<G>(pr.K, kb);
+        for (int j = 0; j < groups; ++j) {
+#pragma unroll
+          for (int box = 0; box < 2; ++box) {
+            if (!mbar_wait(&ss.a_ready[box][tn.buf], tn.phase, abort, p.err, (0x32 << 24) | which)) return false;
+            tc_fence_after();
+            const uint32_t a = tmem + (box * 2 + tn.buf) * Ge::A_COLS;
+            const uint32_t acc = tmem + 4 * Ge::A_COLS + (box * 2 + tn.buf) * Ge::ACC;
+#pragma unroll
+            for (int i = 0; i < G / 16; ++i) {
+              const int k = j * G + i * 16;
+              umma_bf16_ta(acc, a + i * 8, smem_desc_sw128(x + (k / 64) * c.n * 128 + (k % 64) * 2, 16, 1024), idesc,
+                           i != 0 ? 1u : 0u);
+            }
+            umma_commit(&ss.d_full[box][tn.buf]);
+          }
+          tn.step(2);
+        }
+        umma_commit(&ss.empty[rg.stage]);
+      }
+      rg.step(p.stages);
+    }
+    if constexpr (!Ge::Q4) {
+      umma_commit(&ss.acc_full[tn.buf]);
+      tn.step(p.acc_bufs);
+    }
+  }
+  return true;
+}
+
+// --------------------------------------------------------------- row warps
 // The hidden values enter the second product in bf16 parts that add up to
 // them: two (16 significant bits) for a bf16 y, three (24) for an fp32 y.
 // One part alone would cost 2^-9 of each value, as much as the rounding of a
@@ -444,242 +563,323 @@ __device__ bool produce_columns(const StreamParams& p, int which, Shared& ss, ui
 // bf16's range no sooner than the upper one does.
 constexpr float kLowScale = 256.f;
 
-// Sums of the upper part, and of the lower ones together.
-template <int PARTS>
-constexpr int kSums = PARTS > 1 ? 2 : 1;
-
-template <int SUMS, int NT>
-__device__ __forceinline__ float join_parts(const float (&s)[SUMS][NT][4], int n, int i) {
-  if constexpr (SUMS == 2)
-    return fmaf(s[1][n][i], 1.f / kLowScale, s[0][n][i]);
-  else
-    return s[0][n][i];
-}
-
-// One stage, this warp's 8 rows of either box and half of the columns:
-// acc[n][..] += weights . columns.  The 16-row operand holds the first box's
-// rows on top and the second box's below.  Sums of a stage (bf16) or of a
-// group (4 bits) start from zero in the tensor core and are added to acc in
-// fp32, so the chain of additions inside the tensor core, which truncates, is
-// short.
-template <int G, int NT, int PARTS>
-__device__ __forceinline__ void multiply_stage(uint32_t st, int part_bytes, int kleft, int m, float (&acc)[NT][4]) {
-  using Ge = Geo<G>;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rgrp = warp % kRowGroups, half = warp / kRowGroups;
-  const uint32_t cols = st + 2 * (kBoxBytes + Ge::SCALE_BYTES);
-  // matrices (box 0, 16 bytes c), (box 1, c), (box 0, c + 1), (box 1, c + 1)
-  const uint32_t arow = st + ((lane >> 3) & 1) * kBoxBytes + (rgrp * 8 + (lane & 7)) * 128;
-  auto frag = [&](int c, uint32_t (&a)[4]) {
-    ldmatrix_x4(arow + ((static_cast<uint32_t>(c + (lane >> 4)) ^ (lane & 7)) << 4), a);
-  };
-  if constexpr (!Ge::Q4) {
-    float s[kSums<PARTS>][NT][4] = {};
-    uint32_t a[2][4];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) frag(half * 4 + 2 * i, a[i]);
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int q = 0; q < PARTS; ++q) {
-        uint32_t b[4];  // four matrices: 16 bytes c .. c + 3 of the 8 activation rows
-        ldmatrix_x4(cols + q * part_bytes + (n * 8 + (lane & 7)) * Ge::PITCH + (half * 4 + (lane >> 3)) * 16, b);
-        mma_bf16(s[q > 0][n], a[0][0], a[0][1], a[0][2], a[0][3], b[0], b[1]);
-        mma_bf16(s[q > 0][n], a[1][0], a[1][1], a[1][2], a[1][3], b[2], b[3]);
-      }
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[n][i] += join_parts(s, n, i);
-  } else {
-    const int g = lane >> 2, t = lane & 3;
-    const uint32_t scales = st + 2 * kBoxBytes + (rgrp * 8 + g) * 2;
-    constexpr int CHUNKS = 4;                        // 32-column chunks of this warp's half
-    float s[kSums<PARTS>][NT][4];
-#pragma unroll
-    for (int c2 = 0; c2 < CHUNKS; c2 += 2) {
-      if (half * 128 + c2 * 32 >= kleft) break;      // columns past K (a multiple of 64)
-      uint32_t w[4];
-      frag(half * 4 + c2, w);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {                  // chunk c2 + i
-        const int c = half * 4 + c2 + i;
-        const bool group_begins = G == 32 || (i == 0 && (G == 64 || c2 == 0));
-        const bool group_ends = G == 32 || (i == 1 && (G == 64 || c2 == 2));
-        if (group_begins)
-#pragma unroll
-          for (int j = 0; j < kSums<PARTS> * NT * 4; ++j) (&s[0][0][0])[j] = 0.f;
-        uint32_t a[8];                               // pairs 0..3 of either box's row
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          a[2 * j] = q4_pair(w[2 * i], j);
-          a[2 * j + 1] = q4_pair(w[2 * i + 1], j);
-        }
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int q = 0; q < PARTS; ++q) {
-            uint32_t b[4] = {0, 0, 0, 0};
-            if (n * 8 + g < m) lds128(cols + q * part_bytes + (n * 8 + g) * Ge::PITCH + c * 64 + t * 16, b);
-            mma_bf16(s[q > 0][n], a[0], a[1], a[2], a[3], b[0], b[1]);
-            mma_bf16(s[q > 0][n], a[4], a[5], a[6], a[7], b[2], b[3]);
-          }
-        if (group_ends) {
-          const uint32_t sc = scales + (c * 32 / G) * (kBoxRows * 2);
-          const float f0 = lds_bf16(sc), f1 = lds_bf16(sc + Ge::SCALE_BYTES);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            acc[n][0] = fmaf(f0, join_parts(s, n, 0), acc[n][0]);
-            acc[n][1] = fmaf(f0, join_parts(s, n, 1), acc[n][1]);
-            acc[n][2] = fmaf(f1, join_parts(s, n, 2), acc[n][2]);
-            acc[n][3] = fmaf(f1, join_parts(s, n, 3), acc[n][3]);
-          }
-        }
-      }
-    }
+__device__ __forceinline__ void store_hidden(const StreamParams& p, int r, int i, float w, float a, float b) {
+  const float h = w * (a / (1.f + expf(-a)) * b);
+  const size_t part_step = static_cast<size_t>(p.T) * (p.k + p.S) * p.f;
+  uint16_t* to = p.h + static_cast<size_t>(r) * p.f + i;
+  float rest = h;
+  for (int q = 0; q < p.parts; ++q) {
+    const __nv_bfloat16 v = __float2bfloat16_rn(rest);
+    to[q * part_step] = __bfloat16_as_ushort(v);
+    rest = (rest - __bfloat162float(v)) * (q == 0 ? kLowScale : 1.f);
+    if (!isfinite(rest)) rest = 0.f;  // a value that rounds to infinity keeps that alone
   }
 }
 
-__device__ __forceinline__ void store_y(void* y, int y_type, size_t at, float v) {
-  if (y_type == MOE_Y_BF16)
-    static_cast<__nv_bfloat16*>(y)[at] = __float2bfloat16_rn(v);
-  else
-    static_cast<float*>(y)[at] = v;
+template <bool LAYER>
+__device__ __forceinline__ void store_out(const StreamParams& p, int r, int c, float v) {
+  if (LAYER) {
+    if (c < p.d) p.o[static_cast<size_t>(r) * p.d + c] = v;
+  } else if (c < p.n) {
+    const size_t at = static_cast<size_t>(r) * p.n + c;
+    if (p.y_type == MOE_Y_BF16)
+      static_cast<__nv_bfloat16*>(p.y)[at] = __float2bfloat16_rn(v);
+    else
+      static_cast<float*>(p.y)[at] = v;
+  }
 }
 
-// A finished tile's values, one thread's share: row g of either box, columns
-// 2t and 2t + 1 of every 8.
-template <int G, bool LAYER, int NT>
-__device__ __forceinline__ void finish_tile(const StreamParams& p, int which, const Shared& ss, const Segment& s,
-                                            const float (&acc)[NT][4]) {
-  const int lane = threadIdx.x & 31, rgrp = (threadIdx.x >> 5) % kRowGroups;
-  const int row = rgrp * 8 + (lane >> 2), t2 = (lane & 3) * 2;
-  const int m = min(Geo<G>::COLS, ss.m[s.a] - s.nb * Geo<G>::COLS), r0 = ss.row0[s.a] + s.nb * Geo<G>::COLS;
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int col = n * 8 + t2 + i;
-      if (col >= m) continue;
-      const int r = r0 + col;
-      if (LAYER && which == 0) {
-        const float a = acc[n][i], b = acc[n][2 + i];
-        const float h = ss.row_w[r] * (a / (1.f + expf(-a)) * b);
-        const size_t part_step = static_cast<size_t>(p.T) * (p.k + p.S) * p.f;
-        uint16_t* to = p.h + static_cast<size_t>(r) * p.f + s.rt * kBoxRows + row;
-        float rest = h;
-        for (int q = 0; q < p.parts; ++q) {
-          const __nv_bfloat16 v = __float2bfloat16_rn(rest);
-          to[q * part_step] = __bfloat16_as_ushort(v);
-          rest = (rest - __bfloat162float(v)) * (q == 0 ? kLowScale : 1.f);
-          if (!isfinite(rest)) rest = 0.f;  // a value that rounds to infinity keeps that alone
-        }
-      } else {
-#pragma unroll
-        for (int box = 0; box < 2; ++box) {
-          const int c = s.rt * 2 * kBoxRows + box * kBoxRows + row;
-          if (LAYER) {
-            if (c < p.d) p.o[static_cast<size_t>(r) * p.d + c] = acc[n][2 * box + i];
-          } else {
-            if (c < p.n) store_y(p.y, p.y_type, static_cast<size_t>(r) * p.n + c, acc[n][2 * box + i]);
-          }
-        }
-      }
-    }
+// A range's sums of the tile that it begins in, this thread's row.
+__device__ __forceinline__ float* part_of(const StreamParams& p, int worker, int box, int row) {
+  return p.part + (static_cast<size_t>(worker) * 2 + box) * (kMaxTokens * kTileRows) + row;
 }
 
-struct Consumer {
-  Ring rg;
-  uint32_t xphase = 0;  // exchange of the column halves
+// Which share of its tile a segment is: all of it, the end (left for the
+// owner) or the beginning (this range owns the tile and adds the others').
+struct Share {
+  bool leave, add;
+  int v0, v1;     // owning range, last range with a part
+  template <typename W>
+  __device__ Share(const W& walk, const Segment& s, int kblocks) {
+    leave = s.kb0 != 0;
+    add = !leave && s.kb1 != kblocks;
+    v0 = v1 = s.worker;
+    if (leave) v0 = walk.worker_of(s.item * kblocks);
+    if (add) v1 = walk.worker_of(s.item * kblocks + kblocks - 1);
+  }
 };
+__device__ __forceinline__ int* arrivals_of(const StreamParams& p, int which, int worker) {
+  return p.arrive + (static_cast<size_t>(which) * p.workers + worker) * kRowWarps + (threadIdx.x >> 5);
+}
+__device__ __forceinline__ void leave_part(const StreamParams& p, int which, const Share& sh) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) red_release_gpu_add(arrivals_of(p, which, sh.v0), 1);
+}
+__device__ __forceinline__ bool wait_parts(const StreamParams& p, int which, const Share& sh, volatile int* abort) {
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0) {
+    int* cnt = arrivals_of(p, which, sh.v0);
+    ok = wait_count(cnt, sh.v1 - sh.v0, abort, p.err, (0x29 << 24) | which);
+    *cnt = 0;
+  }
+  return __shfl_sync(kFull, ok, 0);
+}
 
-// Sums this warp's share of a segment and, on the lower column half's warp,
-// finishes the tile or leaves its part for the range that does.  False after
-// a wait that gave up.
-template <int G, bool LAYER, int NT, int PARTS>
-__device__ bool consume_segment(const StreamParams& p, int which, Shared& ss, uint8_t* ring, float* xbuf, const Walk& walk,
-                                const Segment& s, Consumer& cs, volatile int* abort) {
-  using Ge = Geo<G>;
+// bf16 weights: a segment's sums are in tensor memory.  Both sets see both
+// accumulators of their rows and take every other column.  `read(c)` gives
+// column c of either box; eight columns are read at a time.
+template <bool H, bool LAYER>
+__device__ bool rows_bf16(const StreamParams& p, int which, Shared& ss, Turn& tn, volatile int* abort) {
   const Product& pr = p.p[which];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rgrp = warp % kRowGroups, half = warp / kRowGroups;
-  const int m = min(Ge::COLS, ss.m[s.a] - s.nb * Ge::COLS);
-  constexpr int N = NT * 4;
-  float acc[NT][4] = {};
-  bool ok = true;
-  for (int kb = s.kb0; kb < s.kb1; ++kb) {
-    ok = mbar_wait(&ss.full_w[cs.rg.stage], cs.rg.phase, abort, p.err, (0x23 << 24) | which) &&
-         mbar_wait(&ss.full_x[cs.rg.stage], cs.rg.phase, abort, p.err, (0x24 << 24) | which);
+  const int quad = warp & 3, set = warp >> 2, row = quad * 32 + lane;
+  Walk<H> walk(pr, ss, p.workers);
+  Segment s;
+  while (walk.next(s)) {
+    const Columns<H> c(p, ss, s);
+    const Share sh(walk, s, pr.kblocks);
+    bool ok = mbar_wait(&ss.acc_full[tn.buf], tn.phase, abort, p.err, (0x33 << 24) | which);
     if (!__all_sync(kFull, ok)) return false;
-    const uint32_t st = smem_u32(ring) + static_cast<uint32_t>(cs.rg.stage) * p.stage_bytes;
-    multiply_stage<G, NT, PARTS>(st, p.cols8 * Ge::PITCH, pr.K - kb * Ge::KB, m, acc);
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&ss.empty[cs.rg.stage]);
-    cs.rg.step(p.stages);
-  }
-  // the two column halves
-  float* xb = xbuf + rgrp * (p.xbuf_bytes / (kRowGroups * static_cast<int>(sizeof(float)))) + lane;
-  if (half == 1) {
-    ok = mbar_wait(&ss.xfree[rgrp], cs.xphase ^ 1, abort, p.err, (0x27 << 24) | which);
-    cs.xphase ^= 1;
-    if (!__all_sync(kFull, ok)) return false;
+    tc_fence_after();
+    const uint32_t acc = ss.tmem + (static_cast<uint32_t>(quad * 32) << 16) + tn.buf * 2 * p.acc_cols;
+    if (sh.add && !wait_parts(p, which, sh, abort)) return false;
+    constexpr int B = 4;  // columns read at a time
+    for (int i0 = set * B; i0 < c.m; i0 += 2 * B) {
+      float v[2][B];
+      uint32_t u[2][3][B];
 #pragma unroll
-    for (int i = 0; i < N; ++i) xb[i * 32] = (&acc[0][0])[i];
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&ss.xfull[rgrp]);
-    return true;
-  }
-  ok = mbar_wait(&ss.xfull[rgrp], cs.xphase, abort, p.err, (0x28 << 24) | which);
-  cs.xphase ^= 1;
-  if (!__all_sync(kFull, ok)) return false;
+      for (int j = 0; j < B; ++j) {
+        const int i = min(i0 + j, c.m - 1);  // past the end: the last column again
+        const int at = H ? i : LAYER ? ss.row_token[c.r0 + i] : i;
 #pragma unroll
-  for (int i = 0; i < N; ++i) (&acc[0][0])[i] += xb[i * 32];
-  __syncwarp();
-  if (lane == 0) mbar_arrive(&ss.xfree[rgrp]);
-
-  const int first = s.item * pr.kblocks;
-  auto part = [&](int v) { return p.part + (static_cast<size_t>(v) * kRowGroups + rgrp) * (16 * 32) + lane; };
-  auto arrived = [&](int v) { return p.arrive + (static_cast<size_t>(which) * p.workers + v) * kRowGroups + rgrp; };
-  if (s.kb0 != 0) {  // the tile began in an earlier range
-    float* mine = part(s.worker);
+        for (int box = 0; box < 2; ++box)
 #pragma unroll
-    for (int i = 0; i < N; ++i) __stcg(mine + i * 32, (&acc[0][0])[i]);
-    __syncwarp();
-    if (lane == 0) red_release_gpu_add(arrived(walk.worker_of(first)), 1);
-    return true;
-  }
-  if (s.kb1 != pr.kblocks) {  // it goes on in later ranges, which began with it
-    const int v1 = walk.worker_of(first + pr.kblocks - 1);
-    int* cnt = arrived(s.worker);
-    if (lane == 0) {
-      ok = wait_count(cnt, v1 - s.worker, abort, p.err, (0x29 << 24) | which);
-      *cnt = 0;
+          for (int q = 0; q < 3; ++q) {
+            u[box][q][j] = 0;
+            if (q == 0 || (H && q < p.parts)) u[box][q][j] = tmem_ld1(acc + box * p.acc_cols + q * 16 * c.n16 + at);
+          }
+      }
+      tmem_ld_wait();
+#pragma unroll
+      for (int j = 0; j < B; ++j)
+#pragma unroll
+        for (int box = 0; box < 2; ++box) {
+          v[box][j] = __uint_as_float(u[box][0][j]);
+          if (H) v[box][j] += (__uint_as_float(u[box][1][j]) + __uint_as_float(u[box][2][j])) * (1.f / kLowScale);
+        }
+      if (sh.leave) {
+#pragma unroll
+        for (int j = 0; j < B; ++j)
+          if (i0 + j < c.m)
+#pragma unroll
+            for (int box = 0; box < 2; ++box) __stcg(part_of(p, s.worker, box, row) + (i0 + j) * kTileRows, v[box][j]);
+        continue;
+      }
+      for (int w = sh.v0 + 1; w <= sh.v1; ++w)
+#pragma unroll
+        for (int j = 0; j < B; ++j)
+          if (i0 + j < c.m)
+#pragma unroll
+            for (int box = 0; box < 2; ++box) v[box][j] += __ldcg(part_of(p, w, box, row) + (i0 + j) * kTileRows);
+#pragma unroll
+      for (int j = 0; j < B; ++j)
+        if (i0 + j < c.m) {
+          const int r = c.r0 + i0 + j;
+          if (LAYER && !H) {
+            const int i = s.rt * kTileRows + row;
+            if (i < p.f) store_hidden(p, r, i, ss.row_w[r], v[0][j], v[1][j]);
+          } else {
+#pragma unroll
+            for (int box = 0; box < 2; ++box)
+              store_out<LAYER>(p, r, (s.rt * 2 + box) * kTileRows + row, v[box][j]);
+          }
+        }
     }
-    if (!__shfl_sync(kFull, ok, 0)) return false;
-    for (int v = s.worker + 1; v <= v1; ++v) {
-      const float* from = part(v);
-#pragma unroll
-      for (int i = 0; i < N; ++i) (&acc[0][0])[i] += __ldcg(from + i * 32);
-    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ss.acc_empty[tn.buf]);
+    tn.step(p.acc_bufs);
+    if (sh.leave) leave_part(p, which, sh);
   }
-  finish_tile<G, LAYER, NT>(p, which, ss, s, acc);
   return true;
 }
 
-template <int G, bool LAYER, int PARTS>
-__device__ bool consume(const StreamParams& p, int which, Shared& ss, uint8_t* ring, float* xbuf, Consumer& cs,
+// 4-bit weights: set 0 owns the first box, set 1 the second, a thread one row
+// of it.  For each group of columns the thread turns its row's codes into the
+// operand, and then, while the tensor core multiplies that, adds the previous
+// group's sums, scaled, to its own.
+//
+// Buffers need no barriers of their own beside a_ready and d_full: a thread
+// arrives on a_ready for group g + 1 after it has read the sums of group
+// g - 1, so the accumulator that g + 1 writes is free; and those sums were
+// complete, so the operand buffer that it wrote for g + 1 was read.
+template <int G, int NC, bool H, bool LAYER>
+struct RowsQ4 {
+  using Ge = Geo<G>;
+  // Columns of an accumulator in each 16-column step: the parts of 16 rows of
+  // h lie n16 steps apart.
+  static __device__ __forceinline__ void add_group(const StreamParams& p, uint32_t acc, int n16, float scale,
+                                                   float (&sum)[NC]) {
+#pragma unroll
+    for (int b = 0; b < NC / 16; ++b) {
+      if (b >= n16) break;
+      uint32_t u[16];
+      tmem_ld16(acc + b * 16, u);
+      if constexpr (H) {
+        uint32_t lo[16];
+        tmem_ld16(acc + (n16 + b) * 16, lo);
+        if (p.parts == 3) {
+          uint32_t lo2[16];
+          tmem_ld16(acc + (2 * n16 + b) * 16, lo2);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) lo[i] = __float_as_uint(__uint_as_float(lo[i]) + __uint_as_float(lo2[i]));
+        } else {
+          tmem_ld_wait();
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          sum[b * 16 + i] = fmaf(scale, fmaf(__uint_as_float(lo[i]), 1.f / kLowScale, __uint_as_float(u[i])), sum[b * 16 + i]);
+      } else {
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sum[b * 16 + i] = fmaf(scale, __uint_as_float(u[i]), sum[b * 16 + i]);
+      }
+    }
+  }
+
+  static __device__ bool segment(const StreamParams& p, int which, Shared& ss, uint8_t* ring, const Walk<H>& walk,
+                                 const Segment& s, Ring& rg, Turn& tn, uint32_t& swap, volatile int* abort) {
+    const Product& pr = p.p[which];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int quad = warp & 3, box = warp >> 2, row = quad * 32 + lane;
+    const uint32_t lanes = ss.tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const Columns<H> c(p, ss, s);
+    const Share sh(walk, s, pr.kblocks);
+    float sum[NC];
+#pragma unroll
+    for (int i = 0; i < NC; ++i) sum[i] = 0.f;
+    float scale_before = 0.f;
+    Turn before = tn;
+    bool pending = false, ok = true;
+    auto take = [&]() {  // the previous group's sums
+      ok = mbar_wait(&ss.d_full[box][before.buf], before.phase, abort, p.err, (0x34 << 24) | which);
+      if (!__all_sync(kFull, ok)) return false;
+      tc_fence_after();
+      add_group(p, lanes + 4 * Ge::A_COLS + (box * 2 + before.buf) * Ge::ACC, c.n16, scale_before, sum);
+      return true;
+    };
+    for (int kb = s.kb0; kb < s.kb1; ++kb) {
+      ok = mbar_wait(&ss.full_w[rg.stage], rg.phase, abort, p.err, (0x23 << 24) | which);
+      if (!__all_sync(kFull, ok)) return false;
+      const uint32_t st = smem_u32(ring) + static_cast<uint32_t>(rg.stage) * p.stage_bytes;
+      const uint32_t codes = st + box * kBoxBytes + row * 128;
+      const uint32_t scales = st + 2 * kBoxBytes + box * Ge::SCALE_BYTES + row * 2;
+      const int groups = stage_groups<G>(pr.K, kb);
+#pragma unroll 1
+      for (int j = 0; j < groups; ++j) {
+        const uint32_t a = lanes + (box * 2 + tn.buf) * Ge::A_COLS;
+        uint32_t w[G / 32][4];
+#pragma unroll
+        for (int i = 0; i < G / 32; ++i) lds128(codes + (((j * (G / 32) + i) ^ (row & 7)) << 4), w[i]);
+        const float scale = lds_bf16(scales + j * (kTileRows * 2));
+#pragma unroll
+        for (int i = 0; i < G / 32; ++i) {
+          uint32_t v[16];
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[t * 4 + q] = q4_pair(w[i][t], q);
+          tmem_st16(a + i * 16, v);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ss.a_ready[box][tn.buf]);
+        if (pending && !take()) return false;
+        before = tn;
+        scale_before = scale;
+        pending = true;
+        tn.step(2);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ss.empty[rg.stage]);
+      rg.step(p.stages);
+    }
+    if (!take()) return false;
+
+    const int real = H ? c.m : p.T;  // columns with values of their own
+    if (sh.leave) {
+#pragma unroll
+      for (int i = 0; i < NC; ++i)
+        if (i < real) __stcg(part_of(p, s.worker, box, row) + i * kTileRows, sum[i]);
+      leave_part(p, which, sh);
+      tc_fence_before();
+      return true;
+    }
+    if (sh.add) {
+      if (!wait_parts(p, which, sh, abort)) return false;
+      for (int w = sh.v0 + 1; w <= sh.v1; ++w)
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+          if (i < real) sum[i] += __ldcg(part_of(p, w, box, row) + i * kTileRows);
+    }
+    if constexpr (LAYER && !H) {
+      // Both boxes' sums of a hidden column meet in tensor memory, in the
+      // accumulators just read; no set goes on before both have read them.
+      const uint32_t acc = lanes + 4 * Ge::A_COLS + before.buf * Ge::ACC;
+#pragma unroll
+      for (int b = 0; b < NC / 16; ++b) {
+        uint32_t u[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(sum[b * 16 + i]);
+        tmem_st16(acc + box * 2 * Ge::ACC + b * 16, u);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ss.swap_ready);
+      ok = mbar_wait(&ss.swap_ready, swap, abort, p.err, 0x35 << 24);
+      if (!__all_sync(kFull, ok)) return false;
+      tc_fence_after();
+      for (int i = box; i < c.m; i += 2) {
+        const int at = ss.row_token[c.r0 + i];
+        const uint32_t ua = tmem_ld1(acc + at), ub = tmem_ld1(acc + 2 * Ge::ACC + at);
+        tmem_ld_wait();
+        const int hi = s.rt * kTileRows + row;
+        if (hi < p.f) store_hidden(p, c.r0 + i, hi, ss.row_w[c.r0 + i], __uint_as_float(ua), __uint_as_float(ub));
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ss.swap_done);
+      ok = mbar_wait(&ss.swap_done, swap, abort, p.err, 0x36 << 24);
+      if (!__all_sync(kFull, ok)) return false;
+      swap ^= 1;
+      tc_fence_after();
+    } else {
+#pragma unroll
+      for (int i = 0; i < NC; ++i)
+        if (i < c.m) store_out<LAYER>(p, c.r0 + i, (s.rt * 2 + box) * kTileRows + row, sum[i]);
+      tc_fence_before();
+    }
+    return true;
+  }
+};
+
+template <int G, bool H, bool LAYER>
+__device__ bool rows_q4(const StreamParams& p, int which, Shared& ss, uint8_t* ring, Ring& rg, Turn& tn, uint32_t& swap,
                         volatile int* abort) {
-  Walk walk(p.p[which], ss, p.workers);
+  Walk<H> walk(p.p[which], ss, p.workers);
   Segment s;
   bool ok = true;
   while (ok && walk.next(s)) {
-    const int m = min(Geo<G>::COLS, ss.m[s.a] - s.nb * Geo<G>::COLS);
-    if (m <= 8)
-      ok = consume_segment<G, LAYER, 1, PARTS>(p, which, ss, ring, xbuf, walk, s, cs, abort);
-    else if (m <= 16)
-      ok = consume_segment<G, LAYER, 2, PARTS>(p, which, ss, ring, xbuf, walk, s, cs, abort);
-    else if constexpr (Geo<G>::COLS > 16)
-      ok = consume_segment<G, LAYER, 4, PARTS>(p, which, ss, ring, xbuf, walk, s, cs, abort);
+    const int n16 = Columns<H>(p, ss, s).n16;
+    if (n16 == 1)
+      ok = RowsQ4<G, 16, H, LAYER>::segment(p, which, ss, ring, walk, s, rg, tn, swap, abort);
+    else if (n16 == 2 || H)
+      ok = RowsQ4<G, 32, H, LAYER>::segment(p, which, ss, ring, walk, s, rg, tn, swap, abort);
+    else
+      ok = RowsQ4<G, H ? 32 : 64, H, LAYER>::segment(p, which, ss, ring, walk, s, rg, tn, swap, abort);
   }
   return ok;
 }
@@ -688,7 +888,7 @@ __device__ bool consume(const StreamParams& p, int which, Shared& ss, uint8_t* r
 __device__ void sum_rows(const StreamParams& p, const Shared& ss) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int d4 = p.d / 4, R = p.T * p.k;
-  const int units = p.T * d4, step = gridDim.x * kMmaWarps * 32;
+  const int units = p.T * d4, step = gridDim.x * kRowWarps * 32;
   for (int i = (warp * gridDim.x + blockIdx.x) * 32 + lane; i < units; i += step) {
     const int t = i / d4, c = (i - t * d4) * 4;
     float4 v[12];
@@ -715,94 +915,133 @@ __device__ void sum_rows(const StreamParams& p, const Shared& ss) {
 
 template <int G, bool LAYER>
 __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_constant__ StreamParams p) {
+  using Ge = Geo<G>;
   extern __shared__ uint8_t dyn[];
   Shared& ss = *reinterpret_cast<Shared*>(dyn);
-  float* xbuf = reinterpret_cast<float*>(dyn + kSharedBytes);
   // stages on 1024-byte boundaries of shared memory (the swizzle's period)
-  const uint32_t ring_at = (smem_u32(xbuf) + p.xbuf_bytes + 1023u) & ~1023u;
+  const uint32_t ring_at = (smem_u32(dyn) + kSharedBytes + 1023u) & ~1023u;
   uint8_t* ring = dyn + (ring_at - smem_u32(dyn));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < p.stages; ++i) {
       mbar_init(&ss.full_w[i], 1);
-      mbar_init(&ss.full_x[i], 32);
-      mbar_init(&ss.empty[i], kMmaWarps);
+      mbar_init(&ss.full_x[i], 1);
+      mbar_init(&ss.empty[i], Ge::Q4 ? kRowWarps + 1 : 1);
     }
-    for (int i = 0; i < kRowGroups; ++i) {
-      mbar_init(&ss.xfull[i], 1);
-      mbar_init(&ss.xfree[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ss.acc_full[i], 1);
+      mbar_init(&ss.acc_empty[i], kRowWarps);
+      for (int j = 0; j < 2; ++j) {
+        mbar_init(&ss.a_ready[i][j], kRowWarps / 2);
+        mbar_init(&ss.d_full[i][j], 1);
+      }
     }
+    mbar_init(&ss.swap_ready, kRowWarps);
+    mbar_init(&ss.swap_done, kRowWarps);
+    mbar_init(&ss.out_done, 1);
+    mbar_init(&ss.drained, 1);
     ss.abort = 0;
     fence_mbar_init();
   }
-  if (LAYER) {
-    build_work_list<Geo<G>::COLS>(p, ss);
-  } else {
-    const int per = (p.T + Geo<G>::COLS - 1) / Geo<G>::COLS;
-    if (tid < p.T) ss.row_token[tid] = static_cast<unsigned char>(tid);
-    if (tid == 0) {
-      ss.nact = 1;
-      ss.nblk = per;
-      ss.e[0] = 0;
-      ss.m[0] = p.T;
-      ss.row0[0] = 0;
-      ss.blk0[0] = 0;
-      ss.blk0[1] = per;
-    }
-    __syncthreads();
+  if (warp == kMmaWarp) {
+    tmem_alloc(&ss.tmem, kTmemCols);
+    tmem_relinquish();
   }
+  if (LAYER) {
+    build_work_list(p, ss);
+  } else if (tid == 0) {
+    ss.nact = ss.nblk = 1;
+    ss.e[0] = ss.row0[0] = ss.blk0[0] = 0;
+    ss.m[0] = p.T;
+    ss.blk0[1] = 1;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
   volatile int* abort = &ss.abort;
-  const int arrivals = kRowGroups * gridDim.x;
+  const int arrivals = kRowWarps * gridDim.x;
   if (warp == kWeightWarp) {
     if (lane == 0) {
       Ring rg;
       Drain dr;
       bool ok = true;
-      if (LAYER) ok = produce_weights<G>(p, 0, ss, ring, rg, dr, abort);
-      if (ok) produce_weights<G>(p, 1, ss, ring, rg, dr, abort);
+      if (LAYER) ok = produce_weights<G, false>(p, 0, ss, ring, rg, dr, abort);
+      if (ok) produce_weights<G, LAYER>(p, 1, ss, ring, rg, dr, abort);
       dr.wait(ss.full_w);
     }
     __syncwarp();
   } else if (warp == kColumnWarp) {
-    Ring rg;
-    bool ok = true;
-    if (LAYER) {
-      ok = produce_columns<G, LAYER>(p, 0, ss, ring, rg, abort);
-      if (ok) {  // every hidden value of every CTA
-        if (lane == 0) ok = wait_count(p.err + kCtrHidden, arrivals, abort, p.err, 0x25 << 24);
-        ok = __shfl_sync(kFull, ok, 0);
+    if (lane == 0) {
+      Ring rg;
+      Drain dr;
+      bool ok = true;
+      if (LAYER) {
+        ok = produce_columns<G, false>(p, 0, ss, ring, rg, dr, abort);
+        // every hidden value of every CTA, for the bulk copies of this one
+        ok = ok && wait_count(p.err + kCtrHidden, arrivals, abort, p.err, 0x25 << 24);
+        fence_proxy_async_global();
       }
+      if (ok) ok = produce_columns<G, LAYER>(p, 1, ss, ring, rg, dr, abort);
+      // One poller a CTA: with one per warp the counter's L2 slice was so busy
+      // answering that the last arrivals came through 8 us late.
+      if (LAYER && ok && wait_count(p.err + kCtrOut, arrivals, abort, p.err, 0x26 << 24)) mbar_arrive(&ss.out_done);
+      dr.wait(ss.full_x);
     }
-    if (ok) produce_columns<G, LAYER>(p, 1, ss, ring, rg, abort);
-    cp_async_wait_all();
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    if (lane == 0) {
+      Ring rg;
+      Turn tn;
+      bool ok = true;
+      if (LAYER) ok = issue_mmas<G, false>(p, 0, ss, ring, rg, tn, abort);
+      if (ok) issue_mmas<G, LAYER>(p, 1, ss, ring, rg, tn, abort);
+      umma_commit(&ss.drained);
+      drain_wait(&ss.drained, 0);
+    }
+    __syncwarp();
   } else {
-    Consumer cs;
-    bool ok;
+    Ring rg;
+    Turn tn;
+    uint32_t swap = 0;
+    bool ok = true;
     if (LAYER) {
       // Counted even after a wait that gave up, so that the counters come
       // back to 0 and the other CTAs go on (the error word is set by then).
       auto publish = [&](int counter) {
         __syncwarp();
-        if (warp < kRowGroups && lane == 0) red_release_gpu_add(p.err + counter, 1);
+        if (lane == 0) red_release_gpu_add(p.err + counter, 1);
       };
-      ok = consume<G, LAYER, 1>(p, 0, ss, ring, xbuf, cs, abort);
+      if constexpr (Ge::Q4)
+        ok = rows_q4<G, false, LAYER>(p, 0, ss, ring, rg, tn, swap, abort);
+      else
+        ok = rows_bf16<false, LAYER>(p, 0, ss, tn, abort);
+      fence_proxy_async_global();  // hidden values, to other CTAs' bulk copies
       publish(kCtrHidden);
-      if (ok) ok = p.parts == 3 ? consume<G, LAYER, 3>(p, 1, ss, ring, xbuf, cs, abort)
-                                : consume<G, LAYER, 2>(p, 1, ss, ring, xbuf, cs, abort);
+      if (ok) {
+        if constexpr (Ge::Q4)
+          ok = rows_q4<G, true, LAYER>(p, 1, ss, ring, rg, tn, swap, abort);
+        else
+          ok = rows_bf16<true, LAYER>(p, 1, ss, tn, abort);
+      }
       publish(kCtrOut);
-      if (lane == 0) ok = ok && wait_count(p.err + kCtrOut, arrivals, abort, p.err, 0x26 << 24);
-      if (__shfl_sync(kFull, ok, 0)) sum_rows(p, ss);
+      ok = ok && mbar_wait(&ss.out_done, 0, abort, p.err, 0x2A << 24);
+      if (__all_sync(kFull, ok)) sum_rows(p, ss);
     } else {
-      consume<G, LAYER, 1>(p, 1, ss, ring, xbuf, cs, abort);
+      if constexpr (Ge::Q4)
+        rows_q4<G, false, LAYER>(p, 1, ss, ring, rg, tn, swap, abort);
+      else
+        rows_bf16<false, LAYER>(p, 1, ss, tn, abort);
     }
   }
-  if (LAYER) {  // the last CTA to pass its waits clears the counters
-    __syncthreads();
-    if (tid == 0 && atomicAdd(p.err + kCtrExit, 1) == static_cast<int>(gridDim.x) - 1) {
-      p.err[kCtrHidden] = 0;
-      p.err[kCtrOut] = 0;
-      p.err[kCtrExit] = 0;
-    }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc(ss.tmem, kTmemCols);
+  // the last CTA to pass its waits clears the counters
+  if (LAYER && tid == 0 && atomicAdd(p.err + kCtrExit, 1) == static_cast<int>(gridDim.x) - 1) {
+    p.err[kCtrHidden] = 0;
+    p.err[kCtrOut] = 0;
+    p.err[kCtrExit] = 0;
   }
 }
 
@@ -814,7 +1053,7 @@ int workers() { return std::min(num_sms(), kMaxWorkers); }
 struct Layout {
   size_t part, arrive, h, o, total;
 };
-// Error region (with the counters), parts, their arrival counters, hidden rows, output rows.
+// Error region (with the counters), arrival counters, parts, hidden rows, output rows.
 Layout layout(size_t rows, size_t d, size_t f) {
   Layout L{};
   size_t o = kErrRegionBytes;
@@ -823,8 +1062,8 @@ Layout layout(size_t rows, size_t d, size_t f) {
     o = align_up(o + bytes, 256);
     return at;
   };
-  L.arrive = take(sizeof(int) * 2 * kMaxWorkers * kRowGroups);
-  L.part = take(sizeof(float) * kMaxWorkers * kRowGroups * 16 * 32);
+  L.arrive = take(sizeof(int) * 2 * kMaxWorkers * kRowWarps);
+  L.part = take(sizeof(float) * kMaxWorkers * 2 * kMaxTokens * kTileRows);
   L.h = take(3 * sizeof(uint16_t) * rows * f);
   L.o = take(sizeof(float) * rows * d);
   L.total = o;
@@ -837,11 +1076,11 @@ bool fill_product(Product& pr, int which, const DecodeWeight& w0, const DecodeWe
   pr.K = K;
   pr.kblocks = ceil_div(K, Ge::KB);
   pr.rows = rows;
-  pr.row_step = which == 0 ? kBoxRows : 2 * kBoxRows;
+  pr.row_step = which == 0 ? kTileRows : 2 * kTileRows;
   pr.row_tiles = ceil_div(rows, pr.row_step);
   auto box = [&](CUtensorMap* m, const DecodeWeight& w) {
-    return Ge::Q4 ? map2d_any(m, w.w, 1, K / 2, mats * rows, 128, kBoxRows, CU_TENSOR_MAP_SWIZZLE_128B)
-                  : map2d(m, w.w, K, mats * rows, 64, kBoxRows);
+    return Ge::Q4 ? map2d_any(m, w.w, 1, K / 2, mats * rows, 128, kTileRows, CU_TENSOR_MAP_SWIZZLE_128B)
+                  : map2d(m, w.w, K, mats * rows, 64, kTileRows);
   };
   bool ok = box(&pr.w0, w0);
   if (w1.w == w0.w)
@@ -850,7 +1089,7 @@ bool fill_product(Product& pr, int which, const DecodeWeight& w0, const DecodeWe
     ok = ok && box(&pr.w1, w1);
   if constexpr (Ge::Q4) {
     auto sc = [&](CUtensorMap* m, const DecodeWeight& w) {
-      return map2d_any(m, w.scales, 2, q4_scale_pitch(rows), mats * (K / G), kBoxRows, Ge::GROUPS,
+      return map2d_any(m, w.scales, 2, q4_scale_pitch(rows), mats * (K / G), kTileRows, Ge::GROUPS,
                        CU_TENSOR_MAP_SWIZZLE_NONE);
     };
     ok = ok && sc(&pr.s0, w0);
@@ -864,16 +1103,15 @@ bool fill_product(Product& pr, int which, const DecodeWeight& w0, const DecodeWe
 
 constexpr int kSmemMax = 232448;  // 227 KB
 
-// Stages that fit beside the tables, and the launch's shared memory.
+// Stages that fit beside the tables, and the launch's shared memory.  A stage
+// has room for the widest tile: `cols` columns.
 template <int G>
-size_t ring_shape(StreamParams& p, int parts) {
+size_t ring_shape(StreamParams& p, int cols) {
   using Ge = Geo<G>;
-  const int cols = std::min(p.T, Ge::COLS);
-  const int nt = cols <= 8 ? 1 : cols <= 16 ? 2 : 4;
-  p.cols8 = nt * 8;  // rows that the widest tile's instructions read
-  p.xbuf_bytes = kRowGroups * 32 * nt * 4 * static_cast<int>(sizeof(float));
-  p.stage_bytes = static_cast<int>(align_up(2 * (kBoxBytes + Ge::SCALE_BYTES) + parts * p.cols8 * Ge::PITCH, 1024));
-  const size_t fixed = kSharedBytes + p.xbuf_bytes + 1024;
+  p.acc_cols = cols;
+  p.acc_bufs = std::min(2, kTmemCols / (2 * cols));
+  p.stage_bytes = static_cast<int>(align_up(Ge::WEIGHT_BYTES + Ge::ATOMS * cols * 128, 1024));
+  const size_t fixed = kSharedBytes + 1024;
   p.stages = std::min<int>(kMaxStages, static_cast<int>((kSmemMax - fixed) / p.stage_bytes));
   return fixed + static_cast<size_t>(p.stages) * p.stage_bytes;
 }
@@ -900,26 +1138,39 @@ int launch_stream(StreamParams& p, size_t smem, int grid_limit, cudaStream_t s) 
   return cudaLaunchKernelEx(&cfg, stream_kernel<G, LAYER>, p) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
+void common_params(StreamParams& p, void* ws, const Layout& L, int T, void* y, int y_type) {
+  uint8_t* at = static_cast<uint8_t*>(ws);
+  p.T = T;
+  p.tcols = ceil_div(T, 16) * 16;
+  p.part = reinterpret_cast<float*>(at + L.part);
+  p.arrive = reinterpret_cast<int*>(at + L.arrive);
+  p.y = y;
+  p.y_type = y_type;
+  p.err = static_cast<int*>(ws);
+  p.workers = workers();
+}
+
 template <int G>
 int decode_g(const DecodeArgs& a, cudaStream_t s) {
   const moe_cfg& c = a.c;
   StreamParams p;
   std::memset(&p, 0, sizeof(p));
   const uint64_t mats = c.E + c.n_shared;
-  if (!fill_product<G>(p.p[0], 0, a.W1, a.W3, mats, c.d_ff, c.d_model) ||
-      !fill_product<G>(p.p[1], 1, a.W2, a.W2, mats, c.d_model, c.d_ff))
-    return MOE_ERR_CUDA;
+  const uint64_t Rs = static_cast<uint64_t>(c.T) * (c.k + c.n_shared);
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
-  const Layout L = layout(static_cast<size_t>(c.T) * (c.k + c.n_shared), c.d_model, c.d_ff);
-  p.T = c.T, p.d = c.d_model, p.f = c.d_ff, p.E = c.E, p.k = c.k, p.S = c.n_shared, p.renorm = c.renorm;
-  p.logits = a.logits, p.x = a.x, p.topk_idx = a.topk_idx, p.topk_w = a.topk_w;
+  const Layout L = layout(Rs, c.d_model, c.d_ff);
+  common_params(p, a.ws, L, c.T, a.y, a.y_type);
+  p.d = c.d_model, p.f = c.d_ff, p.E = c.E, p.k = c.k, p.S = c.n_shared, p.renorm = c.renorm;
+  p.logits = a.logits, p.topk_idx = a.topk_idx, p.topk_w = a.topk_w;
   p.h = reinterpret_cast<uint16_t*>(ws + L.h);
   p.o = reinterpret_cast<float*>(ws + L.o);
-  p.part = reinterpret_cast<float*>(ws + L.part);
-  p.arrive = reinterpret_cast<int*>(ws + L.arrive);
-  p.y = a.y, p.y_type = a.y_type, p.err = reinterpret_cast<int*>(ws), p.workers = workers();
   p.parts = a.y_type == MOE_Y_F32 ? 3 : 2;
-  const size_t smem = ring_shape<G>(p, p.parts);
+  p.h_block = Geo<G>::h_rows(p.parts);
+  if (!fill_product<G>(p.p[0], 0, a.W1, a.W3, mats, c.d_ff, c.d_model) ||
+      !fill_product<G>(p.p[1], 1, a.W2, a.W2, mats, c.d_model, c.d_ff) ||
+      !map2d(&p.p[0].cols, a.x, c.d_model, c.T, 64, p.tcols) || !map2d(&p.p[1].cols, p.h, c.d_ff, p.parts * Rs, 64, 16))
+    return MOE_ERR_CUDA;
+  const size_t smem = ring_shape<G>(p, std::max(p.tcols, p.parts * std::min(p.tcols, p.h_block)));
   TraceScope trace_scope(MOE_K_DECODE, s);
   return launch_stream<G, true>(p, smem, a.grid_limit, s);
 }
@@ -928,14 +1179,12 @@ template <int G>
 int linear_g(const LinearArgs& a, cudaStream_t s) {
   StreamParams p;
   std::memset(&p, 0, sizeof(p));
-  if (!fill_product<G>(p.p[1], 1, a.W, a.W, 1, a.n, a.K)) return MOE_ERR_CUDA;
-  uint8_t* ws = static_cast<uint8_t*>(a.ws);
-  const Layout L = layout(0, 0, 0);
-  p.T = a.T, p.n = a.n, p.x = a.x;
-  p.part = reinterpret_cast<float*>(ws + L.part);
-  p.arrive = reinterpret_cast<int*>(ws + L.arrive);
-  p.y = a.y, p.y_type = a.y_type, p.err = reinterpret_cast<int*>(ws), p.workers = workers();
-  const size_t smem = ring_shape<G>(p, 1);
+  common_params(p, a.ws, layout(0, 0, 0), a.T, a.y, a.y_type);
+  p.n = a.n;
+  p.h_block = kMaxTokens;
+  if (!fill_product<G>(p.p[1], 1, a.W, a.W, 1, a.n, a.K) || !map2d(&p.p[1].cols, a.x, a.K, a.T, 64, p.tcols))
+    return MOE_ERR_CUDA;
+  const size_t smem = ring_shape<G>(p, p.tcols);
   TraceScope trace_scope(MOE_K_LINEAR, s);
   return launch_stream<G, false>(p, smem, a.grid_limit, s);
 }
