@@ -28,11 +28,10 @@
 //     fp32 on its way out, so no weight is rounded.
 //   - The tiles of all picked experts form one sequence of K blocks, cut into
 //     equal contiguous ranges, one per SM, so no SM idles whatever the number
-//     of experts, rows and tokens.  A tile cut by a range border belongs to
-//     the range it begins in.  The ranges it goes on in work on it first and
-//     leave their sums in the workspace; its owner comes to it last, long
-//     after, and adds them in range order: no floating-point atomics, and
-//     nobody waits in the middle of a range.
+//     of experts, rows and tokens.  Every range that works on a cut tile
+//     leaves its sums in the workspace and, once through its range, adds up
+//     all of them, in range order, for its share of the tile's columns: no
+//     floating-point atomics, and nobody waits in the middle of a range.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -85,9 +84,9 @@ struct Geo {
   static constexpr int SCALE_BYTES = GROUPS * kTileRows * 2;   // of one box
   static constexpr int WEIGHT_BYTES = 2 * (kBoxBytes + SCALE_BYTES);
   // Tensor memory, 4 bits: two operand buffers of G / 2 words for either box,
-  // then two accumulators of each (one group each) of ACC columns.
-  [[maybe_unused]] static constexpr int A_COLS = G / 2;
-  [[maybe_unused]] static constexpr int ACC = (kTmemCols - 4 * A_COLS) / 4;
+  // then two accumulators of each (one group each).
+  static __host__ __device__ constexpr int a_cols() { return G / 2; }
+  static __host__ __device__ constexpr int acc_cols() { return (kTmemCols - 4 * a_cols()) / 4; }
   // Rows of h in one tile of the second product.  bf16 weights: all of them.
   // 4 bits: what the accumulators hold; an expert with more rows has its
   // weight tiles visited again, from L2.
@@ -110,8 +109,8 @@ struct StreamParams {
   float* topk_w;
   uint16_t* h;          // [parts][Rs][f]
   float* o;             // [Rs][d]
-  float* part;          // sums of the tile that a range begins in: [workers][2][64][128]
-  int* arrive;          // row warps that left theirs there, by the owning range: [2][workers][row warps]
+  float* part;          // sums of the tiles that a range begins and ends in: [workers][2][2 boxes][64][128]
+  int* arrive;          // row warps that left theirs there, by the first range of the tile: [2][workers]
   void* y;
   int* err;             // error word and counters
   int y_type, workers, stages, stage_bytes;
@@ -140,6 +139,8 @@ struct alignas(16) Shared {
   float pick_w[kMaxPicks];
   short pick_e[kMaxPicks];
   short pick_row[kMaxPicks];
+  short entry[256];                // expert's place in the work list
+  unsigned scan[8];                // packed sums of 32 experts each
   unsigned char row_token[kMaxRows];
 };
 constexpr int kSharedBytes = (sizeof(Shared) + 127) / 128 * 128;
@@ -150,140 +151,149 @@ constexpr int kSharedBytes = (sizeof(Shared) + 127) / 128 * 128;
 // an expert at most once, so an expert's tokens are a 64-bit mask and a row's
 // place in its expert's list is a population count: ascending tokens,
 // whatever the order of the atomics that set the bits.
-template <int EPL>
-__device__ __forceinline__ void route_tokens(const StreamParams& p, Shared& ss) {
+template <int EPL, int U>
+__device__ __forceinline__ void route_all(const StreamParams& p, Shared& ss) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float ahead[EPL];  // the next token's logits
-  if (warp < p.T) row_load<EPL>(p.logits + static_cast<size_t>(warp) * p.E, p.E, lane, ahead);
-  for (int t = warp; t < p.T; t += kWarps) {
-    RowSoftmax<EPL> r;
+  RowSoftmax<EPL> r[U];
+  int t[U];
+  auto load = [&](int t0) {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) r.v[i] = ahead[i];
-    if (t + kWarps < p.T) row_load<EPL>(p.logits + static_cast<size_t>(t + kWarps) * p.E, p.E, lane, ahead);
-    int idx;
-    float w;
-    route_token<EPL>(r, t, p.E, p.k, p.renorm, lane, p.err, idx, w);
-    if (lane < p.k) {
-      ss.pick_e[t * p.k + lane] = static_cast<short>(idx);
-      ss.pick_w[t * p.k + lane] = w;
-      atomicOr(&ss.mask[idx][t >> 5], 1u << (t & 31));
-      if (blockIdx.x == 0) {
-        p.topk_idx[t * p.k + lane] = idx;
-        p.topk_w[t * p.k + lane] = w;
-      }
+    for (int u = 0; u < U; ++u) {
+      t[u] = t0 + u * kWarps;
+      const int from = min(t[u], p.T - 1);
+      row_load<EPL>(p.logits + static_cast<size_t>(from) * p.E, p.E, lane, r[u].v);
     }
+  };
+  load(warp);  // in flight while the masks are cleared
+  for (int i = threadIdx.x; i < 512; i += kThreads) (&ss.mask[0][0])[i] = 0;
+  __syncthreads();
+  for (int t0 = warp; t0 < p.T; t0 += U * kWarps) {
+    int idx[U];
+    float w[U];
+    route_tokens<EPL, U>(r, t, p.E, p.k, p.renorm, lane, p.err, idx, w);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (lane < p.k && t[u] < p.T) {
+        const int at = t[u] * p.k + lane;
+        ss.pick_e[at] = static_cast<short>(idx[u]);
+        ss.pick_w[at] = w[u];
+        atomicOr(&ss.mask[idx[u]][t[u] >> 5], 1u << (t[u] & 31));
+        if (blockIdx.x == 0) {
+          p.topk_idx[at] = idx[u];
+          p.topk_w[at] = w[u];
+        }
+      }
+    if (t0 + U * kWarps < p.T) load(t0 + U * kWarps);
   }
 }
 
-__device__ void build_work_list(const StreamParams& p, Shared& ss) {
-  const int tid = threadIdx.x, lane = tid & 31;
-  for (int i = tid; i < 512; i += kThreads) (&ss.mask[0][0])[i] = 0;
-  __syncthreads();
-  if (p.E <= 32)
-    route_tokens<1>(p, ss);
-  else if (p.E <= 64)
-    route_tokens<2>(p, ss);
-  else if (p.E <= 128)
-    route_tokens<4>(p, ss);
+template <int EPL>
+__device__ __forceinline__ void route_any(const StreamParams& p, Shared& ss) {
+  // more tokens than warps: several at a time on a warp
+  if (EPL <= 4 && p.T > kWarps)
+    route_all<EPL, EPL <= 2 ? 3 : 2>(p, ss);
   else
-    route_tokens<8>(p, ss);
+    route_all<EPL, 1>(p, ss);
+}
+
+__device__ void build_work_list(const StreamParams& p, Shared& ss) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (p.E <= 32)
+    route_any<1>(p, ss);
+  else if (p.E <= 64)
+    route_any<2>(p, ss);
+  else if (p.E <= 128)
+    route_any<4>(p, ss);
+  else
+    route_any<8>(p, ss);
   __syncthreads();
   const int R = p.T * p.k;
-  if (tid < 32) {  // experts 8 lane .. 8 lane + 7: exclusive sums of entries, rows and blocks of h rows
-    int n[8], na = 0, nr = 0, nb = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int e = lane * 8 + j;
-      n[j] = e < p.E ? __popc(ss.mask[e][0]) + __popc(ss.mask[e][1]) : 0;
-      na += n[j] > 0;
-      nr += n[j];
-      nb += (n[j] + p.h_block - 1) / p.h_block;
-    }
-    int ia = na, ir = nr, ib = nb;
+  // Thread e: expert e.  Exclusive sums of rows, entries and blocks of h rows
+  // over the experts, packed into 11 + 10 + 11 bits (at most 512, 256 and 288).
+  unsigned mine = 0, incl = 0;
+  int n = 0;
+  if (tid < 256) {
+    n = tid < p.E ? __popc(ss.mask[tid][0]) + __popc(ss.mask[tid][1]) : 0;
+    mine = n ? static_cast<unsigned>(n) | 1u << 11 | static_cast<unsigned>((n + p.h_block - 1) / p.h_block) << 21 : 0u;
+    incl = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const int xa = __shfl_up_sync(kFull, ia, off), xr = __shfl_up_sync(kFull, ir, off),
-                xb = __shfl_up_sync(kFull, ib, off);
-      if (lane >= off) ia += xa, ir += xr, ib += xb;
+      const unsigned x = __shfl_up_sync(kFull, incl, off);
+      if (lane >= off) incl += x;
     }
-    const int all_a = __shfl_sync(kFull, ia, 31), all_b = __shfl_sync(kFull, ib, 31);
-    ia -= na, ir -= nr, ib -= nb;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (n[j] == 0) continue;
-      ss.e[ia] = lane * 8 + j;
-      ss.m[ia] = n[j];
-      ss.row0[ia] = ir;
-      ss.blk0[ia] = ib;
-      ++ia;
-      ir += n[j];
-      ib += (n[j] + p.h_block - 1) / p.h_block;
-    }
-    const int per = (p.T + p.h_block - 1) / p.h_block;
-    if (lane < p.S) {
-      ss.e[all_a + lane] = p.E + lane;
-      ss.m[all_a + lane] = p.T;
-      ss.row0[all_a + lane] = R + lane * p.T;
-      ss.blk0[all_a + lane] = all_b + lane * per;
-    }
-    if (lane == 0) {
-      ss.nact = all_a + p.S;
-      ss.nblk = all_b + p.S * per;
-      ss.blk0[all_a + p.S] = all_b + p.S * per;
-    }
+    if (lane == 31) ss.scan[warp] = incl;
   }
   __syncthreads();
-  // rows: first row of the expert (entry by binary search) + earlier tokens of its mask
-  for (int i = tid; i < R; i += kThreads) {
-    const int e = ss.pick_e[i], t = i / p.k;
-    int lo = 0, hi = ss.nact - p.S - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi) / 2;
-      if (ss.e[mid] < e)
-        lo = mid + 1;
-      else
-        hi = mid;
-    }
-    const unsigned m0 = ss.mask[e][0], m1 = ss.mask[e][1], below = (1u << (t & 31)) - 1u;
-    const int row = ss.row0[lo] + (t < 32 ? __popc(m0 & below) : __popc(m0) + __popc(m1 & below));
-    ss.pick_row[i] = static_cast<short>(row);
-    ss.row_token[row] = static_cast<unsigned char>(t);
-    ss.row_w[row] = ss.pick_w[i];
+  unsigned before = 0, all = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const unsigned x = ss.scan[i];
+    if (i < warp) before += x;
+    all += x;
+  }
+  const int all_a = all >> 11 & 1023, all_b = all >> 21;
+  if (tid < 256 && n) {
+    const unsigned at = before + incl - mine;
+    const int a = at >> 11 & 1023;
+    ss.entry[tid] = static_cast<short>(a);
+    ss.e[a] = tid;
+    ss.m[a] = n;
+    ss.row0[a] = at & 2047;
+    ss.blk0[a] = at >> 21;
+  }
+  const int per = (p.T + p.h_block - 1) / p.h_block;
+  if (tid < p.S) {
+    ss.e[all_a + tid] = p.E + tid;
+    ss.m[all_a + tid] = p.T;
+    ss.row0[all_a + tid] = R + tid * p.T;
+    ss.blk0[all_a + tid] = all_b + tid * per;
+  }
+  if (tid == 0) {
+    ss.nact = all_a + p.S;
+    ss.nblk = all_b + p.S * per;
+    ss.blk0[all_a + p.S] = all_b + p.S * per;
   }
   for (int i = tid; i < p.S * p.T; i += kThreads) {
     ss.row_token[R + i] = static_cast<unsigned char>(i % p.T);
     ss.row_w[R + i] = 1.f;
   }
   __syncthreads();
+  // rows: first row of the expert + earlier tokens of its mask
+  for (int i = tid; i < R; i += kThreads) {
+    const int e = ss.pick_e[i], t = i / p.k;
+    const unsigned m0 = ss.mask[e][0], m1 = ss.mask[e][1], below = (1u << (t & 31)) - 1u;
+    const int row = ss.row0[ss.entry[e]] + (t < 32 ? __popc(m0 & below) : __popc(m0) + __popc(m1 & below));
+    ss.pick_row[i] = static_cast<short>(row);
+    ss.row_token[row] = static_cast<unsigned char>(t);
+    ss.row_w[row] = ss.pick_w[i];
+  }
 }
 
 // ------------------------------------------------------------------ ranges
-// The K blocks of a product, tile after tile (expert, row tile, block
-// of h rows), cut into `workers` contiguous ranges.  Every role of a CTA walks
-// the same segments: the K blocks [kb0, kb1) of one tile.
+// The K blocks of a product, tile after tile, cut into `workers` contiguous
+// ranges.  Every role of a CTA walks the same segments: the K blocks
+// [kb0, kb1) of one tile.  The tiles of one row tile of all experts follow
+// each other, so the shared experts, which have the most rows to finish, are
+// spread over the ranges.
 struct Segment {
   int worker, item, kb0, kb1;
   int a, rt, nb;   // work list entry, row tile, block of h rows (second product of the layer)
 };
 
-template <bool BLOCKS>  // more than one tile column wise: the layer's second product
+template <bool BLOCKS>  // an expert may have several blocks of h rows: the layer's second product
 struct Walk {
   const Product& pr;
   const Shared& ss;
   int workers, v;
-  int units, u, u1;
-  int item, kb, a;
+  int units, per;    // K blocks, tiles of a row tile
+  int u, u1;
 
-  // A CTA takes the ranges blockIdx.x + i * gridDim.x in descending order:
-  // the owner of a cut tile waits for ranges after its own, so on a capped
-  // grid those come first.
   __device__ Walk(const Product& product, const Shared& shared, int most) : pr(product), ss(shared) {
-    units = (BLOCKS ? ss.nblk : ss.nact) * pr.row_tiles * pr.kblocks;
+    per = BLOCKS ? ss.nblk : ss.nact;
+    units = per * pr.row_tiles * pr.kblocks;
     workers = min(most, units);  // no range is empty
-    const int b = static_cast<int>(blockIdx.x), n = static_cast<int>(gridDim.x);
-    v = b < workers ? b + ((workers - 1 - b) / n + 1) * n : 0;
+    v = static_cast<int>(blockIdx.x) - static_cast<int>(gridDim.x);
     u = u1 = 0;
-    item = kb = a = 0;
   }
   __device__ int begin_of(int worker) const {
     return static_cast<int>(static_cast<long long>(units) * worker / workers);
@@ -292,44 +302,39 @@ struct Walk {
   __device__ int worker_of(int unit) const {
     return static_cast<int>((static_cast<long long>(unit + 1) * workers - 1) / units);
   }
-  __device__ bool next(Segment& s) {
-    if (u >= u1) {
-      v -= static_cast<int>(gridDim.x);
-      if (v < 0) return false;
-      u = begin_of(v);
-      u1 = begin_of(v + 1);
-      item = u / pr.kblocks;
-      kb = u - item * pr.kblocks;
-      if (BLOCKS) {
-        int lo = 0, hi = ss.nact - 1;   // last entry with blk0 * row_tiles <= item
-        while (lo < hi) {
-          const int mid = (lo + hi + 1) / 2;
-          if (ss.blk0[mid] * pr.row_tiles <= item)
-            lo = mid;
-          else
-            hi = mid - 1;
-        }
-        a = lo;
-      }
-    }
+  __device__ void locate(int item, Segment& s) const {
+    s.item = item;
+    s.rt = item / per;
+    const int r = item - s.rt * per;
     if (BLOCKS) {
-      while (item >= ss.blk0[a + 1] * pr.row_tiles) ++a;
-      const int nblk = ss.blk0[a + 1] - ss.blk0[a], r = item - ss.blk0[a] * pr.row_tiles;
-      s.a = a;
-      s.rt = r / nblk;
-      s.nb = r - s.rt * nblk;
+      int lo = 0, hi = ss.nact - 1;   // last entry with blk0 <= r
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (ss.blk0[mid] <= r)
+          lo = mid;
+        else
+          hi = mid - 1;
+      }
+      s.a = lo;
+      s.nb = r - ss.blk0[lo];
     } else {
-      s.a = item / pr.row_tiles;
-      s.rt = item - s.a * pr.row_tiles;
+      s.a = r;
       s.nb = 0;
     }
+  }
+  __device__ bool next(Segment& s) {
+    if (u >= u1) {
+      v += static_cast<int>(gridDim.x);
+      if (v >= workers) return false;
+      u = begin_of(v);
+      u1 = begin_of(v + 1);
+    }
+    const int item = u / pr.kblocks;
+    locate(item, s);
     s.worker = v;
-    s.item = item;
-    s.kb0 = kb;
-    s.kb1 = min(pr.kblocks, kb + (u1 - u));
+    s.kb0 = u - item * pr.kblocks;
+    s.kb1 = min(pr.kblocks, s.kb0 + (u1 - u));
     u += s.kb1 - s.kb0;
-    kb = 0;
-    ++item;
     return true;
   }
 };
@@ -405,6 +410,16 @@ struct Columns {
   }
 };
 
+// The producers and the issuer of the tensor instructions run as whole warps
+// and elect a lane for the asynchronous instructions: their operands are warp
+// registers, and the compiler gets them there without a loop over the lanes
+// only where it sees that the warp is together (64 and more clocks an
+// instruction otherwise, against 19 for the smallest tensor instruction).
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* err, int where) {
+  const bool ok = mbar_wait(bar, parity, abort, err, where);
+  return __all_sync(kFull, ok);
+}
+
 // Everything below is written for one product: `which` picks its tensor maps,
 // H says that its columns are rows of h.
 // --------------------------------------------------------------- producers
@@ -418,21 +433,25 @@ __device__ bool produce_weights(const StreamParams& p, int which, Shared& ss, ui
   while (walk.next(s)) {
     const int row = ss.e[s.a] * pr.rows + s.rt * pr.row_step;
     const int beside = which == 0 ? 0 : kTileRows;  // W3 beside W1, or the tile's other rows
+    [[maybe_unused]] const int scale_row = Ge::Q4 ? ss.e[s.a] * (pr.K / (Ge::Q4 ? G : 1)) : 0;
     for (int kb = s.kb0; kb < s.kb1; ++kb) {
-      if (!mbar_wait(&ss.empty[rg.stage], rg.phase ^ 1, abort, p.err, (0x21 << 24) | which)) return false;
+      if (!warp_wait(&ss.empty[rg.stage], rg.phase ^ 1, abort, p.err, (0x21 << 24) | which)) return false;
       uint8_t* st = ring + static_cast<size_t>(rg.stage) * p.stage_bytes;
       uint64_t* bar = &ss.full_w[rg.stage];
-      mbar_arrive_expect_tx(bar, Ge::WEIGHT_BYTES);
       dr.note(rg.stage, rg.phase);
-      const int col = kb * (Ge::Q4 ? 128 : 64);  // bytes or bf16
-      tma_load_2d(st, &pr.w0, bar, col, row);
-      tma_load_2d(st + kBoxBytes, &pr.w1, bar, col, row + beside);
-      if constexpr (Ge::Q4) {
-        uint8_t* sc = st + 2 * kBoxBytes;
-        const int at = ss.e[s.a] * (pr.K / G) + kb * Ge::GROUPS, r0 = s.rt * pr.row_step;
-        tma_load_2d(sc, &pr.s0, bar, r0, at);
-        tma_load_2d(sc + Ge::SCALE_BYTES, &pr.s1, bar, r0 + beside, at);
+      if (elect_one()) {
+        mbar_arrive_expect_tx(bar, Ge::WEIGHT_BYTES);
+        const int col = kb * (Ge::Q4 ? 128 : 64);  // bytes or bf16
+        tma_load_2d(st, &pr.w0, bar, col, row);
+        tma_load_2d(st + kBoxBytes, &pr.w1, bar, col, row + beside);
+        if constexpr (Ge::Q4) {
+          uint8_t* sc = st + 2 * kBoxBytes;
+          const int at = scale_row + kb * Ge::GROUPS, r0 = s.rt * pr.row_step;
+          tma_load_2d(sc, &pr.s0, bar, r0, at);
+          tma_load_2d(sc + Ge::SCALE_BYTES, &pr.s1, bar, r0 + beside, at);
+        }
       }
+      __syncwarp();
       rg.step(p.stages);
     }
   }
@@ -451,23 +470,26 @@ __device__ bool produce_columns(const StreamParams& p, int which, Shared& ss, ui
   while (walk.next(s)) {
     const Columns<H> c(p, ss, s);
     for (int kb = s.kb0; kb < s.kb1; ++kb) {
-      if (!mbar_wait(&ss.empty[rg.stage], rg.phase ^ 1, abort, p.err, (0x22 << 24) | which)) return false;
+      if (!warp_wait(&ss.empty[rg.stage], rg.phase ^ 1, abort, p.err, (0x22 << 24) | which)) return false;
       uint8_t* st = ring + static_cast<size_t>(rg.stage) * p.stage_bytes + Ge::WEIGHT_BYTES;
       uint64_t* bar = &ss.full_x[rg.stage];
-      mbar_arrive_expect_tx(bar, Ge::ATOMS * c.n * 128);
       dr.note(rg.stage, rg.phase);
-#pragma unroll 1
-      for (int at = 0; at < Ge::ATOMS; ++at) {
-        uint8_t* dst = st + at * c.n * 128;
-        const int col = (kb * Ge::ATOMS + at) * 64;
-        if (!H) {
-          tma_load_2d(dst, &pr.cols, bar, col, 0);
-        } else {
-          for (int q = 0; q < p.parts; ++q)
-            for (int i = 0; i < c.n16; ++i)
-              tma_load_2d(dst + (q * c.n16 + i) * 2048, &pr.cols, bar, col, q * Rs + c.r0 + i * 16);
+      if (elect_one()) {
+        mbar_arrive_expect_tx(bar, Ge::ATOMS * c.n * 128);
+#pragma unroll
+        for (int at = 0; at < Ge::ATOMS; ++at) {
+          uint8_t* dst = st + at * c.n * 128;
+          const int col = (kb * Ge::ATOMS + at) * 64;
+          if (!H) {
+            tma_load_2d(dst, &pr.cols, bar, col, 0);
+          } else {
+            for (int q = 0; q < p.parts; ++q)
+              for (int i = 0; i < c.n16; ++i)
+                tma_load_2d(dst + (q * c.n16 + i) * 2048, &pr.cols, bar, col, q * Rs + c.r0 + i * 16);
+          }
         }
       }
+      __syncwarp();
       rg.step(p.stages);
     }
   }
@@ -505,49 +527,57 @@ __device__ bool issue_mmas(const StreamParams& p, int which, Shared& ss, uint8_t
     const Columns<H> c(p, ss, s);
     const uint32_t idesc = idesc_bf16_f32(kTileRows, c.n, 0, 0);
     if constexpr (!Ge::Q4)
-      if (!mbar_wait(&ss.acc_empty[tn.buf], tn.phase ^ 1, abort, p.err, (0x31 << 24) | which)) return false;
+      if (!warp_wait(&ss.acc_empty[tn.buf], tn.phase ^ 1, abort, p.err, (0x31 << 24) | which)) return false;
     for (int kb = s.kb0; kb < s.kb1; ++kb) {
       const uint32_t st = smem_u32(ring) + static_cast<uint32_t>(rg.stage) * p.stage_bytes;
       const uint32_t x = st + Ge::WEIGHT_BYTES;
-      if (!mbar_wait(&ss.full_x[rg.stage], rg.phase, abort, p.err, (0x24 << 24) | which)) return false;
+      if (!warp_wait(&ss.full_x[rg.stage], rg.phase, abort, p.err, (0x24 << 24) | which)) return false;
       if constexpr (!Ge::Q4) {
-        if (!mbar_wait(&ss.full_w[rg.stage], rg.phase, abort, p.err, (0x23 << 24) | which)) return false;
+        if (!warp_wait(&ss.full_w[rg.stage], rg.phase, abort, p.err, (0x23 << 24) | which)) return false;
         tc_fence_after();
         const uint32_t acc = tmem + tn.buf * 2 * p.acc_cols;
+        if (elect_one()) {
 #pragma unroll
-        for (int k4 = 0; k4 < 4; ++k4) {
-          const uint64_t bd = smem_desc_sw128(x + k4 * 32, 16, 1024);
-          const uint32_t go_on = (kb != s.kb0 || k4 != 0) ? 1u : 0u;
+          for (int k4 = 0; k4 < 4; ++k4) {
+            const uint64_t bd = smem_desc_sw128(x + k4 * 32, 16, 1024);
+            const uint32_t go_on = (kb != s.kb0 || k4 != 0) ? 1u : 0u;
 #pragma unroll
-          for (int box = 0; box < 2; ++box)
-            umma_bf16(acc + box * p.acc_cols, smem_desc_sw128(st + box * kBoxBytes + k4 * 32, 16, 1024), bd, idesc, go_on);
+            for (int box = 0; box < 2; ++box)
+              umma_bf16(acc + box * p.acc_cols, smem_desc_sw128(st + box * kBoxBytes + k4 * 32, 16, 1024), bd, idesc,
+                        go_on);
+          }
+          umma_commit(&ss.empty[rg.stage]);
         }
-        umma_commit(&ss.empty[rg.stage]);
+        __syncwarp();
       } else {
         const int groups = stage_groups<G>(pr.K, kb);
         for (int j = 0; j < groups; ++j) {
 #pragma unroll
           for (int box = 0; box < 2; ++box) {
-            if (!mbar_wait(&ss.a_ready[box][tn.buf], tn.phase, abort, p.err, (0x32 << 24) | which)) return false;
+            if (!warp_wait(&ss.a_ready[box][tn.buf], tn.phase, abort, p.err, (0x32 << 24) | which)) return false;
             tc_fence_after();
-            const uint32_t a = tmem + (box * 2 + tn.buf) * Ge::A_COLS;
-            const uint32_t acc = tmem + 4 * Ge::A_COLS + (box * 2 + tn.buf) * Ge::ACC;
+            const uint32_t a = tmem + (box * 2 + tn.buf) * Ge::a_cols();
+            const uint32_t acc = tmem + 4 * Ge::a_cols() + (box * 2 + tn.buf) * Ge::acc_cols();
+            if (elect_one()) {
 #pragma unroll
-            for (int i = 0; i < G / 16; ++i) {
-              const int k = j * G + i * 16;
-              umma_bf16_ta(acc, a + i * 8, smem_desc_sw128(x + (k / 64) * c.n * 128 + (k % 64) * 2, 16, 1024), idesc,
-                           i != 0 ? 1u : 0u);
+              for (int i = 0; i < G / 16; ++i) {
+                const int k = j * G + i * 16;
+                umma_bf16_ta(acc, a + i * 8, smem_desc_sw128(x + (k / 64) * c.n * 128 + (k % 64) * 2, 16, 1024), idesc,
+                             i != 0 ? 1u : 0u);
+              }
+              umma_commit(&ss.d_full[box][tn.buf]);
+              if (box == 1 && j == groups - 1) umma_commit(&ss.empty[rg.stage]);
             }
-            umma_commit(&ss.d_full[box][tn.buf]);
+            __syncwarp();
           }
           tn.step(2);
         }
-        umma_commit(&ss.empty[rg.stage]);
       }
       rg.step(p.stages);
     }
     if constexpr (!Ge::Q4) {
-      umma_commit(&ss.acc_full[tn.buf]);
+      if (elect_one()) umma_commit(&ss.acc_full[tn.buf]);
+      __syncwarp();
       tn.step(p.acc_bufs);
     }
   }
@@ -589,40 +619,88 @@ __device__ __forceinline__ void store_out(const StreamParams& p, int r, int c, f
   }
 }
 
-// A range's sums of the tile that it begins in, this thread's row.
-__device__ __forceinline__ float* part_of(const StreamParams& p, int worker, int box, int row) {
-  return p.part + (static_cast<size_t>(worker) * 2 + box) * (kMaxTokens * kTileRows) + row;
-}
-
-// Which share of its tile a segment is: all of it, the end (left for the
-// owner) or the beginning (this range owns the tile and adds the others').
+// Which share of its tile a segment is: all of it, or a part that ranges
+// v0..v1 put together.  A range has at most two such parts: of the tile that
+// it begins in the middle of (slot 0) and of the one that it does not end
+// (slot 1).
 struct Share {
-  bool leave, add;
-  int v0, v1;     // owning range, last range with a part
+  bool whole;
+  int v0, v1;
   template <typename W>
-  __device__ Share(const W& walk, const Segment& s, int kblocks) {
-    leave = s.kb0 != 0;
-    add = !leave && s.kb1 != kblocks;
-    v0 = v1 = s.worker;
-    if (leave) v0 = walk.worker_of(s.item * kblocks);
-    if (add) v1 = walk.worker_of(s.item * kblocks + kblocks - 1);
+  __device__ Share(const W& walk, const Segment& s) {
+    const int kblocks = walk.pr.kblocks;
+    whole = s.kb0 == 0 && s.kb1 == kblocks;
+    v0 = s.kb0 == 0 ? s.worker : walk.worker_of(s.item * kblocks);
+    v1 = s.kb1 == kblocks ? s.worker : walk.worker_of(s.item * kblocks + kblocks - 1);
   }
 };
-__device__ __forceinline__ int* arrivals_of(const StreamParams& p, int which, int worker) {
-  return p.arrive + (static_cast<size_t>(which) * p.workers + worker) * kRowWarps + (threadIdx.x >> 5);
+// Column 0 of a part, this thread's row.  Range v has the tile in slot 1 only
+// if the tile begins there.
+__device__ __forceinline__ float* part_of(const StreamParams& p, int v, bool begins, int box, int row) {
+  return p.part + ((static_cast<size_t>(v) * 2 + begins) * 2 + box) * (kMaxTokens * kTileRows) + row;
+}
+__device__ __forceinline__ int* arrivals_of(const StreamParams& p, int which, int v0) {
+  return p.arrive + static_cast<size_t>(which) * kMaxWorkers + v0;
 }
 __device__ __forceinline__ void leave_part(const StreamParams& p, int which, const Share& sh) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) red_release_gpu_add(arrivals_of(p, which, sh.v0), 1);
 }
-__device__ __forceinline__ bool wait_parts(const StreamParams& p, int which, const Share& sh, volatile int* abort) {
-  bool ok = true;
-  if ((threadIdx.x & 31) == 0) {
-    int* cnt = arrivals_of(p, which, sh.v0);
-    ok = wait_count(cnt, sh.v1 - sh.v0, abort, p.err, (0x29 << 24) | which);
-    *cnt = 0;
+
+// A tile's finished column i, this thread's row of either box.
+template <bool H, bool LAYER>
+__device__ __forceinline__ void finish_column(const StreamParams& p, const Shared& ss, const Segment& s, int r0, int i,
+                                              int row, float v0, float v1) {
+  const int r = r0 + i;
+  if (LAYER && !H) {
+    const int at = s.rt * kTileRows + row;
+    if (at < p.f) store_hidden(p, r, at, ss.row_w[r], v0, v1);
+  } else {
+    store_out<LAYER>(p, r, s.rt * 2 * kTileRows + row, v0);
+    store_out<LAYER>(p, r, (s.rt * 2 + 1) * kTileRows + row, v1);
   }
-  return __shfl_sync(kFull, ok, 0);
+}
+
+// After the segments of a product: the cut tiles of this CTA's ranges, this
+// range's share of their columns (column i belongs to the i-th part, modulo
+// the parts), every other one to either set of row warps.
+template <bool H, bool LAYER, bool TOKEN_COLS>
+__device__ bool join_parts(const StreamParams& p, int which, const Shared& ss, volatile int* abort) {
+  const Product& pr = p.p[which];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row = (warp & 3) * 32 + lane, set = warp >> 2;
+  Walk<H> walk(pr, ss, p.workers);
+  Segment s;
+  while (walk.next(s)) {
+    const Share sh(walk, s);
+    if (sh.whole) continue;
+    const Columns<H> c(p, ss, s);
+    const int parts = sh.v1 - sh.v0 + 1;
+    const int first = s.worker - sh.v0 + set * parts;
+    if (first >= c.m) continue;
+    bool ok = true;
+    if (lane == 0) ok = wait_count(arrivals_of(p, which, sh.v0), parts * kRowWarps, abort, p.err, (0x29 << 24) | which);
+    if (!__shfl_sync(kFull, ok, 0)) return false;
+    for (int i = first; i < c.m; i += 2 * parts) {
+      const int at = (TOKEN_COLS ? ss.row_token[c.r0 + i] : i) * kTileRows;
+      float v[2] = {0.f, 0.f};
+      constexpr int B = 4;  // parts on the way at a time
+      for (int w0 = 0; w0 < parts; w0 += B) {
+        float u[B][2];
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+#pragma unroll
+          for (int box = 0; box < 2; ++box)
+            u[b][box] = w0 + b < parts ? __ldcg(part_of(p, sh.v0 + w0 + b, w0 + b == 0, box, row) + at) : 0.f;
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+#pragma unroll
+          for (int box = 0; box < 2; ++box) v[box] += u[b][box];
+      }
+      finish_column<H, LAYER>(p, ss, s, c.r0, i, row, v[0], v[1]);
+    }
+  }
+  return true;
 }
 
 // bf16 weights: a segment's sums are in tensor memory.  Both sets see both
@@ -630,19 +708,17 @@ __device__ __forceinline__ bool wait_parts(const StreamParams& p, int which, con
 // column c of either box; eight columns are read at a time.
 template <bool H, bool LAYER>
 __device__ bool rows_bf16(const StreamParams& p, int which, Shared& ss, Turn& tn, volatile int* abort) {
-  const Product& pr = p.p[which];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int quad = warp & 3, set = warp >> 2, row = quad * 32 + lane;
-  Walk<H> walk(pr, ss, p.workers);
+  Walk<H> walk(p.p[which], ss, p.workers);
   Segment s;
   while (walk.next(s)) {
     const Columns<H> c(p, ss, s);
-    const Share sh(walk, s, pr.kblocks);
+    const Share sh(walk, s);
     bool ok = mbar_wait(&ss.acc_full[tn.buf], tn.phase, abort, p.err, (0x33 << 24) | which);
     if (!__all_sync(kFull, ok)) return false;
     tc_fence_after();
     const uint32_t acc = ss.tmem + (static_cast<uint32_t>(quad * 32) << 16) + tn.buf * 2 * p.acc_cols;
-    if (sh.add && !wait_parts(p, which, sh, abort)) return false;
     constexpr int B = 4;  // columns read at a time
     for (int i0 = set * B; i0 < c.m; i0 += 2 * B) {
       float v[2][B];
@@ -667,31 +743,15 @@ __device__ bool rows_bf16(const StreamParams& p, int which, Shared& ss, Turn& tn
           v[box][j] = __uint_as_float(u[box][0][j]);
           if (H) v[box][j] += (__uint_as_float(u[box][1][j]) + __uint_as_float(u[box][2][j])) * (1.f / kLowScale);
         }
-      if (sh.leave) {
-#pragma unroll
-        for (int j = 0; j < B; ++j)
-          if (i0 + j < c.m)
-#pragma unroll
-            for (int box = 0; box < 2; ++box) __stcg(part_of(p, s.worker, box, row) + (i0 + j) * kTileRows, v[box][j]);
-        continue;
-      }
-      for (int w = sh.v0 + 1; w <= sh.v1; ++w)
-#pragma unroll
-        for (int j = 0; j < B; ++j)
-          if (i0 + j < c.m)
-#pragma unroll
-            for (int box = 0; box < 2; ++box) v[box][j] += __ldcg(part_of(p, w, box, row) + (i0 + j) * kTileRows);
 #pragma unroll
       for (int j = 0; j < B; ++j)
         if (i0 + j < c.m) {
-          const int r = c.r0 + i0 + j;
-          if (LAYER && !H) {
-            const int i = s.rt * kTileRows + row;
-            if (i < p.f) store_hidden(p, r, i, ss.row_w[r], v[0][j], v[1][j]);
+          if (sh.whole) {
+            finish_column<H, LAYER>(p, ss, s, c.r0, i0 + j, row, v[0][j], v[1][j]);
           } else {
 #pragma unroll
             for (int box = 0; box < 2; ++box)
-              store_out<LAYER>(p, r, (s.rt * 2 + box) * kTileRows + row, v[box][j]);
+              __stcg(part_of(p, s.worker, s.kb0 == 0, box, row) + (i0 + j) * kTileRows, v[box][j]);
           }
         }
     }
@@ -699,9 +759,9 @@ __device__ bool rows_bf16(const StreamParams& p, int which, Shared& ss, Turn& tn
     __syncwarp();
     if (lane == 0) mbar_arrive(&ss.acc_empty[tn.buf]);
     tn.step(p.acc_bufs);
-    if (sh.leave) leave_part(p, which, sh);
+    if (!sh.whole) leave_part(p, which, sh);
   }
-  return true;
+  return join_parts<H, LAYER, false>(p, which, ss, abort);
 }
 
 // 4-bit weights: set 0 owns the first box, set 1 the second, a thread one row
@@ -755,7 +815,7 @@ struct RowsQ4 {
     const int quad = warp & 3, box = warp >> 2, row = quad * 32 + lane;
     const uint32_t lanes = ss.tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const Columns<H> c(p, ss, s);
-    const Share sh(walk, s, pr.kblocks);
+    const Share sh(walk, s);
     float sum[NC];
 #pragma unroll
     for (int i = 0; i < NC; ++i) sum[i] = 0.f;
@@ -766,7 +826,7 @@ struct RowsQ4 {
       ok = mbar_wait(&ss.d_full[box][before.buf], before.phase, abort, p.err, (0x34 << 24) | which);
       if (!__all_sync(kFull, ok)) return false;
       tc_fence_after();
-      add_group(p, lanes + 4 * Ge::A_COLS + (box * 2 + before.buf) * Ge::ACC, c.n16, scale_before, sum);
+      add_group(p, lanes + 4 * Ge::a_cols() + (box * 2 + before.buf) * Ge::acc_cols(), c.n16, scale_before, sum);
       return true;
     };
     for (int kb = s.kb0; kb < s.kb1; ++kb) {
@@ -778,7 +838,7 @@ struct RowsQ4 {
       const int groups = stage_groups<G>(pr.K, kb);
 #pragma unroll 1
       for (int j = 0; j < groups; ++j) {
-        const uint32_t a = lanes + (box * 2 + tn.buf) * Ge::A_COLS;
+        const uint32_t a = lanes + (box * 2 + tn.buf) * Ge::a_cols();
         uint32_t w[G / 32][4];
 #pragma unroll
         for (int i = 0; i < G / 32; ++i) lds128(codes + (((j * (G / 32) + i) ^ (row & 7)) << 4), w[i]);
@@ -809,31 +869,24 @@ struct RowsQ4 {
     if (!take()) return false;
 
     const int real = H ? c.m : p.T;  // columns with values of their own
-    if (sh.leave) {
+    if (!sh.whole) {
 #pragma unroll
       for (int i = 0; i < NC; ++i)
-        if (i < real) __stcg(part_of(p, s.worker, box, row) + i * kTileRows, sum[i]);
+        if (i < real) __stcg(part_of(p, s.worker, s.kb0 == 0, box, row) + i * kTileRows, sum[i]);
       leave_part(p, which, sh);
       tc_fence_before();
       return true;
     }
-    if (sh.add) {
-      if (!wait_parts(p, which, sh, abort)) return false;
-      for (int w = sh.v0 + 1; w <= sh.v1; ++w)
-#pragma unroll
-        for (int i = 0; i < NC; ++i)
-          if (i < real) sum[i] += __ldcg(part_of(p, w, box, row) + i * kTileRows);
-    }
     if constexpr (LAYER && !H) {
       // Both boxes' sums of a hidden column meet in tensor memory, in the
       // accumulators just read; no set goes on before both have read them.
-      const uint32_t acc = lanes + 4 * Ge::A_COLS + before.buf * Ge::ACC;
+      const uint32_t acc = lanes + 4 * Ge::a_cols() + before.buf * Ge::acc_cols();
 #pragma unroll
       for (int b = 0; b < NC / 16; ++b) {
         uint32_t u[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(sum[b * 16 + i]);
-        tmem_st16(acc + box * 2 * Ge::ACC + b * 16, u);
+        tmem_st16(acc + box * 2 * Ge::acc_cols() + b * 16, u);
       }
       tmem_st_wait();
       tc_fence_before();
@@ -844,7 +897,7 @@ struct RowsQ4 {
       tc_fence_after();
       for (int i = box; i < c.m; i += 2) {
         const int at = ss.row_token[c.r0 + i];
-        const uint32_t ua = tmem_ld1(acc + at), ub = tmem_ld1(acc + 2 * Ge::ACC + at);
+        const uint32_t ua = tmem_ld1(acc + at), ub = tmem_ld1(acc + 2 * Ge::acc_cols() + at);
         tmem_ld_wait();
         const int hi = s.rt * kTileRows + row;
         if (hi < p.f) store_hidden(p, c.r0 + i, hi, ss.row_w[c.r0 + i], __uint_as_float(ua), __uint_as_float(ub));
@@ -881,7 +934,7 @@ __device__ bool rows_q4(const StreamParams& p, int which, Shared& ss, uint8_t* r
     else
       ok = RowsQ4<G, H ? 32 : 64, H, LAYER>::segment(p, which, ss, ring, walk, s, rg, tn, swap, abort);
   }
-  return ok;
+  return ok && join_parts<H, LAYER, LAYER && !H>(p, which, ss, abort);
 }
 
 // y[t] = its slots' rows in slot order, then the shared experts', in fp32.
@@ -921,7 +974,8 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
   // stages on 1024-byte boundaries of shared memory (the swizzle's period)
   const uint32_t ring_at = (smem_u32(dyn) + kSharedBytes + 1023u) & ~1023u;
   uint8_t* ring = dyn + (ring_at - smem_u32(dyn));
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(kFull, tid >> 5, 0);  // the same for the warp, and known to be
   if (tid == 0) {
     for (int i = 0; i < p.stages; ++i) {
       mbar_init(&ss.full_w[i], 1);
@@ -961,44 +1015,41 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
   volatile int* abort = &ss.abort;
   const int arrivals = kRowWarps * gridDim.x;
   if (warp == kWeightWarp) {
-    if (lane == 0) {
-      Ring rg;
-      Drain dr;
-      bool ok = true;
-      if (LAYER) ok = produce_weights<G, false>(p, 0, ss, ring, rg, dr, abort);
-      if (ok) produce_weights<G, LAYER>(p, 1, ss, ring, rg, dr, abort);
-      dr.wait(ss.full_w);
-    }
-    __syncwarp();
+    Ring rg;
+    Drain dr;
+    bool ok = true;
+    if (LAYER) ok = produce_weights<G, false>(p, 0, ss, ring, rg, dr, abort);
+    if (ok) produce_weights<G, LAYER>(p, 1, ss, ring, rg, dr, abort);
+    dr.wait(ss.full_w);
   } else if (warp == kColumnWarp) {
-    if (lane == 0) {
-      Ring rg;
-      Drain dr;
+    Ring rg;
+    Drain dr;
+    // One poller a CTA: with one per warp the counter's L2 slice was so busy
+    // answering that the last arrivals came through 8 us late.
+    auto wait_all = [&](int counter, int where) {
       bool ok = true;
-      if (LAYER) {
-        ok = produce_columns<G, false>(p, 0, ss, ring, rg, dr, abort);
-        // every hidden value of every CTA, for the bulk copies of this one
-        ok = ok && wait_count(p.err + kCtrHidden, arrivals, abort, p.err, 0x25 << 24);
-        fence_proxy_async_global();
-      }
-      if (ok) ok = produce_columns<G, LAYER>(p, 1, ss, ring, rg, dr, abort);
-      // One poller a CTA: with one per warp the counter's L2 slice was so busy
-      // answering that the last arrivals came through 8 us late.
-      if (LAYER && ok && wait_count(p.err + kCtrOut, arrivals, abort, p.err, 0x26 << 24)) mbar_arrive(&ss.out_done);
-      dr.wait(ss.full_x);
+      if (lane == 0) ok = wait_count(p.err + counter, arrivals, abort, p.err, where << 24);
+      return __shfl_sync(kFull, ok, 0) != 0;
+    };
+    bool ok = true;
+    if (LAYER) {
+      ok = produce_columns<G, false>(p, 0, ss, ring, rg, dr, abort);
+      ok = ok && wait_all(kCtrHidden, 0x25);  // every hidden value of every CTA,
+      fence_proxy_async_global();             // for the bulk copies of this one
     }
-    __syncwarp();
+    if (ok) ok = produce_columns<G, LAYER>(p, 1, ss, ring, rg, dr, abort);
+    if (LAYER && ok && wait_all(kCtrOut, 0x26) && lane == 0) mbar_arrive(&ss.out_done);
+    dr.wait(ss.full_x);
   } else if (warp == kMmaWarp) {
-    if (lane == 0) {
-      Ring rg;
-      Turn tn;
-      bool ok = true;
-      if (LAYER) ok = issue_mmas<G, false>(p, 0, ss, ring, rg, tn, abort);
-      if (ok) issue_mmas<G, LAYER>(p, 1, ss, ring, rg, tn, abort);
-      umma_commit(&ss.drained);
-      drain_wait(&ss.drained, 0);
-    }
+    Ring rg;
+    Turn tn;
+    bool ok = true;
+    if (LAYER) ok = issue_mmas<G, false>(p, 0, ss, ring, rg, tn, abort);
+    if (ok) issue_mmas<G, LAYER>(p, 1, ss, ring, rg, tn, abort);
     __syncwarp();
+    if (elect_one()) umma_commit(&ss.drained);
+    __syncwarp();
+    drain_wait(&ss.drained, 0);
   } else {
     Ring rg;
     Turn tn;
@@ -1038,10 +1089,11 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
   tc_fence_after();
   if (warp == kMmaWarp) tmem_dealloc(ss.tmem, kTmemCols);
   // the last CTA to pass its waits clears the counters
-  if (LAYER && tid == 0 && atomicAdd(p.err + kCtrExit, 1) == static_cast<int>(gridDim.x) - 1) {
-    p.err[kCtrHidden] = 0;
-    p.err[kCtrOut] = 0;
-    p.err[kCtrExit] = 0;
+  if (tid == 0) ss.abort = atomicAdd(p.err + kCtrExit, 1) == static_cast<int>(gridDim.x) - 1;
+  __syncthreads();
+  if (ss.abort) {
+    for (int i = tid; i < 2 * kMaxWorkers; i += kThreads) p.arrive[i] = 0;
+    if (tid < 3) p.err[kCtrHidden + tid] = 0;
   }
 }
 
@@ -1062,8 +1114,8 @@ Layout layout(size_t rows, size_t d, size_t f) {
     o = align_up(o + bytes, 256);
     return at;
   };
-  L.arrive = take(sizeof(int) * 2 * kMaxWorkers * kRowWarps);
-  L.part = take(sizeof(float) * kMaxWorkers * 2 * kMaxTokens * kTileRows);
+  L.arrive = take(sizeof(int) * 2 * kMaxWorkers);
+  L.part = take(sizeof(float) * kMaxWorkers * 4 * kMaxTokens * kTileRows);
   L.h = take(3 * sizeof(uint16_t) * rows * f);
   L.o = take(sizeof(float) * rows * d);
   L.total = o;
