@@ -25,7 +25,8 @@
 //     go to tensor memory, from where the instruction takes them: written
 //     back to shared memory they would need four times the codes' bandwidth
 //     there, twice.  Each group of columns is summed from zero and scaled in
-//     fp32 on its way out, so no weight is rounded.
+//     fp32 on its way out, so no weight is rounded.  Two sets of warps take
+//     turns: one turns codes while the other one's turn is multiplied.
 //   - The tiles of all picked experts form one sequence of K blocks, cut into
 //     equal contiguous ranges, one per SM, so no SM idles whatever the number
 //     of experts, rows and tokens.  Every range that works on a cut tile
@@ -49,15 +50,20 @@ namespace moe {
 
 namespace {
 
-constexpr int kRowWarps = 8;             // two sets of four: a set's warps cover the 128 rows of a tile
+constexpr int kSets = 4;                 // of four row warps each, which cover the 128 rows of a tile
+constexpr int kRowWarps = 4 * kSets;
 constexpr int kWeightWarp = kRowWarps;   // producer of weight tiles
 constexpr int kColumnWarp = kRowWarps + 1;  // producer of activation rows
-constexpr int kMmaWarp = kRowWarps + 2;     // issues the tensor instructions, owns the tensor memory
-constexpr int kWarps = kRowWarps + 3;
+constexpr int kMmaWarp = kRowWarps + 2;     // issues the tensor instructions; 4 bits: the first box's, the next warp the second's
+constexpr int kWarps = kRowWarps + 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTileRows = 128;           // rows of one weight box: an accumulator's lanes
 constexpr int kBoxBytes = kTileRows * 128;
 constexpr int kTmemCols = 512;
+// 4 bits: an operand buffer (128 rows x 128 bf16) and accumulators for either
+// box and turn.
+constexpr int kOperandCols = 64;
+constexpr int kSumCols = 64;
 constexpr int kMaxStages = 8;
 constexpr int kMaxTokens = MOE_DECODE_MAX_T;
 constexpr int kMaxPicks = kMaxTokens * 8;
@@ -71,6 +77,13 @@ constexpr int kMaxWorkers = 256;
 constexpr int kCtrHidden = 8;   // row warps done with the first product
 constexpr int kCtrOut = 9;      // ... with the second
 constexpr int kCtrExit = 10;    // CTAs done
+constexpr int kCtrRouted = 11;  // tokens routed, where the CTAs share the routing
+
+// K blocks of W2 that a CTA asks into L2 when its part of the first product
+// is on the way, beyond what its ring holds.  Memory then stays busy while the
+// hidden values of all CTAs come together, and the second product starts
+// from L2.
+constexpr int kPrefetchBlocks = 12;
 
 // A stage: 128 bytes of 2 x 128 weight rows, the scales of those columns (4
 // bits) and the activation rows, 64 columns (128 bytes, swizzled) at a time.
@@ -83,10 +96,6 @@ struct Geo {
   static constexpr int GROUPS = Q4 ? KB / (Q4 ? G : 1) : 0;    // scale rows
   static constexpr int SCALE_BYTES = GROUPS * kTileRows * 2;   // of one box
   static constexpr int WEIGHT_BYTES = 2 * (kBoxBytes + SCALE_BYTES);
-  // Tensor memory, 4 bits: two operand buffers of G / 2 words for either box,
-  // then two accumulators of each (one group each).
-  static __host__ __device__ constexpr int a_cols() { return G / 2; }
-  static __host__ __device__ constexpr int acc_cols() { return (kTmemCols - 4 * a_cols()) / 4; }
   // Rows of h in one tile of the second product.  bf16 weights: all of them.
   // 4 bits: what the accumulators hold; an expert with more rows has its
   // weight tiles visited again, from L2.
@@ -123,8 +132,8 @@ struct StreamParams {
 struct alignas(16) Shared {
   uint64_t full_w[kMaxStages], full_x[kMaxStages], empty[kMaxStages];
   uint64_t acc_full[2], acc_empty[2];   // bf16: accumulator pairs
-  uint64_t a_ready[2][2], d_full[2][2]; // 4 bits: [box][buffer]
-  uint64_t swap_ready, swap_done;       // 4 bits: both boxes' sums of a tile in tensor memory
+  uint64_t a_ready[2][2], d_full[2][2], d_empty[2][2]; // 4 bits: [box][turn]
+  uint64_t swap_ready, swap_done;       // 4 bits: all sums of a tile in tensor memory
   uint64_t out_done;                    // every CTA's output rows are there
   uint64_t drained;                     // tensor instructions all complete
   uint32_t tmem;
@@ -145,69 +154,87 @@ struct alignas(16) Shared {
 };
 constexpr int kSharedBytes = (sizeof(Shared) + 127) / 128 * 128;
 
-// ---------------------------------------------------------------- work list
-// Routes every token and lists the experts that have rows, each CTA for
-// itself (64 tokens x 64 experts are 16 KB of logits from L2).  A token picks
-// an expert at most once, so an expert's tokens are a 64-bit mask and a row's
-// place in its expert's list is a population count: ascending tokens,
-// whatever the order of the atomics that set the bits.
-template <int EPL, int U>
-__device__ __forceinline__ void route_all(const StreamParams& p, Shared& ss) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  RowSoftmax<EPL> r[U];
-  int t[U];
-  auto load = [&](int t0) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      t[u] = t0 + u * kWarps;
-      const int from = min(t[u], p.T - 1);
-      row_load<EPL>(p.logits + static_cast<size_t>(from) * p.E, p.E, lane, r[u].v);
+// Waits until `target` arrivals are counted (bounded).
+__device__ bool wait_count(const int* c, int target, volatile int* abort, int* err, int where) {
+  uint64_t t0 = 0;
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (ld_acquire_gpu(c) >= target) return true;
+    if (*abort) return false;
+    if (t0 == 0) t0 = globaltimer_ns();
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      record_error(err, MOE_ERR_TIMEOUT_CODE, where);
+      *abort = 1;
+      return false;
     }
-  };
-  load(warp);  // in flight while the masks are cleared
-  for (int i = threadIdx.x; i < 512; i += kThreads) (&ss.mask[0][0])[i] = 0;
-  __syncthreads();
-  for (int t0 = warp; t0 < p.T; t0 += U * kWarps) {
-    int idx[U];
-    float w[U];
-    route_tokens<EPL, U>(r, t, p.E, p.k, p.renorm, lane, p.err, idx, w);
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (lane < p.k && t[u] < p.T) {
-        const int at = t[u] * p.k + lane;
-        ss.pick_e[at] = static_cast<short>(idx[u]);
-        ss.pick_w[at] = w[u];
-        atomicOr(&ss.mask[idx[u]][t[u] >> 5], 1u << (t[u] & 31));
-        if (blockIdx.x == 0) {
-          p.topk_idx[at] = idx[u];
-          p.topk_w[at] = w[u];
-        }
-      }
-    if (t0 + U * kWarps < p.T) load(t0 + U * kWarps);
   }
 }
 
+// ---------------------------------------------------------------- work list
+// Routes the tokens.  Up to kWarps tokens: every CTA all of them, one warp a
+// token.  More: token t is CTA t % gridDim.x's, and every CTA reads the picks
+// of the others from the outputs once all are counted; 64 tokens routed by
+// every CTA itself took 8 us, most of them in the warps' serial pick rounds.
+// A token picks an expert at most once, so an expert's tokens are a 64-bit
+// mask and a row's place in its expert's list is a population count:
+// ascending tokens, whatever the order of the atomics that set the bits.
+__device__ __forceinline__ void note_pick(Shared& ss, int at, int t, int e, float w) {
+  ss.pick_e[at] = static_cast<short>(e);
+  ss.pick_w[at] = w;
+  atomicOr(&ss.mask[e][t >> 5], 1u << (t & 31));
+}
+
 template <int EPL>
-__device__ __forceinline__ void route_any(const StreamParams& p, Shared& ss) {
-  // more tokens than warps: several at a time on a warp
-  if (EPL <= 4 && p.T > kWarps)
-    route_all<EPL, EPL <= 2 ? 3 : 2>(p, ss);
-  else
-    route_all<EPL, 1>(p, ss);
+__device__ __noinline__ void route_all(const StreamParams& p, Shared& ss) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool shared_out = p.T > kWarps;
+  const int step = shared_out ? gridDim.x * kWarps : kWarps;
+  int t = shared_out ? blockIdx.x + warp * gridDim.x : warp;
+  RowSoftmax<EPL> r;
+  if (t < p.T) row_load<EPL>(p.logits + static_cast<size_t>(t) * p.E, p.E, lane, r.v);  // in flight while the masks are cleared
+  if (threadIdx.x < 512) (&ss.mask[0][0])[threadIdx.x] = 0;
+  __syncthreads();
+  while (t < p.T) {
+    int idx;
+    float w;
+    route_token<EPL>(r, t, p.E, p.k, p.renorm, lane, p.err, idx, w);
+    if (lane < p.k) {
+      const int at = t * p.k + lane;
+      if (!shared_out) note_pick(ss, at, t, idx, w);
+      if (shared_out || blockIdx.x == 0) {
+        p.topk_idx[at] = idx;
+        p.topk_w[at] = w;
+      }
+    }
+    if (shared_out) {
+      __syncwarp();
+      if (lane == 0) red_release_gpu_add(p.err + kCtrRouted, 1);
+    }
+    t += step;
+    if (t < p.T) row_load<EPL>(p.logits + static_cast<size_t>(t) * p.E, p.E, lane, r.v);
+  }
 }
 
 __device__ void build_work_list(const StreamParams& p, Shared& ss) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (p.E <= 32)
-    route_any<1>(p, ss);
-  else if (p.E <= 64)
-    route_any<2>(p, ss);
-  else if (p.E <= 128)
-    route_any<4>(p, ss);
-  else
-    route_any<8>(p, ss);
-  __syncthreads();
   const int R = p.T * p.k;
+  if (p.E <= 32)
+    route_all<1>(p, ss);
+  else if (p.E <= 64)
+    route_all<2>(p, ss);
+  else if (p.E <= 128)
+    route_all<4>(p, ss);
+  else
+    route_all<8>(p, ss);
+  if (p.T > kWarps) {
+    if (tid == 0) wait_count(p.err + kCtrRouted, p.T, &ss.abort, p.err, 0x20 << 24);
+    __syncthreads();
+    // After a wait that gave up (abort is set) the picks may be anything: clamped, they stay in bounds.
+    for (int i = tid; i < R; i += kThreads)
+      note_pick(ss, i, i / p.k, min(max(__ldcg(p.topk_idx + i), 0), p.E - 1), __ldcg(p.topk_w + i));
+  }
+  __syncthreads();
   // Thread e: expert e.  Exclusive sums of rows, entries and blocks of h rows
   // over the experts, packed into 11 + 10 + 11 bits (at most 512, 256 and 288).
   unsigned mine = 0, incl = 0;
@@ -371,23 +398,6 @@ struct Drain {
   }
 };
 
-// Waits until `target` arrivals are counted (bounded).
-__device__ bool wait_count(const int* c, int target, volatile int* abort, int* err, int where) {
-  uint64_t t0 = 0;
-  while (true) {
-#pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-      if (ld_acquire_gpu(c) >= target) return true;
-    if (*abort) return false;
-    if (t0 == 0) t0 = globaltimer_ns();
-    if (globaltimer_ns() - t0 > kWaitLimitNs) {
-      record_error(err, MOE_ERR_TIMEOUT_CODE, where);
-      *abort = 1;
-      return false;
-    }
-  }
-}
-
 // Columns of a tile: all tokens (first product, linear form), or the parts of
 // its rows of h, each rounded up to 16.
 template <bool H>
@@ -430,6 +440,18 @@ __device__ bool produce_weights(const StreamParams& p, int which, Shared& ss, ui
   const Product& pr = p.p[which];
   Walk<H> walk(pr, ss, p.workers);
   Segment s;
+  if (H) {
+    Walk<H> ahead(pr, ss, p.workers);
+    for (int n = -p.stages; n < kPrefetchBlocks && ahead.next(s);) {
+      const int row = ss.e[s.a] * pr.rows + s.rt * pr.row_step;
+      for (int kb = s.kb0; kb < s.kb1 && n < kPrefetchBlocks; ++kb, ++n)
+        if (n >= 0 && elect_one()) {
+          tma_prefetch_2d(&pr.w0, kb * (Ge::Q4 ? 128 : 64), row);
+          tma_prefetch_2d(&pr.w1, kb * (Ge::Q4 ? 128 : 64), row + kTileRows);
+        }
+    }
+    __syncwarp();
+  }
   while (walk.next(s)) {
     const int row = ss.e[s.a] * pr.rows + s.rt * pr.row_step;
     const int beside = which == 0 ? 0 : kTileRows;  // W3 beside W1, or the tile's other rows
@@ -497,7 +519,8 @@ __device__ bool produce_columns(const StreamParams& p, int which, Shared& ss, ui
 }
 
 // ----------------------------------------------------- tensor instructions
-// Positions in the row warps' buffers: bf16, segments; 4 bits, groups.
+// Position in a ring of buffers: bf16, accumulator pairs, one a segment; 4
+// bits, turns.
 struct Turn {
   int buf = 0;
   uint32_t phase = 0;
@@ -509,76 +532,102 @@ struct Turn {
   }
 };
 
+// 4 bits: a turn is as many groups of a stage as fit the operand buffer and,
+// with c columns each, the accumulators.
+template <int G>
+__device__ __forceinline__ int turn_groups(int columns) {
+  return max(1, min(kOperandCols * 2 / G, kSumCols / columns));
+}
 // Groups of a stage that lie inside K.
 template <int G>
 __device__ __forceinline__ int stage_groups(int K, int kb) {
   return min(Geo<G>::KB, K - kb * Geo<G>::KB) / G;
 }
+// Columns beyond 32 are added up by the other turn's set (H tiles have at
+// most 32 rows): both sets read the sums of every turn then.
+template <bool H>
+__device__ __forceinline__ bool columns_split(int n16) {
+  return !H && n16 > 2;
+}
+__device__ __forceinline__ uint32_t operand_at(uint32_t tmem, int box, int turn) {
+  return tmem + (box * 2 + turn) * kOperandCols;
+}
+__device__ __forceinline__ uint32_t sums_at(uint32_t tmem, int box, int turn) {
+  return tmem + 4 * kOperandCols + (box * 2 + turn) * kSumCols;
+}
+
+template <bool H>
+__device__ bool issue_bf16(const StreamParams& p, int which, Shared& ss, uint8_t* ring, Ring& rg, Turn& tn,
+                           volatile int* abort) {
+  Walk<H> walk(p.p[which], ss, p.workers);
+  Segment s;
+  while (walk.next(s)) {
+    const Columns<H> c(p, ss, s);
+    const uint32_t idesc = idesc_bf16_f32(kTileRows, c.n, 0, 0);
+    const uint32_t acc = ss.tmem + tn.buf * 2 * p.acc_cols;
+    if (!warp_wait(&ss.acc_empty[tn.buf], tn.phase ^ 1, abort, p.err, (0x31 << 24) | which)) return false;
+    for (int kb = s.kb0; kb < s.kb1; ++kb) {
+      const uint32_t st = smem_u32(ring) + static_cast<uint32_t>(rg.stage) * p.stage_bytes;
+      const uint32_t x = st + Geo<0>::WEIGHT_BYTES;
+      if (!warp_wait(&ss.full_x[rg.stage], rg.phase, abort, p.err, (0x24 << 24) | which)) return false;
+      if (!warp_wait(&ss.full_w[rg.stage], rg.phase, abort, p.err, (0x23 << 24) | which)) return false;
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int k4 = 0; k4 < 4; ++k4) {
+          const uint64_t bd = smem_desc_sw128(x + k4 * 32, 16, 1024);
+          const uint32_t go_on = (kb != s.kb0 || k4 != 0) ? 1u : 0u;
+#pragma unroll
+          for (int box = 0; box < 2; ++box)
+            umma_bf16(acc + box * p.acc_cols, smem_desc_sw128(st + box * kBoxBytes + k4 * 32, 16, 1024), bd, idesc, go_on);
+        }
+        umma_commit(&ss.empty[rg.stage]);
+        if (kb == s.kb1 - 1) umma_commit(&ss.acc_full[tn.buf]);
+      }
+      __syncwarp();
+      rg.step(p.stages);
+    }
+    tn.step(p.acc_bufs);
+  }
+  return true;
+}
 
 template <int G, bool H>
-__device__ bool issue_mmas(const StreamParams& p, int which, Shared& ss, uint8_t* ring, Ring& rg, Turn& tn,
-                           volatile int* abort) {
+__device__ bool issue_q4(const StreamParams& p, int which, int box, Shared& ss, uint8_t* ring, Ring& rg, Turn& tn,
+                         volatile int* abort) {
   using Ge = Geo<G>;
   const Product& pr = p.p[which];
-  const uint32_t tmem = ss.tmem;
   Walk<H> walk(pr, ss, p.workers);
   Segment s;
   while (walk.next(s)) {
     const Columns<H> c(p, ss, s);
     const uint32_t idesc = idesc_bf16_f32(kTileRows, c.n, 0, 0);
-    if constexpr (!Ge::Q4)
-      if (!warp_wait(&ss.acc_empty[tn.buf], tn.phase ^ 1, abort, p.err, (0x31 << 24) | which)) return false;
+    const int tg = turn_groups<G>(c.n);
     for (int kb = s.kb0; kb < s.kb1; ++kb) {
-      const uint32_t st = smem_u32(ring) + static_cast<uint32_t>(rg.stage) * p.stage_bytes;
-      const uint32_t x = st + Ge::WEIGHT_BYTES;
+      const uint32_t x = smem_u32(ring) + static_cast<uint32_t>(rg.stage) * p.stage_bytes + Ge::WEIGHT_BYTES;
       if (!warp_wait(&ss.full_x[rg.stage], rg.phase, abort, p.err, (0x24 << 24) | which)) return false;
-      if constexpr (!Ge::Q4) {
-        if (!warp_wait(&ss.full_w[rg.stage], rg.phase, abort, p.err, (0x23 << 24) | which)) return false;
+      const int groups = stage_groups<G>(pr.K, kb);
+      for (int g0 = 0; g0 < groups; g0 += tg) {
+        if (!warp_wait(&ss.a_ready[box][tn.buf], tn.phase, abort, p.err, (0x32 << 24) | which)) return false;
+        if (!warp_wait(&ss.d_empty[box][tn.buf], tn.phase ^ 1, abort, p.err, (0x37 << 24) | which)) return false;
         tc_fence_after();
-        const uint32_t acc = tmem + tn.buf * 2 * p.acc_cols;
+        const uint32_t a = operand_at(ss.tmem, box, tn.buf), d = sums_at(ss.tmem, box, tn.buf);
+        const int n = min(tg, groups - g0);
         if (elect_one()) {
+          for (int j = 0; j < n; ++j)
 #pragma unroll
-          for (int k4 = 0; k4 < 4; ++k4) {
-            const uint64_t bd = smem_desc_sw128(x + k4 * 32, 16, 1024);
-            const uint32_t go_on = (kb != s.kb0 || k4 != 0) ? 1u : 0u;
-#pragma unroll
-            for (int box = 0; box < 2; ++box)
-              umma_bf16(acc + box * p.acc_cols, smem_desc_sw128(st + box * kBoxBytes + k4 * 32, 16, 1024), bd, idesc,
-                        go_on);
-          }
-          umma_commit(&ss.empty[rg.stage]);
+            for (int i = 0; i < G / 16; ++i) {
+              const int k = (g0 + j) * G + i * 16;
+              umma_bf16_ta(d + j * c.n, a + j * (G / 2) + i * 8,
+                           smem_desc_sw128(x + (k / 64) * c.n * 128 + (k % 64) * 2, 16, 1024), idesc, i != 0 ? 1u : 0u);
+            }
+          umma_commit(&ss.d_full[box][tn.buf]);
+          if (g0 + tg >= groups) umma_commit(&ss.empty[rg.stage]);
         }
         __syncwarp();
-      } else {
-        const int groups = stage_groups<G>(pr.K, kb);
-        for (int j = 0; j < groups; ++j) {
-#pragma unroll
-          for (int box = 0; box < 2; ++box) {
-            if (!warp_wait(&ss.a_ready[box][tn.buf], tn.phase, abort, p.err, (0x32 << 24) | which)) return false;
-            tc_fence_after();
-            const uint32_t a = tmem + (box * 2 + tn.buf) * Ge::a_cols();
-            const uint32_t acc = tmem + 4 * Ge::a_cols() + (box * 2 + tn.buf) * Ge::acc_cols();
-            if (elect_one()) {
-#pragma unroll
-              for (int i = 0; i < G / 16; ++i) {
-                const int k = j * G + i * 16;
-                umma_bf16_ta(acc, a + i * 8, smem_desc_sw128(x + (k / 64) * c.n * 128 + (k % 64) * 2, 16, 1024), idesc,
-                             i != 0 ? 1u : 0u);
-              }
-              umma_commit(&ss.d_full[box][tn.buf]);
-              if (box == 1 && j == groups - 1) umma_commit(&ss.empty[rg.stage]);
-            }
-            __syncwarp();
-          }
-          tn.step(2);
-        }
+        tn.step(2);
       }
       rg.step(p.stages);
-    }
-    if constexpr (!Ge::Q4) {
-      if (elect_one()) umma_commit(&ss.acc_full[tn.buf]);
-      __syncwarp();
-      tn.step(p.acc_bufs);
     }
   }
   return true;
@@ -663,139 +712,152 @@ __device__ __forceinline__ void finish_column(const StreamParams& p, const Share
 
 // After the segments of a product: the cut tiles of this CTA's ranges, this
 // range's share of their columns (column i belongs to the i-th part, modulo
-// the parts), every other one to either set of row warps.
-template <bool H, bool LAYER, bool TOKEN_COLS>
+// the parts), dealt to the sets of row warps.
+template <bool H, bool LAYER>
 __device__ bool join_parts(const StreamParams& p, int which, const Shared& ss, volatile int* abort) {
-  const Product& pr = p.p[which];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int row = (warp & 3) * 32 + lane, set = warp >> 2;
-  Walk<H> walk(pr, ss, p.workers);
+  Walk<H> walk(p.p[which], ss, p.workers);
   Segment s;
   while (walk.next(s)) {
     const Share sh(walk, s);
     if (sh.whole) continue;
     const Columns<H> c(p, ss, s);
-    const int parts = sh.v1 - sh.v0 + 1;
+    const int parts = sh.v1 - sh.v0 + 1, step = kSets * parts;
     const int first = s.worker - sh.v0 + set * parts;
     if (first >= c.m) continue;
     bool ok = true;
     if (lane == 0) ok = wait_count(arrivals_of(p, which, sh.v0), parts * kRowWarps, abort, p.err, (0x29 << 24) | which);
     if (!__shfl_sync(kFull, ok, 0)) return false;
-    for (int i = first; i < c.m; i += 2 * parts) {
-      const int at = (TOKEN_COLS ? ss.row_token[c.r0 + i] : i) * kTileRows;
-      float v[2] = {0.f, 0.f};
-      constexpr int B = 4;  // parts on the way at a time
+    constexpr int C = 2, B = 4;  // columns and parts on the way at a time
+    for (int i0 = first; i0 < c.m; i0 += C * step) {
+      float v[C][2] = {};
       for (int w0 = 0; w0 < parts; w0 += B) {
-        float u[B][2];
+        float u[B][C][2];
 #pragma unroll
         for (int b = 0; b < B; ++b)
 #pragma unroll
-          for (int box = 0; box < 2; ++box)
-            u[b][box] = w0 + b < parts ? __ldcg(part_of(p, sh.v0 + w0 + b, w0 + b == 0, box, row) + at) : 0.f;
+          for (int j = 0; j < C; ++j)
+#pragma unroll
+            for (int box = 0; box < 2; ++box) {
+              const int i = i0 + j * step;
+              u[b][j][box] = 0.f;
+              if (w0 + b < parts && i < c.m)
+                u[b][j][box] = __ldcg(part_of(p, sh.v0 + w0 + b, w0 + b == 0, box, row) + i * kTileRows);
+            }
 #pragma unroll
         for (int b = 0; b < B; ++b)
 #pragma unroll
-          for (int box = 0; box < 2; ++box) v[box] += u[b][box];
+          for (int j = 0; j < C; ++j)
+#pragma unroll
+            for (int box = 0; box < 2; ++box) v[j][box] += u[b][j][box];
       }
-      finish_column<H, LAYER>(p, ss, s, c.r0, i, row, v[0], v[1]);
+#pragma unroll
+      for (int j = 0; j < C; ++j)
+        if (i0 + j * step < c.m) finish_column<H, LAYER>(p, ss, s, c.r0, i0 + j * step, row, v[j][0], v[j][1]);
     }
   }
   return true;
 }
 
-// bf16 weights: a segment's sums are in tensor memory.  Both sets see both
-// accumulators of their rows and take every other column.  `read(c)` gives
-// column c of either box; eight columns are read at a time.
+// A segment's sums are in tensor memory: finishes its tile, or leaves them as
+// a part.  Every set sees all sums of its rows and takes its share of the
+// columns, two at a time.  `read(box, at, u)` starts the loads of one column,
+// `value(u)` makes its sum of them.
+template <bool H, bool LAYER, int LOADS, typename Read, typename Value>
+__device__ __forceinline__ void finish_segment(const StreamParams& p, const Shared& ss, const Segment& s, const Share& sh,
+                                               const Columns<H>& c, const Read& read, const Value& value) {
+  const int warp = threadIdx.x >> 5, row = (warp & 3) * 32 + (threadIdx.x & 31), set = warp >> 2;
+  constexpr int B = 2;
+  for (int i0 = set * B; i0 < c.m; i0 += kSets * B) {
+    uint32_t u[B][2][LOADS];
+#pragma unroll
+    for (int j = 0; j < B; ++j) {
+      const int i = min(i0 + j, c.m - 1);  // past the end: the last column again
+      const int at = H ? i : LAYER ? ss.row_token[c.r0 + i] : i;
+#pragma unroll
+      for (int box = 0; box < 2; ++box) read(box, at, u[j][box]);
+    }
+    tmem_ld_wait();
+#pragma unroll
+    for (int j = 0; j < B; ++j) {
+      const int i = i0 + j;
+      if (i >= c.m) break;
+      const float v0 = value(u[j][0]), v1 = value(u[j][1]);
+      if (sh.whole) {
+        finish_column<H, LAYER>(p, ss, s, c.r0, i, row, v0, v1);
+      } else {
+        __stcg(part_of(p, s.worker, s.kb0 == 0, 0, row) + i * kTileRows, v0);
+        __stcg(part_of(p, s.worker, s.kb0 == 0, 1, row) + i * kTileRows, v1);
+      }
+    }
+  }
+}
+
+// bf16 weights: the accumulators hold a segment's sums.
 template <bool H, bool LAYER>
 __device__ bool rows_bf16(const StreamParams& p, int which, Shared& ss, Turn& tn, volatile int* abort) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int quad = warp & 3, set = warp >> 2, row = quad * 32 + lane;
   Walk<H> walk(p.p[which], ss, p.workers);
   Segment s;
   while (walk.next(s)) {
     const Columns<H> c(p, ss, s);
     const Share sh(walk, s);
-    bool ok = mbar_wait(&ss.acc_full[tn.buf], tn.phase, abort, p.err, (0x33 << 24) | which);
-    if (!__all_sync(kFull, ok)) return false;
+    if (!warp_wait(&ss.acc_full[tn.buf], tn.phase, abort, p.err, (0x33 << 24) | which)) return false;
     tc_fence_after();
-    const uint32_t acc = ss.tmem + (static_cast<uint32_t>(quad * 32) << 16) + tn.buf * 2 * p.acc_cols;
-    constexpr int B = 4;  // columns read at a time
-    for (int i0 = set * B; i0 < c.m; i0 += 2 * B) {
-      float v[2][B];
-      uint32_t u[2][3][B];
+    const uint32_t acc = ss.tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + tn.buf * 2 * p.acc_cols;
+    finish_segment<H, LAYER, H ? 3 : 1>(
+        p, ss, s, sh, c,
+        [&](int box, int at, uint32_t* u) {
 #pragma unroll
-      for (int j = 0; j < B; ++j) {
-        const int i = min(i0 + j, c.m - 1);  // past the end: the last column again
-        const int at = H ? i : LAYER ? ss.row_token[c.r0 + i] : i;
-#pragma unroll
-        for (int box = 0; box < 2; ++box)
-#pragma unroll
-          for (int q = 0; q < 3; ++q) {
-            u[box][q][j] = 0;
-            if (q == 0 || (H && q < p.parts)) u[box][q][j] = tmem_ld1(acc + box * p.acc_cols + q * 16 * c.n16 + at);
+          for (int q = 0; q < (H ? 3 : 1); ++q) {
+            u[q] = 0;
+            if (q < 2 || p.parts == 3) u[q] = tmem_ld1(acc + box * p.acc_cols + q * 16 * c.n16 + at);
           }
-      }
-      tmem_ld_wait();
-#pragma unroll
-      for (int j = 0; j < B; ++j)
-#pragma unroll
-        for (int box = 0; box < 2; ++box) {
-          v[box][j] = __uint_as_float(u[box][0][j]);
-          if (H) v[box][j] += (__uint_as_float(u[box][1][j]) + __uint_as_float(u[box][2][j])) * (1.f / kLowScale);
-        }
-#pragma unroll
-      for (int j = 0; j < B; ++j)
-        if (i0 + j < c.m) {
-          if (sh.whole) {
-            finish_column<H, LAYER>(p, ss, s, c.r0, i0 + j, row, v[0][j], v[1][j]);
-          } else {
-#pragma unroll
-            for (int box = 0; box < 2; ++box)
-              __stcg(part_of(p, s.worker, s.kb0 == 0, box, row) + (i0 + j) * kTileRows, v[box][j]);
-          }
-        }
-    }
+        },
+        [&](const uint32_t* u) {
+          if (!H) return __uint_as_float(u[0]);
+          return fmaf(__uint_as_float(u[H ? 1 : 0]) + __uint_as_float(u[H ? 2 : 0]), 1.f / kLowScale, __uint_as_float(u[0]));
+        });
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&ss.acc_empty[tn.buf]);
     tn.step(p.acc_bufs);
     if (!sh.whole) leave_part(p, which, sh);
   }
-  return join_parts<H, LAYER, false>(p, which, ss, abort);
+  return join_parts<H, LAYER>(p, which, ss, abort);
 }
 
-// 4-bit weights: set 0 owns the first box, set 1 the second, a thread one row
-// of it.  For each group of columns the thread turns its row's codes into the
-// operand, and then, while the tensor core multiplies that, adds the previous
-// group's sums, scaled, to its own.
+// 4-bit weights: set 2 box + t owns a box on every other turn, a thread one
+// row of it.  On its turn the thread turns its row's codes into the operand,
+// and when the tensor core has multiplied that adds the groups' sums, scaled,
+// to its own, while the other set's turn goes on.  (With more than 32 columns
+// it adds half of them on every turn.)
 //
-// Buffers need no barriers of their own beside a_ready and d_full: a thread
-// arrives on a_ready for group g + 1 after it has read the sums of group
-// g - 1, so the accumulator that g + 1 writes is free; and those sums were
-// complete, so the operand buffer that it wrote for g + 1 was read.
+// The operand buffer of a turn is free when the sums of the turn before last
+// are complete, which the set has waited for.
 template <int G, int NC, bool H, bool LAYER>
 struct RowsQ4 {
   using Ge = Geo<G>;
-  // Columns of an accumulator in each 16-column step: the parts of 16 rows of
-  // h lie n16 steps apart.
-  static __device__ __forceinline__ void add_group(const StreamParams& p, uint32_t acc, int n16, float scale,
+  // The parts of 16 rows of h lie n16 steps of 16 columns apart; first: first
+  // step of this thread's columns.
+  static __device__ __forceinline__ void add_group(const StreamParams& p, uint32_t acc, int first, int n16, float scale,
                                                    float (&sum)[NC]) {
 #pragma unroll
     for (int b = 0; b < NC / 16; ++b) {
-      if (b >= n16) break;
+      if (first + b >= n16) break;
       uint32_t u[16];
-      tmem_ld16(acc + b * 16, u);
+      tmem_ld16(acc + (first + b) * 16, u);
       if constexpr (H) {
         uint32_t lo[16];
         tmem_ld16(acc + (n16 + b) * 16, lo);
+        tmem_ld_wait();
         if (p.parts == 3) {
           uint32_t lo2[16];
           tmem_ld16(acc + (2 * n16 + b) * 16, lo2);
           tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < 16; ++i) lo[i] = __float_as_uint(__uint_as_float(lo[i]) + __uint_as_float(lo2[i]));
-        } else {
-          tmem_ld_wait();
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i)
@@ -812,109 +874,94 @@ struct RowsQ4 {
                                  const Segment& s, Ring& rg, Turn& tn, uint32_t& swap, volatile int* abort) {
     const Product& pr = p.p[which];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int quad = warp & 3, box = warp >> 2, row = quad * 32 + lane;
+    const int quad = warp & 3, box = warp >> 3, turn = (warp >> 2) & 1, row = quad * 32 + lane;
     const uint32_t lanes = ss.tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const Columns<H> c(p, ss, s);
     const Share sh(walk, s);
+    const bool split = columns_split<H>(c.n16);
+    const int tg = turn_groups<G>(c.n);
     float sum[NC];
 #pragma unroll
     for (int i = 0; i < NC; ++i) sum[i] = 0.f;
-    float scale_before = 0.f;
-    Turn before = tn;
-    bool pending = false, ok = true;
-    auto take = [&]() {  // the previous group's sums
-      ok = mbar_wait(&ss.d_full[box][before.buf], before.phase, abort, p.err, (0x34 << 24) | which);
-      if (!__all_sync(kFull, ok)) return false;
-      tc_fence_after();
-      add_group(p, lanes + 4 * Ge::a_cols() + (box * 2 + before.buf) * Ge::acc_cols(), c.n16, scale_before, sum);
-      return true;
-    };
     for (int kb = s.kb0; kb < s.kb1; ++kb) {
-      ok = mbar_wait(&ss.full_w[rg.stage], rg.phase, abort, p.err, (0x23 << 24) | which);
-      if (!__all_sync(kFull, ok)) return false;
+      if (!warp_wait(&ss.full_w[rg.stage], rg.phase, abort, p.err, (0x23 << 24) | which)) return false;
       const uint32_t st = smem_u32(ring) + static_cast<uint32_t>(rg.stage) * p.stage_bytes;
       const uint32_t codes = st + box * kBoxBytes + row * 128;
       const uint32_t scales = st + 2 * kBoxBytes + box * Ge::SCALE_BYTES + row * 2;
       const int groups = stage_groups<G>(pr.K, kb);
-#pragma unroll 1
-      for (int j = 0; j < groups; ++j) {
-        const uint32_t a = lanes + (box * 2 + tn.buf) * Ge::a_cols();
-        uint32_t w[G / 32][4];
+      for (int g0 = 0; g0 < groups; g0 += tg) {
+        const int n = min(tg, groups - g0);
+        if (tn.buf == turn) {
+          const uint32_t a = operand_at(lanes, box, turn);
+          for (int j = 0; j < n; ++j) {
+            uint32_t w[G / 32][4];
 #pragma unroll
-        for (int i = 0; i < G / 32; ++i) lds128(codes + (((j * (G / 32) + i) ^ (row & 7)) << 4), w[i]);
-        const float scale = lds_bf16(scales + j * (kTileRows * 2));
+            for (int i = 0; i < G / 32; ++i) lds128(codes + ((((g0 + j) * (G / 32) + i) ^ (row & 7)) << 4), w[i]);
 #pragma unroll
-        for (int i = 0; i < G / 32; ++i) {
-          uint32_t v[16];
+            for (int i = 0; i < G / 32; ++i) {
+              uint32_t v[16];
 #pragma unroll
-          for (int t = 0; t < 4; ++t)
+              for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) v[t * 4 + q] = q4_pair(w[i][t], q);
-          tmem_st16(a + i * 16, v);
+                for (int q = 0; q < 4; ++q) v[t * 4 + q] = q4_pair(w[i][t], q);
+              tmem_st16(a + j * (G / 2) + i * 16, v);
+            }
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ss.a_ready[box][turn]);
         }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ss.a_ready[box][tn.buf]);
-        if (pending && !take()) return false;
-        before = tn;
-        scale_before = scale;
-        pending = true;
+        if (tn.buf == turn || split) {
+          if (!warp_wait(&ss.d_full[box][tn.buf], tn.phase, abort, p.err, (0x34 << 24) | which)) return false;
+          tc_fence_after();
+          const uint32_t acc = sums_at(lanes, box, tn.buf);
+          for (int j = 0; j < n; ++j)
+            add_group(p, acc + j * c.n, split ? turn * 2 : 0, c.n16, lds_bf16(scales + (g0 + j) * (kTileRows * 2)), sum);
+        }
+        if (split || tn.buf == turn) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_n(&ss.d_empty[box][tn.buf], split ? 1 : 2);
+        }
         tn.step(2);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&ss.empty[rg.stage]);
       rg.step(p.stages);
     }
-    if (!take()) return false;
 
-    const int real = H ? c.m : p.T;  // columns with values of their own
-    if (!sh.whole) {
+    // All sums of the tile meet in tensor memory, in the sets' operand
+    // buffers: both boxes' and both turns' (or column halves').  No set goes
+    // on before all have read their share.
 #pragma unroll
-      for (int i = 0; i < NC; ++i)
-        if (i < real) __stcg(part_of(p, s.worker, s.kb0 == 0, box, row) + i * kTileRows, sum[i]);
-      leave_part(p, which, sh);
-      tc_fence_before();
-      return true;
+    for (int b = 0; b < NC / 16; ++b) {
+      uint32_t u[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(sum[b * 16 + i]);
+      tmem_st16(operand_at(lanes, box, turn) + b * 16, u);
     }
-    if constexpr (LAYER && !H) {
-      // Both boxes' sums of a hidden column meet in tensor memory, in the
-      // accumulators just read; no set goes on before both have read them.
-      const uint32_t acc = lanes + 4 * Ge::a_cols() + before.buf * Ge::acc_cols();
-#pragma unroll
-      for (int b = 0; b < NC / 16; ++b) {
-        uint32_t u[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(sum[b * 16 + i]);
-        tmem_st16(acc + box * 2 * Ge::acc_cols() + b * 16, u);
-      }
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ss.swap_ready);
-      ok = mbar_wait(&ss.swap_ready, swap, abort, p.err, 0x35 << 24);
-      if (!__all_sync(kFull, ok)) return false;
-      tc_fence_after();
-      for (int i = box; i < c.m; i += 2) {
-        const int at = ss.row_token[c.r0 + i];
-        const uint32_t ua = tmem_ld1(acc + at), ub = tmem_ld1(acc + 2 * Ge::acc_cols() + at);
-        tmem_ld_wait();
-        const int hi = s.rt * kTileRows + row;
-        if (hi < p.f) store_hidden(p, c.r0 + i, hi, ss.row_w[c.r0 + i], __uint_as_float(ua), __uint_as_float(ub));
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ss.swap_done);
-      ok = mbar_wait(&ss.swap_done, swap, abort, p.err, 0x36 << 24);
-      if (!__all_sync(kFull, ok)) return false;
-      swap ^= 1;
-      tc_fence_after();
-    } else {
-#pragma unroll
-      for (int i = 0; i < NC; ++i)
-        if (i < c.m) store_out<LAYER>(p, c.r0 + i, (s.rt * 2 + box) * kTileRows + row, sum[i]);
-      tc_fence_before();
-    }
+    tmem_st_wait();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ss.swap_ready);
+    if (!warp_wait(&ss.swap_ready, swap, abort, p.err, (0x35 << 24) | which)) return false;
+    tc_fence_after();
+    finish_segment<H, LAYER, 2>(
+        p, ss, s, sh, c,
+        [&](int bx, int at, uint32_t* u) {
+          u[0] = tmem_ld1(operand_at(lanes, bx, split ? at >> 5 : 0) + (split ? at & 31 : at));
+          u[1] = 0;
+          if (!split) u[1] = tmem_ld1(operand_at(lanes, bx, 1) + at);
+        },
+        [&](const uint32_t* u) { return __uint_as_float(u[0]) + __uint_as_float(u[1]); });
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ss.swap_done);
+    if (!warp_wait(&ss.swap_done, swap, abort, p.err, (0x36 << 24) | which)) return false;
+    swap ^= 1;
+    tc_fence_after();
+    if (!sh.whole) leave_part(p, which, sh);
     return true;
   }
 };
@@ -926,15 +973,12 @@ __device__ bool rows_q4(const StreamParams& p, int which, Shared& ss, uint8_t* r
   Segment s;
   bool ok = true;
   while (ok && walk.next(s)) {
-    const int n16 = Columns<H>(p, ss, s).n16;
-    if (n16 == 1)
+    if (Columns<H>(p, ss, s).n16 == 1)
       ok = RowsQ4<G, 16, H, LAYER>::segment(p, which, ss, ring, walk, s, rg, tn, swap, abort);
-    else if (n16 == 2 || H)
-      ok = RowsQ4<G, 32, H, LAYER>::segment(p, which, ss, ring, walk, s, rg, tn, swap, abort);
     else
-      ok = RowsQ4<G, H ? 32 : 64, H, LAYER>::segment(p, which, ss, ring, walk, s, rg, tn, swap, abort);
+      ok = RowsQ4<G, 32, H, LAYER>::segment(p, which, ss, ring, walk, s, rg, tn, swap, abort);
   }
-  return ok && join_parts<H, LAYER, LAYER && !H>(p, which, ss, abort);
+  return ok && join_parts<H, LAYER>(p, which, ss, abort);
 }
 
 // y[t] = its slots' rows in slot order, then the shared experts', in fp32.
@@ -980,20 +1024,21 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
     for (int i = 0; i < p.stages; ++i) {
       mbar_init(&ss.full_w[i], 1);
       mbar_init(&ss.full_x[i], 1);
-      mbar_init(&ss.empty[i], Ge::Q4 ? kRowWarps + 1 : 1);
+      mbar_init(&ss.empty[i], Ge::Q4 ? kRowWarps + 2 : 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ss.acc_full[i], 1);
       mbar_init(&ss.acc_empty[i], kRowWarps);
       for (int j = 0; j < 2; ++j) {
-        mbar_init(&ss.a_ready[i][j], kRowWarps / 2);
+        mbar_init(&ss.a_ready[i][j], 4);
         mbar_init(&ss.d_full[i][j], 1);
+        mbar_init(&ss.d_empty[i][j], 8);  // two sets, or one that arrives twice
       }
     }
     mbar_init(&ss.swap_ready, kRowWarps);
     mbar_init(&ss.swap_done, kRowWarps);
     mbar_init(&ss.out_done, 1);
-    mbar_init(&ss.drained, 1);
+    mbar_init(&ss.drained, 2);
     ss.abort = 0;
     fence_mbar_init();
   }
@@ -1040,12 +1085,18 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
     if (ok) ok = produce_columns<G, LAYER>(p, 1, ss, ring, rg, dr, abort);
     if (LAYER && ok && wait_all(kCtrOut, 0x26) && lane == 0) mbar_arrive(&ss.out_done);
     dr.wait(ss.full_x);
-  } else if (warp == kMmaWarp) {
+  } else if (warp >= kMmaWarp) {
     Ring rg;
     Turn tn;
     bool ok = true;
-    if (LAYER) ok = issue_mmas<G, false>(p, 0, ss, ring, rg, tn, abort);
-    if (ok) issue_mmas<G, LAYER>(p, 1, ss, ring, rg, tn, abort);
+    if constexpr (Ge::Q4) {
+      const int box = warp - kMmaWarp;
+      if (LAYER) ok = issue_q4<G, false>(p, 0, box, ss, ring, rg, tn, abort);
+      if (ok) issue_q4<G, LAYER>(p, 1, box, ss, ring, rg, tn, abort);
+    } else if (warp == kMmaWarp) {
+      if (LAYER) ok = issue_bf16<false>(p, 0, ss, ring, rg, tn, abort);
+      if (ok) issue_bf16<LAYER>(p, 1, ss, ring, rg, tn, abort);
+    }
     __syncwarp();
     if (elect_one()) umma_commit(&ss.drained);
     __syncwarp();
@@ -1093,7 +1144,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
   __syncthreads();
   if (ss.abort) {
     for (int i = tid; i < 2 * kMaxWorkers; i += kThreads) p.arrive[i] = 0;
-    if (tid < 3) p.err[kCtrHidden + tid] = 0;
+    if (tid < 4) p.err[kCtrHidden + tid] = 0;
   }
 }
 

@@ -85,78 +85,57 @@ __device__ __forceinline__ bool row_softmax(const float* __restrict__ row, int E
   return row_stats<EPL>(E, lane, r, key);
 }
 
-// Routes U tokens on one warp (their logit rows already in r[u].v): softmax
+// Routes token t on one warp (its logit row already in r.v): softmax
 // statistics, then k rounds of warp argmax.  Lane j < k ends with slot j's
 // expert and weight.  A row with a non-finite logit is reported and gets the
-// placeholder routing slot j -> expert j with weight 0.  A token's rounds are
-// a serial chain of warp operations; several tokens share its latency.
-template <int EPL, int U>
-__device__ __forceinline__ void route_tokens(RowSoftmax<EPL> (&r)[U], const int (&t)[U], int E, int k, int renorm,
-                                             int lane, int* err, int (&my_idx)[U], float (&my_w)[U]) {
-  unsigned key[U][EPL];
-  bool fine[U];
-  float my_ex[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    fine[u] = row_stats<EPL>(E, lane, r[u], key[u]);
-    if (!fine[u] && lane == 0) record_error(err, MOE_ERR_NONFINITE_CODE, t[u]);
-    my_idx[u] = lane;
-    my_ex[u] = 0.f;
-  }
-  for (int j = 0; j < k; ++j) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      // Best remaining entry of this lane: strictly greater keeps the lower
-      // index on ties (entries are visited in increasing expert index).
-      unsigned bk = 0;
-      unsigned be = 0xffffffffu;
-#pragma unroll
-      for (int i = 0; i < EPL; ++i)
-        if (key[u][i] > bk) {
-          bk = key[u][i];
-          be = static_cast<unsigned>(lane + 32 * i);
-        }
-      // Winner under (value desc, index asc), a strict total order: the
-      // largest key, then the lowest expert index holding it.  Every lane
-      // gets the same winner.
-      const unsigned kbest = __reduce_max_sync(kFull, bk);
-      const int bi = static_cast<int>(__reduce_min_sync(kFull, bk == kbest ? be : 0xffffffffu));
-      const int owner = bi & 31, which = bi >> 5;
-      float ex = 0.f;
-#pragma unroll
-      for (int i = 0; i < EPL; ++i)
-        if (i == which) {
-          if (lane == owner) key[u][i] = 0u;  // taken
-          ex = r[u].ex[i];
-        }
-      ex = __shfl_sync(kFull, ex, owner);
-      if (lane == j && fine[u]) {
-        my_idx[u] = bi;
-        my_ex[u] = ex;
-      }
-    }
-  }
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    // one division per slot, all slots at once, outside the serial picks
-    const float my_p = my_ex[u] / r[u].s;
-    float psum = 0.f;
-    if (renorm)
-      for (int j = 0; j < k; ++j) psum += __shfl_sync(kFull, my_p, j);
-    my_w[u] = !fine[u] ? 0.f : renorm ? my_p / psum : my_p;
-  }
-}
-
+// placeholder routing slot j -> expert j with weight 0.
 template <int EPL>
 __device__ __forceinline__ void route_token(RowSoftmax<EPL>& r, int t, int E, int k, int renorm, int lane, int* err,
                                             int& my_idx, float& my_w) {
-  RowSoftmax<EPL> rs[1] = {r};
-  const int ts[1] = {t};
-  int idx[1];
-  float w[1];
-  route_tokens<EPL, 1>(rs, ts, E, k, renorm, lane, err, idx, w);
-  my_idx = idx[0];
-  my_w = w[0];
+  my_idx = lane;
+  my_w = 0.f;
+  unsigned key[EPL];
+  if (!row_stats<EPL>(E, lane, r, key)) {
+    if (lane == 0) record_error(err, MOE_ERR_NONFINITE_CODE, t);
+    return;
+  }
+  float my_ex = 0.f;
+  for (int j = 0; j < k; ++j) {
+    // Best remaining entry of this lane: strictly greater keeps the lower
+    // index on ties (entries are visited in increasing expert index).
+    unsigned bk = 0;
+    unsigned be = 0xffffffffu;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (key[i] > bk) {
+        bk = key[i];
+        be = static_cast<unsigned>(lane + 32 * i);
+      }
+    // Winner under (value desc, index asc), a strict total order: the
+    // largest key, then the lowest expert index holding it.  Every lane
+    // gets the same winner.
+    const unsigned kbest = __reduce_max_sync(kFull, bk);
+    const int bi = static_cast<int>(__reduce_min_sync(kFull, bk == kbest ? be : 0xffffffffu));
+    const int owner = bi & 31, which = bi >> 5;
+    float ex = 0.f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (i == which) {
+        if (lane == owner) key[i] = 0u;  // taken
+        ex = r.ex[i];
+      }
+    ex = __shfl_sync(kFull, ex, owner);
+    if (lane == j) {
+      my_idx = bi;
+      my_ex = ex;
+    }
+  }
+  // one division per slot, all slots at once, outside the serial picks
+  const float my_p = my_ex / r.s;
+  float psum = 0.f;
+  if (renorm)
+    for (int j = 0; j < k; ++j) psum += __shfl_sync(kFull, my_p, j);
+  my_w = renorm ? my_p / psum : my_p;
 }
 
 }  // namespace moe
