@@ -132,7 +132,7 @@ struct StreamParams {
 struct alignas(16) Shared {
   uint64_t full_w[kMaxStages], full_x[kMaxStages], empty[kMaxStages];
   uint64_t acc_full[2], acc_empty[2];   // bf16: accumulator pairs
-  uint64_t a_ready[2][2], d_full[2][2], d_empty[2][2]; // 4 bits: [box][turn]
+  uint64_t a_ready[2][2], d_full[2][2], d_empty[2][2]; // 4 bits: [box][turn]; d_empty: kSplit
   uint64_t swap_ready, swap_done;       // 4 bits: all sums of a tile in tensor memory
   uint64_t out_done;                    // every CTA's output rows are there
   uint64_t drained;                     // tensor instructions all complete
@@ -532,28 +532,35 @@ struct Turn {
   }
 };
 
-// 4 bits: a turn is as many groups of a stage as fit the operand buffer and,
-// with c columns each, the accumulators.
+// 4 bits: how the sums of a turn are taken.
+//   kOwn    up to 32 columns: by the set whose turn it was, while its next turn
+//           is multiplied into the other half of its accumulators
+//   kWhole  more columns that one set can hold (parts of h): before its next turn
+//   kSplit  more than 32 tokens: by both sets, half the columns each, while the
+//           next turn is multiplied
+enum class Sums { kOwn, kWhole, kSplit };
+template <bool H>
+__device__ __forceinline__ Sums sums_of(const Columns<H>& c) {
+  return c.n <= kSumCols / 2 ? Sums::kOwn : H ? Sums::kWhole : Sums::kSplit;
+}
+// A turn is as many groups of a stage as fit the operand buffer and the
+// accumulators.
+template <int G>
+constexpr int kMaxTurnGroups = kOperandCols * 2 / G < 2 ? 1 : 2;
 template <int G>
 __device__ __forceinline__ int turn_groups(int columns) {
-  return max(1, min(kOperandCols * 2 / G, kSumCols / columns));
+  return max(1, min(kMaxTurnGroups<G>, kSumCols / 2 / columns));
 }
 // Groups of a stage that lie inside K.
 template <int G>
 __device__ __forceinline__ int stage_groups(int K, int kb) {
   return min(Geo<G>::KB, K - kb * Geo<G>::KB) / G;
 }
-// Columns beyond 32 are added up by the other turn's set (H tiles have at
-// most 32 rows): both sets read the sums of every turn then.
-template <bool H>
-__device__ __forceinline__ bool columns_split(int n16) {
-  return !H && n16 > 2;
-}
 __device__ __forceinline__ uint32_t operand_at(uint32_t tmem, int box, int turn) {
   return tmem + (box * 2 + turn) * kOperandCols;
 }
-__device__ __forceinline__ uint32_t sums_at(uint32_t tmem, int box, int turn) {
-  return tmem + 4 * kOperandCols + (box * 2 + turn) * kSumCols;
+__device__ __forceinline__ uint32_t sums_at(uint32_t tmem, int box, const Turn& tn, Sums how) {
+  return tmem + 4 * kOperandCols + (box * 2 + tn.buf) * kSumCols + (how == Sums::kOwn ? tn.phase * (kSumCols / 2) : 0);
 }
 
 template <bool H>
@@ -603,24 +610,33 @@ __device__ bool issue_q4(const StreamParams& p, int which, int box, Shared& ss, 
     const Columns<H> c(p, ss, s);
     const uint32_t idesc = idesc_bf16_f32(kTileRows, c.n, 0, 0);
     const int tg = turn_groups<G>(c.n);
+    const Sums how = sums_of(c);
+    const uint32_t atom = c.n * 128;
     for (int kb = s.kb0; kb < s.kb1; ++kb) {
       const uint32_t x = smem_u32(ring) + static_cast<uint32_t>(rg.stage) * p.stage_bytes + Ge::WEIGHT_BYTES;
       if (!warp_wait(&ss.full_x[rg.stage], rg.phase, abort, p.err, (0x24 << 24) | which)) return false;
       const int groups = stage_groups<G>(pr.K, kb);
       for (int g0 = 0; g0 < groups; g0 += tg) {
+        const uint32_t a = operand_at(ss.tmem, box, tn.buf), d = sums_at(ss.tmem, box, tn, how);
+        const bool second = kMaxTurnGroups<G> == 2 && tg == 2 && g0 + 1 < groups;
+        // 64 columns of the stage start `atom` bytes apart; a group never leaves its own
+        // 64 unless it is 128 wide
+        const uint32_t xg = x + (g0 * G / 64) * atom + (g0 * G % 64) * 2;
+        const uint32_t xg2 = x + ((g0 + 1) * G / 64) * atom + ((g0 + 1) * G % 64) * 2;
+        if (how == Sums::kSplit &&
+            !warp_wait(&ss.d_empty[box][tn.buf], tn.phase ^ 1, abort, p.err, (0x37 << 24) | which))
+          return false;
         if (!warp_wait(&ss.a_ready[box][tn.buf], tn.phase, abort, p.err, (0x32 << 24) | which)) return false;
-        if (!warp_wait(&ss.d_empty[box][tn.buf], tn.phase ^ 1, abort, p.err, (0x37 << 24) | which)) return false;
         tc_fence_after();
-        const uint32_t a = operand_at(ss.tmem, box, tn.buf), d = sums_at(ss.tmem, box, tn.buf);
-        const int n = min(tg, groups - g0);
         if (elect_one()) {
-          for (int j = 0; j < n; ++j)
 #pragma unroll
-            for (int i = 0; i < G / 16; ++i) {
-              const int k = (g0 + j) * G + i * 16;
-              umma_bf16_ta(d + j * c.n, a + j * (G / 2) + i * 8,
-                           smem_desc_sw128(x + (k / 64) * c.n * 128 + (k % 64) * 2, 16, 1024), idesc, i != 0 ? 1u : 0u);
-            }
+          for (int i = 0; i < G / 16; ++i)
+            umma_bf16_ta(d, a + i * 8, smem_desc_sw128(xg + (i / 4) * atom + (i % 4) * 32, 16, 1024), idesc, i != 0);
+          if (second)
+#pragma unroll
+            for (int i = 0; i < G / 16; ++i)
+              umma_bf16_ta(d + c.n, a + G / 2 + i * 8, smem_desc_sw128(xg2 + (i / 4) * atom + (i % 4) * 32, 16, 1024),
+                           idesc, i != 0);
           umma_commit(&ss.d_full[box][tn.buf]);
           if (g0 + tg >= groups) umma_commit(&ss.empty[rg.stage]);
         }
@@ -829,13 +845,14 @@ __device__ bool rows_bf16(const StreamParams& p, int which, Shared& ss, Turn& tn
 }
 
 // 4-bit weights: set 2 box + t owns a box on every other turn, a thread one
-// row of it.  On its turn the thread turns its row's codes into the operand,
-// and when the tensor core has multiplied that adds the groups' sums, scaled,
-// to its own, while the other set's turn goes on.  (With more than 32 columns
-// it adds half of them on every turn.)
+// row of it.  On its turn the thread turns its row's codes into the operand;
+// the sums of an earlier turn, scaled, are added to the thread's own while the
+// tensor core works on a later one (see Sums).
 //
-// The operand buffer of a turn is free when the sums of the turn before last
-// are complete, which the set has waited for.
+// The operand buffer of a turn is free once the sums of the set's previous
+// turn are complete, and so is the half of the accumulators that this turn
+// fills (kOwn: read before the previous turn's codes were handed over; kWhole:
+// before this turn's).
 template <int G, int NC, bool H, bool LAYER>
 struct RowsQ4 {
   using Ge = Geo<G>;
@@ -878,11 +895,31 @@ struct RowsQ4 {
     const uint32_t lanes = ss.tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const Columns<H> c(p, ss, s);
     const Share sh(walk, s);
-    const bool split = columns_split<H>(c.n16);
+    const Sums how = sums_of(c);
+    const bool split = how == Sums::kSplit;
     const int tg = turn_groups<G>(c.n);
     float sum[NC];
 #pragma unroll
     for (int i = 0; i < NC; ++i) sum[i] = 0.f;
+    Turn before;               // the turn whose sums are still to be taken
+    float scale_before[kMaxTurnGroups<G>];
+    int n_before = 0;
+    auto complete = [&]() {
+      const bool ok = warp_wait(&ss.d_full[box][before.buf], before.phase, abort, p.err, (0x34 << 24) | which);
+      tc_fence_after();
+      return ok;
+    };
+    auto add = [&]() {
+      const uint32_t acc = sums_at(lanes, box, before, how);
+#pragma unroll
+      for (int j = 0; j < kMaxTurnGroups<G>; ++j)
+        if (j < n_before) add_group(p, acc + j * c.n, split ? turn * 2 : 0, c.n16, scale_before[j], sum);
+      tc_fence_before();
+      if (split) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ss.d_empty[box][before.buf]);
+      }
+    };
     for (int kb = s.kb0; kb < s.kb1; ++kb) {
       if (!warp_wait(&ss.full_w[rg.stage], rg.phase, abort, p.err, (0x23 << 24) | which)) return false;
       const uint32_t st = smem_u32(ring) + static_cast<uint32_t>(rg.stage) * p.stage_bytes;
@@ -890,45 +927,52 @@ struct RowsQ4 {
       const uint32_t scales = st + 2 * kBoxBytes + box * Ge::SCALE_BYTES + row * 2;
       const int groups = stage_groups<G>(pr.K, kb);
       for (int g0 = 0; g0 < groups; g0 += tg) {
-        const int n = min(tg, groups - g0);
-        if (tn.buf == turn) {
-          const uint32_t a = operand_at(lanes, box, turn);
-          for (int j = 0; j < n; ++j) {
-            uint32_t w[G / 32][4];
-#pragma unroll
-            for (int i = 0; i < G / 32; ++i) lds128(codes + ((((g0 + j) * (G / 32) + i) ^ (row & 7)) << 4), w[i]);
-#pragma unroll
-            for (int i = 0; i < G / 32; ++i) {
-              uint32_t v[16];
-#pragma unroll
-              for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) v[t * 4 + q] = q4_pair(w[i][t], q);
-              tmem_st16(a + j * (G / 2) + i * 16, v);
-            }
+        const bool mine = tn.buf == turn;
+        if (mine || split) {
+          if (!split && n_before) {
+            if (!complete()) return false;
+            if (how == Sums::kWhole) add();
           }
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ss.a_ready[box][turn]);
-        }
-        if (tn.buf == turn || split) {
-          if (!warp_wait(&ss.d_full[box][tn.buf], tn.phase, abort, p.err, (0x34 << 24) | which)) return false;
-          tc_fence_after();
-          const uint32_t acc = sums_at(lanes, box, tn.buf);
-          for (int j = 0; j < n; ++j)
-            add_group(p, acc + j * c.n, split ? turn * 2 : 0, c.n16, lds_bf16(scales + (g0 + j) * (kTileRows * 2)), sum);
-        }
-        if (split || tn.buf == turn) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_n(&ss.d_empty[box][tn.buf], split ? 1 : 2);
+          const int n = min(tg, groups - g0);
+          float scale[kMaxTurnGroups<G>];
+#pragma unroll
+          for (int j = 0; j < kMaxTurnGroups<G>; ++j) scale[j] = j < n ? lds_bf16(scales + (g0 + j) * (kTileRows * 2)) : 0.f;
+          if (mine) {
+            const uint32_t a = operand_at(lanes, box, turn);
+            for (int j = 0; j < n; ++j)
+#pragma unroll
+              for (int i = 0; i < G / 32; ++i) {
+                uint32_t w[4], v[16];
+                lds128(codes + ((((g0 + j) * (G / 32) + i) ^ (row & 7)) << 4), w);
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                  for (int q = 0; q < 4; ++q) v[t * 4 + q] = q4_pair(w[t], q);
+                tmem_st16(a + j * (G / 2) + i * 16, v);
+              }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ss.a_ready[box][turn]);
+          }
+          if (n_before) {
+            if (split && !complete()) return false;
+            if (how != Sums::kWhole) add();
+          }
+          before = tn;
+          n_before = n;
+#pragma unroll
+          for (int j = 0; j < kMaxTurnGroups<G>; ++j) scale_before[j] = scale[j];
         }
         tn.step(2);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&ss.empty[rg.stage]);
       rg.step(p.stages);
+    }
+    if (n_before) {
+      if (!complete()) return false;
+      add();
     }
 
     // All sums of the tile meet in tensor memory, in the sets' operand
@@ -1032,7 +1076,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
       for (int j = 0; j < 2; ++j) {
         mbar_init(&ss.a_ready[i][j], 4);
         mbar_init(&ss.d_full[i][j], 1);
-        mbar_init(&ss.d_empty[i][j], 8);  // two sets, or one that arrives twice
+        mbar_init(&ss.d_empty[i][j], 8);
       }
     }
     mbar_init(&ss.swap_ready, kRowWarps);
