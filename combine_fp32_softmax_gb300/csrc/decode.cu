@@ -7,17 +7,14 @@
 // What bounds it: at 64 tokens the products need 8 flops per weight byte,
 // the tensor cores balance at 280, so the weights' bytes are the work.  The
 // kernel is built around keeping them coming:
-//   - A producer thread keeps a ring of shared-memory stages full of weight
+//   - A producer warp keeps a ring of shared-memory stages full of weight
 //     tiles (two TMA boxes of 128 rows x 128 bytes), 96 to 192 KB in flight
 //     per SM.  It needs nothing but the routing, so it runs ahead into W2
 //     while the hidden values of this and other CTAs are still being made:
 //     the grid-wide dependency between the two products costs no bandwidth.
-//   - A second producer thread brings the activation rows of the same tiles
-//     and is the one that waits for the hidden values of all CTAs before the
-//     second product.  The first product multiplies every tile with all T
-//     tokens' rows of x, one box, and the epilogue picks the expert's: rows
-//     gathered one by one cost more time than the weights of their stage,
-//     while the tensor cores have the columns to spare.
+//   - A second producer brings the activation rows of the same tiles (the
+//     tokens of an expert four at a time by TMA gather) and is the one that
+//     waits for the hidden values of all CTAs before the second product.
 //   - tcgen05: the weights are the 128-row operand, the tokens its columns,
 //     so a handful of tokens costs the smallest instruction (N = 16).
 //     bf16 weights are read from the stage.  4-bit codes are turned into
@@ -96,10 +93,10 @@ struct Geo {
   static constexpr int GROUPS = Q4 ? KB / (Q4 ? G : 1) : 0;    // scale rows
   static constexpr int SCALE_BYTES = GROUPS * kTileRows * 2;   // of one box
   static constexpr int WEIGHT_BYTES = 2 * (kBoxBytes + SCALE_BYTES);
-  // Rows of h in one tile of the second product.  bf16 weights: all of them.
-  // 4 bits: what the accumulators hold; an expert with more rows has its
-  // weight tiles visited again, from L2.
-  __host__ __device__ static constexpr int h_rows(int parts) { return !Q4 ? 64 : parts == 2 ? 32 : 16; }
+  // Activation rows of a tile, in `parts` parts.  bf16 weights: all of an
+  // expert's.  4 bits: what the accumulators hold twice (kOwn, below); an
+  // expert with more rows has its weight tiles visited again, from L2.
+  __host__ __device__ static constexpr int block_rows(int parts) { return !Q4 ? 64 : parts == 1 ? 32 : 16; }
 };
 
 // One product of the launch: weight tiles of `row_step` output rows.
@@ -108,6 +105,7 @@ struct Product {
   CUtensorMap s0, s1;   // their scales (4 bits)
   CUtensorMap cols;     // activation rows
   int K, kblocks, rows, row_step, row_tiles;
+  int block;            // most activation rows of a tile
 };
 
 struct StreamParams {
@@ -123,33 +121,31 @@ struct StreamParams {
   void* y;
   int* err;             // error word and counters
   int y_type, workers, stages, stage_bytes;
-  int tcols;            // T rounded up to 16: columns of the first product and of the linear form
   int parts;            // bf16 parts of a hidden value
-  int h_block;          // rows of h in one tile of the second product
   int acc_cols, acc_bufs;  // bf16 weights: columns of an accumulator, accumulator pairs
 };
 
 struct alignas(16) Shared {
   uint64_t full_w[kMaxStages], full_x[kMaxStages], empty[kMaxStages];
   uint64_t acc_full[2], acc_empty[2];   // bf16: accumulator pairs
-  uint64_t a_ready[2][2], d_full[2][2], d_empty[2][2]; // 4 bits: [box][turn]; d_empty: kSplit
+  uint64_t a_ready[2][2], d_full[2][2]; // 4 bits: [box][turn]
   uint64_t swap_ready, swap_done;       // 4 bits: all sums of a tile in tensor memory
   uint64_t out_done;                    // every CTA's output rows are there
   uint64_t drained;                     // tensor instructions all complete
   uint32_t tmem;
   int abort;
-  int nact, nblk;                  // work list entries, blocks of h rows in all
+  int nact, nblk[2];               // work list entries; blocks of rows in all, by product
   int e[kMaxActive];               // expert
   int m[kMaxActive];               // its rows
   int row0[kMaxActive];            // its first row in h and o
-  int blk0[kMaxActive + 1];        // blocks of h rows before it
+  int blk0[2][kMaxActive + 1];     // blocks of rows before it, by product
   unsigned mask[256][2];           // tokens that picked expert e
   float row_w[kMaxRows];
   float pick_w[kMaxPicks];
   short pick_e[kMaxPicks];
   short pick_row[kMaxPicks];
   short entry[256];                // expert's place in the work list
-  unsigned scan[8];                // packed sums of 32 experts each
+  unsigned scan[8][2];             // packed sums of 32 experts each
   unsigned char row_token[kMaxRows];
 };
 constexpr int kSharedBytes = (sizeof(Shared) + 127) / 128 * 128;
@@ -235,50 +231,61 @@ __device__ void build_work_list(const StreamParams& p, Shared& ss) {
       note_pick(ss, i, i / p.k, min(max(__ldcg(p.topk_idx + i), 0), p.E - 1), __ldcg(p.topk_w + i));
   }
   __syncthreads();
-  // Thread e: expert e.  Exclusive sums of rows, entries and blocks of h rows
-  // over the experts, packed into 11 + 10 + 11 bits (at most 512, 256 and 288).
-  unsigned mine = 0, incl = 0;
+  // Thread e: expert e.  Exclusive sums over the experts of rows and entries
+  // (at most 512 and 256) and of either product's blocks of rows (at most
+  // 288), packed in pairs.
+  unsigned mine[2] = {}, incl[2] = {};
   int n = 0;
+  auto blocks = [&](int which, int rows) { return (rows + p.p[which].block - 1) / p.p[which].block; };
   if (tid < 256) {
     n = tid < p.E ? __popc(ss.mask[tid][0]) + __popc(ss.mask[tid][1]) : 0;
-    mine = n ? static_cast<unsigned>(n) | 1u << 11 | static_cast<unsigned>((n + p.h_block - 1) / p.h_block) << 21 : 0u;
-    incl = mine;
+    mine[0] = n ? n | 1 << 16 : 0;
+    mine[1] = blocks(0, n) | blocks(1, n) << 16;
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const unsigned x = __shfl_up_sync(kFull, incl, off);
-      if (lane >= off) incl += x;
+    for (int j = 0; j < 2; ++j) {
+      incl[j] = mine[j];
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const unsigned x = __shfl_up_sync(kFull, incl[j], off);
+        if (lane >= off) incl[j] += x;
+      }
+      if (lane == 31) ss.scan[warp][j] = incl[j];
     }
-    if (lane == 31) ss.scan[warp] = incl;
   }
   __syncthreads();
-  unsigned before = 0, all = 0;
+  unsigned before[2] = {}, all[2] = {};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const unsigned x = ss.scan[i];
-    if (i < warp) before += x;
-    all += x;
-  }
-  const int all_a = all >> 11 & 1023, all_b = all >> 21;
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const unsigned x = ss.scan[i][j];
+      if (i < warp) before[j] += x;
+      all[j] += x;
+    }
+  const int all_a = all[0] >> 16, all_b[2] = {static_cast<int>(all[1] & 0xFFFF), static_cast<int>(all[1] >> 16)};
   if (tid < 256 && n) {
-    const unsigned at = before + incl - mine;
-    const int a = at >> 11 & 1023;
+    const unsigned at = before[0] + incl[0] - mine[0], blk = before[1] + incl[1] - mine[1];
+    const int a = at >> 16;
     ss.entry[tid] = static_cast<short>(a);
     ss.e[a] = tid;
     ss.m[a] = n;
-    ss.row0[a] = at & 2047;
-    ss.blk0[a] = at >> 21;
+    ss.row0[a] = at & 0xFFFF;
+    ss.blk0[0][a] = blk & 0xFFFF;
+    ss.blk0[1][a] = blk >> 16;
   }
-  const int per = (p.T + p.h_block - 1) / p.h_block;
   if (tid < p.S) {
     ss.e[all_a + tid] = p.E + tid;
     ss.m[all_a + tid] = p.T;
     ss.row0[all_a + tid] = R + tid * p.T;
-    ss.blk0[all_a + tid] = all_b + tid * per;
   }
-  if (tid == 0) {
-    ss.nact = all_a + p.S;
-    ss.nblk = all_b + p.S * per;
-    ss.blk0[all_a + p.S] = all_b + p.S * per;
+  if (tid <= p.S) {  // the shared experts' blocks, and the ends
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int at = all_b[j] + tid * blocks(j, p.T);
+      ss.blk0[j][all_a + tid] = at;
+      if (tid == p.S) ss.nblk[j] = at;
+    }
+    if (tid == p.S) ss.nact = all_a + p.S;
   }
   for (int i = tid; i < p.S * p.T; i += kThreads) {
     ss.row_token[R + i] = static_cast<unsigned char>(i % p.T);
@@ -297,57 +304,47 @@ __device__ void build_work_list(const StreamParams& p, Shared& ss) {
 }
 
 // ------------------------------------------------------------------ ranges
-// The K blocks of a product, tile after tile, cut into `workers` contiguous
-// ranges.  Every role of a CTA walks the same segments: the K blocks
-// [kb0, kb1) of one tile.  The tiles of one row tile of all experts follow
-// each other, so the shared experts, which have the most rows to finish, are
-// spread over the ranges.
+// The K blocks of a product, tile after tile, cut into contiguous ranges.
+// Every role of a CTA walks the same segments: the K blocks [kb0, kb1) of one
+// tile.  The tiles of one row tile of all experts follow each other, so the
+// shared experts, which have the most rows to finish, are spread over the
+// ranges.
+//
+// Putting a cut tile together again costs about 4 us of latency (parts,
+// count, wait, parts back), the streaming time of some 10 K blocks of an SM
+// that has its share of the memory: tiles of at most kWholeBlocks are not
+// cut, and longer ones not into ranges of fewer than kMinBlocks.
+constexpr int kWholeBlocks = 8, kMinBlocks = 4;
+
 struct Segment {
   int worker, item, kb0, kb1;
-  int a, rt, nb;   // work list entry, row tile, block of h rows (second product of the layer)
+  int a, rt, nb;   // work list entry, row tile, block of the expert's rows
 };
 
-template <bool BLOCKS>  // an expert may have several blocks of h rows: the layer's second product
 struct Walk {
   const Product& pr;
   const Shared& ss;
+  const int* blk0;
   int workers, v;
-  int units, per;    // K blocks, tiles of a row tile
+  int units, grain;  // K blocks, and how many a range takes at least of a tile
+  int per;           // tiles of a row tile
   int u, u1;
 
-  __device__ Walk(const Product& product, const Shared& shared, int most) : pr(product), ss(shared) {
-    per = BLOCKS ? ss.nblk : ss.nact;
+  __device__ Walk(const StreamParams& p, int which, const Shared& shared)
+      : pr(p.p[which]), ss(shared), blk0(shared.blk0[which]) {
+    per = ss.nblk[which];
     units = per * pr.row_tiles * pr.kblocks;
-    workers = min(most, units);  // no range is empty
+    grain = pr.kblocks <= kWholeBlocks ? pr.kblocks : 1;
+    workers = max(1, min(p.workers, units / (grain > 1 ? grain : kMinBlocks)));  // no range is empty
     v = static_cast<int>(blockIdx.x) - static_cast<int>(gridDim.x);
     u = u1 = 0;
   }
   __device__ int begin_of(int worker) const {
-    return static_cast<int>(static_cast<long long>(units) * worker / workers);
+    return static_cast<int>(static_cast<long long>(units / grain) * worker / workers) * grain;
   }
   // The range that holds K block `unit`.
   __device__ int worker_of(int unit) const {
-    return static_cast<int>((static_cast<long long>(unit + 1) * workers - 1) / units);
-  }
-  __device__ void locate(int item, Segment& s) const {
-    s.item = item;
-    s.rt = item / per;
-    const int r = item - s.rt * per;
-    if (BLOCKS) {
-      int lo = 0, hi = ss.nact - 1;   // last entry with blk0 <= r
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (ss.blk0[mid] <= r)
-          lo = mid;
-        else
-          hi = mid - 1;
-      }
-      s.a = lo;
-      s.nb = r - ss.blk0[lo];
-    } else {
-      s.a = r;
-      s.nb = 0;
-    }
+    return static_cast<int>((static_cast<long long>(unit / grain + 1) * workers - 1) / (units / grain));
   }
   __device__ bool next(Segment& s) {
     if (u >= u1) {
@@ -356,10 +353,21 @@ struct Walk {
       u = begin_of(v);
       u1 = begin_of(v + 1);
     }
-    const int item = u / pr.kblocks;
-    locate(item, s);
+    s.item = u / pr.kblocks;
+    s.rt = s.item / per;
+    const int r = s.item - s.rt * per;
+    int lo = 0, hi = ss.nact - 1;   // last entry with blk0 <= r
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (blk0[mid] <= r)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    s.a = lo;
+    s.nb = r - blk0[lo];
     s.worker = v;
-    s.kb0 = u - item * pr.kblocks;
+    s.kb0 = u - s.item * pr.kblocks;
     s.kb1 = min(pr.kblocks, s.kb0 + (u1 - u));
     u += s.kb1 - s.kb0;
     return true;
@@ -398,25 +406,25 @@ struct Drain {
   }
 };
 
-// Columns of a tile: all tokens (first product, linear form), or the parts of
-// its rows of h, each rounded up to 16.
-template <bool H>
+// What the columns of a product are.
+//   kRowsOfX   the T rows of x (linear form)
+//   kGathered  the rows of x of an expert's tokens (hidden values)
+//   kRowsOfH   an expert's rows of h, all parts (output rows)
+enum Kind { kRowsOfX, kGathered, kRowsOfH };
+
+// Columns of a tile, each part's rounded up to 16.
+template <Kind KIND>
 struct Columns {
   int m;       // real ones: rows of the expert in this tile
-  int r0;      // its first row in h and o
+  int r0;      // its first row in h and o (linear form: in x)
   int n16;     // 16-row boxes of one part
   int n;       // columns of the tensor instruction
-  __device__ Columns(const StreamParams& p, const Shared& ss, const Segment& s) {
-    if (H) {
-      m = min(p.h_block, ss.m[s.a] - s.nb * p.h_block);
-      n16 = (m + 15) / 16;
-      n = 16 * n16 * p.parts;
-    } else {
-      m = ss.m[s.a];
-      n16 = p.tcols / 16;
-      n = p.tcols;
-    }
-    r0 = ss.row0[s.a] + s.nb * p.h_block;
+  __device__ Columns(const StreamParams& p, int which, const Shared& ss, const Segment& s) {
+    const int block = p.p[which].block;
+    m = min(block, ss.m[s.a] - s.nb * block);
+    r0 = ss.row0[s.a] + s.nb * block;
+    n16 = (m + 15) / 16;
+    n = 16 * n16 * (KIND == kRowsOfH ? p.parts : 1);
   }
 };
 
@@ -430,18 +438,16 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(kFull, ok);
 }
 
-// Everything below is written for one product: `which` picks its tensor maps,
-// H says that its columns are rows of h.
 // --------------------------------------------------------------- producers
-template <int G, bool H>
+template <int G, Kind KIND>
 __device__ bool produce_weights(const StreamParams& p, int which, Shared& ss, uint8_t* ring, Ring& rg, Drain& dr,
                                 volatile int* abort) {
   using Ge = Geo<G>;
   const Product& pr = p.p[which];
-  Walk<H> walk(pr, ss, p.workers);
+  Walk walk(p, which, ss);
   Segment s;
-  if (H) {
-    Walk<H> ahead(pr, ss, p.workers);
+  if (KIND == kRowsOfH) {
+    Walk ahead(p, which, ss);
     for (int n = -p.stages; n < kPrefetchBlocks && ahead.next(s);) {
       const int row = ss.e[s.a] * pr.rows + s.rt * pr.row_step;
       for (int kb = s.kb0; kb < s.kb1 && n < kPrefetchBlocks; ++kb, ++n)
@@ -481,34 +487,44 @@ __device__ bool produce_weights(const StreamParams& p, int which, Shared& ss, ui
 }
 
 // Activation rows: 64 columns at a time, the parts of h below one another.
-template <int G, bool H>
+// What a box or a gather leaves of the 16 rows keeps old values; they are
+// columns that nobody reads.
+template <int G, Kind KIND>
 __device__ bool produce_columns(const StreamParams& p, int which, Shared& ss, uint8_t* ring, Ring& rg, Drain& dr,
                                 volatile int* abort) {
   using Ge = Geo<G>;
   const Product& pr = p.p[which];
   const int Rs = p.T * (p.k + p.S);
-  Walk<H> walk(pr, ss, p.workers);
+  Walk walk(p, which, ss);
   Segment s;
   while (walk.next(s)) {
-    const Columns<H> c(p, ss, s);
+    const Columns<KIND> c(p, which, ss, s);
+    const int gathers = (c.m + 3) / 4;
+    const uint32_t bytes = Ge::ATOMS * (KIND == kGathered ? gathers * 512 : c.n * 128);
     for (int kb = s.kb0; kb < s.kb1; ++kb) {
       if (!warp_wait(&ss.empty[rg.stage], rg.phase ^ 1, abort, p.err, (0x22 << 24) | which)) return false;
       uint8_t* st = ring + static_cast<size_t>(rg.stage) * p.stage_bytes + Ge::WEIGHT_BYTES;
       uint64_t* bar = &ss.full_x[rg.stage];
       dr.note(rg.stage, rg.phase);
       if (elect_one()) {
-        mbar_arrive_expect_tx(bar, Ge::ATOMS * c.n * 128);
+        mbar_arrive_expect_tx(bar, bytes);
+        if (KIND == kGathered) {
+          for (int i = 0; i < gathers; ++i) {
+            int t[4];
 #pragma unroll
-        for (int at = 0; at < Ge::ATOMS; ++at) {
-          uint8_t* dst = st + at * c.n * 128;
-          const int col = (kb * Ge::ATOMS + at) * 64;
-          if (!H) {
-            tma_load_2d(dst, &pr.cols, bar, col, 0);
-          } else {
-            for (int q = 0; q < p.parts; ++q)
-              for (int i = 0; i < c.n16; ++i)
-                tma_load_2d(dst + (q * c.n16 + i) * 2048, &pr.cols, bar, col, q * Rs + c.r0 + i * 16);
+            for (int j = 0; j < 4; ++j) t[j] = ss.row_token[c.r0 + min(i * 4 + j, c.m - 1)];
+#pragma unroll
+            for (int at = 0; at < Ge::ATOMS; ++at)
+              tma_gather4(st + at * c.n * 128 + i * 512, &pr.cols, bar, (kb * Ge::ATOMS + at) * 64, t[0], t[1], t[2], t[3]);
           }
+        } else {
+          const int parts = KIND == kRowsOfH ? p.parts : 1;
+          for (int q = 0; q < parts; ++q)
+            for (int i = 0; i < c.n16; ++i)
+#pragma unroll
+              for (int at = 0; at < Ge::ATOMS; ++at)
+                tma_load_2d(st + at * c.n * 128 + (q * c.n16 + i) * 2048, &pr.cols, bar, (kb * Ge::ATOMS + at) * 64,
+                            q * Rs + c.r0 + i * 16);
         }
       }
       __syncwarp();
@@ -532,17 +548,11 @@ struct Turn {
   }
 };
 
-// 4 bits: how the sums of a turn are taken.
-//   kOwn    up to 32 columns: by the set whose turn it was, while its next turn
-//           is multiplied into the other half of its accumulators
-//   kWhole  more columns that one set can hold (parts of h): before its next turn
-//   kSplit  more than 32 tokens: by both sets, half the columns each, while the
-//           next turn is multiplied
-enum class Sums { kOwn, kWhole, kSplit };
-template <bool H>
-__device__ __forceinline__ Sums sums_of(const Columns<H>& c) {
-  return c.n <= kSumCols / 2 ? Sums::kOwn : H ? Sums::kWhole : Sums::kSplit;
-}
+// 4 bits: how the sums of a turn are taken.  Up to 32 columns: while the set's
+// next turn is multiplied into the other half of its accumulators (kOwn).
+// More: before the next turn (kWhole).
+enum class Sums { kOwn, kWhole };
+__device__ __forceinline__ Sums sums_of(int columns) { return columns <= kSumCols / 2 ? Sums::kOwn : Sums::kWhole; }
 // A turn is as many groups of a stage as fit the operand buffer and the
 // accumulators.
 template <int G>
@@ -563,13 +573,13 @@ __device__ __forceinline__ uint32_t sums_at(uint32_t tmem, int box, const Turn& 
   return tmem + 4 * kOperandCols + (box * 2 + tn.buf) * kSumCols + (how == Sums::kOwn ? tn.phase * (kSumCols / 2) : 0);
 }
 
-template <bool H>
+template <Kind KIND>
 __device__ bool issue_bf16(const StreamParams& p, int which, Shared& ss, uint8_t* ring, Ring& rg, Turn& tn,
                            volatile int* abort) {
-  Walk<H> walk(p.p[which], ss, p.workers);
+  Walk walk(p, which, ss);
   Segment s;
   while (walk.next(s)) {
-    const Columns<H> c(p, ss, s);
+    const Columns<KIND> c(p, which, ss, s);
     const uint32_t idesc = idesc_bf16_f32(kTileRows, c.n, 0, 0);
     const uint32_t acc = ss.tmem + tn.buf * 2 * p.acc_cols;
     if (!warp_wait(&ss.acc_empty[tn.buf], tn.phase ^ 1, abort, p.err, (0x31 << 24) | which)) return false;
@@ -599,18 +609,18 @@ __device__ bool issue_bf16(const StreamParams& p, int which, Shared& ss, uint8_t
   return true;
 }
 
-template <int G, bool H>
+template <int G, Kind KIND>
 __device__ bool issue_q4(const StreamParams& p, int which, int box, Shared& ss, uint8_t* ring, Ring& rg, Turn& tn,
                          volatile int* abort) {
   using Ge = Geo<G>;
   const Product& pr = p.p[which];
-  Walk<H> walk(pr, ss, p.workers);
+  Walk walk(p, which, ss);
   Segment s;
   while (walk.next(s)) {
-    const Columns<H> c(p, ss, s);
+    const Columns<KIND> c(p, which, ss, s);
     const uint32_t idesc = idesc_bf16_f32(kTileRows, c.n, 0, 0);
     const int tg = turn_groups<G>(c.n);
-    const Sums how = sums_of(c);
+    const Sums how = sums_of(c.n);
     const uint32_t atom = c.n * 128;
     for (int kb = s.kb0; kb < s.kb1; ++kb) {
       const uint32_t x = smem_u32(ring) + static_cast<uint32_t>(rg.stage) * p.stage_bytes + Ge::WEIGHT_BYTES;
@@ -623,9 +633,6 @@ __device__ bool issue_q4(const StreamParams& p, int which, int box, Shared& ss, 
         // 64 unless it is 128 wide
         const uint32_t xg = x + (g0 * G / 64) * atom + (g0 * G % 64) * 2;
         const uint32_t xg2 = x + ((g0 + 1) * G / 64) * atom + ((g0 + 1) * G % 64) * 2;
-        if (how == Sums::kSplit &&
-            !warp_wait(&ss.d_empty[box][tn.buf], tn.phase ^ 1, abort, p.err, (0x37 << 24) | which))
-          return false;
         if (!warp_wait(&ss.a_ready[box][tn.buf], tn.phase, abort, p.err, (0x32 << 24) | which)) return false;
         tc_fence_after();
         if (elect_one()) {
@@ -671,9 +678,9 @@ __device__ __forceinline__ void store_hidden(const StreamParams& p, int r, int i
   }
 }
 
-template <bool LAYER>
+template <Kind KIND>
 __device__ __forceinline__ void store_out(const StreamParams& p, int r, int c, float v) {
-  if (LAYER) {
+  if (KIND == kRowsOfH) {
     if (c < p.d) p.o[static_cast<size_t>(r) * p.d + c] = v;
   } else if (c < p.n) {
     const size_t at = static_cast<size_t>(r) * p.n + c;
@@ -713,32 +720,32 @@ __device__ __forceinline__ void leave_part(const StreamParams& p, int which, con
 }
 
 // A tile's finished column i, this thread's row of either box.
-template <bool H, bool LAYER>
+template <Kind KIND>
 __device__ __forceinline__ void finish_column(const StreamParams& p, const Shared& ss, const Segment& s, int r0, int i,
                                               int row, float v0, float v1) {
   const int r = r0 + i;
-  if (LAYER && !H) {
+  if (KIND == kGathered) {
     const int at = s.rt * kTileRows + row;
     if (at < p.f) store_hidden(p, r, at, ss.row_w[r], v0, v1);
   } else {
-    store_out<LAYER>(p, r, s.rt * 2 * kTileRows + row, v0);
-    store_out<LAYER>(p, r, (s.rt * 2 + 1) * kTileRows + row, v1);
+    store_out<KIND>(p, r, s.rt * 2 * kTileRows + row, v0);
+    store_out<KIND>(p, r, (s.rt * 2 + 1) * kTileRows + row, v1);
   }
 }
 
 // After the segments of a product: the cut tiles of this CTA's ranges, this
 // range's share of their columns (column i belongs to the i-th part, modulo
 // the parts), dealt to the sets of row warps.
-template <bool H, bool LAYER>
+template <Kind KIND>
 __device__ bool join_parts(const StreamParams& p, int which, const Shared& ss, volatile int* abort) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int row = (warp & 3) * 32 + lane, set = warp >> 2;
-  Walk<H> walk(p.p[which], ss, p.workers);
+  Walk walk(p, which, ss);
   Segment s;
   while (walk.next(s)) {
     const Share sh(walk, s);
     if (sh.whole) continue;
-    const Columns<H> c(p, ss, s);
+    const Columns<KIND> c(p, which, ss, s);
     const int parts = sh.v1 - sh.v0 + 1, step = kSets * parts;
     const int first = s.worker - sh.v0 + set * parts;
     if (first >= c.m) continue;
@@ -770,7 +777,7 @@ __device__ bool join_parts(const StreamParams& p, int which, const Shared& ss, v
       }
 #pragma unroll
       for (int j = 0; j < C; ++j)
-        if (i0 + j * step < c.m) finish_column<H, LAYER>(p, ss, s, c.r0, i0 + j * step, row, v[j][0], v[j][1]);
+        if (i0 + j * step < c.m) finish_column<KIND>(p, ss, s, c.r0, i0 + j * step, row, v[j][0], v[j][1]);
     }
   }
   return true;
@@ -780,9 +787,9 @@ __device__ bool join_parts(const StreamParams& p, int which, const Shared& ss, v
 // a part.  Every set sees all sums of its rows and takes its share of the
 // columns, two at a time.  `read(box, at, u)` starts the loads of one column,
 // `value(u)` makes its sum of them.
-template <bool H, bool LAYER, int LOADS, typename Read, typename Value>
+template <Kind KIND, int LOADS, typename Read, typename Value>
 __device__ __forceinline__ void finish_segment(const StreamParams& p, const Shared& ss, const Segment& s, const Share& sh,
-                                               const Columns<H>& c, const Read& read, const Value& value) {
+                                               const Columns<KIND>& c, const Read& read, const Value& value) {
   const int warp = threadIdx.x >> 5, row = (warp & 3) * 32 + (threadIdx.x & 31), set = warp >> 2;
   constexpr int B = 2;
   for (int i0 = set * B; i0 < c.m; i0 += kSets * B) {
@@ -790,9 +797,8 @@ __device__ __forceinline__ void finish_segment(const StreamParams& p, const Shar
 #pragma unroll
     for (int j = 0; j < B; ++j) {
       const int i = min(i0 + j, c.m - 1);  // past the end: the last column again
-      const int at = H ? i : LAYER ? ss.row_token[c.r0 + i] : i;
 #pragma unroll
-      for (int box = 0; box < 2; ++box) read(box, at, u[j][box]);
+      for (int box = 0; box < 2; ++box) read(box, i, u[j][box]);
     }
     tmem_ld_wait();
 #pragma unroll
@@ -801,7 +807,7 @@ __device__ __forceinline__ void finish_segment(const StreamParams& p, const Shar
       if (i >= c.m) break;
       const float v0 = value(u[j][0]), v1 = value(u[j][1]);
       if (sh.whole) {
-        finish_column<H, LAYER>(p, ss, s, c.r0, i, row, v0, v1);
+        finish_column<KIND>(p, ss, s, c.r0, i, row, v0, v1);
       } else {
         __stcg(part_of(p, s.worker, s.kb0 == 0, 0, row) + i * kTileRows, v0);
         __stcg(part_of(p, s.worker, s.kb0 == 0, 1, row) + i * kTileRows, v1);
@@ -811,29 +817,31 @@ __device__ __forceinline__ void finish_segment(const StreamParams& p, const Shar
 }
 
 // bf16 weights: the accumulators hold a segment's sums.
-template <bool H, bool LAYER>
+template <Kind KIND>
 __device__ bool rows_bf16(const StreamParams& p, int which, Shared& ss, Turn& tn, volatile int* abort) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  Walk<H> walk(p.p[which], ss, p.workers);
+  Walk walk(p, which, ss);
   Segment s;
   while (walk.next(s)) {
-    const Columns<H> c(p, ss, s);
+    const Columns<KIND> c(p, which, ss, s);
     const Share sh(walk, s);
     if (!warp_wait(&ss.acc_full[tn.buf], tn.phase, abort, p.err, (0x33 << 24) | which)) return false;
     tc_fence_after();
     const uint32_t acc = ss.tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + tn.buf * 2 * p.acc_cols;
-    finish_segment<H, LAYER, H ? 3 : 1>(
+    finish_segment<KIND, KIND == kRowsOfH ? 3 : 1>(
         p, ss, s, sh, c,
         [&](int box, int at, uint32_t* u) {
 #pragma unroll
-          for (int q = 0; q < (H ? 3 : 1); ++q) {
+          for (int q = 0; q < (KIND == kRowsOfH ? 3 : 1); ++q) {
             u[q] = 0;
             if (q < 2 || p.parts == 3) u[q] = tmem_ld1(acc + box * p.acc_cols + q * 16 * c.n16 + at);
           }
         },
         [&](const uint32_t* u) {
-          if (!H) return __uint_as_float(u[0]);
-          return fmaf(__uint_as_float(u[H ? 1 : 0]) + __uint_as_float(u[H ? 2 : 0]), 1.f / kLowScale, __uint_as_float(u[0]));
+          if constexpr (KIND == kRowsOfH)
+            return fmaf(__uint_as_float(u[1]) + __uint_as_float(u[2]), 1.f / kLowScale, __uint_as_float(u[0]));
+          else
+            return __uint_as_float(u[0]);
         });
     tc_fence_before();
     __syncwarp();
@@ -841,7 +849,7 @@ __device__ bool rows_bf16(const StreamParams& p, int which, Shared& ss, Turn& tn
     tn.step(p.acc_bufs);
     if (!sh.whole) leave_part(p, which, sh);
   }
-  return join_parts<H, LAYER>(p, which, ss, abort);
+  return join_parts<KIND>(p, which, ss, abort);
 }
 
 // 4-bit weights: set 2 box + t owns a box on every other turn, a thread one
@@ -853,19 +861,18 @@ __device__ bool rows_bf16(const StreamParams& p, int which, Shared& ss, Turn& tn
 // turn are complete, and so is the half of the accumulators that this turn
 // fills (kOwn: read before the previous turn's codes were handed over; kWhole:
 // before this turn's).
-template <int G, int NC, bool H, bool LAYER>
+template <int G, int NC, Kind KIND>
 struct RowsQ4 {
   using Ge = Geo<G>;
-  // The parts of 16 rows of h lie n16 steps of 16 columns apart; first: first
-  // step of this thread's columns.
-  static __device__ __forceinline__ void add_group(const StreamParams& p, uint32_t acc, int first, int n16, float scale,
+  // The parts of 16 rows of h lie n16 steps of 16 columns apart.
+  static __device__ __forceinline__ void add_group(const StreamParams& p, uint32_t acc, int n16, float scale,
                                                    float (&sum)[NC]) {
 #pragma unroll
     for (int b = 0; b < NC / 16; ++b) {
-      if (first + b >= n16) break;
+      if (b >= n16) break;
       uint32_t u[16];
-      tmem_ld16(acc + (first + b) * 16, u);
-      if constexpr (H) {
+      tmem_ld16(acc + b * 16, u);
+      if constexpr (KIND == kRowsOfH) {
         uint32_t lo[16];
         tmem_ld16(acc + (n16 + b) * 16, lo);
         tmem_ld_wait();
@@ -887,16 +894,15 @@ struct RowsQ4 {
     }
   }
 
-  static __device__ bool segment(const StreamParams& p, int which, Shared& ss, uint8_t* ring, const Walk<H>& walk,
+  static __device__ bool segment(const StreamParams& p, int which, Shared& ss, uint8_t* ring, const Walk& walk,
                                  const Segment& s, Ring& rg, Turn& tn, uint32_t& swap, volatile int* abort) {
     const Product& pr = p.p[which];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int quad = warp & 3, box = warp >> 3, turn = (warp >> 2) & 1, row = quad * 32 + lane;
     const uint32_t lanes = ss.tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    const Columns<H> c(p, ss, s);
+    const Columns<KIND> c(p, which, ss, s);
     const Share sh(walk, s);
-    const Sums how = sums_of(c);
-    const bool split = how == Sums::kSplit;
+    const Sums how = sums_of(c.n);
     const int tg = turn_groups<G>(c.n);
     float sum[NC];
 #pragma unroll
@@ -913,12 +919,8 @@ struct RowsQ4 {
       const uint32_t acc = sums_at(lanes, box, before, how);
 #pragma unroll
       for (int j = 0; j < kMaxTurnGroups<G>; ++j)
-        if (j < n_before) add_group(p, acc + j * c.n, split ? turn * 2 : 0, c.n16, scale_before[j], sum);
+        if (j < n_before) add_group(p, acc + j * c.n, c.n16, scale_before[j], sum);
       tc_fence_before();
-      if (split) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ss.d_empty[box][before.buf]);
-      }
     };
     for (int kb = s.kb0; kb < s.kb1; ++kb) {
       if (!warp_wait(&ss.full_w[rg.stage], rg.phase, abort, p.err, (0x23 << 24) | which)) return false;
@@ -927,42 +929,34 @@ struct RowsQ4 {
       const uint32_t scales = st + 2 * kBoxBytes + box * Ge::SCALE_BYTES + row * 2;
       const int groups = stage_groups<G>(pr.K, kb);
       for (int g0 = 0; g0 < groups; g0 += tg) {
-        const bool mine = tn.buf == turn;
-        if (mine || split) {
-          if (!split && n_before) {
+        if (tn.buf == turn) {
+          if (n_before) {
             if (!complete()) return false;
             if (how == Sums::kWhole) add();
           }
           const int n = min(tg, groups - g0);
-          float scale[kMaxTurnGroups<G>];
+          const uint32_t a = operand_at(lanes, box, turn);
+          for (int j = 0; j < n; ++j)
 #pragma unroll
-          for (int j = 0; j < kMaxTurnGroups<G>; ++j) scale[j] = j < n ? lds_bf16(scales + (g0 + j) * (kTileRows * 2)) : 0.f;
-          if (mine) {
-            const uint32_t a = operand_at(lanes, box, turn);
-            for (int j = 0; j < n; ++j)
+            for (int i = 0; i < G / 32; ++i) {
+              uint32_t w[4], v[16];
+              lds128(codes + ((((g0 + j) * (G / 32) + i) ^ (row & 7)) << 4), w);
 #pragma unroll
-              for (int i = 0; i < G / 32; ++i) {
-                uint32_t w[4], v[16];
-                lds128(codes + ((((g0 + j) * (G / 32) + i) ^ (row & 7)) << 4), w);
+              for (int t = 0; t < 4; ++t)
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
-#pragma unroll
-                  for (int q = 0; q < 4; ++q) v[t * 4 + q] = q4_pair(w[t], q);
-                tmem_st16(a + j * (G / 2) + i * 16, v);
-              }
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ss.a_ready[box][turn]);
-          }
-          if (n_before) {
-            if (split && !complete()) return false;
-            if (how != Sums::kWhole) add();
-          }
+                for (int q = 0; q < 4; ++q) v[t * 4 + q] = q4_pair(w[t], q);
+              tmem_st16(a + j * (G / 2) + i * 16, v);
+            }
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ss.a_ready[box][turn]);
+          if (n_before && how == Sums::kOwn) add();
           before = tn;
           n_before = n;
 #pragma unroll
-          for (int j = 0; j < kMaxTurnGroups<G>; ++j) scale_before[j] = scale[j];
+          for (int j = 0; j < kMaxTurnGroups<G>; ++j)
+            scale_before[j] = j < n ? lds_bf16(scales + (g0 + j) * (kTileRows * 2)) : 0.f;
         }
         tn.step(2);
       }
@@ -976,8 +970,8 @@ struct RowsQ4 {
     }
 
     // All sums of the tile meet in tensor memory, in the sets' operand
-    // buffers: both boxes' and both turns' (or column halves').  No set goes
-    // on before all have read their share.
+    // buffers: both boxes' and both turns'.  No set goes on before all have
+    // read their share.
 #pragma unroll
     for (int b = 0; b < NC / 16; ++b) {
       uint32_t u[16];
@@ -991,12 +985,11 @@ struct RowsQ4 {
     if (lane == 0) mbar_arrive(&ss.swap_ready);
     if (!warp_wait(&ss.swap_ready, swap, abort, p.err, (0x35 << 24) | which)) return false;
     tc_fence_after();
-    finish_segment<H, LAYER, 2>(
+    finish_segment<KIND, 2>(
         p, ss, s, sh, c,
         [&](int bx, int at, uint32_t* u) {
-          u[0] = tmem_ld1(operand_at(lanes, bx, split ? at >> 5 : 0) + (split ? at & 31 : at));
-          u[1] = 0;
-          if (!split) u[1] = tmem_ld1(operand_at(lanes, bx, 1) + at);
+          u[0] = tmem_ld1(operand_at(lanes, bx, 0) + at);
+          u[1] = tmem_ld1(operand_at(lanes, bx, 1) + at);
         },
         [&](const uint32_t* u) { return __uint_as_float(u[0]) + __uint_as_float(u[1]); });
     tc_fence_before();
@@ -1010,19 +1003,20 @@ struct RowsQ4 {
   }
 };
 
-template <int G, bool H, bool LAYER>
+template <int G, Kind KIND>
 __device__ bool rows_q4(const StreamParams& p, int which, Shared& ss, uint8_t* ring, Ring& rg, Turn& tn, uint32_t& swap,
                         volatile int* abort) {
-  Walk<H> walk(p.p[which], ss, p.workers);
+  Walk walk(p, which, ss);
   Segment s;
   bool ok = true;
   while (ok && walk.next(s)) {
-    if (Columns<H>(p, ss, s).n16 == 1)
-      ok = RowsQ4<G, 16, H, LAYER>::segment(p, which, ss, ring, walk, s, rg, tn, swap, abort);
+    // rows of h come at most 16 at a time
+    if (KIND == kRowsOfH || Columns<KIND>(p, which, ss, s).n16 == 1)
+      ok = RowsQ4<G, 16, KIND>::segment(p, which, ss, ring, walk, s, rg, tn, swap, abort);
     else
-      ok = RowsQ4<G, 32, H, LAYER>::segment(p, which, ss, ring, walk, s, rg, tn, swap, abort);
+      ok = RowsQ4<G, KIND == kRowsOfH ? 16 : 32, KIND>::segment(p, which, ss, ring, walk, s, rg, tn, swap, abort);
   }
-  return ok && join_parts<H, LAYER>(p, which, ss, abort);
+  return ok && join_parts<KIND>(p, which, ss, abort);
 }
 
 // y[t] = its slots' rows in slot order, then the shared experts', in fp32.
@@ -1057,6 +1051,7 @@ __device__ void sum_rows(const StreamParams& p, const Shared& ss) {
 template <int G, bool LAYER>
 __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_constant__ StreamParams p) {
   using Ge = Geo<G>;
+  constexpr Kind FIRST = kGathered, SECOND = LAYER ? kRowsOfH : kRowsOfX;
   extern __shared__ uint8_t dyn[];
   Shared& ss = *reinterpret_cast<Shared*>(dyn);
   // stages on 1024-byte boundaries of shared memory (the swizzle's period)
@@ -1076,7 +1071,6 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
       for (int j = 0; j < 2; ++j) {
         mbar_init(&ss.a_ready[i][j], 4);
         mbar_init(&ss.d_full[i][j], 1);
-        mbar_init(&ss.d_empty[i][j], 8);
       }
     }
     mbar_init(&ss.swap_ready, kRowWarps);
@@ -1093,10 +1087,10 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
   if (LAYER) {
     build_work_list(p, ss);
   } else if (tid == 0) {
-    ss.nact = ss.nblk = 1;
-    ss.e[0] = ss.row0[0] = ss.blk0[0] = 0;
+    ss.nact = 1;
+    ss.e[0] = ss.row0[0] = ss.blk0[1][0] = 0;
     ss.m[0] = p.T;
-    ss.blk0[1] = 1;
+    ss.blk0[1][1] = ss.nblk[1] = (p.T + p.p[1].block - 1) / p.p[1].block;
   }
   tc_fence_before();
   __syncthreads();
@@ -1107,8 +1101,8 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
     Ring rg;
     Drain dr;
     bool ok = true;
-    if (LAYER) ok = produce_weights<G, false>(p, 0, ss, ring, rg, dr, abort);
-    if (ok) produce_weights<G, LAYER>(p, 1, ss, ring, rg, dr, abort);
+    if (LAYER) ok = produce_weights<G, FIRST>(p, 0, ss, ring, rg, dr, abort);
+    if (ok) produce_weights<G, SECOND>(p, 1, ss, ring, rg, dr, abort);
     dr.wait(ss.full_w);
   } else if (warp == kColumnWarp) {
     Ring rg;
@@ -1122,11 +1116,11 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
     };
     bool ok = true;
     if (LAYER) {
-      ok = produce_columns<G, false>(p, 0, ss, ring, rg, dr, abort);
+      ok = produce_columns<G, FIRST>(p, 0, ss, ring, rg, dr, abort);
       ok = ok && wait_all(kCtrHidden, 0x25);  // every hidden value of every CTA,
       fence_proxy_async_global();             // for the bulk copies of this one
     }
-    if (ok) ok = produce_columns<G, LAYER>(p, 1, ss, ring, rg, dr, abort);
+    if (ok) ok = produce_columns<G, SECOND>(p, 1, ss, ring, rg, dr, abort);
     if (LAYER && ok && wait_all(kCtrOut, 0x26) && lane == 0) mbar_arrive(&ss.out_done);
     dr.wait(ss.full_x);
   } else if (warp >= kMmaWarp) {
@@ -1135,11 +1129,11 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
     bool ok = true;
     if constexpr (Ge::Q4) {
       const int box = warp - kMmaWarp;
-      if (LAYER) ok = issue_q4<G, false>(p, 0, box, ss, ring, rg, tn, abort);
-      if (ok) issue_q4<G, LAYER>(p, 1, box, ss, ring, rg, tn, abort);
+      if (LAYER) ok = issue_q4<G, FIRST>(p, 0, box, ss, ring, rg, tn, abort);
+      if (ok) issue_q4<G, SECOND>(p, 1, box, ss, ring, rg, tn, abort);
     } else if (warp == kMmaWarp) {
-      if (LAYER) ok = issue_bf16<false>(p, 0, ss, ring, rg, tn, abort);
-      if (ok) issue_bf16<LAYER>(p, 1, ss, ring, rg, tn, abort);
+      if (LAYER) ok = issue_bf16<FIRST>(p, 0, ss, ring, rg, tn, abort);
+      if (ok) issue_bf16<SECOND>(p, 1, ss, ring, rg, tn, abort);
     }
     __syncwarp();
     if (elect_one()) umma_commit(&ss.drained);
@@ -1158,25 +1152,25 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
         if (lane == 0) red_release_gpu_add(p.err + counter, 1);
       };
       if constexpr (Ge::Q4)
-        ok = rows_q4<G, false, LAYER>(p, 0, ss, ring, rg, tn, swap, abort);
+        ok = rows_q4<G, FIRST>(p, 0, ss, ring, rg, tn, swap, abort);
       else
-        ok = rows_bf16<false, LAYER>(p, 0, ss, tn, abort);
+        ok = rows_bf16<FIRST>(p, 0, ss, tn, abort);
       fence_proxy_async_global();  // hidden values, to other CTAs' bulk copies
       publish(kCtrHidden);
       if (ok) {
         if constexpr (Ge::Q4)
-          ok = rows_q4<G, true, LAYER>(p, 1, ss, ring, rg, tn, swap, abort);
+          ok = rows_q4<G, SECOND>(p, 1, ss, ring, rg, tn, swap, abort);
         else
-          ok = rows_bf16<true, LAYER>(p, 1, ss, tn, abort);
+          ok = rows_bf16<SECOND>(p, 1, ss, tn, abort);
       }
       publish(kCtrOut);
       ok = ok && mbar_wait(&ss.out_done, 0, abort, p.err, 0x2A << 24);
       if (__all_sync(kFull, ok)) sum_rows(p, ss);
     } else {
       if constexpr (Ge::Q4)
-        rows_q4<G, false, LAYER>(p, 1, ss, ring, rg, tn, swap, abort);
+        rows_q4<G, SECOND>(p, 1, ss, ring, rg, tn, swap, abort);
       else
-        rows_bf16<false, LAYER>(p, 1, ss, tn, abort);
+        rows_bf16<SECOND>(p, 1, ss, tn, abort);
     }
   }
   tc_fence_before();
@@ -1263,6 +1257,11 @@ size_t ring_shape(StreamParams& p, int cols) {
   return fixed + static_cast<size_t>(p.stages) * p.stage_bytes;
 }
 
+// Columns of a product's widest tile.
+int columns_of(const StreamParams& p, int which, int parts) {
+  return ceil_div(std::min(p.T, p.p[which].block), 16) * 16 * parts;
+}
+
 template <int G, bool LAYER>
 int launch_stream(StreamParams& p, size_t smem, int grid_limit, cudaStream_t s) {
   static bool sized = false;  // the attribute outlives the call; setting it twice is harmless
@@ -1288,7 +1287,6 @@ int launch_stream(StreamParams& p, size_t smem, int grid_limit, cudaStream_t s) 
 void common_params(StreamParams& p, void* ws, const Layout& L, int T, void* y, int y_type) {
   uint8_t* at = static_cast<uint8_t*>(ws);
   p.T = T;
-  p.tcols = ceil_div(T, 16) * 16;
   p.part = reinterpret_cast<float*>(at + L.part);
   p.arrive = reinterpret_cast<int*>(at + L.arrive);
   p.y = y;
@@ -1312,12 +1310,13 @@ int decode_g(const DecodeArgs& a, cudaStream_t s) {
   p.h = reinterpret_cast<uint16_t*>(ws + L.h);
   p.o = reinterpret_cast<float*>(ws + L.o);
   p.parts = a.y_type == MOE_Y_F32 ? 3 : 2;
-  p.h_block = Geo<G>::h_rows(p.parts);
+  p.p[0].block = Geo<G>::block_rows(1);
+  p.p[1].block = Geo<G>::block_rows(p.parts);
   if (!fill_product<G>(p.p[0], 0, a.W1, a.W3, mats, c.d_ff, c.d_model) ||
       !fill_product<G>(p.p[1], 1, a.W2, a.W2, mats, c.d_model, c.d_ff) ||
-      !map2d(&p.p[0].cols, a.x, c.d_model, c.T, 64, p.tcols) || !map2d(&p.p[1].cols, p.h, c.d_ff, p.parts * Rs, 64, 16))
+      !map2d(&p.p[0].cols, a.x, c.d_model, c.T, 64, 1) || !map2d(&p.p[1].cols, p.h, c.d_ff, p.parts * Rs, 64, 16))
     return MOE_ERR_CUDA;
-  const size_t smem = ring_shape<G>(p, std::max(p.tcols, p.parts * std::min(p.tcols, p.h_block)));
+  const size_t smem = ring_shape<G>(p, std::max(columns_of(p, 0, 1), columns_of(p, 1, p.parts)));
   TraceScope trace_scope(MOE_K_DECODE, s);
   return launch_stream<G, true>(p, smem, a.grid_limit, s);
 }
@@ -1328,10 +1327,10 @@ int linear_g(const LinearArgs& a, cudaStream_t s) {
   std::memset(&p, 0, sizeof(p));
   common_params(p, a.ws, layout(0, 0, 0), a.T, a.y, a.y_type);
   p.n = a.n;
-  p.h_block = kMaxTokens;
-  if (!fill_product<G>(p.p[1], 1, a.W, a.W, 1, a.n, a.K) || !map2d(&p.p[1].cols, a.x, a.K, a.T, 64, p.tcols))
+  p.p[1].block = Geo<G>::block_rows(1);
+  if (!fill_product<G>(p.p[1], 1, a.W, a.W, 1, a.n, a.K) || !map2d(&p.p[1].cols, a.x, a.K, a.T, 64, 16))
     return MOE_ERR_CUDA;
-  const size_t smem = ring_shape<G>(p, p.tcols);
+  const size_t smem = ring_shape<G>(p, columns_of(p, 1, 1));
   TraceScope trace_scope(MOE_K_LINEAR, s);
   return launch_stream<G, false>(p, smem, a.grid_limit, s);
 }

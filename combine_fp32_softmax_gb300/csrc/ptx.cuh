@@ -182,6 +182,16 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const void* map, uint64_t
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
       : "memory");
 }
+// Four rows of a 2D tensor, one box row of the map (whose box is one row high)
+// each, into consecutive rows of shared memory.
+__device__ __forceinline__ void tma_gather4(void* dst, const void* map, uint64_t* bar, int c0, int r0, int r1, int r2,
+                                            int r3) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
+      : "memory");
+}
 // CTA pair (tcgen05 CTA group of two): 2D tiled load into this CTA's shared
 // memory whose completion is counted on the barrier at `bar`'s offset in
 // the pair's even CTA, where the MMAs that read both CTAs' tiles are issued.
