@@ -96,7 +96,7 @@ struct Geo {
   // Activation rows of a tile, in `parts` parts.  bf16 weights: all of an
   // expert's.  4 bits: what the accumulators hold twice (kOwn, below); an
   // expert with more rows has its weight tiles visited again, from L2.
-  __host__ __device__ static constexpr int block_rows(int parts) { return !Q4 ? 64 : parts == 1 ? 32 : 16; }
+  static constexpr int block_log2(int parts) { return !Q4 ? 6 : parts == 1 ? 5 : 4; }
 };
 
 // One product of the launch: weight tiles of `row_step` output rows.
@@ -105,7 +105,7 @@ struct Product {
   CUtensorMap s0, s1;   // their scales (4 bits)
   CUtensorMap cols;     // activation rows
   int K, kblocks, rows, row_step, row_tiles;
-  int block;            // most activation rows of a tile
+  int block_log2;       // log2 of the most activation rows of a tile
 };
 
 struct StreamParams {
@@ -125,6 +125,21 @@ struct StreamParams {
   int acc_cols, acc_bufs;  // bf16 weights: columns of an accumulator, accumulator pairs
 };
 
+// One product's K blocks and their ranges: range v takes q grains, one more if
+// v < extra.  The first range of this CTA begins at K block u of tile `item`,
+// which is tile r of row tile rt and belongs to work list entry a.
+struct Plan {
+  int units, workers, grain, q, extra;   // grain: K blocks that a range takes at least of a tile
+  int per;                               // tiles of a row tile
+  int u, item, rt, r, a;
+  __device__ int begin_of(int v) const { return (v * q + min(v, extra)) * grain; }
+  // The range that holds K block `unit`.
+  __device__ int worker_of(int unit) const {
+    const unsigned g = static_cast<unsigned>(unit) / static_cast<unsigned>(grain), wide = extra * (q + 1);
+    return g < wide ? g / static_cast<unsigned>(q + 1) : extra + (g - wide) / static_cast<unsigned>(q);
+  }
+};
+
 struct alignas(16) Shared {
   uint64_t full_w[kMaxStages], full_x[kMaxStages], empty[kMaxStages];
   uint64_t acc_full[2], acc_empty[2];   // bf16: accumulator pairs
@@ -139,6 +154,7 @@ struct alignas(16) Shared {
   int m[kMaxActive];               // its rows
   int row0[kMaxActive];            // its first row in h and o
   int blk0[2][kMaxActive + 1];     // blocks of rows before it, by product
+  Plan plan[2];                    // by product
   unsigned mask[256][2];           // tokens that picked expert e
   float row_w[kMaxRows];
   float pick_w[kMaxPicks];
@@ -168,6 +184,43 @@ __device__ bool wait_count(const int* c, int target, volatile int* abort, int* e
 }
 
 // ---------------------------------------------------------------- work list
+// The K blocks of a product, tile after tile, cut into contiguous ranges.
+// The tiles of one row tile of all experts follow each other, so the shared
+// experts, which have the most rows to finish, are spread over the ranges.
+//
+// Putting a cut tile together again costs a few microseconds of latency
+// (parts, count, wait, parts back), the streaming time of some 10 K blocks of
+// an SM that has its share of the memory: tiles of at most kWholeBlocks are
+// not cut, and longer ones not into ranges of fewer than kMinBlocks.
+constexpr int kWholeBlocks = 8, kMinBlocks = 4;
+
+__device__ void make_plan(const StreamParams& p, int which, Shared& ss) {
+  const Product& pr = p.p[which];
+  Plan& pl = ss.plan[which];
+  pl.per = ss.nblk[which];
+  pl.units = pl.per * pr.row_tiles * pr.kblocks;
+  const bool whole = pr.kblocks <= kWholeBlocks;
+  pl.grain = whole ? pr.kblocks : 1;
+  const int grains = whole ? pl.per * pr.row_tiles : pl.units;
+  pl.workers = max(1, min(p.workers, whole ? grains : grains / kMinBlocks));  // no range is empty
+  pl.q = grains / pl.workers;
+  pl.extra = grains - pl.q * pl.workers;
+  const int v = min(static_cast<int>(blockIdx.x), pl.workers - 1);
+  pl.u = pl.begin_of(v);
+  pl.item = pl.u / pr.kblocks;
+  pl.rt = pl.item / pl.per;
+  pl.r = pl.item - pl.rt * pl.per;
+  int lo = 0, hi = ss.nact - 1;   // last entry with blk0 <= r
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (ss.blk0[which][mid] <= pl.r)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  pl.a = lo;
+}
+
 // Routes the tokens.  Up to kWarps tokens: every CTA all of them, one warp a
 // token.  More: token t is CTA t % gridDim.x's, and every CTA reads the picks
 // of the others from the outputs once all are counted; 64 tokens routed by
@@ -227,8 +280,9 @@ __device__ void build_work_list(const StreamParams& p, Shared& ss) {
     if (tid == 0) wait_count(p.err + kCtrRouted, p.T, &ss.abort, p.err, 0x20 << 24);
     __syncthreads();
     // After a wait that gave up (abort is set) the picks may be anything: clamped, they stay in bounds.
-    for (int i = tid; i < R; i += kThreads)
-      note_pick(ss, i, i / p.k, min(max(__ldcg(p.topk_idx + i), 0), p.E - 1), __ldcg(p.topk_w + i));
+    for (int t = tid >> 3; t < p.T; t += kThreads / 8)
+      if (const int i = t * p.k + (tid & 7); (tid & 7) < p.k)
+        note_pick(ss, i, t, min(max(__ldcg(p.topk_idx + i), 0), p.E - 1), __ldcg(p.topk_w + i));
   }
   __syncthreads();
   // Thread e: expert e.  Exclusive sums over the experts of rows and entries
@@ -236,7 +290,7 @@ __device__ void build_work_list(const StreamParams& p, Shared& ss) {
   // 288), packed in pairs.
   unsigned mine[2] = {}, incl[2] = {};
   int n = 0;
-  auto blocks = [&](int which, int rows) { return (rows + p.p[which].block - 1) / p.p[which].block; };
+  auto blocks = [&](int which, int rows) { return (rows + (1 << p.p[which].block_log2) - 1) >> p.p[which].block_log2; };
   if (tid < 256) {
     n = tid < p.E ? __popc(ss.mask[tid][0]) + __popc(ss.mask[tid][1]) : 0;
     mine[0] = n ? n | 1 << 16 : 0;
@@ -287,35 +341,33 @@ __device__ void build_work_list(const StreamParams& p, Shared& ss) {
     }
     if (tid == p.S) ss.nact = all_a + p.S;
   }
-  for (int i = tid; i < p.S * p.T; i += kThreads) {
-    ss.row_token[R + i] = static_cast<unsigned char>(i % p.T);
-    ss.row_w[R + i] = 1.f;
-  }
   __syncthreads();
-  // rows: first row of the expert + earlier tokens of its mask
-  for (int i = tid; i < R; i += kThreads) {
-    const int e = ss.pick_e[i], t = i / p.k;
-    const unsigned m0 = ss.mask[e][0], m1 = ss.mask[e][1], below = (1u << (t & 31)) - 1u;
-    const int row = ss.row0[ss.entry[e]] + (t < 32 ? __popc(m0 & below) : __popc(m0) + __popc(m1 & below));
-    ss.pick_row[i] = static_cast<short>(row);
-    ss.row_token[row] = static_cast<unsigned char>(t);
-    ss.row_w[row] = ss.pick_w[i];
+  if (tid == kThreads - 32 || tid == kThreads - 64) {
+    make_plan(p, tid == kThreads - 64, ss);
+  } else {
+    // rows: first row of the expert + earlier tokens of its mask; eight lanes a token
+    const int j = tid & 7;
+    for (int t = tid >> 3; t < p.T; t += kThreads / 8) {
+      if (j < p.k) {
+        const int i = t * p.k + j, e = ss.pick_e[i];
+        const unsigned m0 = ss.mask[e][0], m1 = ss.mask[e][1], below = (1u << (t & 31)) - 1u;
+        const int row = ss.row0[ss.entry[e]] + (t < 32 ? __popc(m0 & below) : __popc(m0) + __popc(m1 & below));
+        ss.pick_row[i] = static_cast<short>(row);
+        ss.row_token[row] = static_cast<unsigned char>(t);
+        ss.row_w[row] = ss.pick_w[i];
+      }
+      if (j < p.S) {
+        ss.row_token[R + j * p.T + t] = static_cast<unsigned char>(t);
+        ss.row_w[R + j * p.T + t] = 1.f;
+      }
+    }
   }
 }
 
-// ------------------------------------------------------------------ ranges
-// The K blocks of a product, tile after tile, cut into contiguous ranges.
 // Every role of a CTA walks the same segments: the K blocks [kb0, kb1) of one
-// tile.  The tiles of one row tile of all experts follow each other, so the
-// shared experts, which have the most rows to finish, are spread over the
-// ranges.
-//
-// Putting a cut tile together again costs about 4 us of latency (parts,
-// count, wait, parts back), the streaming time of some 10 K blocks of an SM
-// that has its share of the memory: tiles of at most kWholeBlocks are not
-// cut, and longer ones not into ranges of fewer than kMinBlocks.
-constexpr int kWholeBlocks = 8, kMinBlocks = 4;
-
+// tile.  The ranges and the first position come from the plan: the few
+// divisions take a lone warp a microsecond and more, on every role's way to
+// its first copy.
 struct Segment {
   int worker, item, kb0, kb1;
   int a, rt, nb;   // work list entry, row tile, block of the expert's rows
@@ -323,53 +375,48 @@ struct Segment {
 
 struct Walk {
   const Product& pr;
-  const Shared& ss;
+  const Plan& pl;
   const int* blk0;
-  int workers, v;
-  int units, grain;  // K blocks, and how many a range takes at least of a tile
-  int per;           // tiles of a row tile
-  int u, u1;
+  int v, u, u1;
+  int item, rt, r, a, kb;
 
-  __device__ Walk(const StreamParams& p, int which, const Shared& shared)
-      : pr(p.p[which]), ss(shared), blk0(shared.blk0[which]) {
-    per = ss.nblk[which];
-    units = per * pr.row_tiles * pr.kblocks;
-    grain = pr.kblocks <= kWholeBlocks ? pr.kblocks : 1;
-    workers = max(1, min(p.workers, units / (grain > 1 ? grain : kMinBlocks)));  // no range is empty
-    v = static_cast<int>(blockIdx.x) - static_cast<int>(gridDim.x);
+  __device__ Walk(const StreamParams& p, int which, const Shared& ss)
+      : pr(p.p[which]), pl(ss.plan[which]), blk0(ss.blk0[which]) {
+    v = static_cast<int>(blockIdx.x);
     u = u1 = 0;
-  }
-  __device__ int begin_of(int worker) const {
-    return static_cast<int>(static_cast<long long>(units / grain) * worker / workers) * grain;
-  }
-  // The range that holds K block `unit`.
-  __device__ int worker_of(int unit) const {
-    return static_cast<int>((static_cast<long long>(unit / grain + 1) * workers - 1) / (units / grain));
+    if (v >= pl.workers) return;
+    u = pl.u;
+    u1 = pl.begin_of(v + 1);
+    item = pl.item, rt = pl.rt, r = pl.r, a = pl.a;
+    kb = u - item * pr.kblocks;
   }
   __device__ bool next(Segment& s) {
-    if (u >= u1) {
-      v += static_cast<int>(gridDim.x);
-      if (v >= workers) return false;
-      u = begin_of(v);
-      u1 = begin_of(v + 1);
+    if (u >= u1) {  // a capped grid: the CTA's next range
+      if (v >= pl.workers || (v += static_cast<int>(gridDim.x)) >= pl.workers) return false;
+      u = pl.begin_of(v);
+      u1 = pl.begin_of(v + 1);
+      item = u / pr.kblocks;
+      kb = u - item * pr.kblocks;
+      rt = item / pl.per;
+      r = item - rt * pl.per;
+      a = 0;
     }
-    s.item = u / pr.kblocks;
-    s.rt = s.item / per;
-    const int r = s.item - s.rt * per;
-    int lo = 0, hi = ss.nact - 1;   // last entry with blk0 <= r
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) / 2;
-      if (blk0[mid] <= r)
-        lo = mid;
-      else
-        hi = mid - 1;
-    }
-    s.a = lo;
-    s.nb = r - blk0[lo];
+    while (r >= blk0[a + 1]) ++a;
     s.worker = v;
-    s.kb0 = u - s.item * pr.kblocks;
-    s.kb1 = min(pr.kblocks, s.kb0 + (u1 - u));
+    s.item = item;
+    s.kb0 = kb;
+    s.kb1 = min(pr.kblocks, kb + (u1 - u));
+    s.a = a;
+    s.rt = rt;
+    s.nb = r - blk0[a];
     u += s.kb1 - s.kb0;
+    kb = 0;
+    ++item;
+    if (++r == pl.per) {
+      r = 0;
+      a = 0;
+      ++rt;
+    }
     return true;
   }
 };
@@ -420,9 +467,9 @@ struct Columns {
   int n16;     // 16-row boxes of one part
   int n;       // columns of the tensor instruction
   __device__ Columns(const StreamParams& p, int which, const Shared& ss, const Segment& s) {
-    const int block = p.p[which].block;
-    m = min(block, ss.m[s.a] - s.nb * block);
-    r0 = ss.row0[s.a] + s.nb * block;
+    const int log2 = p.p[which].block_log2, first = s.nb << log2;
+    m = min(1 << log2, ss.m[s.a] - first);
+    r0 = ss.row0[s.a] + first;
     n16 = (m + 15) / 16;
     n = 16 * n16 * (KIND == kRowsOfH ? p.parts : 1);
   }
@@ -698,12 +745,11 @@ __device__ __forceinline__ void store_out(const StreamParams& p, int r, int c, f
 struct Share {
   bool whole;
   int v0, v1;
-  template <typename W>
-  __device__ Share(const W& walk, const Segment& s) {
+  __device__ Share(const Walk& walk, const Segment& s) {
     const int kblocks = walk.pr.kblocks;
     whole = s.kb0 == 0 && s.kb1 == kblocks;
-    v0 = s.kb0 == 0 ? s.worker : walk.worker_of(s.item * kblocks);
-    v1 = s.kb1 == kblocks ? s.worker : walk.worker_of(s.item * kblocks + kblocks - 1);
+    v0 = s.kb0 == 0 ? s.worker : walk.pl.worker_of(s.item * kblocks);
+    v1 = s.kb1 == kblocks ? s.worker : walk.pl.worker_of(s.item * kblocks + kblocks - 1);
   }
 };
 // Column 0 of a part, this thread's row.  Range v has the tile in slot 1 only
@@ -1090,7 +1136,8 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
     ss.nact = 1;
     ss.e[0] = ss.row0[0] = ss.blk0[1][0] = 0;
     ss.m[0] = p.T;
-    ss.blk0[1][1] = ss.nblk[1] = (p.T + p.p[1].block - 1) / p.p[1].block;
+    ss.blk0[1][1] = ss.nblk[1] = (p.T + (1 << p.p[1].block_log2) - 1) >> p.p[1].block_log2;
+    make_plan(p, 1, ss);
   }
   tc_fence_before();
   __syncthreads();
@@ -1259,7 +1306,7 @@ size_t ring_shape(StreamParams& p, int cols) {
 
 // Columns of a product's widest tile.
 int columns_of(const StreamParams& p, int which, int parts) {
-  return ceil_div(std::min(p.T, p.p[which].block), 16) * 16 * parts;
+  return ceil_div(std::min(p.T, 1 << p.p[which].block_log2), 16) * 16 * parts;
 }
 
 template <int G, bool LAYER>
@@ -1310,8 +1357,8 @@ int decode_g(const DecodeArgs& a, cudaStream_t s) {
   p.h = reinterpret_cast<uint16_t*>(ws + L.h);
   p.o = reinterpret_cast<float*>(ws + L.o);
   p.parts = a.y_type == MOE_Y_F32 ? 3 : 2;
-  p.p[0].block = Geo<G>::block_rows(1);
-  p.p[1].block = Geo<G>::block_rows(p.parts);
+  p.p[0].block_log2 = Geo<G>::block_log2(1);
+  p.p[1].block_log2 = Geo<G>::block_log2(p.parts);
   if (!fill_product<G>(p.p[0], 0, a.W1, a.W3, mats, c.d_ff, c.d_model) ||
       !fill_product<G>(p.p[1], 1, a.W2, a.W2, mats, c.d_model, c.d_ff) ||
       !map2d(&p.p[0].cols, a.x, c.d_model, c.T, 64, 1) || !map2d(&p.p[1].cols, p.h, c.d_ff, p.parts * Rs, 64, 16))
@@ -1327,7 +1374,7 @@ int linear_g(const LinearArgs& a, cudaStream_t s) {
   std::memset(&p, 0, sizeof(p));
   common_params(p, a.ws, layout(0, 0, 0), a.T, a.y, a.y_type);
   p.n = a.n;
-  p.p[1].block = Geo<G>::block_rows(1);
+  p.p[1].block_log2 = Geo<G>::block_log2(1);
   if (!fill_product<G>(p.p[1], 1, a.W, a.W, 1, a.n, a.K) || !map2d(&p.p[1].cols, a.x, a.K, a.T, 64, 16))
     return MOE_ERR_CUDA;
   const size_t smem = ring_shape<G>(p, columns_of(p, 1, 1));
