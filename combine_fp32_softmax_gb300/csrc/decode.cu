@@ -71,8 +71,8 @@ constexpr int kMaxActive = 256 + 4;
 constexpr int kMaxWorkers = 256;
 
 // Counters in the error region (ints), all 0 between launches.
-constexpr int kCtrHidden = 8;   // row warps done with the first product
-constexpr int kCtrOut = 9;      // ... with the second
+constexpr int kCtrHidden = 8;   // CTAs through the first product
+constexpr int kCtrOut = 9;      // ... through the second
 constexpr int kCtrExit = 10;    // CTAs done
 constexpr int kCtrRouted = 11;  // tokens routed, where the CTAs share the routing
 
@@ -145,6 +145,7 @@ struct alignas(16) Shared {
   uint64_t acc_full[2], acc_empty[2];   // bf16: accumulator pairs
   uint64_t a_ready[2][2], d_full[2][2]; // 4 bits: [box][turn]
   uint64_t swap_ready, swap_done;       // 4 bits: all sums of a tile in tensor memory
+  uint64_t rows_done;                   // this CTA's row warps are through a product
   uint64_t out_done;                    // every CTA's output rows are there
   uint64_t drained;                     // tensor instructions all complete
   uint32_t tmem;
@@ -192,7 +193,7 @@ __device__ bool wait_count(const int* c, int target, volatile int* abort, int* e
 // (parts, count, wait, parts back), the streaming time of some 10 K blocks of
 // an SM that has its share of the memory: tiles of at most kWholeBlocks are
 // not cut, and longer ones not into ranges of fewer than kMinBlocks.
-constexpr int kWholeBlocks = 8, kMinBlocks = 4;
+constexpr int kWholeBlocks = 4, kMinBlocks = 3;
 
 __device__ void make_plan(const StreamParams& p, int which, Shared& ss) {
   const Product& pr = p.p[which];
@@ -1121,6 +1122,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
     }
     mbar_init(&ss.swap_ready, kRowWarps);
     mbar_init(&ss.swap_done, kRowWarps);
+    mbar_init(&ss.rows_done, kRowWarps);
     mbar_init(&ss.out_done, 1);
     mbar_init(&ss.drained, 2);
     ss.abort = 0;
@@ -1143,7 +1145,6 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
   __syncthreads();
   tc_fence_after();
   volatile int* abort = &ss.abort;
-  const int arrivals = kRowWarps * gridDim.x;
   if (warp == kWeightWarp) {
     Ring rg;
     Drain dr;
@@ -1154,21 +1155,28 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
   } else if (warp == kColumnWarp) {
     Ring rg;
     Drain dr;
-    // One poller a CTA: with one per warp the counter's L2 slice was so busy
-    // answering that the last arrivals came through 8 us late.
-    auto wait_all = [&](int counter, int where) {
-      bool ok = true;
-      if (lane == 0) ok = wait_count(p.err + counter, arrivals, abort, p.err, where << 24);
+    // This warp speaks for its CTA: it counts it in once the CTA's row warps
+    // have left a product, and waits for the others.  (With one count and one
+    // poller per warp the counter's L2 slice was so busy that the last
+    // arrivals came through 8 us late.)
+    auto meet = [&](int which) {
+      bool ok = warp_wait(&ss.rows_done, which, abort, p.err, (0x25 << 24) | which);
+      if (lane == 0) {
+        // after a wait that gave up too, so that the other CTAs go on (the error word is set by then)
+        red_release_gpu_add(p.err + kCtrHidden + which, 1);
+        ok = ok && wait_count(p.err + kCtrHidden + which, gridDim.x, abort, p.err, (0x26 << 24) | which);
+      }
       return __shfl_sync(kFull, ok, 0) != 0;
     };
     bool ok = true;
     if (LAYER) {
       ok = produce_columns<G, FIRST>(p, 0, ss, ring, rg, dr, abort);
-      ok = ok && wait_all(kCtrHidden, 0x25);  // every hidden value of every CTA,
-      fence_proxy_async_global();             // for the bulk copies of this one
+      const bool met = meet(0);    // every hidden value of every CTA,
+      fence_proxy_async_global();  // for the bulk copies of this one
+      ok = ok && met;
     }
     if (ok) ok = produce_columns<G, SECOND>(p, 1, ss, ring, rg, dr, abort);
-    if (LAYER && ok && wait_all(kCtrOut, 0x26) && lane == 0) mbar_arrive(&ss.out_done);
+    if (LAYER && meet(1) && ok && lane == 0) mbar_arrive(&ss.out_done);
     dr.wait(ss.full_x);
   } else if (warp >= kMmaWarp) {
     Ring rg;
@@ -1192,25 +1200,23 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
     uint32_t swap = 0;
     bool ok = true;
     if (LAYER) {
-      // Counted even after a wait that gave up, so that the counters come
-      // back to 0 and the other CTAs go on (the error word is set by then).
-      auto publish = [&](int counter) {
+      auto through = [&]() {  // after a wait that gave up as well
         __syncwarp();
-        if (lane == 0) red_release_gpu_add(p.err + counter, 1);
+        if (lane == 0) mbar_arrive(&ss.rows_done);
       };
       if constexpr (Ge::Q4)
         ok = rows_q4<G, FIRST>(p, 0, ss, ring, rg, tn, swap, abort);
       else
         ok = rows_bf16<FIRST>(p, 0, ss, tn, abort);
-      fence_proxy_async_global();  // hidden values, to other CTAs' bulk copies
-      publish(kCtrHidden);
+      fence_proxy_async_global();  // hidden values, to other CTAs' copies
+      through();
       if (ok) {
         if constexpr (Ge::Q4)
           ok = rows_q4<G, SECOND>(p, 1, ss, ring, rg, tn, swap, abort);
         else
           ok = rows_bf16<SECOND>(p, 1, ss, tn, abort);
       }
-      publish(kCtrOut);
+      through();
       ok = ok && mbar_wait(&ss.out_done, 0, abort, p.err, 0x2A << 24);
       if (__all_sync(kFull, ok)) sum_rows(p, ss);
     } else {
