@@ -94,7 +94,7 @@ struct Geo {
   static constexpr int SCALE_BYTES = GROUPS * kTileRows * 2;   // of one box
   static constexpr int WEIGHT_BYTES = 2 * (kBoxBytes + SCALE_BYTES);
   // Activation rows of a tile, in `parts` parts.  bf16 weights: all of an
-  // expert's.  4 bits: what the accumulators hold twice (kOwn, below); an
+  // expert's.  4 bits: what the accumulators and a thread hold; an
   // expert with more rows has its weight tiles visited again, from L2.
   static constexpr int block_log2(int parts) { return !Q4 ? 6 : parts == 1 ? 5 : 4; }
 };
@@ -481,9 +481,26 @@ struct Columns {
 // registers, and the compiler gets them there without a loop over the lanes
 // only where it sees that the warp is together (64 and more clocks an
 // instruction otherwise, against 19 for the smallest tensor instruction).
+__device__ __noinline__ bool warp_wait_slow(uint32_t addr, uint32_t parity, volatile int* abort, int* err, int where) {
+  uint64_t t0 = 0;
+  bool ok = false;
+  while (!ok) {
+#pragma unroll 1
+    for (int i = 0; i < 16 && !ok; ++i) ok = __all_sync(kFull, mbar_try_wait_for(addr, parity, 20000));
+    if (ok || __any_sync(kFull, *abort)) break;
+    if (t0 == 0) t0 = globaltimer_ns();
+    if (__any_sync(kFull, globaltimer_ns() - t0 > kWaitLimitNs)) {
+      record_error(err, MOE_ERR_TIMEOUT_CODE, where);
+      *abort = 1;
+      break;
+    }
+  }
+  return ok;
+}
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* err, int where) {
-  const bool ok = mbar_wait(bar, parity, abort, err, where);
-  return __all_sync(kFull, ok);
+  const uint32_t a = smem_u32(bar);
+  if (__all_sync(kFull, mbar_try_wait_for(a, parity, 20000))) return true;
+  return warp_wait_slow(a, parity, abort, err, where);
 }
 
 // --------------------------------------------------------------- producers
@@ -596,18 +613,11 @@ struct Turn {
   }
 };
 
-// 4 bits: how the sums of a turn are taken.  Up to 32 columns: while the set's
-// next turn is multiplied into the other half of its accumulators (kOwn).
-// More: before the next turn (kWhole).
-enum class Sums { kOwn, kWhole };
-__device__ __forceinline__ Sums sums_of(int columns) { return columns <= kSumCols / 2 ? Sums::kOwn : Sums::kWhole; }
-// A turn is as many groups of a stage as fit the operand buffer and the
-// accumulators.
-template <int G>
-constexpr int kMaxTurnGroups = kOperandCols * 2 / G < 2 ? 1 : 2;
+// 4 bits: a turn is as many groups of a stage as fit the operand buffer and
+// the accumulators.
 template <int G>
 __device__ __forceinline__ int turn_groups(int columns) {
-  return max(1, min(kMaxTurnGroups<G>, kSumCols / 2 / columns));
+  return max(1, min(kOperandCols * 2 / G, kSumCols / columns));
 }
 // Groups of a stage that lie inside K.
 template <int G>
@@ -617,8 +627,8 @@ __device__ __forceinline__ int stage_groups(int K, int kb) {
 __device__ __forceinline__ uint32_t operand_at(uint32_t tmem, int box, int turn) {
   return tmem + (box * 2 + turn) * kOperandCols;
 }
-__device__ __forceinline__ uint32_t sums_at(uint32_t tmem, int box, const Turn& tn, Sums how) {
-  return tmem + 4 * kOperandCols + (box * 2 + tn.buf) * kSumCols + (how == Sums::kOwn ? tn.phase * (kSumCols / 2) : 0);
+__device__ __forceinline__ uint32_t sums_at(uint32_t tmem, int box, int turn) {
+  return tmem + 4 * kOperandCols + (box * 2 + turn) * kSumCols;
 }
 
 template <Kind KIND>
@@ -668,30 +678,25 @@ __device__ bool issue_q4(const StreamParams& p, int which, int box, Shared& ss, 
     const Columns<KIND> c(p, which, ss, s);
     const uint32_t idesc = idesc_bf16_f32(kTileRows, c.n, 0, 0);
     const int tg = turn_groups<G>(c.n);
-    const Sums how = sums_of(c.n);
-    const uint32_t atom = c.n * 128;
+    const uint32_t atom = c.n * 128, tmem = ss.tmem;
     for (int kb = s.kb0; kb < s.kb1; ++kb) {
       const uint32_t x = smem_u32(ring) + static_cast<uint32_t>(rg.stage) * p.stage_bytes + Ge::WEIGHT_BYTES;
       if (!warp_wait(&ss.full_x[rg.stage], rg.phase, abort, p.err, (0x24 << 24) | which)) return false;
       const int groups = stage_groups<G>(pr.K, kb);
       for (int g0 = 0; g0 < groups; g0 += tg) {
-        const uint32_t a = operand_at(ss.tmem, box, tn.buf), d = sums_at(ss.tmem, box, tn, how);
-        const bool second = kMaxTurnGroups<G> == 2 && tg == 2 && g0 + 1 < groups;
-        // 64 columns of the stage start `atom` bytes apart; a group never leaves its own
-        // 64 unless it is 128 wide
-        const uint32_t xg = x + (g0 * G / 64) * atom + (g0 * G % 64) * 2;
-        const uint32_t xg2 = x + ((g0 + 1) * G / 64) * atom + ((g0 + 1) * G % 64) * 2;
+        const uint32_t a = operand_at(tmem, box, tn.buf), d = sums_at(tmem, box, tn.buf);
+        const int n = min(tg, groups - g0);
         if (!warp_wait(&ss.a_ready[box][tn.buf], tn.phase, abort, p.err, (0x32 << 24) | which)) return false;
         tc_fence_after();
         if (elect_one()) {
-#pragma unroll
-          for (int i = 0; i < G / 16; ++i)
-            umma_bf16_ta(d, a + i * 8, smem_desc_sw128(xg + (i / 4) * atom + (i % 4) * 32, 16, 1024), idesc, i != 0);
-          if (second)
+          // 64 columns of the stage start `atom` bytes apart
+          for (int j = 0; j < n; ++j) {
+            const uint32_t xg = x + ((g0 + j) * G / 64) * atom + ((g0 + j) * G % 64) * 2;
 #pragma unroll
             for (int i = 0; i < G / 16; ++i)
-              umma_bf16_ta(d + c.n, a + G / 2 + i * 8, smem_desc_sw128(xg2 + (i / 4) * atom + (i % 4) * 32, 16, 1024),
-                           idesc, i != 0);
+              umma_bf16_ta(d + j * c.n, a + j * (G / 2) + i * 8,
+                           smem_desc_sw128(xg + (i / 4) * atom + (i % 4) * 32, 16, 1024), idesc, i != 0);
+          }
           umma_commit(&ss.d_full[box][tn.buf]);
           if (g0 + tg >= groups) umma_commit(&ss.empty[rg.stage]);
         }
@@ -900,14 +905,9 @@ __device__ bool rows_bf16(const StreamParams& p, int which, Shared& ss, Turn& tn
 }
 
 // 4-bit weights: set 2 box + t owns a box on every other turn, a thread one
-// row of it.  On its turn the thread turns its row's codes into the operand;
-// the sums of an earlier turn, scaled, are added to the thread's own while the
-// tensor core works on a later one (see Sums).
-//
-// The operand buffer of a turn is free once the sums of the set's previous
-// turn are complete, and so is the half of the accumulators that this turn
-// fills (kOwn: read before the previous turn's codes were handed over; kWhole:
-// before this turn's).
+// row of it.  On its turn the thread turns its row's codes into the operand,
+// waits for the tensor core and adds the groups' sums, scaled, to its own;
+// meanwhile the other set has its turn.
 template <int G, int NC, Kind KIND>
 struct RowsQ4 {
   using Ge = Geo<G>;
@@ -949,26 +949,11 @@ struct RowsQ4 {
     const uint32_t lanes = ss.tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const Columns<KIND> c(p, which, ss, s);
     const Share sh(walk, s);
-    const Sums how = sums_of(c.n);
     const int tg = turn_groups<G>(c.n);
+    const uint32_t operand = operand_at(lanes, box, turn), sums = sums_at(lanes, box, turn);
     float sum[NC];
 #pragma unroll
     for (int i = 0; i < NC; ++i) sum[i] = 0.f;
-    Turn before;               // the turn whose sums are still to be taken
-    float scale_before[kMaxTurnGroups<G>];
-    int n_before = 0;
-    auto complete = [&]() {
-      const bool ok = warp_wait(&ss.d_full[box][before.buf], before.phase, abort, p.err, (0x34 << 24) | which);
-      tc_fence_after();
-      return ok;
-    };
-    auto add = [&]() {
-      const uint32_t acc = sums_at(lanes, box, before, how);
-#pragma unroll
-      for (int j = 0; j < kMaxTurnGroups<G>; ++j)
-        if (j < n_before) add_group(p, acc + j * c.n, c.n16, scale_before[j], sum);
-      tc_fence_before();
-    };
     for (int kb = s.kb0; kb < s.kb1; ++kb) {
       if (!warp_wait(&ss.full_w[rg.stage], rg.phase, abort, p.err, (0x23 << 24) | which)) return false;
       const uint32_t st = smem_u32(ring) + static_cast<uint32_t>(rg.stage) * p.stage_bytes;
@@ -977,12 +962,7 @@ struct RowsQ4 {
       const int groups = stage_groups<G>(pr.K, kb);
       for (int g0 = 0; g0 < groups; g0 += tg) {
         if (tn.buf == turn) {
-          if (n_before) {
-            if (!complete()) return false;
-            if (how == Sums::kWhole) add();
-          }
           const int n = min(tg, groups - g0);
-          const uint32_t a = operand_at(lanes, box, turn);
           for (int j = 0; j < n; ++j)
 #pragma unroll
             for (int i = 0; i < G / 32; ++i) {
@@ -992,18 +972,17 @@ struct RowsQ4 {
               for (int t = 0; t < 4; ++t)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) v[t * 4 + q] = q4_pair(w[t], q);
-              tmem_st16(a + j * (G / 2) + i * 16, v);
+              tmem_st16(operand + j * (G / 2) + i * 16, v);
             }
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&ss.a_ready[box][turn]);
-          if (n_before && how == Sums::kOwn) add();
-          before = tn;
-          n_before = n;
-#pragma unroll
-          for (int j = 0; j < kMaxTurnGroups<G>; ++j)
-            scale_before[j] = j < n ? lds_bf16(scales + (g0 + j) * (kTileRows * 2)) : 0.f;
+          if (!warp_wait(&ss.d_full[box][turn], tn.phase, abort, p.err, (0x34 << 24) | which)) return false;
+          tc_fence_after();
+          for (int j = 0; j < n; ++j)
+            add_group(p, sums + j * c.n, c.n16, lds_bf16(scales + (g0 + j) * (kTileRows * 2)), sum);
+          tc_fence_before();
         }
         tn.step(2);
       }
@@ -1011,11 +990,6 @@ struct RowsQ4 {
       if (lane == 0) mbar_arrive(&ss.empty[rg.stage]);
       rg.step(p.stages);
     }
-    if (n_before) {
-      if (!complete()) return false;
-      add();
-    }
-
     // All sums of the tile meet in tensor memory, in the sets' operand
     // buffers: both boxes' and both turns'.  No set goes on before all have
     // read their share.
@@ -1217,8 +1191,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
           ok = rows_bf16<SECOND>(p, 1, ss, tn, abort);
       }
       through();
-      ok = ok && mbar_wait(&ss.out_done, 0, abort, p.err, 0x2A << 24);
-      if (__all_sync(kFull, ok)) sum_rows(p, ss);
+      if (ok && warp_wait(&ss.out_done, 0, abort, p.err, 0x2A << 24)) sum_rows(p, ss);
     } else {
       if constexpr (Ge::Q4)
         rows_q4<G, SECOND>(p, 1, ss, ring, rg, tn, swap, abort);
