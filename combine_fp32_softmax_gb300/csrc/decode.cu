@@ -71,8 +71,7 @@ constexpr int kMaxActive = 256 + 4;
 constexpr int kMaxWorkers = 256;
 
 // Counters in the error region (ints), all 0 between launches.
-constexpr int kCtrHidden = 8;   // CTAs through the first product
-constexpr int kCtrOut = 9;      // ... through the second
+constexpr int kCtrHidden = 8;   // CTAs through the first product; the next one: through the second
 constexpr int kCtrExit = 10;    // CTAs done
 constexpr int kCtrRouted = 11;  // tokens routed, where the CTAs share the routing
 
@@ -481,29 +480,11 @@ struct Columns {
 // registers, and the compiler gets them there without a loop over the lanes
 // only where it sees that the warp is together (64 and more clocks an
 // instruction otherwise, against 19 for the smallest tensor instruction).
-__device__ __noinline__ bool warp_wait_slow(uint32_t addr, uint32_t parity, volatile int* abort, int* err, int where) {
-  uint64_t t0 = 0;
-  bool ok = false;
-  while (!ok) {
-#pragma unroll 1
-    for (int i = 0; i < 16 && !ok; ++i) ok = __all_sync(kFull, mbar_try_wait_for(addr, parity, 20000));
-    if (ok || __any_sync(kFull, *abort)) break;
-    if (t0 == 0) t0 = globaltimer_ns();
-    if (__any_sync(kFull, globaltimer_ns() - t0 > kWaitLimitNs)) {
-      record_error(err, MOE_ERR_TIMEOUT_CODE, where);
-      *abort = 1;
-      break;
-    }
-  }
-  return ok;
-}
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* err, int where) {
-  const uint32_t a = smem_u32(bar);
-  if (__all_sync(kFull, mbar_try_wait_for(a, parity, 20000))) return true;
-  return warp_wait_slow(a, parity, abort, err, where);
+  const bool ok = mbar_wait(bar, parity, abort, err, where);
+  return __all_sync(kFull, ok);
 }
 
-// --------------------------------------------------------------- producers
 template <int G, Kind KIND>
 __device__ bool produce_weights(const StreamParams& p, int which, Shared& ss, uint8_t* ring, Ring& rg, Drain& dr,
                                 volatile int* abort) {

@@ -141,3 +141,27 @@ def test_quantize_reference_keeps_half_a_step():
     # half a step, and the largest magnitude up to 7 s (1 + 2^-8), s being rounded to bf16
     assert (np.abs(Q.values(codes, scales, 64) - w.double().numpy()) <= s * (0.5 + 7 * 2.0 ** -8)).all()
     assert not scales[:, :, 9:].any()
+
+
+def test_quotient_of_the_quantizer_rounds_like_the_division():
+    """x * r, one Newton step and the addition of 1.5 * 2^23 in fp32 give rint(x / s), ties to even, for every pair of
+    bf16 significands in the range and every r within 1 ulp of 1 / s (fused operations emulated in fp64, where their
+    one rounding is to fp32).  absmax * fl(1/7), rounded to bf16, is the quotient by 7."""
+    f32, f64 = np.float32, np.float64
+    top = torch.arange(128, 256).float() / 128
+    assert torch.equal((top * torch.tensor(1 / 7)).to(torch.bfloat16), (top.double() / 7).to(torch.bfloat16))
+    for ms, off in ((m, o) for m in range(128, 256) for o in (-1, 0, 1)):
+        s = f32(ms / 128)
+        r = f32(1) / s
+        r = np.nextafter(r, f32(9 * off)) if off else r
+        x = np.concatenate([np.arange(128, 256) / 128 * 2.0 ** e for e in range(-12, 4)]).astype(f32)
+        x = x[x <= 7.1 * s]
+        x = np.concatenate([x, -x])
+        y = x * r
+        rest = (x.astype(f64) - y.astype(f64) * f64(s)).astype(f32)
+        y = (rest.astype(f64) * f64(r) + y.astype(f64)).astype(f32)
+        got = ((y + f32(12582912 + 8)).view(np.uint32) & 15).astype(np.int64) - 8
+        num, den = np.rint(x.astype(f64) * 2 ** 20).astype(np.int64), int(f64(s) * 2 ** 20)
+        low, rem = num // den, num % den
+        want = low + ((2 * rem > den) | ((2 * rem == den) & (low % 2 != 0)))
+        assert np.array_equal(got, want), ms
