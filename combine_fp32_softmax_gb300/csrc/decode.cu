@@ -144,7 +144,8 @@ struct alignas(16) Shared {
   uint64_t acc_full[2], acc_empty[2];   // bf16: accumulator pairs
   uint64_t a_ready[2][2], d_full[2][2]; // 4 bits: [box][turn]
   uint64_t swap_ready, swap_done;       // 4 bits: all sums of a tile in tensor memory
-  uint64_t rows_done;                   // this CTA's row warps are through a product
+  uint64_t rows_done[2];                // this CTA's row warps are through a product: a barrier for each, as the
+                                        // second may be over (no work) before anyone looked at the first
   uint64_t out_done;                    // every CTA's output rows are there
   uint64_t drained;                     // tensor instructions all complete
   uint32_t tmem;
@@ -1061,26 +1062,27 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
   uint8_t* ring = dyn + (ring_at - smem_u32(dyn));
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(kFull, tid >> 5, 0);  // the same for the warp, and known to be
-  if (tid == 0) {
-    for (int i = 0; i < p.stages; ++i) {
-      mbar_init(&ss.full_w[i], 1);
-      mbar_init(&ss.full_x[i], 1);
-      mbar_init(&ss.empty[i], Ge::Q4 ? kRowWarps + 2 : 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&ss.acc_full[i], 1);
-      mbar_init(&ss.acc_empty[i], kRowWarps);
-      for (int j = 0; j < 2; ++j) {
-        mbar_init(&ss.a_ready[i][j], 4);
-        mbar_init(&ss.d_full[i][j], 1);
+  if (warp == kWeightWarp) {
+    if (lane < p.stages) {
+      mbar_init(&ss.full_w[lane], 1);
+      mbar_init(&ss.full_x[lane], 1);
+      mbar_init(&ss.empty[lane], Ge::Q4 ? kRowWarps + 2 : 1);
+    } else if (lane >= 16 && lane < 20) {
+      const int i = lane & 1, j = (lane >> 1) & 1;
+      mbar_init(&ss.a_ready[i][j], 4);
+      mbar_init(&ss.d_full[i][j], 1);
+      if (j == 0) {
+        mbar_init(&ss.acc_full[i], 1);
+        mbar_init(&ss.acc_empty[i], kRowWarps);
+        mbar_init(&ss.rows_done[i], kRowWarps);
       }
+    } else if (lane == 20) {
+      mbar_init(&ss.swap_ready, kRowWarps);
+      mbar_init(&ss.swap_done, kRowWarps);
+      mbar_init(&ss.out_done, 1);
+      mbar_init(&ss.drained, 2);
+      ss.abort = 0;
     }
-    mbar_init(&ss.swap_ready, kRowWarps);
-    mbar_init(&ss.swap_done, kRowWarps);
-    mbar_init(&ss.rows_done, kRowWarps);
-    mbar_init(&ss.out_done, 1);
-    mbar_init(&ss.drained, 2);
-    ss.abort = 0;
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -1115,7 +1117,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
     // poller per warp the counter's L2 slice was so busy that the last
     // arrivals came through 8 us late.)
     auto meet = [&](int which) {
-      bool ok = warp_wait(&ss.rows_done, which, abort, p.err, (0x25 << 24) | which);
+      bool ok = warp_wait(&ss.rows_done[which], 0, abort, p.err, (0x25 << 24) | which);
       if (lane == 0) {
         // after a wait that gave up too, so that the other CTAs go on (the error word is set by then)
         red_release_gpu_add(p.err + kCtrHidden + which, 1);
@@ -1155,23 +1157,23 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
     uint32_t swap = 0;
     bool ok = true;
     if (LAYER) {
-      auto through = [&]() {  // after a wait that gave up as well
+      auto through = [&](int which) {  // after a wait that gave up as well
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ss.rows_done);
+        if (lane == 0) mbar_arrive(&ss.rows_done[which]);
       };
       if constexpr (Ge::Q4)
         ok = rows_q4<G, FIRST>(p, 0, ss, ring, rg, tn, swap, abort);
       else
         ok = rows_bf16<FIRST>(p, 0, ss, tn, abort);
       fence_proxy_async_global();  // hidden values, to other CTAs' copies
-      through();
+      through(0);
       if (ok) {
         if constexpr (Ge::Q4)
           ok = rows_q4<G, SECOND>(p, 1, ss, ring, rg, tn, swap, abort);
         else
           ok = rows_bf16<SECOND>(p, 1, ss, tn, abort);
       }
-      through();
+      through(1);
       if (ok && warp_wait(&ss.out_done, 0, abort, p.err, 0x2A << 24)) sum_rows(p, ss);
     } else {
       if constexpr (Ge::Q4)

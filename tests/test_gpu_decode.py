@@ -289,6 +289,26 @@ def test_same_bits_every_time_and_for_every_grid(group):
         moe.moe_set_grid_limit(0)
 
 
+@pytest.mark.parametrize("cfg", [MoEConfig("few_out", 21, 512, 704, 16, 4, S=2), MoEConfig("one_tile", 2, 64, 1408, 4, 2),
+                                 MoEConfig("wide_out", 3, 2048, 64, 8, 2)], ids=lambda c: c.name)
+@pytest.mark.parametrize("group", [0, 64])
+def test_hundreds_of_calls_in_a_row(cfg, group):
+    """Waits whose order varies from call to call: products with fewer ranges than CTAs leave CTAs without work in one
+    product or the other."""
+    layer = Layer(cfg, group=group)
+    ws, out = layer.workspace(), layer.outputs(F32)
+    x, z = layer.x.to(DEV), layer.logits.to(DEV)
+    want = [t.clone() for t in layer.run(ws=ws, out=out, x=x, logits=z)[:3]]
+    for _ in range(8):
+        for t in out:
+            t.zero_()
+        for _ in range(50):
+            layer.run(ws=ws, out=out, x=x, logits=z)
+        assert device_error(ws) == (0, 0)
+        for a, b in zip(out, want):
+            assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("group", [0, 64])
 def test_graph_replays_with_new_inputs(group):
     cfg = MoEConfig("graph", 5, 256, 320, 8, 2, S=1)
