@@ -189,20 +189,29 @@ __device__ bool wait_count(const int* c, int target, volatile int* abort, int* e
 // The tiles of one row tile of all experts follow each other, so the shared
 // experts, which have the most rows to finish, are spread over the ranges.
 //
-// Putting a cut tile together again costs a few microseconds of latency
-// (parts, count, wait, parts back), the streaming time of some 10 K blocks of
-// an SM that has its share of the memory: tiles of at most kWholeBlocks are
-// not cut, and longer ones not into ranges of fewer than kMinBlocks.
-constexpr int kWholeBlocks = 4, kMinBlocks = 3;
+// Whole tiles or cut ones.  In units of 0.37 us: with all SMs at work a K
+// block of 32 KB takes 2 of them (bf16: memory) or 4 (4 bits: turning codes);
+// an SM that has the memory to itself takes 1 for a bf16 block.  Putting cut
+// tiles together again costs 8 more (parts, count, wait, parts back).  Whole
+// tiles take turns of all SMs and a last turn of the rest; one token's 88
+// tiles of W1 and W3 of the layer d=2048 f=1408 k=6 S=2 are faster whole on 88
+// SMs than cut for 152, 17 tiles of a 4097 x 4096 matrix are not.  No range of
+// a cut product has fewer than kMinBlocks.
+constexpr int kMinBlocks = 3, kJoinUnits = 8;
 
+template <bool Q4>
 __device__ void make_plan(const StreamParams& p, int which, Shared& ss) {
   const Product& pr = p.p[which];
   Plan& pl = ss.plan[which];
   pl.per = ss.nblk[which];
-  pl.units = pl.per * pr.row_tiles * pr.kblocks;
-  const bool whole = pr.kblocks <= kWholeBlocks;
+  const int tiles = pl.per * pr.row_tiles, turns = tiles / p.workers, rest = tiles - turns * p.workers;
+  pl.units = tiles * pr.kblocks;
+  const int whole_time = Q4 ? 4 * pr.kblocks * (turns + (rest > 0))
+                            : pr.kblocks * 2 * turns + (rest ? max(pr.kblocks, 2 * pr.kblocks * rest / p.workers) : 0);
+  const int cut_time = (Q4 ? 4 : 2) * (pl.units / p.workers) + kJoinUnits;
+  const bool whole = whole_time <= cut_time;
   pl.grain = whole ? pr.kblocks : 1;
-  const int grains = whole ? pl.per * pr.row_tiles : pl.units;
+  const int grains = whole ? tiles : pl.units;
   pl.workers = max(1, min(p.workers, whole ? grains : grains / kMinBlocks));  // no range is empty
   pl.q = grains / pl.workers;
   pl.extra = grains - pl.q * pl.workers;
@@ -266,6 +275,7 @@ __device__ __noinline__ void route_all(const StreamParams& p, Shared& ss) {
   }
 }
 
+template <bool Q4>
 __device__ void build_work_list(const StreamParams& p, Shared& ss) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int R = p.T * p.k;
@@ -344,7 +354,7 @@ __device__ void build_work_list(const StreamParams& p, Shared& ss) {
   }
   __syncthreads();
   if (tid == kThreads - 32 || tid == kThreads - 64) {
-    make_plan(p, tid == kThreads - 64, ss);
+    make_plan<Q4>(p, tid == kThreads - 64, ss);
   } else {
     // rows: first row of the expert + earlier tokens of its mask; eight lanes a token
     const int j = tid & 7;
@@ -1090,13 +1100,13 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
     tmem_relinquish();
   }
   if (LAYER) {
-    build_work_list(p, ss);
+    build_work_list<Ge::Q4>(p, ss);
   } else if (tid == 0) {
     ss.nact = 1;
     ss.e[0] = ss.row0[0] = ss.blk0[1][0] = 0;
     ss.m[0] = p.T;
     ss.blk0[1][1] = ss.nblk[1] = (p.T + (1 << p.p[1].block_log2) - 1) >> p.p[1].block_log2;
-    make_plan(p, 1, ss);
+    make_plan<Ge::Q4>(p, 1, ss);
   }
   tc_fence_before();
   __syncthreads();
