@@ -62,6 +62,7 @@ constexpr int kTmemCols = 512;
 constexpr int kOperandCols = 64;
 constexpr int kSumCols = 64;
 constexpr int kMaxStages = 8;
+constexpr int kTileSlots = 4;            // drawn tiles on their way to the other roles
 constexpr int kMaxTokens = MOE_DECODE_MAX_T;
 constexpr int kMaxPicks = kMaxTokens * 8;
 constexpr int kMaxRows = kMaxTokens * 12;   // k <= 8 slots and 4 shared experts
@@ -74,6 +75,8 @@ constexpr int kMaxWorkers = 256;
 constexpr int kCtrHidden = 8;   // CTAs through the first product; the next one: through the second
 constexpr int kCtrExit = 10;    // CTAs done
 constexpr int kCtrRouted = 11;  // tokens routed, where the CTAs share the routing
+constexpr int kCtrTicket = 12;  // tiles drawn, by product
+constexpr int kCtrEnd = 14;
 
 // K blocks of W2 that a CTA asks into L2 when its part of the first product
 // is on the way, beyond what its ring holds.  Memory then stays busy while the
@@ -98,6 +101,12 @@ struct Geo {
   static constexpr int block_log2(int parts) { return !Q4 ? 6 : parts == 1 ? 5 : 4; }
 };
 
+// What the columns of a product are.
+//   kRowsOfX   the T rows of x (linear form)
+//   kGathered  the rows of x of an expert's tokens (hidden values)
+//   kRowsOfH   an expert's rows of h, all parts (output rows)
+enum Kind { kRowsOfX, kGathered, kRowsOfH };
+
 // One product of the launch: weight tiles of `row_step` output rows.
 struct Product {
   CUtensorMap w0, w1;   // weight boxes: W1 and W3, or (the same) the two halves of a W2 tile
@@ -105,6 +114,7 @@ struct Product {
   CUtensorMap cols;     // activation rows
   int K, kblocks, rows, row_step, row_tiles;
   int block_log2;       // log2 of the most activation rows of a tile
+  Kind kind;
 };
 
 struct StreamParams {
@@ -129,7 +139,8 @@ struct StreamParams {
 // which is tile r of row tile rt and belongs to work list entry a.
 struct Plan {
   int units, workers, grain, q, extra;   // grain: K blocks that a range takes at least of a tile
-  int per;                               // tiles of a row tile
+  int per, tiles;                        // tiles of a row tile, and of the product
+  bool drawn;                            // whole tiles, drawn by the CTAs
   int u, item, rt, r, a;
   __device__ int begin_of(int v) const { return (v * q + min(v, extra)) * grain; }
   // The range that holds K block `unit`.
@@ -147,6 +158,8 @@ struct alignas(16) Shared {
   uint64_t rows_done[2];                // this CTA's row warps are through a product: a barrier for each, as the
                                         // second may be over (no work) before anyone looked at the first
   uint64_t out_done;                    // every CTA's output rows are there
+  uint64_t tile_full[kTileSlots], tile_empty[kTileSlots];
+  int4 tile[kTileSlots];                // drawn tiles: item (-1: no more), entry, row tile, block
   uint64_t drained;                     // tensor instructions all complete
   uint32_t tmem;
   int abort;
@@ -197,6 +210,11 @@ __device__ bool wait_count(const int* c, int target, volatile int* abort, int* e
 // tiles of W1 and W3 of the layer d=2048 f=1408 k=6 S=2 are faster whole on 88
 // SMs than cut for 152, 17 tiles of a 4097 x 4096 matrix are not.  No range of
 // a cut product has fewer than kMinBlocks.
+//
+// Whole tiles of several turns are drawn from a counter: the SMs do not get
+// equal shares of the memory's rate (64 tokens of that layer: 160,000 clocks
+// for the first product on one SM, 246,000 on another with as many tiles).
+// A tile's sums do not depend on the CTA that makes them.
 constexpr int kMinBlocks = 3, kJoinUnits = 8;
 
 template <bool Q4>
@@ -206,10 +224,15 @@ __device__ void make_plan(const StreamParams& p, int which, Shared& ss) {
   pl.per = ss.nblk[which];
   const int tiles = pl.per * pr.row_tiles, turns = tiles / p.workers, rest = tiles - turns * p.workers;
   pl.units = tiles * pr.kblocks;
+  // output rows whose weights were asked into L2 ahead stream at twice the memory's rate
+  const bool ahead = pr.kind == kRowsOfH && pl.units <= (kPrefetchBlocks + p.stages) * p.workers;
+  const int each = Q4 ? 4 : ahead ? 1 : 2;
   const int whole_time = Q4 ? 4 * pr.kblocks * (turns + (rest > 0))
-                            : pr.kblocks * 2 * turns + (rest ? max(pr.kblocks, 2 * pr.kblocks * rest / p.workers) : 0);
-  const int cut_time = (Q4 ? 4 : 2) * (pl.units / p.workers) + kJoinUnits;
+                            : pr.kblocks * each * turns + (rest ? max(pr.kblocks, each * pr.kblocks * rest / p.workers) : 0);
+  const int cut_time = each * (pl.units / p.workers) + kJoinUnits;
   const bool whole = whole_time <= cut_time;
+  pl.tiles = tiles;
+  pl.drawn = whole && tiles > p.workers;
   pl.grain = whole ? pr.kblocks : 1;
   const int grains = whole ? tiles : pl.units;
   pl.workers = max(1, min(p.workers, whole ? grains : grains / kMinBlocks));  // no range is empty
@@ -432,6 +455,84 @@ struct Walk {
   }
 };
 
+// The segments of a product for one role.  Where tiles are drawn, the producer
+// of weights draws them and passes them on through a short queue.
+struct Queue {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void step() {
+    if (++slot == kTileSlots) {
+      slot = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* err, int where) {
+  const bool ok = mbar_wait(bar, parity, abort, err, where);
+  return __all_sync(kFull, ok);
+}
+
+template <bool DRAWS>
+struct Tiles {
+  Walk walk;
+  const StreamParams& p;
+  Shared& ss;
+  Queue& queue;
+  volatile int* abort;
+  int which, ticket;
+
+  __device__ Tiles(const StreamParams& params, int product, Shared& shared, Queue& q, volatile int* ab)
+      : walk(params, product, shared), p(params), ss(shared), queue(q), abort(ab), which(product), ticket(blockIdx.x) {}
+
+  // Item, work list entry, row tile and block of a tile.
+  __device__ int4 locate(int item) const {
+    const int rt = item / walk.pl.per, r = item - rt * walk.pl.per;
+    int lo = 0, hi = ss.nact - 1;   // last entry with blk0 <= r
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (walk.blk0[mid] <= r)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    return make_int4(item, lo, rt, r - walk.blk0[lo]);
+  }
+
+  __device__ __forceinline__ bool next(Segment& s) {
+    if (!walk.pl.drawn) return walk.next(s);
+    const bool lead = (threadIdx.x & 31) == 0;
+    int4 t;
+    if (DRAWS) {
+      const Plan& pl = walk.pl;
+      const int item = __shfl_sync(kFull, ticket, 0);
+      t = item < pl.tiles ? locate(item) : make_int4(-1, 0, 0, 0);
+      if (!warp_wait(&ss.tile_empty[queue.slot], queue.phase ^ 1, abort, p.err, 0x2B << 24)) return false;
+      if (lead) {
+        ss.tile[queue.slot] = t;
+        mbar_arrive(&ss.tile_full[queue.slot]);
+        // the next one's round trip overlaps this tile
+        if (t.x >= 0) ticket = static_cast<int>(gridDim.x) + atomicAdd(p.err + kCtrTicket + which, 1);
+      }
+    } else {
+      if (!warp_wait(&ss.tile_full[queue.slot], queue.phase, abort, p.err, 0x2C << 24)) return false;
+      t = ss.tile[queue.slot];
+      __syncwarp();
+      if (lead) mbar_arrive(&ss.tile_empty[queue.slot]);
+    }
+    queue.step();
+    if (t.x < 0) return false;
+    s.worker = 0;
+    s.item = t.x;
+    s.a = t.y;
+    s.rt = t.z;
+    s.nb = t.w;
+    s.kb0 = 0;
+    s.kb1 = walk.pr.kblocks;
+    return true;
+  }
+};
+
 struct Ring {
   int stage = 0;
   uint32_t phase = 0;
@@ -464,12 +565,6 @@ struct Drain {
   }
 };
 
-// What the columns of a product are.
-//   kRowsOfX   the T rows of x (linear form)
-//   kGathered  the rows of x of an expert's tokens (hidden values)
-//   kRowsOfH   an expert's rows of h, all parts (output rows)
-enum Kind { kRowsOfX, kGathered, kRowsOfH };
-
 // Columns of a tile, each part's rounded up to 16.
 template <Kind KIND>
 struct Columns {
@@ -491,27 +586,31 @@ struct Columns {
 // registers, and the compiler gets them there without a loop over the lanes
 // only where it sees that the warp is together (64 and more clocks an
 // instruction otherwise, against 19 for the smallest tensor instruction).
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* err, int where) {
-  const bool ok = mbar_wait(bar, parity, abort, err, where);
-  return __all_sync(kFull, ok);
-}
-
 template <int G, Kind KIND>
-__device__ bool produce_weights(const StreamParams& p, int which, Shared& ss, uint8_t* ring, Ring& rg, Drain& dr,
+__device__ bool produce_weights(const StreamParams& p, int which, Shared& ss, uint8_t* ring, Ring& rg, Queue& qu, Drain& dr,
                                 volatile int* abort) {
   using Ge = Geo<G>;
   const Product& pr = p.p[which];
-  Walk walk(p, which, ss);
+  Tiles<true> walk(p, which, ss, qu, abort);
   Segment s;
   if (KIND == kRowsOfH) {
-    Walk ahead(p, which, ss);
-    for (int n = -p.stages; n < kPrefetchBlocks && ahead.next(s);) {
-      const int row = ss.e[s.a] * pr.rows + s.rt * pr.row_step;
-      for (int kb = s.kb0; kb < s.kb1 && n < kPrefetchBlocks; ++kb, ++n)
+    int n = -p.stages;
+    auto ask = [&](int a, int rt, int kb0, int kb1) {
+      const int row = ss.e[a] * pr.rows + rt * pr.row_step;
+      for (int kb = kb0; kb < kb1 && n < kPrefetchBlocks; ++kb, ++n)
         if (n >= 0 && elect_one()) {
           tma_prefetch_2d(&pr.w0, kb * (Ge::Q4 ? 128 : 64), row);
           tma_prefetch_2d(&pr.w1, kb * (Ge::Q4 ? 128 : 64), row + kTileRows);
         }
+    };
+    if (walk.walk.pl.drawn) {  // the tiles that the CTAs draw first
+      for (int item = blockIdx.x; item < walk.walk.pl.tiles && n < kPrefetchBlocks; item += gridDim.x) {
+        const int4 t = walk.locate(item);
+        ask(t.y, t.z, 0, pr.kblocks);
+      }
+    } else {
+      Walk ahead(p, which, ss);
+      while (n < kPrefetchBlocks && ahead.next(s)) ask(s.a, s.rt, s.kb0, s.kb1);
     }
     __syncwarp();
   }
@@ -547,12 +646,12 @@ __device__ bool produce_weights(const StreamParams& p, int which, Shared& ss, ui
 // What a box or a gather leaves of the 16 rows keeps old values; they are
 // columns that nobody reads.
 template <int G, Kind KIND>
-__device__ bool produce_columns(const StreamParams& p, int which, Shared& ss, uint8_t* ring, Ring& rg, Drain& dr,
+__device__ bool produce_columns(const StreamParams& p, int which, Shared& ss, uint8_t* ring, Ring& rg, Queue& qu, Drain& dr,
                                 volatile int* abort) {
   using Ge = Geo<G>;
   const Product& pr = p.p[which];
   const int Rs = p.T * (p.k + p.S);
-  Walk walk(p, which, ss);
+  Tiles<false> walk(p, which, ss, qu, abort);
   Segment s;
   while (walk.next(s)) {
     const Columns<KIND> c(p, which, ss, s);
@@ -624,9 +723,9 @@ __device__ __forceinline__ uint32_t sums_at(uint32_t tmem, int box, int turn) {
 }
 
 template <Kind KIND>
-__device__ bool issue_bf16(const StreamParams& p, int which, Shared& ss, uint8_t* ring, Ring& rg, Turn& tn,
+__device__ bool issue_bf16(const StreamParams& p, int which, Shared& ss, uint8_t* ring, Ring& rg, Queue& qu, Turn& tn,
                            volatile int* abort) {
-  Walk walk(p, which, ss);
+  Tiles<false> walk(p, which, ss, qu, abort);
   Segment s;
   while (walk.next(s)) {
     const Columns<KIND> c(p, which, ss, s);
@@ -660,11 +759,11 @@ __device__ bool issue_bf16(const StreamParams& p, int which, Shared& ss, uint8_t
 }
 
 template <int G, Kind KIND>
-__device__ bool issue_q4(const StreamParams& p, int which, int box, Shared& ss, uint8_t* ring, Ring& rg, Turn& tn,
+__device__ bool issue_q4(const StreamParams& p, int which, int box, Shared& ss, uint8_t* ring, Ring& rg, Queue& qu, Turn& tn,
                          volatile int* abort) {
   using Ge = Geo<G>;
   const Product& pr = p.p[which];
-  Walk walk(p, which, ss);
+  Tiles<false> walk(p, which, ss, qu, abort);
   Segment s;
   while (walk.next(s)) {
     const Columns<KIND> c(p, which, ss, s);
@@ -784,6 +883,7 @@ template <Kind KIND>
 __device__ bool join_parts(const StreamParams& p, int which, const Shared& ss, volatile int* abort) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int row = (warp & 3) * 32 + lane, set = warp >> 2;
+  if (ss.plan[which].grain > 1) return true;  // no tile is cut
   Walk walk(p, which, ss);
   Segment s;
   while (walk.next(s)) {
@@ -862,13 +962,13 @@ __device__ __forceinline__ void finish_segment(const StreamParams& p, const Shar
 
 // bf16 weights: the accumulators hold a segment's sums.
 template <Kind KIND>
-__device__ bool rows_bf16(const StreamParams& p, int which, Shared& ss, Turn& tn, volatile int* abort) {
+__device__ bool rows_bf16(const StreamParams& p, int which, Shared& ss, Queue& qu, Turn& tn, volatile int* abort) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  Walk walk(p, which, ss);
+  Tiles<false> walk(p, which, ss, qu, abort);
   Segment s;
   while (walk.next(s)) {
     const Columns<KIND> c(p, which, ss, s);
-    const Share sh(walk, s);
+    const Share sh(walk.walk, s);
     if (!warp_wait(&ss.acc_full[tn.buf], tn.phase, abort, p.err, (0x33 << 24) | which)) return false;
     tc_fence_after();
     const uint32_t acc = ss.tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + tn.buf * 2 * p.acc_cols;
@@ -1017,17 +1117,17 @@ struct RowsQ4 {
 };
 
 template <int G, Kind KIND>
-__device__ bool rows_q4(const StreamParams& p, int which, Shared& ss, uint8_t* ring, Ring& rg, Turn& tn, uint32_t& swap,
+__device__ bool rows_q4(const StreamParams& p, int which, Shared& ss, uint8_t* ring, Ring& rg, Queue& qu, Turn& tn, uint32_t& swap,
                         volatile int* abort) {
-  Walk walk(p, which, ss);
+  Tiles<false> walk(p, which, ss, qu, abort);
   Segment s;
   bool ok = true;
   while (ok && walk.next(s)) {
     // rows of h come at most 16 at a time
     if (KIND == kRowsOfH || Columns<KIND>(p, which, ss, s).n16 == 1)
-      ok = RowsQ4<G, 16, KIND>::segment(p, which, ss, ring, walk, s, rg, tn, swap, abort);
+      ok = RowsQ4<G, 16, KIND>::segment(p, which, ss, ring, walk.walk, s, rg, tn, swap, abort);
     else
-      ok = RowsQ4<G, KIND == kRowsOfH ? 16 : 32, KIND>::segment(p, which, ss, ring, walk, s, rg, tn, swap, abort);
+      ok = RowsQ4<G, KIND == kRowsOfH ? 16 : 32, KIND>::segment(p, which, ss, ring, walk.walk, s, rg, tn, swap, abort);
   }
   return ok && join_parts<KIND>(p, which, ss, abort);
 }
@@ -1086,6 +1186,10 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
         mbar_init(&ss.acc_empty[i], kRowWarps);
         mbar_init(&ss.rows_done[i], kRowWarps);
       }
+    } else if (lane >= 24 && lane < 24 + kTileSlots) {
+      mbar_init(&ss.tile_full[lane - 24], 1);
+      // readers: row warps, columns, one issuer (bf16) or two
+      mbar_init(&ss.tile_empty[lane - 24], kRowWarps + 1 + (Ge::Q4 ? 2 : 1));
     } else if (lane == 20) {
       mbar_init(&ss.swap_ready, kRowWarps);
       mbar_init(&ss.swap_done, kRowWarps);
@@ -1114,13 +1218,15 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
   volatile int* abort = &ss.abort;
   if (warp == kWeightWarp) {
     Ring rg;
+    Queue qu;
     Drain dr;
     bool ok = true;
-    if (LAYER) ok = produce_weights<G, FIRST>(p, 0, ss, ring, rg, dr, abort);
-    if (ok) produce_weights<G, SECOND>(p, 1, ss, ring, rg, dr, abort);
+    if (LAYER) ok = produce_weights<G, FIRST>(p, 0, ss, ring, rg, qu, dr, abort);
+    if (ok) produce_weights<G, SECOND>(p, 1, ss, ring, rg, qu, dr, abort);
     dr.wait(ss.full_w);
   } else if (warp == kColumnWarp) {
     Ring rg;
+    Queue qu;
     Drain dr;
     // This warp speaks for its CTA: it counts it in once the CTA's row warps
     // have left a product, and waits for the others.  (With one count and one
@@ -1137,25 +1243,26 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
     };
     bool ok = true;
     if (LAYER) {
-      ok = produce_columns<G, FIRST>(p, 0, ss, ring, rg, dr, abort);
+      ok = produce_columns<G, FIRST>(p, 0, ss, ring, rg, qu, dr, abort);
       const bool met = meet(0);    // every hidden value of every CTA,
       fence_proxy_async_global();  // for the bulk copies of this one
       ok = ok && met;
     }
-    if (ok) ok = produce_columns<G, SECOND>(p, 1, ss, ring, rg, dr, abort);
+    if (ok) ok = produce_columns<G, SECOND>(p, 1, ss, ring, rg, qu, dr, abort);
     if (LAYER && meet(1) && ok && lane == 0) mbar_arrive(&ss.out_done);
     dr.wait(ss.full_x);
   } else if (warp >= kMmaWarp) {
     Ring rg;
+    Queue qu;
     Turn tn;
     bool ok = true;
     if constexpr (Ge::Q4) {
       const int box = warp - kMmaWarp;
-      if (LAYER) ok = issue_q4<G, FIRST>(p, 0, box, ss, ring, rg, tn, abort);
-      if (ok) issue_q4<G, SECOND>(p, 1, box, ss, ring, rg, tn, abort);
+      if (LAYER) ok = issue_q4<G, FIRST>(p, 0, box, ss, ring, rg, qu, tn, abort);
+      if (ok) issue_q4<G, SECOND>(p, 1, box, ss, ring, rg, qu, tn, abort);
     } else if (warp == kMmaWarp) {
-      if (LAYER) ok = issue_bf16<FIRST>(p, 0, ss, ring, rg, tn, abort);
-      if (ok) issue_bf16<SECOND>(p, 1, ss, ring, rg, tn, abort);
+      if (LAYER) ok = issue_bf16<FIRST>(p, 0, ss, ring, rg, qu, tn, abort);
+      if (ok) issue_bf16<SECOND>(p, 1, ss, ring, rg, qu, tn, abort);
     }
     __syncwarp();
     if (elect_one()) umma_commit(&ss.drained);
@@ -1163,6 +1270,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
     drain_wait(&ss.drained, 0);
   } else {
     Ring rg;
+    Queue qu;
     Turn tn;
     uint32_t swap = 0;
     bool ok = true;
@@ -1172,24 +1280,24 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
         if (lane == 0) mbar_arrive(&ss.rows_done[which]);
       };
       if constexpr (Ge::Q4)
-        ok = rows_q4<G, FIRST>(p, 0, ss, ring, rg, tn, swap, abort);
+        ok = rows_q4<G, FIRST>(p, 0, ss, ring, rg, qu, tn, swap, abort);
       else
-        ok = rows_bf16<FIRST>(p, 0, ss, tn, abort);
+        ok = rows_bf16<FIRST>(p, 0, ss, qu, tn, abort);
       fence_proxy_async_global();  // hidden values, to other CTAs' copies
       through(0);
       if (ok) {
         if constexpr (Ge::Q4)
-          ok = rows_q4<G, SECOND>(p, 1, ss, ring, rg, tn, swap, abort);
+          ok = rows_q4<G, SECOND>(p, 1, ss, ring, rg, qu, tn, swap, abort);
         else
-          ok = rows_bf16<SECOND>(p, 1, ss, tn, abort);
+          ok = rows_bf16<SECOND>(p, 1, ss, qu, tn, abort);
       }
       through(1);
       if (ok && warp_wait(&ss.out_done, 0, abort, p.err, 0x2A << 24)) sum_rows(p, ss);
     } else {
       if constexpr (Ge::Q4)
-        rows_q4<G, SECOND>(p, 1, ss, ring, rg, tn, swap, abort);
+        rows_q4<G, SECOND>(p, 1, ss, ring, rg, qu, tn, swap, abort);
       else
-        rows_bf16<SECOND>(p, 1, ss, tn, abort);
+        rows_bf16<SECOND>(p, 1, ss, qu, tn, abort);
     }
   }
   tc_fence_before();
@@ -1201,7 +1309,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
   __syncthreads();
   if (ss.abort) {
     for (int i = tid; i < 2 * kMaxWorkers; i += kThreads) p.arrive[i] = 0;
-    if (tid < 4) p.err[kCtrHidden + tid] = 0;
+    if (tid < kCtrEnd - kCtrHidden) p.err[kCtrHidden + tid] = 0;
   }
 }
 
@@ -1331,6 +1439,8 @@ int decode_g(const DecodeArgs& a, cudaStream_t s) {
   p.parts = a.y_type == MOE_Y_F32 ? 3 : 2;
   p.p[0].block_log2 = Geo<G>::block_log2(1);
   p.p[1].block_log2 = Geo<G>::block_log2(p.parts);
+  p.p[0].kind = kGathered;
+  p.p[1].kind = kRowsOfH;
   if (!fill_product<G>(p.p[0], 0, a.W1, a.W3, mats, c.d_ff, c.d_model) ||
       !fill_product<G>(p.p[1], 1, a.W2, a.W2, mats, c.d_model, c.d_ff) ||
       !map2d(&p.p[0].cols, a.x, c.d_model, c.T, 64, 1) || !map2d(&p.p[1].cols, p.h, c.d_ff, p.parts * Rs, 64, 16))
@@ -1347,6 +1457,7 @@ int linear_g(const LinearArgs& a, cudaStream_t s) {
   common_params(p, a.ws, layout(0, 0, 0), a.T, a.y, a.y_type);
   p.n = a.n;
   p.p[1].block_log2 = Geo<G>::block_log2(1);
+  p.p[1].kind = kRowsOfX;
   if (!fill_product<G>(p.p[1], 1, a.W, a.W, 1, a.n, a.K) || !map2d(&p.p[1].cols, a.x, a.K, a.T, 64, 16))
     return MOE_ERR_CUDA;
   const size_t smem = ring_shape<G>(p, columns_of(p, 1, 1));
