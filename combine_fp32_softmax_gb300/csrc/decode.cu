@@ -82,7 +82,7 @@ constexpr int kCtrEnd = 14;
 // is on the way, beyond what its ring holds.  Memory then stays busy while the
 // hidden values of all CTAs come together, and the second product starts
 // from L2.
-constexpr int kPrefetchBlocks = 12;
+constexpr int kPrefetchBlocks = 6;
 
 // A stage: 128 bytes of 2 x 128 weight rows, the scales of those columns (4
 // bits) and the activation rows, 64 columns (128 bytes, swizzled) at a time.
@@ -469,7 +469,8 @@ struct Queue {
 };
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* err, int where) {
-  const bool ok = mbar_wait(bar, parity, abort, err, where);
+  if (__all_sync(kFull, mbar_try_wait(smem_u32(bar), parity))) return true;
+  const bool ok = mbar_wait_slow<false>(bar, parity, abort, err, where);
   return __all_sync(kFull, ok);
 }
 
@@ -1061,9 +1062,7 @@ struct RowsQ4 {
               uint32_t w[4], v[16];
               lds128(codes + ((((g0 + j) * (G / 32) + i) ^ (row & 7)) << 4), w);
 #pragma unroll
-              for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) v[t * 4 + q] = q4_pair(w[t], q);
+              for (int t = 0; t < 4; ++t) q4_pairs(w[t], *reinterpret_cast<uint32_t(*)[4]>(&v[4 * t]));
               tmem_st16(operand + j * (G / 2) + i * 16, v);
             }
           tmem_st_wait();
@@ -1089,7 +1088,7 @@ struct RowsQ4 {
     for (int b = 0; b < NC / 16; ++b) {
       uint32_t u[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(sum[b * 16 + i]);
+      for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(sum[b * 16 + i] * kQ4Unit);
       tmem_st16(operand_at(lanes, box, turn) + b * 16, u);
     }
     tmem_st_wait();

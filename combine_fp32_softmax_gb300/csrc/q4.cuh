@@ -30,6 +30,21 @@ __device__ __forceinline__ uint32_t q4_pair(uint32_t word, int i) {
   asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(v) : "r"(biased), "r"(0x3F803F80u), "r"(0xC308C308u));
   return v;
 }
+// The four pairs of a word as (q - 8) / 64, exact in bf16, with two integer
+// instructions less.  bf16 bit patterns below 256 are equidistant numbers,
+// pattern b being b 2^-133 (the subnormals and the first binade share their
+// step), so a nibble in bits 0-3 or 4-7 of a half is the number q or 16 q
+// times 2^-133 as it stands, and one exact fused multiply-add by 2^127 or
+// 2^123 brings it to its place.
+constexpr float kQ4Unit = 64.f;  // what the pairs have to be multiplied by
+__device__ __forceinline__ void q4_pairs(uint32_t word, uint32_t (&v)[4]) {
+  const uint32_t up = word >> 8;
+  const uint32_t m = 0x000F000Fu, bias = 0xBE00BE00u;  // -8 / 64
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(v[0]) : "r"(word & m), "r"(0x7F007F00u), "r"(bias));
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(v[1]) : "r"(word & (m << 4)), "r"(0x7D007D00u), "r"(bias));
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(v[2]) : "r"(up & m), "r"(0x7F007F00u), "r"(bias));
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(v[3]) : "r"(up & (m << 4)), "r"(0x7D007D00u), "r"(bias));
+}
 #endif
 
 }  // namespace moe
