@@ -79,9 +79,10 @@ constexpr int kCtrTicket = 12;  // tiles drawn, by product
 constexpr int kCtrEnd = 14;
 
 // K blocks of W2 that a CTA asks into L2 when its part of the first product
-// is on the way, beyond what its ring holds.  Memory then stays busy while the
-// hidden values of all CTAs come together, and the second product starts
-// from L2.
+// is on the way, beyond what its ring holds, where whole tiles are drawn.
+// Memory then stays busy while the hidden values of all CTAs come together:
+// 64 tokens of d=2048 f=1408 E=64 k=6 S=2 199 -> 197 us.  Cut tiles, whose
+// parts are on their way at that time, measured 3% slower with it.
 constexpr int kPrefetchBlocks = 6;
 
 // A stage: 128 bytes of 2 x 128 weight rows, the scales of those columns (4
@@ -126,7 +127,7 @@ struct StreamParams {
   uint16_t* h;          // [parts][Rs][f]
   float* o;             // [Rs][d]
   float* part;          // sums of the tiles that a range begins and ends in: [workers][2][2 boxes][64][128]
-  int* arrive;          // row warps that left theirs there, by the first range of the tile: [2][workers]
+  int* arrive;          // what has come in, by the first range of the tile: [2][workers]
   void* y;
   int* err;             // error word and counters
   int y_type, workers, stages, stage_bytes;
@@ -224,9 +225,7 @@ __device__ void make_plan(const StreamParams& p, int which, Shared& ss) {
   pl.per = ss.nblk[which];
   const int tiles = pl.per * pr.row_tiles, turns = tiles / p.workers, rest = tiles - turns * p.workers;
   pl.units = tiles * pr.kblocks;
-  // output rows whose weights were asked into L2 ahead stream at twice the memory's rate
-  const bool ahead = pr.kind == kRowsOfH && pl.units <= (kPrefetchBlocks + p.stages) * p.workers;
-  const int each = Q4 ? 4 : ahead ? 1 : 2;
+  const int each = Q4 ? 4 : 2;
   const int whole_time = Q4 ? 4 * pr.kblocks * (turns + (rest > 0))
                             : pr.kblocks * each * turns + (rest ? max(pr.kblocks, each * pr.kblocks * rest / p.workers) : 0);
   const int cut_time = each * (pl.units / p.workers) + kJoinUnits;
@@ -468,9 +467,13 @@ struct Queue {
   }
 };
 
+// A whole warp's wait.  INLINE: the first poll in the open, without a call,
+// where the warps' instructions are what bounds the kernel (4 bits, 3%); bf16
+// weights measured 4% faster without it.
+template <bool INLINE>
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* err, int where) {
-  if (__all_sync(kFull, mbar_try_wait(smem_u32(bar), parity))) return true;
-  const bool ok = mbar_wait_slow<false>(bar, parity, abort, err, where);
+  if (INLINE && __all_sync(kFull, mbar_try_wait(smem_u32(bar), parity))) return true;
+  const bool ok = mbar_wait(bar, parity, abort, err, where);
   return __all_sync(kFull, ok);
 }
 
@@ -508,7 +511,7 @@ struct Tiles {
       const Plan& pl = walk.pl;
       const int item = __shfl_sync(kFull, ticket, 0);
       t = item < pl.tiles ? locate(item) : make_int4(-1, 0, 0, 0);
-      if (!warp_wait(&ss.tile_empty[queue.slot], queue.phase ^ 1, abort, p.err, 0x2B << 24)) return false;
+      if (!warp_wait<false>(&ss.tile_empty[queue.slot], queue.phase ^ 1, abort, p.err, 0x2B << 24)) return false;
       if (lead) {
         ss.tile[queue.slot] = t;
         mbar_arrive(&ss.tile_full[queue.slot]);
@@ -516,7 +519,7 @@ struct Tiles {
         if (t.x >= 0) ticket = static_cast<int>(gridDim.x) + atomicAdd(p.err + kCtrTicket + which, 1);
       }
     } else {
-      if (!warp_wait(&ss.tile_full[queue.slot], queue.phase, abort, p.err, 0x2C << 24)) return false;
+      if (!warp_wait<false>(&ss.tile_full[queue.slot], queue.phase, abort, p.err, 0x2C << 24)) return false;
       t = ss.tile[queue.slot];
       __syncwarp();
       if (lead) mbar_arrive(&ss.tile_empty[queue.slot]);
@@ -594,24 +597,16 @@ __device__ bool produce_weights(const StreamParams& p, int which, Shared& ss, ui
   const Product& pr = p.p[which];
   Tiles<true> walk(p, which, ss, qu, abort);
   Segment s;
-  if (KIND == kRowsOfH) {
+  if (KIND == kRowsOfH && walk.walk.pl.drawn) {  // the tiles that the CTAs draw first
     int n = -p.stages;
-    auto ask = [&](int a, int rt, int kb0, int kb1) {
-      const int row = ss.e[a] * pr.rows + rt * pr.row_step;
-      for (int kb = kb0; kb < kb1 && n < kPrefetchBlocks; ++kb, ++n)
+    for (int item = blockIdx.x; item < walk.walk.pl.tiles && n < kPrefetchBlocks; item += gridDim.x) {
+      const int4 t = walk.locate(item);
+      const int row = ss.e[t.y] * pr.rows + t.z * pr.row_step;
+      for (int kb = 0; kb < pr.kblocks && n < kPrefetchBlocks; ++kb, ++n)
         if (n >= 0 && elect_one()) {
           tma_prefetch_2d(&pr.w0, kb * (Ge::Q4 ? 128 : 64), row);
           tma_prefetch_2d(&pr.w1, kb * (Ge::Q4 ? 128 : 64), row + kTileRows);
         }
-    };
-    if (walk.walk.pl.drawn) {  // the tiles that the CTAs draw first
-      for (int item = blockIdx.x; item < walk.walk.pl.tiles && n < kPrefetchBlocks; item += gridDim.x) {
-        const int4 t = walk.locate(item);
-        ask(t.y, t.z, 0, pr.kblocks);
-      }
-    } else {
-      Walk ahead(p, which, ss);
-      while (n < kPrefetchBlocks && ahead.next(s)) ask(s.a, s.rt, s.kb0, s.kb1);
     }
     __syncwarp();
   }
@@ -620,7 +615,7 @@ __device__ bool produce_weights(const StreamParams& p, int which, Shared& ss, ui
     const int beside = which == 0 ? 0 : kTileRows;  // W3 beside W1, or the tile's other rows
     [[maybe_unused]] const int scale_row = Ge::Q4 ? ss.e[s.a] * (pr.K / (Ge::Q4 ? G : 1)) : 0;
     for (int kb = s.kb0; kb < s.kb1; ++kb) {
-      if (!warp_wait(&ss.empty[rg.stage], rg.phase ^ 1, abort, p.err, (0x21 << 24) | which)) return false;
+      if (!warp_wait<Ge::Q4>(&ss.empty[rg.stage], rg.phase ^ 1, abort, p.err, (0x21 << 24) | which)) return false;
       uint8_t* st = ring + static_cast<size_t>(rg.stage) * p.stage_bytes;
       uint64_t* bar = &ss.full_w[rg.stage];
       dr.note(rg.stage, rg.phase);
@@ -659,7 +654,7 @@ __device__ bool produce_columns(const StreamParams& p, int which, Shared& ss, ui
     const int gathers = (c.m + 3) / 4;
     const uint32_t bytes = Ge::ATOMS * (KIND == kGathered ? gathers * 512 : c.n * 128);
     for (int kb = s.kb0; kb < s.kb1; ++kb) {
-      if (!warp_wait(&ss.empty[rg.stage], rg.phase ^ 1, abort, p.err, (0x22 << 24) | which)) return false;
+      if (!warp_wait<Ge::Q4>(&ss.empty[rg.stage], rg.phase ^ 1, abort, p.err, (0x22 << 24) | which)) return false;
       uint8_t* st = ring + static_cast<size_t>(rg.stage) * p.stage_bytes + Ge::WEIGHT_BYTES;
       uint64_t* bar = &ss.full_x[rg.stage];
       dr.note(rg.stage, rg.phase);
@@ -732,12 +727,12 @@ __device__ bool issue_bf16(const StreamParams& p, int which, Shared& ss, uint8_t
     const Columns<KIND> c(p, which, ss, s);
     const uint32_t idesc = idesc_bf16_f32(kTileRows, c.n, 0, 0);
     const uint32_t acc = ss.tmem + tn.buf * 2 * p.acc_cols;
-    if (!warp_wait(&ss.acc_empty[tn.buf], tn.phase ^ 1, abort, p.err, (0x31 << 24) | which)) return false;
+    if (!warp_wait<false>(&ss.acc_empty[tn.buf], tn.phase ^ 1, abort, p.err, (0x31 << 24) | which)) return false;
     for (int kb = s.kb0; kb < s.kb1; ++kb) {
       const uint32_t st = smem_u32(ring) + static_cast<uint32_t>(rg.stage) * p.stage_bytes;
       const uint32_t x = st + Geo<0>::WEIGHT_BYTES;
-      if (!warp_wait(&ss.full_x[rg.stage], rg.phase, abort, p.err, (0x24 << 24) | which)) return false;
-      if (!warp_wait(&ss.full_w[rg.stage], rg.phase, abort, p.err, (0x23 << 24) | which)) return false;
+      if (!warp_wait<false>(&ss.full_x[rg.stage], rg.phase, abort, p.err, (0x24 << 24) | which)) return false;
+      if (!warp_wait<false>(&ss.full_w[rg.stage], rg.phase, abort, p.err, (0x23 << 24) | which)) return false;
       tc_fence_after();
       if (elect_one()) {
 #pragma unroll
@@ -773,12 +768,12 @@ __device__ bool issue_q4(const StreamParams& p, int which, int box, Shared& ss, 
     const uint32_t atom = c.n * 128, tmem = ss.tmem;
     for (int kb = s.kb0; kb < s.kb1; ++kb) {
       const uint32_t x = smem_u32(ring) + static_cast<uint32_t>(rg.stage) * p.stage_bytes + Ge::WEIGHT_BYTES;
-      if (!warp_wait(&ss.full_x[rg.stage], rg.phase, abort, p.err, (0x24 << 24) | which)) return false;
+      if (!warp_wait<true>(&ss.full_x[rg.stage], rg.phase, abort, p.err, (0x24 << 24) | which)) return false;
       const int groups = stage_groups<G>(pr.K, kb);
       for (int g0 = 0; g0 < groups; g0 += tg) {
         const uint32_t a = operand_at(tmem, box, tn.buf), d = sums_at(tmem, box, tn.buf);
         const int n = min(tg, groups - g0);
-        if (!warp_wait(&ss.a_ready[box][tn.buf], tn.phase, abort, p.err, (0x32 << 24) | which)) return false;
+        if (!warp_wait<true>(&ss.a_ready[box][tn.buf], tn.phase, abort, p.err, (0x32 << 24) | which)) return false;
         tc_fence_after();
         if (elect_one()) {
           // 64 columns of the stage start `atom` bytes apart
@@ -858,9 +853,13 @@ __device__ __forceinline__ float* part_of(const StreamParams& p, int v, bool beg
 __device__ __forceinline__ int* arrivals_of(const StreamParams& p, int which, int v0) {
   return p.arrive + static_cast<size_t>(which) * kMaxWorkers + v0;
 }
-__device__ __forceinline__ void leave_part(const StreamParams& p, int which, const Share& sh) {
+// Counts a part in: a row warp's share of it (bf16), or all of it, by thread 0
+// after a barrier of the row warps that is there anyhow (4 bits; 4% of a call
+// at one token.  A barrier for this alone costs bf16 what it saves).
+template <bool WARPS>
+__device__ __forceinline__ void count_part(const StreamParams& p, int which, const Share& sh) {
   __syncwarp();
-  if ((threadIdx.x & 31) == 0) red_release_gpu_add(arrivals_of(p, which, sh.v0), 1);
+  if ((threadIdx.x & (WARPS ? 31 : ~0u)) == 0) red_release_gpu_add(arrivals_of(p, which, sh.v0), 1);
 }
 
 // A tile's finished column i, this thread's row of either box.
@@ -880,7 +879,7 @@ __device__ __forceinline__ void finish_column(const StreamParams& p, const Share
 // After the segments of a product: the cut tiles of this CTA's ranges, this
 // range's share of their columns (column i belongs to the i-th part, modulo
 // the parts), dealt to the sets of row warps.
-template <Kind KIND>
+template <Kind KIND, bool WARPS>
 __device__ bool join_parts(const StreamParams& p, int which, const Shared& ss, volatile int* abort) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int row = (warp & 3) * 32 + lane, set = warp >> 2;
@@ -895,7 +894,7 @@ __device__ bool join_parts(const StreamParams& p, int which, const Shared& ss, v
     const int first = s.worker - sh.v0 + set * parts;
     if (first >= c.m) continue;
     bool ok = true;
-    if (lane == 0) ok = wait_count(arrivals_of(p, which, sh.v0), parts * kRowWarps, abort, p.err, (0x29 << 24) | which);
+    if (lane == 0) ok = wait_count(arrivals_of(p, which, sh.v0), parts * (WARPS ? kRowWarps : 1), abort, p.err, (0x29 << 24) | which);
     if (!__shfl_sync(kFull, ok, 0)) return false;
     constexpr int C = 2, B = 4;  // columns and parts on the way at a time
     for (int i0 = first; i0 < c.m; i0 += C * step) {
@@ -970,7 +969,7 @@ __device__ bool rows_bf16(const StreamParams& p, int which, Shared& ss, Queue& q
   while (walk.next(s)) {
     const Columns<KIND> c(p, which, ss, s);
     const Share sh(walk.walk, s);
-    if (!warp_wait(&ss.acc_full[tn.buf], tn.phase, abort, p.err, (0x33 << 24) | which)) return false;
+    if (!warp_wait<false>(&ss.acc_full[tn.buf], tn.phase, abort, p.err, (0x33 << 24) | which)) return false;
     tc_fence_after();
     const uint32_t acc = ss.tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + tn.buf * 2 * p.acc_cols;
     finish_segment<KIND, KIND == kRowsOfH ? 3 : 1>(
@@ -992,9 +991,9 @@ __device__ bool rows_bf16(const StreamParams& p, int which, Shared& ss, Queue& q
     __syncwarp();
     if (lane == 0) mbar_arrive(&ss.acc_empty[tn.buf]);
     tn.step(p.acc_bufs);
-    if (!sh.whole) leave_part(p, which, sh);
+    if (!sh.whole) count_part<true>(p, which, sh);
   }
-  return join_parts<KIND>(p, which, ss, abort);
+  return join_parts<KIND, true>(p, which, ss, abort);
 }
 
 // 4-bit weights: set 2 box + t owns a box on every other turn, a thread one
@@ -1048,7 +1047,7 @@ struct RowsQ4 {
 #pragma unroll
     for (int i = 0; i < NC; ++i) sum[i] = 0.f;
     for (int kb = s.kb0; kb < s.kb1; ++kb) {
-      if (!warp_wait(&ss.full_w[rg.stage], rg.phase, abort, p.err, (0x23 << 24) | which)) return false;
+      if (!warp_wait<true>(&ss.full_w[rg.stage], rg.phase, abort, p.err, (0x23 << 24) | which)) return false;
       const uint32_t st = smem_u32(ring) + static_cast<uint32_t>(rg.stage) * p.stage_bytes;
       const uint32_t codes = st + box * kBoxBytes + row * 128;
       const uint32_t scales = st + 2 * kBoxBytes + box * Ge::SCALE_BYTES + row * 2;
@@ -1069,7 +1068,7 @@ struct RowsQ4 {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&ss.a_ready[box][turn]);
-          if (!warp_wait(&ss.d_full[box][turn], tn.phase, abort, p.err, (0x34 << 24) | which)) return false;
+          if (!warp_wait<true>(&ss.d_full[box][turn], tn.phase, abort, p.err, (0x34 << 24) | which)) return false;
           tc_fence_after();
           for (int j = 0; j < n; ++j)
             add_group(p, sums + j * c.n, c.n16, lds_bf16(scales + (g0 + j) * (kTileRows * 2)), sum);
@@ -1095,7 +1094,7 @@ struct RowsQ4 {
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&ss.swap_ready);
-    if (!warp_wait(&ss.swap_ready, swap, abort, p.err, (0x35 << 24) | which)) return false;
+    if (!warp_wait<true>(&ss.swap_ready, swap, abort, p.err, (0x35 << 24) | which)) return false;
     tc_fence_after();
     finish_segment<KIND, 2>(
         p, ss, s, sh, c,
@@ -1107,10 +1106,10 @@ struct RowsQ4 {
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&ss.swap_done);
-    if (!warp_wait(&ss.swap_done, swap, abort, p.err, (0x36 << 24) | which)) return false;
+    if (!warp_wait<true>(&ss.swap_done, swap, abort, p.err, (0x36 << 24) | which)) return false;
     swap ^= 1;
     tc_fence_after();
-    if (!sh.whole) leave_part(p, which, sh);
+    if (!sh.whole) count_part<false>(p, which, sh);  // swap_done: all row warps are here
     return true;
   }
 };
@@ -1128,7 +1127,7 @@ __device__ bool rows_q4(const StreamParams& p, int which, Shared& ss, uint8_t* r
     else
       ok = RowsQ4<G, KIND == kRowsOfH ? 16 : 32, KIND>::segment(p, which, ss, ring, walk.walk, s, rg, tn, swap, abort);
   }
-  return ok && join_parts<KIND>(p, which, ss, abort);
+  return ok && join_parts<KIND, false>(p, which, ss, abort);
 }
 
 // y[t] = its slots' rows in slot order, then the shared experts', in fp32.
@@ -1232,7 +1231,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
     // poller per warp the counter's L2 slice was so busy that the last
     // arrivals came through 8 us late.)
     auto meet = [&](int which) {
-      bool ok = warp_wait(&ss.rows_done[which], 0, abort, p.err, (0x25 << 24) | which);
+      bool ok = warp_wait<Ge::Q4>(&ss.rows_done[which], 0, abort, p.err, (0x25 << 24) | which);
       if (lane == 0) {
         // after a wait that gave up too, so that the other CTAs go on (the error word is set by then)
         red_release_gpu_add(p.err + kCtrHidden + which, 1);
@@ -1271,7 +1270,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
     Ring rg;
     Queue qu;
     Turn tn;
-    uint32_t swap = 0;
+    [[maybe_unused]] uint32_t swap = 0;
     bool ok = true;
     if (LAYER) {
       auto through = [&](int which) {  // after a wait that gave up as well
@@ -1291,7 +1290,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
           ok = rows_bf16<SECOND>(p, 1, ss, qu, tn, abort);
       }
       through(1);
-      if (ok && warp_wait(&ss.out_done, 0, abort, p.err, 0x2A << 24)) sum_rows(p, ss);
+      if (ok && warp_wait<Ge::Q4>(&ss.out_done, 0, abort, p.err, 0x2A << 24)) sum_rows(p, ss);
     } else {
       if constexpr (Ge::Q4)
         rows_q4<G, SECOND>(p, 1, ss, ring, rg, qu, tn, swap, abort);
