@@ -30,6 +30,19 @@
 //     leaves its sums in the workspace and, once through its range, adds up
 //     all of them, in range order, for its share of the tile's columns: no
 //     floating-point atomics, and nobody waits in the middle of a range.
+//     Where whole tiles are as fast, they are dealt or drawn whole.
+//
+// What it measures (a call in a graph; GB/s are of the bytes that have to be
+// moved, the copy rate is 6790):
+//   d=2048 f=1408 E=64 k=6 S=2, bf16: 1 token 39.1 us, 3540 GB/s; 64 tokens
+//     197 us, 5780 GB/s (7100 while it streams).  At one token the work itself
+//     takes 22 us; the rest is a chain of latencies: launch, router (4 us),
+//     first tile, two grid-wide meetings, the joining of cut tiles.
+//   The same in 4 bits: 1 token 30.5 us; d=4096 f=14336 E=8 k=2, 16 tokens
+//     214 us, 3490 GB/s: turning codes, 1150 of the 1360 clocks that an SM
+//     spends on a K block, is what bounds it.
+//   Linear form: 37 rows x 4097 x 4096 bf16 17 us, 1 row x 14336 x 4096 in 4
+//     bits 15.5 us.
 #include <cuda_runtime.h>
 
 #include <algorithm>

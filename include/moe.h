@@ -313,8 +313,13 @@ enum { MOE_Y_F32 = 0, MOE_Y_BF16 = 1 }; /* type of y */
 
 /* Workspace of moe_decode_fwd and moe_decode_q4_fwd (0 if cfg is outside their
  * limits: those of moe_cfg and T <= MOE_DECODE_MAX_T).  Clear it once
- * with moe_decode_ws_init; the calls leave its counters at 0.  Calls sharing a workspace must not run
- * concurrently. */
+ * with moe_decode_ws_init; a call leaves its counters at 0, except one that
+ * ended with MOE_ERR_TIMEOUT (a wait inside ran out): clear the workspace
+ * again after that.  Calls sharing a workspace must not run concurrently.
+ * Each call of this section is one launch on `stream` (a cooperative one, on
+ * all SMs or moe_set_grid_limit's number of CTAs, so work on other streams
+ * may run beside it but should not hold SMs for long) and may be captured
+ * into a CUDA graph. */
 size_t moe_decode_workspace_bytes(const moe_cfg* cfg);
 int moe_decode_ws_init(const moe_cfg* cfg, void* ws, void* stream);
 
@@ -324,7 +329,8 @@ int moe_decode_ws_init(const moe_cfg* cfg, void* ws, void* stream);
  *   y[t]    = sum_j h[t, j] . W2_e^T + sum_s h[t, s] . W2_(E+s)^T
  * (shared experts with weight 1).  Layouts as moe_layer_fwd.  All sums are
  * fp32; h enters the second product as the sum of two bf16 values (16
- * significant bits); y [T, d] is rounded once to y_type.  Only the weights of
+ * significant bits) for a bf16 y and of three (24 bits) for an fp32 y; y
+ * [T, d] is rounded once to y_type.  Only the weights of
  * experts that some token picked (and of the shared experts) are read.  A
  * non-finite logit sets MOE_ERR_NONFINITE, as in moe_route, and leaves that
  * token's outputs unspecified.  Bitwise reproducible.  Pointers 16-byte
