@@ -167,7 +167,7 @@ struct Plan {
 struct alignas(16) Shared {
   uint64_t full_w[kMaxStages], full_x[kMaxStages], empty[kMaxStages];
   uint64_t acc_full[2], acc_empty[2];   // bf16: accumulator pairs
-  uint64_t a_ready[2][2], d_full[2][2]; // 4 bits: [box][turn]
+  uint64_t a_ready[2][2], d_full[2][2]; // 4 bits: [box][set]
   uint64_t swap_ready, swap_done;       // 4 bits: all sums of a tile in tensor memory
   uint64_t rows_done[2];                // this CTA's row warps are through a product: a barrier for each, as the
                                         // second may be over (no work) before anyone looked at the first
@@ -713,16 +713,22 @@ struct Turn {
   }
 };
 
-// 4 bits: a turn is as many groups of a stage as fit the operand buffer and
-// the accumulators.
+// 4 bits: what the row warps hand the tensor core at a time is 64 columns of a
+// box: a group, two, or half of one.  One group of 32 if the sums of two would
+// not fit the accumulators.  A set takes every other one (128: group).
+constexpr int kChunk = 32;  // columns of 16 bytes of codes
 template <int G>
-__device__ __forceinline__ int turn_groups(int columns) {
-  return max(1, min(kOperandCols * 2 / G, kSumCols / columns));
+__device__ __forceinline__ int push_chunks(int columns) {
+  return G == 32 && 2 * columns > kSumCols ? 1 : 2;
 }
-// Groups of a stage that lie inside K.
+// Chunks of a stage that lie inside K.
 template <int G>
-__device__ __forceinline__ int stage_groups(int K, int kb) {
-  return min(Geo<G>::KB, K - kb * Geo<G>::KB) / G;
+__device__ __forceinline__ int stage_chunks(int K, int kb) {
+  return min(Geo<G>::KB, K - kb * Geo<G>::KB) / kChunk;
+}
+template <int G>
+__device__ __forceinline__ bool ends_group(int chunk) {
+  return G < 128 || (chunk & 2);
 }
 __device__ __forceinline__ uint32_t operand_at(uint32_t tmem, int box, int turn) {
   return tmem + (box * 2 + turn) * kOperandCols;
@@ -777,31 +783,32 @@ __device__ bool issue_q4(const StreamParams& p, int which, int box, Shared& ss, 
   while (walk.next(s)) {
     const Columns<KIND> c(p, which, ss, s);
     const uint32_t idesc = idesc_bf16_f32(kTileRows, c.n, 0, 0);
-    const int tg = turn_groups<G>(c.n);
+    const int pc = push_chunks<G>(c.n);
     const uint32_t atom = c.n * 128, tmem = ss.tmem;
     for (int kb = s.kb0; kb < s.kb1; ++kb) {
       const uint32_t x = smem_u32(ring) + static_cast<uint32_t>(rg.stage) * p.stage_bytes + Ge::WEIGHT_BYTES;
       if (!warp_wait<true>(&ss.full_x[rg.stage], rg.phase, abort, p.err, (0x24 << 24) | which)) return false;
-      const int groups = stage_groups<G>(pr.K, kb);
-      for (int g0 = 0; g0 < groups; g0 += tg) {
-        const uint32_t a = operand_at(tmem, box, tn.buf), d = sums_at(tmem, box, tn.buf);
-        const int n = min(tg, groups - g0);
-        if (!warp_wait<true>(&ss.a_ready[box][tn.buf], tn.phase, abort, p.err, (0x32 << 24) | which)) return false;
+      const int chunks = stage_chunks<G>(pr.K, kb);
+      for (int ch = 0; ch < chunks; ch += pc) {
+        const int set = tn.buf;
+        const uint32_t turn = (tn.phase >> set) & 1;  // the set's buffer, and its barriers' phase
+        const uint32_t a = operand_at(tmem, box, set) + turn * (kOperandCols / 2), d = sums_at(tmem, box, set);
+        if (!warp_wait<true>(&ss.a_ready[box][set], turn, abort, p.err, (0x32 << 24) | which)) return false;
         tc_fence_after();
         if (elect_one()) {
           // 64 columns of the stage start `atom` bytes apart
-          for (int j = 0; j < n; ++j) {
-            const uint32_t xg = x + ((g0 + j) * G / 64) * atom + ((g0 + j) * G % 64) * 2;
+          const uint32_t xc = x + (ch / 2) * atom + (ch % 2) * 64;
 #pragma unroll
-            for (int i = 0; i < G / 16; ++i)
-              umma_bf16_ta(d + j * c.n, a + j * (G / 2) + i * 8,
-                           smem_desc_sw128(xg + (i / 4) * atom + (i % 4) * 32, 16, 1024), idesc, i != 0);
-          }
-          umma_commit(&ss.d_full[box][tn.buf]);
-          if (g0 + tg >= groups) umma_commit(&ss.empty[rg.stage]);
+          for (int i = 0; i < 4; ++i)
+            if (i < 2 * pc)
+              umma_bf16_ta(d + (G == 32 ? (i / 2) * c.n : 0), a + i * 8, smem_desc_sw128(xc + i * 32, 16, 1024), idesc,
+                           G == 32 ? i % 2 : i != 0 || (G == 128 && (ch & 2)));
+          umma_commit(&ss.d_full[box][set]);
+          if (ch + pc >= chunks) umma_commit(&ss.empty[rg.stage]);
         }
         __syncwarp();
-        tn.step(2);
+        tn.phase ^= 1u << set;
+        if (ends_group<G>(ch)) tn.buf ^= 1;
       }
       rg.step(p.stages);
     }
@@ -1009,10 +1016,10 @@ __device__ bool rows_bf16(const StreamParams& p, int which, Shared& ss, Queue& q
   return join_parts<KIND, true>(p, which, ss, abort);
 }
 
-// 4-bit weights: set 2 box + t owns a box on every other turn, a thread one
-// row of it.  On its turn the thread turns its row's codes into the operand,
-// waits for the tensor core and adds the groups' sums, scaled, to its own;
-// meanwhile the other set has its turn.
+// 4-bit weights: two sets share a box, a thread one row of it.  A thread turns
+// 64 of its row's codes into one of two operand buffers while the tensor core
+// multiplies those in the other, then adds the groups' sums, scaled, to its
+// own and hands the new operand over.
 template <int G, int NC, Kind KIND>
 struct RowsQ4 {
   using Ge = Geo<G>;
@@ -1050,49 +1057,60 @@ struct RowsQ4 {
                                  const Segment& s, Ring& rg, Turn& tn, uint32_t& swap, volatile int* abort) {
     const Product& pr = p.p[which];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int quad = warp & 3, box = warp >> 3, turn = (warp >> 2) & 1, row = quad * 32 + lane;
+    const int quad = warp & 3, box = warp >> 3, set = (warp >> 2) & 1, row = quad * 32 + lane;
     const uint32_t lanes = ss.tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const Columns<KIND> c(p, which, ss, s);
     const Share sh(walk, s);
-    const int tg = turn_groups<G>(c.n);
-    const uint32_t operand = operand_at(lanes, box, turn), sums = sums_at(lanes, box, turn);
-    float sum[NC];
+    const int pc = push_chunks<G>(c.n);
+    const uint32_t operand = operand_at(lanes, box, set), sums = sums_at(lanes, box, set);
+    float sum[NC], scale[2];
+    int left = -1;  // groups of the last push that are not added yet; -1: no push on its way
 #pragma unroll
     for (int i = 0; i < NC; ++i) sum[i] = 0.f;
+    auto take = [&]() {
+      if (left < 0) return true;
+      if (!warp_wait<true>(&ss.d_full[box][set], tn.phase ^ 1, abort, p.err, (0x34 << 24) | which)) return false;
+      tc_fence_after();
+#pragma unroll
+      for (int j = 0; j < (G == 32 ? 2 : 1); ++j)
+        if (j < left) add_group(p, sums + j * c.n, c.n16, scale[j], sum);
+      return true;
+    };
     for (int kb = s.kb0; kb < s.kb1; ++kb) {
       if (!warp_wait<true>(&ss.full_w[rg.stage], rg.phase, abort, p.err, (0x23 << 24) | which)) return false;
       const uint32_t st = smem_u32(ring) + static_cast<uint32_t>(rg.stage) * p.stage_bytes;
       const uint32_t codes = st + box * kBoxBytes + row * 128;
       const uint32_t scales = st + 2 * kBoxBytes + box * Ge::SCALE_BYTES + row * 2;
-      const int groups = stage_groups<G>(pr.K, kb);
-      for (int g0 = 0; g0 < groups; g0 += tg) {
-        if (tn.buf == turn) {
-          const int n = min(tg, groups - g0);
-          for (int j = 0; j < n; ++j)
+      const int chunks = stage_chunks<G>(pr.K, kb);
+#pragma unroll 1
+      for (int ch = 0; ch < chunks; ch += pc) {
+        if (tn.buf == set) {
 #pragma unroll
-            for (int i = 0; i < G / 32; ++i) {
+          for (int j = 0; j < 2; ++j)
+            if (j < pc) {
               uint32_t w[4], v[16];
-              lds128(codes + ((((g0 + j) * (G / 32) + i) ^ (row & 7)) << 4), w);
+              lds128(codes + (((ch + j) ^ (row & 7)) << 4), w);
 #pragma unroll
               for (int t = 0; t < 4; ++t) q4_pairs(w[t], *reinterpret_cast<uint32_t(*)[4]>(&v[4 * t]));
-              tmem_st16(operand + j * (G / 2) + i * 16, v);
+              tmem_st16(operand + tn.phase * (kOperandCols / 2) + j * 16, v);
             }
+          if (!take()) return false;
+          left = ends_group<G>(ch) ? (G == 32 ? pc : 1) : 0;
+          scale[0] = lds_bf16(scales + (ch * kChunk / G) * (kTileRows * 2));
+          if (G == 32 && pc == 2) scale[1] = lds_bf16(scales + (ch + 1) * (kTileRows * 2));
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&ss.a_ready[box][turn]);
-          if (!warp_wait<true>(&ss.d_full[box][turn], tn.phase, abort, p.err, (0x34 << 24) | which)) return false;
-          tc_fence_after();
-          for (int j = 0; j < n; ++j)
-            add_group(p, sums + j * c.n, c.n16, lds_bf16(scales + (g0 + j) * (kTileRows * 2)), sum);
-          tc_fence_before();
+          if (lane == 0) mbar_arrive(&ss.a_ready[box][set]);
+          tn.phase ^= 1;
         }
-        tn.step(2);
+        if (ends_group<G>(ch)) tn.buf ^= 1;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&ss.empty[rg.stage]);
       rg.step(p.stages);
     }
+    if (!take()) return false;
     // All sums of the tile meet in tensor memory, in the sets' operand
     // buffers: both boxes' and both turns'.  No set goes on before all have
     // read their share.
@@ -1101,7 +1119,7 @@ struct RowsQ4 {
       uint32_t u[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(sum[b * 16 + i] * kQ4Unit);
-      tmem_st16(operand_at(lanes, box, turn) + b * 16, u);
+      tmem_st16(operand + b * 16, u);
     }
     tmem_st_wait();
     tc_fence_before();
