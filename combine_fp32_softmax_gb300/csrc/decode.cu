@@ -167,7 +167,7 @@ struct Plan {
 struct alignas(16) Shared {
   uint64_t full_w[kMaxStages], full_x[kMaxStages], empty[kMaxStages];
   uint64_t acc_full[2], acc_empty[2];   // bf16: accumulator pairs
-  uint64_t a_ready[2][2], d_full[2][2]; // 4 bits: [box][set]
+  uint64_t a_ready[2], d_full[2];       // 4 bits: by box
   uint64_t swap_ready, swap_done;       // 4 bits: all sums of a tile in tensor memory
   uint64_t rows_done[2];                // this CTA's row warps are through a product: a barrier for each, as the
                                         // second may be over (no work) before anyone looked at the first
@@ -713,23 +713,24 @@ struct Turn {
   }
 };
 
-// 4 bits: what the row warps hand the tensor core at a time is 64 columns of a
-// box: a group, two, or half of one.  One group of 32 if the sums of two would
-// not fit the accumulators.  A set takes every other one (128: group).
+// 4 bits: both sets of a box hand the tensor core 64 columns each at a time
+// (a push): a group, two, or half of one.  32 if two groups' sums would not
+// fit the accumulators.  A push costs the issuing warp some 450 clocks beside
+// four busy warps, as much as its instructions take: with a push for each set
+// that warp was what bounded the kernel (d=4096 f=14336 E=8 k=2, 16 tokens).
 constexpr int kChunk = 32;  // columns of 16 bytes of codes
 template <int G>
-__device__ __forceinline__ int push_chunks(int columns) {
-  return G == 32 && 2 * columns > kSumCols ? 1 : 2;
-}
-// Chunks of a stage that lie inside K.
-template <int G>
-__device__ __forceinline__ int stage_chunks(int K, int kb) {
-  return min(Geo<G>::KB, K - kb * Geo<G>::KB) / kChunk;
-}
-template <int G>
-__device__ __forceinline__ bool ends_group(int chunk) {
-  return G < 128 || (chunk & 2);
-}
+struct Push {
+  int size, chunks, count;  // chunks of a set's push, chunks of the stage that lie inside K, pushes
+  __device__ Push(int columns, int K, int kb) {
+    size = G == 32 && 2 * columns > kSumCols ? 1 : 2;
+    chunks = min(Geo<G>::KB, K - kb * Geo<G>::KB) / kChunk;
+    count = G == 128 ? 2 : (chunks / size + 1) / 2;
+  }
+  // First chunk of a set's i-th push; none if it lies behind the last.  A
+  // group is one set's.
+  __device__ int at(int i, int set) const { return G == 128 ? set * 4 + i * 2 : (2 * i + set) * size; }
+};
 __device__ __forceinline__ uint32_t operand_at(uint32_t tmem, int box, int turn) {
   return tmem + (box * 2 + turn) * kOperandCols;
 }
@@ -783,32 +784,32 @@ __device__ bool issue_q4(const StreamParams& p, int which, int box, Shared& ss, 
   while (walk.next(s)) {
     const Columns<KIND> c(p, which, ss, s);
     const uint32_t idesc = idesc_bf16_f32(kTileRows, c.n, 0, 0);
-    const int pc = push_chunks<G>(c.n);
     const uint32_t atom = c.n * 128, tmem = ss.tmem;
     for (int kb = s.kb0; kb < s.kb1; ++kb) {
       const uint32_t x = smem_u32(ring) + static_cast<uint32_t>(rg.stage) * p.stage_bytes + Ge::WEIGHT_BYTES;
       if (!warp_wait<true>(&ss.full_x[rg.stage], rg.phase, abort, p.err, (0x24 << 24) | which)) return false;
-      const int chunks = stage_chunks<G>(pr.K, kb);
-      for (int ch = 0; ch < chunks; ch += pc) {
-        const int set = tn.buf;
-        const uint32_t turn = (tn.phase >> set) & 1;  // the set's buffer, and its barriers' phase
-        const uint32_t a = operand_at(tmem, box, set) + turn * (kOperandCols / 2), d = sums_at(tmem, box, set);
-        if (!warp_wait<true>(&ss.a_ready[box][set], turn, abort, p.err, (0x32 << 24) | which)) return false;
+      const Push<G> push(c.n, pr.K, kb);
+      for (int j = 0; j < push.count; ++j) {
+        if (!warp_wait<true>(&ss.a_ready[box], tn.phase, abort, p.err, (0x32 << 24) | which)) return false;
         tc_fence_after();
         if (elect_one()) {
-          // 64 columns of the stage start `atom` bytes apart
-          const uint32_t xc = x + (ch / 2) * atom + (ch % 2) * 64;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i < 2 * pc)
-              umma_bf16_ta(d + (G == 32 ? (i / 2) * c.n : 0), a + i * 8, smem_desc_sw128(xc + i * 32, 16, 1024), idesc,
-                           G == 32 ? i % 2 : i != 0 || (G == 128 && (ch & 2)));
-          umma_commit(&ss.d_full[box][set]);
-          if (ch + pc >= chunks) umma_commit(&ss.empty[rg.stage]);
+          for (int set = 0; set < 2; ++set) {
+            const int ch = push.at(j, set);
+            if (ch >= push.chunks) continue;
+            const uint32_t a = operand_at(tmem, box, set) + tn.phase * (kOperandCols / 2), d = sums_at(tmem, box, set);
+            const uint32_t xc = x + (ch / 2) * atom + (ch % 2) * 64;  // 64 columns of the stage start `atom` bytes apart
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (G != 32 || i < 2 * push.size)
+                umma_bf16_ta(d + (G == 32 ? (i / 2) * c.n : 0), a + i * 8, smem_desc_sw128(xc + i * 32, 16, 1024), idesc,
+                             G == 32 ? i % 2 : i != 0 || (G == 128 && j));
+          }
+          umma_commit(&ss.d_full[box]);
+          if (j == push.count - 1) umma_commit(&ss.empty[rg.stage]);
         }
         __syncwarp();
-        tn.phase ^= 1u << set;
-        if (ends_group<G>(ch)) tn.buf ^= 1;
+        tn.phase ^= 1;
       }
       rg.step(p.stages);
     }
@@ -1061,7 +1062,6 @@ struct RowsQ4 {
     const uint32_t lanes = ss.tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const Columns<KIND> c(p, which, ss, s);
     const Share sh(walk, s);
-    const int pc = push_chunks<G>(c.n);
     const uint32_t operand = operand_at(lanes, box, set), sums = sums_at(lanes, box, set);
     float sum[NC], scale[2];
     int left = -1;  // groups of the last push that are not added yet; -1: no push on its way
@@ -1069,7 +1069,7 @@ struct RowsQ4 {
     for (int i = 0; i < NC; ++i) sum[i] = 0.f;
     auto take = [&]() {
       if (left < 0) return true;
-      if (!warp_wait<true>(&ss.d_full[box][set], tn.phase ^ 1, abort, p.err, (0x34 << 24) | which)) return false;
+      if (!warp_wait<true>(&ss.d_full[box], tn.phase ^ 1, abort, p.err, (0x34 << 24) | which)) return false;
       tc_fence_after();
 #pragma unroll
       for (int j = 0; j < (G == 32 ? 2 : 1); ++j)
@@ -1081,30 +1081,34 @@ struct RowsQ4 {
       const uint32_t st = smem_u32(ring) + static_cast<uint32_t>(rg.stage) * p.stage_bytes;
       const uint32_t codes = st + box * kBoxBytes + row * 128;
       const uint32_t scales = st + 2 * kBoxBytes + box * Ge::SCALE_BYTES + row * 2;
-      const int chunks = stage_chunks<G>(pr.K, kb);
+      const Push<G> push(c.n, pr.K, kb);
 #pragma unroll 1
-      for (int ch = 0; ch < chunks; ch += pc) {
-        if (tn.buf == set) {
+      for (int i = 0; i < push.count; ++i) {
+        const int ch = push.at(i, set);
+        const bool some = ch < push.chunks;
+        if (some) {
 #pragma unroll
           for (int j = 0; j < 2; ++j)
-            if (j < pc) {
+            if (G != 32 || j < push.size) {
               uint32_t w[4], v[16];
               lds128(codes + (((ch + j) ^ (row & 7)) << 4), w);
 #pragma unroll
               for (int t = 0; t < 4; ++t) q4_pairs(w[t], *reinterpret_cast<uint32_t(*)[4]>(&v[4 * t]));
               tmem_st16(operand + tn.phase * (kOperandCols / 2) + j * 16, v);
             }
-          if (!take()) return false;
-          left = ends_group<G>(ch) ? (G == 32 ? pc : 1) : 0;
-          scale[0] = lds_bf16(scales + (ch * kChunk / G) * (kTileRows * 2));
-          if (G == 32 && pc == 2) scale[1] = lds_bf16(scales + (ch + 1) * (kTileRows * 2));
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ss.a_ready[box][set]);
-          tn.phase ^= 1;
         }
-        if (ends_group<G>(ch)) tn.buf ^= 1;
+        if (!take()) return false;
+        left = 0;
+        if (some && (G != 128 || i)) {
+          left = G == 32 ? push.size : 1;
+          scale[0] = lds_bf16(scales + (ch * kChunk / G) * (kTileRows * 2));
+          if (G == 32 && left == 2) scale[1] = lds_bf16(scales + (ch + 1) * (kTileRows * 2));
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ss.a_ready[box]);
+        tn.phase ^= 1;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&ss.empty[rg.stage]);
@@ -1206,15 +1210,13 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
       mbar_init(&ss.full_w[lane], 1);
       mbar_init(&ss.full_x[lane], 1);
       mbar_init(&ss.empty[lane], Ge::Q4 ? kRowWarps + 2 : 1);
-    } else if (lane >= 16 && lane < 20) {
-      const int i = lane & 1, j = (lane >> 1) & 1;
-      mbar_init(&ss.a_ready[i][j], 4);
-      mbar_init(&ss.d_full[i][j], 1);
-      if (j == 0) {
-        mbar_init(&ss.acc_full[i], 1);
-        mbar_init(&ss.acc_empty[i], kRowWarps);
-        mbar_init(&ss.rows_done[i], kRowWarps);
-      }
+    } else if (lane >= 16 && lane < 18) {
+      const int i = lane & 1;
+      mbar_init(&ss.a_ready[i], kRowWarps / 2);
+      mbar_init(&ss.d_full[i], 1);
+      mbar_init(&ss.acc_full[i], 1);
+      mbar_init(&ss.acc_empty[i], kRowWarps);
+      mbar_init(&ss.rows_done[i], kRowWarps);
     } else if (lane >= 24 && lane < 24 + kTileSlots) {
       mbar_init(&ss.tile_full[lane - 24], 1);
       // readers: row warps, columns, one issuer (bf16) or two
