@@ -70,10 +70,9 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kTileRows = 128;           // rows of one weight box: an accumulator's lanes
 constexpr int kBoxBytes = kTileRows * 128;
 constexpr int kTmemCols = 512;
-// 4 bits: an operand buffer (128 rows x 128 bf16) and accumulators for either
-// box and turn.
-constexpr int kOperandCols = 64;
-constexpr int kSumCols = 64;
+// 4 bits: tensor memory of one of two buffers of a set of row warps, operand
+// and sums.
+constexpr int kBufferCols = 64;
 constexpr int kMaxStages = 8;
 constexpr int kTileSlots = 4;            // drawn tiles on their way to the other roles
 constexpr int kMaxTokens = MOE_DECODE_MAX_T;
@@ -167,7 +166,7 @@ struct Plan {
 struct alignas(16) Shared {
   uint64_t full_w[kMaxStages], full_x[kMaxStages], empty[kMaxStages];
   uint64_t acc_full[2], acc_empty[2];   // bf16: accumulator pairs
-  uint64_t a_ready[2], d_full[2];       // 4 bits: by box
+  uint64_t a_ready[2][2], d_full[2][2]; // 4 bits: [box][buffer]
   uint64_t swap_ready, swap_done;       // 4 bits: all sums of a tile in tensor memory
   uint64_t rows_done[2];                // this CTA's row warps are through a product: a barrier for each, as the
                                         // second may be over (no work) before anyone looked at the first
@@ -700,10 +699,11 @@ __device__ bool produce_columns(const StreamParams& p, int which, Shared& ss, ui
 }
 
 // ----------------------------------------------------- tensor instructions
-// Position in a ring of buffers: bf16, accumulator pairs, one a segment; 4
-// bits, turns.
+// bf16: position in the ring of accumulator pairs, one a segment.  4 bits: the
+// buffers' phase, and which of them holds the sums of a group that fills a
+// stage.
 struct Turn {
-  int buf = 0;
+  int buf = 0, sums = 0;
   uint32_t phase = 0;
   __device__ __forceinline__ void step(int bufs) {
     if (++buf == bufs) {
@@ -713,29 +713,49 @@ struct Turn {
   }
 };
 
-// 4 bits: both sets of a box hand the tensor core 64 columns each at a time
-// (a push): a group, two, or half of one.  32 if two groups' sums would not
-// fit the accumulators.  A push costs the issuing warp some 450 clocks beside
-// four busy warps, as much as its instructions take: with a push for each set
-// that warp was what bounded the kernel (d=4096 f=14336 E=8 k=2, 16 tokens).
+// 4 bits: both sets of a box hand the tensor core 64 columns each at a time (a
+// push): a group, two, or a part of one; 32 where a buffer would not hold the
+// sums.  N16, PARTS: steps of 16 rows and their parts.  Pushes alternate
+// between two buffers, and every stage makes the same number of them (empty
+// ones behind K), so that everything about a push but its phase is known to
+// the compiler: worked out by the row warps, four to a scheduler, that took as
+// long as turning the codes.
 constexpr int kChunk = 32;  // columns of 16 bytes of codes
-template <int G>
+template <int G, int N16, int PARTS>
 struct Push {
-  int size, chunks, count;  // chunks of a set's push, chunks of the stage that lie inside K, pushes
-  __device__ Push(int columns, int K, int kb) {
-    size = G == 32 && 2 * columns > kSumCols ? 1 : 2;
-    chunks = min(Geo<G>::KB, K - kb * Geo<G>::KB) / kChunk;
-    count = G == 128 ? 2 : (chunks / size + 1) / 2;
+  static constexpr int N = 16 * N16 * PARTS;
+  static constexpr int GROUPS = G == 32 ? 2 : 1;                   // of a push of two chunks, at most
+  static constexpr int SIZE = 2 * (kChunk / 2) + GROUPS * N <= kBufferCols ? 2 : 1;  // chunks of a set's push
+  static constexpr int SLAB = G == 32 ? SIZE : G / kChunk;         // consecutive chunks that are one set's
+  static constexpr int EACH = SLAB / SIZE;                         // pushes of a slab
+  static constexpr int COUNT = Geo<G>::KB / kChunk / 2 / SIZE;     // pushes of a stage
+  static_assert(SIZE * (kChunk / 2) + (SIZE == 2 ? GROUPS : 1) * N <= kBufferCols, "tensor memory of a buffer");
+  // The first chunk of set 0's push j; set 1's is SLAB further on.
+  __host__ __device__ static constexpr int first(int j) { return j / EACH * 2 * SLAB + j % EACH * SIZE; }
+  __host__ __device__ static constexpr bool begins(int j) { return j % EACH == 0; }
+  __host__ __device__ static constexpr bool ends(int j) { return j % EACH == EACH - 1; }
+  __host__ __device__ static constexpr int buf(int j) { return j & 1; }
+  static __device__ uint32_t phase(const Turn& tn, int j) { return tn.phase ^ ((j >> 1) & 1); }
+  static __device__ int sums(const Turn& tn, int j) { return COUNT == EACH ? tn.sums : (j / EACH) & 1; }
+  static __device__ void stage_done(Turn& tn) {
+    if (COUNT == 2) tn.phase ^= 1;
+    tn.sums ^= 1;
   }
-  // First chunk of a set's i-th push; none if it lies behind the last.  A
-  // group is one set's.
-  __device__ int at(int i, int set) const { return G == 128 ? set * 4 + i * 2 : (2 * i + set) * size; }
+  static __device__ int chunks(int K, int kb) { return min(Geo<G>::KB, K - kb * Geo<G>::KB) / kChunk; }
 };
-__device__ __forceinline__ uint32_t operand_at(uint32_t tmem, int box, int turn) {
-  return tmem + (box * 2 + turn) * kOperandCols;
+// Calls f with the Push of a segment.
+template <int G, Kind KIND, typename F>
+__device__ __forceinline__ bool with_push(int n16, int parts, const F& f) {
+  if constexpr (KIND == kRowsOfH)  // at most 16 rows at a time
+    return parts == 3 ? f(Push<G, 1, 3>{}) : f(Push<G, 1, 2>{});
+  else
+    return n16 == 1 ? f(Push<G, 1, 1>{}) : f(Push<G, 2, 1>{});
 }
-__device__ __forceinline__ uint32_t sums_at(uint32_t tmem, int box, int turn) {
-  return tmem + 4 * kOperandCols + (box * 2 + turn) * kSumCols;
+__device__ __forceinline__ uint32_t operand_at(uint32_t tmem, int box, int set, int buf) {
+  return tmem + ((box * 2 + set) * 2 + buf) * kBufferCols;
+}
+__device__ __forceinline__ uint32_t sums_at(uint32_t tmem, int box, int set, int buf, int size) {
+  return operand_at(tmem, box, set, buf) + size * (kChunk / 2);
 }
 
 template <Kind KIND>
@@ -774,45 +794,53 @@ __device__ bool issue_bf16(const StreamParams& p, int which, Shared& ss, uint8_t
   return true;
 }
 
+template <int G, int N16, int PARTS>
+__device__ __forceinline__ bool issue_segment(Push<G, N16, PARTS>, const StreamParams& p, int which, int box, Shared& ss,
+                                              uint8_t* ring, const Segment& s, Ring& rg, Turn& tn, volatile int* abort) {
+  using Pu = Push<G, N16, PARTS>;
+  constexpr uint32_t idesc = idesc_bf16_f32(kTileRows, Pu::N, 0, 0);
+  constexpr uint32_t atom = Pu::N * 128;  // 64 columns of the stage start this many bytes apart
+  const uint32_t tmem = ss.tmem;
+  for (int kb = s.kb0; kb < s.kb1; ++kb) {
+    const uint32_t x = smem_u32(ring) + static_cast<uint32_t>(rg.stage) * p.stage_bytes + Geo<G>::WEIGHT_BYTES;
+    const uint64_t xd = smem_desc_sw128(x, 16, 1024);
+    const int chunks = Pu::chunks(p.p[which].K, kb);
+    if (!warp_wait<true>(&ss.full_x[rg.stage], rg.phase, abort, p.err, (0x24 << 24) | which)) return false;
+#pragma unroll
+    for (int j = 0; j < Pu::COUNT; ++j) {
+      if (!warp_wait<true>(&ss.a_ready[box][Pu::buf(j)], Pu::phase(tn, j), abort, p.err, (0x32 << 24) | which)) return false;
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int set = 0; set < 2; ++set) {
+          const int ch = Pu::first(j) + set * Pu::SLAB;
+          if (ch >= chunks) continue;
+          const uint32_t a = operand_at(tmem, box, set, Pu::buf(j)), d = sums_at(tmem, box, set, Pu::sums(tn, j), Pu::SIZE);
+#pragma unroll
+          for (int i = 0; i < 2 * Pu::SIZE; ++i)
+            umma_bf16_ta(d + (G == 32 ? (i / 2) * Pu::N : 0), a + i * 8, xd + (ch / 2 * atom + ch % 2 * 64 + i * 32) / 16,
+                         idesc, G == 32 ? i % 2 : i != 0 || !Pu::begins(j));
+        }
+        umma_commit(&ss.d_full[box][Pu::buf(j)]);
+        if (j == Pu::COUNT - 1) umma_commit(&ss.empty[rg.stage]);
+      }
+      __syncwarp();
+    }
+    Pu::stage_done(tn);
+    rg.step(p.stages);
+  }
+  return true;
+}
+
 template <int G, Kind KIND>
 __device__ bool issue_q4(const StreamParams& p, int which, int box, Shared& ss, uint8_t* ring, Ring& rg, Queue& qu, Turn& tn,
                          volatile int* abort) {
-  using Ge = Geo<G>;
-  const Product& pr = p.p[which];
   Tiles<false> walk(p, which, ss, qu, abort);
   Segment s;
   while (walk.next(s)) {
     const Columns<KIND> c(p, which, ss, s);
-    const uint32_t idesc = idesc_bf16_f32(kTileRows, c.n, 0, 0);
-    const uint32_t atom = c.n * 128, tmem = ss.tmem;
-    for (int kb = s.kb0; kb < s.kb1; ++kb) {
-      const uint32_t x = smem_u32(ring) + static_cast<uint32_t>(rg.stage) * p.stage_bytes + Ge::WEIGHT_BYTES;
-      if (!warp_wait<true>(&ss.full_x[rg.stage], rg.phase, abort, p.err, (0x24 << 24) | which)) return false;
-      const Push<G> push(c.n, pr.K, kb);
-      for (int j = 0; j < push.count; ++j) {
-        if (!warp_wait<true>(&ss.a_ready[box], tn.phase, abort, p.err, (0x32 << 24) | which)) return false;
-        tc_fence_after();
-        if (elect_one()) {
-#pragma unroll
-          for (int set = 0; set < 2; ++set) {
-            const int ch = push.at(j, set);
-            if (ch >= push.chunks) continue;
-            const uint32_t a = operand_at(tmem, box, set) + tn.phase * (kOperandCols / 2), d = sums_at(tmem, box, set);
-            const uint32_t xc = x + (ch / 2) * atom + (ch % 2) * 64;  // 64 columns of the stage start `atom` bytes apart
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (G != 32 || i < 2 * push.size)
-                umma_bf16_ta(d + (G == 32 ? (i / 2) * c.n : 0), a + i * 8, smem_desc_sw128(xc + i * 32, 16, 1024), idesc,
-                             G == 32 ? i % 2 : i != 0 || (G == 128 && j));
-          }
-          umma_commit(&ss.d_full[box]);
-          if (j == push.count - 1) umma_commit(&ss.empty[rg.stage]);
-        }
-        __syncwarp();
-        tn.phase ^= 1;
-      }
-      rg.step(p.stages);
-    }
+    if (!with_push<G, KIND>(c.n16, p.parts, [&](auto push) { return issue_segment(push, p, which, box, ss, ring, s, rg, tn, abort); }))
+      return false;
   }
   return true;
 }
@@ -1018,103 +1046,107 @@ __device__ bool rows_bf16(const StreamParams& p, int which, Shared& ss, Queue& q
 }
 
 // 4-bit weights: two sets share a box, a thread one row of it.  A thread turns
-// 64 of its row's codes into one of two operand buffers while the tensor core
-// multiplies those in the other, then adds the groups' sums, scaled, to its
-// own and hands the new operand over.
-template <int G, int NC, Kind KIND>
+// 64 of its row's codes into one of two buffers in tensor memory and hands it
+// over, and adds, scaled, the sums of the groups that the push before ended.
+// The tensor core's way from a push to its sums (600 clocks) is as long as a
+// thread's from one push to the next.
+template <int G, int N16, int PARTS, Kind KIND>
 struct RowsQ4 {
   using Ge = Geo<G>;
-  // The parts of 16 rows of h lie n16 steps of 16 columns apart.
-  static __device__ __forceinline__ void add_group(const StreamParams& p, uint32_t acc, int n16, float scale,
-                                                   float (&sum)[NC]) {
+  using Pu = Push<G, N16, PARTS>;
+  static constexpr int NC = 16 * N16;
+  // The parts of 16 rows of h lie N16 steps of 16 columns apart.
+  static __device__ __forceinline__ void add_group(uint32_t acc, float scale, float (&sum)[NC]) {
 #pragma unroll
-    for (int b = 0; b < NC / 16; ++b) {
-      if (b >= n16) break;
-      uint32_t u[16];
+    for (int b = 0; b < N16; ++b) {
+      uint32_t u[16], lo[16];
       tmem_ld16(acc + b * 16, u);
-      if constexpr (KIND == kRowsOfH) {
-        uint32_t lo[16];
-        tmem_ld16(acc + (n16 + b) * 16, lo);
-        tmem_ld_wait();
-        if (p.parts == 3) {
-          uint32_t lo2[16];
-          tmem_ld16(acc + (2 * n16 + b) * 16, lo2);
-          tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) lo[i] = __float_as_uint(__uint_as_float(lo[i]) + __uint_as_float(lo2[i]));
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          sum[b * 16 + i] = fmaf(scale, fmaf(__uint_as_float(lo[i]), 1.f / kLowScale, __uint_as_float(u[i])), sum[b * 16 + i]);
-      } else {
+      if constexpr (PARTS > 1) tmem_ld16(acc + (N16 + b) * 16, lo);
+      tmem_ld_wait();
+      if constexpr (PARTS > 2) {
+        uint32_t lo2[16];
+        tmem_ld16(acc + (2 * N16 + b) * 16, lo2);
         tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) sum[b * 16 + i] = fmaf(scale, __uint_as_float(u[i]), sum[b * 16 + i]);
+        for (int i = 0; i < 16; ++i) lo[i] = __float_as_uint(__uint_as_float(lo[i]) + __uint_as_float(lo2[i]));
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        float v = __uint_as_float(u[i]);
+        if constexpr (PARTS > 1) v = fmaf(__uint_as_float(lo[i]), 1.f / kLowScale, v);
+        sum[b * 16 + i] = fmaf(scale, v, sum[b * 16 + i]);
       }
     }
   }
 
-  static __device__ bool segment(const StreamParams& p, int which, Shared& ss, uint8_t* ring, const Walk& walk,
-                                 const Segment& s, Ring& rg, Turn& tn, uint32_t& swap, volatile int* abort) {
-    const Product& pr = p.p[which];
+  static __device__ __forceinline__ bool segment(const StreamParams& p, int which, Shared& ss, uint8_t* ring,
+                                                 const Walk& walk, const Segment& s, Ring& rg, Turn& tn, uint32_t& swap,
+                                                 volatile int* abort) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int quad = warp & 3, box = warp >> 3, set = (warp >> 2) & 1, row = quad * 32 + lane;
     const uint32_t lanes = ss.tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const Columns<KIND> c(p, which, ss, s);
     const Share sh(walk, s);
-    const uint32_t operand = operand_at(lanes, box, set), sums = sums_at(lanes, box, set);
-    float sum[NC], scale[2];
-    int left = -1;  // groups of the last push that are not added yet; -1: no push on its way
+    const int K = p.p[which].K;
+    // A row's chunks are swizzled; chunk numbers of different j and set differ in different bits.
+    const uint32_t codes_at = box * kBoxBytes + row * 128 + (((set * Pu::SLAB) ^ (row & 7)) << 4);
+    const uint32_t scales_at = 2 * kBoxBytes + box * Ge::SCALE_BYTES + row * 2 + set * (G == 32 ? Pu::SIZE : 1) * (kTileRows * 2);
+    float sum[NC], scale[2] = {};
 #pragma unroll
     for (int i = 0; i < NC; ++i) sum[i] = 0.f;
-    auto take = [&]() {
-      if (left < 0) return true;
-      if (!warp_wait<true>(&ss.d_full[box], tn.phase ^ 1, abort, p.err, (0x34 << 24) | which)) return false;
+    int before = -1;  // whether the last stage's last push had codes; -1: there was none
+    // Adds what push j ended; `tn` is at its stage.
+    auto take = [&](int j, uint32_t phase, int sums, bool some) {
+      if (!warp_wait<true>(&ss.d_full[box][Pu::buf(j)], phase, abort, p.err, (0x34 << 24) | which)) return false;
       tc_fence_after();
-#pragma unroll
-      for (int j = 0; j < (G == 32 ? 2 : 1); ++j)
-        if (j < left) add_group(p, sums + j * c.n, c.n16, scale[j], sum);
+      if (Pu::ends(j) && some) {
+        const uint32_t at = sums_at(lanes, box, set, sums, Pu::SIZE);
+        add_group(at, scale[0], sum);
+        if (G == 32 && Pu::SIZE == 2) add_group(at + Pu::N, scale[1], sum);
+      }
       return true;
     };
     for (int kb = s.kb0; kb < s.kb1; ++kb) {
-      if (!warp_wait<true>(&ss.full_w[rg.stage], rg.phase, abort, p.err, (0x23 << 24) | which)) return false;
       const uint32_t st = smem_u32(ring) + static_cast<uint32_t>(rg.stage) * p.stage_bytes;
-      const uint32_t codes = st + box * kBoxBytes + row * 128;
-      const uint32_t scales = st + 2 * kBoxBytes + box * Ge::SCALE_BYTES + row * 2;
-      const Push<G> push(c.n, pr.K, kb);
-#pragma unroll 1
-      for (int i = 0; i < push.count; ++i) {
-        const int ch = push.at(i, set);
-        const bool some = ch < push.chunks;
+      const uint32_t codes = st + codes_at, scales = st + scales_at;
+      const int chunks = Pu::chunks(K, kb) - set * Pu::SLAB;
+      if (!warp_wait<true>(&ss.full_w[rg.stage], rg.phase, abort, p.err, (0x23 << 24) | which)) return false;
+#pragma unroll
+      for (int j = 0; j < Pu::COUNT; ++j) {
+        const bool some = Pu::first(j) < chunks;
         if (some) {
+          const uint32_t operand = operand_at(lanes, box, set, Pu::buf(j));
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-            if (G != 32 || j < push.size) {
-              uint32_t w[4], v[16];
-              lds128(codes + (((ch + j) ^ (row & 7)) << 4), w);
+          for (int i = 0; i < Pu::SIZE; ++i) {
+            uint32_t w[4], v[16];
+            lds128(codes ^ ((Pu::first(j) + i) << 4), w);
 #pragma unroll
-              for (int t = 0; t < 4; ++t) q4_pairs(w[t], *reinterpret_cast<uint32_t(*)[4]>(&v[4 * t]));
-              tmem_st16(operand + tn.phase * (kOperandCols / 2) + j * 16, v);
-            }
+            for (int t = 0; t < 4; ++t) q4_pairs(w[t], *reinterpret_cast<uint32_t(*)[4]>(&v[4 * t]));
+            tmem_st16(operand + i * (kChunk / 2), v);
+          }
+          tmem_st_wait();
         }
-        if (!take()) return false;
-        left = 0;
-        if (some && (G != 128 || i)) {
-          left = G == 32 ? push.size : 1;
-          scale[0] = lds_bf16(scales + (ch * kChunk / G) * (kTileRows * 2));
-          if (G == 32 && left == 2) scale[1] = lds_bf16(scales + (ch + 1) * (kTileRows * 2));
-        }
-        tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ss.a_ready[box]);
-        tn.phase ^= 1;
+        if (lane == 0) mbar_arrive(&ss.a_ready[box][Pu::buf(j)]);
+        if (j > 0) {
+          if (!take(j - 1, Pu::phase(tn, j - 1), Pu::sums(tn, j - 1), Pu::first(j - 1) < chunks)) return false;
+        } else if (before >= 0) {
+          if (!take(Pu::COUNT - 1, tn.phase ^ 1, Pu::COUNT == Pu::EACH ? tn.sums ^ 1 : 1, before)) return false;
+        }
+        if (Pu::ends(j) && some) {
+          constexpr int step = kTileRows * 2;
+          scale[0] = lds_bf16(scales + (G == 32 ? Pu::first(j) : j / Pu::EACH * 2) * step);
+          if (G == 32 && Pu::SIZE == 2) scale[1] = lds_bf16(scales + (Pu::first(j) + 1) * step);
+        }
       }
+      before = Pu::first(Pu::COUNT - 1) < chunks;
+      Pu::stage_done(tn);
       __syncwarp();
       if (lane == 0) mbar_arrive(&ss.empty[rg.stage]);
       rg.step(p.stages);
     }
-    if (!take()) return false;
+    if (!take(Pu::COUNT - 1, tn.phase ^ 1, Pu::COUNT == Pu::EACH ? tn.sums ^ 1 : 1, before)) return false;
     // All sums of the tile meet in tensor memory, in the sets' operand
     // buffers: both boxes' and both turns'.  No set goes on before all have
     // read their share.
@@ -1123,7 +1155,7 @@ struct RowsQ4 {
       uint32_t u[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(sum[b * 16 + i] * kQ4Unit);
-      tmem_st16(operand + b * 16, u);
+      tmem_st16(operand_at(lanes, box, set, 0) + b * 16, u);
     }
     tmem_st_wait();
     tc_fence_before();
@@ -1134,8 +1166,8 @@ struct RowsQ4 {
     finish_segment<KIND, 2>(
         p, ss, s, sh, c,
         [&](int bx, int at, uint32_t* u) {
-          u[0] = tmem_ld1(operand_at(lanes, bx, 0) + at);
-          u[1] = tmem_ld1(operand_at(lanes, bx, 1) + at);
+          u[0] = tmem_ld1(operand_at(lanes, bx, 0, 0) + at);
+          u[1] = tmem_ld1(operand_at(lanes, bx, 1, 0) + at);
         },
         [&](const uint32_t* u) { return __uint_as_float(u[0]) + __uint_as_float(u[1]); });
     tc_fence_before();
@@ -1149,19 +1181,21 @@ struct RowsQ4 {
   }
 };
 
+template <Kind KIND, int G, int N16, int PARTS, typename... Args>
+__device__ __forceinline__ bool rows_segment(Push<G, N16, PARTS>, Args&... args) {
+  return RowsQ4<G, N16, PARTS, KIND>::segment(args...);
+}
+
 template <int G, Kind KIND>
 __device__ bool rows_q4(const StreamParams& p, int which, Shared& ss, uint8_t* ring, Ring& rg, Queue& qu, Turn& tn, uint32_t& swap,
                         volatile int* abort) {
   Tiles<false> walk(p, which, ss, qu, abort);
   Segment s;
   bool ok = true;
-  while (ok && walk.next(s)) {
-    // rows of h come at most 16 at a time
-    if (KIND == kRowsOfH || Columns<KIND>(p, which, ss, s).n16 == 1)
-      ok = RowsQ4<G, 16, KIND>::segment(p, which, ss, ring, walk.walk, s, rg, tn, swap, abort);
-    else
-      ok = RowsQ4<G, KIND == kRowsOfH ? 16 : 32, KIND>::segment(p, which, ss, ring, walk.walk, s, rg, tn, swap, abort);
-  }
+  while (ok && walk.next(s))
+    ok = with_push<G, KIND>(Columns<KIND>(p, which, ss, s).n16, p.parts, [&](auto push) {
+      return rows_segment<KIND>(push, p, which, ss, ring, walk.walk, s, rg, tn, swap, abort);
+    });
   return ok && join_parts<KIND, false>(p, which, ss, abort);
 }
 
@@ -1212,8 +1246,10 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
       mbar_init(&ss.empty[lane], Ge::Q4 ? kRowWarps + 2 : 1);
     } else if (lane >= 16 && lane < 18) {
       const int i = lane & 1;
-      mbar_init(&ss.a_ready[i], kRowWarps / 2);
-      mbar_init(&ss.d_full[i], 1);
+      for (int j = 0; j < 2; ++j) {
+        mbar_init(&ss.a_ready[i][j], kRowWarps / 2);
+        mbar_init(&ss.d_full[i][j], 1);
+      }
       mbar_init(&ss.acc_full[i], 1);
       mbar_init(&ss.acc_empty[i], kRowWarps);
       mbar_init(&ss.rows_done[i], kRowWarps);
