@@ -22,8 +22,8 @@
 //     go to tensor memory, from where the instruction takes them: written
 //     back to shared memory they would need four times the codes' bandwidth
 //     there, twice.  Each group of columns is summed from zero and scaled in
-//     fp32 on its way out, so no weight is rounded.  Two sets of warps take
-//     turns: one turns codes while the other one's turn is multiplied.
+//     fp32 on its way out, so no weight is rounded.  Operand and sums are
+//     double-buffered: a warp turns codes while its last ones are multiplied.
 //   - The tiles of all picked experts form one sequence of K blocks, cut into
 //     equal contiguous ranges, one per SM, so no SM idles whatever the number
 //     of experts, rows and tokens.  Every range that works on a cut tile
@@ -38,11 +38,12 @@
 //     197 us, 5780 GB/s (7100 while it streams).  At one token the work itself
 //     takes 22 us; the rest is a chain of latencies: launch, router (4 us),
 //     first tile, two grid-wide meetings, the joining of cut tiles.
-//   The same in 4 bits: 1 token 30.5 us; d=4096 f=14336 E=8 k=2, 16 tokens
-//     214 us, 3490 GB/s: turning codes, 1150 of the 1360 clocks that an SM
-//     spends on a K block, is what bounds it.
+//   The same in 4 bits: 1 token 27.5 us; d=4096 f=14336 E=8 k=2, 16 tokens
+//     171 us, 4360 GB/s.  An SM spends some 1800 clocks on a K block of 32 KB,
+//     906 of them the least that turning its codes takes (measured alone: 5
+//     integer instructions at half rate and 4 multiply-adds a word).
 //   Linear form: 37 rows x 4097 x 4096 bf16 17 us, 1 row x 14336 x 4096 in 4
-//     bits 15.5 us.
+//     bits 14.1 us.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -216,9 +217,9 @@ __device__ bool wait_count(const int* c, int target, volatile int* abort, int* e
 // experts, which have the most rows to finish, are spread over the ranges.
 //
 // Whole tiles or cut ones.  In units of 0.37 us: with all SMs at work a K
-// block of 32 KB takes 2 of them (bf16: memory) or 4 (4 bits: turning codes);
+// block of 32 KB takes 2 of them (bf16: memory) or 3 (4 bits: turning codes);
 // an SM that has the memory to itself takes 1 for a bf16 block.  Putting cut
-// tiles together again costs 8 more (parts, count, wait, parts back).  Whole
+// tiles together again costs 12 more (parts, count, wait, parts back).  Whole
 // tiles take turns of all SMs and a last turn of the rest; one token's 88
 // tiles of W1 and W3 of the layer d=2048 f=1408 k=6 S=2 are faster whole on 88
 // SMs than cut for 152, 17 tiles of a 4097 x 4096 matrix are not.  No range of
@@ -228,7 +229,7 @@ __device__ bool wait_count(const int* c, int target, volatile int* abort, int* e
 // equal shares of the memory's rate (64 tokens of that layer: 160,000 clocks
 // for the first product on one SM, 246,000 on another with as many tiles).
 // A tile's sums do not depend on the CTA that makes them.
-constexpr int kMinBlocks = 3, kJoinUnits = 8;
+constexpr int kMinBlocks = 3, kJoinUnits = 12;
 
 template <bool Q4>
 __device__ void make_plan(const StreamParams& p, int which, Shared& ss) {
@@ -237,8 +238,8 @@ __device__ void make_plan(const StreamParams& p, int which, Shared& ss) {
   pl.per = ss.nblk[which];
   const int tiles = pl.per * pr.row_tiles, turns = tiles / p.workers, rest = tiles - turns * p.workers;
   pl.units = tiles * pr.kblocks;
-  const int each = Q4 ? 4 : 2;
-  const int whole_time = Q4 ? 4 * pr.kblocks * (turns + (rest > 0))
+  const int each = Q4 ? 3 : 2;
+  const int whole_time = Q4 ? 3 * pr.kblocks * (turns + (rest > 0))
                             : pr.kblocks * each * turns + (rest ? max(pr.kblocks, each * pr.kblocks * rest / p.workers) : 0);
   const int cut_time = each * (pl.units / p.workers) + kJoinUnits;
   const bool whole = whole_time <= cut_time;
