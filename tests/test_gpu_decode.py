@@ -385,3 +385,32 @@ def test_weights_beyond_two_to_the_31(group):
     p = math.exp(3) / (math.exp(3) + 255 * math.exp(-9))
     ref = small.reference()
     check_y("y", y, ref.y / ref.routing.w * p)
+
+
+# Widths that end 64, 128 or 192 columns into a stage of 256, experts with 1, 16, 17 and more than 32 rows.
+ENDS = [MoEConfig("ends_64", 21, 320, 576, 3, 2, S=1), MoEConfig("ends_128", 40, 128, 640, 2, 1, S=1),
+        MoEConfig("ends_192", 17, 448, 192, 16, 3), MoEConfig("ends_0", 64, 512, 256, 24, 2, S=1, zipf=True)]
+
+
+@pytest.mark.parametrize("cfg", ENDS, ids=lambda c: c.name)
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_q4_layer_of_either_type_wherever_the_columns_end(cfg, dtype, group):
+    if group == 128:
+        cfg = cfg.with_(d=-(-cfg.d // 128) * 128, f=-(-cfg.f // 128) * 128)
+    _check(Layer(cfg, group=group), dtype)
+
+
+@pytest.mark.parametrize("group", [32, 128])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_q4_hundreds_of_calls_in_a_row_of_either_type(group, dtype):
+    layer = Layer(MoEConfig("many", 37, 384, 640, 16, 4, S=1, zipf=True), group=group)
+    ws, out = layer.workspace(), layer.outputs(dtype)
+    x, z = layer.x.to(DEV), layer.logits.to(DEV)
+    want = [t.clone() for t in layer.run(dtype, ws=ws, out=out, x=x, logits=z)[:3]]
+    for _ in range(4):
+        for _ in range(50):
+            layer.run(dtype, ws=ws, out=out, x=x, logits=z)
+        assert device_error(ws) == (0, 0)
+        for a, b in zip(out, want):
+            assert torch.equal(a, b)
