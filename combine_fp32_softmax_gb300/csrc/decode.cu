@@ -110,9 +110,12 @@ struct Geo {
   static constexpr int SCALE_BYTES = GROUPS * kTileRows * 2;   // of one box
   static constexpr int WEIGHT_BYTES = 2 * (kBoxBytes + SCALE_BYTES);
   // Activation rows of a tile, in `parts` parts.  bf16 weights: all of an
-  // expert's.  4 bits: what the accumulators and a thread hold; an
-  // expert with more rows has its weight tiles visited again, from L2.
-  static constexpr int block_log2(int parts) { return !Q4 ? 6 : parts == 1 ? 5 : 4; }
+  // expert's.  4 bits: what a buffer in tensor memory and a thread hold; an
+  // expert with more rows has its weight tiles visited again, from L2.  Groups
+  // of 32 come with half the pushes where rows are 16 at a time, so that two
+  // visits cost what one for 32 rows does and the ranges come out even (33
+  // tokens of d=4096 f=2048 E=128 k=8, skewed: 127 us against 147).
+  static constexpr int block_log2(int parts) { return !Q4 ? 6 : parts == 1 && G != 32 ? 5 : 4; }
 };
 
 // What the columns of a product are.
@@ -747,8 +750,10 @@ struct Push {
 // Calls f with the Push of a segment.
 template <int G, Kind KIND, typename F>
 __device__ __forceinline__ bool with_push(int n16, int parts, const F& f) {
-  if constexpr (KIND == kRowsOfH)  // at most 16 rows at a time
+  if constexpr (KIND == kRowsOfH)  // at most 16 rows at a time, as with groups of 32
     return parts == 3 ? f(Push<G, 1, 3>{}) : f(Push<G, 1, 2>{});
+  else if constexpr (G == 32)
+    return f(Push<G, 1, 1>{});
   else
     return n16 == 1 ? f(Push<G, 1, 1>{}) : f(Push<G, 2, 1>{});
 }
