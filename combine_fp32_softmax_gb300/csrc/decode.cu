@@ -71,6 +71,14 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kTileRows = 128;           // rows of one weight box: an accumulator's lanes
 constexpr int kBoxBytes = kTileRows * 128;
 constexpr int kTmemCols = 512;
+// bf16 weights: the tensor core cuts off what its running sum has no room for,
+// always towards zero, which over K = 3840 comes to 1e-5 of an output.  For an
+// fp32 y it adds up 2 K blocks (8 instructions) at a time, 4 where there are
+// no two pairs of accumulators, and the row warps add those sums, rounded to
+// nearest, in the last columns of tensor memory.  A bf16 y, off by 2^-9, needs
+// none of it.
+constexpr int kRunBlocks = 2;
+constexpr int kRunCols = 2 * MOE_DECODE_MAX_T;
 // 4 bits: tensor memory of one of two buffers of a set of row warps, operand
 // and sums.
 constexpr int kBufferCols = 64;
@@ -149,6 +157,7 @@ struct StreamParams {
   int y_type, workers, stages, stage_bytes;
   int parts;            // bf16 parts of a hidden value
   int acc_cols, acc_bufs;  // bf16 weights: columns of an accumulator, accumulator pairs
+  int run;                 // bf16 weights: K blocks that the tensor core adds up at a time
 };
 
 // One product's K blocks and their ranges: range v takes q grains, one more if
@@ -772,9 +781,9 @@ __device__ bool issue_bf16(const StreamParams& p, int which, Shared& ss, uint8_t
   while (walk.next(s)) {
     const Columns<KIND> c(p, which, ss, s);
     const uint32_t idesc = idesc_bf16_f32(kTileRows, c.n, 0, 0);
-    const uint32_t acc = ss.tmem + tn.buf * 2 * p.acc_cols;
-    if (!warp_wait<false>(&ss.acc_empty[tn.buf], tn.phase ^ 1, abort, p.err, (0x31 << 24) | which)) return false;
-    for (int kb = s.kb0; kb < s.kb1; ++kb) {
+    for (int kb = s.kb0, done = 0; kb < s.kb1; ++kb) {
+      const uint32_t acc = ss.tmem + tn.buf * 2 * p.acc_cols;
+      if (done == 0 && !warp_wait<false>(&ss.acc_empty[tn.buf], tn.phase ^ 1, abort, p.err, (0x31 << 24) | which)) return false;
       const uint32_t st = smem_u32(ring) + static_cast<uint32_t>(rg.stage) * p.stage_bytes;
       const uint32_t x = st + Geo<0>::WEIGHT_BYTES;
       if (!warp_wait<false>(&ss.full_x[rg.stage], rg.phase, abort, p.err, (0x24 << 24) | which)) return false;
@@ -784,18 +793,21 @@ __device__ bool issue_bf16(const StreamParams& p, int which, Shared& ss, uint8_t
 #pragma unroll
         for (int k4 = 0; k4 < 4; ++k4) {
           const uint64_t bd = smem_desc_sw128(x + k4 * 32, 16, 1024);
-          const uint32_t go_on = (kb != s.kb0 || k4 != 0) ? 1u : 0u;
+          const uint32_t go_on = (done != 0 || k4 != 0) ? 1u : 0u;
 #pragma unroll
           for (int box = 0; box < 2; ++box)
             umma_bf16(acc + box * p.acc_cols, smem_desc_sw128(st + box * kBoxBytes + k4 * 32, 16, 1024), bd, idesc, go_on);
         }
         umma_commit(&ss.empty[rg.stage]);
-        if (kb == s.kb1 - 1) umma_commit(&ss.acc_full[tn.buf]);
+        if (done + 1 == p.run || kb == s.kb1 - 1) umma_commit(&ss.acc_full[tn.buf]);
       }
       __syncwarp();
       rg.step(p.stages);
+      if (++done == p.run || kb == s.kb1 - 1) {
+        tn.step(p.acc_bufs);
+        done = 0;
+      }
     }
-    tn.step(p.acc_bufs);
   }
   return true;
 }
@@ -982,40 +994,47 @@ __device__ bool join_parts(const StreamParams& p, int which, const Shared& ss, v
   return true;
 }
 
-// A segment's sums are in tensor memory: finishes its tile, or leaves them as
-// a part.  Every set sees all sums of its rows and takes its share of the
-// columns, two at a time.  `read(box, at, u)` starts the loads of one column,
-// `value(u)` makes its sum of them.
-template <Kind KIND, int LOADS, typename Read, typename Value>
-__device__ __forceinline__ void finish_segment(const StreamParams& p, const Shared& ss, const Segment& s, const Share& sh,
-                                               const Columns<KIND>& c, const Read& read, const Value& value) {
-  const int warp = threadIdx.x >> 5, row = (warp & 3) * 32 + (threadIdx.x & 31), set = warp >> 2;
+// Every set sees all sums of its rows in tensor memory and takes its share of
+// the m columns, two at a time.  `read(box, at, u)` starts the loads of one
+// column, `value(u)` makes its sum of them, `done(i, v0, v1)` takes both boxes'.
+template <int LOADS, typename Read, typename Value, typename Done>
+__device__ __forceinline__ void each_column(int m, const Read& read, const Value& value, const Done& done) {
+  const int set = threadIdx.x >> 7;
   constexpr int B = 2;
-  for (int i0 = set * B; i0 < c.m; i0 += kSets * B) {
+  for (int i0 = set * B; i0 < m; i0 += kSets * B) {
     uint32_t u[B][2][LOADS];
 #pragma unroll
     for (int j = 0; j < B; ++j) {
-      const int i = min(i0 + j, c.m - 1);  // past the end: the last column again
+      const int i = min(i0 + j, m - 1);  // past the end: the last column again
 #pragma unroll
       for (int box = 0; box < 2; ++box) read(box, i, u[j][box]);
     }
     tmem_ld_wait();
 #pragma unroll
     for (int j = 0; j < B; ++j) {
-      const int i = i0 + j;
-      if (i >= c.m) break;
-      const float v0 = value(u[j][0]), v1 = value(u[j][1]);
-      if (sh.whole) {
-        finish_column<KIND>(p, ss, s, c.r0, i, row, v0, v1);
-      } else {
-        __stcg(part_of(p, s.worker, s.kb0 == 0, 0, row) + i * kTileRows, v0);
-        __stcg(part_of(p, s.worker, s.kb0 == 0, 1, row) + i * kTileRows, v1);
-      }
+      if (i0 + j >= m) break;
+      done(i0 + j, value(u[j][0]), value(u[j][1]));
     }
   }
 }
 
-// bf16 weights: the accumulators hold a segment's sums.
+// A segment's sums are in tensor memory: finishes its tile, or leaves them as
+// a part.
+template <Kind KIND, int LOADS, typename Read, typename Value>
+__device__ __forceinline__ void finish_segment(const StreamParams& p, const Shared& ss, const Segment& s, const Share& sh,
+                                               const Columns<KIND>& c, const Read& read, const Value& value) {
+  const int row = threadIdx.x & (kTileRows - 1);
+  each_column<LOADS>(c.m, read, value, [&](int i, float v0, float v1) {
+    if (sh.whole) {
+      finish_column<KIND>(p, ss, s, c.r0, i, row, v0, v1);
+    } else {
+      __stcg(part_of(p, s.worker, s.kb0 == 0, 0, row) + i * kTileRows, v0);
+      __stcg(part_of(p, s.worker, s.kb0 == 0, 1, row) + i * kTileRows, v1);
+    }
+  });
+}
+
+// bf16 weights: the accumulators hold the sums of a run of a segment's K blocks.
 template <Kind KIND>
 __device__ bool rows_bf16(const StreamParams& p, int which, Shared& ss, Queue& qu, Turn& tn, volatile int* abort) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -1024,28 +1043,39 @@ __device__ bool rows_bf16(const StreamParams& p, int which, Shared& ss, Queue& q
   while (walk.next(s)) {
     const Columns<KIND> c(p, which, ss, s);
     const Share sh(walk.walk, s);
-    if (!warp_wait<false>(&ss.acc_full[tn.buf], tn.phase, abort, p.err, (0x33 << 24) | which)) return false;
-    tc_fence_after();
-    const uint32_t acc = ss.tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + tn.buf * 2 * p.acc_cols;
-    finish_segment<KIND, KIND == kRowsOfH ? 3 : 1>(
-        p, ss, s, sh, c,
-        [&](int box, int at, uint32_t* u) {
+    constexpr int PARTS = KIND == kRowsOfH ? 3 : 1;
+    const uint32_t lanes = ss.tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16), sums = lanes + kTmemCols - kRunCols;
+    for (int kb = s.kb0; kb < s.kb1; kb += p.run) {
+      if (!warp_wait<false>(&ss.acc_full[tn.buf], tn.phase, abort, p.err, (0x33 << 24) | which)) return false;
+      tc_fence_after();
+      const uint32_t acc = lanes + tn.buf * 2 * p.acc_cols;
+      const auto read = [&](int box, int at, uint32_t* u) {
 #pragma unroll
-          for (int q = 0; q < (KIND == kRowsOfH ? 3 : 1); ++q) {
-            u[q] = 0;
-            if (q < 2 || p.parts == 3) u[q] = tmem_ld1(acc + box * p.acc_cols + q * 16 * c.n16 + at);
-          }
-        },
-        [&](const uint32_t* u) {
-          if constexpr (KIND == kRowsOfH)
-            return fmaf(__uint_as_float(u[1]) + __uint_as_float(u[2]), 1.f / kLowScale, __uint_as_float(u[0]));
-          else
-            return __uint_as_float(u[0]);
+        for (int q = 0; q < PARTS; ++q) {
+          u[q] = 0;
+          if (q < 2 || p.parts == 3) u[q] = tmem_ld1(acc + box * p.acc_cols + q * 16 * c.n16 + at);
+        }
+        u[PARTS] = kb == s.kb0 ? 0 : tmem_ld1(sums + box * kMaxTokens + at);  // of the runs before
+      };
+      const auto value = [&](const uint32_t* u) {
+        float v = __uint_as_float(u[0]);
+        if constexpr (PARTS == 3) v = fmaf(__uint_as_float(u[1]) + __uint_as_float(u[2]), 1.f / kLowScale, v);
+        return v + __uint_as_float(u[PARTS]);
+      };
+      if (kb + p.run < s.kb1) {
+        each_column<PARTS + 1>(c.m, read, value, [&](int i, float v0, float v1) {
+          tmem_st1(sums + i, __float_as_uint(v0));
+          tmem_st1(sums + kMaxTokens + i, __float_as_uint(v1));
         });
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&ss.acc_empty[tn.buf]);
-    tn.step(p.acc_bufs);
+        tmem_st_wait();
+      } else {
+        finish_segment<KIND, PARTS + 1>(p, ss, s, sh, c, read, value);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ss.acc_empty[tn.buf]);
+      tn.step(p.acc_bufs);
+    }
     if (!sh.whole) count_part<true>(p, which, sh);
   }
   return join_parts<KIND, true>(p, which, ss, abort);
@@ -1450,7 +1480,9 @@ template <int G>
 size_t ring_shape(StreamParams& p, int cols) {
   using Ge = Geo<G>;
   p.acc_cols = cols;
-  p.acc_bufs = std::min(2, kTmemCols / (2 * cols));
+  const bool runs = !Ge::Q4 && p.y_type == MOE_Y_F32;
+  p.acc_bufs = std::min(2, (kTmemCols - (runs ? kRunCols : 0)) / (2 * cols));
+  p.run = !runs ? 1 << 30 : p.acc_bufs == 2 ? kRunBlocks : 2 * kRunBlocks;
   p.stage_bytes = static_cast<int>(align_up(Ge::WEIGHT_BYTES + Ge::ATOMS * cols * 128, 1024));
   const size_t fixed = kSharedBytes + 1024;
   p.stages = std::min<int>(kMaxStages, static_cast<int>((kSmemMax - fixed) / p.stage_bytes));

@@ -414,3 +414,25 @@ def test_q4_hundreds_of_calls_in_a_row_of_either_type(group, dtype):
         assert device_error(ws) == (0, 0)
         for a, b in zip(out, want):
             assert torch.equal(a, b)
+
+
+# An fp32 y.  The tensor core cuts its running sum off at 2^-23 of it or less for each instruction, always towards zero:
+# over 16 of them (the most that are added up before the sums are rounded to nearest) at most 16 2^-23 = 1.9e-6 of a sum
+# that only grows, half of that where it grows evenly.  The layer's second product adds as much again; roundings to
+# nearest have signs as good as random and are far below.  So 4e-6 for the layer and 2e-6 for the linear form.
+@pytest.mark.parametrize("T", [1, 9, 40, 64])
+def test_fp32_sums_stay_exact_over_many_columns(T):
+    layer = Layer(MoEConfig("deep", T, 3840, 1920, 7, 3))
+    y, _, _, ws = layer.run(F32)
+    assert device_error(ws) == (0, 0)
+    assert relf(np64(y), layer.reference().y) <= 4e-6
+
+
+@pytest.mark.parametrize("T,n,K", [(1, 40000, 4096), (9, 20000, 4096), (64, 20000, 8192)])
+def test_fp32_linear_sums_stay_exact_over_many_columns(T, n, K):
+    g = torch.Generator().manual_seed(K)
+    x, W = torch.randn(T, K, generator=g).to(BF16), torch.randn(n, K, generator=g).to(BF16)
+    y = torch.empty(T, n, dtype=F32, device=DEV)
+    moe.moe_linear_fwd(x.to(DEV), W.to(DEV), y, moe.alloc_linear_workspace(T, n, K))
+    ref = x.to(DEV).double() @ W.to(DEV).double().T
+    assert ((y.double() - ref).norm() / ref.norm()).item() <= 2e-6
