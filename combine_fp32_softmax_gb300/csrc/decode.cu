@@ -73,11 +73,11 @@ constexpr int kBoxBytes = kTileRows * 128;
 constexpr int kTmemCols = 512;
 // bf16 weights: the tensor core cuts off what its running sum has no room for,
 // always towards zero, which over K = 3840 comes to 1e-5 of an output.  For an
-// fp32 y it adds up 2 K blocks (8 instructions) at a time, 4 where there are
+// fp32 y it adds up 3 K blocks (12 instructions) at a time, 4 where there are
 // no two pairs of accumulators, and the row warps add those sums, rounded to
-// nearest, in the last columns of tensor memory.  A bf16 y, off by 2^-9, needs
-// none of it.
-constexpr int kRunBlocks = 2;
+// nearest, in the last columns of tensor memory: 5e-7, about what fp32
+// multiply-adds come to.  A bf16 y, off by 2^-9, needs none of it.
+constexpr int kRunBlocks = 3, kRunBlocksAlone = 4;
 constexpr int kRunCols = 2 * MOE_DECODE_MAX_T;
 // 4 bits: tensor memory of one of two buffers of a set of row warps, operand
 // and sums.
@@ -157,7 +157,7 @@ struct StreamParams {
   int y_type, workers, stages, stage_bytes;
   int parts;            // bf16 parts of a hidden value
   int acc_cols, acc_bufs;  // bf16 weights: columns of an accumulator, accumulator pairs
-  int run;                 // bf16 weights: K blocks that the tensor core adds up at a time
+  int run;                 // bf16 weights, fp32 y: K blocks that the tensor core adds up at a time
 };
 
 // One product's K blocks and their ranges: range v takes q grains, one more if
@@ -773,7 +773,7 @@ __device__ __forceinline__ uint32_t sums_at(uint32_t tmem, int box, int set, int
   return operand_at(tmem, box, set, buf) + size * (kChunk / 2);
 }
 
-template <Kind KIND>
+template <Kind KIND, bool RUNS>
 __device__ bool issue_bf16(const StreamParams& p, int which, Shared& ss, uint8_t* ring, Ring& rg, Queue& qu, Turn& tn,
                            volatile int* abort) {
   Tiles<false> walk(p, which, ss, qu, abort);
@@ -783,7 +783,9 @@ __device__ bool issue_bf16(const StreamParams& p, int which, Shared& ss, uint8_t
     const uint32_t idesc = idesc_bf16_f32(kTileRows, c.n, 0, 0);
     for (int kb = s.kb0, done = 0; kb < s.kb1; ++kb) {
       const uint32_t acc = ss.tmem + tn.buf * 2 * p.acc_cols;
-      if (done == 0 && !warp_wait<false>(&ss.acc_empty[tn.buf], tn.phase ^ 1, abort, p.err, (0x31 << 24) | which)) return false;
+      const bool begins = RUNS ? done == 0 : kb == s.kb0;
+      const bool ends = (RUNS && done + 1 == p.run) || kb == s.kb1 - 1;
+      if (begins && !warp_wait<false>(&ss.acc_empty[tn.buf], tn.phase ^ 1, abort, p.err, (0x31 << 24) | which)) return false;
       const uint32_t st = smem_u32(ring) + static_cast<uint32_t>(rg.stage) * p.stage_bytes;
       const uint32_t x = st + Geo<0>::WEIGHT_BYTES;
       if (!warp_wait<false>(&ss.full_x[rg.stage], rg.phase, abort, p.err, (0x24 << 24) | which)) return false;
@@ -793,20 +795,18 @@ __device__ bool issue_bf16(const StreamParams& p, int which, Shared& ss, uint8_t
 #pragma unroll
         for (int k4 = 0; k4 < 4; ++k4) {
           const uint64_t bd = smem_desc_sw128(x + k4 * 32, 16, 1024);
-          const uint32_t go_on = (done != 0 || k4 != 0) ? 1u : 0u;
+          const uint32_t go_on = (!begins || k4 != 0) ? 1u : 0u;
 #pragma unroll
           for (int box = 0; box < 2; ++box)
             umma_bf16(acc + box * p.acc_cols, smem_desc_sw128(st + box * kBoxBytes + k4 * 32, 16, 1024), bd, idesc, go_on);
         }
         umma_commit(&ss.empty[rg.stage]);
-        if (done + 1 == p.run || kb == s.kb1 - 1) umma_commit(&ss.acc_full[tn.buf]);
+        if (ends) umma_commit(&ss.acc_full[tn.buf]);
       }
       __syncwarp();
       rg.step(p.stages);
-      if (++done == p.run || kb == s.kb1 - 1) {
-        tn.step(p.acc_bufs);
-        done = 0;
-      }
+      done = ends ? 0 : done + 1;
+      if (ends) tn.step(p.acc_bufs);
     }
   }
   return true;
@@ -1035,7 +1035,7 @@ __device__ __forceinline__ void finish_segment(const StreamParams& p, const Shar
 }
 
 // bf16 weights: the accumulators hold the sums of a run of a segment's K blocks.
-template <Kind KIND>
+template <Kind KIND, bool RUNS>
 __device__ bool rows_bf16(const StreamParams& p, int which, Shared& ss, Queue& qu, Turn& tn, volatile int* abort) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   Tiles<false> walk(p, which, ss, qu, abort);
@@ -1045,7 +1045,7 @@ __device__ bool rows_bf16(const StreamParams& p, int which, Shared& ss, Queue& q
     const Share sh(walk.walk, s);
     constexpr int PARTS = KIND == kRowsOfH ? 3 : 1;
     const uint32_t lanes = ss.tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16), sums = lanes + kTmemCols - kRunCols;
-    for (int kb = s.kb0; kb < s.kb1; kb += p.run) {
+    for (int kb = s.kb0; kb < s.kb1; kb = RUNS ? kb + p.run : s.kb1) {
       if (!warp_wait<false>(&ss.acc_full[tn.buf], tn.phase, abort, p.err, (0x33 << 24) | which)) return false;
       tc_fence_after();
       const uint32_t acc = lanes + tn.buf * 2 * p.acc_cols;
@@ -1055,21 +1055,21 @@ __device__ bool rows_bf16(const StreamParams& p, int which, Shared& ss, Queue& q
           u[q] = 0;
           if (q < 2 || p.parts == 3) u[q] = tmem_ld1(acc + box * p.acc_cols + q * 16 * c.n16 + at);
         }
-        u[PARTS] = kb == s.kb0 ? 0 : tmem_ld1(sums + box * kMaxTokens + at);  // of the runs before
+        if (RUNS) u[PARTS] = kb == s.kb0 ? 0 : tmem_ld1(sums + box * kMaxTokens + at);  // of the runs before
       };
       const auto value = [&](const uint32_t* u) {
         float v = __uint_as_float(u[0]);
         if constexpr (PARTS == 3) v = fmaf(__uint_as_float(u[1]) + __uint_as_float(u[2]), 1.f / kLowScale, v);
-        return v + __uint_as_float(u[PARTS]);
+        return RUNS ? v + __uint_as_float(u[PARTS]) : v;
       };
-      if (kb + p.run < s.kb1) {
-        each_column<PARTS + 1>(c.m, read, value, [&](int i, float v0, float v1) {
+      if (RUNS && kb + p.run < s.kb1) {
+        each_column<PARTS + RUNS>(c.m, read, value, [&](int i, float v0, float v1) {
           tmem_st1(sums + i, __float_as_uint(v0));
           tmem_st1(sums + kMaxTokens + i, __float_as_uint(v1));
         });
         tmem_st_wait();
       } else {
-        finish_segment<KIND, PARTS + 1>(p, ss, s, sh, c, read, value);
+        finish_segment<KIND, PARTS + RUNS>(p, ss, s, sh, c, read, value);
       }
       tc_fence_before();
       __syncwarp();
@@ -1264,7 +1264,8 @@ __device__ void sum_rows(const StreamParams& p, const Shared& ss) {
   }
 }
 
-template <int G, bool LAYER>
+// RUNS: bf16 weights, fp32 y.
+template <int G, bool LAYER, bool RUNS>
 __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_constant__ StreamParams p) {
   using Ge = Geo<G>;
   constexpr Kind FIRST = kGathered, SECOND = LAYER ? kRowsOfH : kRowsOfX;
@@ -1364,8 +1365,8 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
       if (LAYER) ok = issue_q4<G, FIRST>(p, 0, box, ss, ring, rg, qu, tn, abort);
       if (ok) issue_q4<G, SECOND>(p, 1, box, ss, ring, rg, qu, tn, abort);
     } else if (warp == kMmaWarp) {
-      if (LAYER) ok = issue_bf16<FIRST>(p, 0, ss, ring, rg, qu, tn, abort);
-      if (ok) issue_bf16<SECOND>(p, 1, ss, ring, rg, qu, tn, abort);
+      if (LAYER) ok = issue_bf16<FIRST, RUNS>(p, 0, ss, ring, rg, qu, tn, abort);
+      if (ok) issue_bf16<SECOND, RUNS>(p, 1, ss, ring, rg, qu, tn, abort);
     }
     __syncwarp();
     if (elect_one()) umma_commit(&ss.drained);
@@ -1385,14 +1386,14 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
       if constexpr (Ge::Q4)
         ok = rows_q4<G, FIRST>(p, 0, ss, ring, rg, qu, tn, swap, abort);
       else
-        ok = rows_bf16<FIRST>(p, 0, ss, qu, tn, abort);
+        ok = rows_bf16<FIRST, RUNS>(p, 0, ss, qu, tn, abort);
       fence_proxy_async_global();  // hidden values, to other CTAs' copies
       through(0);
       if (ok) {
         if constexpr (Ge::Q4)
           ok = rows_q4<G, SECOND>(p, 1, ss, ring, rg, qu, tn, swap, abort);
         else
-          ok = rows_bf16<SECOND>(p, 1, ss, qu, tn, abort);
+          ok = rows_bf16<SECOND, RUNS>(p, 1, ss, qu, tn, abort);
       }
       through(1);
       if (ok && warp_wait<Ge::Q4>(&ss.out_done, 0, abort, p.err, 0x2A << 24)) sum_rows(p, ss);
@@ -1400,7 +1401,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
       if constexpr (Ge::Q4)
         rows_q4<G, SECOND>(p, 1, ss, ring, rg, qu, tn, swap, abort);
       else
-        rows_bf16<SECOND>(p, 1, ss, qu, tn, abort);
+        rows_bf16<SECOND, RUNS>(p, 1, ss, qu, tn, abort);
     }
   }
   tc_fence_before();
@@ -1482,7 +1483,7 @@ size_t ring_shape(StreamParams& p, int cols) {
   p.acc_cols = cols;
   const bool runs = !Ge::Q4 && p.y_type == MOE_Y_F32;
   p.acc_bufs = std::min(2, (kTmemCols - (runs ? kRunCols : 0)) / (2 * cols));
-  p.run = !runs ? 1 << 30 : p.acc_bufs == 2 ? kRunBlocks : 2 * kRunBlocks;
+  p.run = p.acc_bufs == 2 ? kRunBlocks : kRunBlocksAlone;
   p.stage_bytes = static_cast<int>(align_up(Ge::WEIGHT_BYTES + Ge::ATOMS * cols * 128, 1024));
   const size_t fixed = kSharedBytes + 1024;
   p.stages = std::min<int>(kMaxStages, static_cast<int>((kSmemMax - fixed) / p.stage_bytes));
@@ -1494,11 +1495,11 @@ int columns_of(const StreamParams& p, int which, int parts) {
   return ceil_div(std::min(p.T, 1 << p.p[which].block_log2), 16) * 16 * parts;
 }
 
-template <int G, bool LAYER>
-int launch_stream(StreamParams& p, size_t smem, int grid_limit, cudaStream_t s) {
+template <int G, bool LAYER, bool RUNS>
+int launch_kernel(StreamParams& p, size_t smem, int grid_limit, cudaStream_t s) {
   static bool sized = false;  // the attribute outlives the call; setting it twice is harmless
   if (!sized) {
-    if (cudaFuncSetAttribute(stream_kernel<G, LAYER>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax) != cudaSuccess)
+    if (cudaFuncSetAttribute(stream_kernel<G, LAYER, RUNS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax) != cudaSuccess)
       return MOE_ERR_CUDA;
     sized = true;
   }
@@ -1513,7 +1514,13 @@ int launch_stream(StreamParams& p, size_t smem, int grid_limit, cudaStream_t s) 
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, stream_kernel<G, LAYER>, p) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, stream_kernel<G, LAYER, RUNS>, p) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+template <int G, bool LAYER>
+int launch_stream(StreamParams& p, size_t smem, int grid_limit, cudaStream_t s) {
+  if constexpr (G == 0)
+    if (p.y_type == MOE_Y_F32) return launch_kernel<G, LAYER, true>(p, smem, grid_limit, s);
+  return launch_kernel<G, LAYER, false>(p, smem, grid_limit, s);
 }
 
 void common_params(StreamParams& p, void* ws, const Layout& L, int T, void* y, int y_type) {
