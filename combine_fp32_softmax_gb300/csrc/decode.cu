@@ -781,11 +781,14 @@ __device__ bool issue_bf16(const StreamParams& p, int which, Shared& ss, uint8_t
   while (walk.next(s)) {
     const Columns<KIND> c(p, which, ss, s);
     const uint32_t idesc = idesc_bf16_f32(kTileRows, c.n, 0, 0);
+    uint32_t acc = 0;
+    const auto begin = [&]() {
+      acc = ss.tmem + tn.buf * 2 * p.acc_cols;
+      return warp_wait<false>(&ss.acc_empty[tn.buf], tn.phase ^ 1, abort, p.err, (0x31 << 24) | which);
+    };
+    if (!RUNS && !begin()) return false;
     for (int kb = s.kb0, done = 0; kb < s.kb1; ++kb) {
-      const uint32_t acc = ss.tmem + tn.buf * 2 * p.acc_cols;
-      const bool begins = RUNS ? done == 0 : kb == s.kb0;
-      const bool ends = (RUNS && done + 1 == p.run) || kb == s.kb1 - 1;
-      if (begins && !warp_wait<false>(&ss.acc_empty[tn.buf], tn.phase ^ 1, abort, p.err, (0x31 << 24) | which)) return false;
+      if (RUNS && done == 0 && !begin()) return false;
       const uint32_t st = smem_u32(ring) + static_cast<uint32_t>(rg.stage) * p.stage_bytes;
       const uint32_t x = st + Geo<0>::WEIGHT_BYTES;
       if (!warp_wait<false>(&ss.full_x[rg.stage], rg.phase, abort, p.err, (0x24 << 24) | which)) return false;
@@ -795,19 +798,22 @@ __device__ bool issue_bf16(const StreamParams& p, int which, Shared& ss, uint8_t
 #pragma unroll
         for (int k4 = 0; k4 < 4; ++k4) {
           const uint64_t bd = smem_desc_sw128(x + k4 * 32, 16, 1024);
-          const uint32_t go_on = (!begins || k4 != 0) ? 1u : 0u;
+          const uint32_t go_on = ((RUNS ? done != 0 : kb != s.kb0) || k4 != 0) ? 1u : 0u;
 #pragma unroll
           for (int box = 0; box < 2; ++box)
             umma_bf16(acc + box * p.acc_cols, smem_desc_sw128(st + box * kBoxBytes + k4 * 32, 16, 1024), bd, idesc, go_on);
         }
         umma_commit(&ss.empty[rg.stage]);
-        if (ends) umma_commit(&ss.acc_full[tn.buf]);
+        if ((RUNS && done + 1 == p.run) || kb == s.kb1 - 1) umma_commit(&ss.acc_full[tn.buf]);
       }
       __syncwarp();
       rg.step(p.stages);
-      done = ends ? 0 : done + 1;
-      if (ends) tn.step(p.acc_bufs);
+      if (RUNS && ++done == p.run && kb < s.kb1 - 1) {
+        tn.step(p.acc_bufs);
+        done = 0;
+      }
     }
+    tn.step(p.acc_bufs);
   }
   return true;
 }
