@@ -328,7 +328,8 @@ int moe_decode_ws_init(const moe_cfg* cfg, void* ws, void* stream);
  *   h[t, j] = topk_w[t, j] * silu(x_t . W1_e^T) * (x_t . W3_e^T)
  *   y[t]    = sum_j h[t, j] . W2_e^T + sum_s h[t, s] . W2_(E+s)^T
  * (shared experts with weight 1).  Layouts as moe_layer_fwd.  All sums are
- * fp32; h enters the second product as the sum of two bf16 values (16
+ * fp32 (for an fp32 y, relative error of y below 1e-6: the tensor core's
+ * truncating sums are kept to 16 instructions); h enters the second product as the sum of two bf16 values (16
  * significant bits) for a bf16 y and of three (24 bits) for an fp32 y; y
  * [T, d] is rounded once to y_type.  Only the weights of
  * experts that some token picked (and of the shared experts) are read.  A
