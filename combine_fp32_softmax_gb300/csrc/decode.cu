@@ -34,11 +34,11 @@
 //
 // What it measures (a call in a graph; GB/s are of the bytes that have to be
 // moved, the copy rate is 6790):
-//   d=2048 f=1408 E=64 k=6 S=2, bf16: 1 token 39.1 us, 3540 GB/s; 64 tokens
-//     197 us, 5780 GB/s (7100 while it streams).  At one token the work itself
-//     takes 22 us; the rest is a chain of latencies: launch, router (4 us),
-//     first tile, two grid-wide meetings, the joining of cut tiles.
-//   The same in 4 bits: 1 token 27.5 us; d=4096 f=14336 E=8 k=2, 16 tokens
+//   d=2048 f=1408 E=64 k=6 S=2, bf16: 1 token 39.5 us, 3500 GB/s; 64 tokens
+//     197 us, 5780 GB/s (7100 while it streams).  One token: start and router
+//     5 us; W1 and W3 17 us, whole tiles on 88 SMs; W2 10 us, on 64; two
+//     grid-wide meetings 5 us.
+//   The same in 4 bits: 1 token 27.8 us; d=4096 f=14336 E=8 k=2, 16 tokens
 //     171 us, 4360 GB/s.  An SM spends some 1800 clocks on a K block of 32 KB,
 //     906 of them the least that turning its codes takes (measured alone: 5
 //     integer instructions at half rate and 4 multiply-adds a word).
