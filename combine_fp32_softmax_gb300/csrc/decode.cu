@@ -1065,7 +1065,11 @@ __device__ bool rows_bf16(const StreamParams& p, int which, Shared& ss, Queue& q
       };
       const auto value = [&](const uint32_t* u) {
         float v = __uint_as_float(u[0]);
-        if constexpr (PARTS == 3) v = fmaf(__uint_as_float(u[1]) + __uint_as_float(u[2]), 1.f / kLowScale, v);
+        // An infinite weight: the sum of the upper parts of h is the infinity or NaN that h has; those of the lower
+        // parts, which are 0 or of the other sign, would turn it into NaN.
+        if constexpr (PARTS == 3) {
+          if (isfinite(v)) v = fmaf(__uint_as_float(u[1]) + __uint_as_float(u[2]), 1.f / kLowScale, v);
+        }
         return RUNS ? v + __uint_as_float(u[PARTS]) : v;
       };
       if (RUNS && kb + p.run < s.kb1) {

@@ -334,8 +334,9 @@ int moe_decode_ws_init(const moe_cfg* cfg, void* ws, void* stream);
  * [T, d] is rounded once to y_type.  Only the weights of
  * experts that some token picked (and of the shared experts) are read.  A
  * non-finite logit sets MOE_ERR_NONFINITE, as in moe_route, and leaves that
- * token's outputs unspecified.  Bitwise reproducible.  Pointers 16-byte
- * aligned, ws 256-byte. */
+ * token's outputs unspecified.  Infinite and NaN weights of picked experts
+ * give what the formula gives (an h below 2^-134 counts as 0 beside them).
+ * Bitwise reproducible.  Pointers 16-byte aligned, ws 256-byte. */
 int moe_decode_fwd(const moe_cfg* cfg, const float* logits, const uint16_t* x, const uint16_t* W1,
                    const uint16_t* W3, const uint16_t* W2, void* y, int y_type, int32_t* topk_idx,
                    float* topk_w, void* ws, void* stream);
@@ -343,7 +344,8 @@ int moe_decode_fwd(const moe_cfg* cfg, const float* logits, const uint16_t* x, c
 /* The same with 4-bit weights: W1q/W1s, W3q/W3s [E+S] matrices [f, d], W2q/W2s
  * [E+S] matrices [d, f]; d_model and d_ff multiples of `group` (32, 64 or 128;
  * MOE_ERR_SHAPE otherwise).  Codes multiply the bf16 activations exactly and
- * each group's fp32 sum is scaled in fp32: no weight is rounded. */
+ * each group's fp32 sum is scaled in fp32: no weight is rounded.  A scale that
+ * is not finite makes the outputs of its row infinite or NaN. */
 int moe_decode_q4_fwd(const moe_cfg* cfg, int group, const float* logits, const uint16_t* x,
                       const uint8_t* W1q, const uint16_t* W1s, const uint8_t* W3q, const uint16_t* W3s,
                       const uint8_t* W2q, const uint16_t* W2s, void* y, int y_type, int32_t* topk_idx,
