@@ -1510,12 +1510,9 @@ int columns_of(const StreamParams& p, int which, int parts) {
 
 template <int G, bool LAYER, bool RUNS>
 int launch_kernel(StreamParams& p, size_t smem, int grid_limit, cudaStream_t s) {
-  static bool sized = false;  // the attribute outlives the call; setting it twice is harmless
-  if (!sized) {
-    if (cudaFuncSetAttribute(stream_kernel<G, LAYER, RUNS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax) != cudaSuccess)
-      return MOE_ERR_CUDA;
-    sized = true;
-  }
+  // at each launch: the attribute holds for the current device only
+  if (cudaFuncSetAttribute(stream_kernel<G, LAYER, RUNS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax) != cudaSuccess)
+    return MOE_ERR_CUDA;
   const int grid = grid_limit > 0 ? std::min(grid_limit, p.workers) : p.workers;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
