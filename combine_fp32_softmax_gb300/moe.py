@@ -9,6 +9,7 @@ not built, loading it raises immediately.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -136,13 +137,14 @@ def _ptr(t):
 # The current stream's handle without building a Stream object, where this torch has it: a generation step makes its
 # calls back to back, and each costs the host more than the smallest of them costs the GPU.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream):
     if stream is not None:
         return stream.cuda_stream
     if _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(_device())
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -247,33 +249,101 @@ def _y_type(y) -> int:
     return _Y_TYPES.get(y.dtype, -1)
 
 
+# Addresses of arrays whose sizes and types are known (None is refused by the library).
+def _array(name, t, dtype, n):
+    """Address of a tensor that must hold n elements of a type."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.numel() != n:
+        raise ValueError(f"{name}: {n} elements of {dtype} expected, got {t.numel()} of {t.dtype}")
+    if not t.is_cuda or not t.is_contiguous():
+        _ptr(t)
+    return t.data_ptr()
+
+
+def _rows(name, t, dtype, rows, cols):
+    """Address of a tensor [rows, cols] of a type (None: any), or one with more such rows, which are left alone."""
+    if t is None:
+        return None
+    n = t.numel()
+    if (dtype is not None and t.dtype is not dtype) or n < rows * cols or (n > rows * cols and t.shape[-1] != cols):
+        raise ValueError(f"{name}: {rows} x {cols} elements of {dtype or 'fp32 or bf16'} expected, got "
+                         f"{tuple(t.shape)} of {t.dtype}")
+    if not t.is_cuda or not t.is_contiguous():
+        _ptr(t)
+    return t.data_ptr()
+
+
+def _workspace(ws, nbytes):
+    if ws is not None and ws.nbytes < nbytes:
+        raise ValueError(f"ws: {nbytes} bytes expected, got {ws.nbytes}")
+    return _ptr(ws)
+
+
+@functools.lru_cache(maxsize=1024)
+def _decode_sizes(T, d, f, E, k, S, renorm, group=1):
+    """The C configuration of these sizes, the bytes of a workspace, and the elements of a weight array and of the
+    scales of W1 or W3 and of W2."""
+    c = ctypes.byref(moe_cfg(T, d, f, E, k, S, renorm))
+    return (c, int(lib().moe_decode_workspace_bytes(c)), (E + S) * d * f, _q4_scales(E + S, f, d, group),
+            _q4_scales(E + S, d, f, group))
+
+
+@functools.lru_cache(maxsize=1024)
+def _linear_bytes(T, n, K):
+    return int(lib().moe_linear_workspace_bytes(T, n, K))
+
+
+def _dims(c):
+    """(T, d, f, E, k, S, renorm)."""
+    if isinstance(c, moe_cfg):
+        return c.T, c.d_model, c.d_ff, c.E, c.k, c.n_shared, c.renorm
+    return c.T, c.d, c.f, c.E, c.k, c.S, c.renorm
+
+
 def moe_decode_workspace_bytes(cfg) -> int:
-    return int(lib().moe_decode_workspace_bytes(_cfg(cfg)))
+    """Bytes of the workspace (0 outside the limits).  One made for T tokens also serves calls with fewer."""
+    return _decode_sizes(*_dims(cfg))[1]
 
 
 def moe_decode_ws_init(cfg, ws, stream=None):
-    _call("moe_decode_ws_init", _cfg(cfg), _ptr(ws), _stream(stream))
+    c, nbytes, *_ = _decode_sizes(*_dims(cfg))
+    _call("moe_decode_ws_init", c, _workspace(ws, nbytes), _stream(stream))
 
 
 def moe_decode_fwd(cfg, logits, x, W1, W3, W2, y, topk_idx, topk_w, ws, stream=None):
-    """Whole layer forward for T <= 64 tokens; y [T, d] fp32 or bf16."""
-    _call("moe_decode_fwd", _cfg(cfg), _ptr(logits), _ptr(x), _ptr(W1), _ptr(W3), _ptr(W2), _ptr(y), _y_type(y),
-          _ptr(topk_idx), _ptr(topk_w), _ptr(ws), _stream(stream))
+    """Whole layer forward for T <= 64 tokens; y [T, d] fp32 or bf16.  The arrays that have a row for each token may
+    have more of them."""
+    dims = T, d, _, E, k, _, _ = _dims(cfg)
+    c, nbytes, n, _, _ = _decode_sizes(*dims)
+    f32, bf16 = torch.float32, torch.bfloat16
+    _call("moe_decode_fwd", c, _rows("logits", logits, f32, T, E), _rows("x", x, bf16, T, d),
+          _array("W1", W1, bf16, n), _array("W3", W3, bf16, n), _array("W2", W2, bf16, n), _rows("y", y, None, T, d),
+          _y_type(y), _rows("topk_idx", topk_idx, torch.int32, T, k), _rows("topk_w", topk_w, f32, T, k),
+          _workspace(ws, nbytes), _stream(stream))
 
 
 def moe_decode_q4_fwd(cfg, group, logits, x, W1q, W1s, W3q, W3s, W2q, W2s, y, topk_idx, topk_w, ws, stream=None):
     """The same with 4-bit weights (codes [E+S, rows, cols/2] uint8, scales as q4_empty gives them)."""
-    _call("moe_decode_q4_fwd", _cfg(cfg), int(group), _ptr(logits), _ptr(x), _ptr(W1q), _ptr(W1s), _ptr(W3q),
-          _ptr(W3s), _ptr(W2q), _ptr(W2s), _ptr(y), _y_type(y), _ptr(topk_idx), _ptr(topk_w), _ptr(ws),
-          _stream(stream))
+    dims = T, d, _, E, k, _, _ = _dims(cfg)
+    group = int(group)
+    c, nbytes, n, up, down = _decode_sizes(*dims, group)
+    f32, bf16, u8 = torch.float32, torch.bfloat16, torch.uint8
+    n //= 2
+    _call("moe_decode_q4_fwd", c, group, _rows("logits", logits, f32, T, E), _rows("x", x, bf16, T, d),
+          _array("W1q", W1q, u8, n), _array("W1s", W1s, bf16, up), _array("W3q", W3q, u8, n),
+          _array("W3s", W3s, bf16, up), _array("W2q", W2q, u8, n), _array("W2s", W2s, bf16, down),
+          _rows("y", y, None, T, d), _y_type(y), _rows("topk_idx", topk_idx, torch.int32, T, k),
+          _rows("topk_w", topk_w, f32, T, k), _workspace(ws, nbytes), _stream(stream))
 
 
 def moe_linear_workspace_bytes(T, n, K) -> int:
-    return int(lib().moe_linear_workspace_bytes(int(T), int(n), int(K)))
+    return _linear_bytes(int(T), int(n), int(K))
 
 
 def moe_linear_ws_init(T, n, K, ws, stream=None):
-    _call("moe_linear_ws_init", int(T), int(n), int(K), _ptr(ws), _stream(stream))
+    T, n, K = int(T), int(n), int(K)
+    _call("moe_linear_ws_init", T, n, K, _workspace(ws, _linear_bytes(T, n, K)), _stream(stream))
 
 
 def _linear_shape(x, y):
@@ -286,24 +356,23 @@ def _linear_shape(x, y):
 def moe_linear_fwd(x, W, y, ws, stream=None):
     """y [T, n] = x [T, K] . W [n, K]^T for T <= 64 rows; y fp32 or bf16."""
     T, n, K = _linear_shape(x, y)
-    if W.numel() != n * K:
-        raise ValueError(f"W of {n} x {K} weights expected, got {tuple(W.shape)}")
-    _call("moe_linear_fwd", T, n, K, _ptr(x), _ptr(W), _ptr(y), _y_type(y), _ptr(ws), _stream(stream))
+    bf16 = torch.bfloat16
+    _call("moe_linear_fwd", T, n, K, _array("x", x, bf16, T * K), _array("W", W, bf16, n * K), _ptr(y), _y_type(y),
+          _workspace(ws, _linear_bytes(T, n, K)), _stream(stream))
 
 
 def moe_linear_q4_fwd(x, Wq, Ws, group, y, ws, stream=None):
     """The same with a 4-bit W (codes Wq, scales Ws, groups of `group` columns)."""
     T, n, K = _linear_shape(x, y)
-    _q4_check(Wq, Ws, 1, n, K, group)
-    _call("moe_linear_q4_fwd", T, n, K, int(group), _ptr(x), _ptr(Wq), _ptr(Ws), _ptr(y), _y_type(y), _ptr(ws),
-          _stream(stream))
+    bf16 = torch.bfloat16
+    _call("moe_linear_q4_fwd", T, n, K, int(group), _array("x", x, bf16, T * K),
+          _array("Wq", Wq, torch.uint8, n * K // 2), _array("Ws", Ws, bf16, _q4_scales(1, n, K, group)), _ptr(y),
+          _y_type(y), _workspace(ws, _linear_bytes(T, n, K)), _stream(stream))
 
 
-def _q4_check(codes, scales, mats, rows, cols, group):
-    want = mats * rows * cols // 2, mats * (cols // max(1, group)) * (-(-rows // 8) * 8)
-    if (codes.numel(), scales.numel()) != want:
-        raise ValueError(f"{want[0]} bytes of codes and {want[1]} scales expected, got {codes.numel()} and "
-                         f"{scales.numel()}")
+def _q4_scales(mats, rows, cols, group):
+    """Scales of `mats` matrices, their rows rounded up to 8."""
+    return mats * (cols // max(1, group)) * (-(-rows // 8) * 8)
 
 
 def q4_empty(mats, rows, cols, group, device="cuda"):
@@ -313,20 +382,25 @@ def q4_empty(mats, rows, cols, group, device="cuda"):
             torch.empty(mats, cols // group, -(-rows // 8) * 8, dtype=torch.bfloat16, device=device))
 
 
-def moe_q4_quantize(W, codes, scales, group, stream=None):
-    """W [mats, rows, cols] (or [rows, cols]) bf16 -> 4-bit codes and scales of groups of `group` columns."""
+def _q4_arrays(W, codes, scales, group):
+    """Addresses of the arrays, and (mats, rows, cols) of W [mats, rows, cols] or [rows, cols]."""
     rows, cols = W.shape[-2:]
     mats = W.shape[0] if W.dim() == 3 else 1
-    _q4_check(codes, scales, mats, rows, cols, group)
-    _call("moe_q4_quantize", _ptr(W), _ptr(codes), _ptr(scales), mats, rows, cols, int(group), _stream(stream))
+    n, bf16 = mats * rows * cols, torch.bfloat16
+    return (_array("W", W, bf16, n), _array("codes", codes, torch.uint8, n // 2),
+            _array("scales", scales, bf16, _q4_scales(mats, rows, cols, group)), mats, rows, cols)
+
+
+def moe_q4_quantize(W, codes, scales, group, stream=None):
+    """W [mats, rows, cols] (or [rows, cols]) bf16 -> 4-bit codes and scales of groups of `group` columns."""
+    w, c, s, mats, rows, cols = _q4_arrays(W, codes, scales, group)
+    _call("moe_q4_quantize", w, c, s, mats, rows, cols, int(group), _stream(stream))
 
 
 def moe_q4_dequantize(codes, scales, W, group, stream=None):
     """The bf16 values W [mats, rows, cols] (or [rows, cols]) that codes and scales stand for."""
-    rows, cols = W.shape[-2:]
-    mats = W.shape[0] if W.dim() == 3 else 1
-    _q4_check(codes, scales, mats, rows, cols, group)
-    _call("moe_q4_dequantize", _ptr(codes), _ptr(scales), _ptr(W), mats, rows, cols, int(group), _stream(stream))
+    w, c, s, mats, rows, cols = _q4_arrays(W, codes, scales, group)
+    _call("moe_q4_dequantize", c, s, w, mats, rows, cols, int(group), _stream(stream))
 
 
 def moe_get_device_error(ws, stream=None):

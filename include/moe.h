@@ -316,6 +316,9 @@ enum { MOE_Y_F32 = 0, MOE_Y_BF16 = 1 }; /* type of y */
  * with moe_decode_ws_init; a call leaves its counters at 0, except one that
  * ended with MOE_ERR_TIMEOUT (a wait inside ran out): clear the workspace
  * again after that.  Calls sharing a workspace must not run concurrently.
+ * A workspace made for T tokens also serves calls with fewer, its other sizes
+ * being the same; the calls do not see its length.  34 MB of it, and all of a
+ * linear call's, are for sums of tiles that several SMs share.
  * Each call of this section is one launch on `stream` (a cooperative one, on
  * all SMs or moe_set_grid_limit's number of CTAs, so work on other streams
  * may run beside it but should not hold SMs for long) and may be captured

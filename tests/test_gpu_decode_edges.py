@@ -65,3 +65,19 @@ def test_infinite_weights_meet_hidden_values_that_bf16_holds(dtype):
     assert got[:, 5].tolist() == [INF, -INF, INF] and got[:, 6].tolist() == [-INF, INF, -INF]
     assert torch.isnan(got[:, 7]).all()
     assert got[:, 0].tolist() == [128.0, -256.0, 128.0]
+
+
+# --------------------------------------------- one workspace, several counts
+@pytest.mark.parametrize("group", [0, 64])
+def test_a_workspace_for_64_tokens_serves_any_count(group):
+    full = Layer(MoEConfig("batch", 64, 256, 320, 8, 2, S=1), group=group)
+    ws = full.workspace()
+    x, z = full.x.to(DEV), full.logits.to(DEV)
+    for T in (64, 1, 21, 20, 7, 64, 33):
+        part = Layer.__new__(Layer)
+        part.cfg, part.group, part.dev = full.cfg.with_(T=T), group, full.dev
+        got = part.run(ws=ws, x=x, logits=z)          # x and logits with more rows than T
+        assert device_error(ws) == (0, 0)
+        want = part.run(x=x[:T].clone(), logits=z[:T].clone())
+        for a, b in zip(got[:3], want[:3]):
+            assert torch.equal(a, b), T
