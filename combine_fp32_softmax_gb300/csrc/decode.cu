@@ -968,6 +968,7 @@ __device__ bool join_parts(const StreamParams& p, int which, const Shared& ss, v
     if (first >= c.m) continue;
     bool ok = true;
     if (lane == 0) ok = wait_count(arrivals_of(p, which, sh.v0), parts * (WARPS ? kRowWarps : 1), abort, p.err, (0x29 << 24) | which);
+    __syncwarp();  // what lane 0 acquired, to all lanes: a shuffle orders no memory
     if (!__shfl_sync(kFull, ok, 0)) return false;
     constexpr int C = 2, B = 4;  // columns and parts on the way at a time
     for (int i0 = first; i0 < c.m; i0 += C * step) {
@@ -1356,6 +1357,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
         red_release_gpu_add(p.err + kCtrHidden + which, 1);
         ok = ok && wait_count(p.err + kCtrHidden + which, gridDim.x, abort, p.err, (0x26 << 24) | which);
       }
+      __syncwarp();  // what lane 0 acquired, to the lane that issues the copies
       return __shfl_sync(kFull, ok, 0) != 0;
     };
     bool ok = true;
