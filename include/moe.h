@@ -330,11 +330,16 @@ int moe_decode_ws_init(const moe_cfg* cfg, void* ws, void* stream);
  * (the same topk_idx and topk_w bits), then with e = topk_idx[t, j]
  *   h[t, j] = topk_w[t, j] * silu(x_t . W1_e^T) * (x_t . W3_e^T)
  *   y[t]    = sum_j h[t, j] . W2_e^T + sum_s h[t, s] . W2_(E+s)^T
- * (shared experts with weight 1).  Layouts as moe_layer_fwd.  All sums are
- * fp32 (for an fp32 y, relative error of y below 1e-6: the tensor core's
- * truncating sums are kept to 16 instructions); h enters the second product as the sum of two bf16 values (16
- * significant bits) for a bf16 y and of three (24 bits) for an fp32 y; y
- * [T, d] is rounded once to y_type.  Only the weights of
+ * (shared experts with weight 1).  Layouts as moe_layer_fwd.  h enters the
+ * second product as the sum of two bf16 values (16 significant bits) for a
+ * bf16 y and of three (24 bits) for an fp32 y; y [T, d] is rounded once to
+ * y_type.  All sums are fp32.  The tensor core's cut off what a sum has no room
+ * for, towards zero: for each 16 columns at most 2^-23 of the sum of the terms'
+ * magnitudes.  For an fp32 y (and with 4-bit weights for either) they restart
+ * after 16 such steps at most, so that a product loses at most 2^-19 of that,
+ * and are added up rounded to nearest: y measures 1e-7 to 8e-7 of its norm.
+ * For a bf16 y with bf16 weights they run over all columns: at most 2^-13 at
+ * 16384 columns, against 2^-9 to 2^-8 for y's own rounding.  Only the weights of
  * experts that some token picked (and of the shared experts) are read.  A
  * non-finite logit sets MOE_ERR_NONFINITE, as in moe_route, and leaves that
  * token's outputs unspecified.  Infinite and NaN weights of picked experts
@@ -356,7 +361,8 @@ int moe_decode_q4_fwd(const moe_cfg* cfg, int group, const float* logits, const 
 
 /* y [T, n] = x [T, K] . W [n, K]^T for T <= MOE_DECODE_MAX_T rows (the gate
  * projection that gives the layer's logits; dense layers beside it): bf16 x
- * and W, fp32 sums, y fp32 or bf16.  Limits (MOE_ERR_SHAPE): T, n >= 1, K a
+ * and W, fp32 sums as in moe_decode_fwd (a bf16 y loses at most K 2^-27 beside
+ * its rounding), y fp32 or bf16.  Limits (MOE_ERR_SHAPE): T, n >= 1, K a
  * positive multiple of 64, n < 2^31 - 256.  Workspace:
  * moe_linear_workspace_bytes (0 outside the limits), cleared once with
  * moe_linear_ws_init. */

@@ -6,8 +6,10 @@ import torch
 
 from combine_fp32_softmax_gb300 import moe
 from combine_fp32_softmax_gb300.configs import MoEConfig
+from combine_fp32_softmax_gb300.inputs import make_layer_inputs
 from oracle import moe_oracle as O
-from tests.gpu_util import DEV, np64
+from oracle import q4_oracle as Q
+from tests.gpu_util import DEV, np64, relf
 from tests.test_gpu_decode import BF16, F32, Layer, check_y, device_error
 
 pytestmark = pytest.mark.gpu
@@ -81,3 +83,99 @@ def test_a_workspace_for_64_tokens_serves_any_count(group):
         want = part.run(x=x[:T].clone(), logits=z[:T].clone())
         for a, b in zip(got[:3], want[:3]):
             assert torch.equal(a, b), T
+
+
+# ------------------------------------------------------------ fp32 precision
+# The tensor core cuts its running sum of positive terms off below 2^-23 of it, once for each 16 columns.  Sums restart
+# after at most 16 instructions (4 bits: with every group, 8 at most), so that 16 2^-23 = 2^-19 of a sum of positive terms
+# is lost at most; the sums of those runs and groups are added rounded to nearest, 2^-24 each, K / 32 of them at most.
+def cut(K):
+    return 2.0 ** -19 + -(-K // 32) * 2.0 ** -24
+
+
+@pytest.mark.parametrize("T,n,K", [(1, 4096, 4096), (9, 257, 14336), (64, 2048, 4096)])
+@pytest.mark.parametrize("group", [0, 32, 128])
+def test_fp32_linear_sums_of_one_sign(T, n, K, group):
+    g = torch.Generator(device=DEV).manual_seed(T + K)
+    x = torch.randn(T, K, generator=g, device=DEV).abs().to(BF16)
+    W = torch.randn(n, K, generator=g, device=DEV).abs().to(BF16)
+    y, ws = torch.empty(T, n, device=DEV), moe.alloc_linear_workspace(T, n, K)
+    if group:
+        codes, scales = moe.q4_empty(1, n, K, group)
+        moe.moe_q4_quantize(W, codes, scales, group)
+        moe.moe_linear_q4_fwd(x, codes, scales, group, y, ws)
+        W = torch.from_numpy(Q.values(codes, scales, group)[0]).to(DEV)
+    else:
+        moe.moe_linear_fwd(x, W, y, ws)
+    assert device_error(ws) == (0, 0)
+    ref = x.double() @ W.double().T
+    assert ((y.double() - ref).abs() / ref).max().item() <= cut(K)
+
+
+@pytest.mark.parametrize("group", [0, 32, 128])
+@pytest.mark.parametrize("T", [1, 33])
+def test_fp32_layer_sums_of_one_sign(T, group):
+    """x, W1, W3, W2 >= 0: a relative error of a comes through silu at most 1.28 times, b's and h's once; 16 roundings
+    for silu, the gate's weight and the sum over the slots."""
+    cfg = MoEConfig("positive", T, 1024, 1408, 5, 2, S=1, renorm=1)
+    inp = make_layer_inputs(cfg, 3)
+    layer = Layer(cfg, 3, group=group)
+    W = {n: getattr(inp, n).abs() for n in ("W1", "W3", "W2")}
+    layer.x = inp.x.abs()
+    if group:
+        q = {n: Q.quantize(w, group) for n, w in W.items()}
+        layer.dev = [t.to(DEV) for n in W for t in q[n]]
+        W = {n: Q.values(*q[n], group) for n in W}
+    else:
+        layer.dev = [W[n].to(DEV) for n in W]
+    layer.host = W
+    y, _, _, ws = layer.run(F32)
+    assert device_error(ws) == (0, 0)
+    ref = layer.reference().y
+    assert (ref > 0).all()
+    assert (np.abs(np64(y) - ref) / ref).max() <= 2.28 * cut(1024) + cut(1408) + 16 * 2.0 ** -24
+
+
+def layer_with_16_bit_hidden_values(layer):
+    """The layer in fp64 but for h, which is the sum of two bf16 values."""
+    c, x, out = layer.cfg, O.f64(layer.x), np.zeros((layer.cfg.T, layer.cfg.d))
+    W1, W3, W2 = (O.f64(layer.host[n]) for n in ("W1", "W3", "W2"))
+    r = O.route(layer.logits, c.k, c.renorm)
+    for t in range(c.T):
+        for j in range(c.k + c.S):
+            e, w = (r.sel[t, j], r.w[t, j]) if j < c.k else (c.E + j - c.k, 1.0)
+            a = W1[e] @ x[t]
+            h = torch.from_numpy(w * a / (1 + np.exp(-a)) * (W3[e] @ x[t]))
+            high = h.to(BF16).double()
+            out[t] += W2[e] @ (high + (h - high).to(BF16).double()).numpy()
+    return out
+
+
+@pytest.mark.parametrize("T", [1, 9, 40])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_fp32_q4_layer_keeps_24_bits_of_the_hidden_values(T, group):
+    """Errors of random sign, relative to y's norm.  A group's sum loses at most half of 8 2^-23 on average, half of that
+    again as the sum grows: 2.4e-7 for a, b and y each, and a few roundings of 2^-24: below 1.5e-6 together.  An h of
+    16 bits would be off by 2e-6 and more."""
+    layer = Layer(MoEConfig("three_parts", T, 512, 768, 5, 2, S=1), group=group)
+    y, _, _, ws = layer.run(F32)
+    assert device_error(ws) == (0, 0)
+    ref = layer.reference().y
+    assert relf(layer_with_16_bit_hidden_values(layer), ref) > 1.6e-6
+    assert relf(np64(y), ref) <= 1.5e-6
+
+
+@pytest.mark.parametrize("T,n,K", [(1, 2048, 65536), (64, 512, 16384)])
+def test_bf16_linear_sums_of_one_sign_over_many_columns(T, n, K):
+    """A bf16 y: the tensor core's sum runs over all of K and loses at most 2^-23 for each 16 columns; then y's own
+    rounding, 2^-8 at most."""
+    g = torch.Generator(device=DEV).manual_seed(K)
+    x = torch.randn(T, K, generator=g, device=DEV).abs().to(BF16)
+    W = torch.randn(n, K, generator=g, device=DEV).abs().to(BF16)
+    y, ws = torch.empty(T, n, dtype=BF16, device=DEV), moe.alloc_linear_workspace(T, n, K)
+    moe.moe_linear_fwd(x, W, y, ws)
+    assert device_error(ws) == (0, 0)
+    ref = x.double() @ W.double().T
+    err = (y.double() - ref) / ref
+    assert err.abs().max().item() <= 2.0 ** -8 + K / 16 * 2.0 ** -23
+    assert abs(err.mean().item()) <= K / 16 * 2.0 ** -23 + 2.0 ** -8 / (T * n) ** 0.5
