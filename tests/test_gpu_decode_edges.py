@@ -179,3 +179,71 @@ def test_bf16_linear_sums_of_one_sign_over_many_columns(T, n, K):
     err = (y.double() - ref) / ref
     assert err.abs().max().item() <= 2.0 ** -8 + K / 16 * 2.0 ** -23
     assert abs(err.mean().item()) <= K / 16 * 2.0 ** -23 + 2.0 ** -8 / (T * n) ** 0.5
+
+
+# --------------------------------------------- tiles drawn from a counter
+def matrix(W, scales, e, group):
+    """fp64 values of matrix e of device weights."""
+    if not group:
+        return W[e].double()
+    word, q = W[e].view(torch.int32), torch.empty(W.shape[1], 2 * W.shape[2], dtype=torch.float64, device=DEV)
+    for i, c in enumerate(Q.NIBBLE_COLUMN):
+        q[:, c::8] = ((word >> (4 * i)) & 15).double() - 8
+    return q * scales[e, :, :W.shape[1]].double().T.repeat_interleave(group, 1)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("group", [0, 64, 128])
+def test_whole_tiles_drawn_by_the_CTAs(group, dtype):
+    """More than one turn of whole tiles for 152 SMs in either product: 374 tiles of 24 K blocks and 204 of 22 (bf16),
+    374 of 7 and 238 of 6 (4 bits).  Who draws what differs from call to call and from grid to grid; the bits do not."""
+    T, d = (16, 1792) if group else (64, 1536)
+    cfg = MoEConfig("drawn", T, d, 1408, 32, 4, S=2)
+    g = torch.Generator(device=DEV).manual_seed(d)
+    W = [(torch.randn(34, *s, generator=g, device=DEV) * s[1] ** -0.5).to(BF16)
+         for s in ((1408, d), (1408, d), (d, 1408))]
+    z = torch.randn(T, 32, generator=g, device=DEV)
+    for t in range(T):                                    # every expert has as many tokens
+        z[t, (4 * t + torch.arange(4, device=DEV)) % 32] += 20
+    layer = Layer.__new__(Layer)
+    layer.cfg, layer.group, layer.logits = cfg, group, z
+    layer.x = torch.randn(T, d, generator=g, device=DEV).to(BF16)
+    if group:
+        layer.dev = []
+        for w in W:
+            q = moe.q4_empty(*w.shape, group)
+            moe.moe_q4_quantize(w, *q, group)
+            layer.dev += q
+        pairs = list(zip(layer.dev[::2], layer.dev[1::2]))
+    else:
+        layer.dev, pairs = W, [(w, None) for w in W]
+    ws, out = layer.workspace(), layer.outputs(dtype)
+    want = [t.clone() for t in layer.run(dtype, ws=ws, out=out)[:3]]
+    r = O.route(z.cpu(), 4)
+    assert np.array_equal(want[1].cpu().numpy(), r.sel)
+    ref, x = torch.zeros(T, d, dtype=torch.float64, device=DEV), layer.x.double()
+    for e in range(34):
+        token, slot = np.nonzero(r.sel == e) if e < 32 else (np.arange(T), None)
+        w = torch.from_numpy(r.w[token, slot] if e < 32 else np.ones(T)).to(DEV)[:, None]
+        token = torch.from_numpy(token).to(DEV)
+        a, b = (x[token] @ matrix(*pairs[i], e, group).T for i in (0, 1))
+        ref.index_add_(0, token, w * a * torch.sigmoid(a) * b @ matrix(*pairs[2], e, group).T)
+    check_y("y", want[0], ref.cpu().numpy())
+    trash = torch.empty(1 << 26, device=DEV)
+    try:
+        for limit in (0, 1, 37, 151, 0):
+            moe.moe_set_grid_limit(limit)
+            for _ in range(20 if limit != 1 else 1):
+                out[0].fill_(float("nan"))
+                trash.zero_()                             # weights from memory
+                layer.run(dtype, ws=ws, out=out)
+                for a, b in zip(out, want):
+                    assert torch.equal(a, b), limit
+            assert device_error(ws) == (0, 0)
+    finally:
+        moe.moe_set_grid_limit(0)
+    for _ in range(200):
+        layer.run(dtype, ws=ws, out=out)
+    assert device_error(ws) == (0, 0)
+    for a, b in zip(out, want):
+        assert torch.equal(a, b)
