@@ -158,7 +158,15 @@ struct StreamParams {
   int parts;            // bf16 parts of a hidden value
   int acc_cols, acc_bufs;  // bf16 weights: columns of an accumulator, accumulator pairs
   int run;                 // bf16 weights, fp32 y: K blocks that the tensor core adds up at a time
+  int drop;                // testing aid: counts that are left out (kDrop...), 0: none
 };
+
+// Counts that the testing aid leaves out, so that the waits for them run out.
+constexpr int kDropRouted = 1;   // token 0's routing, where the CTAs share it
+constexpr int kDropParts = 2;    // all parts of cut tiles
+constexpr int kDropMeeting = 3;  // CTA 0 at the end of the first product; the next one: of the second
+constexpr int kDropMax = 4;
+int g_drop = 0;
 
 // One product's K blocks and their ranges: range v takes q grains, one more if
 // v < extra.  The first range of this CTA begins at K block u of tile `item`,
@@ -315,7 +323,7 @@ __device__ __noinline__ void route_all(const StreamParams& p, Shared& ss) {
     }
     if (shared_out) {
       __syncwarp();
-      if (lane == 0) red_release_gpu_add(p.err + kCtrRouted, 1);
+      if (lane == 0 && (t != 0 || p.drop != kDropRouted)) red_release_gpu_add(p.err + kCtrRouted, 1);
     }
     t += step;
     if (t < p.T) row_load<EPL>(p.logits + static_cast<size_t>(t) * p.E, p.E, lane, r.v);
@@ -510,6 +518,7 @@ struct Tiles {
   Queue& queue;
   volatile int* abort;
   int which, ticket;
+  bool through = true;  // false once a wait gave up: the role must not take the other product's tiles for this one's
 
   __device__ Tiles(const StreamParams& params, int product, Shared& shared, Queue& q, volatile int* ab)
       : walk(params, product, shared), p(params), ss(shared), queue(q), abort(ab), which(product), ticket(blockIdx.x) {}
@@ -536,7 +545,7 @@ struct Tiles {
       const Plan& pl = walk.pl;
       const int item = __shfl_sync(kFull, ticket, 0);
       t = item < pl.tiles ? locate(item) : make_int4(-1, 0, 0, 0);
-      if (!warp_wait<false>(&ss.tile_empty[queue.slot], queue.phase ^ 1, abort, p.err, 0x2B << 24)) return false;
+      if (!warp_wait<false>(&ss.tile_empty[queue.slot], queue.phase ^ 1, abort, p.err, 0x2B << 24)) return through = false;
       if (lead) {
         ss.tile[queue.slot] = t;
         mbar_arrive(&ss.tile_full[queue.slot]);
@@ -544,7 +553,7 @@ struct Tiles {
         if (t.x >= 0) ticket = static_cast<int>(gridDim.x) + atomicAdd(p.err + kCtrTicket + which, 1);
       }
     } else {
-      if (!warp_wait<false>(&ss.tile_full[queue.slot], queue.phase, abort, p.err, 0x2C << 24)) return false;
+      if (!warp_wait<false>(&ss.tile_full[queue.slot], queue.phase, abort, p.err, 0x2C << 24)) return through = false;
       t = ss.tile[queue.slot];
       __syncwarp();
       if (lead) mbar_arrive(&ss.tile_empty[queue.slot]);
@@ -660,7 +669,7 @@ __device__ bool produce_weights(const StreamParams& p, int which, Shared& ss, ui
       rg.step(p.stages);
     }
   }
-  return true;
+  return walk.through;
 }
 
 // Activation rows: 64 columns at a time, the parts of h below one another.
@@ -708,7 +717,7 @@ __device__ bool produce_columns(const StreamParams& p, int which, Shared& ss, ui
       rg.step(p.stages);
     }
   }
-  return true;
+  return walk.through;
 }
 
 // ----------------------------------------------------- tensor instructions
@@ -815,7 +824,7 @@ __device__ bool issue_bf16(const StreamParams& p, int which, Shared& ss, uint8_t
     }
     tn.step(p.acc_bufs);
   }
-  return true;
+  return walk.through;
 }
 
 template <int G, int N16, int PARTS>
@@ -866,7 +875,7 @@ __device__ bool issue_q4(const StreamParams& p, int which, int box, Shared& ss, 
     if (!with_push<G, KIND>(c.n16, p.parts, [&](auto push) { return issue_segment(push, p, which, box, ss, ring, s, rg, tn, abort); }))
       return false;
   }
-  return true;
+  return walk.through;
 }
 
 // --------------------------------------------------------------- row warps
@@ -932,7 +941,7 @@ __device__ __forceinline__ int* arrivals_of(const StreamParams& p, int which, in
 template <bool WARPS>
 __device__ __forceinline__ void count_part(const StreamParams& p, int which, const Share& sh) {
   __syncwarp();
-  if ((threadIdx.x & (WARPS ? 31 : ~0u)) == 0) red_release_gpu_add(arrivals_of(p, which, sh.v0), 1);
+  if ((threadIdx.x & (WARPS ? 31 : ~0u)) == 0 && p.drop != kDropParts) red_release_gpu_add(arrivals_of(p, which, sh.v0), 1);
 }
 
 // A tile's finished column i, this thread's row of either box.
@@ -1089,7 +1098,7 @@ __device__ bool rows_bf16(const StreamParams& p, int which, Shared& ss, Queue& q
     }
     if (!sh.whole) count_part<true>(p, which, sh);
   }
-  return join_parts<KIND, true>(p, which, ss, abort);
+  return walk.through && join_parts<KIND, true>(p, which, ss, abort);
 }
 
 // 4-bit weights: two sets share a box, a thread one row of it.  A thread turns
@@ -1246,7 +1255,7 @@ __device__ bool rows_q4(const StreamParams& p, int which, Shared& ss, uint8_t* r
     ok = with_push<G, KIND>(Columns<KIND>(p, which, ss, s).n16, p.parts, [&](auto push) {
       return rows_segment<KIND>(push, p, which, ss, ring, walk.walk, s, rg, tn, swap, abort);
     });
-  return ok && join_parts<KIND, false>(p, which, ss, abort);
+  return ok && walk.through && join_parts<KIND, false>(p, which, ss, abort);
 }
 
 // y[t] = its slots' rows in slot order, then the shared experts', in fp32.
@@ -1354,7 +1363,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
       bool ok = warp_wait<Ge::Q4>(&ss.rows_done[which], 0, abort, p.err, (0x25 << 24) | which);
       if (lane == 0) {
         // after a wait that gave up too, so that the other CTAs go on (the error word is set by then)
-        red_release_gpu_add(p.err + kCtrHidden + which, 1);
+        if (blockIdx.x != 0 || p.drop != kDropMeeting + which) red_release_gpu_add(p.err + kCtrHidden + which, 1);
         ok = ok && wait_count(p.err + kCtrHidden + which, gridDim.x, abort, p.err, (0x26 << 24) | which);
       }
       __syncwarp();  // what lane 0 acquired, to the lane that issues the copies
@@ -1544,6 +1553,7 @@ void common_params(StreamParams& p, void* ws, const Layout& L, int T, void* y, i
   p.y_type = y_type;
   p.err = static_cast<int*>(ws);
   p.workers = workers();
+  p.drop = g_drop;
 }
 
 template <int G>
@@ -1620,3 +1630,9 @@ int launch_linear(const LinearArgs& a, cudaStream_t s) {
 }
 
 }  // namespace moe
+
+extern "C" int moe_debug_drop_decode_count(int which) {
+  if (which > moe::kDropMax) return MOE_ERR_ARG;
+  moe::g_drop = which > 0 ? which : 0;
+  return MOE_OK;
+}

@@ -89,6 +89,7 @@ _SIGS = {
     "moe_set_bwd_fused_gemms": ([_I], _I),
     "moe_autotune": ([_CFG] + [_P] * 15 + [_I, _P, ctypes.POINTER(moe_tune_result)], _I),
     "moe_debug_skip_megakernel_task": ([_I], _I),
+    "moe_debug_drop_decode_count": ([_I], _I),
     "moe_debug_megakernel_trace": ([_P, _I], _I),
     "moe_trace_enable": ([_I], _I),
     "moe_trace_reset": ([], _I),
@@ -500,6 +501,10 @@ def moe_gemm_pair_capacity(kind: int) -> int:
 
 def moe_debug_skip_megakernel_task(ticket: int):
     _call("moe_debug_skip_megakernel_task", int(ticket))
+
+
+def moe_debug_drop_decode_count(which: int):
+    _call("moe_debug_drop_decode_count", int(which))
 
 
 def moe_debug_megakernel_trace(buf, records_per_cta: int = 0):

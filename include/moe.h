@@ -593,6 +593,13 @@ enum {
  * CUDA context stays usable.  ticket < 0 disables it (the default).
  * Process-wide, not thread-safe; never set in normal use. */
 int moe_debug_skip_megakernel_task(int ticket);
+/* The same for the calls for a few tokens: a count that CTAs wait for is left
+ * out, 1: a token's routing (calls of more than 20 tokens), 2: the parts of
+ * tiles that several CTAs share, 3 and 4: one CTA at the meeting after the first
+ * and after the second product.  Calls that wait for it end with
+ * MOE_ERR_TIMEOUT after a second or two; their workspace has to be cleared.
+ * which <= 0 disables it (the default). */
+int moe_debug_drop_decode_count(int which);
 
 /* Profiling aid: per-task timeline of the forward MegaKernel.  While `buf`
  * (device memory, 16-byte aligned, at least grid * records_per_cta * 24

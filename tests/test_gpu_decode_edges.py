@@ -1,5 +1,7 @@
 """The layer for a few tokens at its edges: infinite weights, tiles drawn from a counter, one workspace for several
 token counts, sums of one sign, waits that run out."""
+import time
+
 import numpy as np
 import pytest
 import torch
@@ -192,11 +194,8 @@ def matrix(W, scales, e, group):
     return q * scales[e, :, :W.shape[1]].double().T.repeat_interleave(group, 1)
 
 
-@pytest.mark.parametrize("dtype", [F32, BF16])
-@pytest.mark.parametrize("group", [0, 64, 128])
-def test_whole_tiles_drawn_by_the_CTAs(group, dtype):
-    """More than one turn of whole tiles for 152 SMs in either product: 374 tiles of 24 K blocks and 204 of 22 (bf16),
-    374 of 7 and 238 of 6 (4 bits).  Who draws what differs from call to call and from grid to grid; the bits do not."""
+def drawn_layer(group):
+    """The layer on the GPU, and its weights with their scales."""
     T, d = (16, 1792) if group else (64, 1536)
     cfg = MoEConfig("drawn", T, d, 1408, 32, 4, S=2)
     g = torch.Generator(device=DEV).manual_seed(d)
@@ -217,6 +216,16 @@ def test_whole_tiles_drawn_by_the_CTAs(group, dtype):
         pairs = list(zip(layer.dev[::2], layer.dev[1::2]))
     else:
         layer.dev, pairs = W, [(w, None) for w in W]
+    return layer, pairs
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("group", [0, 64, 128])
+def test_whole_tiles_drawn_by_the_CTAs(group, dtype):
+    """More than one turn of whole tiles for 152 SMs in either product: 374 tiles of 24 K blocks and 204 of 22 (bf16),
+    374 of 7 and 238 of 6 (4 bits).  Who draws what differs from call to call and from grid to grid; the bits do not."""
+    layer, pairs = drawn_layer(group)
+    T, d, z = layer.cfg.T, layer.cfg.d, layer.logits
     ws, out = layer.workspace(), layer.outputs(dtype)
     want = [t.clone() for t in layer.run(dtype, ws=ws, out=out)[:3]]
     r = O.route(z.cpu(), 4)
@@ -247,3 +256,93 @@ def test_whole_tiles_drawn_by_the_CTAs(group, dtype):
     assert device_error(ws) == (0, 0)
     for a, b in zip(out, want):
         assert torch.equal(a, b)
+
+
+# ------------------------------------------------------- waits that run out
+ROUTED, PARTS, MEETING_1, MEETING_2 = 1, 2, 3, 4
+
+
+def gives_up(drop, ws, call):
+    """A call that waits for a count which never comes ends within seconds, with the error set."""
+    begin = time.monotonic()
+    try:
+        moe.moe_debug_drop_decode_count(drop)
+        call()
+        code, info = device_error(ws)
+    finally:
+        moe.moe_debug_drop_decode_count(0)
+    assert code == moe.MOE_ERR_TIMEOUT, (code, info)
+    assert 0.5 < time.monotonic() - begin < 20
+    return info >> 24
+
+
+# tiles of the second product cut, and of the first
+GIVE_UP = [MoEConfig("cut_out", 30, 64, 1408, 4, 2), MoEConfig("cut_hidden", 30, 2048, 64, 4, 2)]
+
+
+@pytest.mark.parametrize("cfg", GIVE_UP, ids=lambda c: c.name)
+@pytest.mark.parametrize("drop", [ROUTED, PARTS, MEETING_1, MEETING_2])
+@pytest.mark.parametrize("group,dtype", [(0, F32), (0, BF16), (64, F32)])
+def test_a_layer_call_whose_wait_runs_out_ends_with_an_error(cfg, drop, group, dtype):
+    layer = Layer(cfg, group=group)
+    ws, out = layer.workspace(), layer.outputs(dtype)
+    want = [t.clone() for t in layer.run(dtype, ws=ws, out=out)[:3]]
+    site = gives_up(drop, ws, lambda: layer.run(dtype, ws=ws, out=out))
+    if drop == ROUTED:
+        assert site == 0x20
+    moe.moe_decode_ws_init(cfg, ws)
+    layer.run(dtype, ws=ws, out=out)
+    assert device_error(ws) == (0, 0)
+    for a, b in zip(out, want):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("group", [0, 128])
+def test_a_linear_call_whose_wait_runs_out_ends_with_an_error(group):
+    g = torch.Generator().manual_seed(9)
+    x, W = torch.randn(30, 4096, generator=g).to(BF16).to(DEV), torch.randn(300, 4096, generator=g).to(BF16).to(DEV)
+    q = moe.q4_empty(1, 300, 4096, 128)
+    moe.moe_q4_quantize(W, *q, 128)
+    y, ws = torch.empty(30, 300, device=DEV), moe.alloc_linear_workspace(30, 300, 4096)
+
+    def call():
+        if group:
+            moe.moe_linear_q4_fwd(x, *q, group, y, ws)
+        else:
+            moe.moe_linear_fwd(x, W, y, ws)
+    call()
+    want = y.clone()
+    assert gives_up(PARTS, ws, call) == 0x29
+    moe.moe_linear_ws_init(30, 300, 4096, ws)
+    call()
+    assert device_error(ws) == (0, 0) and torch.equal(y, want)
+
+
+@pytest.mark.parametrize("drop", [MEETING_1, MEETING_2])
+@pytest.mark.parametrize("group", [0, 64])
+def test_calls_with_drawn_tiles_whose_wait_runs_out_end_with_an_error(group, drop):
+    """After the first product the producers are ahead, in the second one's tiles."""
+    layer, _ = drawn_layer(group)
+    ws, out = layer.workspace(), layer.outputs(BF16)
+    want = [t.clone() for t in layer.run(BF16, ws=ws, out=out)[:3]]
+    gives_up(drop, ws, lambda: layer.run(BF16, ws=ws, out=out))
+    moe.moe_decode_ws_init(layer.cfg, ws)
+    layer.run(BF16, ws=ws, out=out)
+    assert device_error(ws) == (0, 0)
+    for a, b in zip(out, want):
+        assert torch.equal(a, b)
+
+
+def test_counts_that_nobody_waits_for_change_nothing():
+    layer = Layer(MoEConfig("few", 20, 256, 320, 8, 2, S=1))   # routed by every CTA itself
+    want = layer.run(F32)
+    try:
+        moe.moe_debug_drop_decode_count(ROUTED)
+        got = layer.run(F32)
+    finally:
+        moe.moe_debug_drop_decode_count(0)
+    assert device_error(got[3]) == (0, 0)
+    for a, b in zip(got[:3], want[:3]):
+        assert torch.equal(a, b)
+    with pytest.raises(moe.MoeError):
+        moe.moe_debug_drop_decode_count(5)
