@@ -139,7 +139,6 @@ struct Product {
   CUtensorMap cols;     // activation rows
   int K, kblocks, rows, row_step, row_tiles;
   int block_log2;       // log2 of the most activation rows of a tile
-  Kind kind;
 };
 
 struct StreamParams {
@@ -1573,8 +1572,6 @@ int decode_g(const DecodeArgs& a, cudaStream_t s) {
   p.parts = a.y_type == MOE_Y_F32 ? 3 : 2;
   p.p[0].block_log2 = Geo<G>::block_log2(1);
   p.p[1].block_log2 = Geo<G>::block_log2(p.parts);
-  p.p[0].kind = kGathered;
-  p.p[1].kind = kRowsOfH;
   if (!fill_product<G>(p.p[0], 0, a.W1, a.W3, mats, c.d_ff, c.d_model) ||
       !fill_product<G>(p.p[1], 1, a.W2, a.W2, mats, c.d_model, c.d_ff) ||
       !map2d(&p.p[0].cols, a.x, c.d_model, c.T, 64, 1) || !map2d(&p.p[1].cols, p.h, c.d_ff, p.parts * Rs, 64, 16))
@@ -1591,7 +1588,6 @@ int linear_g(const LinearArgs& a, cudaStream_t s) {
   common_params(p, a.ws, layout(0, 0, 0), a.T, a.y, a.y_type);
   p.n = a.n;
   p.p[1].block_log2 = Geo<G>::block_log2(1);
-  p.p[1].kind = kRowsOfX;
   if (!fill_product<G>(p.p[1], 1, a.W, a.W, 1, a.n, a.K) || !map2d(&p.p[1].cols, a.x, a.K, a.T, 64, 16))
     return MOE_ERR_CUDA;
   const size_t smem = ring_shape<G>(p, columns_of(p, 1, 1));
