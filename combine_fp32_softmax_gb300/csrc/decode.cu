@@ -32,18 +32,19 @@
 //     floating-point atomics, and nobody waits in the middle of a range.
 //     Where whole tiles are as fast, they are dealt or drawn whole.
 //
-// What it measures (a call in a graph; GB/s are of the bytes that have to be
-// moved, the copy rate is 6790):
-//   d=2048 f=1408 E=64 k=6 S=2, bf16: 1 token 39.5 us, 3500 GB/s; 64 tokens
-//     197 us, 5780 GB/s (7100 while it streams).  One token: start and router
-//     5 us; W1 and W3 17 us, whole tiles on 88 SMs; W2 10 us, on 64; two
+// What it measures (a call in a graph, 1 to 2 us more for calls one by one;
+// GB/s are of the bytes that have to be moved, the copy rate is 6770):
+//   d=2048 f=1408 E=64 k=6 S=2, bf16: 1 token 39.2 us, 3530 GB/s; 64 tokens
+//     197 to 201 us, 5780 GB/s (7100 while it streams).  One token: start and
+//     router 5 us; W1 and W3 17 us, whole tiles on 88 SMs; W2 10 us, on 64; two
 //     grid-wide meetings 5 us.
-//   The same in 4 bits: 1 token 27.8 us; d=4096 f=14336 E=8 k=2, 16 tokens
-//     164 us, 4550 GB/s.  An SM spends some 1700 clocks on a K block of 32 KB,
-//     906 of them the least that turning its codes takes (measured alone: 5
-//     integer instructions at half rate and 4 multiply-adds a word).
-//   Linear form: 37 rows x 4097 x 4096 bf16 17 us, 1 row x 14336 x 4096 in 4
-//     bits 14.1 us.
+//   The same in 4 bits: 1 token 28.6 us; d=4096 f=14336 E=8 k=2, 16 tokens
+//     164 us, 4550 GB/s.  An SM spends 1470 clocks on a K block of 32 KB while
+//     it streams, with 90 % of its issue slots taken; turning the codes takes
+//     906 at the least (measured alone: 5 integer instructions at half rate and
+//     4 multiply-adds a word).
+//   Linear form: 37 rows x 4097 x 4096 bf16 17.6 us, 1 row x 14336 x 4096 in 4
+//     bits 15.8 us.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -75,7 +76,7 @@ constexpr int kTmemCols = 512;
 // always towards zero, which over K = 3840 comes to 1e-5 of an output.  For an
 // fp32 y it adds up 3 K blocks (12 instructions) at a time, 4 where there are
 // no two pairs of accumulators, and the row warps add those sums, rounded to
-// nearest, in the last columns of tensor memory: 5e-7, about what fp32
+// nearest, in the last columns of tensor memory: 5e-7 to 7e-7, about what fp32
 // multiply-adds come to.  A bf16 y, off by 2^-9, needs none of it.
 constexpr int kRunBlocks = 3, kRunBlocksAlone = 4;
 constexpr int kRunCols = 2 * MOE_DECODE_MAX_T;
@@ -242,7 +243,10 @@ __device__ bool wait_count(const int* c, int target, volatile int* abort, int* e
 // tiles take turns of all SMs and a last turn of the rest; one token's 88
 // tiles of W1 and W3 of the layer d=2048 f=1408 k=6 S=2 are faster whole on 88
 // SMs than cut for 152, 17 tiles of a 4097 x 4096 matrix are not.  No range of
-// a cut product has fewer than kMinBlocks.
+// a cut product has fewer than kMinBlocks.  The estimate takes equal blocks as
+// equal in time, which they are not where the SMs' shares of the memory's rate
+// or the experts' rows differ: the ranges of 33 skewed tokens in 4 bits end
+// between 97,000 and 160,000 clocks.
 //
 // Whole tiles of several turns are drawn from a counter: the SMs do not get
 // equal shares of the memory's rate (64 tokens of that layer: 160,000 clocks
