@@ -267,7 +267,8 @@ def _rows(name, t, dtype, rows, cols):
     if t is None:
         return None
     n = t.numel()
-    if (dtype is not None and t.dtype is not dtype) or n < rows * cols or (n > rows * cols and t.shape[-1] != cols):
+    if (dtype is not None and t.dtype is not dtype) or n < rows * cols or (
+            n > rows * cols and t.dim() > 1 and t.shape[-1] != cols):
         raise ValueError(f"{name}: {rows} x {cols} elements of {dtype or 'fp32 or bf16'} expected, got "
                          f"{tuple(t.shape)} of {t.dtype}")
     if not t.is_cuda or not t.is_contiguous():

@@ -93,7 +93,7 @@ def test_right_arrays_pass_and_either_type_of_y_does():
 
 def test_buffers_for_more_tokens_serve_fewer():
     big = dict(logits=zeros(64, E), x=zeros(64, D, dtype=BF16), y=zeros(64, D),
-               topk_idx=zeros(64, K, dtype=I32), topk_w=zeros(64, K))
+               topk_idx=zeros(64, K, dtype=I32), topk_w=zeros(64 * K))
     with pytest.raises(Called):
         moe.moe_decode_fwd(CFG, **layer_args(**big))
     with pytest.raises(Called):
