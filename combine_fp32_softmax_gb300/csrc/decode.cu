@@ -48,6 +48,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstring>
 
 #include "decode.h"
@@ -1524,9 +1525,16 @@ int columns_of(const StreamParams& p, int which, int parts) {
 
 template <int G, bool LAYER, bool RUNS>
 int launch_kernel(StreamParams& p, size_t smem, int grid_limit, cudaStream_t s) {
-  // at each launch: the attribute holds for the current device only
-  if (cudaFuncSetAttribute(stream_kernel<G, LAYER, RUNS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax) != cudaSuccess)
-    return MOE_ERR_CUDA;
+  // The attribute holds for one device, and costs half a microsecond to set.
+  static std::atomic<uint64_t> sized{0};  // a bit a device
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
+  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+  if (!(sized.load(std::memory_order_relaxed) & bit)) {
+    if (cudaFuncSetAttribute(stream_kernel<G, LAYER, RUNS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    sized.fetch_or(bit, std::memory_order_relaxed);
+  }
   const int grid = grid_limit > 0 ? std::min(grid_limit, p.workers) : p.workers;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];

@@ -250,45 +250,58 @@ def _y_type(y) -> int:
     return _Y_TYPES.get(y.dtype, -1)
 
 
-# Addresses of arrays whose sizes and types are known (None is refused by the library).
+# Sizes and types of the arrays are compared with the configuration.  A generation step makes these calls back to back, so
+# the usual case is one expression over all arrays; where that fails, the functions below name the array that is wrong, or
+# find that all may pass.
+_F32, _BF16, _I32, _U8 = torch.float32, torch.bfloat16, torch.int32, torch.uint8
+
+
 def _array(name, t, dtype, n):
-    """Address of a tensor that must hold n elements of a type."""
-    if t is None:
-        return None
-    if t.dtype is not dtype or t.numel() != n:
+    """A tensor must hold n elements of a type (None is refused by the library)."""
+    if t is not None and (t.dtype is not dtype or t.numel() != n):
         raise ValueError(f"{name}: {n} elements of {dtype} expected, got {t.numel()} of {t.dtype}")
-    if not t.is_cuda or not t.is_contiguous():
-        _ptr(t)
-    return t.data_ptr()
 
 
 def _rows(name, t, dtype, rows, cols):
-    """Address of a tensor [rows, cols] of a type (None: any), or one with more such rows, which are left alone."""
+    """A tensor must be [rows, cols] of a type (None: any), or have more such rows, which are left alone."""
     if t is None:
-        return None
+        return
     n = t.numel()
     if (dtype is not None and t.dtype is not dtype) or n < rows * cols or (
             n > rows * cols and t.dim() > 1 and t.shape[-1] != cols):
         raise ValueError(f"{name}: {rows} x {cols} elements of {dtype or 'fp32 or bf16'} expected, got "
                          f"{tuple(t.shape)} of {t.dtype}")
-    if not t.is_cuda or not t.is_contiguous():
-        _ptr(t)
-    return t.data_ptr()
 
 
 def _workspace(ws, nbytes):
+    """Address of a workspace that must have nbytes."""
     if ws is not None and ws.nbytes < nbytes:
         raise ValueError(f"ws: {nbytes} bytes expected, got {ws.nbytes}")
     return _ptr(ws)
 
 
+def _key(c):
+    """The fields of a configuration, T to renorm, in a form that can be looked up."""
+    return bytes(c) if isinstance(c, moe_cfg) else (c.T, c.d, c.f, c.E, c.k, c.S, c.renorm)
+
+
 @functools.lru_cache(maxsize=1024)
-def _decode_sizes(T, d, f, E, k, S, renorm, group=1):
-    """The C configuration of these sizes, the bytes of a workspace, and the elements of a weight array and of the
-    scales of W1 or W3 and of W2."""
-    c = ctypes.byref(moe_cfg(T, d, f, E, k, S, renorm))
-    return (c, int(lib().moe_decode_workspace_bytes(c)), (E + S) * d * f, _q4_scales(E + S, f, d, group),
-            _q4_scales(E + S, d, f, group))
+def _decode_sizes(key, group=1):
+    """The C configuration, the bytes of a workspace, and the elements of the logits, of x, of a routing table, of a weight
+    array and of the scales of W1 or W3 and of W2."""
+    c = moe_cfg(*key) if isinstance(key, tuple) else moe_cfg.from_buffer_copy(key)
+    mats, d, f = c.E + c.n_shared, c.d_model, c.d_ff
+    return (ctypes.byref(c), int(lib().moe_decode_workspace_bytes(ctypes.byref(c))), c.T * c.E, c.T * d, c.T * c.k,
+            mats * d * f, _q4_scales(mats, f, d, group), _q4_scales(mats, d, f, group))
+
+
+def _check_tokens(cfg, logits, x, y, topk_idx, topk_w):
+    c = cfg if isinstance(cfg, moe_cfg) else cfg_of(cfg)
+    _rows("logits", logits, _F32, c.T, c.E)
+    _rows("x", x, _BF16, c.T, c.d_model)
+    _rows("y", y, None, c.T, c.d_model)
+    _rows("topk_idx", topk_idx, _I32, c.T, c.k)
+    _rows("topk_w", topk_w, _F32, c.T, c.k)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -296,47 +309,54 @@ def _linear_bytes(T, n, K):
     return int(lib().moe_linear_workspace_bytes(T, n, K))
 
 
-def _dims(c):
-    """(T, d, f, E, k, S, renorm)."""
-    if isinstance(c, moe_cfg):
-        return c.T, c.d_model, c.d_ff, c.E, c.k, c.n_shared, c.renorm
-    return c.T, c.d, c.f, c.E, c.k, c.S, c.renorm
-
-
 def moe_decode_workspace_bytes(cfg) -> int:
     """Bytes of the workspace (0 outside the limits).  One made for T tokens also serves calls with fewer."""
-    return _decode_sizes(*_dims(cfg))[1]
+    return _decode_sizes(_key(cfg))[1]
 
 
 def moe_decode_ws_init(cfg, ws, stream=None):
-    c, nbytes, *_ = _decode_sizes(*_dims(cfg))
+    c, nbytes, *_ = _decode_sizes(_key(cfg))
     _call("moe_decode_ws_init", c, _workspace(ws, nbytes), _stream(stream))
 
 
 def moe_decode_fwd(cfg, logits, x, W1, W3, W2, y, topk_idx, topk_w, ws, stream=None):
     """Whole layer forward for T <= 64 tokens; y [T, d] fp32 or bf16.  The arrays that have a row for each token may
     have more of them."""
-    dims = T, d, _, E, k, _, _ = _dims(cfg)
-    c, nbytes, n, _, _ = _decode_sizes(*dims)
-    f32, bf16 = torch.float32, torch.bfloat16
-    _call("moe_decode_fwd", c, _rows("logits", logits, f32, T, E), _rows("x", x, bf16, T, d),
-          _array("W1", W1, bf16, n), _array("W3", W3, bf16, n), _array("W2", W2, bf16, n), _rows("y", y, None, T, d),
-          _y_type(y), _rows("topk_idx", topk_idx, torch.int32, T, k), _rows("topk_w", topk_w, f32, T, k),
-          _workspace(ws, nbytes), _stream(stream))
+    c, nbytes, nz, nx, nk, n, _, _ = _decode_sizes(_key(cfg))
+    try:
+        right = (logits.numel() == nz and x.numel() == y.numel() == nx and topk_idx.numel() == topk_w.numel() == nk
+                 and W1.numel() == W3.numel() == W2.numel() == n and logits.dtype is topk_w.dtype is _F32
+                 and x.dtype is W1.dtype is W3.dtype is W2.dtype is _BF16 and topk_idx.dtype is _I32)
+    except AttributeError:  # None
+        right = False
+    if not right:
+        _check_tokens(cfg, logits, x, y, topk_idx, topk_w)
+        for name, t in ("W1", W1), ("W3", W3), ("W2", W2):
+            _array(name, t, _BF16, n)
+    _call("moe_decode_fwd", c, _ptr(logits), _ptr(x), _ptr(W1), _ptr(W3), _ptr(W2), _ptr(y), _y_type(y), _ptr(topk_idx),
+          _ptr(topk_w), _workspace(ws, nbytes), _stream(stream))
 
 
 def moe_decode_q4_fwd(cfg, group, logits, x, W1q, W1s, W3q, W3s, W2q, W2s, y, topk_idx, topk_w, ws, stream=None):
     """The same with 4-bit weights (codes [E+S, rows, cols/2] uint8, scales as q4_empty gives them)."""
-    dims = T, d, _, E, k, _, _ = _dims(cfg)
     group = int(group)
-    c, nbytes, n, up, down = _decode_sizes(*dims, group)
-    f32, bf16, u8 = torch.float32, torch.bfloat16, torch.uint8
+    c, nbytes, nz, nx, nk, n, up, down = _decode_sizes(_key(cfg), group)
     n //= 2
-    _call("moe_decode_q4_fwd", c, group, _rows("logits", logits, f32, T, E), _rows("x", x, bf16, T, d),
-          _array("W1q", W1q, u8, n), _array("W1s", W1s, bf16, up), _array("W3q", W3q, u8, n),
-          _array("W3s", W3s, bf16, up), _array("W2q", W2q, u8, n), _array("W2s", W2s, bf16, down),
-          _rows("y", y, None, T, d), _y_type(y), _rows("topk_idx", topk_idx, torch.int32, T, k),
-          _rows("topk_w", topk_w, f32, T, k), _workspace(ws, nbytes), _stream(stream))
+    try:
+        right = (logits.numel() == nz and x.numel() == y.numel() == nx and topk_idx.numel() == topk_w.numel() == nk
+                 and W1q.numel() == W3q.numel() == W2q.numel() == n and W1s.numel() == W3s.numel() == up
+                 and W2s.numel() == down and logits.dtype is topk_w.dtype is _F32 and topk_idx.dtype is _I32
+                 and x.dtype is W1s.dtype is W3s.dtype is W2s.dtype is _BF16
+                 and W1q.dtype is W3q.dtype is W2q.dtype is _U8)
+    except AttributeError:  # None
+        right = False
+    if not right:
+        _check_tokens(cfg, logits, x, y, topk_idx, topk_w)
+        for name, q, s, ns in ("W1", W1q, W1s, up), ("W3", W3q, W3s, up), ("W2", W2q, W2s, down):
+            _array(name + "q", q, _U8, n)
+            _array(name + "s", s, _BF16, ns)
+    _call("moe_decode_q4_fwd", c, group, _ptr(logits), _ptr(x), _ptr(W1q), _ptr(W1s), _ptr(W3q), _ptr(W3s), _ptr(W2q),
+          _ptr(W2s), _ptr(y), _y_type(y), _ptr(topk_idx), _ptr(topk_w), _workspace(ws, nbytes), _stream(stream))
 
 
 def moe_linear_workspace_bytes(T, n, K) -> int:
@@ -350,26 +370,30 @@ def moe_linear_ws_init(T, n, K, ws, stream=None):
 
 def _linear_shape(x, y):
     """(T, n, K) of y [T, n] = x [T, K] . W^T."""
-    if x.dim() != 2 or y.dim() != 2 or x.shape[0] != y.shape[0]:
-        raise ValueError(f"x [T, K] and y [T, n] expected, got {tuple(x.shape)} and {tuple(y.shape)}")
-    return x.shape[0], y.shape[1], x.shape[1]
+    xs, ys = x.shape, y.shape
+    if len(xs) != 2 or len(ys) != 2 or xs[0] != ys[0]:
+        raise ValueError(f"x [T, K] and y [T, n] expected, got {tuple(xs)} and {tuple(ys)}")
+    if x.dtype is not _BF16:
+        raise ValueError(f"x: {_BF16} expected, got {x.dtype}")
+    return xs[0], ys[1], xs[1]
 
 
 def moe_linear_fwd(x, W, y, ws, stream=None):
     """y [T, n] = x [T, K] . W [n, K]^T for T <= 64 rows; y fp32 or bf16."""
     T, n, K = _linear_shape(x, y)
-    bf16 = torch.bfloat16
-    _call("moe_linear_fwd", T, n, K, _array("x", x, bf16, T * K), _array("W", W, bf16, n * K), _ptr(y), _y_type(y),
-          _workspace(ws, _linear_bytes(T, n, K)), _stream(stream))
+    if W is not None and (W.numel() != n * K or W.dtype is not _BF16):
+        _array("W", W, _BF16, n * K)
+    _call("moe_linear_fwd", T, n, K, _ptr(x), _ptr(W), _ptr(y), _y_type(y), _workspace(ws, _linear_bytes(T, n, K)),
+          _stream(stream))
 
 
 def moe_linear_q4_fwd(x, Wq, Ws, group, y, ws, stream=None):
     """The same with a 4-bit W (codes Wq, scales Ws, groups of `group` columns)."""
     T, n, K = _linear_shape(x, y)
-    bf16 = torch.bfloat16
-    _call("moe_linear_q4_fwd", T, n, K, int(group), _array("x", x, bf16, T * K),
-          _array("Wq", Wq, torch.uint8, n * K // 2), _array("Ws", Ws, bf16, _q4_scales(1, n, K, group)), _ptr(y),
-          _y_type(y), _workspace(ws, _linear_bytes(T, n, K)), _stream(stream))
+    _array("Wq", Wq, _U8, n * K // 2)
+    _array("Ws", Ws, _BF16, _q4_scales(1, n, K, group))
+    _call("moe_linear_q4_fwd", T, n, K, int(group), _ptr(x), _ptr(Wq), _ptr(Ws), _ptr(y), _y_type(y),
+          _workspace(ws, _linear_bytes(T, n, K)), _stream(stream))
 
 
 def _q4_scales(mats, rows, cols, group):
@@ -384,25 +408,34 @@ def q4_empty(mats, rows, cols, group, device="cuda"):
             torch.empty(mats, cols // group, -(-rows // 8) * 8, dtype=torch.bfloat16, device=device))
 
 
-def _q4_arrays(W, codes, scales, group):
-    """Addresses of the arrays, and (mats, rows, cols) of W [mats, rows, cols] or [rows, cols]."""
-    rows, cols = W.shape[-2:]
-    mats = W.shape[0] if W.dim() == 3 else 1
-    n, bf16 = mats * rows * cols, torch.bfloat16
-    return (_array("W", W, bf16, n), _array("codes", codes, torch.uint8, n // 2),
-            _array("scales", scales, bf16, _q4_scales(mats, rows, cols, group)), mats, rows, cols)
+def _q4_matrices(W, codes, scales, group):
+    """(mats, rows, cols) of W [mats, rows, cols] or [rows, cols]."""
+    shape = W.shape
+    if len(shape) == 3:
+        mats, rows, cols = shape
+    elif len(shape) == 2:
+        (rows, cols), mats = shape, 1
+    else:
+        raise ValueError(f"W [mats, rows, cols] or [rows, cols] expected, got {tuple(shape)}")
+    n, ns = mats * rows * cols, _q4_scales(mats, rows, cols, group)
+    if not (W.dtype is _BF16 and codes.dtype is _U8 and scales.dtype is _BF16 and codes.numel() == n // 2
+            and scales.numel() == ns):
+        _array("W", W, _BF16, n)
+        _array("codes", codes, _U8, n // 2)
+        _array("scales", scales, _BF16, ns)
+    return mats, rows, cols
 
 
 def moe_q4_quantize(W, codes, scales, group, stream=None):
     """W [mats, rows, cols] (or [rows, cols]) bf16 -> 4-bit codes and scales of groups of `group` columns."""
-    w, c, s, mats, rows, cols = _q4_arrays(W, codes, scales, group)
-    _call("moe_q4_quantize", w, c, s, mats, rows, cols, int(group), _stream(stream))
+    mats, rows, cols = _q4_matrices(W, codes, scales, group)
+    _call("moe_q4_quantize", _ptr(W), _ptr(codes), _ptr(scales), mats, rows, cols, int(group), _stream(stream))
 
 
 def moe_q4_dequantize(codes, scales, W, group, stream=None):
     """The bf16 values W [mats, rows, cols] (or [rows, cols]) that codes and scales stand for."""
-    w, c, s, mats, rows, cols = _q4_arrays(W, codes, scales, group)
-    _call("moe_q4_dequantize", c, s, w, mats, rows, cols, int(group), _stream(stream))
+    mats, rows, cols = _q4_matrices(W, codes, scales, group)
+    _call("moe_q4_dequantize", _ptr(codes), _ptr(scales), _ptr(W), mats, rows, cols, int(group), _stream(stream))
 
 
 def moe_get_device_error(ws, stream=None):

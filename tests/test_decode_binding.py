@@ -159,3 +159,24 @@ def test_host_tensors_and_strides_are_refused():
     for bad in (torch.zeros(N, F, D, dtype=BF16), zeros(N, D, F, dtype=BF16).transpose(1, 2)):
         with pytest.raises(ValueError, match="CUDA|contiguous"):
             moe.moe_decode_fwd(CFG, **layer_args(W1=bad))
+
+
+@pytest.mark.parametrize("name", ["logits", "x", "W1", "W3", "W2", "topk_idx", "topk_w", "ws"])
+def test_missing_arrays_reach_the_library(name):
+    """None becomes a null pointer, which the library refuses."""
+    with pytest.raises(Called):
+        moe.moe_decode_fwd(CFG, **layer_args(**{name: None}))
+    names = [name] if name[0] != "W" else [name + "q", name + "s"]
+    for n in names:
+        with pytest.raises(Called):
+            moe.moe_decode_q4_fwd(CFG, G, **q4_args(**{n: None}))
+
+
+def test_both_forms_of_a_configuration():
+    c = moe.moe_cfg(T, D, F, E, K, 1, 0)
+    assert moe.moe_decode_workspace_bytes(c) == moe.moe_decode_workspace_bytes(CFG) > 0
+    with pytest.raises(Called):
+        moe.moe_decode_fwd(c, **layer_args())
+    c.T = T + 1                                    # the same object with another number of tokens
+    with pytest.raises(ValueError, match="^logits: "):
+        moe.moe_decode_fwd(c, **layer_args())
