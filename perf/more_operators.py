@@ -250,7 +250,8 @@ def _own(st):
         if not st["grad"]:
             return {"loss": st["loss"], "lse": st["lse"]}
         dlse = (2 * st["z"]) * st["dloss"] * st["lse"] if st["z"] else None
-        moe.moe_xent_bwd(st["x"], st["W"], st["target"], st["lse"], st["dloss"], dlse, st["dx"], st["dW"], st["ws"])
+        moe.moe_xent_bwd(st["x"], st["W"], st["target"], st["loss"], st["lse"], st["dloss"], dlse, st["dx"], st["dW"],
+                         st["ws"])
         return {n: st[n] for n in ("loss", "lse", "dx", "dW")}
     if "ws" not in st:
         st["ws"] = moe.alloc_orthogonalize_workspace(st["mats"], st["rows"], st["cols"])
