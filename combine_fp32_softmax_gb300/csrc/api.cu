@@ -10,6 +10,8 @@
 #include "decode.h"
 #include "gemm.h"
 #include "kernels.h"
+#include "ortho.h"
+#include "xent.h"
 
 namespace moe {
 int megakernel_fwd(const moe_cfg& c, const WsLayout& L, uint8_t* ws, const uint16_t* x, const uint16_t* W1,
@@ -170,6 +172,20 @@ int check_q4_mats(int mats, int rows, int cols, int group) {
   return MOE_OK;
 }
 bool y_type_ok(int y_type) { return y_type == MOE_Y_F32 || y_type == MOE_Y_BF16; }
+
+// Limits of the cross entropy and of the orthogonalised matrices.
+int check_xent(int T, int V, int d) {
+  constexpr int kMax = 1 << 22;
+  return T < 1 || T > kMax || V < 1 || V > kMax || d < 64 || d % 64 || d > 65536 ? MOE_ERR_SHAPE : MOE_OK;
+}
+int check_ortho(int mats, int rows, int cols) {
+  constexpr int kMax = 32768;
+  if (mats < 1 || mats > 65536 || rows < 1 || rows > kMax || cols < 1 || cols > kMax) return MOE_ERR_SHAPE;
+  // tiles of one launch
+  return static_cast<long long>(mats) * ceil_div(rows, kBM) * ceil_div(cols, kBM) < (1ll << 30) ? MOE_OK : MOE_ERR_SHAPE;
+}
+// Sequences of the balance loss: all of one length.
+int check_seqs(const moe_cfg& c, int seqs) { return seqs < 1 || c.T % seqs ? MOE_ERR_SHAPE : MOE_OK; }
 
 int fwd_gemms(const moe_cfg& c, const WsLayout& L, void* ws, const uint16_t* Xp, const uint16_t* x,
               const int32_t* offsets, const int32_t* row_slot, const float* topk_w, const uint16_t* W1,
@@ -612,6 +628,90 @@ int moe_q4_dequantize(const uint8_t* codes, const uint16_t* scales, uint16_t* W,
   MOE_TRY(check_arrays({W, codes, scales}));
   MOE_TRY_CUDA(launch_q4_dequantize(codes, scales, W, mats, rows, cols, group, static_cast<cudaStream_t>(stream)));
   return MOE_OK;
+}
+
+int moe_balance_fwd(const moe_cfg* cfg, const float* logits, const int32_t* topk_idx, const uint8_t* mask, int seqs,
+                    int32_t* counts, float* mean_p, float* loss, float* zloss, void* ws, void* stream) {
+  MOE_TRY(check_cfg(cfg));
+  MOE_TRY(check_seqs(*cfg, seqs));
+  MOE_TRY(check_ptrs({logits, topk_idx, counts, mean_p, loss, zloss}, {mask}, ws));
+  const WsLayout L = ws_layout(*cfg);
+  const moe_cfg& c = *cfg;
+  MOE_TRY_CUDA(launch_balance(logits, topk_idx, mask, c.T, seqs, c.E, c.k, counts, mean_p, loss, zloss,
+                              at<int32_t>(ws, L.hist), at<float>(ws, L.base), at<float>(ws, L.partial),
+                              at<int>(ws, L.err), static_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+int moe_balance_bwd(const moe_cfg* cfg, const float* logits, const int32_t* counts, const uint8_t* mask, int seqs,
+                    const float* dloss, const float* dzloss, const float* dlogits_in, float* dlogits, void* ws,
+                    void* stream) {
+  MOE_TRY(check_cfg(cfg));
+  MOE_TRY(check_seqs(*cfg, seqs));
+  MOE_TRY(check_ptrs({logits, counts, dloss, dzloss, dlogits}, {mask, dlogits_in}, ws));
+  const moe_cfg& c = *cfg;
+  MOE_TRY_CUDA(launch_balance_bwd(logits, counts, mask, dloss, dzloss, c.T, seqs, c.E, c.k, dlogits_in, dlogits,
+                                  static_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+size_t moe_xent_workspace_bytes(int T, int V, int d, int backward) {
+  return check_xent(T, V, d) == MOE_OK ? xent_workspace_bytes(T, V, d, backward != 0) : 0;
+}
+
+int moe_xent_ws_init(void* ws, void* stream) {
+  MOE_TRY(check_ptrs({}, {}, ws));
+  MOE_TRY_CUDA(cudaMemsetAsync(ws, 0, kErrRegionBytes, static_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+int moe_xent_fwd(int T, int V, int d, const uint16_t* x, const uint16_t* W, const void* target, int target_type,
+                 float* loss, float* lse, void* ws, void* stream) {
+  MOE_TRY(check_xent(T, V, d));
+  if (target_type != MOE_I32 && target_type != MOE_I64) return MOE_ERR_ARG;
+  MOE_TRY(check_ptrs({x, W, target, loss, lse}, {}, ws));
+  XentArgs a{};
+  a.T = T;
+  a.V = V;
+  a.d = d;
+  a.x = x;
+  a.W = W;
+  a.target = target;
+  a.target_type = target_type;
+  a.loss = loss;
+  a.lse = lse;
+  a.ws = ws;
+  a.grid_limit = g_grid_limit;
+  return launch_xent_fwd(a, static_cast<cudaStream_t>(stream));
+}
+
+int moe_xent_bwd(int T, int V, int d, const uint16_t* x, const uint16_t* W, const void* target, int target_type,
+                 const float* loss, const float* lse, const float* dloss, const float* dlse, void* dx, int dx_type,
+                 void* dW, int dW_type, void* ws, void* stream) {
+  MOE_TRY(check_xent(T, V, d));
+  if ((target_type != MOE_I32 && target_type != MOE_I64) || (!dx && !dW)) return MOE_ERR_ARG;
+  if ((dx && !y_type_ok(dx_type)) || (dW && !y_type_ok(dW_type))) return MOE_ERR_ARG;
+  MOE_TRY(check_ptrs({x, W, target, loss, lse, dloss}, {dlse, dx, dW}, ws));
+  XentArgs a{T, V, d, x, W, target, target_type, const_cast<float*>(loss), const_cast<float*>(lse), dloss, dlse, dx, dW,
+             dx_type, dW_type, ws, g_grid_limit};
+  return launch_xent_bwd(a, static_cast<cudaStream_t>(stream));
+}
+
+size_t moe_orthogonalize_workspace_bytes(int mats, int rows, int cols) {
+  return check_ortho(mats, rows, cols) == MOE_OK ? ortho_workspace_bytes(mats, rows, cols) : 0;
+}
+
+int moe_orthogonalize_ws_init(void* ws, void* stream) { return moe_xent_ws_init(ws, stream); }
+
+int moe_orthogonalize(int mats, int rows, int cols, const void* G, int g_type, uint16_t* O, int steps, void* ws,
+                      void* stream) {
+  MOE_TRY(check_ortho(mats, rows, cols));
+  if (steps < 1 || steps > MOE_ORTHOGONALIZE_MAX_STEPS) return MOE_ERR_SHAPE;
+  if (!y_type_ok(g_type)) return MOE_ERR_ARG;
+  MOE_TRY(check_ptrs({G, O}, {}, ws));
+  if (static_cast<const void*>(O) == G) return MOE_ERR_ARG;
+  return launch_ortho(OrthoArgs{mats, rows, cols, G, g_type, O, steps, ws, g_grid_limit},
+                      static_cast<cudaStream_t>(stream));
 }
 
 int moe_get_device_error(const void* ws, void* stream, int* code, int* info) {

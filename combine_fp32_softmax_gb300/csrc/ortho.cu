@@ -1,0 +1,433 @@
+// Matrices to nearly orthogonal ones: X = G / (|G| + eps) in the Frobenius norm,
+// then a number of steps of
+//   A = X X^T,  B = b A + c A A,  X <- a X + B X
+// with (a, b, c) = (3.4445, -4.7750, 2.0315), which bring every singular value of
+// X near 1 (between 0.7 and 1.2 after five steps for those above 0.002).  Where
+// there are more rows than columns the products are X^T X and X B, so that A is
+// always the smaller of the two and nothing is transposed in memory.
+//
+// X, A and B are kept in fp16 between the products, scaled by powers of two so
+// that their whole range is normal numbers: a rounding is at most 2^-11 of a value, eight
+// times finer than bf16's at the same tensor-core rate.  Five steps multiply
+// what is rounded away of a small singular value by 485 as they do the value,
+// and with bf16 the result would be off by six times its own final rounding; with
+// fp16 by less than that rounding.  The norm itself enters as an fp32 factor of
+// the first step, so a bf16 G is taken exactly.
+//
+// A and A A are symmetric: only the tiles on and above the diagonal are computed,
+// and their epilogue stores both halves.
+#include <algorithm>
+#include <cstring>
+
+#include <cuda_fp16.h>
+
+#include "dense.cuh"
+#include "ortho.h"
+
+namespace moe {
+namespace {
+
+constexpr int kCodeOrtho = 0x19;
+constexpr float kNsA = 3.4445f, kNsB = -4.7750f, kNsC = 2.0315f;
+constexpr float kNsEps = 1e-7f;
+// |X| <= 1 in the Frobenius norm at first and its singular values stay below
+// 1.3, so entries of X, A, B are below 1.3, 1.7, 14: times 2^10, 2^12, 2^11 they
+// stay below fp16's 65504, and entries 2^-24, 2^-26, 2^-25 are still normal.
+constexpr float kSX = 1024.f, kSA = 4096.f, kSB = 2048.f;
+constexpr int kSXLog2 = 10;
+// Below this norm of X the cubic term of a step is under 2^-19 of the linear one
+// for five steps on: the result is a^steps X.
+constexpr float kTiny = 0x1p-17f;
+constexpr int kNormParts = 1024;  // partial sums of squares of a matrix, at most
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float2 unpack_f16(uint32_t v) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+
+// ------------------------------------------------------------- products
+enum OrthoKind : int { kGramWide, kGramTall, kSquare, kUpdateWide, kUpdateTall };
+
+template <int KIND>
+struct OrthoOp {
+  static constexpr bool SYM = KIND == kGramWide || KIND == kGramTall || KIND == kSquare;
+  static constexpr bool A_MN = KIND == kGramTall;
+  static constexpr bool B_MN = KIND == kGramTall || KIND == kUpdateWide;
+  static constexpr bool F16 = true, ONE = false;
+  struct Params : DenseParams {
+    const float* scal;   // [mats]: X of the first step is scal times what is stored; 0: matrix needs no products
+    int first;           // the first step
+    const __half* old;   // square: A; update: X, laid out as the result
+    int pitch;           // of old
+    uint16_t* O;         // last update where its rows are not whole 16-byte pieces (else null)
+    int bf16;            // last update: bf16 results
+  };
+  template <int CG>
+  static __device__ __forceinline__ DenseTile tile(const Params& p, int i, int rank) {
+    int mat, mb, nb;
+    if constexpr (SYM) {  // row mb has the tiles mb, mb + 1, ... of its columns
+      const int per = p.nt * (p.nt + 1) / 2;
+      mat = i / per;
+      int j = i - mat * per;
+      mb = 0;
+      while (j >= p.nt - mb) j -= p.nt - mb++;
+      nb = mb + j;
+    } else {
+      const int per = p.mt * p.nt;
+      mat = i / per;
+      const int j = i - mat * per;
+      mb = j / p.nt;
+      nb = j - mb * p.nt;
+    }
+    const bool skip = p.scal[mat] == 0.f;
+    return {mat, mb * DensePipe<CG>::TILE_M + rank * kBM, nb * kBN, 0, skip ? 0 : p.nkb};
+  }
+  static __device__ __forceinline__ void coords(const Params&, const DenseTile& t, int kb, int& ak, int& am, int& bk,
+                                                int& bn) {
+    ak = bk = kb * kBK;
+    am = t.m0;
+    bn = t.n0;
+  }
+  static __device__ __forceinline__ float pre(const Params& p, const DenseTile& t, const DenseEpi&) {
+    return p.first ? p.scal[t.mat] : 1.f / kSX;
+  }
+  static __device__ __forceinline__ void epilogue(const Params& p, const DenseTile& t, DenseEpi& e, float r,
+                                                  uint32_t (&acc)[4][32]) {
+    if (t.kb1 == t.kb0) return;
+    const int x0 = t.n0 + 128 * e.part, y = t.m0 + 32 * e.q;
+    // gram: A = r^2 sums; square: B = b A + c sums; update: X' = a r X + r sums
+    const float fs = KIND == kSquare                         ? kNsC * (kSB / (kSA * kSA))
+                     : (KIND == kGramWide || KIND == kGramTall) ? r * r * kSA
+                                                             : r * ((p.bf16 ? 1.f : kSX) / kSB);
+    const float fo = KIND == kSquare ? kNsB * (kSB / kSA) : kNsA * r * (p.bf16 ? 1.f : kSX);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int x = x0 + 32 * c;
+      if (x >= p.N) break;
+      float v[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = fs * __uint_as_float(acc[c][j]);
+      if constexpr (KIND == kSquare || !SYM) {
+        if (y + e.lane < p.M) {
+          const uint4* from = reinterpret_cast<const uint4*>(
+              p.old + (static_cast<size_t>(t.mat) * p.M + y + e.lane) * p.pitch + x);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const uint4 w = from[u];  // x is a multiple of 32, the pitch of 64
+            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 o = unpack_f16(ws[k]);
+              v[8 * u + 2 * k] = fmaf(fo, o.x, v[8 * u + 2 * k]);
+              v[8 * u + 2 * k + 1] = fmaf(fo, o.y, v[8 * u + 2 * k + 1]);
+            }
+          }
+        }
+      }
+      uint32_t w[16];
+      if (!SYM && p.bf16) {
+#pragma unroll
+        for (int u = 0; u < 16; ++u) w[u] = pack_bf16(v[2 * u], v[2 * u + 1]);
+        if (p.O) {  // no TMA store: the warp writes its 32 x 32 values row by row
+          __syncwarp();
+          stage_row64(e.stg, e.lane, w);
+          __syncwarp();
+          uint16_t* out = p.O + (static_cast<size_t>(t.mat) * p.M + y) * p.N + x;
+          if (x + e.lane < p.N)
+            for (int i = 0; i < 32 && y + i < p.M; ++i)
+              out[static_cast<size_t>(i) * p.N + e.lane] = *reinterpret_cast<const uint16_t*>(
+                  e.stg + i * 64 + (((e.lane >> 3) ^ ((i >> 1) & 3)) << 4) + (e.lane & 7) * 2);
+          continue;
+        }
+      } else {
+#pragma unroll
+        for (int u = 0; u < 16; ++u) w[u] = pack_f16(v[2 * u], v[2 * u + 1]);
+      }
+      dense_store(e, w, &p.tmO, x, y, t.mat);
+      if constexpr (SYM) {
+        if (t.n0 >= (t.m0 / kBN + 1) * kBN) {  // a tile off the diagonal: also to the other side
+          uint8_t* buf = e.stg + (e.chunks & 1) * kChunkBytes;
+          staging_reuse_wait<1>(e.chunks);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {  // row j of the transposed chunk: this lane's column is its row
+            const uint16_t h = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
+            *reinterpret_cast<uint16_t*>(buf + j * 64 + (((e.lane >> 3) ^ ((j >> 1) & 3)) << 4) + (e.lane & 7) * 2) = h;
+          }
+          staging_publish();
+          if (e.lane == 0) {
+            tma_store_3d(&p.tmO, buf, y, x, t.mat);
+            bulk_commit();
+          }
+          ++e.chunks;
+        }
+      }
+    }
+  }
+};
+
+// ---------------------------------------------------------------- the norm
+// Elements [lo, hi) of G in pieces of 16 bytes with the ends that are not whole
+// pieces taken one by one: a matrix may begin anywhere in a piece.
+template <typename F, bool BF16>
+__device__ __forceinline__ void for_elements(const void* G, size_t lo, size_t hi, int tid, int threads, F f) {
+  constexpr int VE = BF16 ? 8 : 4;
+  const size_t a = min((lo + VE - 1) / VE * VE, hi), b = max(a, hi / VE * VE);
+  auto one = [&](size_t i) {
+    f(i, BF16 ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(G)[i]) << 16)
+              : static_cast<const float*>(G)[i]);
+  };
+  if (tid < static_cast<int>(a - lo)) one(lo + tid);
+  if (tid < static_cast<int>(hi - b)) one(b + tid);
+  for (size_t i = a + static_cast<size_t>(tid) * VE; i < b; i += static_cast<size_t>(threads) * VE) {
+    const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(G) + i * (BF16 ? 2 : 4));
+    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (BF16) {
+        f(i + 2 * k, bf16_lo(ws[k]));
+        f(i + 2 * k + 1, bf16_hi(ws[k]));
+      } else {
+        f(i + k, __uint_as_float(ws[k]));
+      }
+    }
+  }
+}
+
+// Elements of the part-th of `parts` parts of a matrix.
+__device__ __forceinline__ void part_range(size_t n, int mat, int part, int parts, size_t& lo, size_t& hi) {
+  const size_t per = (n + parts - 1) / parts;
+  lo = static_cast<size_t>(mat) * n + min(n, per * part);
+  hi = static_cast<size_t>(mat) * n + min(n, per * (part + 1));
+}
+
+// Sums of squares of the parts of each matrix.
+template <bool BF16>
+__global__ void __launch_bounds__(256) ortho_norm_kernel(const void* __restrict__ G, size_t n, int mats,
+                                                         double* __restrict__ sums) {
+  griddep_wait();
+  griddep_launch_dependents();
+  __shared__ double ws[8];
+  const int parts = gridDim.x;
+  for (int mat = blockIdx.y; mat < mats; mat += gridDim.y) {
+    size_t lo, hi;
+    part_range(n, mat, blockIdx.x, parts, lo, hi);
+    float s = 0.f;
+    auto add = [&](size_t, float v) { s = fmaf(v, v, s); };
+    for_elements<decltype(add), BF16>(G, lo, hi, threadIdx.x, 256, add);
+    double d = s;
+#pragma unroll
+    for (int off = 16; off; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
+    if ((threadIdx.x & 31) == 0) ws[threadIdx.x >> 5] = d;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      d = 0.;
+      for (int i = 0; i < 8; ++i) d += ws[i];
+      sums[static_cast<size_t>(mat) * parts + blockIdx.x] = d;
+    }
+    __syncthreads();
+  }
+}
+
+// G to fp16 with its norm between 2^9 and 2^10, and what the first step makes of
+// that.  A matrix of zeros, or so small beside eps that the steps are linear, or
+// without a finite norm, is finished here.
+template <bool BF16>
+__global__ void __launch_bounds__(256)
+    ortho_cast_kernel(const void* __restrict__ G, int rows, int cols, int pitch, int mats, const double* __restrict__ sums,
+                      int steps, float* __restrict__ scal, __half* __restrict__ X, uint16_t* __restrict__ O) {
+  griddep_wait();
+  griddep_launch_dependents();
+  __shared__ float shared_norm;
+  const size_t n = static_cast<size_t>(rows) * cols;
+  const int parts = gridDim.x;
+  for (int mat = blockIdx.y; mat < mats; mat += gridDim.y) {
+    if (threadIdx.x < 32) {
+      double d = 0.;
+      for (int i = threadIdx.x; i < parts; i += 32) d += sums[static_cast<size_t>(mat) * parts + i];
+#pragma unroll
+      for (int off = 16; off; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
+      if (threadIdx.x == 0) shared_norm = static_cast<float>(sqrt(d));
+    }
+    __syncthreads();
+    const float norm = shared_norm;
+    __syncthreads();
+    const float inv = 1.f / (norm + kNsEps);
+    size_t lo, hi;
+    part_range(n, mat, blockIdx.x, parts, lo, hi);
+    const size_t at = static_cast<size_t>(mat) * n;
+    if (!(norm * inv >= kTiny) || isinf(norm)) {  // also where the norm is NaN
+      float f = isfinite(norm) ? inv : __uint_as_float(0x7fc00000u);
+      for (int i = 0; i < steps; ++i) f *= kNsA;
+      auto put = [&](size_t i, float v) { O[i] = static_cast<uint16_t>(pack_bf16(f * v, 0.f)); };
+      if (isfinite(norm))
+        for_elements<decltype(put), BF16>(G, lo, hi, threadIdx.x, 256, put);
+      else
+        for (size_t i = lo + threadIdx.x; i < hi; i += 256) O[i] = 0x7fc0;
+      if (blockIdx.x == 0 && threadIdx.x == 0) scal[mat] = 0.f;
+      continue;
+    }
+    int ex;
+    frexpf(norm, &ex);
+    const int k = kSXLog2 - ex;
+    if (blockIdx.x == 0 && threadIdx.x == 0) scal[mat] = ldexpf(inv, -k);
+    const float up = ldexpf(1.f, k);  // the norm is between 2^-41 and 2^64 here: 2^k is a normal number
+    __half* Xm = X + static_cast<size_t>(mat) * rows * pitch;
+    auto put = [&](size_t i, float v) {
+      const uint32_t j = static_cast<uint32_t>(i - at), row = j / cols;
+      Xm[static_cast<size_t>(row) * pitch + (j - row * cols)] = __float2half_rn(up * v);
+    };
+    for_elements<decltype(put), BF16>(G, lo, hi, threadIdx.x, 256, put);
+  }
+}
+
+// ------------------------------------------------------------------ host
+struct Plan {
+  int small, pitch, spitch, parts;
+  size_t err, sums, scal, X[2], A, B, total;
+};
+Plan plan(int mats, int rows, int cols) {
+  Plan p{};
+  p.small = std::min(rows, cols);
+  p.pitch = ceil_div(cols, 64) * 64;
+  p.spitch = ceil_div(p.small, 64) * 64;
+  const long long n = static_cast<long long>(rows) * cols;
+  p.parts = static_cast<int>(std::max(1ll, std::min<long long>(kNormParts, n / 32768)));
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o = align_up(o + bytes, 256);
+    return at;
+  };
+  p.err = take(kErrRegionBytes);
+  p.sums = take(sizeof(double) * p.parts * mats);
+  p.scal = take(sizeof(float) * mats);
+  for (int i = 0; i < 2; ++i) p.X[i] = take(size_t(2) * mats * rows * p.pitch);
+  p.A = take(size_t(2) * mats * p.small * p.spitch);
+  p.B = take(size_t(2) * mats * p.small * p.spitch);
+  p.total = o;
+  return p;
+}
+
+template <int KIND>
+int launch_kind(typename OrthoOp<KIND>::Params& p, int mats, const OrthoArgs& a, int trace, cudaStream_t s) {
+  const bool single = p.M <= kBM;
+  p.nt = ceil_div(p.N, kBN);
+  p.mt = single ? 1 : ceil_div(p.M, 2 * kBM);
+  p.total = mats * (OrthoOp<KIND>::SYM ? p.nt * (p.nt + 1) / 2 : p.mt * p.nt);
+  return single ? dense_launch<OrthoOp<KIND>, 1>(p, a.grid_limit, trace, s)
+                : dense_launch<OrthoOp<KIND>, 2>(p, a.grid_limit, trace, s);
+}
+
+}  // namespace
+
+size_t ortho_workspace_bytes(int mats, int rows, int cols) { return plan(mats, rows, cols).total; }
+
+int launch_ortho(const OrthoArgs& a, cudaStream_t s) {
+  const Plan L = plan(a.mats, a.rows, a.cols);
+  uint8_t* ws = static_cast<uint8_t*>(a.ws);
+  int* err = reinterpret_cast<int*>(ws + L.err);
+  double* sums = reinterpret_cast<double*>(ws + L.sums);
+  float* scal = reinterpret_cast<float*>(ws + L.scal);
+  __half* X[2] = {reinterpret_cast<__half*>(ws + L.X[0]), reinterpret_cast<__half*>(ws + L.X[1])};
+  __half* A = reinterpret_cast<__half*>(ws + L.A);
+  __half* B = reinterpret_cast<__half*>(ws + L.B);
+  const bool bf = a.g_type == MOE_Y_BF16, wide = a.rows <= a.cols;
+  const dim3 grid(L.parts, std::min(a.mats, 65535));
+  {
+    TraceScope trace_scope(MOE_K_ORTHO_NORM, s);
+    const size_t n = static_cast<size_t>(a.rows) * a.cols;
+    cudaError_t e = bf ? launch_pdl(ortho_norm_kernel<true>, grid, dim3(256), 0, s, a.G, n, a.mats, sums)
+                       : launch_pdl(ortho_norm_kernel<false>, grid, dim3(256), 0, s, a.G, n, a.mats, sums);
+    if (e == cudaSuccess)
+      e = bf ? launch_pdl(ortho_cast_kernel<true>, grid, dim3(256), 0, s, a.G, a.rows, a.cols, L.pitch, a.mats, sums, a.steps,
+                          scal, X[0], a.O)
+             : launch_pdl(ortho_cast_kernel<false>, grid, dim3(256), 0, s, a.G, a.rows, a.cols, L.pitch, a.mats, sums,
+                          a.steps, scal, X[0], a.O);
+    if (e != cudaSuccess) return MOE_ERR_CUDA;
+  }
+  const int m = L.small;
+  constexpr auto kF16 = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  auto base = [&](DenseParams& p, int code, int M, int N, int K) {
+    p.M = M;
+    p.N = N;
+    p.nkb = ceil_div(K, kBK);
+    p.run_kb = p.nkb;  // rounded to 16 bits
+    p.code = kCodeOrtho + code;
+    p.err = err;
+  };
+  const uint32_t bn = m <= kBM ? 256 : 128;  // columns of B that a CTA loads where C has m rows
+  int rc = MOE_OK;
+  for (int it = 0; it < a.steps && rc == MOE_OK; ++it) {
+    const __half* Xi = X[it & 1];
+    __half* Xo = X[(it + 1) & 1];
+    const bool last = it + 1 == a.steps;
+    auto gram = [&](auto& p) {
+      std::memset(&p, 0, sizeof(p));
+      base(p, 0, m, m, wide ? a.cols : a.rows);
+      p.scal = scal;
+      p.first = it == 0;
+      bool ok = dense_map_out(&p.tmO, A, kF16, m, m, a.mats, L.spitch);
+      if (wide)
+        ok = ok && dense_map_k(&p.tmA, Xi, true, a.cols, a.rows, a.mats, L.pitch, 128) &&
+             dense_map_k(&p.tmB, Xi, true, a.cols, a.rows, a.mats, L.pitch, bn);
+      else
+        ok = ok && dense_map_mn(&p.tmA, Xi, true, L.pitch, a.rows, a.mats, 2) &&
+             dense_map_mn(&p.tmB, Xi, true, L.pitch, a.rows, a.mats, bn / 64);
+      return ok;
+    };
+    if (wide) {
+      OrthoOp<kGramWide>::Params p;
+      rc = gram(p) ? launch_kind<kGramWide>(p, a.mats, a, MOE_K_ORTHO_GRAM, s) : MOE_ERR_CUDA;
+    } else {
+      OrthoOp<kGramTall>::Params p;
+      rc = gram(p) ? launch_kind<kGramTall>(p, a.mats, a, MOE_K_ORTHO_GRAM, s) : MOE_ERR_CUDA;
+    }
+    if (rc != MOE_OK) break;
+    {
+      OrthoOp<kSquare>::Params p;
+      std::memset(&p, 0, sizeof(p));
+      base(p, 1, m, m, m);
+      p.scal = scal;
+      p.old = A;
+      p.pitch = L.spitch;
+      if (!dense_map_k(&p.tmA, A, true, m, m, a.mats, L.spitch, 128) ||
+          !dense_map_k(&p.tmB, A, true, m, m, a.mats, L.spitch, bn) || !dense_map_out(&p.tmO, B, kF16, m, m, a.mats, L.spitch))
+        return MOE_ERR_CUDA;
+      if ((rc = launch_kind<kSquare>(p, a.mats, a, MOE_K_ORTHO_SQUARE, s)) != MOE_OK) break;
+    }
+    auto update = [&](auto& p) {
+      std::memset(&p, 0, sizeof(p));
+      base(p, 2, a.rows, a.cols, m);
+      p.scal = scal;
+      p.first = it == 0;
+      p.old = Xi;
+      p.pitch = L.pitch;
+      p.bf16 = last;
+      const bool tma = !last || a.cols % 8 == 0;
+      if (!tma) p.O = a.O;
+      bool ok = !tma || (last ? dense_map_out(&p.tmO, a.O, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.cols, a.rows, a.mats, a.cols)
+                              : dense_map_out(&p.tmO, Xo, kF16, a.cols, a.rows, a.mats, L.pitch));
+      const uint32_t ubn = a.rows <= kBM ? 256 : 128;
+      if (wide)
+        ok = ok && dense_map_k(&p.tmA, B, true, m, m, a.mats, L.spitch, 128) &&
+             dense_map_mn(&p.tmB, Xi, true, L.pitch, a.rows, a.mats, ubn / 64);
+      else
+        ok = ok && dense_map_k(&p.tmA, Xi, true, a.cols, a.rows, a.mats, L.pitch, 128) &&
+             dense_map_k(&p.tmB, B, true, m, m, a.mats, L.spitch, ubn);
+      return ok;
+    };
+    if (wide) {
+      OrthoOp<kUpdateWide>::Params p;
+      rc = update(p) ? launch_kind<kUpdateWide>(p, a.mats, a, MOE_K_ORTHO_UPDATE, s) : MOE_ERR_CUDA;
+    } else {
+      OrthoOp<kUpdateTall>::Params p;
+      rc = update(p) ? launch_kind<kUpdateTall>(p, a.mats, a, MOE_K_ORTHO_UPDATE, s) : MOE_ERR_CUDA;
+    }
+  }
+  return rc;
+}
+
+}  // namespace moe

@@ -1,0 +1,544 @@
+// Softmax cross entropy of z = x W^T over a vocabulary of V rows, without
+// keeping the logits.
+//
+//   forward   lse_t = log sum_v exp z_tv,  loss_t = lse_t - z_t,target(t)
+//   backward  D_tv = (g_t + h_t) exp(z_tv - lse_t) - [v = target(t)] g_t,
+//             dx = D W, dW = D^T x, g and h the gradients of loss and lse
+//
+// The forward is one product whose epilogue keeps, of each row's 128 logits of
+// a tile half, their maximum m and sum of exp(z - m); a second kernel joins a
+// row's pairs.  loss is formed as (m - z_target) + log(sum), so that a certain
+// token's small loss does not come out of the difference of two large numbers.
+//
+// The backward takes the vocabulary in pieces: the product again, with an
+// epilogue that turns logits into D (bf16, or the sum of two bf16 values where a
+// gradient is kept in fp32), then the two products that read D.
+#include <algorithm>
+#include <cstring>
+
+#include "dense.cuh"
+#include "xent.h"
+
+namespace moe {
+namespace {
+
+constexpr int kCodeXent = 0x11;  // + operation, in the error word of a wait that ran out
+
+// K blocks of a run of sums where fp32 results come out: 16 tensor-core steps.
+constexpr int kExactRun = 4;
+// Bytes of D that a piece of the vocabulary takes at least, and its columns at least.
+constexpr size_t kPieceBytes = size_t(512) << 20;
+constexpr int kPieceCols = 8192;
+
+struct Target {
+  const void* p;
+  int wide;  // int64
+};
+// The target of row t, or -1 for none.
+__device__ __forceinline__ int load_target(const Target& g, int t, int V) {
+  const long long v = g.wide ? static_cast<const long long*>(g.p)[t] : static_cast<const int*>(g.p)[t];
+  return v >= 0 && v < V ? static_cast<int>(v) : -1;
+}
+
+// Tiles whose rows change fastest: the row blocks that share a tile of W run at
+// the same time, and x stays in L2.
+template <int CG>
+__device__ __forceinline__ DenseTile rows_first(const DenseParams& p, int i, int rank) {
+  const int nb = i / p.mt, mb = i - nb * p.mt;
+  return {0, mb * DensePipe<CG>::TILE_M + rank * kBM, nb * kBN, 0, p.nkb};
+}
+
+// ------------------------------------------------------------- forward
+struct StatsOp {
+  static constexpr bool A_MN = false, B_MN = false, F16 = false, ONE = true;
+  struct Params : DenseParams {
+    Target target;
+    float2* part;  // [T][2 nt]: maximum and sum of exp of half a tile's logits
+    float* zt;     // [T] the target's logit
+  };
+  template <int CG>
+  static __device__ __forceinline__ DenseTile tile(const Params& p, int i, int rank) {
+    return rows_first<CG>(p, i, rank);
+  }
+  static __device__ __forceinline__ void coords(const Params&, const DenseTile& t, int kb, int& ak, int& am, int& bk,
+                                                int& bn) {
+    ak = bk = kb * kBK;
+    am = t.m0;
+    bn = t.n0;
+  }
+  static __device__ __forceinline__ int pre(const Params& p, const DenseTile& t, const DenseEpi& e) {
+    const int row = t.m0 + 32 * e.q + e.lane;
+    return row < p.M ? load_target(p.target, row, p.N) : -1;
+  }
+  static __device__ __forceinline__ void epilogue(const Params& p, const DenseTile& t, DenseEpi& e, int target,
+                                                  uint32_t (&acc)[4][32]) {
+    const int row = t.m0 + 32 * e.q + e.lane;
+    const int col = t.n0 + 128 * e.part;
+    const int n = p.N - col;  // columns that exist
+    if (n < 128) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (32 * c + j >= n) acc[c][j] = 0xff800000u;  // -inf: exp is 0
+    }
+    float m4[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      m4[c] = __uint_as_float(acc[c][0]);
+#pragma unroll
+      for (int j = 1; j < 32; ++j) m4[c] = fmaxf(m4[c], __uint_as_float(acc[c][j]));
+    }
+    const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+    const float base = m == -INFINITY ? 0.f : m;  // nothing but -inf: the sum is 0
+    float s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int j = 0; j < 32; ++j) s4[j & 3] += __expf(__uint_as_float(acc[c][j]) - base);
+    if (row < p.M)
+      p.part[static_cast<size_t>(row) * (2 * p.nt) + 2 * (t.n0 / kBN) + e.part] =
+          make_float2(m, (s4[0] + s4[1]) + (s4[2] + s4[3]));
+    const int rel = target - col;
+    const bool here = target >= 0 && rel >= 0 && rel < 128;
+    if (__any_sync(0xffffffffu, here)) {
+      uint32_t z = 0u;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (rel == 32 * c + j) z = acc[c][j];
+      if (here) p.zt[row] = __uint_as_float(z);
+    }
+  }
+};
+
+// Joins the pairs of a row: one warp a row, the pairs in a fixed order.
+__global__ void __launch_bounds__(256) xent_join_kernel(const float2* __restrict__ part, const float* __restrict__ zt,
+                                                        Target target, int T, int V, int np, float* __restrict__ loss,
+                                                        float* __restrict__ lse, int* err) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int t = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (t >= T) return;
+  const float2* row = part + static_cast<size_t>(t) * np;
+  float m = -INFINITY, s = 0.f;
+  for (int i = lane; i < np; i += 32) {
+    const float2 v = row[i];
+    const float nm = fmaxf(m, v.x);
+    // a pair without a finite logit has sum 0 and leaves s as it is
+    const float keep = m == nm ? 1.f : expf(m - nm), add = v.x == nm ? 1.f : expf(v.x - nm);
+    s = (s == 0.f ? 0.f : s * keep) + (v.y == 0.f ? 0.f : v.y * add);
+    m = nm;
+  }
+#pragma unroll
+  for (int off = 16; off; off >>= 1) {
+    const float om = __shfl_xor_sync(0xffffffffu, m, off), os = __shfl_xor_sync(0xffffffffu, s, off);
+    const float nm = fmaxf(m, om);
+    const float a = s == 0.f ? 0.f : s * (m == nm ? 1.f : expf(m - nm));
+    const float b = os == 0.f ? 0.f : os * (om == nm ? 1.f : expf(om - nm));
+    s = a + b;
+    m = nm;
+  }
+  if (lane == 0) {
+    const float ls = logf(s);
+    lse[t] = m + ls;
+    const long long v = target.wide ? static_cast<const long long*>(target.p)[t] : static_cast<const int*>(target.p)[t];
+    if (v >= V) record_error(err, MOE_ERR_ARG, t);
+    loss[t] = v >= 0 && v < V ? (m - zt[t]) + ls : 0.f;
+  }
+}
+
+// ------------------------------------------------------------ backward: D
+struct GradOp {
+  static constexpr bool A_MN = false, B_MN = false, F16 = false, ONE = true;
+  struct Params : DenseParams {
+    Target target;
+    const float* loss;
+    const float* lse;
+    const float* dloss;
+    const float* dlse;  // or null
+    int V, v0;          // the piece is columns [v0, v0 + N) of V; columns from V on are zeros
+    int split;          // D is the sum of two bf16 values, the second N columns further
+  };
+  struct Pre {
+    float w, lse, at;  // of exp(z - lse); log of the sum; D at the target
+    int rel;           // the target's column in this thread's 128, or another number
+  };
+  template <int CG>
+  static __device__ __forceinline__ DenseTile tile(const Params& p, int i, int rank) {
+    return rows_first<CG>(p, i, rank);
+  }
+  static __device__ __forceinline__ void coords(const Params& p, const DenseTile& t, int kb, int& ak, int& am, int& bk,
+                                                int& bn) {
+    ak = bk = kb * kBK;
+    am = t.m0;
+    bn = p.v0 + t.n0;
+  }
+  static __device__ __forceinline__ Pre pre(const Params& p, const DenseTile& t, const DenseEpi& e) {
+    const int row = t.m0 + 32 * e.q + e.lane;
+    Pre r{0.f, 0.f, 0.f, -1};
+    if (row < p.M) {
+      const int target = load_target(p.target, row, p.V);
+      const float g = target >= 0 ? p.dloss[row] : 0.f, h = p.dlse ? p.dlse[row] : 0.f;
+      r.w = g + h;
+      r.lse = p.lse[row];
+      // (g + h) p - g with p = exp(-loss): what is left of a certain token's
+      // gradient is not the difference of two numbers near g
+      if (g != 0.f) {
+        const float l = -p.loss[row];
+        r.at = h * expf(l) + g * expm1f(l);
+        r.rel = target - (p.v0 + t.n0 + 128 * e.part);
+      }
+    }
+    return r;
+  }
+  static __device__ __forceinline__ void epilogue(const Params& p, const DenseTile& t, DenseEpi& e, const Pre& r,
+                                                  uint32_t (&acc)[4][32]) {
+    const int col = t.n0 + 128 * e.part;   // of the piece
+    const int n = p.V - (p.v0 + col);      // columns that exist
+    const int y = t.m0 + 32 * e.q;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      uint32_t hi[16], lo[16];
+#pragma unroll
+      for (int u = 0; u < 16; ++u) {
+        float d[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int j = 32 * c + 2 * u + k;
+          const float v = r.w * __expf(__uint_as_float(acc[c][2 * u + k]) - r.lse);
+          // a row that no gradient reaches adds nothing, whatever its logits are
+          d[k] = (r.w != 0.f && j < n) ? v : 0.f;
+          if (j == r.rel) d[k] = r.at;
+        }
+        hi[u] = pack_bf16(d[0], d[1]);
+        lo[u] = pack_bf16(d[0] - bf16_lo(hi[u]), d[1] - bf16_hi(hi[u]));
+      }
+      dense_store(e, hi, &p.tmO, col + 32 * c, y, 0);
+      if (p.split) dense_store(e, lo, &p.tmO, p.N + col + 32 * c, y, 0);
+    }
+  }
+};
+
+// ----------------------------------------------- backward: products of D
+// out (+)= A . B with 16-bit or fp32 results.  DX: A = D [T, N (+ N)], B = rows
+// [v0, ..) of W, K runs over the piece (and once more over it for the second
+// halves of D).  DW: A = D^T, B = x, K runs over the tokens.
+template <bool DX>
+struct ProdOp {
+  static constexpr bool A_MN = !DX, B_MN = true, F16 = false, ONE = true;
+  struct Params : DenseParams {
+    int v0;           // DX: the piece's first column of the vocabulary
+    int half;         // K blocks after which the second halves of D come
+    int cols;         // columns of the piece: where D's second halves are
+    int per_split;    // DX: K blocks of a split; each has a matrix of its own in out
+    const float* prev;  // added to the products, laid out as out is in fp32
+    int bf16;         // type of out
+  };
+  template <int CG>
+  static __device__ __forceinline__ DenseTile tile(const Params& p, int i, int rank) {
+    // columns fastest: the tiles that run at one time are about as many row
+    // blocks as column blocks
+    const int per = p.mt * p.nt, split = i / per, j = i - split * per;
+    const int mb = j / p.nt, nb = j - mb * p.nt;
+    const int kb0 = min(p.nkb, split * p.per_split);
+    return {split, mb * DensePipe<CG>::TILE_M + rank * kBM, nb * kBN, kb0, min(p.nkb, kb0 + p.per_split)};
+  }
+  static __device__ __forceinline__ void coords(const Params& p, const DenseTile& t, int kb, int& ak, int& am, int& bk,
+                                                int& bn) {
+    const bool second = kb >= p.half;
+    const int k = (second ? kb - p.half : kb) * kBK;
+    if constexpr (DX) {
+      ak = kb * kBK;  // the second halves follow the first in a row of D
+      am = t.m0;
+      bk = p.v0 + k;
+    } else {
+      ak = bk = k;
+      am = t.m0 + (second ? p.cols : 0);
+    }
+    bn = t.n0;
+  }
+  static __device__ __forceinline__ int pre(const Params&, const DenseTile&, const DenseEpi&) { return 0; }
+  static __device__ __forceinline__ void epilogue(const Params& p, const DenseTile& t, DenseEpi& e, int,
+                                                  uint32_t (&acc)[4][32]) {
+    const int x = t.n0 + 128 * e.part, y = t.m0 + 32 * e.q;
+    if (p.prev && y + e.lane < p.M) {
+      const float4* from =
+          reinterpret_cast<const float4*>(p.prev + (static_cast<size_t>(t.mat) * p.M + y + e.lane) * p.N + x);
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (x + 32 * c < p.N)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float4 v = from[8 * c + j];
+            uint32_t* a = &acc[c][4 * j];
+            a[0] = __float_as_uint(__uint_as_float(a[0]) + v.x);
+            a[1] = __float_as_uint(__uint_as_float(a[1]) + v.y);
+            a[2] = __float_as_uint(__uint_as_float(a[2]) + v.z);
+            a[3] = __float_as_uint(__uint_as_float(a[3]) + v.w);
+          }
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (x + 32 * c >= p.N) break;  // N is a multiple of 64
+      if (p.bf16) {
+        uint32_t w[16];
+#pragma unroll
+        for (int u = 0; u < 16; ++u)
+          w[u] = pack_bf16(__uint_as_float(acc[c][2 * u]), __uint_as_float(acc[c][2 * u + 1]));
+        dense_store(e, w, &p.tmO, x + 32 * c, y, t.mat);
+      } else {
+        dense_store(e, &acc[c][0], &p.tmO, x + 32 * c, y, t.mat);
+        dense_store(e, &acc[c][16], &p.tmO, x + 32 * c + 16, y, t.mat);
+      }
+    }
+  }
+};
+
+// x with the rows that no gradient reaches cleared: what they hold (padding may
+// hold anything) must not meet D's zeros in dW's sums.
+__global__ void __launch_bounds__(256) xent_rows_kernel(const uint4* __restrict__ x, Target target,
+                                                        const float* __restrict__ dloss, const float* __restrict__ dlse,
+                                                        int T, int V, int pieces, uint4* __restrict__ out) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const size_t total = static_cast<size_t>(T) * pieces;
+  for (size_t i = blockIdx.x * 256ull + threadIdx.x; i < total; i += gridDim.x * 256ull) {
+    const int t = static_cast<int>(i / pieces);
+    const bool live = (load_target(target, t, V) >= 0 && dloss[t] != 0.f) || (dlse && dlse[t] != 0.f);
+    out[i] = live ? x[i] : make_uint4(0, 0, 0, 0);
+  }
+}
+
+// Sum of the splits' dx in their order.
+__global__ void __launch_bounds__(256) xent_sum_kernel(const float4* __restrict__ part, int splits, size_t n4, int bf16,
+                                                       void* __restrict__ out) {
+  griddep_wait();
+  griddep_launch_dependents();
+  for (size_t i = blockIdx.x * 256ull + threadIdx.x; i < n4; i += gridDim.x * 256ull) {
+    float4 a = part[i];
+    for (int s = 1; s < splits; ++s) {
+      const float4 v = part[s * n4 + i];
+      a.x += v.x;
+      a.y += v.y;
+      a.z += v.z;
+      a.w += v.w;
+    }
+    if (bf16)
+      static_cast<uint2*>(out)[i] = make_uint2(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w));
+    else
+      static_cast<float4*>(out)[i] = a;
+  }
+}
+
+// ------------------------------------------------------------------ host
+constexpr int kMaxSplits = 64;
+
+struct Plan {
+  int cols;    // most columns of a piece, a multiple of 256, counted in bf16 values of a row of D
+  int splits;  // most of dx's sums
+  size_t err, part, zt, D, acc, xz, total;
+};
+
+// Splits of dx's sums over the vocabulary: where its tiles are fewer than the
+// SMs can run at one time, several of them share a tile's K.
+int dx_splits(int T, int d) {
+  const int cg = T <= kBM ? 1 : 2;
+  const int tiles = ceil_div(T, kBM * cg) * ceil_div(d, kBN);
+  return std::max(1, std::min(kMaxSplits, 152 / cg / tiles));
+}
+
+Plan plan(int T, int V, int d, int backward) {
+  Plan p{};
+  const int nt = ceil_div(V, kBN);
+  const long long want = std::max<long long>(kPieceBytes / 2 / T / kBN * kBN, kPieceCols);
+  // both halves of D for the whole vocabulary at most
+  p.cols = static_cast<int>(std::min<long long>(want, 2ll * nt * kBN));
+  p.splits = dx_splits(T, d);
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o = align_up(o + bytes, 256);
+    return at;
+  };
+  p.err = take(kErrRegionBytes);
+  const size_t begin = o;
+  p.part = take(sizeof(float2) * 2 * nt * T);
+  p.zt = take(sizeof(float) * T);
+  size_t end = o;
+  if (backward) {
+    o = begin;  // the forward's scratch is free by then
+    p.D = take(size_t(2) * T * p.cols);
+    p.acc = take(sizeof(float) * p.splits * T * d);
+    p.xz = take(size_t(2) * T * d);
+    end = std::max(end, o);
+  }
+  p.total = end;
+  return p;
+}
+
+template <class Op>
+int launch_rows(typename Op::Params& p, int T, const XentArgs& a, int trace, cudaStream_t s) {
+  const bool single = T <= kBM;
+  p.mt = single ? 1 : ceil_div(T, 2 * kBM);
+  p.total = p.mt * p.nt;
+  return single ? dense_launch<Op, 1>(p, a.grid_limit, trace, s) : dense_launch<Op, 2>(p, a.grid_limit, trace, s);
+}
+
+}  // namespace
+
+size_t xent_workspace_bytes(int T, int V, int d, int backward) { return plan(T, V, d, backward).total; }
+
+int launch_xent_fwd(const XentArgs& a, cudaStream_t s) {
+  const Plan L = plan(a.T, a.V, a.d, 0);
+  uint8_t* ws = static_cast<uint8_t*>(a.ws);
+  int* err = reinterpret_cast<int*>(ws + L.err);
+  StatsOp::Params p;
+  std::memset(&p, 0, sizeof(p));
+  const uint32_t bn = a.T <= kBM ? 256 : 128;
+  if (!dense_map_k(&p.tmA, a.x, false, a.d, a.T, 1, a.d, 128) || !dense_map_k(&p.tmB, a.W, false, a.d, a.V, 1, a.d, bn))
+    return MOE_ERR_CUDA;
+  p.M = a.T;
+  p.N = a.V;
+  p.nt = ceil_div(a.V, kBN);
+  p.nkb = a.d / kBK;
+  p.run_kb = kExactRun;
+  p.code = kCodeXent;
+  p.err = err;
+  p.target = {a.target, a.target_type};
+  p.part = reinterpret_cast<float2*>(ws + L.part);
+  p.zt = reinterpret_cast<float*>(ws + L.zt);
+  const int rc = launch_rows<StatsOp>(p, a.T, a, MOE_K_XENT, s);
+  if (rc != MOE_OK) return rc;
+  TraceScope trace_scope(MOE_K_XENT_JOIN, s);
+  return launch_pdl(xent_join_kernel, dim3(ceil_div(a.T, 8)), dim3(256), 0, s, p.part, p.zt, p.target, a.T, a.V, 2 * p.nt,
+                    a.loss, a.lse, err) == cudaSuccess
+             ? MOE_OK
+             : MOE_ERR_CUDA;
+}
+
+int launch_xent_bwd(const XentArgs& a, cudaStream_t s) {
+  const Plan L = plan(a.T, a.V, a.d, 1);
+  uint8_t* ws = static_cast<uint8_t*>(a.ws);
+  int* err = reinterpret_cast<int*>(ws + L.err);
+  void* D = ws + L.D;
+  float* accbuf = reinterpret_cast<float*>(ws + L.acc);
+  uint16_t* xz = reinterpret_cast<uint16_t*>(ws + L.xz);
+  const Target target{a.target, a.target_type};
+  const int split = (a.dx && a.dx_type == MOE_Y_F32) || (a.dW && a.dW_type == MOE_Y_F32);
+  const int h = 1 + split;
+  // pieces of about equal size, whole tiles wide
+  const int most = L.cols / h / kBN * kBN;
+  const int pieces = ceil_div(a.V, most);
+  const int width = ceil_div(ceil_div(a.V, pieces), kBN) * kBN;
+  const bool single = a.T <= kBM;
+  int rc;
+
+  if (a.dW) {
+    TraceScope trace_scope(MOE_K_XENT_ROWS, s);
+    const long long n = static_cast<long long>(a.T) * (a.d / 8);
+    const int blocks = static_cast<int>(std::min<long long>(ceil_div(n, 256), num_sms() * 8ll));
+    if (launch_pdl(xent_rows_kernel, dim3(blocks), dim3(256), 0, s, reinterpret_cast<const uint4*>(a.x), target, a.dloss,
+                   a.dlse, a.T, a.V, a.d / 8, reinterpret_cast<uint4*>(xz)) != cudaSuccess)
+      return MOE_ERR_CUDA;
+  }
+  for (int v0 = 0; v0 < a.V; v0 += width) {
+    const int real = std::min(width, a.V - v0);
+    const int cols = ceil_div(real, kBN) * kBN;
+    {
+      GradOp::Params p;
+      std::memset(&p, 0, sizeof(p));
+      if (!dense_map_k(&p.tmA, a.x, false, a.d, a.T, 1, a.d, 128) ||
+          !dense_map_k(&p.tmB, a.W, false, a.d, a.V, 1, a.d, single ? 256 : 128) ||
+          !dense_map_out(&p.tmO, D, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, size_t(cols) * h, a.T, 1, size_t(cols) * h))
+        return MOE_ERR_CUDA;
+      p.M = a.T;
+      p.N = cols;
+      p.nt = cols / kBN;
+      p.nkb = a.d / kBK;
+      p.run_kb = kExactRun;  // the forward's logits, bit for bit
+      p.code = kCodeXent + 1;
+      p.err = err;
+      p.target = target;
+      p.loss = a.loss;
+      p.lse = a.lse;
+      p.dloss = a.dloss;
+      p.dlse = a.dlse;
+      p.V = a.V;
+      p.v0 = v0;
+      p.split = split;
+      if ((rc = launch_rows<GradOp>(p, a.T, a, MOE_K_XENT_GRAD, s)) != MOE_OK) return rc;
+    }
+    if (a.dx) {
+      ProdOp<true>::Params p;
+      std::memset(&p, 0, sizeof(p));
+      const bool f32 = a.dx_type == MOE_Y_F32;
+      p.M = a.T;
+      p.N = a.d;
+      p.nt = ceil_div(a.d, kBN);
+      p.half = cols / kBK;
+      p.nkb = f32 ? 2 * p.half : p.half;
+      p.run_kb = f32 ? kExactRun : p.nkb;
+      p.code = kCodeXent + 2;
+      p.err = err;
+      p.v0 = v0;
+      p.cols = cols;
+      p.per_split = ceil_div(p.nkb, L.splits);  // a split without K blocks keeps the sums so far
+      p.mt = single ? 1 : ceil_div(a.T, 2 * kBM);
+      p.total = p.mt * p.nt * L.splits;
+      const bool last = v0 + width >= a.V;
+      // fp32 sums of the pieces so far: in dx itself where it has that type
+      float* sums = L.splits == 1 && f32 ? static_cast<float*>(a.dx) : accbuf;
+      p.prev = v0 > 0 ? sums : nullptr;
+      void* out = L.splits == 1 && last ? a.dx : sums;
+      p.bf16 = L.splits == 1 && last && !f32;
+      if (!dense_map_k(&p.tmA, D, false, size_t(cols) * h, a.T, 1, size_t(cols) * h, 128) ||
+          !dense_map_mn(&p.tmB, a.W, false, a.d, a.V, 1, single ? 4 : 2) ||
+          !dense_map_out(&p.tmO, out, p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.d, a.T,
+                         L.splits, a.d))
+        return MOE_ERR_CUDA;
+      rc = single ? dense_launch<ProdOp<true>, 1>(p, a.grid_limit, MOE_K_XENT_DX, s)
+                  : dense_launch<ProdOp<true>, 2>(p, a.grid_limit, MOE_K_XENT_DX, s);
+      if (rc != MOE_OK) return rc;
+    }
+    if (a.dW) {
+      ProdOp<false>::Params p;
+      std::memset(&p, 0, sizeof(p));
+      const bool f32 = a.dW_type == MOE_Y_F32, one = real <= kBM;
+      p.M = real;
+      p.N = a.d;
+      p.nt = ceil_div(a.d, kBN);
+      p.half = ceil_div(a.T, kBK);
+      p.nkb = f32 ? 2 * p.half : p.half;
+      p.run_kb = f32 ? kExactRun : p.nkb;
+      p.code = kCodeXent + 3;
+      p.err = err;
+      p.cols = cols;
+      p.per_split = p.nkb;
+      p.mt = one ? 1 : ceil_div(real, 2 * kBM);
+      p.total = p.mt * p.nt;
+      p.bf16 = !f32;
+      uint8_t* out = static_cast<uint8_t*>(a.dW) + size_t(v0) * a.d * (f32 ? 4 : 2);
+      if (!dense_map_mn(&p.tmA, D, false, size_t(cols) * h, a.T, 1, 2) ||
+          !dense_map_mn(&p.tmB, xz, false, a.d, a.T, 1, one ? 4 : 2) ||
+          !dense_map_out(&p.tmO, out, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.d, real, 1,
+                         a.d))
+        return MOE_ERR_CUDA;
+      rc = one ? dense_launch<ProdOp<false>, 1>(p, a.grid_limit, MOE_K_XENT_DW, s)
+               : dense_launch<ProdOp<false>, 2>(p, a.grid_limit, MOE_K_XENT_DW, s);
+      if (rc != MOE_OK) return rc;
+    }
+  }
+  if (a.dx && L.splits > 1) {
+    TraceScope trace_scope(MOE_K_XENT_ROWS, s);
+    const size_t n4 = size_t(a.T) * a.d / 4;
+    if (launch_pdl(xent_sum_kernel, dim3(static_cast<int>(std::min<size_t>((n4 + 255) / 256, num_sms() * 8))), dim3(256), 0,
+                   s, reinterpret_cast<const float4*>(accbuf), L.splits, n4, a.dx_type == MOE_Y_BF16, a.dx) != cudaSuccess)
+      return MOE_ERR_CUDA;
+  }
+  return MOE_OK;
+}
+
+}  // namespace moe

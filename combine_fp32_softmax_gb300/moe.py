@@ -74,6 +74,15 @@ _SIGS = {
     "moe_linear_q4_fwd": ([_I] * 4 + [_P] * 4 + [_I, _P, _P], _I),
     "moe_q4_quantize": ([_P] * 3 + [_I] * 4 + [_P], _I),
     "moe_q4_dequantize": ([_P] * 3 + [_I] * 4 + [_P], _I),
+    "moe_balance_fwd": ([_CFG] + [_P] * 3 + [_I] + [_P] * 6, _I),
+    "moe_balance_bwd": ([_CFG] + [_P] * 3 + [_I] + [_P] * 6, _I),
+    "moe_xent_workspace_bytes": ([_I] * 4, ctypes.c_size_t),
+    "moe_xent_ws_init": ([_P, _P], _I),
+    "moe_xent_fwd": ([_I] * 3 + [_P] * 3 + [_I] + [_P] * 4, _I),
+    "moe_xent_bwd": ([_I] * 3 + [_P] * 3 + [_I] + [_P] * 5 + [_I, _P, _I, _P, _P], _I),
+    "moe_orthogonalize_workspace_bytes": ([_I] * 3, ctypes.c_size_t),
+    "moe_orthogonalize_ws_init": ([_P, _P], _I),
+    "moe_orthogonalize": ([_I] * 3 + [_P, _I, _P, _I, _P, _P], _I),
     "moe_get_device_error": ([_P, _P, ctypes.POINTER(_I), ctypes.POINTER(_I)], _I),
     "moe_num_sms": ([], _I),
     "moe_set_grid_limit": ([_I], _I),
@@ -101,7 +110,9 @@ _SIGS = {
 TRACE_KINDS = ["route", "hist", "scan", "scatter", "gather", "gemm1_swiglu", "gemm2_scale", "combine",
                "combine_bwd", "gemm_dh", "dw_reduce", "route_bwd", "gemm_dx", "dispatch_bwd", "gemm_dw13",
                "gemm_dw2", "megakernel", "megakernel_bwd",
-               "route_tables", "bwd_gemms", "decode", "linear", "q4"]
+               "route_tables", "bwd_gemms", "decode", "linear", "q4",
+               "balance", "balance_bwd", "xent", "xent_join", "xent_grad", "xent_dx", "xent_dw", "xent_rows",
+               "ortho_norm", "ortho_gram", "ortho_square", "ortho_update"]
 
 _lib = None
 
@@ -438,6 +449,136 @@ def moe_q4_dequantize(codes, scales, W, group, stream=None):
     _call("moe_q4_dequantize", _ptr(codes), _ptr(scales), _ptr(W), mats, rows, cols, int(group), _stream(stream))
 
 
+# ------------------------------------------------- the ends of a training step
+def _typed(name, t, dtypes, shape):
+    """A required tensor must have one of the types and the shape."""
+    if t is None or t.dtype not in dtypes or tuple(t.shape) != tuple(shape):
+        got = None if t is None else f"{tuple(t.shape)} of {t.dtype}"
+        raise ValueError(f"{name}: {tuple(shape)} of {' or '.join(map(str, dtypes))} expected, got {got}")
+
+
+def _one_device(*tensors):
+    """The launches go to the current device: every tensor has to be there."""
+    for t in tensors:
+        if t is not None and t.is_cuda and t.device.index != _device():
+            raise ValueError(f"a tensor on cuda:{t.device.index} while the current device is cuda:{_device()}")
+
+
+def _token_mask(mask, T):
+    if mask is not None:
+        _typed("mask", mask, (torch.bool, _U8), (T,))
+
+
+def moe_balance_fwd(cfg, logits, topk_idx, mask, counts, mean_p, loss, zloss, ws, stream=None):
+    """Picks and mean probabilities of each expert, counts int32 and mean_p fp32 [B, E], and the balance and z losses
+    [B] of B sequences of T / B tokens; mask [T] bool (None: every token counts)."""
+    c = cfg if isinstance(cfg, moe_cfg) else cfg_of(cfg)
+    B = loss.numel()
+    _typed("logits", logits, (_F32,), (c.T, c.E))
+    _typed("topk_idx", topk_idx, (_I32,), (c.T, c.k))
+    _typed("counts", counts, (_I32,), (B, c.E))
+    _typed("mean_p", mean_p, (_F32,), (B, c.E))
+    _typed("loss", loss, (_F32,), (B,))
+    _typed("zloss", zloss, (_F32,), (B,))
+    _token_mask(mask, c.T)
+    _one_device(logits, topk_idx, mask, counts, mean_p, loss, zloss, ws)
+    _call("moe_balance_fwd", _cfg(c), _ptr(logits), _ptr(topk_idx), _ptr(mask), B, _ptr(counts), _ptr(mean_p), _ptr(loss),
+          _ptr(zloss), _workspace(ws, moe_workspace_bytes(c)), _stream(stream))
+
+
+def moe_balance_bwd(cfg, logits, counts, mask, dloss, dzloss, dlogits_in, dlogits, ws, stream=None):
+    """dlogits [T, E] = dlogits_in (None: 0; may be dlogits) + the gradient of dloss . loss + dzloss . zloss."""
+    c = cfg if isinstance(cfg, moe_cfg) else cfg_of(cfg)
+    B = dloss.numel()
+    _typed("logits", logits, (_F32,), (c.T, c.E))
+    _typed("counts", counts, (_I32,), (B, c.E))
+    _typed("dloss", dloss, (_F32,), (B,))
+    _typed("dzloss", dzloss, (_F32,), (B,))
+    if dlogits_in is not None:
+        _typed("dlogits_in", dlogits_in, (_F32,), (c.T, c.E))
+    _typed("dlogits", dlogits, (_F32,), (c.T, c.E))
+    _token_mask(mask, c.T)
+    _one_device(logits, counts, mask, dloss, dzloss, dlogits_in, dlogits, ws)
+    _call("moe_balance_bwd", _cfg(c), _ptr(logits), _ptr(counts), _ptr(mask), B, _ptr(dloss), _ptr(dzloss),
+          _ptr(dlogits_in), _ptr(dlogits), _workspace(ws, moe_workspace_bytes(c)), _stream(stream))
+
+
+MOE_I32, MOE_I64 = 0, 1
+
+
+@functools.lru_cache(maxsize=1024)
+def _xent_bytes(T, V, d, backward):
+    return int(lib().moe_xent_workspace_bytes(T, V, d, backward))
+
+
+def moe_xent_workspace_bytes(T, V, d, backward=True) -> int:
+    return _xent_bytes(int(T), int(V), int(d), int(bool(backward)))
+
+
+def moe_xent_ws_init(ws, stream=None):
+    _call("moe_xent_ws_init", _workspace(ws, 256), _stream(stream))
+
+
+def _xent_shape(x, W, target, *rows):
+    """(T, V, d, type of target) of x [T, d], W [V, d], target [T] and fp32 tensors [T]."""
+    if x.dim() != 2 or W.dim() != 2 or x.shape[1] != W.shape[1]:
+        raise ValueError(f"x [T, d] and W [V, d] expected, got {tuple(x.shape)} and {tuple(W.shape)}")
+    (T, d), V = x.shape, W.shape[0]
+    _typed("x", x, (_BF16,), (T, d))
+    _typed("W", W, (_BF16,), (V, d))
+    _typed("target", target, (_I32, torch.int64), (T,))
+    for name, t in rows:
+        _typed(name, t, (_F32,), (T,))
+    return T, V, d, MOE_I32 if target.dtype is _I32 else MOE_I64
+
+
+def moe_xent_fwd(x, W, target, loss, lse, ws, stream=None):
+    """loss [T] and lse [T] fp32 of the logits x [T, d] . W [V, d]^T against target [T] int32 or int64 (below 0: none)."""
+    T, V, d, tt = _xent_shape(x, W, target, ("loss", loss), ("lse", lse))
+    _one_device(x, W, target, loss, lse, ws)
+    _call("moe_xent_fwd", T, V, d, _ptr(x), _ptr(W), _ptr(target), tt, _ptr(loss), _ptr(lse),
+          _workspace(ws, _xent_bytes(T, V, d, 0)), _stream(stream))
+
+
+def moe_xent_bwd(x, W, target, loss, lse, dloss, dlse, dx, dW, ws, stream=None):
+    """dx [T, d] and dW [V, d] (fp32 or bf16; either may be None) of dloss . loss + dlse . lse (dlse may be None), loss and
+    lse being what moe_xent_fwd gave."""
+    T, V, d, tt = _xent_shape(x, W, target, ("loss", loss), ("lse", lse), ("dloss", dloss))
+    if dlse is not None:
+        _typed("dlse", dlse, (_F32,), (T,))
+    for name, t, rows in ("dx", dx, T), ("dW", dW, V):
+        if t is not None:
+            _typed(name, t, (_F32, _BF16), (rows, d))
+    _one_device(x, W, target, loss, lse, dloss, dlse, dx, dW, ws)
+    _call("moe_xent_bwd", T, V, d, _ptr(x), _ptr(W), _ptr(target), tt, _ptr(loss), _ptr(lse), _ptr(dloss), _ptr(dlse),
+          _ptr(dx), 0 if dx is None else _y_type(dx), _ptr(dW), 0 if dW is None else _y_type(dW),
+          _workspace(ws, _xent_bytes(T, V, d, 1)), _stream(stream))
+
+
+MOE_ORTHOGONALIZE_MAX_STEPS = 16
+
+
+def moe_orthogonalize_workspace_bytes(mats, rows, cols) -> int:
+    return int(lib().moe_orthogonalize_workspace_bytes(int(mats), int(rows), int(cols)))
+
+
+def moe_orthogonalize_ws_init(ws, stream=None):
+    _call("moe_orthogonalize_ws_init", _workspace(ws, 256), _stream(stream))
+
+
+def moe_orthogonalize(G, O, steps, ws, stream=None):
+    """O bf16 = G (fp32 or bf16) made nearly orthogonal, each of [mats, rows, cols] matrices (or one [rows, cols]) by
+    itself, in `steps` steps (5 is usual)."""
+    if G.dim() not in (2, 3):
+        raise ValueError(f"G [mats, rows, cols] or [rows, cols] expected, got {tuple(G.shape)}")
+    _typed("G", G, (_F32, _BF16), G.shape)
+    _typed("O", O, (_BF16,), G.shape)
+    mats, rows, cols = G.shape if G.dim() == 3 else (1, *G.shape)
+    _one_device(G, O, ws)
+    _call("moe_orthogonalize", mats, rows, cols, _ptr(G), _y_type(G), _ptr(O), int(steps),
+          _workspace(ws, moe_orthogonalize_workspace_bytes(mats, rows, cols)), _stream(stream))
+
+
 def moe_get_device_error(ws, stream=None):
     code, info = _I(0), _I(0)
     _call("moe_get_device_error", _ptr(ws), _stream(stream), ctypes.byref(code), ctypes.byref(info))
@@ -644,4 +785,24 @@ def alloc_linear_workspace(T, n, K, device="cuda", stream=None) -> torch.Tensor:
         raise MoeError("moe_linear_workspace_bytes", MOE_ERR_SHAPE)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
     moe_linear_ws_init(T, n, K, ws, stream)
+    return ws
+
+
+def alloc_xent_workspace(T, V, d, backward=True, device="cuda", stream=None) -> torch.Tensor:
+    """Workspace of moe_xent_fwd and, unless backward is False, moe_xent_bwd, ready for use."""
+    nbytes = moe_xent_workspace_bytes(T, V, d, backward)
+    if nbytes == 0:
+        raise MoeError("moe_xent_workspace_bytes", MOE_ERR_SHAPE)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    moe_xent_ws_init(ws, stream)
+    return ws
+
+
+def alloc_orthogonalize_workspace(mats, rows, cols, device="cuda", stream=None) -> torch.Tensor:
+    """Workspace of moe_orthogonalize, ready for use."""
+    nbytes = moe_orthogonalize_workspace_bytes(mats, rows, cols)
+    if nbytes == 0:
+        raise MoeError("moe_orthogonalize_workspace_bytes", MOE_ERR_SHAPE)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    moe_orthogonalize_ws_init(ws, stream)
     return ws

@@ -386,6 +386,95 @@ int moe_q4_quantize(const uint16_t* W, uint8_t* codes, uint16_t* scales, int mat
 int moe_q4_dequantize(const uint8_t* codes, const uint16_t* scales, uint16_t* W, int mats, int rows, int cols,
                       int group, void* stream);
 
+/* ------------------------------------------------- the ends of a training step
+ * What a training step needs beside the layer: the loss that makes its gradient,
+ * the balance loss of its router, and the update that its weight gradients
+ * drive.  None of them is on the pages; formulas are the common ones, given here.
+ *
+ * Balance of the routing, for each of `seqs` sequences of L = T / seqs tokens
+ * (seqs = 1: of the whole batch).  mask [T] bytes or NULL: tokens with 0 (padding)
+ * do not count, whatever their logits and picks hold.  Over the n tokens of a
+ * sequence that count:
+ *   counts [seqs, E]   c_e = picks of expert e (exact)
+ *   mean_p [seqs, E]   P_e = mean of p_te, p as moe_route computes it
+ *   loss   [seqs]      E / (k n) * sum_e c_e P_e   (1 for an even spread)
+ *   zloss  [seqs]      mean of lse_t^2, lse_t = log sum_e exp(logits_te)
+ * (all 0 where n = 0).  Sums over tokens are fp64 beyond a block's.  cfg and ws
+ * are the layer's; ws lends its histogram and partial-dot scratch, so the calls
+ * may stand anywhere between and after moe_layer_fwd and moe_layer_bwd.  d_model,
+ * d_ff, n_shared and renorm do not matter.  A non-finite logit of a token that
+ * counts sets MOE_ERR_NONFINITE (its sequence's mean_p, loss and zloss are then
+ * unspecified and its gradient 0), a pick outside [0, E) MOE_ERR_ARG (it is not
+ * counted).  MOE_ERR_SHAPE unless seqs >= 1 divides T. */
+int moe_balance_fwd(const moe_cfg* cfg, const float* logits, const int32_t* topk_idx, const uint8_t* mask, int seqs,
+                    int32_t* counts, float* mean_p, float* loss, float* zloss, void* ws, void* stream);
+/* Its gradient for the logits, dloss and dzloss [seqs] being those of loss and
+ * zloss (the picks have none):
+ *   dlogits_te = dlogits_in_te + p_te (a_e - sum_j a_j p_tj) + 2 dzloss / n lse_t p_te,
+ *   a_e = dloss E c_e / (k n^2)
+ * dlogits_in [T, E]: the gradient of moe_layer_bwd, to which it is added; it may be
+ * dlogits itself, or NULL for none.  Tokens that do not count get dlogits_in. */
+int moe_balance_bwd(const moe_cfg* cfg, const float* logits, const int32_t* counts, const uint8_t* mask, int seqs,
+                    const float* dloss, const float* dzloss, const float* dlogits_in, float* dlogits, void* ws,
+                    void* stream);
+
+/* Softmax cross entropy of the logits z = x W^T, x [T, d] bf16 (a token's hidden
+ * state), W [V, d] bf16 (the output projection), against one target a token:
+ *   lse  [T] fp32 = log sum_v exp z_tv
+ *   loss [T] fp32 = lse_t - z_t,target(t); 0 where target(t) < 0 (no target)
+ * target [T] int32 or int64 (target_type).  A target >= V counts as none and sets
+ * MOE_ERR_ARG (info: the token).  The logits are never in memory.  They are fp32
+ * sums whose tensor-core runs are 256 columns long and are added up rounded to
+ * nearest (so at most 2^-19 of the sum of the terms' magnitudes is lost), and
+ * loss keeps its relative precision where a token is certain: it is not formed
+ * as a difference of lse and z.  Infinite logits give NaN.
+ * Limits (MOE_ERR_SHAPE): 1 <= T, V <= 2^22, d a multiple of 64 up to 65536.
+ * Workspace: moe_xent_workspace_bytes (0 outside the limits; backward = 0: only
+ * for the forward), its first bytes cleared once with moe_xent_ws_init; it keeps
+ * nothing between calls, and calls that share it must not overlap on the GPU.
+ * The forward is two launches, the backward at most 2 and three for each piece
+ * of the vocabulary; all may be captured into a CUDA graph. */
+enum { MOE_I32 = 0, MOE_I64 = 1 }; /* type of target */
+size_t moe_xent_workspace_bytes(int T, int V, int d, int backward);
+int moe_xent_ws_init(void* ws, void* stream);
+int moe_xent_fwd(int T, int V, int d, const uint16_t* x, const uint16_t* W, const void* target, int target_type,
+                 float* loss, float* lse, void* ws, void* stream);
+/* Gradients, loss and lse being what moe_xent_fwd gave for the same x, W and
+ * target, dloss [T] and dlse [T] (NULL: none) the gradients of loss and lse (a
+ * mean over tokens is dloss = 1 / n; a weight on lse^2 goes through dlse):
+ *   D_tv = (g_t + dlse_t) exp(z_tv - lse_t) - [v = target(t)] g_t,
+ *   g_t = dloss_t, 0 for a token without target
+ *   dx [T, d] = D W,  dW [V, d] = D^T x
+ * each fp32 or bf16 (MOE_Y_F32, MOE_Y_BF16), either NULL if not wanted.  D is
+ * formed from the logits again, in pieces of the vocabulary, and enters the
+ * products in bf16 (2^-8 of each value, beside the final rounding) for bf16
+ * results and as the sum of two bf16 values (2^-16) for fp32 ones, whose runs of
+ * sums are kept short as the logits' are.  A token whose dloss and dlse are 0 or
+ * that has neither target nor dlse adds nothing, whatever x holds. */
+int moe_xent_bwd(int T, int V, int d, const uint16_t* x, const uint16_t* W, const void* target, int target_type,
+                 const float* loss, const float* lse, const float* dloss, const float* dlse, void* dx, int dx_type,
+                 void* dW, int dW_type, void* ws, void* stream);
+
+/* Matrices G [mats, rows, cols] (fp32 or bf16: g_type MOE_Y_F32 or MOE_Y_BF16; the
+ * weight gradients of the experts, or a mean of them over steps) to nearly
+ * orthogonal ones O [mats, rows, cols] bf16, each by itself: X = G / (|G| + 1e-7) in
+ * the Frobenius norm, then `steps` (1 to MOE_ORTHOGONALIZE_MAX_STEPS; 5 is usual)
+ * times
+ *   A = X X^T,  X <- 3.4445 X + (-4.7750 A + 2.0315 A A) X
+ * (for rows > cols the same with X^T).  Between the products X, A and the
+ * polynomial are held in fp16, sums in fp32: O differs from the formula by about
+ * 1.2e-3 of its norm, and its rounding to bf16 by 1.7e-3.  A matrix of zeros (an
+ * expert that saw no token) gives zeros; one that holds a NaN or an Inf, or whose
+ * sum of squares passes fp32's range, gives NaN everywhere; norms below 1e-10
+ * lose bits.  rows, cols any from 1 to 32768 (MOE_ERR_SHAPE otherwise).  O may not
+ * be G.  Workspace as above: moe_orthogonalize_workspace_bytes, cleared once with
+ * moe_orthogonalize_ws_init. */
+#define MOE_ORTHOGONALIZE_MAX_STEPS 16
+size_t moe_orthogonalize_workspace_bytes(int mats, int rows, int cols);
+int moe_orthogonalize_ws_init(void* ws, void* stream);
+int moe_orthogonalize(int mats, int rows, int cols, const void* G, int g_type, uint16_t* O, int steps, void* ws,
+                      void* stream);
+
 /* Reads the device error word of `ws` into *code (MOE_OK or a negative
  * MOE_ERR_*) and *info (a code-specific detail, e.g. the token of a
  * non-finite logit or the task of a timed-out wait).  Synchronises
@@ -584,7 +673,19 @@ enum {
   MOE_K_DECODE = 20,      /* layer for a few tokens */
   MOE_K_LINEAR = 21,      /* linear layer for a few tokens */
   MOE_K_Q4 = 22,          /* to and from 4-bit weights */
-  MOE_K_COUNT = 23
+  MOE_K_BALANCE = 23,     /* balance loss: sums and their join */
+  MOE_K_BALANCE_BWD = 24, /* its gradient */
+  MOE_K_XENT = 25,        /* cross entropy: logits and their statistics */
+  MOE_K_XENT_JOIN = 26,   /* join of a token's statistics */
+  MOE_K_XENT_GRAD = 27,   /* gradient of a piece of the logits */
+  MOE_K_XENT_DX = 28,     /* product for dx */
+  MOE_K_XENT_DW = 29,     /* product for dW */
+  MOE_K_XENT_ROWS = 30,   /* rows of x that count; sum of dx's splits */
+  MOE_K_ORTHO_NORM = 31,  /* norms, fp16 copy */
+  MOE_K_ORTHO_GRAM = 32,  /* X X^T or X^T X */
+  MOE_K_ORTHO_SQUARE = 33,/* b A + c A A */
+  MOE_K_ORTHO_UPDATE = 34,/* a X + B X or a X + X B */
+  MOE_K_COUNT = 35
 };
 /* Testing aid for failure detection (no device fault involved): the forward
  * MegaKernel claims task `ticket` but never runs or signals it, so the

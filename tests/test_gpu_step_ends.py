@@ -1,0 +1,435 @@
+"""The ends of a training step on the GPU against the fp64 oracle: balance loss, cross entropy over a vocabulary,
+orthogonalised matrices.
+
+Tolerances, derived from the kernels' stated roundings:
+  * a logit: its sum loses at most 2^-19 of S = sum |x||W| in the tensor core's runs of 256 columns and 2^-24 of S for each
+    of the d / 256 additions of runs: dz = (2^-19 + d 2^-32) max S;
+  * lse: dz, the error of the exponentials, sum and log (2^-20 together: __expf is within 2 + |z| ulp of terms that
+    add up to the sum), and its own rounding; loss: 2 dz and the same;
+  * D: relative 2 dz + 2^-20 + 2^-23 |lse| for the exponential, plus its rounding, 2^-8 in bf16 and 2^-16 as two bf16
+    values; a product of it: that part of sum |D||W|, the tensor core's loss over the K of one run (2^-23 for each 16
+    terms), and the result's own rounding, 2^-8 or 2^-24."""
+import numpy as np
+import pytest
+import torch
+
+from combine_fp32_softmax_gb300 import moe
+from oracle import moe_oracle as O
+from oracle import step_oracle as S
+from tests import gpu_util as U
+
+pytestmark = pytest.mark.gpu
+F32, BF16, I32 = torch.float32, torch.bfloat16, torch.int32
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def put(t, label="in"):
+    """A device copy between guard regions."""
+    d = U.guarded_empty(tuple(t.shape), t.dtype, label)
+    d.copy_(t)
+    return d
+
+
+def workspace(nbytes, init):
+    ws = U.guarded_empty((nbytes,), torch.uint8, "ws")
+    ws.fill_(0xFF)  # NaN in every type: nothing may depend on what a workspace held
+    init(ws)
+    return ws
+
+
+# ----------------------------------------------------------------- balance
+def balance_inputs(T, E, k, B, masked, seed=0, scale=1.0):
+    z = torch.randn(T, E, generator=gen(seed)) * scale
+    idx = torch.sort(z, dim=1, descending=True, stable=True).indices[:, :k].int()
+    mask = None
+    if masked == "tail":
+        keep = torch.randint(0, T // B + 1, (B, 1), generator=gen(seed + 1))
+        mask = (torch.arange(T // B) < keep).reshape(T)
+    elif masked == "none left":
+        mask = torch.zeros(T, dtype=torch.bool)
+    elif masked == "random":
+        mask = torch.rand(T, generator=gen(seed + 1)) < 0.5
+    if mask is not None:
+        z[~mask] = float("nan")
+        idx[~mask] = 1 << 30
+    return z, idx, mask
+
+
+def run_balance(z, idx, mask, B, dloss, dz, add, in_place=False):
+    T, E = z.shape
+    cfg = moe.moe_cfg(T, 64, 64, E, idx.shape[1], 0, 0)
+    ws = workspace(moe.moe_workspace_bytes(cfg), lambda w: moe.moe_ws_init(cfg, w))
+    g = {n: put(t) if t is not None else None for n, t in dict(z=z, idx=idx, mask=mask, dloss=dloss, dz=dz, add=add).items()}
+    counts, mean_p = U.guarded_empty((B, E), I32), U.guarded_empty((B, E), F32)
+    loss, zloss = U.guarded_empty((B,), F32), U.guarded_empty((B,), F32)
+    out = g["add"] if in_place else U.guarded_empty((T, E), F32)
+    moe.moe_balance_fwd(cfg, g["z"], g["idx"], g["mask"], counts, mean_p, loss, zloss, ws)
+    moe.moe_balance_bwd(cfg, g["z"], counts, g["mask"], g["dloss"], g["dz"], g["add"], out, ws)
+    return counts, mean_p, loss, zloss, out, ws
+
+
+@pytest.mark.parametrize("T,E,k,B,masked", [
+    (1, 1, 1, 1, None), (1, 5, 3, 1, None), (7, 8, 2, 7, None), (64, 2, 2, 1, "random"), (512, 8, 2, 1, None),
+    (513, 33, 3, 1, "random"), (700, 64, 6, 7, "tail"), (1000, 65, 8, 2, "tail"), (1000, 128, 8, 1, None),
+    (2048, 129, 5, 4, "random"), (999, 256, 8, 3, None), (96, 16, 4, 2, "none left"), (33 * 40, 20, 4, 40, "tail"),
+    (20000, 64, 6, 1, "random"), (40000, 8, 2, 5, "tail"), (4096, 8, 2, 4096, "random")])
+def test_balance(T, E, k, B, masked):
+    z, idx, mask = balance_inputs(T, E, k, B, masked)
+    dloss, dz = torch.randn(B, generator=gen(5)), torch.randn(B, generator=gen(6))
+    add = torch.randn(T, E, generator=gen(7))
+    counts, mean_p, loss, zloss, out, ws = run_balance(z, idx, mask, B, dloss, dz, add)
+    assert U.device_error(ws) == (0, 0)
+    zn, mn = z.numpy(), None if mask is None else mask.numpy()
+    rc, rp, rl, rz = S.balance_fwd(np.nan_to_num(zn), np.where(idx.numpy() < E, idx.numpy(), 0), B, mn)
+    assert np.array_equal(counts.cpu().numpy(), rc)
+    # p: the router's own bound (4e-6 relative); a block adds up to T / 608 + 32 of them in fp32, and its sum is rounded
+    tol = 4e-6 + (T / 608 / 8 + 8) * 2.0 ** -24
+    assert np.all(np.abs(U.np64(mean_p) - rp) <= tol * rp + 1e-30)
+    assert np.all(np.abs(U.np64(loss) - rl) <= tol * np.abs(rl))
+    # lse is off by 2^-24 (|m| + |log s|) and the log's own error; |lse| <= |m| + log E
+    big = np.abs(np.nan_to_num(zn)).max() + np.log(E)
+    assert np.all(np.abs(U.np64(zloss) - rz) <= 8 * 2.0 ** -23 * big * (big + 1) + tol * rz)
+    ref = S.balance_bwd(np.nan_to_num(zn), np.where(idx.numpy() < E, idx.numpy(), 0), B, dloss.numpy(), dz.numpy(),
+                        add.numpy(), mn)
+    # the two terms of a gradient, each 1e-5 of its largest possible size: a softmax to 4e-6, a dot of E terms, lse
+    n = np.array([len(S._rows(T, B, b, mn)) for b in range(B)]).repeat(T // B)[:, None]
+    c = np.abs(dloss.numpy())[:, None] * rc.max(1, keepdims=True) * E / k
+    size = (c.repeat(T // B, 0) / np.maximum(n, 1) + 2 * np.abs(dz.numpy()).repeat(T // B)[:, None] * big) / np.maximum(n, 1)
+    assert np.all(np.abs(U.np64(out) - ref) <= 2.0 ** -24 * np.abs(ref) + 2e-5 * size)
+
+
+def test_balance_adds_in_place_and_without():
+    z, idx, mask = balance_inputs(300, 64, 6, 3, "tail")
+    d, add = torch.ones(3), torch.randn(300, 64, generator=gen(1))
+    a = run_balance(z, idx, mask, 3, d, d, add)[4]
+    b = run_balance(z, idx, mask, 3, d, d, add, in_place=True)[4]
+    assert torch.equal(a, b)
+    none = run_balance(z, idx, mask, 3, d, d, None)[4]
+    assert torch.equal(none[~mask.to(none.device)], torch.zeros_like(none[~mask.to(none.device)]))
+    assert torch.equal(a[~mask.to(a.device)].cpu(), add[~mask])  # tokens that do not count: as they were
+
+
+def test_balance_same_bits_and_grid():
+    z, idx, mask = balance_inputs(30000, 64, 6, 2, "random")
+    d = torch.ones(2)
+    a = run_balance(z, idx, mask, 2, d, d, None)
+    moe.moe_set_grid_limit(5)
+    try:
+        b = run_balance(z, idx, mask, 2, d, d, None)
+    finally:
+        moe.moe_set_grid_limit(0)
+    assert all(torch.equal(x, y) for x, y in zip(a[:5], b[:5]))
+
+
+def test_balance_reports_bad_logits_and_picks():
+    z, idx, _ = balance_inputs(200, 16, 2, 1, None)
+    z[77, 3] = float("inf")
+    d = torch.ones(1)
+    *_, out, ws = run_balance(z, idx, None, 1, d, d, None)
+    assert U.device_error(ws) == (moe.MOE_ERR_NONFINITE, 77)
+    assert not out[77].any()
+    z, idx, _ = balance_inputs(200, 16, 2, 1, None)
+    idx[5, 1] = 16
+    counts, *_, ws = run_balance(z, idx, None, 1, d, d, None)
+    assert U.device_error(ws) == (moe.MOE_ERR_ARG, 5)
+    assert int(counts.sum()) == 399
+
+
+def test_balance_gradient_against_differences():
+    T, E, k, B = 12, 6, 2, 2
+    z, idx, mask = balance_inputs(T, E, k, B, None, seed=3)
+    dl, dz = torch.tensor([0.7, -1.3]), torch.tensor([0.2, 0.5])
+    got = U.np64(run_balance(z, idx, mask, B, dl, dz, None)[4])
+
+    def f(zz):
+        _, _, l, zl = S.balance_fwd(zz, idx.numpy(), B)
+        return (l * dl.double().numpy()).sum() + (zl * dz.double().numpy()).sum()
+
+    base = z.double().numpy()
+    for t in range(T):
+        for e in range(E):
+            h = np.zeros_like(base)
+            h[t, e] = 1e-5
+            d = (f(base + h) - f(base - h)) / 2e-5
+            assert abs(got[t, e] - d) <= 1e-5
+
+
+# ----------------------------------------------------------- cross entropy
+def xent_inputs(T, V, d, ignored=0.0, seed=0, sure=12.0):
+    W = (torch.randn(V, d, generator=gen(seed)) * d ** -0.5).to(BF16)
+    target = torch.randint(V, (T,), generator=gen(seed + 1))
+    x = torch.randn(T, d, generator=gen(seed + 2)) + torch.rand(T, 1, generator=gen(seed + 3)) * sure * W[target].float()
+    target[torch.rand(T, generator=gen(seed + 4)) < ignored] = -100
+    return x.to(BF16), W, target
+
+
+def logit_error(x, W):
+    """Per token: bound on the error of its logits."""
+    return (2.0 ** -19 + x.shape[1] * 2.0 ** -32) * (np.abs(x) @ np.abs(W).T).max(1)
+
+
+def run_xent(x, W, target, backward=False, dloss=None, dlse=None, dx=None, dW=None, ws=None):
+    T, d = x.shape
+    V = W.shape[0]
+    g = [put(t) for t in (x, W, target)]
+    loss, lse = U.guarded_empty((T,), F32), U.guarded_empty((T,), F32)
+    if ws is None:
+        ws = workspace(moe.moe_xent_workspace_bytes(T, V, d, backward), moe.moe_xent_ws_init)
+    moe.moe_xent_fwd(*g, loss, lse, ws)
+    if not backward:
+        return loss, lse, ws
+    gx = None if dx is None else U.guarded_empty((T, d), dx, "dx")
+    gW = None if dW is None else U.guarded_empty((V, d), dW, "dW")
+    for t in (gx, gW):
+        if t is not None:
+            t.fill_(float("nan"))
+    moe.moe_xent_bwd(*g, loss, lse, put(dloss), None if dlse is None else put(dlse), gx, gW, ws)
+    return loss, lse, gx, gW, ws
+
+
+def check_fwd(x, W, target, loss, lse):
+    xn, Wn, tn = U.np64(x), U.np64(W), target.numpy().astype(np.int64)
+    rl, rs = S.xent_fwd(xn, Wn, tn)
+    dz = logit_error(xn, Wn)
+    assert np.all(np.abs(U.np64(lse) - rs) <= dz + 2.0 ** -20 + 2.0 ** -23 * np.abs(rs))
+    use = tn >= 0
+    assert np.all(U.np64(loss)[~use] == 0)
+    # log s and m - z are within an ulp each of what they stand for, and exp's error goes into s - 1 alone
+    assert np.all(np.abs(U.np64(loss) - rl)[use] <= (2 * dz * np.minimum(1, rl) + 2.0 ** -20 * rl + 2.0 ** -22)[use])
+    return dz, rs
+
+
+def check_bwd(x, W, target, dloss, dlse, lse, dz, dx, dW, T, V):
+    xn, Wn, tn = U.np64(x), U.np64(W), target.numpy().astype(np.int64)
+    D = S.xent_grad(xn, Wn, tn, dloss.double().numpy(), None if dlse is None else dlse.double().numpy())
+    g = np.where(tn >= 0, np.abs(dloss.double().numpy()), 0) + (0 if dlse is None else np.abs(dlse.double().numpy()))
+    rel = (2 * dz + 2.0 ** -20 + 2.0 ** -23 * np.abs(lse))[:, None]
+    # the target's own entry is off by that part of 1 - p, and by 2^-22 of the weight
+    one = np.zeros_like(D)
+    use = tn >= 0
+    one[np.arange(T)[use], tn[use]] = (2.0 ** -22 * g)[use]
+    for name, got, other, K, prod in (("dx", dx, Wn, V, lambda m: m @ np.abs(Wn)), ("dW", dW, xn, T, lambda m: m.T @ np.abs(xn))):
+        if got is None:
+            continue
+        exact = D @ Wn if name == "dx" else D.T @ xn
+        half = got.dtype == BF16
+        run = 2.0 ** -23 * (-(-K // 16)) if half else 2.0 ** -19 + K * 2.0 ** -31
+        bound = prod(np.abs(D) * (rel + (2.0 ** -8 if half else 2.0 ** -16) + run) + one)
+        bound += (2.0 ** -8 if half else 2.0 ** -24) * np.abs(exact)
+        err = np.abs(U.np64(got) - exact)
+        assert np.all(err <= bound + 1e-30), (name, float((err / (bound + 1e-30)).max()))
+
+
+@pytest.mark.parametrize("T,V,d", [(1, 1, 64), (1, 2, 64), (1, 1000, 256), (3, 255, 64), (5, 257, 128), (64, 5003, 320),
+                                   (128, 300, 2048), (129, 513, 192), (300, 1000, 1024), (517, 4097, 576)])
+def test_xent_fwd(T, V, d):
+    x, W, target = xent_inputs(T, V, d, 0.2)
+    loss, lse, ws = run_xent(x, W, target)
+    check_fwd(x, W, target, loss, lse)
+    assert U.device_error(ws) == (0, 0)
+
+
+@pytest.mark.parametrize("wide", [I32, torch.int64])
+@pytest.mark.parametrize("types", [(BF16, BF16), (F32, F32), (BF16, F32), (F32, None), (None, BF16)],
+                         ids=lambda t: "/".join(str(x)[6:] for x in t))
+@pytest.mark.parametrize("T,V,d", [(1, 1, 64), (1, 1000, 256), (65, 129, 64), (130, 1000, 192), (300, 2049, 320)])
+def test_xent_bwd(T, V, d, types, wide):
+    x, W, target = xent_inputs(T, V, d, 0.3, seed=T)
+    target = target.to(wide)
+    dloss = torch.rand(T, generator=gen(9)) / T
+    dlse = torch.randn(T, generator=gen(10)) * 1e-3 if types[0] is not None else None
+    loss, lse, dx, dW, ws = run_xent(x, W, target, True, dloss, dlse, *types)
+    dz, rs = check_fwd(x, W, target, loss, lse)
+    check_bwd(x, W, target, dloss, dlse, rs, dz, dx, dW, T, V)
+    assert U.device_error(ws) == (0, 0)
+
+
+def test_xent_pieces_of_the_vocabulary():
+    """More columns than a piece holds: sums over pieces, the last one narrow."""
+    T, V, d = 40000, 17000, 64
+    x, W, target = xent_inputs(T, V, d, 0.1)
+    dloss = torch.full((T,), 1.0 / T)
+    for dt in (BF16, F32):
+        loss, lse, dx, dW, ws = run_xent(x, W, target, True, dloss, None, dt, dt)
+        # the formula on the GPU in fp64 (the oracle's arrays would not fit a test's time)
+        xd, Wd, tg = x.to(U.DEV).double(), W.to(U.DEV).double(), target.to(U.DEV)
+        z = xd @ Wd.t()
+        ls = torch.logsumexp(z, 1)
+        use = (tg >= 0).nonzero()[:, 0]
+        assert (lse.double() - ls).abs().max() < 1e-4
+        D = torch.exp(z - ls[:, None]) * torch.where(tg >= 0, 1.0 / T, 0.0)[:, None]
+        D[use, tg[use]] -= 1.0 / T
+        bar = 2.0 ** -8 * 1.5 if dt == BF16 else 2.0 ** -15
+        for got, ref in ((dx, D @ Wd), (dW, D.t() @ xd)):
+            assert ((got.double() - ref).norm() / ref.norm()).item() <= bar
+        del z, D
+        assert U.device_error(ws) == (0, 0)
+
+
+def test_xent_certain_tokens_keep_their_precision():
+    """Targets so likely that lse and the logit agree to many digits: loss and gradient are those of the rest."""
+    T, V, d = 16, 700, 256
+    x, W, target = xent_inputs(T, V, d, sure=0.0)
+    x = (x.float() + 40.0 * W[target].float()).to(BF16)
+    loss, lse, dx, dW, ws = run_xent(x, W, target, True, torch.ones(T), None, F32, F32)
+    rl, _ = S.xent_fwd(U.np64(x), U.np64(W), target.numpy())
+    assert rl.max() < 1e-6
+    dz = logit_error(U.np64(x), U.np64(W))
+    assert np.all(np.abs(U.np64(loss) - rl) <= 2 * dz * rl + 2.0 ** -22)
+
+
+def test_xent_rows_without_weight_add_nothing():
+    """NaN and infinities in tokens that do not count stay there."""
+    T, V, d = 200, 777, 128
+    x, W, target = xent_inputs(T, V, d, 0.5)
+    off = target < 0
+    ref = run_xent(torch.where(off[:, None], torch.zeros((), dtype=BF16), x), W, target, True, torch.ones(T), None, F32, F32)
+    x[off] = float("nan")
+    x[off.nonzero()[0, 0]] = float("inf")
+    loss, lse, dx, dW, ws = run_xent(x, W, target, True, torch.ones(T), None, F32, F32)
+    assert torch.equal(dW, ref[3]) and torch.equal(dx, ref[2]) and torch.equal(loss, ref[0])
+    assert not dx[off.to(dx.device)].any()
+    # all of them: nothing left
+    *_, dx, dW, ws = run_xent(x, W, torch.full((T,), -1), True, torch.ones(T), None, BF16, BF16)
+    assert not dx.any() and not dW.any()
+
+
+def test_xent_target_outside_the_vocabulary():
+    T, V, d = 10, 100, 64
+    x, W, target = xent_inputs(T, V, d)
+    target[7] = V
+    loss, lse, dx, dW, ws = run_xent(x, W, target, True, torch.ones(T), None, F32, F32)
+    assert U.device_error(ws) == (moe.MOE_ERR_ARG, 7)
+    assert loss[7] == 0 and not dx[7].any()
+
+
+def test_xent_same_bits_grid_graph_and_stream():
+    T, V, d = 300, 3001, 256
+    x, W, target = xent_inputs(T, V, d, 0.2)
+    dloss = torch.full((T,), 1.0 / T)
+    ref = run_xent(x, W, target, True, dloss, None, BF16, F32)[:4]
+    moe.moe_set_grid_limit(3)
+    try:
+        got = run_xent(x, W, target, True, dloss, None, BF16, F32)[:4]
+    finally:
+        moe.moe_set_grid_limit(0)
+    assert all(torch.equal(a, b) for a, b in zip(ref, got))
+    g = [put(t) for t in (x, W, target)]
+    dl = put(dloss)
+    out = [torch.empty_like(t) for t in ref]
+    ws = moe.alloc_xent_workspace(T, V, d)
+    side = torch.cuda.Stream()
+
+    def step():
+        moe.moe_xent_fwd(*g, out[0], out[1], ws)
+        moe.moe_xent_bwd(*g, out[0], out[1], dl, None, out[2], out[3], ws)
+
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(ref, out))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(3):
+        for t in out:
+            t.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(ref, out))
+
+
+def test_xent_gradient_against_differences():
+    T, V, d = 4, 9, 64
+    x, W, target = xent_inputs(T, V, d, sure=2.0)
+    target[1] = -1
+    dl, dh = torch.tensor([1.0, 0.5, -2.0, 0.25]), torch.tensor([0.1, 0.3, 0.0, -0.7])
+    *_, dx, dW, ws = run_xent(x, W, target, True, dl, dh, F32, F32)
+
+    def f(xx, WW):
+        l, s = S.xent_fwd(xx, WW, target.numpy())
+        return (l * dl.double().numpy()).sum() + (s * dh.double().numpy()).sum()
+
+    xn, Wn = U.np64(x), U.np64(W)
+    rng = np.random.default_rng(0)
+    for _ in range(40):
+        ux, uW = rng.standard_normal(xn.shape), rng.standard_normal(Wn.shape)
+        d = (f(xn + 1e-5 * ux, Wn + 1e-5 * uW) - f(xn - 1e-5 * ux, Wn - 1e-5 * uW)) / 2e-5
+        got = (U.np64(dx) * ux).sum() + (U.np64(dW) * uW).sum()
+        size = np.abs(U.np64(dx) * ux).sum() + np.abs(U.np64(dW) * uW).sum()
+        assert abs(got - d) <= 2.0 ** -14 * size
+
+
+# --------------------------------------------------------- orthogonalised
+def run_ortho(G, steps=5, ws=None):
+    mats, rows, cols = G.shape if G.dim() == 3 else (1, *G.shape)
+    if ws is None:
+        ws = workspace(moe.moe_orthogonalize_workspace_bytes(mats, rows, cols), moe.moe_orthogonalize_ws_init)
+    out = U.guarded_empty(tuple(G.shape), BF16, "O")
+    out.fill_(float("nan"))
+    moe.moe_orthogonalize(put(G), out, steps, ws)
+    return out, ws
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("mats,rows,cols,steps", [
+    (1, 1, 1, 5), (1, 1, 100, 5), (3, 100, 1, 5), (2, 7, 9, 1), (2, 63, 65, 5), (1, 64, 2048, 5), (3, 128, 128, 5),
+    (2, 129, 257, 5), (2, 257, 129, 5), (2, 333, 1001, 3), (2, 1001, 333, 5), (1, 300, 300, 5), (1, 520, 264, 5),
+    (1, 700, 520, 2), (5, 256, 512, 5)])
+def test_orthogonalize(mats, rows, cols, steps, dt):
+    G = (torch.randn(mats, rows, cols, generator=gen(1)) * 1e-3).to(dt)
+    G[0] += (torch.randn(rows, 1, generator=gen(2)) @ torch.randn(1, cols, generator=gen(3)) * 2e-3).to(dt)
+    got, ws = run_ortho(G, steps)
+    assert U.device_error(ws) == (0, 0)
+    for i in range(mats):
+        ref = S.orthogonalize(U.np64(G[i]), steps)
+        # what fp16 between the products leaves, and the result's rounding to bf16
+        bar = S.orthogonalize_spread(U.np64(G[i]), steps) + 2.0 ** -8
+        assert U.relf(U.np64(got[i]), ref) <= bar
+    if steps == 5 and min(rows, cols) > 1:
+        s = np.linalg.svd(U.np64(got[0]), compute_uv=False)
+        assert s.max() < 1.3
+
+
+def test_orthogonalize_scales_zeros_and_bad_matrices():
+    rows, cols = 96, 160
+    base = torch.randn(rows, cols, generator=gen(4))
+    scales = [1.0, 0.0, 1e-20, 1e15, 1e-9, 1e-4]
+    G = torch.stack([base * s for s in scales] + [base.clone(), base.clone()])
+    G[-2, 3, 5] = float("nan")
+    G[-1, 90, 159] = float("inf")
+    got, ws = run_ortho(G)
+    for i, s in enumerate(scales):
+        ref = S.orthogonalize(U.np64(G[i]), 5)
+        if s == 0.0:
+            assert not got[i].any()
+        else:
+            assert U.relf(U.np64(got[i]), ref) <= S.orthogonalize_spread(U.np64(G[i]), 5) + 2.0 ** -8, s
+    assert got[-2:].isnan().all()
+    assert U.device_error(ws) == (0, 0)
+
+
+def test_orthogonalize_same_bits_grid_graph():
+    G = torch.randn(3, 300, 500, generator=gen(5))
+    ref, _ = run_ortho(G)
+    moe.moe_set_grid_limit(3)
+    try:
+        got, ws = run_ortho(G)
+    finally:
+        moe.moe_set_grid_limit(0)
+    assert torch.equal(ref, got)
+    g, out = put(G), torch.empty_like(ref)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moe.moe_orthogonalize(g, out, 5, ws)
+    for _ in range(3):
+        out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(ref, out)
+    one, _ = run_ortho(G[1])  # a matrix by itself: the same
+    assert torch.equal(ref[1], one)
