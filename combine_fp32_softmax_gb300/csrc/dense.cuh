@@ -4,11 +4,12 @@
 // One persistent kernel per operation; CG = 2 runs it on CTA pairs (a 256 x 256
 // tile of C for each pair, tcgen05 MMAs of the CTA group of two), CG = 1 on
 // single CTAs (128 x 256), for products whose C has at most 128 rows: half of
-// a pair's tile would be empty there.  320 threads:
-//   warp 0     TMA producer, 64-deep K blocks through a ring of 192 KB;
-//   warp 1     issues the MMAs;
-//   warps 2-9  epilogue: two warps for each TMEM lane quadrant, so a thread has
-//              one row and 128 of its 256 columns, all of them in registers.
+// a pair's tile would be empty there.  384 threads:
+//   warp 0      TMA producer, 64-deep K blocks through a ring of 192 KB;
+//   warp 1      issues the MMAs (warps 2 and 3 fill up their warpgroup, whose
+//               registers go to the other two);
+//   warps 4-11  epilogue: two warps for each TMEM lane quadrant, so a thread has
+//               one row and 128 of its 256 columns, all of them in registers.
 // The sums of a tile are taken out of TMEM in runs of run_kb K blocks and
 // added up in registers, rounded to nearest: the tensor core's own fp32
 // additions cut off what a sum has no room for, and an operation whose results
@@ -26,7 +27,11 @@
 namespace moe {
 namespace {
 
-constexpr int kDenseThreads = 64 + 32 * 8;
+constexpr int kDenseThreads = 128 + 32 * 8;
+// Registers a thread: 168 at launch (384 of them fill the SM's 65,536), then 40 for
+// the first warpgroup and 232 for the epilogue's two: 40 + 2 * 232 = 3 * 168.
+constexpr int kDenseRegs = 168, kIssueRegs = 40, kEpiRegs = 232;
+static_assert(kIssueRegs + 2 * kEpiRegs == 3 * kDenseRegs && kDenseRegs * kDenseThreads <= 65536, "register shares");
 constexpr int kDenseStg = 2 * kChunkBytes;  // staging of one epilogue warp: two chunks in flight
 template <int CG>
 struct DensePipe {
@@ -82,6 +87,24 @@ __device__ __forceinline__ void dense_store(DenseEpi& e, const uint32_t* w, cons
     bulk_commit();
   }
   ++e.chunks;
+}
+
+// mbar_wait without a call: an epilogue thread holds 128 sums that a call would
+// have to save.
+__device__ __forceinline__ bool mbar_wait_inline(uint64_t* bar, uint32_t parity, volatile int* abort, int* err, int where) {
+  const uint32_t a = smem_u32(bar);
+  uint64_t t0 = 0;
+  for (int i = 1; !mbar_try_wait(a, parity); ++i) {
+    if (i & 63) continue;
+    if (t0 == 0) t0 = globaltimer_ns();
+    if (*abort) return false;
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      record_error(err, MOE_ERR_TIMEOUT_CODE, where);
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
 }
 
 // One stage of loads.
@@ -162,8 +185,9 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_kernel(const __grid_co
   const int where0 = p.code << 24 | rank << 23;
   auto where = [&](int role, int i) { return where0 | role << 20 | (i & 0xfffff); };
 
-  if (warp == 0) {
-    if (lane == 0) {
+  if (warp < 4) {
+    regs_give<kIssueRegs>();
+    if (warp == 0 && lane == 0) {
       tma_prefetch_desc(&p.tmA);
       tma_prefetch_desc(&p.tmB);
       int stage = 0;
@@ -194,8 +218,8 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_kernel(const __grid_co
         for (int s = 0; s < NST; ++s)
           if (filled & (1u << s)) mbar_wait_drain(&ss.full[s], (fill_par >> s) & 1);
     }
-  } else if (warp == 1) {
-    if (rank == 0) {
+    __syncwarp();
+    if (warp == 1 && rank == 0) {
       constexpr uint32_t idesc = Op::F16 ? idesc_f16_f32(kBM * CG, kBN, Op::A_MN ? 1 : 0, Op::B_MN ? 1 : 0)
                                          : idesc_bf16_f32(kBM * CG, kBN, Op::A_MN ? 1 : 0, Op::B_MN ? 1 : 0);
       int stage = 0, it = 0;
@@ -257,11 +281,12 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_kernel(const __grid_co
       }
     }
   } else {
+    regs_take<kEpiRegs>();
     DenseEpi e;
-    e.stg = stg_base + (warp - 2) * kDenseStg;
+    e.stg = stg_base + (warp - 4) * kDenseStg;
     e.lane = lane;
     e.q = warp & 3;  // TMEM lanes [32q, 32q + 32) are reachable from this warp
-    e.part = (warp - 2) >> 2;
+    e.part = (warp - 4) >> 2;
     int it = 0;
     bool ok = true;
     for (int i = first; ok && i < p.total && !*abort; i += step) {
@@ -279,7 +304,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_kernel(const __grid_co
 #pragma unroll 1
       for (int r = 0; r < runs; ++r) {
         const int buf = it & 1;
-        if (!mbar_wait(&ss.tfull[buf], (it >> 1) & 1, abort, p.err, where(4, i))) {
+        if (!mbar_wait_inline(&ss.tfull[buf], (it >> 1) & 1, abort, p.err, where(4, i))) {
           ok = false;
           break;
         }

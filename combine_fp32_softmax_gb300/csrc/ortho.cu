@@ -91,12 +91,29 @@ struct OrthoOp {
     am = t.m0;
     bn = t.n0;
   }
-  static __device__ __forceinline__ float pre(const Params& p, const DenseTile& t, const DenseEpi&) {
-    return p.first ? p.scal[t.mat] : 1.f / kSX;
+  // Read while the tile's products still run: the first step's factor and, for
+  // square and update, this thread's 128 values of the old matrix.
+  struct Pre {
+    float r;
+    uint4 old[SYM && KIND != kSquare ? 1 : 16];
+  };
+  static __device__ __forceinline__ Pre pre(const Params& p, const DenseTile& t, const DenseEpi& e) {
+    Pre o;
+    o.r = p.first ? p.scal[t.mat] : 1.f / kSX;
+    if constexpr (KIND == kSquare || !SYM) {
+      const int x = t.n0 + 128 * e.part, row = t.m0 + 32 * e.q + e.lane;
+      const uint4* from =
+          reinterpret_cast<const uint4*>(p.old + (static_cast<size_t>(t.mat) * p.M + row) * p.pitch + x);
+#pragma unroll
+      for (int u = 0; u < 16; ++u)  // the pitch is a multiple of 64
+        o.old[u] = row < p.M && x + 8 * u < p.pitch && t.kb1 > t.kb0 ? from[u] : make_uint4(0, 0, 0, 0);
+    }
+    return o;
   }
-  static __device__ __forceinline__ void epilogue(const Params& p, const DenseTile& t, DenseEpi& e, float r,
+  static __device__ __forceinline__ void epilogue(const Params& p, const DenseTile& t, DenseEpi& e, const Pre& pre,
                                                   uint32_t (&acc)[4][32]) {
     if (t.kb1 == t.kb0) return;
+    const float r = pre.r;
     const int x0 = t.n0 + 128 * e.part, y = t.m0 + 32 * e.q;
     // gram: A = r^2 sums; square: B = b A + c sums; update: X' = a r X + r sums
     const float fs = KIND == kSquare                         ? kNsC * (kSB / (kSA * kSA))
@@ -111,19 +128,15 @@ struct OrthoOp {
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] = fs * __uint_as_float(acc[c][j]);
       if constexpr (KIND == kSquare || !SYM) {
-        if (y + e.lane < p.M) {
-          const uint4* from = reinterpret_cast<const uint4*>(
-              p.old + (static_cast<size_t>(t.mat) * p.M + y + e.lane) * p.pitch + x);
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const uint4 w = from[u];  // x is a multiple of 32, the pitch of 64
-            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+        for (int u = 0; u < 4; ++u) {
+          const uint4 w = pre.old[4 * c + u];
+          const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float2 o = unpack_f16(ws[k]);
-              v[8 * u + 2 * k] = fmaf(fo, o.x, v[8 * u + 2 * k]);
-              v[8 * u + 2 * k + 1] = fmaf(fo, o.y, v[8 * u + 2 * k + 1]);
-            }
+          for (int k = 0; k < 4; ++k) {
+            const float2 o = unpack_f16(ws[k]);
+            v[8 * u + 2 * k] = fmaf(fo, o.x, v[8 * u + 2 * k]);
+            v[8 * u + 2 * k + 1] = fmaf(fo, o.y, v[8 * u + 2 * k + 1]);
           }
         }
       }

@@ -307,6 +307,16 @@ __device__ __forceinline__ float lds_bf16(uint32_t addr) {
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
   return __uint_as_float(static_cast<uint32_t>(v) << 16);
 }
+// Registers of a warpgroup's threads from here on (every warp of it calls
+// this); a kernel's warpgroups may not come to more than its launch's total.
+template <int N>
+__device__ __forceinline__ void regs_give() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_take() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
 // ------------------------------------------------------------------ tcgen05
 // CG is the tcgen05 CTA group of the kernel: 1, or 2 for a CTA pair whose
 // MMAs are issued by the pair's even CTA.  Every tcgen05 instruction of a

@@ -11,7 +11,7 @@
 // token's small loss does not come out of the difference of two large numbers.
 //
 // The backward takes the vocabulary in pieces: the product again, with an
-// epilogue that turns logits into D (bf16, or the sum of two bf16 values where a
+// epilogue that turns logits into D (bf16, or the sum of three bf16 values where a
 // gradient is kept in fp32), then the two products that read D.
 #include <algorithm>
 #include <cstring>
@@ -24,11 +24,16 @@ namespace {
 
 constexpr int kCodeXent = 0x11;  // + operation, in the error word of a wait that ran out
 
-// K blocks of a run of sums where fp32 results come out: 16 tensor-core steps.
-constexpr int kExactRun = 4;
+// K blocks of a run of sums where fp32 results come out.
+#ifndef XRUN
+#define XRUN 8
+#endif
+constexpr int kExactRun = XRUN;
 // Bytes of D that a piece of the vocabulary takes at least, and its columns at least.
 constexpr size_t kPieceBytes = size_t(512) << 20;
 constexpr int kPieceCols = 8192;
+// bf16 values that D is the sum of where a gradient comes out in fp32: 24 bits.
+constexpr int kTerms = 3;
 
 struct Target {
   const void* p;
@@ -160,7 +165,7 @@ struct GradOp {
     const float* dloss;
     const float* dlse;  // or null
     int V, v0;          // the piece is columns [v0, v0 + N) of V; columns from V on are zeros
-    int split;          // D is the sum of two bf16 values, the second N columns further
+    int terms;          // D is the sum of so many bf16 values, each N columns further
   };
   struct Pre {
     float w, lse, at;  // of exp(z - lse); log of the sum; D at the target
@@ -201,38 +206,41 @@ struct GradOp {
     const int y = t.m0 + 32 * e.q;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      uint32_t hi[16], lo[16];
+      float f[32];
 #pragma unroll
-      for (int u = 0; u < 16; ++u) {
-        float d[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int j = 32 * c + 2 * u + k;
-          const float v = r.w * __expf(__uint_as_float(acc[c][2 * u + k]) - r.lse);
-          // a row that no gradient reaches adds nothing, whatever its logits are
-          d[k] = (r.w != 0.f && j < n) ? v : 0.f;
-          if (j == r.rel) d[k] = r.at;
-        }
-        hi[u] = pack_bf16(d[0], d[1]);
-        lo[u] = pack_bf16(d[0] - bf16_lo(hi[u]), d[1] - bf16_hi(hi[u]));
+      for (int j = 0; j < 32; ++j) {
+        const float v = r.w * __expf(__uint_as_float(acc[c][j]) - r.lse);
+        // a row that no gradient reaches adds nothing, whatever its logits are
+        f[j] = (r.w != 0.f && 32 * c + j < n) ? v : 0.f;
+        if (32 * c + j == r.rel) f[j] = r.at;
       }
-      dense_store(e, hi, &p.tmO, col + 32 * c, y, 0);
-      if (p.split) dense_store(e, lo, &p.tmO, p.N + col + 32 * c, y, 0);
+      for (int k = 0;; ++k) {
+        uint32_t w[16];
+#pragma unroll
+        for (int u = 0; u < 16; ++u) w[u] = pack_bf16(f[2 * u], f[2 * u + 1]);
+        dense_store(e, w, &p.tmO, k * p.N + col + 32 * c, y, 0);
+        if (k + 1 == p.terms) break;
+#pragma unroll
+        for (int u = 0; u < 16; ++u) {  // what the value so far leaves, exactly
+          f[2 * u] -= bf16_lo(w[u]);
+          f[2 * u + 1] -= bf16_hi(w[u]);
+        }
+      }
     }
   }
 };
 
 // ----------------------------------------------- backward: products of D
-// out (+)= A . B with 16-bit or fp32 results.  DX: A = D [T, N (+ N)], B = rows
-// [v0, ..) of W, K runs over the piece (and once more over it for the second
-// halves of D).  DW: A = D^T, B = x, K runs over the tokens.
+// out (+)= A . B with 16-bit or fp32 results.  DX: A = D [T, terms N], B = rows
+// [v0, ..) of W, K runs over the piece, once for each bf16 term of D.  DW: A =
+// D^T, B = x, K runs over the tokens, likewise.
 template <bool DX>
 struct ProdOp {
   static constexpr bool A_MN = !DX, B_MN = true, F16 = false, ONE = true;
   struct Params : DenseParams {
     int v0;           // DX: the piece's first column of the vocabulary
-    int half;         // K blocks after which the second halves of D come
-    int cols;         // columns of the piece: where D's second halves are
+    int once;         // K blocks of one of D's bf16 terms
+    int cols;         // columns of the piece: from one term of D to the next
     int per_split;    // DX: K blocks of a split; each has a matrix of its own in out
     const float* prev;  // added to the products, laid out as out is in fp32
     int bf16;         // type of out
@@ -248,15 +256,14 @@ struct ProdOp {
   }
   static __device__ __forceinline__ void coords(const Params& p, const DenseTile& t, int kb, int& ak, int& am, int& bk,
                                                 int& bn) {
-    const bool second = kb >= p.half;
-    const int k = (second ? kb - p.half : kb) * kBK;
+    const int term = kb / p.once, k = (kb - term * p.once) * kBK;
     if constexpr (DX) {
-      ak = kb * kBK;  // the second halves follow the first in a row of D
+      ak = kb * kBK;  // the terms follow one another in a row of D
       am = t.m0;
       bk = p.v0 + k;
     } else {
       ak = bk = k;
-      am = t.m0 + (second ? p.cols : 0);
+      am = t.m0 + term * p.cols;
     }
     bn = t.n0;
   }
@@ -343,20 +350,20 @@ struct Plan {
 };
 
 // Splits of dx's sums over the vocabulary: where its tiles are fewer than the
-// SMs can run at one time, several of them share a tile's K.
-int dx_splits(int T, int d) {
+// SMs can run at one time, several of them share a tile's K, at least 8 blocks each.
+int dx_splits(int T, int d, int cols) {
   const int cg = T <= kBM ? 1 : 2;
   const int tiles = ceil_div(T, kBM * cg) * ceil_div(d, kBN);
-  return std::max(1, std::min(kMaxSplits, 152 / cg / tiles));
+  return std::max(1, std::min({kMaxSplits, 152 / cg / tiles, cols / (8 * kBK)}));
 }
 
 Plan plan(int T, int V, int d, int backward) {
   Plan p{};
   const int nt = ceil_div(V, kBN);
   const long long want = std::max<long long>(kPieceBytes / 2 / T / kBN * kBN, kPieceCols);
-  // both halves of D for the whole vocabulary at most
-  p.cols = static_cast<int>(std::min<long long>(want, 2ll * nt * kBN));
-  p.splits = dx_splits(T, d);
+  // every term of D for the whole vocabulary at most
+  p.cols = static_cast<int>(std::min<long long>(want, 1ll * kTerms * nt * kBN));
+  p.splits = dx_splits(T, d, std::min(p.cols, nt * kBN));
   size_t o = 0;
   auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -427,8 +434,7 @@ int launch_xent_bwd(const XentArgs& a, cudaStream_t s) {
   float* accbuf = reinterpret_cast<float*>(ws + L.acc);
   uint16_t* xz = reinterpret_cast<uint16_t*>(ws + L.xz);
   const Target target{a.target, a.target_type};
-  const int split = (a.dx && a.dx_type == MOE_Y_F32) || (a.dW && a.dW_type == MOE_Y_F32);
-  const int h = 1 + split;
+  const int h = (a.dx && a.dx_type == MOE_Y_F32) || (a.dW && a.dW_type == MOE_Y_F32) ? kTerms : 1;
   // pieces of about equal size, whole tiles wide
   const int most = L.cols / h / kBN * kBN;
   const int pieces = ceil_div(a.V, most);
@@ -468,7 +474,7 @@ int launch_xent_bwd(const XentArgs& a, cudaStream_t s) {
       p.dlse = a.dlse;
       p.V = a.V;
       p.v0 = v0;
-      p.split = split;
+      p.terms = h;
       if ((rc = launch_rows<GradOp>(p, a.T, a, MOE_K_XENT_GRAD, s)) != MOE_OK) return rc;
     }
     if (a.dx) {
@@ -478,8 +484,8 @@ int launch_xent_bwd(const XentArgs& a, cudaStream_t s) {
       p.M = a.T;
       p.N = a.d;
       p.nt = ceil_div(a.d, kBN);
-      p.half = cols / kBK;
-      p.nkb = f32 ? 2 * p.half : p.half;
+      p.once = cols / kBK;
+      p.nkb = f32 ? kTerms * p.once : p.once;
       p.run_kb = f32 ? kExactRun : p.nkb;
       p.code = kCodeXent + 2;
       p.err = err;
@@ -510,8 +516,8 @@ int launch_xent_bwd(const XentArgs& a, cudaStream_t s) {
       p.M = real;
       p.N = a.d;
       p.nt = ceil_div(a.d, kBN);
-      p.half = ceil_div(a.T, kBK);
-      p.nkb = f32 ? 2 * p.half : p.half;
+      p.once = ceil_div(a.T, kBK);
+      p.nkb = f32 ? kTerms * p.once : p.once;
       p.run_kb = f32 ? kExactRun : p.nkb;
       p.code = kCodeXent + 3;
       p.err = err;

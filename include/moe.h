@@ -448,7 +448,7 @@ int moe_xent_fwd(int T, int V, int d, const uint16_t* x, const uint16_t* W, cons
  * each fp32 or bf16 (MOE_Y_F32, MOE_Y_BF16), either NULL if not wanted.  D is
  * formed from the logits again, in pieces of the vocabulary, and enters the
  * products in bf16 (2^-8 of each value, beside the final rounding) for bf16
- * results and as the sum of two bf16 values (2^-16) for fp32 ones, whose runs of
+ * results and as the sum of three bf16 values (24 bits) for fp32 ones, whose runs of
  * sums are kept short as the logits' are.  A token whose dloss and dlse are 0 or
  * that has neither target nor dlse adds nothing, whatever x holds. */
 int moe_xent_bwd(int T, int V, int d, const uint16_t* x, const uint16_t* W, const void* target, int target_type,
