@@ -28,7 +28,7 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnits = 152 * 8;  // blocks to spread the tokens over; fixed, so the sums' order is
+constexpr int kUnits = 152 * 6;  // blocks to spread the tokens over; fixed, so the sums' order is
 
 // Blocks of a sequence: at least 32 tokens each, so that all blocks' sums fit in
 // the E ceil(T / 32) words of the histogram regions of the workspace.
@@ -136,7 +136,7 @@ __device__ __forceinline__ void finish_sequence(const BalanceOut& o, int b, int 
 }
 
 template <class Y>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 6)
     balance_sums_kernel(const float* __restrict__ logits, const int32_t* __restrict__ topk_idx,
                         const uint8_t* __restrict__ mask, int L, int B, int parts, int E, int k, int32_t* __restrict__ counts,
                         float* __restrict__ psums, float2* __restrict__ zn, BalanceOut out, int* err) {
@@ -155,23 +155,23 @@ __global__ void __launch_bounds__(kThreads)
     hist[threadIdx.x] = 0;
     __syncthreads();
     const int t0 = b * L + min(L, c * per), t1 = b * L + min(L, (c + 1) * per);
-    for (int i = threadIdx.x; i < (t1 - t0) * k; i += kThreads) {
-      const int t = t0 + i / k;
-      if (mask && !mask[t]) continue;  // whatever it holds
-      const int e = topk_idx[static_cast<size_t>(t0) * k + i];
-      if (static_cast<unsigned>(e) < static_cast<unsigned>(E))
-        atomicAdd(&hist[e], 1);
-      else
-        record_error(err, MOE_ERR_ARG, t);
-    }
-    float p[Y::E] = {};
-    float z = 0.f;
-    int n = 0;
     auto live = [&](int t) { return t < t1 && (!mask || mask[t]); };
     int t = t0 + warp * ROWS + sub;
     bool on = live(t);
     float v[Y::E];
     load_values<Y>(logits + static_cast<size_t>(t) * E, on ? E : 0, l, v, -INFINITY);
+    for (int i = threadIdx.x; i < (t1 - t0) * k; i += kThreads) {
+      const int ti = t0 + i / k;
+      if (mask && !mask[ti]) continue;  // whatever it holds
+      const int e = topk_idx[static_cast<size_t>(t0) * k + i];
+      if (static_cast<unsigned>(e) < static_cast<unsigned>(E))
+        atomicAdd(&hist[e], 1);
+      else
+        record_error(err, MOE_ERR_ARG, ti);
+    }
+    float p[Y::E] = {};
+    float z = 0.f;
+    int n = 0;
     for (int tw = t0 + warp * ROWS; tw < t1; tw += WARPS * ROWS) {  // the same rounds for all lanes of the warp
       // the next row is on its way while this one is worked on
       const int tn = t + WARPS * ROWS;
@@ -233,55 +233,76 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// One block a sequence: the experts of a part side by side, groups of threads on
-// every (1024 / width)-th part, then the groups in their order.
+// One block a sequence: a thread takes V experts (a 16-byte piece where rows are
+// whole ones) of every (1024 / width)-th part, then the groups of threads are
+// added in a fixed order.
+template <int V>
 __global__ void __launch_bounds__(1024)
     balance_join_kernel(const int32_t* __restrict__ counts, const float* __restrict__ psums, const float2* __restrict__ zn,
                         int B, int parts, int E, int k, BalanceOut out) {
   griddep_wait();
   griddep_launch_dependents();
-  __shared__ float sp[1024];
-  __shared__ int sc[1024];
+  __shared__ float sp[1024 * V];
+  __shared__ int sc[1024 * V];
   __shared__ float red[8], zred[32];
   __shared__ int nred[32];
-  int shift = 1;  // of the groups' width, a power of two of at least E and 2
-  while ((1 << shift) < E) ++shift;
-  const int groups = 1024 >> shift, g = threadIdx.x >> shift, e = threadIdx.x & ((1 << shift) - 1);
+  const int tid = threadIdx.x;
+  int shift = 0;  // of the groups' width, a power of two of at least E / V
+  while ((V << shift) < E) ++shift;
+  const int groups = 1024 >> shift, g = tid >> shift, e = V * (tid & ((1 << shift) - 1));
   for (int b = blockIdx.x; b < B; b += gridDim.x) {
-    Sum2 s, z;
-    int c = 0, n = 0;
+    Sum2 s[V], z;
+    int c[V] = {}, n = 0;
     const size_t at = static_cast<size_t>(b) * parts;
     if (e < E) {
-#pragma unroll 8
+#pragma unroll 4
       for (int i = g; i < parts; i += groups) {
-        s.add(psums[(at + i) * E + e]);
-        c += counts[(at + i) * E + e];
+        const size_t from = (at + i) * E + e;
+        if constexpr (V == 4) {
+          const float4 p = *reinterpret_cast<const float4*>(psums + from);
+          const int4 q = *reinterpret_cast<const int4*>(counts + from);
+          s[0].add(p.x);
+          s[1].add(p.y);
+          s[2].add(p.z);
+          s[3].add(p.w);
+          c[0] += q.x;
+          c[1] += q.y;
+          c[2] += q.z;
+          c[3] += q.w;
+        } else {
+          s[0].add(psums[from]);
+          c[0] += counts[from];
+        }
       }
     }
-    for (int i = threadIdx.x; i < parts; i += 1024) {
+    for (int i = tid; i < parts; i += 1024) {
       const float2 v = zn[at + i];
       z.add(v.x);
       n += static_cast<int>(v.y);  // tokens of a part: far below 2^24
     }
-    sp[threadIdx.x] = s.value();
-    sc[threadIdx.x] = c;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      sp[V * tid + j] = s[j].value();
+      sc[V * tid + j] = c[j];
+    }
     float zs = z.value();
 #pragma unroll
     for (int off = 16; off; off >>= 1) {
       zs += __shfl_xor_sync(kFull, zs, off);
       n += __shfl_xor_sync(kFull, n, off);
     }
-    if ((threadIdx.x & 31) == 0) {
-      zred[threadIdx.x >> 5] = zs;
-      nred[threadIdx.x >> 5] = n;
+    if ((tid & 31) == 0) {
+      zred[tid >> 5] = zs;
+      nred[tid >> 5] = n;
     }
-    // the groups, halved: a fixed order
     for (int h = groups >> 1; h; h >>= 1) {
       __syncthreads();
-      if (g < h) {
-        sp[threadIdx.x] += sp[threadIdx.x + (h << shift)];
-        sc[threadIdx.x] += sc[threadIdx.x + (h << shift)];
-      }
+      if (g < h)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          sp[V * tid + j] += sp[V * (tid + (h << shift)) + j];
+          sc[V * tid + j] += sc[V * (tid + (h << shift)) + j];
+        }
     }
     __syncthreads();
     zs = 0.f;
@@ -290,14 +311,14 @@ __global__ void __launch_bounds__(1024)
       zs += zred[i];
       n += nred[i];
     }
-    finish_sequence(out, b, E, k, sc[threadIdx.x], sp[threadIdx.x], zs, n, red);
+    finish_sequence(out, b, E, k, sc[tid], sp[tid], zs, n, red);  // expert e's sums are at e
     __syncthreads();
   }
 }
 
 // dlogits = add + gradient; add may be dlogits itself or null.
 template <class Y>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
     balance_bwd_kernel(const float* __restrict__ logits, const int32_t* __restrict__ counts, const uint8_t* __restrict__ mask,
                        const float* __restrict__ dloss, const float* __restrict__ dz, int T, int L, int E, int k,
                        const float* add, float* dlogits) {
@@ -402,15 +423,15 @@ cudaError_t launch_balance(const float* logits, const int32_t* topk_idx, const u
   TraceScope trace_scope(MOE_K_BALANCE, s);
   const int parts = seq_parts(T, B);
   const BalanceOut out{counts, mean_p, loss, zloss};
-  const int units = static_cast<int>(std::min<long long>(static_cast<long long>(B) * parts, num_sms() * 8));
+  const int units = static_cast<int>(std::min<long long>(static_cast<long long>(B) * parts, num_sms() * 6));
   float2* zn = reinterpret_cast<float2*>(part_zn);
   cudaError_t e = with_layout(E, [&](auto y) {
     return launch_pdl(balance_sums_kernel<decltype(y)>, dim3(units), dim3(kThreads), 0, s, logits, topk_idx, mask, T / B, B,
                       parts, E, k, part_counts, part_p, zn, out, err);
   });
   if (e == cudaSuccess && parts > 1)
-    e = launch_pdl(balance_join_kernel, dim3(std::min(B, 65535)), dim3(1024), 0, s, part_counts, part_p, zn, B, parts, E, k,
-                   out);
+    e = launch_pdl(E % 4 ? balance_join_kernel<1> : balance_join_kernel<4>, dim3(std::min(B, 65535)), dim3(1024), 0, s,
+                   part_counts, part_p, zn, B, parts, E, k, out);
   return e;
 }
 
@@ -420,7 +441,7 @@ cudaError_t launch_balance_bwd(const float* logits, const int32_t* counts, const
   TraceScope trace_scope(MOE_K_BALANCE_BWD, s);
   return with_layout(E, [&](auto y) {
     const long long warps = ceil_div(T, 32 / decltype(y)::LANES);
-    const int blocks = static_cast<int>(std::min<long long>(ceil_div(warps, kThreads / 32), num_sms() * 8));
+    const int blocks = static_cast<int>(std::min<long long>(ceil_div(warps, kThreads / 32), num_sms() * 4));
     return launch_pdl(balance_bwd_kernel<decltype(y)>, dim3(blocks), dim3(kThreads), 0, s, logits, counts, mask, dloss, dz, T,
                       T / B, E, k, add, dlogits);
   });

@@ -55,7 +55,9 @@ struct DenseParams {
   CUtensorMap tmA, tmB;  // operands
   CUtensorMap tmO;       // what the epilogue stores by TMA
   int M, N;              // rows and columns of C
-  int mt, nt;            // tiles of its rows (of TILE_M) and columns (of 256)
+  int mt, nt;            // tiles of its rows (of TILE_M) and columns (of tn)
+  int tn;                // columns of a tile: 256, on single CTAs also fewer (a multiple of 16)
+  int b_bytes;           // of B in one CTA's part of a stage
   int nkb;               // K blocks
   int run_kb;            // K blocks of a run of sums
   int total;             // tiles of the launch
@@ -68,6 +70,15 @@ struct DenseTile {
   int mat, m0, n0;  // matrix, first row (of this CTA) and column
   int kb0, kb1;     // its K blocks
 };
+// Columns of C in a tile, and the N of its MMAs: a last tile with fewer columns
+// takes less of the tensor core's time.  A pair's CTAs hold half of them each, in
+// whole groups of 64 where B is MN-major.
+__device__ __forceinline__ int dense_cols(const DenseParams& p, const DenseTile& t) { return min(p.tn, p.N - t.n0); }
+template <int CG, bool B_MN>
+__device__ __forceinline__ int dense_mma_n(const DenseParams& p, const DenseTile& t) {
+  constexpr int unit = CG == 1 ? 16 : B_MN ? 128 : 64;
+  return (dense_cols(p, t) + unit - 1) / unit * unit;
+}
 
 struct DenseEpi {
   uint8_t* stg;
@@ -109,11 +120,11 @@ __device__ __forceinline__ bool mbar_wait_inline(uint64_t* bar, uint32_t parity,
 
 // One stage of loads.
 template <class Op, int CG>
-__device__ __forceinline__ void dense_loads(const typename Op::Params& p, const DenseTile& t, int kb, uint8_t* sA,
-                                            uint8_t* sB, uint64_t* bar, int rank) {
+__device__ __forceinline__ void dense_loads(const typename Op::Params& p, const DenseTile& t, int kb, int b_off,
+                                            uint8_t* sA, uint8_t* sB, uint64_t* bar, int rank) {
   int ak, am, bk, bn;
   Op::coords(p, t, kb, ak, am, bk, bn);
-  bn += CG == 2 ? 128 * rank : 0;
+  bn += b_off;
   const bool to_even = CG == 2 && rank == 1;
   const int mat = Op::ONE ? 0 : t.mat;  // ONE: a single A and B, t.mat tells results apart
   if constexpr (Op::A_MN) {
@@ -195,6 +206,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_kernel(const __grid_co
       bool ok = true;
       for (int i = first; ok && i < p.total && !*abort; i += step) {
         const DenseTile t = Op::template tile<CG>(p, i, rank);
+        const int b_off = CG == 2 ? rank * dense_mma_n<CG, Op::B_MN>(p, t) / 2 : 0;
         for (int kb = t.kb0; kb < t.kb1; ++kb) {
           if (!mbar_wait(&ss.empty[stage], phase ^ 1, abort, p.err, where(0, i))) {
             ok = false;
@@ -203,11 +215,11 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_kernel(const __grid_co
           uint8_t* sA = smem + stage * SB;
           // a pair's loads are all counted on the even CTA's barrier
           if (rank == 0) {
-            mbar_arrive_expect_tx(&ss.full[stage], CG * SB);
+            mbar_arrive_expect_tx(&ss.full[stage], CG * (kABytes + p.b_bytes));
             filled |= 1u << stage;
             fill_par = (fill_par & ~(1u << stage)) | phase << stage;
           }
-          dense_loads<Op, CG>(p, t, kb, sA, sA + kABytes, &ss.full[stage], rank);
+          dense_loads<Op, CG>(p, t, kb, b_off, sA, sA + kABytes, &ss.full[stage], rank);
           if (++stage == NST) {
             stage = 0;
             phase ^= 1;
@@ -220,13 +232,14 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_kernel(const __grid_co
     }
     __syncwarp();
     if (warp == 1 && rank == 0) {
-      constexpr uint32_t idesc = Op::F16 ? idesc_f16_f32(kBM * CG, kBN, Op::A_MN ? 1 : 0, Op::B_MN ? 1 : 0)
-                                         : idesc_bf16_f32(kBM * CG, kBN, Op::A_MN ? 1 : 0, Op::B_MN ? 1 : 0);
+      constexpr uint32_t idesc0 = Op::F16 ? idesc_f16_f32(kBM * CG, 0, Op::A_MN ? 1 : 0, Op::B_MN ? 1 : 0)
+                                          : idesc_bf16_f32(kBM * CG, 0, Op::A_MN ? 1 : 0, Op::B_MN ? 1 : 0);
       int stage = 0, it = 0;
       uint32_t phase = 0;
       bool ok = true, issued = false;
       for (int i = first; ok && i < p.total && !*abort; i += step) {
         const DenseTile t = Op::template tile<CG>(p, i, rank);
+        const uint32_t idesc = idesc0 | static_cast<uint32_t>(dense_mma_n<CG, Op::B_MN>(p, t) >> 3) << 17;
         int left = 0;  // K blocks left of the run
         uint32_t dtm = 0;
         for (int kb = t.kb0; ok && kb < t.kb1; ++kb) {
@@ -381,6 +394,10 @@ int dense_resident() {
 
 template <class Op, int CG>
 int dense_launch(typename Op::Params& p, int grid_limit, int trace, cudaStream_t s) {
+  if (p.tn == 0) {  // whole tiles
+    p.tn = kBN;
+    p.b_bytes = DensePipe<CG>::B_BYTES;
+  }
   const int resident = dense_resident<Op, CG>();
   if (resident <= 0) return MOE_ERR_CUDA;
   int units = resident;

@@ -25,10 +25,10 @@ namespace {
 constexpr int kCodeXent = 0x11;  // + operation, in the error word of a wait that ran out
 
 // K blocks of a run of sums where fp32 results come out.
-#ifndef XRUN
-#define XRUN 8
-#endif
-constexpr int kExactRun = XRUN;
+// Short ones leave the epilogue less time beside the products (two runs wait at
+// most): at 8192 tokens of d = 2048 and V = 100000 the forward takes 2.37, 2.22 and
+// 2.20 ms with runs of 4, 8 and 16 blocks, the pieces' D 2.74, 2.40 and 2.38 ms.
+constexpr int kExactRun = 8;
 // Bytes of D that a piece of the vocabulary takes at least, and its columns at least.
 constexpr size_t kPieceBytes = size_t(512) << 20;
 constexpr int kPieceCols = 8192;
@@ -50,7 +50,7 @@ __device__ __forceinline__ int load_target(const Target& g, int t, int V) {
 template <int CG>
 __device__ __forceinline__ DenseTile rows_first(const DenseParams& p, int i, int rank) {
   const int nb = i / p.mt, mb = i - nb * p.mt;
-  return {0, mb * DensePipe<CG>::TILE_M + rank * kBM, nb * kBN, 0, p.nkb};
+  return {0, mb * DensePipe<CG>::TILE_M + rank * kBM, nb * p.tn, 0, p.nkb};
 }
 
 // ------------------------------------------------------------- forward
@@ -79,7 +79,7 @@ struct StatsOp {
                                                   uint32_t (&acc)[4][32]) {
     const int row = t.m0 + 32 * e.q + e.lane;
     const int col = t.n0 + 128 * e.part;
-    const int n = p.N - col;  // columns that exist
+    const int n = dense_cols(p, t) - 128 * e.part;  // columns that the tile has
     if (n < 128) {
 #pragma unroll
       for (int c = 0; c < 4; ++c)
@@ -102,10 +102,10 @@ struct StatsOp {
 #pragma unroll
       for (int j = 0; j < 32; ++j) s4[j & 3] += __expf(__uint_as_float(acc[c][j]) - base);
     if (row < p.M)
-      p.part[static_cast<size_t>(row) * (2 * p.nt) + 2 * (t.n0 / kBN) + e.part] =
+      p.part[static_cast<size_t>(row) * (2 * p.nt) + 2 * (t.n0 / p.tn) + e.part] =
           make_float2(m, (s4[0] + s4[1]) + (s4[2] + s4[3]));
     const int rel = target - col;
-    const bool here = target >= 0 && rel >= 0 && rel < 128;
+    const bool here = target >= 0 && rel >= 0 && rel < min(n, 128);
     if (__any_sync(0xffffffffu, here)) {
       uint32_t z = 0u;
 #pragma unroll
@@ -203,9 +203,11 @@ struct GradOp {
                                                   uint32_t (&acc)[4][32]) {
     const int col = t.n0 + 128 * e.part;   // of the piece
     const int n = p.V - (p.v0 + col);      // columns that exist
+    const int w = dense_cols(p, t) - 128 * e.part;  // columns that the tile has, a multiple of 32
     const int y = t.m0 + 32 * e.q;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
+      if (32 * c >= w) break;
       float f[32];
 #pragma unroll
       for (int j = 0; j < 32; ++j) {
@@ -349,21 +351,50 @@ struct Plan {
   size_t err, part, zt, D, acc, xz, total;
 };
 
-// Splits of dx's sums over the vocabulary: where its tiles are fewer than the
-// SMs can run at one time, several of them share a tile's K, at least 8 blocks each.
+// Splits of dx's sums over a piece of the vocabulary: several CTAs share a tile's
+// K where the tiles do not fill the GPU's rounds.  Estimated: 0.28 us a K block and
+// round, 8 bytes of fp32 sums a split and element at 5 TB/s.
 int dx_splits(int T, int d, int cols) {
-  const int cg = T <= kBM ? 1 : 2;
+  const int cg = T <= kBM ? 1 : 2, units = 152 / cg, nkb = cols / kBK;
   const int tiles = ceil_div(T, kBM * cg) * ceil_div(d, kBN);
-  return std::max(1, std::min({kMaxSplits, 152 / cg / tiles, cols / (8 * kBK)}));
+  int best = 1;
+  double least = 1e30;
+  for (int s = 1; s <= kMaxSplits && (s == 1 || nkb / s >= 8); ++s) {
+    const double us = ceil_div(static_cast<long long>(tiles) * s, units) * (0.28 * ceil_div(nkb, s)) +
+                      (s > 1 ? s * 8.0 * T * d / 5e6 : 0.0);
+    if (us < 0.97 * least) {
+      least = us;
+      best = s;
+    }
+  }
+  return best;
+}
+
+// Columns of a tile of the logits where one row block has all tokens: the CTAs
+// get equal shares of the vocabulary's rows, which are all that counts then.
+int few_rows_tile(int cols, int unit) {
+  const int rounds = ceil_div(cols, 152 * kBN);
+  return std::min(kBN, ceil_div(ceil_div(cols, 152 * rounds), unit) * unit);
+}
+
+// Tiles of the logits [T, cols], tn a multiple of `unit`.
+void logit_tiles(DenseParams& p, int T, int cols, int unit) {
+  const bool single = T <= kBM;
+  p.tn = single ? few_rows_tile(cols, unit) : kBN;
+  p.b_bytes = single ? p.tn * 128 : DensePipe<2>::B_BYTES;
+  p.mt = single ? 1 : ceil_div(T, 2 * kBM);
+  p.nt = ceil_div(cols, p.tn);
+  p.total = p.mt * p.nt;
 }
 
 Plan plan(int T, int V, int d, int backward) {
   Plan p{};
-  const int nt = ceil_div(V, kBN);
+  const int nt = ceil_div(V, T <= kBM ? few_rows_tile(V, 16) : kBN);
+  const int all = ceil_div(V, kBN) * kBN;
   const long long want = std::max<long long>(kPieceBytes / 2 / T / kBN * kBN, kPieceCols);
   // every term of D for the whole vocabulary at most
-  p.cols = static_cast<int>(std::min<long long>(want, 1ll * kTerms * nt * kBN));
-  p.splits = dx_splits(T, d, std::min(p.cols, nt * kBN));
+  p.cols = static_cast<int>(std::min<long long>(want, 1ll * kTerms * all));
+  p.splits = dx_splits(T, d, std::min(p.cols, all));
   size_t o = 0;
   auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -387,11 +418,8 @@ Plan plan(int T, int V, int d, int backward) {
 }
 
 template <class Op>
-int launch_rows(typename Op::Params& p, int T, const XentArgs& a, int trace, cudaStream_t s) {
-  const bool single = T <= kBM;
-  p.mt = single ? 1 : ceil_div(T, 2 * kBM);
-  p.total = p.mt * p.nt;
-  return single ? dense_launch<Op, 1>(p, a.grid_limit, trace, s) : dense_launch<Op, 2>(p, a.grid_limit, trace, s);
+int launch_logits(typename Op::Params& p, const XentArgs& a, int trace, cudaStream_t s) {
+  return a.T <= kBM ? dense_launch<Op, 1>(p, a.grid_limit, trace, s) : dense_launch<Op, 2>(p, a.grid_limit, trace, s);
 }
 
 }  // namespace
@@ -404,12 +432,12 @@ int launch_xent_fwd(const XentArgs& a, cudaStream_t s) {
   int* err = reinterpret_cast<int*>(ws + L.err);
   StatsOp::Params p;
   std::memset(&p, 0, sizeof(p));
-  const uint32_t bn = a.T <= kBM ? 256 : 128;
-  if (!dense_map_k(&p.tmA, a.x, false, a.d, a.T, 1, a.d, 128) || !dense_map_k(&p.tmB, a.W, false, a.d, a.V, 1, a.d, bn))
+  logit_tiles(p, a.T, a.V, 16);
+  if (!dense_map_k(&p.tmA, a.x, false, a.d, a.T, 1, a.d, 128) ||
+      !dense_map_k(&p.tmB, a.W, false, a.d, a.V, 1, a.d, p.b_bytes / 128))
     return MOE_ERR_CUDA;
   p.M = a.T;
   p.N = a.V;
-  p.nt = ceil_div(a.V, kBN);
   p.nkb = a.d / kBK;
   p.run_kb = kExactRun;
   p.code = kCodeXent;
@@ -417,7 +445,7 @@ int launch_xent_fwd(const XentArgs& a, cudaStream_t s) {
   p.target = {a.target, a.target_type};
   p.part = reinterpret_cast<float2*>(ws + L.part);
   p.zt = reinterpret_cast<float*>(ws + L.zt);
-  const int rc = launch_rows<StatsOp>(p, a.T, a, MOE_K_XENT, s);
+  const int rc = launch_logits<StatsOp>(p, a, MOE_K_XENT, s);
   if (rc != MOE_OK) return rc;
   TraceScope trace_scope(MOE_K_XENT_JOIN, s);
   return launch_pdl(xent_join_kernel, dim3(ceil_div(a.T, 8)), dim3(256), 0, s, p.part, p.zt, p.target, a.T, a.V, 2 * p.nt,
@@ -456,13 +484,13 @@ int launch_xent_bwd(const XentArgs& a, cudaStream_t s) {
     {
       GradOp::Params p;
       std::memset(&p, 0, sizeof(p));
+      logit_tiles(p, a.T, cols, 32);
       if (!dense_map_k(&p.tmA, a.x, false, a.d, a.T, 1, a.d, 128) ||
-          !dense_map_k(&p.tmB, a.W, false, a.d, a.V, 1, a.d, single ? 256 : 128) ||
+          !dense_map_k(&p.tmB, a.W, false, a.d, a.V, 1, a.d, p.b_bytes / 128) ||
           !dense_map_out(&p.tmO, D, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, size_t(cols) * h, a.T, 1, size_t(cols) * h))
         return MOE_ERR_CUDA;
       p.M = a.T;
       p.N = cols;
-      p.nt = cols / kBN;
       p.nkb = a.d / kBK;
       p.run_kb = kExactRun;  // the forward's logits, bit for bit
       p.code = kCodeXent + 1;
@@ -475,7 +503,7 @@ int launch_xent_bwd(const XentArgs& a, cudaStream_t s) {
       p.V = a.V;
       p.v0 = v0;
       p.terms = h;
-      if ((rc = launch_rows<GradOp>(p, a.T, a, MOE_K_XENT_GRAD, s)) != MOE_OK) return rc;
+      if ((rc = launch_logits<GradOp>(p, a, MOE_K_XENT_GRAD, s)) != MOE_OK) return rc;
     }
     if (a.dx) {
       ProdOp<true>::Params p;

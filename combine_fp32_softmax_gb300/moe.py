@@ -452,55 +452,71 @@ def moe_q4_dequantize(codes, scales, W, group, stream=None):
 # ------------------------------------------------- the ends of a training step
 def _typed(name, t, dtypes, shape):
     """A required tensor must have one of the types and the shape."""
-    if t is None or t.dtype not in dtypes or tuple(t.shape) != tuple(shape):
+    if t is None or t.dtype not in dtypes or t.shape != shape:
         got = None if t is None else f"{tuple(t.shape)} of {t.dtype}"
         raise ValueError(f"{name}: {tuple(shape)} of {' or '.join(map(str, dtypes))} expected, got {got}")
 
 
-def _one_device(*tensors):
-    """The launches go to the current device: every tensor has to be there."""
+def _addresses(*tensors):
+    """Addresses of contiguous tensors on the current device, where the launches go (None stays None)."""
+    dev, out = _device(), []
     for t in tensors:
-        if t is not None and t.is_cuda and t.device.index != _device():
-            raise ValueError(f"a tensor on cuda:{t.device.index} while the current device is cuda:{_device()}")
+        if t is None:
+            out.append(None)
+            continue
+        if t.get_device() != dev or not t.is_contiguous():
+            raise ValueError(f"expected a contiguous tensor on the current device (cuda:{dev}), got one on {t.device}"
+                             + ("" if t.is_contiguous() else ", not contiguous"))
+        out.append(t.data_ptr())
+    return out
 
 
-def _token_mask(mask, T):
-    if mask is not None:
-        _typed("mask", mask, (torch.bool, _U8), (T,))
+_F32_ONLY, _I32_ONLY, _BF16_ONLY, _FLOATS = (_F32,), (_I32,), (_BF16,), (_F32, _BF16)
+_INDEX_TYPES, _MASK_TYPES = (_I32, torch.int64), (torch.bool, _U8)
+
+
+@functools.lru_cache(maxsize=1024)
+def _balance_sizes(key, B):
+    """The C configuration, the bytes of a workspace, and the shapes [T, E], [T, k], [B, E], [B], [T]."""
+    c = moe_cfg(*key) if isinstance(key, tuple) else moe_cfg.from_buffer_copy(key)
+    return (ctypes.byref(c), int(lib().moe_workspace_bytes(ctypes.byref(c))), torch.Size((c.T, c.E)), torch.Size((c.T, c.k)),
+            torch.Size((B, c.E)), torch.Size((B,)), torch.Size((c.T,)))
 
 
 def moe_balance_fwd(cfg, logits, topk_idx, mask, counts, mean_p, loss, zloss, ws, stream=None):
     """Picks and mean probabilities of each expert, counts int32 and mean_p fp32 [B, E], and the balance and z losses
     [B] of B sequences of T / B tokens; mask [T] bool (None: every token counts)."""
-    c = cfg if isinstance(cfg, moe_cfg) else cfg_of(cfg)
     B = loss.numel()
-    _typed("logits", logits, (_F32,), (c.T, c.E))
-    _typed("topk_idx", topk_idx, (_I32,), (c.T, c.k))
-    _typed("counts", counts, (_I32,), (B, c.E))
-    _typed("mean_p", mean_p, (_F32,), (B, c.E))
-    _typed("loss", loss, (_F32,), (B,))
-    _typed("zloss", zloss, (_F32,), (B,))
-    _token_mask(mask, c.T)
-    _one_device(logits, topk_idx, mask, counts, mean_p, loss, zloss, ws)
-    _call("moe_balance_fwd", _cfg(c), _ptr(logits), _ptr(topk_idx), _ptr(mask), B, _ptr(counts), _ptr(mean_p), _ptr(loss),
-          _ptr(zloss), _workspace(ws, moe_workspace_bytes(c)), _stream(stream))
+    c, nbytes, TE, Tk, BE, B_, T_ = _balance_sizes(_key(cfg), B)
+    _typed("logits", logits, _F32_ONLY, TE)
+    _typed("topk_idx", topk_idx, _I32_ONLY, Tk)
+    _typed("counts", counts, _I32_ONLY, BE)
+    _typed("mean_p", mean_p, _F32_ONLY, BE)
+    _typed("loss", loss, _F32_ONLY, B_)
+    _typed("zloss", zloss, _F32_ONLY, B_)
+    if mask is not None:
+        _typed("mask", mask, _MASK_TYPES, T_)
+    _workspace(ws, nbytes)
+    pz, pi, pm, pc, pp, pl, pzl, pw = _addresses(logits, topk_idx, mask, counts, mean_p, loss, zloss, ws)
+    _call("moe_balance_fwd", c, pz, pi, pm, B, pc, pp, pl, pzl, pw, _stream(stream))
 
 
 def moe_balance_bwd(cfg, logits, counts, mask, dloss, dzloss, dlogits_in, dlogits, ws, stream=None):
     """dlogits [T, E] = dlogits_in (None: 0; may be dlogits) + the gradient of dloss . loss + dzloss . zloss."""
-    c = cfg if isinstance(cfg, moe_cfg) else cfg_of(cfg)
     B = dloss.numel()
-    _typed("logits", logits, (_F32,), (c.T, c.E))
-    _typed("counts", counts, (_I32,), (B, c.E))
-    _typed("dloss", dloss, (_F32,), (B,))
-    _typed("dzloss", dzloss, (_F32,), (B,))
+    c, nbytes, TE, Tk, BE, B_, T_ = _balance_sizes(_key(cfg), B)
+    _typed("logits", logits, _F32_ONLY, TE)
+    _typed("counts", counts, _I32_ONLY, BE)
+    _typed("dloss", dloss, _F32_ONLY, B_)
+    _typed("dzloss", dzloss, _F32_ONLY, B_)
     if dlogits_in is not None:
-        _typed("dlogits_in", dlogits_in, (_F32,), (c.T, c.E))
-    _typed("dlogits", dlogits, (_F32,), (c.T, c.E))
-    _token_mask(mask, c.T)
-    _one_device(logits, counts, mask, dloss, dzloss, dlogits_in, dlogits, ws)
-    _call("moe_balance_bwd", _cfg(c), _ptr(logits), _ptr(counts), _ptr(mask), B, _ptr(dloss), _ptr(dzloss),
-          _ptr(dlogits_in), _ptr(dlogits), _workspace(ws, moe_workspace_bytes(c)), _stream(stream))
+        _typed("dlogits_in", dlogits_in, _F32_ONLY, TE)
+    _typed("dlogits", dlogits, _F32_ONLY, TE)
+    if mask is not None:
+        _typed("mask", mask, _MASK_TYPES, T_)
+    _workspace(ws, nbytes)
+    pz, pc, pm, pl, pzl, pin, po, pw = _addresses(logits, counts, mask, dloss, dzloss, dlogits_in, dlogits, ws)
+    _call("moe_balance_bwd", c, pz, pc, pm, B, pl, pzl, pin, po, pw, _stream(stream))
 
 
 MOE_I32, MOE_I64 = 0, 1
@@ -524,20 +540,20 @@ def _xent_shape(x, W, target, *rows):
     if x.dim() != 2 or W.dim() != 2 or x.shape[1] != W.shape[1]:
         raise ValueError(f"x [T, d] and W [V, d] expected, got {tuple(x.shape)} and {tuple(W.shape)}")
     (T, d), V = x.shape, W.shape[0]
-    _typed("x", x, (_BF16,), (T, d))
-    _typed("W", W, (_BF16,), (V, d))
-    _typed("target", target, (_I32, torch.int64), (T,))
+    _typed("x", x, _BF16_ONLY, x.shape)
+    _typed("W", W, _BF16_ONLY, W.shape)
+    _typed("target", target, _INDEX_TYPES, (T,))
     for name, t in rows:
-        _typed(name, t, (_F32,), (T,))
+        _typed(name, t, _F32_ONLY, (T,))
     return T, V, d, MOE_I32 if target.dtype is _I32 else MOE_I64
 
 
 def moe_xent_fwd(x, W, target, loss, lse, ws, stream=None):
     """loss [T] and lse [T] fp32 of the logits x [T, d] . W [V, d]^T against target [T] int32 or int64 (below 0: none)."""
     T, V, d, tt = _xent_shape(x, W, target, ("loss", loss), ("lse", lse))
-    _one_device(x, W, target, loss, lse, ws)
-    _call("moe_xent_fwd", T, V, d, _ptr(x), _ptr(W), _ptr(target), tt, _ptr(loss), _ptr(lse),
-          _workspace(ws, _xent_bytes(T, V, d, 0)), _stream(stream))
+    _workspace(ws, _xent_bytes(T, V, d, 0))
+    px, pW, pt, pl, ps, pw = _addresses(x, W, target, loss, lse, ws)
+    _call("moe_xent_fwd", T, V, d, px, pW, pt, tt, pl, ps, pw, _stream(stream))
 
 
 def moe_xent_bwd(x, W, target, loss, lse, dloss, dlse, dx, dW, ws, stream=None):
@@ -545,21 +561,27 @@ def moe_xent_bwd(x, W, target, loss, lse, dloss, dlse, dx, dW, ws, stream=None):
     lse being what moe_xent_fwd gave."""
     T, V, d, tt = _xent_shape(x, W, target, ("loss", loss), ("lse", lse), ("dloss", dloss))
     if dlse is not None:
-        _typed("dlse", dlse, (_F32,), (T,))
-    for name, t, rows in ("dx", dx, T), ("dW", dW, V):
-        if t is not None:
-            _typed(name, t, (_F32, _BF16), (rows, d))
-    _one_device(x, W, target, loss, lse, dloss, dlse, dx, dW, ws)
-    _call("moe_xent_bwd", T, V, d, _ptr(x), _ptr(W), _ptr(target), tt, _ptr(loss), _ptr(lse), _ptr(dloss), _ptr(dlse),
-          _ptr(dx), 0 if dx is None else _y_type(dx), _ptr(dW), 0 if dW is None else _y_type(dW),
-          _workspace(ws, _xent_bytes(T, V, d, 1)), _stream(stream))
+        _typed("dlse", dlse, _F32_ONLY, (T,))
+    if dx is not None:
+        _typed("dx", dx, _FLOATS, (T, d))
+    if dW is not None:
+        _typed("dW", dW, _FLOATS, (V, d))
+    _workspace(ws, _xent_bytes(T, V, d, 1))
+    px, pW, pt, pl, ps, pdl, pds, pdx, pdW, pw = _addresses(x, W, target, loss, lse, dloss, dlse, dx, dW, ws)
+    _call("moe_xent_bwd", T, V, d, px, pW, pt, tt, pl, ps, pdl, pds, pdx, 0 if dx is None else _y_type(dx), pdW,
+          0 if dW is None else _y_type(dW), pw, _stream(stream))
 
 
 MOE_ORTHOGONALIZE_MAX_STEPS = 16
 
 
+@functools.lru_cache(maxsize=1024)
+def _ortho_bytes(mats, rows, cols):
+    return int(lib().moe_orthogonalize_workspace_bytes(mats, rows, cols))
+
+
 def moe_orthogonalize_workspace_bytes(mats, rows, cols) -> int:
-    return int(lib().moe_orthogonalize_workspace_bytes(int(mats), int(rows), int(cols)))
+    return _ortho_bytes(int(mats), int(rows), int(cols))
 
 
 def moe_orthogonalize_ws_init(ws, stream=None):
@@ -571,12 +593,12 @@ def moe_orthogonalize(G, O, steps, ws, stream=None):
     itself, in `steps` steps (5 is usual)."""
     if G.dim() not in (2, 3):
         raise ValueError(f"G [mats, rows, cols] or [rows, cols] expected, got {tuple(G.shape)}")
-    _typed("G", G, (_F32, _BF16), G.shape)
-    _typed("O", O, (_BF16,), G.shape)
+    _typed("G", G, _FLOATS, G.shape)
+    _typed("O", O, _BF16_ONLY, G.shape)
     mats, rows, cols = G.shape if G.dim() == 3 else (1, *G.shape)
-    _one_device(G, O, ws)
-    _call("moe_orthogonalize", mats, rows, cols, _ptr(G), _y_type(G), _ptr(O), int(steps),
-          _workspace(ws, moe_orthogonalize_workspace_bytes(mats, rows, cols)), _stream(stream))
+    _workspace(ws, _ortho_bytes(mats, rows, cols))
+    pG, pO, pw = _addresses(G, O, ws)
+    _call("moe_orthogonalize", mats, rows, cols, pG, _y_type(G), pO, int(steps), pw, _stream(stream))
 
 
 def moe_get_device_error(ws, stream=None):
