@@ -5,7 +5,7 @@
 // tile of C for each pair, tcgen05 MMAs of the CTA group of two), CG = 1 on
 // single CTAs (128 x 256), for products whose C has at most 128 rows: half of
 // a pair's tile would be empty there.  384 threads:
-//   warp 0      TMA producer, 64-deep K blocks through a ring of 192 KB;
+//   warp 0      TMA producer, 64-deep K blocks through a ring of 224 KB;
 //   warp 1      issues the MMAs (warps 2 and 3 fill up their warpgroup, whose
 //               registers go to the other two);
 //   warps 4-11  epilogue: two warps for each TMEM lane quadrant, so a thread has
@@ -28,36 +28,31 @@ namespace moe {
 namespace {
 
 constexpr int kDenseThreads = 128 + 32 * 8;
-// Registers a thread: 168 at launch (384 of them fill the SM's 65,536), then 40 for
-// the first warpgroup and 232 for the epilogue's two: 40 + 2 * 232 = 3 * 168.
-constexpr int kDenseRegs = 168, kIssueRegs = 40, kEpiRegs = 232;
+// Registers a thread: 168 at launch (384 of them fill the SM's 65,536), then 56 for
+// the first warpgroup and 224 for the epilogue's two: 56 + 2 * 224 = 3 * 168.
+constexpr int kDenseRegs = 168, kIssueRegs = 56, kEpiRegs = 224;
 static_assert(kIssueRegs + 2 * kEpiRegs == 3 * kDenseRegs && kDenseRegs * kDenseThreads <= 65536, "register shares");
-constexpr int kDenseStg = 2 * kChunkBytes;  // staging of one epilogue warp: two chunks in flight
-template <int CG>
-struct DensePipe {
-  static constexpr int STAGES = CG == 1 ? 4 : 6;
-  static constexpr int B_BYTES = kBBytes / CG;
-  static constexpr int STAGE_BYTES = kABytes + B_BYTES;
-  static constexpr int TILE_M = kBM * CG;
-};
+// The ring takes nearly all shared memory (the epilogue stores from registers):
+// seven stages of 32 KB on pairs, as many as fit of what a K block takes on single
+// CTAs.
+constexpr int kDenseRing = 7 * (kABytes + kBBytes / 2);
+constexpr int kDenseMaxStages = 14;
 struct DenseState {
-  uint64_t full[6], empty[6], tfull[2], tempty[2], drain;
+  uint64_t full[kDenseMaxStages], empty[kDenseMaxStages], tfull[2], tempty[2], drain;
   uint32_t tmem_base;
   int abort;
 };
-constexpr int kDenseSmem = 6 * DensePipe<2>::STAGE_BYTES + 8 * kDenseStg + static_cast<int>(sizeof(DenseState));
-static_assert(DensePipe<1>::STAGES * DensePipe<1>::STAGE_BYTES == DensePipe<2>::STAGES * DensePipe<2>::STAGE_BYTES,
-              "one shared-memory layout for both");
+constexpr int kDenseSmem = kDenseRing + static_cast<int>(sizeof(DenseState));
 static_assert(kDenseSmem <= kSmemBudget, "shared memory budget of one CTA");
 
 // What every operation's launch has.
 struct DenseParams {
   CUtensorMap tmA, tmB;  // operands
-  CUtensorMap tmO;       // what the epilogue stores by TMA
   int M, N;              // rows and columns of C
   int mt, nt;            // tiles of its rows (of TILE_M) and columns (of tn)
   int tn;                // columns of a tile: 256, on single CTAs also fewer (a multiple of 16)
-  int b_bytes;           // of B in one CTA's part of a stage
+  int a_bytes, b_bytes;  // of A and B in one CTA's part of a stage
+  int nst;               // stages of the ring
   int nkb;               // K blocks
   int run_kb;            // K blocks of a run of sums
   int total;             // tiles of the launch
@@ -80,24 +75,81 @@ __device__ __forceinline__ int dense_mma_n(const DenseParams& p, const DenseTile
   return (dense_cols(p, t) + unit - 1) / unit * unit;
 }
 
+// Where an epilogue thread stands: lane of its warp, TMEM lane quadrant, half of
+// the columns.
 struct DenseEpi {
-  uint8_t* stg;
-  uint32_t chunks = 0;  // staged chunks so far
   int lane, q, part;
 };
 
-// Stages the warp's 32 rows x 64 bytes (16 words of each lane's row) and stores
-// them at column x, row y of matrix z; what lies outside is cut off.
-__device__ __forceinline__ void dense_store(DenseEpi& e, const uint32_t* w, const CUtensorMap* map, int x, int y, int z) {
-  uint8_t* buf = e.stg + (e.chunks & 1) * kChunkBytes;
-  staging_reuse_wait<1>(e.chunks);
-  stage_row64(buf, e.lane, w);
-  staging_publish();
-  if (e.lane == 0) {
-    tma_store_3d(map, buf, x, y, z);
-    bulk_commit();
-  }
-  ++e.chunks;
+// 32 bytes from or to a 32-byte boundary: whole sectors, one row a lane.
+__device__ __forceinline__ void st_32(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+__device__ __forceinline__ void ld_32(const void* p, uint32_t* w) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p)
+               : "memory");
+}
+// Two 16-byte halves where a caller's array does not begin on a 32-byte boundary.
+__device__ __forceinline__ void st_2x16(void* p, const uint32_t* w) {
+  reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+// Arrives on `bar` (in both CTAs of a pair) when the MMAs that the lane with
+// `lead` issued before are done.
+template <int CG>
+__device__ __forceinline__ void dense_commit(uint32_t lead, uint32_t bar) {
+  if constexpr (CG == 1)
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+        "r"(lead)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n\t}" ::"r"(
+            bar),
+        "r"(lead), "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+// The four MMAs (16 deep each) of a K block and the release of its stage, from
+// the lane with `lead`.  a and b: shared-memory addresses / 16 of the tiles; the
+// first MMA overwrites C unless `add`.
+template <int CG, bool A_MN, bool B_MN>
+__device__ __forceinline__ void dense_mma(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add,
+                                          uint32_t empty) {
+  // descriptor words as in smem_desc_sw128: leading byte offset above the address,
+  // stride byte offset, version and swizzle in the upper word
+  constexpr uint32_t kHi = (1024u >> 4) | 1u << 14 | 2u << 29;
+  const uint32_t alo = a | (A_MN ? kBoxBytes >> 4 : 1u) << 16, blo = b | (B_MN ? kBoxBytes >> 4 : 1u) << 16;
+  constexpr uint32_t sa = A_MN ? 128 : 2, sb = B_MN ? 128 : 2;  // 16 elements of K further
+#define MOE_DENSE_MMA(GROUP)                                                                                         \
+  asm volatile(                                                                                                      \
+      "{\n\t.reg .pred q, f, t;\n\t.reg .b32 x, y;\n\t.reg .b64 u, v;\n\t"                                             \
+      "setp.ne.b32 q, %0, 0;\n\tsetp.ne.b32 f, %6, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"                                   \
+      "mov.b64 u, {%2, %5};\n\tmov.b64 v, {%3, %5};\n\t"                                                             \
+      "@q tcgen05.mma.cta_group::" GROUP ".kind::f16 [%1], u, v, %4, f;\n\t"                                         \
+      "add.u32 x, %2, %7;\n\tadd.u32 y, %3, %8;\n\tmov.b64 u, {x, %5};\n\tmov.b64 v, {y, %5};\n\t"                   \
+      "@q tcgen05.mma.cta_group::" GROUP ".kind::f16 [%1], u, v, %4, t;\n\t"                                         \
+      "add.u32 x, x, %7;\n\tadd.u32 y, y, %8;\n\tmov.b64 u, {x, %5};\n\tmov.b64 v, {y, %5};\n\t"                     \
+      "@q tcgen05.mma.cta_group::" GROUP ".kind::f16 [%1], u, v, %4, t;\n\t"                                         \
+      "add.u32 x, x, %7;\n\tadd.u32 y, y, %8;\n\tmov.b64 u, {x, %5};\n\tmov.b64 v, {y, %5};\n\t"                     \
+      "@q tcgen05.mma.cta_group::" GROUP ".kind::f16 [%1], u, v, %4, t;\n\t}" ::"r"(lead),                           \
+      "r"(d), "r"(alo), "r"(blo), "r"(idesc), "r"(kHi), "r"(add ? 1u : 0u), "n"(sa), "n"(sb)                         \
+      : "memory")
+  if constexpr (CG == 1)
+    MOE_DENSE_MMA("1");
+  else
+    MOE_DENSE_MMA("2");
+#undef MOE_DENSE_MMA
+  dense_commit<CG>(lead, empty);
 }
 
 // mbar_wait without a call: an epilogue thread holds 128 sums that a call would
@@ -153,16 +205,14 @@ __device__ __forceinline__ void dense_loads(const typename Op::Params& p, const 
 
 template <class Op, int CG>
 __global__ void __launch_bounds__(kDenseThreads, 1) dense_kernel(const __grid_constant__ typename Op::Params p) {
-  using Pipe = DensePipe<CG>;
-  constexpr int NST = Pipe::STAGES, SB = Pipe::STAGE_BYTES;
+  const int NST = p.nst, SB = p.a_bytes + p.b_bytes;  // both multiples of 1024
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   if (smem_u32(smem_raw) & 1023) {  // as in grouped_gemm_kernel: reported, never computed on
     if (threadIdx.x == 0) record_error(p.err, MOE_ERR_CUDA, 0x5A11);
     return;
   }
   uint8_t* smem = smem_raw;
-  uint8_t* stg_base = smem + NST * SB;
-  DenseState& ss = *reinterpret_cast<DenseState*>(stg_base + 8 * kDenseStg);
+  DenseState& ss = *reinterpret_cast<DenseState*>(smem + kDenseRing);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = CG == 2 ? static_cast<int>(cluster_ctarank()) : 0;
 
@@ -215,11 +265,11 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_kernel(const __grid_co
           uint8_t* sA = smem + stage * SB;
           // a pair's loads are all counted on the even CTA's barrier
           if (rank == 0) {
-            mbar_arrive_expect_tx(&ss.full[stage], CG * (kABytes + p.b_bytes));
+            mbar_arrive_expect_tx(&ss.full[stage], CG * SB);
             filled |= 1u << stage;
             fill_par = (fill_par & ~(1u << stage)) | phase << stage;
           }
-          dense_loads<Op, CG>(p, t, kb, b_off, sA, sA + kABytes, &ss.full[stage], rank);
+          dense_loads<Op, CG>(p, t, kb, b_off, sA, sA + p.a_bytes, &ss.full[stage], rank);
           if (++stage == NST) {
             stage = 0;
             phase ^= 1;
@@ -232,61 +282,53 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_kernel(const __grid_co
     }
     __syncwarp();
     if (warp == 1 && rank == 0) {
+      // The warp stays together: one lane issues by predicate, everything it needs
+      // is the same in all lanes, and the next stage's barrier is asked while this
+      // one's MMAs go out.
       constexpr uint32_t idesc0 = Op::F16 ? idesc_f16_f32(kBM * CG, 0, Op::A_MN ? 1 : 0, Op::B_MN ? 1 : 0)
                                           : idesc_bf16_f32(kBM * CG, 0, Op::A_MN ? 1 : 0, Op::B_MN ? 1 : 0);
+      const uint32_t lead = elect_one();
+      const uint32_t ring = smem_u32(smem) >> 4, sb16 = SB >> 4, a16 = p.a_bytes >> 4;
+      const uint32_t full0 = smem_u32(&ss.full[0]), empty0 = smem_u32(&ss.empty[0]), tfull0 = smem_u32(&ss.tfull[0]);
       int stage = 0, it = 0;
       uint32_t phase = 0;
       bool ok = true, issued = false;
+      bool ready = false;  // the stage's data is known to be there
       for (int i = first; ok && i < p.total && !*abort; i += step) {
         const DenseTile t = Op::template tile<CG>(p, i, rank);
         const uint32_t idesc = idesc0 | static_cast<uint32_t>(dense_mma_n<CG, Op::B_MN>(p, t) >> 3) << 17;
         int left = 0;  // K blocks left of the run
         uint32_t dtm = 0;
-        for (int kb = t.kb0; ok && kb < t.kb1; ++kb) {
+        for (int kb = t.kb0; kb < t.kb1; ++kb) {
           const bool fresh = left == 0;
           if (fresh) {
             ok = mbar_wait<CG == 2>(&ss.tempty[it & 1], ((it >> 1) & 1) ^ 1, abort, p.err, where(2, i));
             if (!ok) break;
-            tc_fence_after();
             dtm = tmem + (it & 1) * kBN;
             left = min(p.run_kb, t.kb1 - kb);
           }
-          ok = mbar_wait(&ss.full[stage], phase, abort, p.err, where(3, i));
-          if (!ok) break;
+          if (!ready) {
+            ok = mbar_wait(&ss.full[stage], phase, abort, p.err, where(3, i));
+            if (!ok) break;
+          }
           tc_fence_after();
           --left;
-          if (lane == 0) {
-            const uint32_t a0 = smem_u32(smem + stage * SB), b0 = a0 + kABytes;
-#pragma unroll
-            for (int k4 = 0; k4 < kBK / 16; ++k4) {
-              const uint64_t ad = Op::A_MN ? smem_desc_sw128(a0 + k4 * 2048, kBoxBytes, 1024)
-                                           : smem_desc_sw128(a0 + k4 * 32, 16, 1024);
-              const uint64_t bd = Op::B_MN ? smem_desc_sw128(b0 + k4 * 2048, kBoxBytes, 1024)
-                                           : smem_desc_sw128(b0 + k4 * 32, 16, 1024);
-              umma_bf16<CG>(dtm, ad, bd, idesc, !(fresh && k4 == 0));
-            }
-            if constexpr (CG == 2)
-              umma_commit_pair(&ss.empty[stage]);
-            else
-              umma_commit(&ss.empty[stage]);
-            if (left == 0) {
-              if constexpr (CG == 2)
-                umma_commit_pair(&ss.tfull[it & 1]);
-              else
-                umma_commit(&ss.tfull[it & 1]);
-            }
-            issued = true;
-          }
-          __syncwarp();
-          if (left == 0) ++it;
+          const uint32_t a = ring + stage * sb16, empty = empty0 + 8 * stage;
           if (++stage == NST) {
             stage = 0;
             phase ^= 1;
           }
+          ready = __all_sync(0xffffffffu, mbar_test_wait(full0 + 8 * stage, phase));
+          dense_mma<CG, Op::A_MN, Op::B_MN>(lead, dtm, a, a + a16, idesc, !fresh, empty);
+          issued = true;
+          if (left == 0) {
+            dense_commit<CG>(lead, tfull0 + 8 * (it & 1));
+            ++it;
+          }
         }
       }
-      if (*abort) {
-        if (lane == 0 && issued) {
+      if (*abort && issued) {
+        if (lead) {
           umma_commit<CG>(&ss.drain);
           mbar_wait_drain(&ss.drain, 0);
         }
@@ -296,7 +338,6 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_kernel(const __grid_co
   } else {
     regs_take<kEpiRegs>();
     DenseEpi e;
-    e.stg = stg_base + (warp - 4) * kDenseStg;
     e.lane = lane;
     e.q = warp & 3;  // TMEM lanes [32q, 32q + 32) are reachable from this warp
     e.part = (warp - 4) >> 2;
@@ -350,8 +391,6 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_kernel(const __grid_co
       }
       if (ok && active) Op::epilogue(p, t, e, pre, acc);
     }
-    if (lane == 0) bulk_wait_all();
-    __syncwarp();
   }
 
   tc_fence_before();
@@ -396,7 +435,14 @@ template <class Op, int CG>
 int dense_launch(typename Op::Params& p, int grid_limit, int trace, cudaStream_t s) {
   if (p.tn == 0) {  // whole tiles
     p.tn = kBN;
-    p.b_bytes = DensePipe<CG>::B_BYTES;
+    p.b_bytes = kBBytes / CG;
+  }
+  if (p.a_bytes == 0) p.a_bytes = kABytes;
+  {
+    // The MMAs read 128 rows of A, also where fewer are loaded: what lies behind
+    // them (B, the next stage) then gives rows of C that are not there.
+    const int stage = p.a_bytes + p.b_bytes;
+    p.nst = std::min(kDenseMaxStages, (kDenseRing - (kABytes - p.a_bytes)) / stage);
   }
   const int resident = dense_resident<Op, CG>();
   if (resident <= 0) return MOE_ERR_CUDA;
@@ -448,19 +494,5 @@ bool dense_map_mn(CUtensorMap* m, const void* base, bool f16, uint64_t cols, uin
             strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-// What epilogues store: chunks of 32 rows x 64 bytes.
-bool dense_map_out(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t cols, uint64_t rows, uint64_t mats,
-                   uint64_t pitch) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
-  const uint32_t es = dt == CU_TENSOR_MAP_DATA_TYPE_FLOAT32 ? 4 : 2;
-  const cuuint64_t dims[3] = {cols, rows, mats};
-  const cuuint64_t strides[2] = {pitch * es, rows * pitch * es};
-  const cuuint32_t box[3] = {64 / es, 32, 1};
-  const cuuint32_t one[3] = {1, 1, 1};
-  return fn(m, dt, 3, const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 }  // namespace
 }  // namespace moe

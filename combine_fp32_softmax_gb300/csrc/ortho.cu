@@ -62,8 +62,10 @@ struct OrthoOp {
     int first;           // the first step
     const __half* old;   // square: A; update: X, laid out as the result
     int pitch;           // of old
-    uint16_t* O;         // last update where its rows are not whole 16-byte pieces (else null)
+    void* out;           // [mats][M] rows
+    int out_pitch;       // of out, a multiple of 16
     int bf16;            // last update: bf16 results
+    int apart;           // 1: out is not on a 32-byte boundary
   };
   template <int CG>
   static __device__ __forceinline__ DenseTile tile(const Params& p, int i, int rank) {
@@ -83,7 +85,7 @@ struct OrthoOp {
       nb = j - mb * p.nt;
     }
     const bool skip = p.scal[mat] == 0.f;
-    return {mat, mb * DensePipe<CG>::TILE_M + rank * kBM, nb * kBN, 0, skip ? 0 : p.nkb};
+    return {mat, mb * kBM * CG + rank * kBM, nb * kBN, 0, skip ? 0 : p.nkb};
   }
   static __device__ __forceinline__ void coords(const Params&, const DenseTile& t, int kb, int& ak, int& am, int& bk,
                                                 int& bn) {
@@ -95,18 +97,23 @@ struct OrthoOp {
   // square and update, this thread's 128 values of the old matrix.
   struct Pre {
     float r;
-    uint4 old[SYM && KIND != kSquare ? 1 : 16];
+    uint32_t old[SYM && KIND != kSquare ? 1 : 64];
   };
   static __device__ __forceinline__ Pre pre(const Params& p, const DenseTile& t, const DenseEpi& e) {
     Pre o;
     o.r = p.first ? p.scal[t.mat] : 1.f / kSX;
     if constexpr (KIND == kSquare || !SYM) {
       const int x = t.n0 + 128 * e.part, row = t.m0 + 32 * e.q + e.lane;
-      const uint4* from =
-          reinterpret_cast<const uint4*>(p.old + (static_cast<size_t>(t.mat) * p.M + row) * p.pitch + x);
+      const __half* from = p.old + (static_cast<size_t>(t.mat) * p.M + row) * p.pitch + x;
 #pragma unroll
-      for (int u = 0; u < 16; ++u)  // the pitch is a multiple of 64
-        o.old[u] = row < p.M && x + 8 * u < p.pitch && t.kb1 > t.kb0 ? from[u] : make_uint4(0, 0, 0, 0);
+      for (int u = 0; u < 8; ++u) {  // the pitch is a multiple of 64
+        if (row < p.M && x + 16 * u < p.pitch && t.kb1 > t.kb0) {
+          ld_32(from + 16 * u, &o.old[8 * u]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) o.old[8 * u + k] = 0u;
+        }
+      }
     }
     return o;
   }
@@ -129,52 +136,41 @@ struct OrthoOp {
       for (int j = 0; j < 32; ++j) v[j] = fs * __uint_as_float(acc[c][j]);
       if constexpr (KIND == kSquare || !SYM) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const uint4 w = pre.old[4 * c + u];
-          const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 o = unpack_f16(ws[k]);
-            v[8 * u + 2 * k] = fmaf(fo, o.x, v[8 * u + 2 * k]);
-            v[8 * u + 2 * k + 1] = fmaf(fo, o.y, v[8 * u + 2 * k + 1]);
-          }
+        for (int u = 0; u < 16; ++u) {
+          const float2 o = unpack_f16(pre.old[16 * c + u]);
+          v[2 * u] = fmaf(fo, o.x, v[2 * u]);
+          v[2 * u + 1] = fmaf(fo, o.y, v[2 * u + 1]);
         }
       }
       uint32_t w[16];
-      if (!SYM && p.bf16) {
 #pragma unroll
-        for (int u = 0; u < 16; ++u) w[u] = pack_bf16(v[2 * u], v[2 * u + 1]);
-        if (p.O) {  // no TMA store: the warp writes its 32 x 32 values row by row
-          __syncwarp();
-          stage_row64(e.stg, e.lane, w);
-          __syncwarp();
-          uint16_t* out = p.O + (static_cast<size_t>(t.mat) * p.M + y) * p.N + x;
-          if (x + e.lane < p.N)
-            for (int i = 0; i < 32 && y + i < p.M; ++i)
-              out[static_cast<size_t>(i) * p.N + e.lane] = *reinterpret_cast<const uint16_t*>(
-                  e.stg + i * 64 + (((e.lane >> 3) ^ ((i >> 1) & 3)) << 4) + (e.lane & 7) * 2);
-          continue;
-        }
-      } else {
+      for (int u = 0; u < 16; ++u)
+        w[u] = !SYM && p.bf16 ? pack_bf16(v[2 * u], v[2 * u + 1]) : pack_f16(v[2 * u], v[2 * u + 1]);
+      uint16_t* mat = static_cast<uint16_t*>(p.out) + static_cast<size_t>(t.mat) * p.M * p.out_pitch;
+      if (y + e.lane < p.M) {
+        uint16_t* to = mat + static_cast<size_t>(y + e.lane) * p.out_pitch + x;
 #pragma unroll
-        for (int u = 0; u < 16; ++u) w[u] = pack_f16(v[2 * u], v[2 * u + 1]);
+        for (int h = 0; h < 2; ++h)  // columns between the last and the pitch may hold anything
+          if (x + 16 * h < p.out_pitch) {
+            if (!SYM && p.apart)
+              st_2x16(to + 16 * h, w + 8 * h);
+            else
+              st_32(to + 16 * h, w + 8 * h);
+          }
       }
-      dense_store(e, w, &p.tmO, x, y, t.mat);
       if constexpr (SYM) {
         if (t.n0 >= (t.m0 / kBN + 1) * kBN) {  // a tile off the diagonal: also to the other side
-          uint8_t* buf = e.stg + (e.chunks & 1) * kChunkBytes;
-          staging_reuse_wait<1>(e.chunks);
+          // neighbouring lanes' rows side by side: even lanes take the even columns,
+          // odd ones the odd, and a store covers 32 rows of two columns
+          const bool odd = e.lane & 1;
+          uint16_t* to = mat + static_cast<size_t>(x + odd) * p.out_pitch + y + (e.lane & ~1);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {  // row j of the transposed chunk: this lane's column is its row
-            const uint16_t h = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
-            *reinterpret_cast<uint16_t*>(buf + j * 64 + (((e.lane >> 3) ^ ((j >> 1) & 3)) << 4) + (e.lane & 7) * 2) = h;
+          for (int u = 0; u < 16; ++u) {
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, w[u], 1);
+            const uint32_t both = odd ? __byte_perm(other, w[u], 0x7632) : __byte_perm(w[u], other, 0x5410);
+            if (x + 2 * u + odd < p.N)  // rows past the last one end before the pitch
+              *reinterpret_cast<uint32_t*>(to + static_cast<size_t>(2 * u) * p.out_pitch) = both;
           }
-          staging_publish();
-          if (e.lane == 0) {
-            tma_store_3d(&p.tmO, buf, y, x, t.mat);
-            bulk_commit();
-          }
-          ++e.chunks;
         }
       }
     }
@@ -296,6 +292,20 @@ __global__ void __launch_bounds__(256)
   }
 }
 
+// Padded rows of bf16 to the caller's, a warp a row; matrices that the cast
+// finished are left alone.
+__global__ void __launch_bounds__(256) ortho_rows_kernel(const uint16_t* __restrict__ X, const float* __restrict__ scal,
+                                                         long long n, int rows, int cols, int pitch,
+                                                         uint16_t* __restrict__ O) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  for (long long r = blockIdx.x * 8ll + (threadIdx.x >> 5); r < n; r += gridDim.x * 8ll) {
+    if (scal[r / rows] == 0.f) continue;
+    for (int c = lane; c < cols; c += 32) O[r * cols + c] = X[r * pitch + c];
+  }
+}
+
 // ------------------------------------------------------------------ host
 struct Plan {
   int small, pitch, spitch, parts;
@@ -362,7 +372,8 @@ int launch_ortho(const OrthoArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return MOE_ERR_CUDA;
   }
   const int m = L.small;
-  constexpr auto kF16 = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  // rows that are not whole 32-byte pieces come out padded and are then brought together
+  const bool copy = a.cols % 16 != 0;
   auto base = [&](DenseParams& p, int code, int M, int N, int K) {
     p.M = M;
     p.N = N;
@@ -382,12 +393,14 @@ int launch_ortho(const OrthoArgs& a, cudaStream_t s) {
       base(p, 0, m, m, wide ? a.cols : a.rows);
       p.scal = scal;
       p.first = it == 0;
-      bool ok = dense_map_out(&p.tmO, A, kF16, m, m, a.mats, L.spitch);
+      p.out = A;
+      p.out_pitch = L.spitch;
+      bool ok;
       if (wide)
-        ok = ok && dense_map_k(&p.tmA, Xi, true, a.cols, a.rows, a.mats, L.pitch, 128) &&
+        ok = dense_map_k(&p.tmA, Xi, true, a.cols, a.rows, a.mats, L.pitch, 128) &&
              dense_map_k(&p.tmB, Xi, true, a.cols, a.rows, a.mats, L.pitch, bn);
       else
-        ok = ok && dense_map_mn(&p.tmA, Xi, true, L.pitch, a.rows, a.mats, 2) &&
+        ok = dense_map_mn(&p.tmA, Xi, true, L.pitch, a.rows, a.mats, 2) &&
              dense_map_mn(&p.tmB, Xi, true, L.pitch, a.rows, a.mats, bn / 64);
       return ok;
     };
@@ -407,8 +420,10 @@ int launch_ortho(const OrthoArgs& a, cudaStream_t s) {
       p.old = A;
       p.pitch = L.spitch;
       if (!dense_map_k(&p.tmA, A, true, m, m, a.mats, L.spitch, 128) ||
-          !dense_map_k(&p.tmB, A, true, m, m, a.mats, L.spitch, bn) || !dense_map_out(&p.tmO, B, kF16, m, m, a.mats, L.spitch))
+          !dense_map_k(&p.tmB, A, true, m, m, a.mats, L.spitch, bn))
         return MOE_ERR_CUDA;
+      p.out = B;
+      p.out_pitch = L.spitch;
       if ((rc = launch_kind<kSquare>(p, a.mats, a, MOE_K_ORTHO_SQUARE, s)) != MOE_OK) break;
     }
     auto update = [&](auto& p) {
@@ -419,16 +434,16 @@ int launch_ortho(const OrthoArgs& a, cudaStream_t s) {
       p.old = Xi;
       p.pitch = L.pitch;
       p.bf16 = last;
-      const bool tma = !last || a.cols % 8 == 0;
-      if (!tma) p.O = a.O;
-      bool ok = !tma || (last ? dense_map_out(&p.tmO, a.O, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.cols, a.rows, a.mats, a.cols)
-                              : dense_map_out(&p.tmO, Xo, kF16, a.cols, a.rows, a.mats, L.pitch));
+      p.out = last && !copy ? a.O : reinterpret_cast<uint16_t*>(Xo);
+      p.out_pitch = last && !copy ? a.cols : L.pitch;
+      p.apart = (reinterpret_cast<uintptr_t>(p.out) & 31) != 0;
+      bool ok;
       const uint32_t ubn = a.rows <= kBM ? 256 : 128;
       if (wide)
-        ok = ok && dense_map_k(&p.tmA, B, true, m, m, a.mats, L.spitch, 128) &&
+        ok = dense_map_k(&p.tmA, B, true, m, m, a.mats, L.spitch, 128) &&
              dense_map_mn(&p.tmB, Xi, true, L.pitch, a.rows, a.mats, ubn / 64);
       else
-        ok = ok && dense_map_k(&p.tmA, Xi, true, a.cols, a.rows, a.mats, L.pitch, 128) &&
+        ok = dense_map_k(&p.tmA, Xi, true, a.cols, a.rows, a.mats, L.pitch, 128) &&
              dense_map_k(&p.tmB, B, true, m, m, a.mats, L.spitch, ubn);
       return ok;
     };
@@ -439,6 +454,14 @@ int launch_ortho(const OrthoArgs& a, cudaStream_t s) {
       OrthoOp<kUpdateTall>::Params p;
       rc = update(p) ? launch_kind<kUpdateTall>(p, a.mats, a, MOE_K_ORTHO_UPDATE, s) : MOE_ERR_CUDA;
     }
+  }
+  if (rc == MOE_OK && copy) {
+    TraceScope trace_scope(MOE_K_ORTHO_NORM, s);
+    const long long n = static_cast<long long>(a.mats) * a.rows;
+    if (launch_pdl(ortho_rows_kernel, dim3(static_cast<int>(std::min<long long>((n + 7) / 8, num_sms() * 8))), dim3(256), 0, s,
+                   reinterpret_cast<const uint16_t*>(X[a.steps & 1]), scal, n, a.rows, a.cols, L.pitch,
+                   a.O) != cudaSuccess)
+      return MOE_ERR_CUDA;
   }
   return rc;
 }

@@ -50,7 +50,7 @@ __device__ __forceinline__ int load_target(const Target& g, int t, int V) {
 template <int CG>
 __device__ __forceinline__ DenseTile rows_first(const DenseParams& p, int i, int rank) {
   const int nb = i / p.mt, mb = i - nb * p.mt;
-  return {0, mb * DensePipe<CG>::TILE_M + rank * kBM, nb * p.tn, 0, p.nkb};
+  return {0, mb * kBM * CG + rank * kBM, nb * p.tn, 0, p.nkb};
 }
 
 // ------------------------------------------------------------- forward
@@ -166,6 +166,7 @@ struct GradOp {
     const float* dlse;  // or null
     int V, v0;          // the piece is columns [v0, v0 + N) of V; columns from V on are zeros
     int terms;          // D is the sum of so many bf16 values, each N columns further
+    uint16_t* D;        // [T, terms N]
   };
   struct Pre {
     float w, lse, at;  // of exp(z - lse); log of the sum; D at the target
@@ -220,7 +221,11 @@ struct GradOp {
         uint32_t w[16];
 #pragma unroll
         for (int u = 0; u < 16; ++u) w[u] = pack_bf16(f[2 * u], f[2 * u + 1]);
-        dense_store(e, w, &p.tmO, k * p.N + col + 32 * c, y, 0);
+        if (y + e.lane < p.M) {
+          uint16_t* to = p.D + static_cast<size_t>(y + e.lane) * (p.terms * p.N) + k * p.N + col + 32 * c;
+          st_32(to, w);
+          st_32(to + 16, w + 8);
+        }
         if (k + 1 == p.terms) break;
 #pragma unroll
         for (int u = 0; u < 16; ++u) {  // what the value so far leaves, exactly
@@ -245,7 +250,9 @@ struct ProdOp {
     int cols;         // columns of the piece: from one term of D to the next
     int per_split;    // DX: K blocks of a split; each has a matrix of its own in out
     const float* prev;  // added to the products, laid out as out is in fp32
+    void* out;        // [splits][M][N]
     int bf16;         // type of out
+    int apart, prev_apart;  // 1: not on a 32-byte boundary
   };
   template <int CG>
   static __device__ __forceinline__ DenseTile tile(const Params& p, int i, int rank) {
@@ -254,7 +261,7 @@ struct ProdOp {
     const int per = p.mt * p.nt, split = i / per, j = i - split * per;
     const int mb = j / p.nt, nb = j - mb * p.nt;
     const int kb0 = min(p.nkb, split * p.per_split);
-    return {split, mb * DensePipe<CG>::TILE_M + rank * kBM, nb * kBN, kb0, min(p.nkb, kb0 + p.per_split)};
+    return {split, mb * kBM * CG + rank * kBM, nb * kBN, kb0, min(p.nkb, kb0 + p.per_split)};
   }
   static __device__ __forceinline__ void coords(const Params& p, const DenseTile& t, int kb, int& ak, int& am, int& bk,
                                                 int& bn) {
@@ -272,23 +279,34 @@ struct ProdOp {
   static __device__ __forceinline__ int pre(const Params&, const DenseTile&, const DenseEpi&) { return 0; }
   static __device__ __forceinline__ void epilogue(const Params& p, const DenseTile& t, DenseEpi& e, int,
                                                   uint32_t (&acc)[4][32]) {
-    const int x = t.n0 + 128 * e.part, y = t.m0 + 32 * e.q;
-    if (p.prev && y + e.lane < p.M) {
-      const float4* from =
-          reinterpret_cast<const float4*>(p.prev + (static_cast<size_t>(t.mat) * p.M + y + e.lane) * p.N + x);
+    const int x = t.n0 + 128 * e.part, row = t.m0 + 32 * e.q + e.lane;
+    if (row >= p.M) return;
+    const size_t at = (static_cast<size_t>(t.mat) * p.M + row) * p.N + x;
+    if (p.prev) {
 #pragma unroll
       for (int c = 0; c < 4; ++c)
         if (x + 32 * c < p.N)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float4 v = from[8 * c + j];
-            uint32_t* a = &acc[c][4 * j];
-            a[0] = __float_as_uint(__uint_as_float(a[0]) + v.x);
-            a[1] = __float_as_uint(__uint_as_float(a[1]) + v.y);
-            a[2] = __float_as_uint(__uint_as_float(a[2]) + v.z);
-            a[3] = __float_as_uint(__uint_as_float(a[3]) + v.w);
+          for (int j = 0; j < 4; ++j) {
+            uint32_t v[8];
+            const float* from = p.prev + at + 32 * c + 8 * j;
+            if (p.prev_apart) {
+              *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(from);
+              *reinterpret_cast<uint4*>(v + 4) = *reinterpret_cast<const uint4*>(from + 4);
+            } else {
+              ld_32(from, v);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              acc[c][8 * j + i] = __float_as_uint(__uint_as_float(acc[c][8 * j + i]) + __uint_as_float(v[i]));
           }
     }
+    auto store = [&](void* to, const uint32_t* w) {
+      if (p.apart)
+        st_2x16(to, w);
+      else
+        st_32(to, w);
+    };
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       if (x + 32 * c >= p.N) break;  // N is a multiple of 64
@@ -297,10 +315,13 @@ struct ProdOp {
 #pragma unroll
         for (int u = 0; u < 16; ++u)
           w[u] = pack_bf16(__uint_as_float(acc[c][2 * u]), __uint_as_float(acc[c][2 * u + 1]));
-        dense_store(e, w, &p.tmO, x + 32 * c, y, t.mat);
+        uint16_t* to = static_cast<uint16_t*>(p.out) + at + 32 * c;
+        store(to, w);
+        store(to + 16, w + 8);
       } else {
-        dense_store(e, &acc[c][0], &p.tmO, x + 32 * c, y, t.mat);
-        dense_store(e, &acc[c][16], &p.tmO, x + 32 * c + 16, y, t.mat);
+        float* to = static_cast<float*>(p.out) + at + 32 * c;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) store(to + 8 * j, &acc[c][8 * j]);
       }
     }
   }
@@ -381,7 +402,9 @@ int few_rows_tile(int cols, int unit) {
 void logit_tiles(DenseParams& p, int T, int cols, int unit) {
   const bool single = T <= kBM;
   p.tn = single ? few_rows_tile(cols, unit) : kBN;
-  p.b_bytes = single ? p.tn * 128 : DensePipe<2>::B_BYTES;
+  // a few rows of x: no more than they are
+  p.a_bytes = single ? ceil_div(T, 8) * 8 * 128 : kABytes;
+  p.b_bytes = single ? p.tn * 128 : kBBytes / 2;
   p.mt = single ? 1 : ceil_div(T, 2 * kBM);
   p.nt = ceil_div(cols, p.tn);
   p.total = p.mt * p.nt;
@@ -433,7 +456,7 @@ int launch_xent_fwd(const XentArgs& a, cudaStream_t s) {
   StatsOp::Params p;
   std::memset(&p, 0, sizeof(p));
   logit_tiles(p, a.T, a.V, 16);
-  if (!dense_map_k(&p.tmA, a.x, false, a.d, a.T, 1, a.d, 128) ||
+  if (!dense_map_k(&p.tmA, a.x, false, a.d, a.T, 1, a.d, p.a_bytes / 128) ||
       !dense_map_k(&p.tmB, a.W, false, a.d, a.V, 1, a.d, p.b_bytes / 128))
     return MOE_ERR_CUDA;
   p.M = a.T;
@@ -485,10 +508,10 @@ int launch_xent_bwd(const XentArgs& a, cudaStream_t s) {
       GradOp::Params p;
       std::memset(&p, 0, sizeof(p));
       logit_tiles(p, a.T, cols, 32);
-      if (!dense_map_k(&p.tmA, a.x, false, a.d, a.T, 1, a.d, 128) ||
-          !dense_map_k(&p.tmB, a.W, false, a.d, a.V, 1, a.d, p.b_bytes / 128) ||
-          !dense_map_out(&p.tmO, D, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, size_t(cols) * h, a.T, 1, size_t(cols) * h))
+      if (!dense_map_k(&p.tmA, a.x, false, a.d, a.T, 1, a.d, p.a_bytes / 128) ||
+          !dense_map_k(&p.tmB, a.W, false, a.d, a.V, 1, a.d, p.b_bytes / 128))
         return MOE_ERR_CUDA;
+      p.D = static_cast<uint16_t*>(D);
       p.M = a.T;
       p.N = cols;
       p.nkb = a.d / kBK;
@@ -526,13 +549,14 @@ int launch_xent_bwd(const XentArgs& a, cudaStream_t s) {
       // fp32 sums of the pieces so far: in dx itself where it has that type
       float* sums = L.splits == 1 && f32 ? static_cast<float*>(a.dx) : accbuf;
       p.prev = v0 > 0 ? sums : nullptr;
+      p.prev_apart = (reinterpret_cast<uintptr_t>(sums) & 31) != 0;
       void* out = L.splits == 1 && last ? a.dx : sums;
       p.bf16 = L.splits == 1 && last && !f32;
       if (!dense_map_k(&p.tmA, D, false, size_t(cols) * h, a.T, 1, size_t(cols) * h, 128) ||
-          !dense_map_mn(&p.tmB, a.W, false, a.d, a.V, 1, single ? 4 : 2) ||
-          !dense_map_out(&p.tmO, out, p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.d, a.T,
-                         L.splits, a.d))
+          !dense_map_mn(&p.tmB, a.W, false, a.d, a.V, 1, single ? 4 : 2))
         return MOE_ERR_CUDA;
+      p.out = out;
+      p.apart = (reinterpret_cast<uintptr_t>(out) & 31) != 0;
       rc = single ? dense_launch<ProdOp<true>, 1>(p, a.grid_limit, MOE_K_XENT_DX, s)
                   : dense_launch<ProdOp<true>, 2>(p, a.grid_limit, MOE_K_XENT_DX, s);
       if (rc != MOE_OK) return rc;
@@ -556,10 +580,10 @@ int launch_xent_bwd(const XentArgs& a, cudaStream_t s) {
       p.bf16 = !f32;
       uint8_t* out = static_cast<uint8_t*>(a.dW) + size_t(v0) * a.d * (f32 ? 4 : 2);
       if (!dense_map_mn(&p.tmA, D, false, size_t(cols) * h, a.T, 1, 2) ||
-          !dense_map_mn(&p.tmB, xz, false, a.d, a.T, 1, one ? 4 : 2) ||
-          !dense_map_out(&p.tmO, out, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.d, real, 1,
-                         a.d))
+          !dense_map_mn(&p.tmB, xz, false, a.d, a.T, 1, one ? 4 : 2))
         return MOE_ERR_CUDA;
+      p.out = out;
+      p.apart = (reinterpret_cast<uintptr_t>(out) & 31) != 0;
       rc = one ? dense_launch<ProdOp<false>, 1>(p, a.grid_limit, MOE_K_XENT_DW, s)
                : dense_launch<ProdOp<false>, 2>(p, a.grid_limit, MOE_K_XENT_DW, s);
       if (rc != MOE_OK) return rc;
