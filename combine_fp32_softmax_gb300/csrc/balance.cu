@@ -27,8 +27,8 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kUnits = 152 * 6;  // blocks to spread the tokens over; fixed, so the sums' order is
+constexpr int kThreads = 512;
+constexpr int kUnits = 152 * 3;  // blocks to spread the tokens over; fixed, so the sums' order is
 
 // Blocks of a sequence: at least 32 tokens each, so that all blocks' sums fit in
 // the E ceil(T / 32) words of the histogram regions of the workspace.
@@ -136,7 +136,7 @@ __device__ __forceinline__ void finish_sequence(const BalanceOut& o, int b, int 
 }
 
 template <class Y>
-__global__ void __launch_bounds__(kThreads, 6)
+__global__ void __launch_bounds__(kThreads, 3)
     balance_sums_kernel(const float* __restrict__ logits, const int32_t* __restrict__ topk_idx,
                         const uint8_t* __restrict__ mask, int L, int B, int parts, int E, int k, int32_t* __restrict__ counts,
                         float* __restrict__ psums, float2* __restrict__ zn, BalanceOut out, int* err) {
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, 6)
   const int per = (L + parts - 1) / parts;
   for (int u = blockIdx.x; u < B * parts; u += gridDim.x) {
     const int b = u / parts, c = u - b * parts;
-    hist[threadIdx.x] = 0;
+    if (threadIdx.x < 256) hist[threadIdx.x] = 0;
     __syncthreads();
     const int t0 = b * L + min(L, c * per), t1 = b * L + min(L, (c + 1) * per);
     auto live = [&](int t) { return t < t1 && (!mask || mask[t]); };
@@ -215,13 +215,14 @@ __global__ void __launch_bounds__(kThreads, 6)
     const int e = threadIdx.x;
     float psum = 0.f, zsum = 0.f;
     int total = 0;
+#pragma unroll
     for (int w = 0; w < WARPS; ++w) {
       if (e < E) psum += ps[w][e];
       zsum += zw[w];
       total += nw[w];
     }
     if (parts == 1) {
-      finish_sequence(out, b, E, k, hist[e], psum, zsum, total, red);
+      finish_sequence(out, b, E, k, e < E ? hist[e] : 0, psum, zsum, total, red);
     } else {
       if (e < E) {
         counts[static_cast<size_t>(u) * E + e] = hist[e];
@@ -234,22 +235,24 @@ __global__ void __launch_bounds__(kThreads, 6)
 }
 
 // One block a sequence: a thread takes V experts (a 16-byte piece where rows are
-// whole ones) of every (1024 / width)-th part, then the groups of threads are
+// whole ones) of every group-th part; then the groups of a warp, and the warps, are
 // added in a fixed order.
+constexpr int kJoin = 512;
 template <int V>
-__global__ void __launch_bounds__(1024)
+__global__ void __launch_bounds__(kJoin)
     balance_join_kernel(const int32_t* __restrict__ counts, const float* __restrict__ psums, const float2* __restrict__ zn,
                         int B, int parts, int E, int k, BalanceOut out) {
   griddep_wait();
   griddep_launch_dependents();
-  __shared__ float sp[1024 * V];
-  __shared__ int sc[1024 * V];
-  __shared__ float red[8], zred[32];
-  __shared__ int nred[32];
-  const int tid = threadIdx.x;
+  constexpr int WARPS = kJoin / 32;
+  __shared__ float sp[WARPS][256];
+  __shared__ int sc[WARPS][256];
+  __shared__ float red[8], zred[WARPS];
+  __shared__ int nred[WARPS];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int shift = 0;  // of the groups' width, a power of two of at least E / V
   while ((V << shift) < E) ++shift;
-  const int groups = 1024 >> shift, g = tid >> shift, e = V * (tid & ((1 << shift) - 1));
+  const int groups = kJoin >> shift, g = tid >> shift, e = V * (tid & ((1 << shift) - 1));
   for (int b = blockIdx.x; b < B; b += gridDim.x) {
     Sum2 s[V], z;
     int c[V] = {}, n = 0;
@@ -275,15 +278,10 @@ __global__ void __launch_bounds__(1024)
         }
       }
     }
-    for (int i = tid; i < parts; i += 1024) {
+    for (int i = tid; i < parts; i += kJoin) {
       const float2 v = zn[at + i];
       z.add(v.x);
       n += static_cast<int>(v.y);  // tokens of a part: far below 2^24
-    }
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      sp[V * tid + j] = s[j].value();
-      sc[V * tid + j] = c[j];
     }
     float zs = z.value();
 #pragma unroll
@@ -291,34 +289,49 @@ __global__ void __launch_bounds__(1024)
       zs += __shfl_xor_sync(kFull, zs, off);
       n += __shfl_xor_sync(kFull, n, off);
     }
-    if ((tid & 31) == 0) {
-      zred[tid >> 5] = zs;
-      nred[tid >> 5] = n;
+    if (lane == 0) {
+      zred[warp] = zs;
+      nred[warp] = n;
     }
-    for (int h = groups >> 1; h; h >>= 1) {
-      __syncthreads();
-      if (g < h)
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          sp[V * tid + j] += sp[V * (tid + (h << shift)) + j];
-          sc[V * tid + j] += sc[V * (tid + (h << shift)) + j];
-        }
+    for (int j = 0; j < V; ++j) {
+      float v = s[j].value();
+      int q = c[j];
+      for (int off = 1 << shift; off < 32; off <<= 1) {
+        v += __shfl_xor_sync(kFull, v, off);
+        q += __shfl_xor_sync(kFull, q, off);
+      }
+      // groups wider than a warp: the warps of one group hold different experts
+      if (e < E && (shift >= 5 || (lane >> shift) == 0)) {
+        sp[shift > 5 ? g : warp][e + j] = v;
+        sc[shift > 5 ? g : warp][e + j] = q;
+      }
     }
     __syncthreads();
+    float ps = 0.f;
+    int count = 0;
     zs = 0.f;
     n = 0;
-    for (int i = 0; i < 32; ++i) {
+    const int rows = shift > 5 ? groups : WARPS;
+    for (int i = 0; i < rows; ++i) {
+      if (tid < E) {
+        ps += sp[i][tid];
+        count += sc[i][tid];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < WARPS; ++i) {
       zs += zred[i];
       n += nred[i];
     }
-    finish_sequence(out, b, E, k, sc[tid], sp[tid], zs, n, red);  // expert e's sums are at e
+    finish_sequence(out, b, E, k, count, ps, zs, n, red);
     __syncthreads();
   }
 }
 
 // dlogits = add + gradient; add may be dlogits itself or null.
 template <class Y>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, 2)
     balance_bwd_kernel(const float* __restrict__ logits, const int32_t* __restrict__ counts, const uint8_t* __restrict__ mask,
                        const float* __restrict__ dloss, const float* __restrict__ dz, int T, int L, int E, int k,
                        const float* add, float* dlogits) {
@@ -423,14 +436,14 @@ cudaError_t launch_balance(const float* logits, const int32_t* topk_idx, const u
   TraceScope trace_scope(MOE_K_BALANCE, s);
   const int parts = seq_parts(T, B);
   const BalanceOut out{counts, mean_p, loss, zloss};
-  const int units = static_cast<int>(std::min<long long>(static_cast<long long>(B) * parts, num_sms() * 6));
+  const int units = static_cast<int>(std::min<long long>(static_cast<long long>(B) * parts, num_sms() * 3));
   float2* zn = reinterpret_cast<float2*>(part_zn);
   cudaError_t e = with_layout(E, [&](auto y) {
     return launch_pdl(balance_sums_kernel<decltype(y)>, dim3(units), dim3(kThreads), 0, s, logits, topk_idx, mask, T / B, B,
                       parts, E, k, part_counts, part_p, zn, out, err);
   });
   if (e == cudaSuccess && parts > 1)
-    e = launch_pdl(E % 4 ? balance_join_kernel<1> : balance_join_kernel<4>, dim3(std::min(B, 65535)), dim3(1024), 0, s,
+    e = launch_pdl(E % 4 ? balance_join_kernel<1> : balance_join_kernel<4>, dim3(std::min(B, 65535)), dim3(kJoin), 0, s,
                    part_counts, part_p, zn, B, parts, E, k, out);
   return e;
 }
@@ -441,7 +454,7 @@ cudaError_t launch_balance_bwd(const float* logits, const int32_t* counts, const
   TraceScope trace_scope(MOE_K_BALANCE_BWD, s);
   return with_layout(E, [&](auto y) {
     const long long warps = ceil_div(T, 32 / decltype(y)::LANES);
-    const int blocks = static_cast<int>(std::min<long long>(ceil_div(warps, kThreads / 32), num_sms() * 4));
+    const int blocks = static_cast<int>(std::min<long long>(ceil_div(warps, kThreads / 32), num_sms() * 2));
     return launch_pdl(balance_bwd_kernel<decltype(y)>, dim3(blocks), dim3(kThreads), 0, s, logits, counts, mask, dloss, dz, T,
                       T / B, E, k, add, dlogits);
   });

@@ -3,8 +3,8 @@
 //
 // One persistent kernel per operation; CG = 2 runs it on CTA pairs (a 256 x 256
 // tile of C for each pair, tcgen05 MMAs of the CTA group of two), CG = 1 on
-// single CTAs (128 x 256), for products whose C has at most 128 rows: half of
-// a pair's tile would be empty there.  384 threads:
+// single CTAs (128 rows x up to 256 columns), for products that would leave
+// pairs without work (dense_pick).  384 threads:
 //   warp 0      TMA producer, 64-deep K blocks through a ring of 224 KB;
 //   warp 1      issues the MMAs (warps 2 and 3 fill up their warpgroup, whose
 //               registers go to the other two);
@@ -51,6 +51,7 @@ struct DenseParams {
   int M, N;              // rows and columns of C
   int mt, nt;            // tiles of its rows (of TILE_M) and columns (of tn)
   int tn;                // columns of a tile: 256, on single CTAs also fewer (a multiple of 16)
+  int half;              // columns of a tile that the first half of the epilogue's warps takes, a multiple of 32
   int a_bytes, b_bytes;  // of A and B in one CTA's part of a stage
   int nst;               // stages of the ring
   int nkb;               // K blocks
@@ -80,6 +81,14 @@ __device__ __forceinline__ int dense_mma_n(const DenseParams& p, const DenseTile
 struct DenseEpi {
   int lane, q, part;
 };
+
+// First column of C of an epilogue thread, and how many it has (0 or less: none).
+__device__ __forceinline__ int dense_col(const DenseParams& p, const DenseTile& t, const DenseEpi& e) {
+  return t.n0 + p.half * e.part;
+}
+__device__ __forceinline__ int dense_width(const DenseParams& p, const DenseTile& t, const DenseEpi& e) {
+  return min(p.half, dense_cols(p, t) - p.half * e.part);
+}
 
 // 32 bytes from or to a 32-byte boundary: whole sectors, one row a lane.
 __device__ __forceinline__ void st_32(void* p, const uint32_t* w) {
@@ -364,7 +373,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_kernel(const __grid_co
         }
         ++it;
         tc_fence_after();
-        const uint32_t ta = tmem + (static_cast<uint32_t>(e.q * 32) << 16) + buf * kBN + e.part * 128;
+        const uint32_t ta = tmem + (static_cast<uint32_t>(e.q * 32) << 16) + buf * kBN + e.part * p.half;
         if (r == 0) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_ld_32x32(ta + 32 * c, acc[c]);
@@ -431,19 +440,59 @@ int dense_resident() {
   return cached[dev] = n;
 }
 
+// Tile shape and splits of K of a product of an M x N C.
+struct DenseShape {
+  int cg, tn, splits;
+};
+
+// The shape with the shortest estimated time: rounds of tiles over the SMs, each
+// its K blocks (us each: a CTA takes in about 100 GB/s, a pair's MMAs 0.3) and an
+// epilogue; splits of K (a matrix of fp32 sums each, added up by another launch)
+// cost their bytes twice at 5 TB/s.  sym: C is symmetric, its tiles square and only
+// those from the diagonal on computed.  152: the SMs of the GB300; fixed, so that
+// results and workspaces do not depend on the device asked.
+DenseShape dense_pick(long long M, long long N, int mats, int nkb, bool sym, int max_splits) {
+  struct Option {
+    int cg, tn;
+    double kb, epi;
+  };
+  constexpr Option kOptions[] = {{2, 256, 0.30, 3.0}, {1, 256, 0.40, 3.0}, {1, 128, 0.28, 2.0}, {1, 64, 0.22, 1.5}};
+  DenseShape best{2, 256, 1};
+  double least = 1e30;
+  for (const Option& o : kOptions) {
+    const int tm = kBM * o.cg;
+    if (sym && o.tn != tm) continue;
+    const long long nt = (N + o.tn - 1) / o.tn, mt = (M + tm - 1) / tm;
+    const long long tiles = mats * (sym ? nt * (nt + 1) / 2 : nt * mt);
+    for (int sp = 1; sp <= max_splits && sp <= nkb; sp += (sp + 3) / 4) {  // 1 to 5, 7, 9, 12, 15, 19, ...
+      const long long units = 152 / o.cg, rounds = (tiles * sp + units - 1) / units;
+      const double us = rounds * (o.kb * ((nkb + sp - 1) / sp) + o.epi) + (sp > 1 ? 3.0 + sp * 8.0 * M * N / 5e6 : 0.0);
+      if (us < 0.97 * least) {
+        least = us;
+        best = {o.cg, o.tn, sp};
+      }
+    }
+  }
+  return best;
+}
+
+// Rows and columns of tiles, what a K block brings, and the tiles of `mats`
+// matrices (or splits).
+void dense_shape(DenseParams& p, int cg, int tn, int mats, bool sym) {
+  p.tn = tn;
+  p.half = ceil_div(tn, 64) * 32;
+  p.a_bytes = kABytes;
+  p.b_bytes = tn * 128 / cg;
+  p.mt = ceil_div(p.M, kBM * cg);
+  p.nt = ceil_div(p.N, tn);
+  p.total = mats * (sym ? p.nt * (p.nt + 1) / 2 : p.mt * p.nt);
+}
+
 template <class Op, int CG>
 int dense_launch(typename Op::Params& p, int grid_limit, int trace, cudaStream_t s) {
-  if (p.tn == 0) {  // whole tiles
-    p.tn = kBN;
-    p.b_bytes = kBBytes / CG;
-  }
-  if (p.a_bytes == 0) p.a_bytes = kABytes;
-  {
-    // The MMAs read 128 rows of A, also where fewer are loaded: what lies behind
-    // them (B, the next stage) then gives rows of C that are not there.
-    const int stage = p.a_bytes + p.b_bytes;
-    p.nst = std::min(kDenseMaxStages, (kDenseRing - (kABytes - p.a_bytes)) / stage);
-  }
+  // The MMAs read 128 rows of A, also where fewer are loaded: what lies behind
+  // them (B, the next stage) then gives rows of C that are not there.
+  p.nst = std::min(kDenseMaxStages, (kDenseRing - (kABytes - p.a_bytes)) / (p.a_bytes + p.b_bytes));
   const int resident = dense_resident<Op, CG>();
   if (resident <= 0) return MOE_ERR_CUDA;
   int units = resident;
@@ -465,6 +514,10 @@ int dense_launch(typename Op::Params& p, int grid_limit, int trace, cudaStream_t
   cfg.attrs = attr;
   TraceScope trace_scope(trace, s);
   return cudaLaunchKernelEx(&cfg, dense_kernel<Op, CG>, p) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+template <class Op>
+int dense_launch(int cg, typename Op::Params& p, int grid_limit, int trace, cudaStream_t s) {
+  return cg == 1 ? dense_launch<Op, 1>(p, grid_limit, trace, s) : dense_launch<Op, 2>(p, grid_limit, trace, s);
 }
 
 // Matrices [mats][rows][cols] of 16-bit elements, rows `pitch` elements apart, as

@@ -85,7 +85,7 @@ struct OrthoOp {
       nb = j - mb * p.nt;
     }
     const bool skip = p.scal[mat] == 0.f;
-    return {mat, mb * kBM * CG + rank * kBM, nb * kBN, 0, skip ? 0 : p.nkb};
+    return {mat, mb * kBM * CG + rank * kBM, nb * p.tn, 0, skip ? 0 : p.nkb};
   }
   static __device__ __forceinline__ void coords(const Params&, const DenseTile& t, int kb, int& ak, int& am, int& bk,
                                                 int& bn) {
@@ -103,11 +103,12 @@ struct OrthoOp {
     Pre o;
     o.r = p.first ? p.scal[t.mat] : 1.f / kSX;
     if constexpr (KIND == kSquare || !SYM) {
-      const int x = t.n0 + 128 * e.part, row = t.m0 + 32 * e.q + e.lane;
+      const int x = dense_col(p, t, e), row = t.m0 + 32 * e.q + e.lane;
+      const int w = dense_width(p, t, e);  // what it reads past the last column lies before the pitch
       const __half* from = p.old + (static_cast<size_t>(t.mat) * p.M + row) * p.pitch + x;
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {  // the pitch is a multiple of 64
-        if (row < p.M && x + 16 * u < p.pitch && t.kb1 > t.kb0) {
+      for (int u = 0; u < 8; ++u) {
+        if (row < p.M && 16 * u < w && t.kb1 > t.kb0) {
           ld_32(from + 16 * u, &o.old[8 * u]);
         } else {
 #pragma unroll
@@ -121,7 +122,7 @@ struct OrthoOp {
                                                   uint32_t (&acc)[4][32]) {
     if (t.kb1 == t.kb0) return;
     const float r = pre.r;
-    const int x0 = t.n0 + 128 * e.part, y = t.m0 + 32 * e.q;
+    const int x0 = dense_col(p, t, e), x1 = x0 + dense_width(p, t, e), y = t.m0 + 32 * e.q;
     // gram: A = r^2 sums; square: B = b A + c sums; update: X' = a r X + r sums
     const float fs = KIND == kSquare                         ? kNsC * (kSB / (kSA * kSA))
                      : (KIND == kGramWide || KIND == kGramTall) ? r * r * kSA
@@ -130,7 +131,7 @@ struct OrthoOp {
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const int x = x0 + 32 * c;
-      if (x >= p.N) break;
+      if (x >= x1) break;
       float v[32];
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] = fs * __uint_as_float(acc[c][j]);
@@ -159,7 +160,7 @@ struct OrthoOp {
           }
       }
       if constexpr (SYM) {
-        if (t.n0 >= (t.m0 / kBN + 1) * kBN) {  // a tile off the diagonal: also to the other side
+        if (t.n0 / p.tn > t.m0 / p.tn) {  // a tile off the diagonal: also to the other side
           // neighbouring lanes' rows side by side: even lanes take the even columns,
           // odd ones the odd, and a store covers 32 rows of two columns
           const bool odd = e.lane & 1;
@@ -284,11 +285,31 @@ __global__ void __launch_bounds__(256)
     if (blockIdx.x == 0 && threadIdx.x == 0) scal[mat] = ldexpf(inv, -k);
     const float up = ldexpf(1.f, k);  // the norm is between 2^-41 and 2^64 here: 2^k is a normal number
     __half* Xm = X + static_cast<size_t>(mat) * rows * pitch;
-    auto put = [&](size_t i, float v) {
-      const uint32_t j = static_cast<uint32_t>(i - at), row = j / cols;
-      Xm[static_cast<size_t>(row) * pitch + (j - row * cols)] = __float2half_rn(up * v);
-    };
-    for_elements<decltype(put), BF16>(G, lo, hi, threadIdx.x, 256, put);
+    constexpr int VE = BF16 ? 8 : 4;
+    if (cols % VE == 0) {  // whole 16-byte pieces of G in a row: one place for each
+      const uint32_t v0 = static_cast<uint32_t>((lo - at + VE - 1) / VE), v1 = static_cast<uint32_t>((hi - at + VE - 1) / VE);
+      const uint32_t vc = cols / VE;
+      const uint4* from = reinterpret_cast<const uint4*>(G) + at / VE;
+      for (uint32_t i = v0 + threadIdx.x; i < v1; i += 256) {
+        const uint4 w = from[i];
+        const uint32_t row = i / vc;
+        __half* to = Xm + static_cast<size_t>(row) * pitch + (i - row * vc) * VE;
+        if constexpr (BF16) {
+          *reinterpret_cast<uint4*>(to) =
+              make_uint4(pack_f16(up * bf16_lo(w.x), up * bf16_hi(w.x)), pack_f16(up * bf16_lo(w.y), up * bf16_hi(w.y)),
+                         pack_f16(up * bf16_lo(w.z), up * bf16_hi(w.z)), pack_f16(up * bf16_lo(w.w), up * bf16_hi(w.w)));
+        } else {
+          *reinterpret_cast<uint2*>(to) = make_uint2(pack_f16(up * __uint_as_float(w.x), up * __uint_as_float(w.y)),
+                                                     pack_f16(up * __uint_as_float(w.z), up * __uint_as_float(w.w)));
+        }
+      }
+    } else {
+      auto put = [&](size_t i, float v) {
+        const uint32_t j = static_cast<uint32_t>(i - at), row = j / cols;
+        Xm[static_cast<size_t>(row) * pitch + (j - row * cols)] = __float2half_rn(up * v);
+      };
+      for_elements<decltype(put), BF16>(G, lo, hi, threadIdx.x, 256, put);
+    }
   }
 }
 
@@ -317,7 +338,9 @@ Plan plan(int mats, int rows, int cols) {
   p.pitch = ceil_div(cols, 64) * 64;
   p.spitch = ceil_div(p.small, 64) * 64;
   const long long n = static_cast<long long>(rows) * cols;
-  p.parts = static_cast<int>(std::max(1ll, std::min<long long>(kNormParts, n / 32768)));
+  // enough for every SM where there are few matrices, 32,768 elements each else
+  const long long few = std::min<long long>(n / 1024, 1216 / mats);
+  p.parts = static_cast<int>(std::max(1ll, std::min<long long>(kNormParts, std::max(n / 32768, few))));
   size_t o = 0;
   auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -332,16 +355,6 @@ Plan plan(int mats, int rows, int cols) {
   p.B = take(size_t(2) * mats * p.small * p.spitch);
   p.total = o;
   return p;
-}
-
-template <int KIND>
-int launch_kind(typename OrthoOp<KIND>::Params& p, int mats, const OrthoArgs& a, int trace, cudaStream_t s) {
-  const bool single = p.M <= kBM;
-  p.nt = ceil_div(p.N, kBN);
-  p.mt = single ? 1 : ceil_div(p.M, 2 * kBM);
-  p.total = mats * (OrthoOp<KIND>::SYM ? p.nt * (p.nt + 1) / 2 : p.mt * p.nt);
-  return single ? dense_launch<OrthoOp<KIND>, 1>(p, a.grid_limit, trace, s)
-                : dense_launch<OrthoOp<KIND>, 2>(p, a.grid_limit, trace, s);
 }
 
 }  // namespace
@@ -382,7 +395,9 @@ int launch_ortho(const OrthoArgs& a, cudaStream_t s) {
     p.code = kCodeOrtho + code;
     p.err = err;
   };
-  const uint32_t bn = m <= kBM ? 256 : 128;  // columns of B that a CTA loads where C has m rows
+  const DenseShape gram_shape = dense_pick(m, m, a.mats, ceil_div(wide ? a.cols : a.rows, kBK), true, 1);
+  const DenseShape square_shape = dense_pick(m, m, a.mats, ceil_div(m, kBK), true, 1);
+  const DenseShape update_shape = dense_pick(a.rows, a.cols, a.mats, ceil_div(m, kBK), false, 1);
   int rc = MOE_OK;
   for (int it = 0; it < a.steps && rc == MOE_OK; ++it) {
     const __half* Xi = X[it & 1];
@@ -391,6 +406,7 @@ int launch_ortho(const OrthoArgs& a, cudaStream_t s) {
     auto gram = [&](auto& p) {
       std::memset(&p, 0, sizeof(p));
       base(p, 0, m, m, wide ? a.cols : a.rows);
+      dense_shape(p, gram_shape.cg, gram_shape.tn, a.mats, true);
       p.scal = scal;
       p.first = it == 0;
       p.out = A;
@@ -398,37 +414,39 @@ int launch_ortho(const OrthoArgs& a, cudaStream_t s) {
       bool ok;
       if (wide)
         ok = dense_map_k(&p.tmA, Xi, true, a.cols, a.rows, a.mats, L.pitch, 128) &&
-             dense_map_k(&p.tmB, Xi, true, a.cols, a.rows, a.mats, L.pitch, bn);
+             dense_map_k(&p.tmB, Xi, true, a.cols, a.rows, a.mats, L.pitch, p.b_bytes / 128);
       else
         ok = dense_map_mn(&p.tmA, Xi, true, L.pitch, a.rows, a.mats, 2) &&
-             dense_map_mn(&p.tmB, Xi, true, L.pitch, a.rows, a.mats, bn / 64);
+             dense_map_mn(&p.tmB, Xi, true, L.pitch, a.rows, a.mats, p.b_bytes / kBoxBytes);
       return ok;
     };
     if (wide) {
       OrthoOp<kGramWide>::Params p;
-      rc = gram(p) ? launch_kind<kGramWide>(p, a.mats, a, MOE_K_ORTHO_GRAM, s) : MOE_ERR_CUDA;
+      rc = gram(p) ? dense_launch<OrthoOp<kGramWide>>(gram_shape.cg, p, a.grid_limit, MOE_K_ORTHO_GRAM, s) : MOE_ERR_CUDA;
     } else {
       OrthoOp<kGramTall>::Params p;
-      rc = gram(p) ? launch_kind<kGramTall>(p, a.mats, a, MOE_K_ORTHO_GRAM, s) : MOE_ERR_CUDA;
+      rc = gram(p) ? dense_launch<OrthoOp<kGramTall>>(gram_shape.cg, p, a.grid_limit, MOE_K_ORTHO_GRAM, s) : MOE_ERR_CUDA;
     }
     if (rc != MOE_OK) break;
     {
       OrthoOp<kSquare>::Params p;
       std::memset(&p, 0, sizeof(p));
       base(p, 1, m, m, m);
+      dense_shape(p, square_shape.cg, square_shape.tn, a.mats, true);
       p.scal = scal;
       p.old = A;
       p.pitch = L.spitch;
       if (!dense_map_k(&p.tmA, A, true, m, m, a.mats, L.spitch, 128) ||
-          !dense_map_k(&p.tmB, A, true, m, m, a.mats, L.spitch, bn))
+          !dense_map_k(&p.tmB, A, true, m, m, a.mats, L.spitch, p.b_bytes / 128))
         return MOE_ERR_CUDA;
       p.out = B;
       p.out_pitch = L.spitch;
-      if ((rc = launch_kind<kSquare>(p, a.mats, a, MOE_K_ORTHO_SQUARE, s)) != MOE_OK) break;
+      if ((rc = dense_launch<OrthoOp<kSquare>>(square_shape.cg, p, a.grid_limit, MOE_K_ORTHO_SQUARE, s)) != MOE_OK) break;
     }
     auto update = [&](auto& p) {
       std::memset(&p, 0, sizeof(p));
       base(p, 2, a.rows, a.cols, m);
+      dense_shape(p, update_shape.cg, update_shape.tn, a.mats, false);
       p.scal = scal;
       p.first = it == 0;
       p.old = Xi;
@@ -438,21 +456,20 @@ int launch_ortho(const OrthoArgs& a, cudaStream_t s) {
       p.out_pitch = last && !copy ? a.cols : L.pitch;
       p.apart = (reinterpret_cast<uintptr_t>(p.out) & 31) != 0;
       bool ok;
-      const uint32_t ubn = a.rows <= kBM ? 256 : 128;
       if (wide)
         ok = dense_map_k(&p.tmA, B, true, m, m, a.mats, L.spitch, 128) &&
-             dense_map_mn(&p.tmB, Xi, true, L.pitch, a.rows, a.mats, ubn / 64);
+             dense_map_mn(&p.tmB, Xi, true, L.pitch, a.rows, a.mats, p.b_bytes / kBoxBytes);
       else
         ok = dense_map_k(&p.tmA, Xi, true, a.cols, a.rows, a.mats, L.pitch, 128) &&
-             dense_map_k(&p.tmB, B, true, m, m, a.mats, L.spitch, ubn);
+             dense_map_k(&p.tmB, B, true, m, m, a.mats, L.spitch, p.b_bytes / 128);
       return ok;
     };
     if (wide) {
       OrthoOp<kUpdateWide>::Params p;
-      rc = update(p) ? launch_kind<kUpdateWide>(p, a.mats, a, MOE_K_ORTHO_UPDATE, s) : MOE_ERR_CUDA;
+      rc = update(p) ? dense_launch<OrthoOp<kUpdateWide>>(update_shape.cg, p, a.grid_limit, MOE_K_ORTHO_UPDATE, s) : MOE_ERR_CUDA;
     } else {
       OrthoOp<kUpdateTall>::Params p;
-      rc = update(p) ? launch_kind<kUpdateTall>(p, a.mats, a, MOE_K_ORTHO_UPDATE, s) : MOE_ERR_CUDA;
+      rc = update(p) ? dense_launch<OrthoOp<kUpdateTall>>(update_shape.cg, p, a.grid_limit, MOE_K_ORTHO_UPDATE, s) : MOE_ERR_CUDA;
     }
   }
   if (rc == MOE_OK && copy) {

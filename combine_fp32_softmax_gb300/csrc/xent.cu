@@ -78,8 +78,7 @@ struct StatsOp {
   static __device__ __forceinline__ void epilogue(const Params& p, const DenseTile& t, DenseEpi& e, int target,
                                                   uint32_t (&acc)[4][32]) {
     const int row = t.m0 + 32 * e.q + e.lane;
-    const int col = t.n0 + 128 * e.part;
-    const int n = dense_cols(p, t) - 128 * e.part;  // columns that the tile has
+    const int col = dense_col(p, t, e), n = dense_width(p, t, e);
     if (n < 128) {
 #pragma unroll
       for (int c = 0; c < 4; ++c)
@@ -118,40 +117,46 @@ struct StatsOp {
   }
 };
 
-// Joins the pairs of a row: one warp a row, the pairs in a fixed order.
+// Joins the pairs of a row, WARPS warps a row (eight where there are few rows), the
+// pairs in a fixed order.
+__device__ __forceinline__ float2 join_pairs(float2 a, float2 b) {
+  const float m = fmaxf(a.x, b.x);
+  // a pair without a finite logit has sum 0 and adds nothing
+  const float x = a.y == 0.f ? 0.f : a.y * (a.x == m ? 1.f : expf(a.x - m));
+  const float y = b.y == 0.f ? 0.f : b.y * (b.x == m ? 1.f : expf(b.x - m));
+  return make_float2(m, x + y);
+}
+template <int WARPS>
 __global__ void __launch_bounds__(256) xent_join_kernel(const float2* __restrict__ part, const float* __restrict__ zt,
                                                         Target target, int T, int V, int np, float* __restrict__ loss,
                                                         float* __restrict__ lse, int* err) {
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int t = blockIdx.x * 8 + (threadIdx.x >> 5);
+  __shared__ float2 sw[8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int t = WARPS == 1 ? blockIdx.x * 8 + warp : blockIdx.x;
   if (t >= T) return;
   const float2* row = part + static_cast<size_t>(t) * np;
-  float m = -INFINITY, s = 0.f;
-  for (int i = lane; i < np; i += 32) {
-    const float2 v = row[i];
-    const float nm = fmaxf(m, v.x);
-    // a pair without a finite logit has sum 0 and leaves s as it is
-    const float keep = m == nm ? 1.f : expf(m - nm), add = v.x == nm ? 1.f : expf(v.x - nm);
-    s = (s == 0.f ? 0.f : s * keep) + (v.y == 0.f ? 0.f : v.y * add);
-    m = nm;
-  }
+  float2 v = make_float2(-INFINITY, 0.f);
+  for (int i = WARPS == 1 ? lane : static_cast<int>(threadIdx.x); i < np; i += 32 * WARPS) v = join_pairs(v, row[i]);
 #pragma unroll
-  for (int off = 16; off; off >>= 1) {
-    const float om = __shfl_xor_sync(0xffffffffu, m, off), os = __shfl_xor_sync(0xffffffffu, s, off);
-    const float nm = fmaxf(m, om);
-    const float a = s == 0.f ? 0.f : s * (m == nm ? 1.f : expf(m - nm));
-    const float b = os == 0.f ? 0.f : os * (om == nm ? 1.f : expf(om - nm));
-    s = a + b;
-    m = nm;
+  for (int off = 16; off; off >>= 1)
+    v = join_pairs(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, off), __shfl_xor_sync(0xffffffffu, v.y, off)));
+  if constexpr (WARPS > 1) {
+    if (lane == 0) sw[warp] = v;
+    __syncthreads();
+    if (warp) return;
+    v = sw[lane & 7];
+#pragma unroll
+    for (int off = 4; off; off >>= 1)
+      v = join_pairs(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, off), __shfl_xor_sync(0xffffffffu, v.y, off)));
   }
   if (lane == 0) {
-    const float ls = logf(s);
-    lse[t] = m + ls;
-    const long long v = target.wide ? static_cast<const long long*>(target.p)[t] : static_cast<const int*>(target.p)[t];
-    if (v >= V) record_error(err, MOE_ERR_ARG, t);
-    loss[t] = v >= 0 && v < V ? (m - zt[t]) + ls : 0.f;
+    const float ls = logf(v.y);
+    lse[t] = v.x + ls;
+    const long long g = target.wide ? static_cast<const long long*>(target.p)[t] : static_cast<const int*>(target.p)[t];
+    if (g >= V) record_error(err, MOE_ERR_ARG, t);
+    loss[t] = g >= 0 && g < V ? (v.x - zt[t]) + ls : 0.f;
   }
 }
 
@@ -170,7 +175,7 @@ struct GradOp {
   };
   struct Pre {
     float w, lse, at;  // of exp(z - lse); log of the sum; D at the target
-    int rel;           // the target's column in this thread's 128, or another number
+    int rel;           // the target's column among this thread's, or another number
   };
   template <int CG>
   static __device__ __forceinline__ DenseTile tile(const Params& p, int i, int rank) {
@@ -195,16 +200,16 @@ struct GradOp {
       if (g != 0.f) {
         const float l = -p.loss[row];
         r.at = h * expf(l) + g * expm1f(l);
-        r.rel = target - (p.v0 + t.n0 + 128 * e.part);
+        r.rel = target - (p.v0 + dense_col(p, t, e));
       }
     }
     return r;
   }
   static __device__ __forceinline__ void epilogue(const Params& p, const DenseTile& t, DenseEpi& e, const Pre& r,
                                                   uint32_t (&acc)[4][32]) {
-    const int col = t.n0 + 128 * e.part;   // of the piece
-    const int n = p.V - (p.v0 + col);      // columns that exist
-    const int w = dense_cols(p, t) - 128 * e.part;  // columns that the tile has, a multiple of 32
+    const int col = dense_col(p, t, e);  // of the piece
+    const int n = p.V - (p.v0 + col);    // columns that exist
+    const int w = dense_width(p, t, e);  // a multiple of 32
     const int y = t.m0 + 32 * e.q;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
@@ -248,7 +253,7 @@ struct ProdOp {
     int v0;           // DX: the piece's first column of the vocabulary
     int once;         // K blocks of one of D's bf16 terms
     int cols;         // columns of the piece: from one term of D to the next
-    int per_split;    // DX: K blocks of a split; each has a matrix of its own in out
+    int per_split;    // K blocks of a split; each has a matrix of its own in out
     const float* prev;  // added to the products, laid out as out is in fp32
     void* out;        // [splits][M][N]
     int bf16;         // type of out
@@ -261,7 +266,7 @@ struct ProdOp {
     const int per = p.mt * p.nt, split = i / per, j = i - split * per;
     const int mb = j / p.nt, nb = j - mb * p.nt;
     const int kb0 = min(p.nkb, split * p.per_split);
-    return {split, mb * kBM * CG + rank * kBM, nb * kBN, kb0, min(p.nkb, kb0 + p.per_split)};
+    return {split, mb * kBM * CG + rank * kBM, nb * p.tn, kb0, min(p.nkb, kb0 + p.per_split)};
   }
   static __device__ __forceinline__ void coords(const Params& p, const DenseTile& t, int kb, int& ak, int& am, int& bk,
                                                 int& bn) {
@@ -279,13 +284,14 @@ struct ProdOp {
   static __device__ __forceinline__ int pre(const Params&, const DenseTile&, const DenseEpi&) { return 0; }
   static __device__ __forceinline__ void epilogue(const Params& p, const DenseTile& t, DenseEpi& e, int,
                                                   uint32_t (&acc)[4][32]) {
-    const int x = t.n0 + 128 * e.part, row = t.m0 + 32 * e.q + e.lane;
+    const int x = dense_col(p, t, e), row = t.m0 + 32 * e.q + e.lane;
+    const int w = dense_width(p, t, e);  // a multiple of 32
     if (row >= p.M) return;
     const size_t at = (static_cast<size_t>(t.mat) * p.M + row) * p.N + x;
     if (p.prev) {
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        if (x + 32 * c < p.N)
+        if (32 * c < w)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             uint32_t v[8];
@@ -309,15 +315,15 @@ struct ProdOp {
     };
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      if (x + 32 * c >= p.N) break;  // N is a multiple of 64
+      if (32 * c >= w) break;
       if (p.bf16) {
-        uint32_t w[16];
+        uint32_t b[16];
 #pragma unroll
         for (int u = 0; u < 16; ++u)
-          w[u] = pack_bf16(__uint_as_float(acc[c][2 * u]), __uint_as_float(acc[c][2 * u + 1]));
+          b[u] = pack_bf16(__uint_as_float(acc[c][2 * u]), __uint_as_float(acc[c][2 * u + 1]));
         uint16_t* to = static_cast<uint16_t*>(p.out) + at + 32 * c;
-        store(to, w);
-        store(to + 16, w + 8);
+        store(to, b);
+        store(to + 16, b + 8);
       } else {
         float* to = static_cast<float*>(p.out) + at + 32 * c;
 #pragma unroll
@@ -342,7 +348,7 @@ __global__ void __launch_bounds__(256) xent_rows_kernel(const uint4* __restrict_
   }
 }
 
-// Sum of the splits' dx in their order.
+// Sum of the splits in their order.
 __global__ void __launch_bounds__(256) xent_sum_kernel(const float4* __restrict__ part, int splits, size_t n4, int bf16,
                                                        void* __restrict__ out) {
   griddep_wait();
@@ -368,56 +374,41 @@ constexpr int kMaxSplits = 64;
 
 struct Plan {
   int cols;    // most columns of a piece, a multiple of 256, counted in bf16 values of a row of D
-  int splits;  // most of dx's sums
+  DenseShape dx, dW;
   size_t err, part, zt, D, acc, xz, total;
 };
 
-// Splits of dx's sums over a piece of the vocabulary: several CTAs share a tile's
-// K where the tiles do not fill the GPU's rounds.  Estimated: 0.28 us a K block and
-// round, 8 bytes of fp32 sums a split and element at 5 TB/s.
-int dx_splits(int T, int d, int cols) {
-  const int cg = T <= kBM ? 1 : 2, units = 152 / cg, nkb = cols / kBK;
-  const int tiles = ceil_div(T, kBM * cg) * ceil_div(d, kBN);
-  int best = 1;
-  double least = 1e30;
-  for (int s = 1; s <= kMaxSplits && (s == 1 || nkb / s >= 8); ++s) {
-    const double us = ceil_div(static_cast<long long>(tiles) * s, units) * (0.28 * ceil_div(nkb, s)) +
-                      (s > 1 ? s * 8.0 * T * d / 5e6 : 0.0);
-    if (us < 0.97 * least) {
-      least = us;
-      best = s;
-    }
-  }
-  return best;
-}
-
-// Columns of a tile of the logits where one row block has all tokens: the CTAs
-// get equal shares of the vocabulary's rows, which are all that counts then.
-int few_rows_tile(int cols, int unit) {
-  const int rounds = ceil_div(cols, 152 * kBN);
-  return std::min(kBN, ceil_div(ceil_div(cols, 152 * rounds), unit) * unit);
-}
-
-// Tiles of the logits [T, cols], tn a multiple of `unit`.
+// Tiles of the logits [T, cols], tn a multiple of `unit`.  Where a row block or a few
+// have all tokens, or all tiles run at one time, single CTAs take equal shares of
+// the vocabulary: its rows' bytes, or latency, are what counts then.
 void logit_tiles(DenseParams& p, int T, int cols, int unit) {
-  const bool single = T <= kBM;
-  p.tn = single ? few_rows_tile(cols, unit) : kBN;
-  // a few rows of x: no more than they are
-  p.a_bytes = single ? ceil_div(T, 8) * 8 * 128 : kABytes;
-  p.b_bytes = single ? p.tn * 128 : kBBytes / 2;
-  p.mt = single ? 1 : ceil_div(T, 2 * kBM);
-  p.nt = ceil_div(cols, p.tn);
-  p.total = p.mt * p.nt;
+  const int mt = ceil_div(T, kBM);
+  if (mt > 1 && static_cast<long long>(mt) * ceil_div(cols, kBN) > 152) {
+    dense_shape(p, 2, kBN, 1, false);
+    return;
+  }
+  const int each = std::max(1, 152 / mt), rounds = ceil_div(cols, static_cast<long long>(each) * kBN);
+  const int tn = std::max(64, ceil_div(ceil_div(cols, static_cast<long long>(each) * rounds), unit) * unit);
+  dense_shape(p, 1, std::min(kBN, tn), 1, false);
+  p.a_bytes = std::min(kBM, ceil_div(T, 8) * 8) * 128;  // no more rows than there are
 }
+int logit_cg(const DenseParams& p, int T) { return p.mt == ceil_div(T, kBM) ? 1 : 2; }
 
 Plan plan(int T, int V, int d, int backward) {
   Plan p{};
-  const int nt = ceil_div(V, T <= kBM ? few_rows_tile(V, 16) : kBN);
+  DenseParams tiles{};
+  tiles.M = T;
+  tiles.N = V;
+  logit_tiles(tiles, T, V, 16);
   const int all = ceil_div(V, kBN) * kBN;
   const long long want = std::max<long long>(kPieceBytes / 2 / T / kBN * kBN, kPieceCols);
   // every term of D for the whole vocabulary at most
   p.cols = static_cast<int>(std::min<long long>(want, 1ll * kTerms * all));
-  p.splits = dx_splits(T, d, std::min(p.cols, all));
+  if (backward) {  // one bf16 term's K
+    const int width = std::min(V, p.cols);
+    p.dx = dense_pick(T, d, 1, ceil_div(width, kBK), false, kMaxSplits);
+    p.dW = dense_pick(width, d, 1, ceil_div(T, kBK), false, width == V ? kMaxSplits : 1);
+  }
   size_t o = 0;
   auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -426,13 +417,13 @@ Plan plan(int T, int V, int d, int backward) {
   };
   p.err = take(kErrRegionBytes);
   const size_t begin = o;
-  p.part = take(sizeof(float2) * 2 * nt * T);
+  p.part = take(sizeof(float2) * 2 * tiles.nt * T);
   p.zt = take(sizeof(float) * T);
   size_t end = o;
   if (backward) {
     o = begin;  // the forward's scratch is free by then
     p.D = take(size_t(2) * T * p.cols);
-    p.acc = take(sizeof(float) * p.splits * T * d);
+    p.acc = take(sizeof(float) * std::max(size_t(p.dx.splits) * T, p.dW.splits > 1 ? size_t(p.dW.splits) * V : 0) * d);
     p.xz = take(size_t(2) * T * d);
     end = std::max(end, o);
   }
@@ -442,7 +433,18 @@ Plan plan(int T, int V, int d, int backward) {
 
 template <class Op>
 int launch_logits(typename Op::Params& p, const XentArgs& a, int trace, cudaStream_t s) {
-  return a.T <= kBM ? dense_launch<Op, 1>(p, a.grid_limit, trace, s) : dense_launch<Op, 2>(p, a.grid_limit, trace, s);
+  return dense_launch<Op>(logit_cg(p, a.T), p, a.grid_limit, trace, s);
+}
+
+// out [n] = sum of `splits` fp32 arrays.
+int launch_sum(const float* part, int splits, size_t n, bool bf16, void* out, cudaStream_t s) {
+  TraceScope trace_scope(MOE_K_XENT_ROWS, s);
+  const size_t n4 = n / 4;
+  const int blocks = static_cast<int>(std::min<size_t>((n4 + 255) / 256, num_sms() * 8));
+  return launch_pdl(xent_sum_kernel, dim3(blocks), dim3(256), 0, s, reinterpret_cast<const float4*>(part), splits, n4, bf16,
+                    out) == cudaSuccess
+             ? MOE_OK
+             : MOE_ERR_CUDA;
 }
 
 }  // namespace
@@ -455,12 +457,12 @@ int launch_xent_fwd(const XentArgs& a, cudaStream_t s) {
   int* err = reinterpret_cast<int*>(ws + L.err);
   StatsOp::Params p;
   std::memset(&p, 0, sizeof(p));
+  p.M = a.T;
+  p.N = a.V;
   logit_tiles(p, a.T, a.V, 16);
   if (!dense_map_k(&p.tmA, a.x, false, a.d, a.T, 1, a.d, p.a_bytes / 128) ||
       !dense_map_k(&p.tmB, a.W, false, a.d, a.V, 1, a.d, p.b_bytes / 128))
     return MOE_ERR_CUDA;
-  p.M = a.T;
-  p.N = a.V;
   p.nkb = a.d / kBK;
   p.run_kb = kExactRun;
   p.code = kCodeXent;
@@ -471,8 +473,9 @@ int launch_xent_fwd(const XentArgs& a, cudaStream_t s) {
   const int rc = launch_logits<StatsOp>(p, a, MOE_K_XENT, s);
   if (rc != MOE_OK) return rc;
   TraceScope trace_scope(MOE_K_XENT_JOIN, s);
-  return launch_pdl(xent_join_kernel, dim3(ceil_div(a.T, 8)), dim3(256), 0, s, p.part, p.zt, p.target, a.T, a.V, 2 * p.nt,
-                    a.loss, a.lse, err) == cudaSuccess
+  const bool few = a.T <= 4 * 152;  // a block a row as long as all rows run at one time
+  return launch_pdl(few ? xent_join_kernel<8> : xent_join_kernel<1>, dim3(few ? a.T : ceil_div(a.T, 8)), dim3(256), 0, s,
+                    p.part, p.zt, p.target, a.T, a.V, 2 * p.nt, a.loss, a.lse, err) == cudaSuccess
              ? MOE_OK
              : MOE_ERR_CUDA;
 }
@@ -490,7 +493,6 @@ int launch_xent_bwd(const XentArgs& a, cudaStream_t s) {
   const int most = L.cols / h / kBN * kBN;
   const int pieces = ceil_div(a.V, most);
   const int width = ceil_div(ceil_div(a.V, pieces), kBN) * kBN;
-  const bool single = a.T <= kBM;
   int rc;
 
   if (a.dW) {
@@ -507,13 +509,13 @@ int launch_xent_bwd(const XentArgs& a, cudaStream_t s) {
     {
       GradOp::Params p;
       std::memset(&p, 0, sizeof(p));
+      p.M = a.T;
+      p.N = cols;
       logit_tiles(p, a.T, cols, 32);
       if (!dense_map_k(&p.tmA, a.x, false, a.d, a.T, 1, a.d, p.a_bytes / 128) ||
           !dense_map_k(&p.tmB, a.W, false, a.d, a.V, 1, a.d, p.b_bytes / 128))
         return MOE_ERR_CUDA;
       p.D = static_cast<uint16_t*>(D);
-      p.M = a.T;
-      p.N = cols;
       p.nkb = a.d / kBK;
       p.run_kb = kExactRun;  // the forward's logits, bit for bit
       p.code = kCodeXent + 1;
@@ -532,9 +534,9 @@ int launch_xent_bwd(const XentArgs& a, cudaStream_t s) {
       ProdOp<true>::Params p;
       std::memset(&p, 0, sizeof(p));
       const bool f32 = a.dx_type == MOE_Y_F32;
+      const int splits = L.dx.splits;
       p.M = a.T;
       p.N = a.d;
-      p.nt = ceil_div(a.d, kBN);
       p.once = cols / kBK;
       p.nkb = f32 ? kTerms * p.once : p.once;
       p.run_kb = f32 ? kExactRun : p.nkb;
@@ -542,59 +544,46 @@ int launch_xent_bwd(const XentArgs& a, cudaStream_t s) {
       p.err = err;
       p.v0 = v0;
       p.cols = cols;
-      p.per_split = ceil_div(p.nkb, L.splits);  // a split without K blocks keeps the sums so far
-      p.mt = single ? 1 : ceil_div(a.T, 2 * kBM);
-      p.total = p.mt * p.nt * L.splits;
+      p.per_split = ceil_div(p.nkb, splits);  // a split without K blocks keeps the sums so far
+      dense_shape(p, L.dx.cg, L.dx.tn, splits, false);
       const bool last = v0 + width >= a.V;
       // fp32 sums of the pieces so far: in dx itself where it has that type
-      float* sums = L.splits == 1 && f32 ? static_cast<float*>(a.dx) : accbuf;
+      float* sums = splits == 1 && f32 ? static_cast<float*>(a.dx) : accbuf;
       p.prev = v0 > 0 ? sums : nullptr;
       p.prev_apart = (reinterpret_cast<uintptr_t>(sums) & 31) != 0;
-      void* out = L.splits == 1 && last ? a.dx : sums;
-      p.bf16 = L.splits == 1 && last && !f32;
+      p.out = splits == 1 && last ? a.dx : sums;
+      p.bf16 = splits == 1 && last && !f32;
+      p.apart = (reinterpret_cast<uintptr_t>(p.out) & 31) != 0;
       if (!dense_map_k(&p.tmA, D, false, size_t(cols) * h, a.T, 1, size_t(cols) * h, 128) ||
-          !dense_map_mn(&p.tmB, a.W, false, a.d, a.V, 1, single ? 4 : 2))
+          !dense_map_mn(&p.tmB, a.W, false, a.d, a.V, 1, p.b_bytes / kBoxBytes))
         return MOE_ERR_CUDA;
-      p.out = out;
-      p.apart = (reinterpret_cast<uintptr_t>(out) & 31) != 0;
-      rc = single ? dense_launch<ProdOp<true>, 1>(p, a.grid_limit, MOE_K_XENT_DX, s)
-                  : dense_launch<ProdOp<true>, 2>(p, a.grid_limit, MOE_K_XENT_DX, s);
-      if (rc != MOE_OK) return rc;
+      if ((rc = dense_launch<ProdOp<true>>(L.dx.cg, p, a.grid_limit, MOE_K_XENT_DX, s)) != MOE_OK) return rc;
+      if (last && splits > 1 && (rc = launch_sum(accbuf, splits, size_t(a.T) * a.d, !f32, a.dx, s)) != MOE_OK) return rc;
     }
     if (a.dW) {
       ProdOp<false>::Params p;
       std::memset(&p, 0, sizeof(p));
-      const bool f32 = a.dW_type == MOE_Y_F32, one = real <= kBM;
+      const bool f32 = a.dW_type == MOE_Y_F32;
+      const int splits = pieces == 1 ? L.dW.splits : 1;  // accbuf holds dx's sums else
       p.M = real;
       p.N = a.d;
-      p.nt = ceil_div(a.d, kBN);
       p.once = ceil_div(a.T, kBK);
       p.nkb = f32 ? kTerms * p.once : p.once;
       p.run_kb = f32 ? kExactRun : p.nkb;
       p.code = kCodeXent + 3;
       p.err = err;
       p.cols = cols;
-      p.per_split = p.nkb;
-      p.mt = one ? 1 : ceil_div(real, 2 * kBM);
-      p.total = p.mt * p.nt;
-      p.bf16 = !f32;
-      uint8_t* out = static_cast<uint8_t*>(a.dW) + size_t(v0) * a.d * (f32 ? 4 : 2);
+      p.per_split = ceil_div(p.nkb, splits);
+      dense_shape(p, L.dW.cg, L.dW.tn, splits, false);
+      p.bf16 = splits == 1 && !f32;
+      p.out = splits > 1 ? static_cast<void*>(accbuf) : static_cast<uint8_t*>(a.dW) + size_t(v0) * a.d * (f32 ? 4 : 2);
+      p.apart = (reinterpret_cast<uintptr_t>(p.out) & 31) != 0;
       if (!dense_map_mn(&p.tmA, D, false, size_t(cols) * h, a.T, 1, 2) ||
-          !dense_map_mn(&p.tmB, xz, false, a.d, a.T, 1, one ? 4 : 2))
+          !dense_map_mn(&p.tmB, xz, false, a.d, a.T, 1, p.b_bytes / kBoxBytes))
         return MOE_ERR_CUDA;
-      p.out = out;
-      p.apart = (reinterpret_cast<uintptr_t>(out) & 31) != 0;
-      rc = one ? dense_launch<ProdOp<false>, 1>(p, a.grid_limit, MOE_K_XENT_DW, s)
-               : dense_launch<ProdOp<false>, 2>(p, a.grid_limit, MOE_K_XENT_DW, s);
-      if (rc != MOE_OK) return rc;
+      if ((rc = dense_launch<ProdOp<false>>(L.dW.cg, p, a.grid_limit, MOE_K_XENT_DW, s)) != MOE_OK) return rc;
+      if (splits > 1 && (rc = launch_sum(accbuf, splits, size_t(a.V) * a.d, !f32, a.dW, s)) != MOE_OK) return rc;
     }
-  }
-  if (a.dx && L.splits > 1) {
-    TraceScope trace_scope(MOE_K_XENT_ROWS, s);
-    const size_t n4 = size_t(a.T) * a.d / 4;
-    if (launch_pdl(xent_sum_kernel, dim3(static_cast<int>(std::min<size_t>((n4 + 255) / 256, num_sms() * 8))), dim3(256), 0,
-                   s, reinterpret_cast<const float4*>(accbuf), L.splits, n4, a.dx_type == MOE_Y_BF16, a.dx) != cudaSuccess)
-      return MOE_ERR_CUDA;
   }
   return MOE_OK;
 }
