@@ -639,7 +639,8 @@ int moe_balance_fwd(const moe_cfg* cfg, const float* logits, const int32_t* topk
   const moe_cfg& c = *cfg;
   MOE_TRY_CUDA(launch_balance(logits, topk_idx, mask, c.T, seqs, c.E, c.k, counts, mean_p, loss, zloss,
                               at<int32_t>(ws, L.hist), at<float>(ws, L.base), at<float>(ws, L.partial),
-                              at<int>(ws, L.err), static_cast<cudaStream_t>(stream)));
+                              at<int>(ws, L.err) + kErrBalanceWord, at<int>(ws, L.err),
+                              static_cast<cudaStream_t>(stream)));
   return MOE_OK;
 }
 

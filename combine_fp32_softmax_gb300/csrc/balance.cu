@@ -13,9 +13,9 @@
 // and the next rows are loaded while these are worked on.
 //
 // A sequence's sums are taken by as many blocks as its tokens give work to; each
-// keeps the sums of its tokens in registers, in fp32, and a second launch adds the
-// blocks' sums in a fixed order, with the roundings kept.  A sequence that one
-// block takes is finished in the first launch.  (fp64 sums took longer than all
+// keeps the sums of its tokens in registers, in fp32, and the last of them to end
+// (a second launch where there are more sequences than counters) adds the blocks'
+// sums in a fixed order, with the roundings kept.  (fp64 sums took longer than all
 // the rest: the part has two such additions a clock and SM.)
 #include <algorithm>
 
@@ -135,65 +135,178 @@ __device__ __forceinline__ void finish_sequence(const BalanceOut& o, int b, int 
   }
 }
 
+// Sums of sequence b from those of its parts, by one block: a thread takes V experts
+// (a 16-byte piece where rows are whole ones) of every group-th part; then the
+// groups of a warp, and the warps, are added in a fixed order.
+struct JoinShared {
+  float sp[kThreads / 32][256];
+  int sc[kThreads / 32][256];
+  float red[8], z[kThreads / 32];
+  int n[kThreads / 32];
+};
+template <int V>
+__device__ __forceinline__ void join_sequence(const int32_t* counts, const float* psums, const float2* zn, int b, int parts,
+                                              int E, int k, const BalanceOut& out, JoinShared& sh) {
+  constexpr int WARPS = kThreads / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int shift = 0;  // of the groups' width, a power of two of at least E / V
+  while ((V << shift) < E) ++shift;
+  const int groups = kThreads >> shift, g = tid >> shift, e = V * (tid & ((1 << shift) - 1));
+  Sum2 s[V], z;
+  int c[V] = {}, n = 0;
+  const size_t at = static_cast<size_t>(b) * parts;
+  // the parts were written by other blocks of this launch: read past L1
+  if (e < E) {
+#pragma unroll 4
+    for (int i = g; i < parts; i += groups) {
+      const size_t from = (at + i) * E + e;
+      if constexpr (V == 4) {
+        const float4 p = __ldcg(reinterpret_cast<const float4*>(psums + from));
+        const int4 q = __ldcg(reinterpret_cast<const int4*>(counts + from));
+        s[0].add(p.x);
+        s[1].add(p.y);
+        s[2].add(p.z);
+        s[3].add(p.w);
+        c[0] += q.x;
+        c[1] += q.y;
+        c[2] += q.z;
+        c[3] += q.w;
+      } else {
+        s[0].add(__ldcg(psums + from));
+        c[0] += __ldcg(counts + from);
+      }
+    }
+  }
+  for (int i = tid; i < parts; i += kThreads) {
+    const float2 v = __ldcg(zn + at + i);
+    z.add(v.x);
+    n += static_cast<int>(v.y);  // tokens of a part: far below 2^24
+  }
+  float zs = z.value();
+#pragma unroll
+  for (int off = 16; off; off >>= 1) {
+    zs += __shfl_xor_sync(kFull, zs, off);
+    n += __shfl_xor_sync(kFull, n, off);
+  }
+  if (lane == 0) {
+    sh.z[warp] = zs;
+    sh.n[warp] = n;
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    float v = s[j].value();
+    int q = c[j];
+    for (int off = 1 << shift; off < 32; off <<= 1) {
+      v += __shfl_xor_sync(kFull, v, off);
+      q += __shfl_xor_sync(kFull, q, off);
+    }
+    // groups wider than a warp: the warps of one group hold different experts
+    if (e < E && (shift >= 5 || (lane >> shift) == 0)) {
+      sh.sp[shift > 5 ? g : warp][e + j] = v;
+      sh.sc[shift > 5 ? g : warp][e + j] = q;
+    }
+  }
+  __syncthreads();
+  float ps = 0.f;
+  int count = 0;
+  zs = 0.f;
+  n = 0;
+  const int rows = shift > 5 ? groups : WARPS;
+  if (tid < E)
+    for (int i = 0; i < rows; ++i) {
+      ps += sh.sp[i][tid];
+      count += sh.sc[i][tid];
+    }
+#pragma unroll
+  for (int i = 0; i < WARPS; ++i) {
+    zs += sh.z[i];
+    n += sh.n[i];
+  }
+  finish_sequence(out, b, E, k, count, ps, zs, n, sh.red);
+}
+
 template <class Y>
 __global__ void __launch_bounds__(kThreads, 3)
     balance_sums_kernel(const float* __restrict__ logits, const int32_t* __restrict__ topk_idx,
                         const uint8_t* __restrict__ mask, int L, int B, int parts, int E, int k, int32_t* __restrict__ counts,
-                        float* __restrict__ psums, float2* __restrict__ zn, BalanceOut out, int* err) {
+                        float* __restrict__ psums, float2* __restrict__ zn, int* arrived, BalanceOut out, int* err) {
   griddep_wait();
   griddep_launch_dependents();
   constexpr int ROWS = 32 / Y::LANES, WARPS = kThreads / 32;
+  constexpr int AHEAD = Y::E <= 4 ? 2 : 1;  // rows on their way while one is worked on
+  constexpr int PICKS = 4;                  // picks of a thread that are asked for before the rows
+  __shared__ int last_part;
   __shared__ int hist[256];
-  __shared__ float ps[WARPS][256];
-  __shared__ float red[8], zw[WARPS];
-  __shared__ int nw[WARPS];
+  __shared__ JoinShared join;
+  auto& ps = join.sp;
+  auto& zw = join.z;
+  auto& nw = join.n;
+  auto& red = join.red;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane / Y::LANES, l = lane % Y::LANES;
   const int per = (L + parts - 1) / parts;
   for (int u = blockIdx.x; u < B * parts; u += gridDim.x) {
     const int b = u / parts, c = u - b * parts;
     if (threadIdx.x < 256) hist[threadIdx.x] = 0;
-    __syncthreads();
     const int t0 = b * L + min(L, c * per), t1 = b * L + min(L, (c + 1) * per);
+    const int32_t* picks = topk_idx + static_cast<size_t>(t0) * k;
+    const int slots = (t1 - t0) * k;
+    int first[PICKS];
+#pragma unroll
+    for (int i = 0; i < PICKS; ++i) {
+      const int at = threadIdx.x + i * kThreads;
+      first[i] = at < slots ? picks[at] : 0;
+    }
     auto live = [&](int t) { return t < t1 && (!mask || mask[t]); };
-    int t = t0 + warp * ROWS + sub;
-    bool on = live(t);
-    float v[Y::E];
-    load_values<Y>(logits + static_cast<size_t>(t) * E, on ? E : 0, l, v, -INFINITY);
-    for (int i = threadIdx.x; i < (t1 - t0) * k; i += kThreads) {
-      const int ti = t0 + i / k;
-      if (mask && !mask[ti]) continue;  // whatever it holds
-      const int e = topk_idx[static_cast<size_t>(t0) * k + i];
+    constexpr int STEP = WARPS * ROWS;
+    const int tw0 = t0 + warp * ROWS;
+    float v[AHEAD][Y::E];
+    bool on[AHEAD];
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {
+      const int t = tw0 + sub + j * STEP;
+      on[j] = live(t);
+      load_values<Y>(logits + static_cast<size_t>(t) * E, on[j] ? E : 0, l, v[j], -INFINITY);
+    }
+    __syncthreads();
+    auto count = [&](int at, int e) {
+      const int t = t0 + at / k;
+      if (mask && !mask[t]) return;  // whatever it holds
       if (static_cast<unsigned>(e) < static_cast<unsigned>(E))
         atomicAdd(&hist[e], 1);
       else
-        record_error(err, MOE_ERR_ARG, ti);
-    }
+        record_error(err, MOE_ERR_ARG, t);
+    };
+#pragma unroll
+    for (int i = 0; i < PICKS; ++i)
+      if (static_cast<int>(threadIdx.x) + i * kThreads < slots) count(threadIdx.x + i * kThreads, first[i]);
+    for (int at = threadIdx.x + PICKS * kThreads; at < slots; at += kThreads) count(at, picks[at]);
     float p[Y::E] = {};
     float z = 0.f;
     int n = 0;
-    for (int tw = t0 + warp * ROWS; tw < t1; tw += WARPS * ROWS) {  // the same rounds for all lanes of the warp
-      // the next row is on its way while this one is worked on
-      const int tn = t + WARPS * ROWS;
-      const bool on_n = live(tn);
-      float w[Y::E];
-      load_values<Y>(logits + static_cast<size_t>(tn) * E, on_n ? E : 0, l, w, -INFINITY);
-      float lse;
-      const bool ok = softmax_values<Y>(v, on ? E : 0, l, lse);
-      if (on) {
-        ++n;
-        if (ok) {
+    for (int tw = tw0; tw < t1; tw += AHEAD * STEP) {  // the same rounds for all lanes of the warp
 #pragma unroll
-          for (int i = 0; i < Y::E; ++i) p[i] += v[i];
-          z = fmaf(lse, lse, z);
-        } else if (l == 0) {
-          record_error(err, MOE_ERR_NONFINITE_CODE, t);
+      for (int j = 0; j < AHEAD; ++j) {
+        const int t = tw + sub + j * STEP, tn = t + AHEAD * STEP;
+        float w[Y::E];
+#pragma unroll
+        for (int i = 0; i < Y::E; ++i) w[i] = v[j][i];
+        const bool now = on[j];
+        on[j] = live(tn);
+        load_values<Y>(logits + static_cast<size_t>(tn) * E, on[j] ? E : 0, l, v[j], -INFINITY);
+        float lse;
+        const bool ok = softmax_values<Y>(w, now ? E : 0, l, lse);
+        if (now) {
+          ++n;
+          if (ok) {
+#pragma unroll
+            for (int i = 0; i < Y::E; ++i) p[i] += w[i];
+            z = fmaf(lse, lse, z);
+          } else if (l == 0) {
+            record_error(err, MOE_ERR_NONFINITE_CODE, t);
+          }
         }
       }
-#pragma unroll
-      for (int i = 0; i < Y::E; ++i) v[i] = w[i];
-      t = tn;
-      on = on_n;
     }
     // the rows of a warp, then the warps
 #pragma unroll
@@ -229,102 +342,34 @@ __global__ void __launch_bounds__(kThreads, 3)
         psums[static_cast<size_t>(u) * E + e] = psum;
       }
       if (e == 0) zn[u] = make_float2(zsum, static_cast<float>(total));
+      if (arrived) {  // the last block of a sequence joins its parts
+        __threadfence();
+        __syncthreads();
+        if (e == 0) {
+          last_part = atomicAdd(arrived + b, 1) == parts - 1;
+          if (last_part) arrived[b] = 0;  // for the next call
+        }
+        __syncthreads();
+        if (last_part) {
+          __threadfence();
+          join_sequence<Y::V>(counts, psums, zn, b, parts, E, k, out, join);
+        }
+      }
     }
     __syncthreads();
   }
 }
 
-// One block a sequence: a thread takes V experts (a 16-byte piece where rows are
-// whole ones) of every group-th part; then the groups of a warp, and the warps, are
-// added in a fixed order.
-constexpr int kJoin = 512;
+// The parts' sums of more sequences than there are counters for.
 template <int V>
-__global__ void __launch_bounds__(kJoin)
-    balance_join_kernel(const int32_t* __restrict__ counts, const float* __restrict__ psums, const float2* __restrict__ zn,
-                        int B, int parts, int E, int k, BalanceOut out) {
+__global__ void __launch_bounds__(kThreads)
+    balance_join_kernel(const int32_t* counts, const float* psums, const float2* zn, int B, int parts, int E, int k,
+                        BalanceOut out) {
   griddep_wait();
   griddep_launch_dependents();
-  constexpr int WARPS = kJoin / 32;
-  __shared__ float sp[WARPS][256];
-  __shared__ int sc[WARPS][256];
-  __shared__ float red[8], zred[WARPS];
-  __shared__ int nred[WARPS];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int shift = 0;  // of the groups' width, a power of two of at least E / V
-  while ((V << shift) < E) ++shift;
-  const int groups = kJoin >> shift, g = tid >> shift, e = V * (tid & ((1 << shift) - 1));
+  __shared__ JoinShared join;
   for (int b = blockIdx.x; b < B; b += gridDim.x) {
-    Sum2 s[V], z;
-    int c[V] = {}, n = 0;
-    const size_t at = static_cast<size_t>(b) * parts;
-    if (e < E) {
-#pragma unroll 4
-      for (int i = g; i < parts; i += groups) {
-        const size_t from = (at + i) * E + e;
-        if constexpr (V == 4) {
-          const float4 p = *reinterpret_cast<const float4*>(psums + from);
-          const int4 q = *reinterpret_cast<const int4*>(counts + from);
-          s[0].add(p.x);
-          s[1].add(p.y);
-          s[2].add(p.z);
-          s[3].add(p.w);
-          c[0] += q.x;
-          c[1] += q.y;
-          c[2] += q.z;
-          c[3] += q.w;
-        } else {
-          s[0].add(psums[from]);
-          c[0] += counts[from];
-        }
-      }
-    }
-    for (int i = tid; i < parts; i += kJoin) {
-      const float2 v = zn[at + i];
-      z.add(v.x);
-      n += static_cast<int>(v.y);  // tokens of a part: far below 2^24
-    }
-    float zs = z.value();
-#pragma unroll
-    for (int off = 16; off; off >>= 1) {
-      zs += __shfl_xor_sync(kFull, zs, off);
-      n += __shfl_xor_sync(kFull, n, off);
-    }
-    if (lane == 0) {
-      zred[warp] = zs;
-      nred[warp] = n;
-    }
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      float v = s[j].value();
-      int q = c[j];
-      for (int off = 1 << shift; off < 32; off <<= 1) {
-        v += __shfl_xor_sync(kFull, v, off);
-        q += __shfl_xor_sync(kFull, q, off);
-      }
-      // groups wider than a warp: the warps of one group hold different experts
-      if (e < E && (shift >= 5 || (lane >> shift) == 0)) {
-        sp[shift > 5 ? g : warp][e + j] = v;
-        sc[shift > 5 ? g : warp][e + j] = q;
-      }
-    }
-    __syncthreads();
-    float ps = 0.f;
-    int count = 0;
-    zs = 0.f;
-    n = 0;
-    const int rows = shift > 5 ? groups : WARPS;
-    for (int i = 0; i < rows; ++i) {
-      if (tid < E) {
-        ps += sp[i][tid];
-        count += sc[i][tid];
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < WARPS; ++i) {
-      zs += zred[i];
-      n += nred[i];
-    }
-    finish_sequence(out, b, E, k, count, ps, zs, n, red);
+    join_sequence<V>(counts, psums, zn, b, parts, E, k, out, join);
     __syncthreads();
   }
 }
@@ -432,18 +477,19 @@ cudaError_t with_layout(int E, F f) {
 
 cudaError_t launch_balance(const float* logits, const int32_t* topk_idx, const uint8_t* mask, int T, int B, int E, int k,
                            int32_t* counts, float* mean_p, float* loss, float* zloss, int32_t* part_counts, float* part_p,
-                           float* part_zn, int* err, cudaStream_t s) {
+                           float* part_zn, int* arrived, int* err, cudaStream_t s) {
   TraceScope trace_scope(MOE_K_BALANCE, s);
   const int parts = seq_parts(T, B);
   const BalanceOut out{counts, mean_p, loss, zloss};
   const int units = static_cast<int>(std::min<long long>(static_cast<long long>(B) * parts, num_sms() * 3));
   float2* zn = reinterpret_cast<float2*>(part_zn);
+  int* counters = B <= kBalanceCounters ? arrived : nullptr;
   cudaError_t e = with_layout(E, [&](auto y) {
     return launch_pdl(balance_sums_kernel<decltype(y)>, dim3(units), dim3(kThreads), 0, s, logits, topk_idx, mask, T / B, B,
-                      parts, E, k, part_counts, part_p, zn, out, err);
+                      parts, E, k, part_counts, part_p, zn, counters, out, err);
   });
-  if (e == cudaSuccess && parts > 1)
-    e = launch_pdl(E % 4 ? balance_join_kernel<1> : balance_join_kernel<4>, dim3(std::min(B, 65535)), dim3(kJoin), 0, s,
+  if (e == cudaSuccess && parts > 1 && !counters)
+    e = launch_pdl(E % 4 ? balance_join_kernel<1> : balance_join_kernel<4>, dim3(std::min(B, 65535)), dim3(kThreads), 0, s,
                    part_counts, part_p, zn, B, parts, E, k, out);
   return e;
 }

@@ -69,6 +69,9 @@ constexpr int kErrBarrierWord = 8;
 // GEMM kind's tile-ticket counter and finished-CTA count, two per kind from
 // this word on; both are back at 0 after every complete launch.
 constexpr int kErrSchedWord = 16;
+// Words of the error region that count the blocks of a sequence that have its
+// balance sums ready, one for each of the first sequences; 0 between calls.
+constexpr int kErrBalanceWord = 32, kBalanceCounters = 32;
 constexpr int kErrRegionBytes = 256;
 
 // Router / permutation: tokens per histogram block (the router and the fused

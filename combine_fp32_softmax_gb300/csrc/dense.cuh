@@ -466,7 +466,7 @@ DenseShape dense_pick(long long M, long long N, int mats, int nkb, bool sym, int
     const long long tiles = mats * (sym ? nt * (nt + 1) / 2 : nt * mt);
     for (int sp = 1; sp <= max_splits && sp <= nkb; sp += (sp + 3) / 4) {  // 1 to 5, 7, 9, 12, 15, 19, ...
       const long long units = 152 / o.cg, rounds = (tiles * sp + units - 1) / units;
-      const double us = rounds * (o.kb * ((nkb + sp - 1) / sp) + o.epi) + (sp > 1 ? 3.0 + sp * 8.0 * M * N / 5e6 : 0.0);
+      const double us = rounds * (o.kb * ((nkb + sp - 1) / sp) + o.epi) + (sp > 1 ? 3.0 + (sp - 1) * 8.0 * M * N / 5e6 : 0.0);
       if (us < 0.97 * least) {
         least = us;
         best = {o.cg, o.tn, sp};

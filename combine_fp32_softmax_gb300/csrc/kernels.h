@@ -49,10 +49,11 @@ cudaError_t launch_route_bwd(const float* logits, const int32_t* topk_idx, const
                              int T, int E, int k, int renorm, float* dlogits, int* err, cudaStream_t s);
 // Balance of the routing over B sequences of T / B tokens (balance.cu), and its
 // gradient added to `add` (which may be dlogits or null).  part_*: scratch of
-// E ceil(T / 32) ints, as many floats, and 2 ceil(T / 32) floats.
+// E ceil(T / 32) ints, as many floats, and 2 ceil(T / 32) floats; arrived:
+// kBalanceCounters ints that are 0 before and after the call.
 cudaError_t launch_balance(const float* logits, const int32_t* topk_idx, const uint8_t* mask, int T, int B, int E, int k,
                            int32_t* counts, float* mean_p, float* loss, float* zloss, int32_t* part_counts, float* part_p,
-                           float* part_zn, int* err, cudaStream_t s);
+                           float* part_zn, int* arrived, int* err, cudaStream_t s);
 cudaError_t launch_balance_bwd(const float* logits, const int32_t* counts, const uint8_t* mask, const float* dloss,
                                const float* dz, int T, int B, int E, int k, const float* add, float* dlogits,
                                cudaStream_t s);

@@ -22,31 +22,14 @@
 #include <cuda_fp16.h>
 
 #include "dense.cuh"
+#include "ortho.cuh"
 #include "ortho.h"
 
 namespace moe {
 namespace {
 
 constexpr int kCodeOrtho = 0x19;
-constexpr float kNsA = 3.4445f, kNsB = -4.7750f, kNsC = 2.0315f;
-constexpr float kNsEps = 1e-7f;
-// |X| <= 1 in the Frobenius norm at first and its singular values stay below
-// 1.3, so entries of X, A, B are below 1.3, 1.7, 14: times 2^10, 2^12, 2^11 they
-// stay below fp16's 65504, and entries 2^-24, 2^-26, 2^-25 are still normal.
-constexpr float kSX = 1024.f, kSA = 4096.f, kSB = 2048.f;
-constexpr int kSXLog2 = 10;
-// Below this norm of X the cubic term of a step is under 2^-19 of the linear one
-// for five steps on: the result is a^steps X.
-constexpr float kTiny = 0x1p-17f;
 constexpr int kNormParts = 1024;  // partial sums of squares of a matrix, at most
-
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-__device__ __forceinline__ float2 unpack_f16(uint32_t v) {
-  return __half22float2(*reinterpret_cast<const __half2*>(&v));
-}
 
 // ------------------------------------------------------------- products
 enum OrthoKind : int { kGramWide, kGramTall, kSquare, kUpdateWide, kUpdateTall };
@@ -362,6 +345,7 @@ Plan plan(int mats, int rows, int cols) {
 size_t ortho_workspace_bytes(int mats, int rows, int cols) { return plan(mats, rows, cols).total; }
 
 int launch_ortho(const OrthoArgs& a, cudaStream_t s) {
+  if (ortho_small(a.mats, a.rows, a.cols)) return launch_ortho_small(a, s);
   const Plan L = plan(a.mats, a.rows, a.cols);
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
   int* err = reinterpret_cast<int*>(ws + L.err);

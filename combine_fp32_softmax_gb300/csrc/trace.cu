@@ -52,7 +52,7 @@ const char* kNames[MOE_K_COUNT] = {"route",     "hist",          "scan",      "s
                                    "dw_reduce", "route_bwd",     "gemm_dx",   "dispatch_bwd", "gemm_dw13",
                                    "gemm_dw2",  "megakernel", "megakernel_bwd", "route_tables", "bwd_gemms", "decode", "linear", "q4",
                                    "balance", "balance_bwd", "xent", "xent_join", "xent_grad", "xent_dx", "xent_dw",
-                                   "xent_rows", "ortho_norm", "ortho_gram", "ortho_square", "ortho_update"};
+                                   "xent_rows", "ortho_norm", "ortho_gram", "ortho_square", "ortho_update", "ortho_small"};
 
 }  // namespace
 

@@ -138,7 +138,17 @@ __global__ void __launch_bounds__(256) xent_join_kernel(const float2* __restrict
   if (t >= T) return;
   const float2* row = part + static_cast<size_t>(t) * np;
   float2 v = make_float2(-INFINITY, 0.f);
-  for (int i = WARPS == 1 ? lane : static_cast<int>(threadIdx.x); i < np; i += 32 * WARPS) v = join_pairs(v, row[i]);
+  constexpr int STEP = 32 * WARPS;
+  for (int i = WARPS == 1 ? lane : static_cast<int>(threadIdx.x); i < np; i += 4 * STEP) {
+    float2 w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = i + j * STEP < np ? row[i + j * STEP] : make_float2(-INFINITY, 0.f);
+    const float m = fmaxf(fmaxf(fmaxf(v.x, w[0].x), fmaxf(w[1].x, w[2].x)), w[3].x);
+    float s = v.y == 0.f ? 0.f : v.y * (v.x == m ? 1.f : expf(v.x - m));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s += w[j].y == 0.f ? 0.f : w[j].y * (w[j].x == m ? 1.f : expf(w[j].x - m));
+    v = make_float2(m, s);
+  }
 #pragma unroll
   for (int off = 16; off; off >>= 1)
     v = join_pairs(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, off), __shfl_xor_sync(0xffffffffu, v.y, off)));
@@ -394,7 +404,7 @@ void logit_tiles(DenseParams& p, int T, int cols, int unit) {
 }
 int logit_cg(const DenseParams& p, int T) { return p.mt == ceil_div(T, kBM) ? 1 : 2; }
 
-Plan plan(int T, int V, int d, int backward) {
+Plan plan(int T, int V, int d, int backward, int terms) {
   Plan p{};
   DenseParams tiles{};
   tiles.M = T;
@@ -404,10 +414,10 @@ Plan plan(int T, int V, int d, int backward) {
   const long long want = std::max<long long>(kPieceBytes / 2 / T / kBN * kBN, kPieceCols);
   // every term of D for the whole vocabulary at most
   p.cols = static_cast<int>(std::min<long long>(want, 1ll * kTerms * all));
-  if (backward) {  // one bf16 term's K
-    const int width = std::min(V, p.cols);
-    p.dx = dense_pick(T, d, 1, ceil_div(width, kBK), false, kMaxSplits);
-    p.dW = dense_pick(width, d, 1, ceil_div(T, kBK), false, width == V ? kMaxSplits : 1);
+  if (backward) {
+    const int width = std::min(V, p.cols / terms);
+    p.dx = dense_pick(T, d, 1, terms * ceil_div(width, kBK), false, kMaxSplits);
+    p.dW = dense_pick(width, d, 1, terms * ceil_div(T, kBK), false, width == V ? kMaxSplits : 1);
   }
   size_t o = 0;
   auto take = [&](size_t bytes) {
@@ -449,10 +459,12 @@ int launch_sum(const float* part, int splits, size_t n, bool bf16, void* out, cu
 
 }  // namespace
 
-size_t xent_workspace_bytes(int T, int V, int d, int backward) { return plan(T, V, d, backward).total; }
+size_t xent_workspace_bytes(int T, int V, int d, int backward) {
+  return std::max(plan(T, V, d, backward, 1).total, backward ? plan(T, V, d, 1, kTerms).total : 0);
+}
 
 int launch_xent_fwd(const XentArgs& a, cudaStream_t s) {
-  const Plan L = plan(a.T, a.V, a.d, 0);
+  const Plan L = plan(a.T, a.V, a.d, 0, 1);
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
   int* err = reinterpret_cast<int*>(ws + L.err);
   StatsOp::Params p;
@@ -481,14 +493,14 @@ int launch_xent_fwd(const XentArgs& a, cudaStream_t s) {
 }
 
 int launch_xent_bwd(const XentArgs& a, cudaStream_t s) {
-  const Plan L = plan(a.T, a.V, a.d, 1);
+  const int h = (a.dx && a.dx_type == MOE_Y_F32) || (a.dW && a.dW_type == MOE_Y_F32) ? kTerms : 1;
+  const Plan L = plan(a.T, a.V, a.d, 1, h);
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
   int* err = reinterpret_cast<int*>(ws + L.err);
   void* D = ws + L.D;
   float* accbuf = reinterpret_cast<float*>(ws + L.acc);
   uint16_t* xz = reinterpret_cast<uint16_t*>(ws + L.xz);
   const Target target{a.target, a.target_type};
-  const int h = (a.dx && a.dx_type == MOE_Y_F32) || (a.dW && a.dW_type == MOE_Y_F32) ? kTerms : 1;
   // pieces of about equal size, whole tiles wide
   const int most = L.cols / h / kBN * kBN;
   const int pieces = ceil_div(a.V, most);

@@ -112,7 +112,7 @@ TRACE_KINDS = ["route", "hist", "scan", "scatter", "gather", "gemm1_swiglu", "ge
                "gemm_dw2", "megakernel", "megakernel_bwd",
                "route_tables", "bwd_gemms", "decode", "linear", "q4",
                "balance", "balance_bwd", "xent", "xent_join", "xent_grad", "xent_dx", "xent_dw", "xent_rows",
-               "ortho_norm", "ortho_gram", "ortho_square", "ortho_update"]
+               "ortho_norm", "ortho_gram", "ortho_square", "ortho_update", "ortho_small"]
 
 _lib = None
 
@@ -488,15 +488,18 @@ def moe_balance_fwd(cfg, logits, topk_idx, mask, counts, mean_p, loss, zloss, ws
     [B] of B sequences of T / B tokens; mask [T] bool (None: every token counts)."""
     B = loss.numel()
     c, nbytes, TE, Tk, BE, B_, T_ = _balance_sizes(_key(cfg), B)
-    _typed("logits", logits, _F32_ONLY, TE)
-    _typed("topk_idx", topk_idx, _I32_ONLY, Tk)
-    _typed("counts", counts, _I32_ONLY, BE)
-    _typed("mean_p", mean_p, _F32_ONLY, BE)
-    _typed("loss", loss, _F32_ONLY, B_)
-    _typed("zloss", zloss, _F32_ONLY, B_)
+    if not (logits.shape == TE and topk_idx.shape == Tk and counts.shape == mean_p.shape == BE and loss.shape == B_
+            and zloss.shape == B_ and logits.dtype is mean_p.dtype is loss.dtype is zloss.dtype is _F32
+            and topk_idx.dtype is counts.dtype is _I32 and ws.nbytes >= nbytes):
+        _typed("logits", logits, _F32_ONLY, TE)
+        _typed("topk_idx", topk_idx, _I32_ONLY, Tk)
+        _typed("counts", counts, _I32_ONLY, BE)
+        _typed("mean_p", mean_p, _F32_ONLY, BE)
+        _typed("loss", loss, _F32_ONLY, B_)
+        _typed("zloss", zloss, _F32_ONLY, B_)
+        _workspace(ws, nbytes)
     if mask is not None:
         _typed("mask", mask, _MASK_TYPES, T_)
-    _workspace(ws, nbytes)
     pz, pi, pm, pc, pp, pl, pzl, pw = _addresses(logits, topk_idx, mask, counts, mean_p, loss, zloss, ws)
     _call("moe_balance_fwd", c, pz, pi, pm, B, pc, pp, pl, pzl, pw, _stream(stream))
 
@@ -505,16 +508,19 @@ def moe_balance_bwd(cfg, logits, counts, mask, dloss, dzloss, dlogits_in, dlogit
     """dlogits [T, E] = dlogits_in (None: 0; may be dlogits) + the gradient of dloss . loss + dzloss . zloss."""
     B = dloss.numel()
     c, nbytes, TE, Tk, BE, B_, T_ = _balance_sizes(_key(cfg), B)
-    _typed("logits", logits, _F32_ONLY, TE)
-    _typed("counts", counts, _I32_ONLY, BE)
-    _typed("dloss", dloss, _F32_ONLY, B_)
-    _typed("dzloss", dzloss, _F32_ONLY, B_)
+    if not (logits.shape == dlogits.shape == TE and counts.shape == BE and dloss.shape == dzloss.shape == B_
+            and logits.dtype is dlogits.dtype is dloss.dtype is dzloss.dtype is _F32 and counts.dtype is _I32
+            and ws.nbytes >= nbytes):
+        _typed("logits", logits, _F32_ONLY, TE)
+        _typed("counts", counts, _I32_ONLY, BE)
+        _typed("dloss", dloss, _F32_ONLY, B_)
+        _typed("dzloss", dzloss, _F32_ONLY, B_)
+        _typed("dlogits", dlogits, _F32_ONLY, TE)
+        _workspace(ws, nbytes)
     if dlogits_in is not None:
         _typed("dlogits_in", dlogits_in, _F32_ONLY, TE)
-    _typed("dlogits", dlogits, _F32_ONLY, TE)
     if mask is not None:
         _typed("mask", mask, _MASK_TYPES, T_)
-    _workspace(ws, nbytes)
     pz, pc, pm, pl, pzl, pin, po, pw = _addresses(logits, counts, mask, dloss, dzloss, dlogits_in, dlogits, ws)
     _call("moe_balance_bwd", c, pz, pc, pm, B, pl, pzl, pin, po, pw, _stream(stream))
 

@@ -685,7 +685,8 @@ enum {
   MOE_K_ORTHO_GRAM = 32,  /* X X^T or X^T X */
   MOE_K_ORTHO_SQUARE = 33,/* b A + c A A */
   MOE_K_ORTHO_UPDATE = 34,/* a X + B X or a X + X B */
-  MOE_K_COUNT = 35
+  MOE_K_ORTHO_SMALL = 35, /* all steps of small matrices */
+  MOE_K_COUNT = 36
 };
 /* Testing aid for failure detection (no device fault involved): the forward
  * MegaKernel claims task `ticket` but never runs or signals it, so the
