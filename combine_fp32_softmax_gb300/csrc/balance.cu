@@ -8,9 +8,10 @@
 //
 // Both directions are bound by memory: the forward reads the logits and the
 // picks, the backward the logits and the gradient to add to, and writes one.  A
-// row lies on as few lanes as its 16-byte pieces need (two for 8 experts, 16 for
-// 64), so that a warp has several rows and their chains of shuffles in flight,
-// and the next rows are loaded while these are worked on.
+// row lies on few lanes, two 16-byte pieces each (one lane for 8 experts, eight for
+// 64): a warp has several rows at one time, which share the instructions of its
+// shuffles, logarithm and addresses (with one piece a lane these were most of 85
+// instructions a token at 64 experts), and the next rows are loaded meanwhile.
 //
 // A sequence's sums are taken by as many blocks as its tokens give work to; each
 // keeps the sums of its tokens in registers, in fp32, and the last of them to end
@@ -46,19 +47,21 @@ struct Lay {
   static constexpr int V = V_, LANES = LANES_, E = V_ * N_;  // E: values of a lane
   static __device__ __forceinline__ int expert(int l, int i) { return V * (l + LANES * (i / V)) + i % V; }
 };
+// The row's values, `none` beyond E; zeros where the row is not wanted.
 template <class Y>
-__device__ __forceinline__ void load_values(const float* row, int E, int l, float (&v)[Y::E], float none) {
+__device__ __forceinline__ void load_values(const float* row, bool on, int E, int l, float (&v)[Y::E], float none) {
+  none = on ? none : 0.f;
 #pragma unroll
   for (int i = 0; i < Y::E; i += Y::V) {
     const int e = Y::expert(l, i);
     if constexpr (Y::V == 4) {
-      const float4 w = e < E ? *reinterpret_cast<const float4*>(row + e) : make_float4(none, none, none, none);
+      const float4 w = on && e < E ? *reinterpret_cast<const float4*>(row + e) : make_float4(none, none, none, none);
       v[i] = w.x;
       v[i + 1] = w.y;
       v[i + 2] = w.z;
       v[i + 3] = w.w;
     } else {
-      v[i] = e < E ? row[e] : none;
+      v[i] = on && e < E ? row[e] : none;
     }
   }
 }
@@ -68,27 +71,27 @@ __device__ __forceinline__ float lanes_reduce(float v, F f) {
   for (int off = Y::LANES / 2; off; off >>= 1) v = f(v, __shfl_xor_sync(kFull, v, off));
   return v;
 }
-// p and lse of the row in v (in place); false where a logit is not finite.
+// exp(v - max) of the row in v, in place, 1 / their sum and lse; false where a
+// logit is not finite.  The instructions are what bounds a token here, so exp and
+// log are the short forms: p is off by at most 2^-21 + |z - max| 2^-23 of itself.
 template <class Y>
-__device__ __forceinline__ bool softmax_values(float (&v)[Y::E], int E, int l, float& lse) {
-  float m = -INFINITY, bad = 0.f;
+__device__ __forceinline__ bool softmax_values(float (&v)[Y::E], int E, int l, float& inv, float& lse) {
+  float m = v[0], bad = 0.f;
 #pragma unroll
   for (int i = 0; i < Y::E; ++i) {
-    m = fmaxf(m, v[i]);
+    if (i) m = fmaxf(m, v[i]);
     if (Y::expert(l, i) < E) bad = fmaf(0.f, v[i], bad);  // NaN where v is not finite
   }
   m = lanes_reduce<Y>(m, [](float a, float b) { return fmaxf(a, b); });
   float s = bad;
 #pragma unroll
   for (int i = 0; i < Y::E; ++i) {
-    v[i] = expf(v[i] - m);  // 0 beyond E
+    v[i] = __expf(v[i] - m);  // 0 beyond E
     s += v[i];
   }
   s = lanes_reduce<Y>(s, [](float a, float b) { return a + b; });
-  const float inv = 1.f / s;
-#pragma unroll
-  for (int i = 0; i < Y::E; ++i) v[i] *= inv;
-  lse = m + logf(s);
+  inv = __fdividef(1.f, s);
+  lse = m + __logf(s);
   return s == s;
 }
 
@@ -266,16 +269,15 @@ __global__ void __launch_bounds__(kThreads, 3)
     for (int j = 0; j < AHEAD; ++j) {
       const int t = tw0 + sub + j * STEP;
       on[j] = live(t);
-      load_values<Y>(logits + static_cast<size_t>(t) * E, on[j] ? E : 0, l, v[j], -INFINITY);
+      load_values<Y>(logits + static_cast<size_t>(t) * E, on[j], E, l, v[j], -INFINITY);
     }
     __syncthreads();
     auto count = [&](int at, int e) {
-      const int t = t0 + at / k;
-      if (mask && !mask[t]) return;  // whatever it holds
+      if (mask && !mask[t0 + at / k]) return;  // whatever it holds
       if (static_cast<unsigned>(e) < static_cast<unsigned>(E))
         atomicAdd(&hist[e], 1);
       else
-        record_error(err, MOE_ERR_ARG, t);
+        record_error(err, MOE_ERR_ARG, t0 + at / k);
     };
 #pragma unroll
     for (int i = 0; i < PICKS; ++i)
@@ -293,19 +295,15 @@ __global__ void __launch_bounds__(kThreads, 3)
         for (int i = 0; i < Y::E; ++i) w[i] = v[j][i];
         const bool now = on[j];
         on[j] = live(tn);
-        load_values<Y>(logits + static_cast<size_t>(tn) * E, on[j] ? E : 0, l, v[j], -INFINITY);
-        float lse;
-        const bool ok = softmax_values<Y>(w, now ? E : 0, l, lse);
-        if (now) {
-          ++n;
-          if (ok) {
+        load_values<Y>(logits + static_cast<size_t>(tn) * E, on[j], E, l, v[j], -INFINITY);
+        float inv, lse;
+        const bool ok = softmax_values<Y>(w, E, l, inv, lse);
+        const float use = now ? inv : 0.f;  // a row that is not there: zeros' exponentials, times 0
+        n += now;
 #pragma unroll
-            for (int i = 0; i < Y::E; ++i) p[i] += w[i];
-            z = fmaf(lse, lse, z);
-          } else if (l == 0) {
-            record_error(err, MOE_ERR_NONFINITE_CODE, t);
-          }
-        }
+        for (int i = 0; i < Y::E; ++i) p[i] = fmaf(w[i], use, p[i]);
+        z = fmaf(now ? lse : 0.f, lse, z);
+        if (__any_sync(kFull, now && !ok) && now && !ok && l == 0) record_error(err, MOE_ERR_NONFINITE_CODE, t);
       }
     }
     // the rows of a warp, then the warps
@@ -390,14 +388,14 @@ __global__ void __launch_bounds__(kThreads, 2)
   // consecutive rows to a warp: the sequence rarely changes
   const int per = (rounds + nwarps - 1) / nwarps;
   const int r0 = min(rounds, w * per), r1 = min(rounds, r0 + per);
-  int cur = -1;
+  int next = 0;  // first token after the sequence in hand
   float a[Y::E] = {}, hz = 0.f;
   auto read = [&](int r, float (&v)[Y::E], float (&in)[Y::E], bool& on) {
     const int t = r * ROWS + sub;
     const bool here = r < r1 && t < T;
     on = here && (!mask || mask[t]);
-    load_values<Y>(logits + static_cast<size_t>(t) * E, on ? E : 0, l, v, -INFINITY);
-    load_values<Y>(add + static_cast<size_t>(t) * E, here && add ? E : 0, l, in, 0.f);
+    load_values<Y>(logits + static_cast<size_t>(t) * E, on, E, l, v, -INFINITY);
+    load_values<Y>(add + static_cast<size_t>(t) * E, here && add, E, l, in, 0.f);
   };
   float v[Y::E], in[Y::E];
   bool on;
@@ -406,9 +404,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     float vn[Y::E], inn[Y::E];
     bool on_n;
     read(r + 1, vn, inn, on_n);
-    const int t = r * ROWS + sub, b = min(t, T - 1) / L;
-    if (__any_sync(kFull, b != cur)) {
-      cur = b;
+    const int t = r * ROWS + sub;
+    if (__any_sync(kFull, t >= next)) {
+      const int b = min(t, T - 1) / L;
+      next = (b + 1) * L;
       int c[Y::E], sum = 0;
 #pragma unroll
       for (int i = 0; i < Y::E; ++i) {
@@ -424,17 +423,16 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int i = 0; i < Y::E; ++i) a[i] = f * c[i];
       hz = n > 0.f ? 2.f * dz[b] / n : 0.f;
     }
-    float lse;
-    const bool ok = softmax_values<Y>(v, on ? E : 0, l, lse);
+    float inv, lse;
+    const bool ok = softmax_values<Y>(v, E, l, inv, lse);
     float dot = 0.f;
 #pragma unroll
     for (int i = 0; i < Y::E; ++i) dot = fmaf(a[i], v[i], dot);
     dot = lanes_reduce<Y>(dot, [](float x, float y) { return x + y; });
-    if (on && ok) {
-      const float shift = hz * lse - dot;
+    const float use = on ? inv : 0.f, shift = fmaf(hz, lse, -dot * inv);
+    if (ok)  // a row that is not there is: zeros' exponentials, times 0
 #pragma unroll
-      for (int i = 0; i < Y::E; ++i) in[i] = fmaf(v[i], a[i] + shift, in[i]);
-    }
+      for (int i = 0; i < Y::E; ++i) in[i] = fmaf(v[i] * use, a[i] + shift, in[i]);
     if (t < T) {
       float* to = dlogits + static_cast<size_t>(t) * E;
 #pragma unroll
@@ -460,11 +458,11 @@ __global__ void __launch_bounds__(kThreads, 2)
 template <typename F>
 cudaError_t with_layout(int E, F f) {
   if (E % 4 == 0) {  // whole 16-byte pieces
-    if (E <= 8) return f(Lay<4, 2, 1>{});
-    if (E <= 16) return f(Lay<4, 4, 1>{});
-    if (E <= 32) return f(Lay<4, 8, 1>{});
-    if (E <= 64) return f(Lay<4, 16, 1>{});
-    if (E <= 128) return f(Lay<4, 32, 1>{});
+    if (E <= 8) return f(Lay<4, 1, 2>{});
+    if (E <= 16) return f(Lay<4, 2, 2>{});
+    if (E <= 32) return f(Lay<4, 4, 2>{});
+    if (E <= 64) return f(Lay<4, 8, 2>{});
+    if (E <= 128) return f(Lay<4, 16, 2>{});
     return f(Lay<4, 32, 2>{});
   }
   if (E <= 8) return f(Lay<1, 8, 1>{});
