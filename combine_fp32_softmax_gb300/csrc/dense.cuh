@@ -48,6 +48,7 @@ static_assert(kDenseSmem <= kSmemBudget, "shared memory budget of one CTA");
 // What every operation's launch has.
 struct DenseParams {
   CUtensorMap tmA, tmB;  // operands
+  CUtensorMap tmT;       // a symmetric operand's MN-major view (see dense_flip)
   int M, N;              // rows and columns of C
   int mt, nt;            // tiles of its rows (of TILE_M) and columns (of tn)
   int tn;                // columns of a tile: 256, on single CTAs also fewer (a multiple of 16)
@@ -56,6 +57,7 @@ struct DenseParams {
   int nst;               // stages of the ring
   int nkb;               // K blocks
   int run_kb;            // K blocks of a run of sums
+  int upper;             // a symmetric operand holds only its tiles from the diagonal on
   int total;             // tiles of the launch
   int code;              // names the operation in the error word of a wait that ran out
   int* err;
@@ -72,8 +74,16 @@ struct DenseTile {
 __device__ __forceinline__ int dense_cols(const DenseParams& p, const DenseTile& t) { return min(p.tn, p.N - t.n0); }
 template <int CG, bool B_MN>
 __device__ __forceinline__ int dense_mma_n(const DenseParams& p, const DenseTile& t) {
-  constexpr int unit = CG == 1 ? 16 : B_MN ? 128 : 64;
+  constexpr int unit = CG == 1 ? 16 : B_MN ? 128 : 64;  // B_MN: for some K blocks at least
   return (dense_cols(p, t) + unit - 1) / unit * unit;
+}
+
+// Of a symmetric matrix only the 256 x 256 tiles on and above the diagonal need be
+// stored: an operand's rows of a lower tile are the columns of an upper one, read
+// as an MN-major tile.  True where K block kb of the rows from `row` on is such a
+// one.
+__device__ __forceinline__ bool dense_flip(const DenseParams& p, int kb, int row) {
+  return p.upper && kb * kBK / kBN < row / kBN;
 }
 
 // Where an epilogue thread stands: lane of its warp, TMEM lane quadrant, half of
@@ -129,16 +139,17 @@ __device__ __forceinline__ void dense_commit(uint32_t lead, uint32_t bar) {
         : "memory");
 }
 // The four MMAs (16 deep each) of a K block and the release of its stage, from
-// the lane with `lead`.  a and b: shared-memory addresses / 16 of the tiles; the
-// first MMA overwrites C unless `add`.
-template <int CG, bool A_MN, bool B_MN>
-__device__ __forceinline__ void dense_mma(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add,
-                                          uint32_t empty) {
+// the lane with `lead`.  a and b: shared-memory addresses / 16 of the tiles, each
+// MN-major or K-major; the first MMA overwrites C unless `add`.
+template <int CG>
+__device__ __forceinline__ void dense_mma(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, bool a_mn, bool b_mn,
+                                          uint32_t idesc, bool add, uint32_t empty) {
   // descriptor words as in smem_desc_sw128: leading byte offset above the address,
   // stride byte offset, version and swizzle in the upper word
   constexpr uint32_t kHi = (1024u >> 4) | 1u << 14 | 2u << 29;
-  const uint32_t alo = a | (A_MN ? kBoxBytes >> 4 : 1u) << 16, blo = b | (B_MN ? kBoxBytes >> 4 : 1u) << 16;
-  constexpr uint32_t sa = A_MN ? 128 : 2, sb = B_MN ? 128 : 2;  // 16 elements of K further
+  const uint32_t alo = a | (a_mn ? kBoxBytes >> 4 : 1u) << 16, blo = b | (b_mn ? kBoxBytes >> 4 : 1u) << 16;
+  const uint32_t sa = a_mn ? 128 : 2, sb = b_mn ? 128 : 2;  // 16 elements of K further
+  idesc |= (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
 #define MOE_DENSE_MMA(GROUP)                                                                                         \
   asm volatile(                                                                                                      \
       "{\n\t.reg .pred q, f, t;\n\t.reg .b32 x, y;\n\t.reg .b64 u, v;\n\t"                                             \
@@ -151,7 +162,7 @@ __device__ __forceinline__ void dense_mma(uint32_t lead, uint32_t d, uint32_t a,
       "@q tcgen05.mma.cta_group::" GROUP ".kind::f16 [%1], u, v, %4, t;\n\t"                                         \
       "add.u32 x, x, %7;\n\tadd.u32 y, y, %8;\n\tmov.b64 u, {x, %5};\n\tmov.b64 v, {y, %5};\n\t"                     \
       "@q tcgen05.mma.cta_group::" GROUP ".kind::f16 [%1], u, v, %4, t;\n\t}" ::"r"(lead),                           \
-      "r"(d), "r"(alo), "r"(blo), "r"(idesc), "r"(kHi), "r"(add ? 1u : 0u), "n"(sa), "n"(sb)                         \
+      "r"(d), "r"(alo), "r"(blo), "r"(idesc), "r"(kHi), "r"(add ? 1u : 0u), "r"(sa), "r"(sb)                         \
       : "memory")
   if constexpr (CG == 1)
     MOE_DENSE_MMA("1");
@@ -188,22 +199,25 @@ __device__ __forceinline__ void dense_loads(const typename Op::Params& p, const 
   bn += b_off;
   const bool to_even = CG == 2 && rank == 1;
   const int mat = Op::ONE ? 0 : t.mat;  // ONE: a single A and B, t.mat tells results apart
-  if constexpr (Op::A_MN) {
+  const bool flip_a = Op::FLIP_A && dense_flip(p, kb, t.m0), flip_b = Op::FLIP_B && dense_flip(p, kb, t.n0);
+  if (Op::A_MN || flip_a) {
+    const CUtensorMap* map = flip_a ? &p.tmT : &p.tmA;
     if (to_even)
-      tma_load_4d_to_even(sA, &p.tmA, bar, 0, ak, am / 64, mat);
+      tma_load_4d_to_even(sA, map, bar, 0, ak, am / 64, mat);
     else
-      tma_load_4d(sA, &p.tmA, bar, 0, ak, am / 64, mat);
+      tma_load_4d(sA, map, bar, 0, ak, am / 64, mat);
   } else {
     if (to_even)
       tma_load_3d_to_even(sA, &p.tmA, bar, ak, am, mat);
     else
       tma_load_3d(sA, &p.tmA, bar, ak, am, mat);
   }
-  if constexpr (Op::B_MN) {
+  if (Op::B_MN || flip_b) {
+    const CUtensorMap* map = flip_b ? &p.tmT : &p.tmB;
     if (to_even)
-      tma_load_4d_to_even(sB, &p.tmB, bar, 0, bk, bn / 64, mat);
+      tma_load_4d_to_even(sB, map, bar, 0, bk, bn / 64, mat);
     else
-      tma_load_4d(sB, &p.tmB, bar, 0, bk, bn / 64, mat);
+      tma_load_4d(sB, map, bar, 0, bk, bn / 64, mat);
   } else {
     if (to_even)
       tma_load_3d_to_even(sB, &p.tmB, bar, bk, bn, mat);
@@ -265,7 +279,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_kernel(const __grid_co
       bool ok = true;
       for (int i = first; ok && i < p.total && !*abort; i += step) {
         const DenseTile t = Op::template tile<CG>(p, i, rank);
-        const int b_off = CG == 2 ? rank * dense_mma_n<CG, Op::B_MN>(p, t) / 2 : 0;
+        const int b_off = CG == 2 ? rank * dense_mma_n<CG, Op::B_MN || Op::FLIP_B>(p, t) / 2 : 0;
         for (int kb = t.kb0; kb < t.kb1; ++kb) {
           if (!mbar_wait(&ss.empty[stage], phase ^ 1, abort, p.err, where(0, i))) {
             ok = false;
@@ -294,8 +308,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_kernel(const __grid_co
       // The warp stays together: one lane issues by predicate, everything it needs
       // is the same in all lanes, and the next stage's barrier is asked while this
       // one's MMAs go out.
-      constexpr uint32_t idesc0 = Op::F16 ? idesc_f16_f32(kBM * CG, 0, Op::A_MN ? 1 : 0, Op::B_MN ? 1 : 0)
-                                          : idesc_bf16_f32(kBM * CG, 0, Op::A_MN ? 1 : 0, Op::B_MN ? 1 : 0);
+      constexpr uint32_t idesc0 = Op::F16 ? idesc_f16_f32(kBM * CG, 0, 0, 0) : idesc_bf16_f32(kBM * CG, 0, 0, 0);
       const uint32_t lead = elect_one();
       const uint32_t ring = smem_u32(smem) >> 4, sb16 = SB >> 4, a16 = p.a_bytes >> 4;
       const uint32_t full0 = smem_u32(&ss.full[0]), empty0 = smem_u32(&ss.empty[0]), tfull0 = smem_u32(&ss.tfull[0]);
@@ -305,7 +318,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_kernel(const __grid_co
       bool ready = false;  // the stage's data is known to be there
       for (int i = first; ok && i < p.total && !*abort; i += step) {
         const DenseTile t = Op::template tile<CG>(p, i, rank);
-        const uint32_t idesc = idesc0 | static_cast<uint32_t>(dense_mma_n<CG, Op::B_MN>(p, t) >> 3) << 17;
+        const uint32_t idesc = idesc0 | static_cast<uint32_t>(dense_mma_n<CG, Op::B_MN || Op::FLIP_B>(p, t) >> 3) << 17;
         int left = 0;  // K blocks left of the run
         uint32_t dtm = 0;
         for (int kb = t.kb0; kb < t.kb1; ++kb) {
@@ -328,7 +341,9 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_kernel(const __grid_co
             phase ^= 1;
           }
           ready = __all_sync(0xffffffffu, mbar_test_wait(full0 + 8 * stage, phase));
-          dense_mma<CG, Op::A_MN, Op::B_MN>(lead, dtm, a, a + a16, idesc, !fresh, empty);
+          const bool a_mn = Op::A_MN || (Op::FLIP_A && dense_flip(p, kb, t.m0));
+          const bool b_mn = Op::B_MN || (Op::FLIP_B && dense_flip(p, kb, t.n0));
+          dense_mma<CG>(lead, dtm, a, a + a16, a_mn, b_mn, idesc, !fresh, empty);
           issued = true;
           if (left == 0) {
             dense_commit<CG>(lead, tfull0 + 8 * (it & 1));

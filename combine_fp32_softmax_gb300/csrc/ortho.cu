@@ -14,8 +14,10 @@
 // fp16 by less than that rounding.  The norm itself enters as an fp32 factor of
 // the first step, so a bf16 G is taken exactly.
 //
-// A and A A are symmetric: only the tiles on and above the diagonal are computed,
-// and their epilogue stores both halves.
+// A and A A are symmetric: only the tiles on and above the diagonal are computed.
+// Where the products run on CTA pairs only those are stored, and the products that
+// read them take the others transposed (dense_flip); on single CTAs, whose tiles
+// are smaller, the epilogue stores both halves.
 #include <algorithm>
 #include <cstring>
 
@@ -40,6 +42,8 @@ struct OrthoOp {
   static constexpr bool A_MN = KIND == kGramTall;
   static constexpr bool B_MN = KIND == kGramTall || KIND == kUpdateWide;
   static constexpr bool F16 = true, ONE = false;
+  // which operands are symmetric matrices
+  static constexpr bool FLIP_A = KIND == kSquare || KIND == kUpdateWide, FLIP_B = KIND == kSquare || KIND == kUpdateTall;
   struct Params : DenseParams {
     const float* scal;   // [mats]: X of the first step is scal times what is stored; 0: matrix needs no products
     int first;           // the first step
@@ -143,7 +147,7 @@ struct OrthoOp {
           }
       }
       if constexpr (SYM) {
-        if (t.n0 / p.tn > t.m0 / p.tn) {  // a tile off the diagonal: also to the other side
+        if (!p.upper && t.n0 / p.tn > t.m0 / p.tn) {  // a tile off the diagonal: also to the other side
           // neighbouring lanes' rows side by side: even lanes take the even columns,
           // odd ones the odd, and a store covers 32 rows of two columns
           const bool odd = e.lane & 1;
@@ -382,6 +386,7 @@ int launch_ortho(const OrthoArgs& a, cudaStream_t s) {
   const DenseShape gram_shape = dense_pick(m, m, a.mats, ceil_div(wide ? a.cols : a.rows, kBK), true, 1);
   const DenseShape square_shape = dense_pick(m, m, a.mats, ceil_div(m, kBK), true, 1);
   const DenseShape update_shape = dense_pick(a.rows, a.cols, a.mats, ceil_div(m, kBK), false, 1);
+  const int upper = gram_shape.cg == 2 && square_shape.cg == 2;
   int rc = MOE_OK;
   for (int it = 0; it < a.steps && rc == MOE_OK; ++it) {
     const __half* Xi = X[it & 1];
@@ -393,6 +398,7 @@ int launch_ortho(const OrthoArgs& a, cudaStream_t s) {
       dense_shape(p, gram_shape.cg, gram_shape.tn, a.mats, true);
       p.scal = scal;
       p.first = it == 0;
+      p.upper = upper;
       p.out = A;
       p.out_pitch = L.spitch;
       bool ok;
@@ -418,10 +424,12 @@ int launch_ortho(const OrthoArgs& a, cudaStream_t s) {
       base(p, 1, m, m, m);
       dense_shape(p, square_shape.cg, square_shape.tn, a.mats, true);
       p.scal = scal;
+      p.upper = upper;
       p.old = A;
       p.pitch = L.spitch;
       if (!dense_map_k(&p.tmA, A, true, m, m, a.mats, L.spitch, 128) ||
-          !dense_map_k(&p.tmB, A, true, m, m, a.mats, L.spitch, p.b_bytes / 128))
+          !dense_map_k(&p.tmB, A, true, m, m, a.mats, L.spitch, p.b_bytes / 128) ||
+          !dense_map_mn(&p.tmT, A, true, L.spitch, m, a.mats, 2))
         return MOE_ERR_CUDA;
       p.out = B;
       p.out_pitch = L.spitch;
@@ -433,18 +441,20 @@ int launch_ortho(const OrthoArgs& a, cudaStream_t s) {
       dense_shape(p, update_shape.cg, update_shape.tn, a.mats, false);
       p.scal = scal;
       p.first = it == 0;
+      p.upper = upper;
       p.old = Xi;
       p.pitch = L.pitch;
       p.bf16 = last;
       p.out = last && !copy ? a.O : reinterpret_cast<uint16_t*>(Xo);
       p.out_pitch = last && !copy ? a.cols : L.pitch;
       p.apart = (reinterpret_cast<uintptr_t>(p.out) & 31) != 0;
-      bool ok;
+      // rows of A of one CTA, or its columns of B
+      bool ok = dense_map_mn(&p.tmT, B, true, L.spitch, m, a.mats, wide ? 2 : p.b_bytes / kBoxBytes);
       if (wide)
-        ok = dense_map_k(&p.tmA, B, true, m, m, a.mats, L.spitch, 128) &&
+        ok = ok && dense_map_k(&p.tmA, B, true, m, m, a.mats, L.spitch, 128) &&
              dense_map_mn(&p.tmB, Xi, true, L.pitch, a.rows, a.mats, p.b_bytes / kBoxBytes);
       else
-        ok = dense_map_k(&p.tmA, Xi, true, a.cols, a.rows, a.mats, L.pitch, 128) &&
+        ok = ok && dense_map_k(&p.tmA, Xi, true, a.cols, a.rows, a.mats, L.pitch, 128) &&
              dense_map_k(&p.tmB, B, true, m, m, a.mats, L.spitch, p.b_bytes / 128);
       return ok;
     };

@@ -55,7 +55,7 @@ __device__ __forceinline__ DenseTile rows_first(const DenseParams& p, int i, int
 
 // ------------------------------------------------------------- forward
 struct StatsOp {
-  static constexpr bool A_MN = false, B_MN = false, F16 = false, ONE = true;
+  static constexpr bool A_MN = false, B_MN = false, F16 = false, ONE = true, FLIP_A = false, FLIP_B = false;
   struct Params : DenseParams {
     Target target;
     float2* part;  // [T][2 nt]: maximum and sum of exp of half a tile's logits
@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(256) xent_join_kernel(const float2* __restrict
 
 // ------------------------------------------------------------ backward: D
 struct GradOp {
-  static constexpr bool A_MN = false, B_MN = false, F16 = false, ONE = true;
+  static constexpr bool A_MN = false, B_MN = false, F16 = false, ONE = true, FLIP_A = false, FLIP_B = false;
   struct Params : DenseParams {
     Target target;
     const float* loss;
@@ -258,7 +258,7 @@ struct GradOp {
 // D^T, B = x, K runs over the tokens, likewise.
 template <bool DX>
 struct ProdOp {
-  static constexpr bool A_MN = !DX, B_MN = true, F16 = false, ONE = true;
+  static constexpr bool A_MN = !DX, B_MN = true, F16 = false, ONE = true, FLIP_A = false, FLIP_B = false;
   struct Params : DenseParams {
     int v0;           // DX: the piece's first column of the vocabulary
     int once;         // K blocks of one of D's bf16 terms
