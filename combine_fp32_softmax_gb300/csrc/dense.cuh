@@ -226,6 +226,22 @@ __device__ __forceinline__ void dense_loads(const typename Op::Params& p, const 
   }
 }
 
+// The tiles of a CTA one after the other.  Whether a tile has products at all is
+// read from memory for some operations: a tile ahead, so that no role waits for it.
+template <class Op, int CG>
+struct DenseWalk {
+  int step, rank;
+  float flag;
+  __device__ __forceinline__ DenseWalk(const typename Op::Params& p, int first, int step_, int rank_)
+      : step(step_), rank(rank_), flag(first < p.total ? Op::flag(p, first) : 0.f) {}
+  __device__ __forceinline__ DenseTile next(const typename Op::Params& p, int i) {
+    DenseTile t = Op::template tile<CG>(p, i, rank);
+    if (flag == 0.f) t.kb1 = t.kb0;
+    if (i + step < p.total) flag = Op::flag(p, i + step);
+    return t;
+  }
+};
+
 template <class Op, int CG>
 __global__ void __launch_bounds__(kDenseThreads, 1) dense_kernel(const __grid_constant__ typename Op::Params p) {
   const int NST = p.nst, SB = p.a_bytes + p.b_bytes;  // both multiples of 1024
@@ -277,8 +293,9 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_kernel(const __grid_co
       int stage = 0;
       uint32_t phase = 0, filled = 0, fill_par = 0;
       bool ok = true;
+      DenseWalk<Op, CG> walk(p, first, step, rank);
       for (int i = first; ok && i < p.total && !*abort; i += step) {
-        const DenseTile t = Op::template tile<CG>(p, i, rank);
+        const DenseTile t = walk.next(p, i);
         const int b_off = CG == 2 ? rank * dense_mma_n<CG, Op::B_MN || Op::FLIP_B>(p, t) / 2 : 0;
         for (int kb = t.kb0; kb < t.kb1; ++kb) {
           if (!mbar_wait(&ss.empty[stage], phase ^ 1, abort, p.err, where(0, i))) {
@@ -316,8 +333,9 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_kernel(const __grid_co
       uint32_t phase = 0;
       bool ok = true, issued = false;
       bool ready = false;  // the stage's data is known to be there
+      DenseWalk<Op, CG> walk(p, first, step, rank);
       for (int i = first; ok && i < p.total && !*abort; i += step) {
-        const DenseTile t = Op::template tile<CG>(p, i, rank);
+        const DenseTile t = walk.next(p, i);
         const uint32_t idesc = idesc0 | static_cast<uint32_t>(dense_mma_n<CG, Op::B_MN || Op::FLIP_B>(p, t) >> 3) << 17;
         int left = 0;  // K blocks left of the run
         uint32_t dtm = 0;
@@ -367,8 +385,9 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_kernel(const __grid_co
     e.part = (warp - 4) >> 2;
     int it = 0;
     bool ok = true;
+    DenseWalk<Op, CG> walk(p, first, step, rank);
     for (int i = first; ok && i < p.total && !*abort; i += step) {
-      const DenseTile t = Op::template tile<CG>(p, i, rank);
+      const DenseTile t = walk.next(p, i);
       const bool active = t.m0 + 32 * e.q < p.M;
       const auto pre = Op::pre(p, t, e);
       uint32_t acc[4][32];

@@ -54,25 +54,21 @@ struct OrthoOp {
     int bf16;            // last update: bf16 results
     int apart;           // 1: out is not on a 32-byte boundary
   };
+  static __device__ __forceinline__ int tiles_each(const Params& p) { return SYM ? p.nt * (p.nt + 1) / 2 : p.mt * p.nt; }
+  static __device__ __forceinline__ float flag(const Params& p, int i) { return p.scal[i / tiles_each(p)]; }
   template <int CG>
   static __device__ __forceinline__ DenseTile tile(const Params& p, int i, int rank) {
-    int mat, mb, nb;
+    const int per = tiles_each(p), mat = i / per;
+    int j = i - mat * per, mb, nb;
     if constexpr (SYM) {  // row mb has the tiles mb, mb + 1, ... of its columns
-      const int per = p.nt * (p.nt + 1) / 2;
-      mat = i / per;
-      int j = i - mat * per;
       mb = 0;
       while (j >= p.nt - mb) j -= p.nt - mb++;
       nb = mb + j;
     } else {
-      const int per = p.mt * p.nt;
-      mat = i / per;
-      const int j = i - mat * per;
       mb = j / p.nt;
       nb = j - mb * p.nt;
     }
-    const bool skip = p.scal[mat] == 0.f;
-    return {mat, mb * kBM * CG + rank * kBM, nb * p.tn, 0, skip ? 0 : p.nkb};
+    return {mat, mb * kBM * CG + rank * kBM, nb * p.tn, 0, p.nkb};
   }
   static __device__ __forceinline__ void coords(const Params&, const DenseTile& t, int kb, int& ak, int& am, int& bk,
                                                 int& bn) {

@@ -61,6 +61,7 @@ struct StatsOp {
     float2* part;  // [T][2 nt]: maximum and sum of exp of half a tile's logits
     float* zt;     // [T] the target's logit
   };
+  static __device__ __forceinline__ float flag(const Params&, int) { return 1.f; }
   template <int CG>
   static __device__ __forceinline__ DenseTile tile(const Params& p, int i, int rank) {
     return rows_first<CG>(p, i, rank);
@@ -187,6 +188,7 @@ struct GradOp {
     float w, lse, at;  // of exp(z - lse); log of the sum; D at the target
     int rel;           // the target's column among this thread's, or another number
   };
+  static __device__ __forceinline__ float flag(const Params&, int) { return 1.f; }
   template <int CG>
   static __device__ __forceinline__ DenseTile tile(const Params& p, int i, int rank) {
     return rows_first<CG>(p, i, rank);
@@ -269,6 +271,7 @@ struct ProdOp {
     int bf16;         // type of out
     int apart, prev_apart;  // 1: not on a 32-byte boundary
   };
+  static __device__ __forceinline__ float flag(const Params&, int) { return 1.f; }
   template <int CG>
   static __device__ __forceinline__ DenseTile tile(const Params& p, int i, int rank) {
     // columns fastest: the tiles that run at one time are about as many row
