@@ -457,6 +457,12 @@ def _typed(name, t, dtypes, shape):
         raise ValueError(f"{name}: {tuple(shape)} of {' or '.join(map(str, dtypes))} expected, got {got}")
 
 
+def _room(ws, nbytes):
+    """A workspace must have nbytes."""
+    if ws is None or ws.nbytes < nbytes:
+        raise ValueError(f"ws: {nbytes} bytes expected, got {None if ws is None else ws.nbytes}")
+
+
 def _addresses(*tensors):
     """Addresses of contiguous tensors on the current device, where the launches go (None stays None)."""
     dev, out = _device(), []
@@ -488,16 +494,20 @@ def moe_balance_fwd(cfg, logits, topk_idx, mask, counts, mean_p, loss, zloss, ws
     [B] of B sequences of T / B tokens; mask [T] bool (None: every token counts)."""
     B = loss.numel()
     c, nbytes, TE, Tk, BE, B_, T_ = _balance_sizes(_key(cfg), B)
-    if not (logits.shape == TE and topk_idx.shape == Tk and counts.shape == mean_p.shape == BE and loss.shape == B_
-            and zloss.shape == B_ and logits.dtype is mean_p.dtype is loss.dtype is zloss.dtype is _F32
-            and topk_idx.dtype is counts.dtype is _I32 and ws.nbytes >= nbytes):
+    try:
+        right = (logits.shape == TE and topk_idx.shape == Tk and counts.shape == mean_p.shape == BE and loss.shape == B_
+                 and zloss.shape == B_ and logits.dtype is mean_p.dtype is loss.dtype is zloss.dtype is _F32
+                 and topk_idx.dtype is counts.dtype is _I32 and ws.nbytes >= nbytes)
+    except AttributeError:  # None
+        right = False
+    if not right:
         _typed("logits", logits, _F32_ONLY, TE)
         _typed("topk_idx", topk_idx, _I32_ONLY, Tk)
         _typed("counts", counts, _I32_ONLY, BE)
         _typed("mean_p", mean_p, _F32_ONLY, BE)
         _typed("loss", loss, _F32_ONLY, B_)
         _typed("zloss", zloss, _F32_ONLY, B_)
-        _workspace(ws, nbytes)
+        _room(ws, nbytes)
     if mask is not None:
         _typed("mask", mask, _MASK_TYPES, T_)
     pz, pi, pm, pc, pp, pl, pzl, pw = _addresses(logits, topk_idx, mask, counts, mean_p, loss, zloss, ws)
@@ -508,15 +518,19 @@ def moe_balance_bwd(cfg, logits, counts, mask, dloss, dzloss, dlogits_in, dlogit
     """dlogits [T, E] = dlogits_in (None: 0; may be dlogits) + the gradient of dloss . loss + dzloss . zloss."""
     B = dloss.numel()
     c, nbytes, TE, Tk, BE, B_, T_ = _balance_sizes(_key(cfg), B)
-    if not (logits.shape == dlogits.shape == TE and counts.shape == BE and dloss.shape == dzloss.shape == B_
-            and logits.dtype is dlogits.dtype is dloss.dtype is dzloss.dtype is _F32 and counts.dtype is _I32
-            and ws.nbytes >= nbytes):
+    try:
+        right = (logits.shape == dlogits.shape == TE and counts.shape == BE and dloss.shape == dzloss.shape == B_
+                 and logits.dtype is dlogits.dtype is dloss.dtype is dzloss.dtype is _F32 and counts.dtype is _I32
+                 and ws.nbytes >= nbytes)
+    except AttributeError:  # None
+        right = False
+    if not right:
         _typed("logits", logits, _F32_ONLY, TE)
         _typed("counts", counts, _I32_ONLY, BE)
         _typed("dloss", dloss, _F32_ONLY, B_)
         _typed("dzloss", dzloss, _F32_ONLY, B_)
         _typed("dlogits", dlogits, _F32_ONLY, TE)
-        _workspace(ws, nbytes)
+        _room(ws, nbytes)
     if dlogits_in is not None:
         _typed("dlogits_in", dlogits_in, _F32_ONLY, TE)
     if mask is not None:
@@ -557,7 +571,7 @@ def _xent_shape(x, W, target, *rows):
 def moe_xent_fwd(x, W, target, loss, lse, ws, stream=None):
     """loss [T] and lse [T] fp32 of the logits x [T, d] . W [V, d]^T against target [T] int32 or int64 (below 0: none)."""
     T, V, d, tt = _xent_shape(x, W, target, ("loss", loss), ("lse", lse))
-    _workspace(ws, _xent_bytes(T, V, d, 0))
+    _room(ws, _xent_bytes(T, V, d, 0))
     px, pW, pt, pl, ps, pw = _addresses(x, W, target, loss, lse, ws)
     _call("moe_xent_fwd", T, V, d, px, pW, pt, tt, pl, ps, pw, _stream(stream))
 
@@ -572,7 +586,7 @@ def moe_xent_bwd(x, W, target, loss, lse, dloss, dlse, dx, dW, ws, stream=None):
         _typed("dx", dx, _FLOATS, (T, d))
     if dW is not None:
         _typed("dW", dW, _FLOATS, (V, d))
-    _workspace(ws, _xent_bytes(T, V, d, 1))
+    _room(ws, _xent_bytes(T, V, d, 1))
     px, pW, pt, pl, ps, pdl, pds, pdx, pdW, pw = _addresses(x, W, target, loss, lse, dloss, dlse, dx, dW, ws)
     _call("moe_xent_bwd", T, V, d, px, pW, pt, tt, pl, ps, pdl, pds, pdx, 0 if dx is None else _y_type(dx), pdW,
           0 if dW is None else _y_type(dW), pw, _stream(stream))
@@ -602,7 +616,7 @@ def moe_orthogonalize(G, O, steps, ws, stream=None):
     _typed("G", G, _FLOATS, G.shape)
     _typed("O", O, _BF16_ONLY, G.shape)
     mats, rows, cols = G.shape if G.dim() == 3 else (1, *G.shape)
-    _workspace(ws, _ortho_bytes(mats, rows, cols))
+    _room(ws, _ortho_bytes(mats, rows, cols))
     pG, pO, pw = _addresses(G, O, ws)
     _call("moe_orthogonalize", mats, rows, cols, pG, _y_type(G), pO, int(steps), pw, _stream(stream))
 
