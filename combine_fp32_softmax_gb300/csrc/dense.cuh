@@ -227,13 +227,13 @@ __device__ __forceinline__ void dense_loads(const typename Op::Params& p, const 
 }
 
 // The tiles of a CTA one after the other.  Whether a tile has products at all is
-// read from memory for some operations: a tile ahead, so that no role waits for it.
+// read from memory for some operations: a tile ahead, so that no role waits for it
+// (a first tile without is computed all the same; the epilogue drops it).
 template <class Op, int CG>
 struct DenseWalk {
   int step, rank;
-  float flag;
-  __device__ __forceinline__ DenseWalk(const typename Op::Params& p, int first, int step_, int rank_)
-      : step(step_), rank(rank_), flag(first < p.total ? Op::flag(p, first) : 0.f) {}
+  float flag = 1.f;
+  __device__ __forceinline__ DenseWalk(int step_, int rank_) : step(step_), rank(rank_) {}
   __device__ __forceinline__ DenseTile next(const typename Op::Params& p, int i) {
     DenseTile t = Op::template tile<CG>(p, i, rank);
     if (flag == 0.f) t.kb1 = t.kb0;
@@ -268,6 +268,11 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_kernel(const __grid_co
     ss.abort = 0;
     fence_mbar_init();
   }
+  if (threadIdx.x == 32 * 2) {  // while the kernel before still runs
+    tma_prefetch_desc(&p.tmA);
+    tma_prefetch_desc(&p.tmB);
+    if (Op::FLIP_A || Op::FLIP_B) tma_prefetch_desc(&p.tmT);
+  }
   if (warp == 1) {
     tmem_alloc<CG>(&ss.tmem_base, kTmemCols);
     tmem_relinquish<CG>();
@@ -288,12 +293,10 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_kernel(const __grid_co
   if (warp < 4) {
     regs_give<kIssueRegs>();
     if (warp == 0 && lane == 0) {
-      tma_prefetch_desc(&p.tmA);
-      tma_prefetch_desc(&p.tmB);
       int stage = 0;
       uint32_t phase = 0, filled = 0, fill_par = 0;
       bool ok = true;
-      DenseWalk<Op, CG> walk(p, first, step, rank);
+      DenseWalk<Op, CG> walk(step, rank);
       for (int i = first; ok && i < p.total && !*abort; i += step) {
         const DenseTile t = walk.next(p, i);
         const int b_off = CG == 2 ? rank * dense_mma_n<CG, Op::B_MN || Op::FLIP_B>(p, t) / 2 : 0;
@@ -333,7 +336,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_kernel(const __grid_co
       uint32_t phase = 0;
       bool ok = true, issued = false;
       bool ready = false;  // the stage's data is known to be there
-      DenseWalk<Op, CG> walk(p, first, step, rank);
+      DenseWalk<Op, CG> walk(step, rank);
       for (int i = first; ok && i < p.total && !*abort; i += step) {
         const DenseTile t = walk.next(p, i);
         const uint32_t idesc = idesc0 | static_cast<uint32_t>(dense_mma_n<CG, Op::B_MN || Op::FLIP_B>(p, t) >> 3) << 17;
@@ -385,7 +388,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_kernel(const __grid_co
     e.part = (warp - 4) >> 2;
     int it = 0;
     bool ok = true;
-    DenseWalk<Op, CG> walk(p, first, step, rank);
+    DenseWalk<Op, CG> walk(step, rank);
     for (int i = first; ok && i < p.total && !*abort; i += step) {
       const DenseTile t = walk.next(p, i);
       const bool active = t.m0 + 32 * e.q < p.M;

@@ -76,7 +76,7 @@ struct OrthoOp {
     am = t.m0;
     bn = t.n0;
   }
-  // Read while the tile's products still run: the first step's factor and, for
+  // Read while the tile's products still run: the matrix's factor and, for
   // square and update, this thread's 128 values of the old matrix.
   struct Pre {
     float r;
@@ -84,7 +84,7 @@ struct OrthoOp {
   };
   static __device__ __forceinline__ Pre pre(const Params& p, const DenseTile& t, const DenseEpi& e) {
     Pre o;
-    o.r = p.first ? p.scal[t.mat] : 1.f / kSX;
+    o.r = p.scal[t.mat];
     if constexpr (KIND == kSquare || !SYM) {
       const int x = dense_col(p, t, e), row = t.m0 + 32 * e.q + e.lane;
       const int w = dense_width(p, t, e);  // what it reads past the last column lies before the pitch
@@ -103,8 +103,8 @@ struct OrthoOp {
   }
   static __device__ __forceinline__ void epilogue(const Params& p, const DenseTile& t, DenseEpi& e, const Pre& pre,
                                                   uint32_t (&acc)[4][32]) {
-    if (t.kb1 == t.kb0) return;
-    const float r = pre.r;
+    if (pre.r == 0.f) return;  // no products for this matrix
+    const float r = p.first ? pre.r : 1.f / kSX;
     const int x0 = dense_col(p, t, e), x1 = x0 + dense_width(p, t, e), y = t.m0 + 32 * e.q;
     // gram: A = r^2 sums; square: B = b A + c sums; update: X' = a r X + r sums
     const float fs = KIND == kSquare                         ? kNsC * (kSB / (kSA * kSA))
