@@ -28,8 +28,12 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kUnits = 152 * 3;  // blocks to spread the tokens over; fixed, so the sums' order is
+// Threads of a block of the sums and of the backward.  Blocks to spread the tokens
+// over: two a SM; fixed, so the sums' order is.  (131,072 tokens of 64 experts, both
+// directions: 31 us with 2, 35 with 3 and 40 with 4 blocks of 512 threads a SM, 47
+// with 6 of 256: each block's own sums and their join cost more than the rows gain.)
+constexpr int kThreads = 512, kBwdThreads = 256;
+constexpr int kUnits = 152 * 2;
 
 // Blocks of a sequence: at least 32 tokens each, so that all blocks' sums fit in
 // the E ceil(T / 32) words of the histogram regions of the workspace.
@@ -229,7 +233,7 @@ __device__ __forceinline__ void join_sequence(const int32_t* counts, const float
 }
 
 template <class Y>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, 2)
     balance_sums_kernel(const float* __restrict__ logits, const int32_t* __restrict__ topk_idx,
                         const uint8_t* __restrict__ mask, int L, int B, int parts, int E, int k, int32_t* __restrict__ counts,
                         float* __restrict__ psums, float2* __restrict__ zn, int* arrived, BalanceOut out, int* err) {
@@ -326,12 +330,15 @@ __global__ void __launch_bounds__(kThreads, 3)
     const int e = threadIdx.x;
     float psum = 0.f, zsum = 0.f;
     int total = 0;
+    if (e < E)
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-      if (e < E) psum += ps[w][e];
-      zsum += zw[w];
-      total += nw[w];
-    }
+      for (int w = 0; w < WARPS; ++w) psum += ps[w][e];
+    if (parts == 1 || e == 0)
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        zsum += zw[w];
+        total += nw[w];
+      }
     if (parts == 1) {
       finish_sequence(out, b, E, k, e < E ? hist[e] : 0, psum, zsum, total, red);
     } else {
@@ -374,7 +381,7 @@ __global__ void __launch_bounds__(kThreads)
 
 // dlogits = add + gradient; add may be dlogits itself or null.
 template <class Y>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kBwdThreads, 4)
     balance_bwd_kernel(const float* __restrict__ logits, const int32_t* __restrict__ counts, const uint8_t* __restrict__ mask,
                        const float* __restrict__ dloss, const float* __restrict__ dz, int T, int L, int E, int k,
                        const float* add, float* dlogits) {
@@ -384,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int lane = threadIdx.x & 31;
   const int sub = lane / Y::LANES, l = lane % Y::LANES;
   const int rounds = (T + ROWS - 1) / ROWS;
-  const int nwarps = gridDim.x * (kThreads / 32), w = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  const int nwarps = gridDim.x * (kBwdThreads / 32), w = blockIdx.x * (kBwdThreads / 32) + (threadIdx.x >> 5);
   // consecutive rows to a warp: the sequence rarely changes
   const int per = (rounds + nwarps - 1) / nwarps;
   const int r0 = min(rounds, w * per), r1 = min(rounds, r0 + per);
@@ -479,7 +486,7 @@ cudaError_t launch_balance(const float* logits, const int32_t* topk_idx, const u
   TraceScope trace_scope(MOE_K_BALANCE, s);
   const int parts = seq_parts(T, B);
   const BalanceOut out{counts, mean_p, loss, zloss};
-  const int units = static_cast<int>(std::min<long long>(static_cast<long long>(B) * parts, num_sms() * 3));
+  const int units = static_cast<int>(std::min<long long>(static_cast<long long>(B) * parts, num_sms() * 2));
   float2* zn = reinterpret_cast<float2*>(part_zn);
   int* counters = B <= kBalanceCounters ? arrived : nullptr;
   cudaError_t e = with_layout(E, [&](auto y) {
@@ -498,8 +505,8 @@ cudaError_t launch_balance_bwd(const float* logits, const int32_t* counts, const
   TraceScope trace_scope(MOE_K_BALANCE_BWD, s);
   return with_layout(E, [&](auto y) {
     const long long warps = ceil_div(T, 32 / decltype(y)::LANES);
-    const int blocks = static_cast<int>(std::min<long long>(ceil_div(warps, kThreads / 32), num_sms() * 2));
-    return launch_pdl(balance_bwd_kernel<decltype(y)>, dim3(blocks), dim3(kThreads), 0, s, logits, counts, mask, dloss, dz, T,
+    const int blocks = static_cast<int>(std::min<long long>(ceil_div(warps, kBwdThreads / 32), num_sms() * 4));
+    return launch_pdl(balance_bwd_kernel<decltype(y)>, dim3(blocks), dim3(kBwdThreads), 0, s, logits, counts, mask, dloss, dz, T,
                       T / B, E, k, add, dlogits);
   });
 }
