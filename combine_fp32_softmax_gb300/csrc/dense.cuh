@@ -411,19 +411,25 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_kernel(const __grid_co
         ++it;
         tc_fence_after();
         const uint32_t ta = tmem + (static_cast<uint32_t>(e.q * 32) << 16) + buf * kBN + e.part * p.half;
-        if (r == 0) {
+        if (!active) {
+          // rows that are not there
+        } else if (r == 0) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_ld_32x32(ta + 32 * c, acc[c]);
           tmem_ld_wait();
         } else {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t v[32];
-            tmem_ld_32x32(ta + 32 * c, v);
+          for (int c = 0; c < 4; c += 2) {
+            if (32 * c >= p.half) break;
+            uint32_t v[2][32];
+            tmem_ld_32x32(ta + 32 * c, v[0]);
+            tmem_ld_32x32(ta + 32 * c + 32, v[1]);
             tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              acc[c][j] = __float_as_uint(__uint_as_float(acc[c][j]) + __uint_as_float(v[j]));
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                acc[c + h][j] = __float_as_uint(__uint_as_float(acc[c + h][j]) + __uint_as_float(v[h][j]));
           }
         }
         tc_fence_before();

@@ -29,11 +29,20 @@ constexpr int kCodeXent = 0x11;  // + operation, in the error word of a wait tha
 // most): at 8192 tokens of d = 2048 and V = 100000 the forward takes 2.37, 2.22 and
 // 2.20 ms with runs of 4, 8 and 16 blocks, the pieces' D 2.74, 2.40 and 2.38 ms.
 constexpr int kExactRun = 8;
+// Few tokens' time is their weights' bytes: runs of one block, whose losses nearly
+// vanish (loss off by 1e-7 of itself, as a plain fp32 product's; 1e-6 with 8), cost
+// 3 % there (37 tokens of d = 4096 and V = 50257: 76.8 against 74 us).
+int logit_run(int T) { return T <= kBM ? 1 : kExactRun; }
 // Bytes of D that a piece of the vocabulary takes at least, and its columns at least.
 constexpr size_t kPieceBytes = size_t(512) << 20;
 constexpr int kPieceCols = 8192;
-// bf16 values that D is the sum of where a gradient comes out in fp32: 24 bits.
+// bf16 values that D is the sum of: three (24 bits) for an fp32 gradient; two for a
+// bf16 one of up to 256 tokens, where bytes and latency count more than the
+// products: a row of a gradient is then little more than its target's term, whose
+// rounding would be as large again as the result's own (2.4e-3 of the norm against
+// 1.7e-3); one for more tokens.
 constexpr int kTerms = 3;
+int terms_of(int T, bool f32) { return f32 ? kTerms : T <= 256 ? 2 : 1; }
 
 struct Target {
   const void* p;
@@ -172,15 +181,35 @@ __global__ void __launch_bounds__(256) xent_join_kernel(const float2* __restrict
 }
 
 // ------------------------------------------------------------ backward: D
+// What the backward needs of a row.
+struct RowGrads {
+  Target target;
+  const float* loss;
+  const float* dloss;
+  const float* dlse;  // or null
+  int V;
+  // D at the target: (g + h) p - g with p = exp(-loss), so that what is left of a
+  // certain token's gradient is not the difference of two numbers near g.
+  __device__ __forceinline__ float at_target(int row, float g, float h) const {
+    const float l = -loss[row];
+    return h * expf(l) + g * expm1f(l);
+  }
+};
+// Where D is kept in one bf16 value, a row of it is kept divided by that number
+// which makes its target's entry, the largest as a rule, a bf16 value exactly; dx,
+// whose rows are sums over a row of D, is multiplied by it again in fp32.
+__device__ __forceinline__ float row_unit(float at) {
+  const float b = bf16_lo(pack_bf16(at, 0.f));
+  const float s = at / b;
+  return b != 0.f && isfinite(s) ? s : 1.f;
+}
+
 struct GradOp {
   static constexpr bool A_MN = false, B_MN = false, F16 = false, ONE = true, FLIP_A = false, FLIP_B = false;
   struct Params : DenseParams {
-    Target target;
-    const float* loss;
+    RowGrads rows;
     const float* lse;
-    const float* dloss;
-    const float* dlse;  // or null
-    int V, v0;          // the piece is columns [v0, v0 + N) of V; columns from V on are zeros
+    int v0;             // the piece is columns [v0, v0 + N) of V; columns from V on are zeros
     int terms;          // D is the sum of so many bf16 values, each N columns further
     uint16_t* D;        // [T, terms N]
   };
@@ -203,16 +232,18 @@ struct GradOp {
     const int row = t.m0 + 32 * e.q + e.lane;
     Pre r{0.f, 0.f, 0.f, -1};
     if (row < p.M) {
-      const int target = load_target(p.target, row, p.V);
-      const float g = target >= 0 ? p.dloss[row] : 0.f, h = p.dlse ? p.dlse[row] : 0.f;
+      const int target = load_target(p.rows.target, row, p.rows.V);
+      const float g = target >= 0 ? p.rows.dloss[row] : 0.f, h = p.rows.dlse ? p.rows.dlse[row] : 0.f;
       r.w = g + h;
       r.lse = p.lse[row];
-      // (g + h) p - g with p = exp(-loss): what is left of a certain token's
-      // gradient is not the difference of two numbers near g
       if (g != 0.f) {
-        const float l = -p.loss[row];
-        r.at = h * expf(l) + g * expm1f(l);
+        r.at = p.rows.at_target(row, g, h);
         r.rel = target - (p.v0 + dense_col(p, t, e));
+        if (p.terms == 1) {
+          const float s = row_unit(r.at);
+          r.w /= s;
+          r.at /= s;
+        }
       }
     }
     return r;
@@ -220,7 +251,7 @@ struct GradOp {
   static __device__ __forceinline__ void epilogue(const Params& p, const DenseTile& t, DenseEpi& e, const Pre& r,
                                                   uint32_t (&acc)[4][32]) {
     const int col = dense_col(p, t, e);  // of the piece
-    const int n = p.V - (p.v0 + col);    // columns that exist
+    const int n = p.rows.V - (p.v0 + col);  // columns that exist
     const int w = dense_width(p, t, e);  // a multiple of 32
     const int y = t.m0 + 32 * e.q;
 #pragma unroll
@@ -266,6 +297,8 @@ struct ProdOp {
     int once;         // K blocks of one of D's bf16 terms
     int cols;         // columns of the piece: from one term of D to the next
     int per_split;    // K blocks of a split; each has a matrix of its own in out
+    RowGrads rows;      // DX
+    int unit;           // DX: rows of D are kept divided by row_unit
     const float* prev;  // added to the products, laid out as out is in fp32
     void* out;        // [splits][M][N]
     int bf16;         // type of out
@@ -294,13 +327,25 @@ struct ProdOp {
     }
     bn = t.n0;
   }
-  static __device__ __forceinline__ int pre(const Params&, const DenseTile&, const DenseEpi&) { return 0; }
-  static __device__ __forceinline__ void epilogue(const Params& p, const DenseTile& t, DenseEpi& e, int,
+  static __device__ __forceinline__ float pre(const Params& p, const DenseTile& t, const DenseEpi& e) {
+    const int row = t.m0 + 32 * e.q + e.lane;
+    if (!DX || !p.unit || row >= p.M || load_target(p.rows.target, row, p.rows.V) < 0) return 1.f;
+    const float g = p.rows.dloss[row], h = p.rows.dlse ? p.rows.dlse[row] : 0.f;
+    return g != 0.f ? row_unit(p.rows.at_target(row, g, h)) : 1.f;
+  }
+  static __device__ __forceinline__ void epilogue(const Params& p, const DenseTile& t, DenseEpi& e, float unit,
                                                   uint32_t (&acc)[4][32]) {
     const int x = dense_col(p, t, e), row = t.m0 + 32 * e.q + e.lane;
     const int w = dense_width(p, t, e);  // a multiple of 32
     if (row >= p.M) return;
     const size_t at = (static_cast<size_t>(t.mat) * p.M + row) * p.N + x;
+    if constexpr (DX) {
+      if (p.unit)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) acc[c][j] = __float_as_uint(unit * __uint_as_float(acc[c][j]));
+    }
     if (p.prev) {
 #pragma unroll
       for (int c = 0; c < 4; ++c)
@@ -463,7 +508,7 @@ int launch_sum(const float* part, int splits, size_t n, bool bf16, void* out, cu
 }  // namespace
 
 size_t xent_workspace_bytes(int T, int V, int d, int backward) {
-  return std::max(plan(T, V, d, backward, 1).total, backward ? plan(T, V, d, 1, kTerms).total : 0);
+  return std::max(plan(T, V, d, backward, terms_of(T, false)).total, backward ? plan(T, V, d, 1, kTerms).total : 0);
 }
 
 int launch_xent_fwd(const XentArgs& a, cudaStream_t s) {
@@ -479,7 +524,7 @@ int launch_xent_fwd(const XentArgs& a, cudaStream_t s) {
       !dense_map_k(&p.tmB, a.W, false, a.d, a.V, 1, a.d, p.b_bytes / 128))
     return MOE_ERR_CUDA;
   p.nkb = a.d / kBK;
-  p.run_kb = kExactRun;
+  p.run_kb = logit_run(a.T);
   p.code = kCodeXent;
   p.err = err;
   p.target = {a.target, a.target_type};
@@ -496,7 +541,7 @@ int launch_xent_fwd(const XentArgs& a, cudaStream_t s) {
 }
 
 int launch_xent_bwd(const XentArgs& a, cudaStream_t s) {
-  const int h = (a.dx && a.dx_type == MOE_Y_F32) || (a.dW && a.dW_type == MOE_Y_F32) ? kTerms : 1;
+  const int h = std::max(a.dx ? terms_of(a.T, a.dx_type == MOE_Y_F32) : 1, a.dW ? terms_of(a.T, a.dW_type == MOE_Y_F32) : 1);
   const Plan L = plan(a.T, a.V, a.d, 1, h);
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
   int* err = reinterpret_cast<int*>(ws + L.err);
@@ -504,6 +549,7 @@ int launch_xent_bwd(const XentArgs& a, cudaStream_t s) {
   float* accbuf = reinterpret_cast<float*>(ws + L.acc);
   uint16_t* xz = reinterpret_cast<uint16_t*>(ws + L.xz);
   const Target target{a.target, a.target_type};
+  const RowGrads rows{target, a.loss, a.dloss, a.dlse, a.V};
   // pieces of about equal size, whole tiles wide
   const int most = L.cols / h / kBN * kBN;
   const int pieces = ceil_div(a.V, most);
@@ -532,15 +578,11 @@ int launch_xent_bwd(const XentArgs& a, cudaStream_t s) {
         return MOE_ERR_CUDA;
       p.D = static_cast<uint16_t*>(D);
       p.nkb = a.d / kBK;
-      p.run_kb = kExactRun;  // the forward's logits, bit for bit
+      p.run_kb = logit_run(a.T);  // the forward's logits, bit for bit
       p.code = kCodeXent + 1;
       p.err = err;
-      p.target = target;
-      p.loss = a.loss;
+      p.rows = rows;
       p.lse = a.lse;
-      p.dloss = a.dloss;
-      p.dlse = a.dlse;
-      p.V = a.V;
       p.v0 = v0;
       p.terms = h;
       if ((rc = launch_logits<GradOp>(p, a, MOE_K_XENT_GRAD, s)) != MOE_OK) return rc;
@@ -553,8 +595,10 @@ int launch_xent_bwd(const XentArgs& a, cudaStream_t s) {
       p.M = a.T;
       p.N = a.d;
       p.once = cols / kBK;
-      p.nkb = f32 ? kTerms * p.once : p.once;
+      p.nkb = terms_of(a.T, f32) * p.once;
       p.run_kb = f32 ? kExactRun : p.nkb;
+      p.rows = rows;
+      p.unit = h == 1;
       p.code = kCodeXent + 2;
       p.err = err;
       p.v0 = v0;
@@ -583,7 +627,7 @@ int launch_xent_bwd(const XentArgs& a, cudaStream_t s) {
       p.M = real;
       p.N = a.d;
       p.once = ceil_div(a.T, kBK);
-      p.nkb = f32 ? kTerms * p.once : p.once;
+      p.nkb = terms_of(a.T, f32) * p.once;
       p.run_kb = f32 ? kExactRun : p.nkb;
       p.code = kCodeXent + 3;
       p.err = err;
