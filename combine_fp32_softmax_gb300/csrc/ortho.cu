@@ -106,11 +106,12 @@ struct OrthoOp {
     if (pre.r == 0.f) return;  // no products for this matrix
     const float r = p.first ? pre.r : 1.f / kSX;
     const int x0 = dense_col(p, t, e), x1 = x0 + dense_width(p, t, e), y = t.m0 + 32 * e.q;
-    // gram: A = r^2 sums; square: B = b A + c sums; update: X' = a r X + r sums
+    // gram: A = r^2 sums; square: B + 2.5 I = b A + c sums + 2.5 I; update: X' =
+    // (a - 2.5) r X + r sums
     const float fs = KIND == kSquare                         ? kNsC * (kSB / (kSA * kSA))
                      : (KIND == kGramWide || KIND == kGramTall) ? r * r * kSA
                                                              : r * ((p.bf16 ? 1.f : kSX) / kSB);
-    const float fo = KIND == kSquare ? kNsB * (kSB / kSA) : kNsA * r * (p.bf16 ? 1.f : kSX);
+    const float fo = KIND == kSquare ? kNsB * (kSB / kSA) : (kNsA - kNsShift) * r * (p.bf16 ? 1.f : kSX);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const int x = x0 + 32 * c;
@@ -125,6 +126,11 @@ struct OrthoOp {
           v[2 * u] = fmaf(fo, o.x, v[2 * u]);
           v[2 * u + 1] = fmaf(fo, o.y, v[2 * u + 1]);
         }
+      }
+      if (KIND == kSquare && x == y) {  // the chunk on the diagonal: column lane of a lane's row
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (j == e.lane) v[j] += kNsShift * kSB;
       }
       uint32_t w[16];
 #pragma unroll

@@ -9,6 +9,10 @@ namespace moe {
 namespace {
 
 constexpr float kNsA = 3.4445f, kNsB = -4.7750f, kNsC = 2.0315f;
+// The polynomial is kept as B + 2.5 I, and the step is (a - 2.5) X + (B + 2.5 I) X:
+// where X nears orthogonality the diagonal of B nears b + c = -2.74, and its
+// rounding to fp16 would be as large as all others together.
+constexpr float kNsShift = 2.5f;
 constexpr float kNsEps = 1e-7f;
 // |X| <= 1 in the Frobenius norm at first and its singular values stay below
 // 1.3, so entries of X, A, B are below 1.3, 1.7, 14: times 2^10, 2^12, 2^11 they

@@ -205,7 +205,8 @@ __global__ void __launch_bounds__(kSmallThreads)
     constexpr float fs2 = kNsC * (kSB / (kSA * kSA)), fo2 = kNsB * (kSB / kSA);
     gram_pieces(A, as, sp, sp, warp, lane, [&](int i, int j, float a, float b, bool off) {
       const float2 o = __half22float2(*reinterpret_cast<const __half2*>(A + i * as + j));
-      const __half2 v = __floats2half2_rn(fmaf(fo2, o.x, fs2 * a), fmaf(fo2, o.y, fs2 * b));
+      const float di = i == j ? kNsShift * kSB : 0.f, dj = i == j + 1 ? kNsShift * kSB : 0.f;
+      const __half2 v = __floats2half2_rn(fmaf(fo2, o.x, fmaf(fs2, a, di)), fmaf(fo2, o.y, fmaf(fs2, b, dj)));
       *reinterpret_cast<__half2*>(B + i * as + j) = v;
       if (off) {
         B[j * as + i] = __low2half(v);
@@ -214,7 +215,7 @@ __global__ void __launch_bounds__(kSmallThreads)
     });
     __syncthreads();
     const bool last = step + 1 == steps;
-    const float fs = r * ((last ? 1.f : kSX) / kSB), fo = kNsA * r * (last ? 1.f : kSX);
+    const float fs = r * ((last ? 1.f : kSX) / kSB), fo = (kNsA - kNsShift) * r * (last ? 1.f : kSX);
     // a warp takes 16 columns: it reads all of theirs before it writes any
     for (int slab = warp; slab < nc / 16; slab += kSmallThreads / 32) {
       float c[8][2][4] = {};

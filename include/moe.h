@@ -424,8 +424,9 @@ int moe_balance_bwd(const moe_cfg* cfg, const float* logits, const int32_t* coun
  *   loss [T] fp32 = lse_t - z_t,target(t); 0 where target(t) < 0 (no target)
  * target [T] int32 or int64 (target_type).  A target >= V counts as none and sets
  * MOE_ERR_ARG (info: the token).  The logits are never in memory.  They are fp32
- * sums whose tensor-core runs are 512 columns long and are added up rounded to
- * nearest (so at most 2^-18 of the sum of the terms' magnitudes is lost), and
+ * sums whose tensor-core runs are 512 columns long (64 up to 128 tokens) and are
+ * added up rounded to nearest (so at most 2^-18 of the sum of the terms'
+ * magnitudes is lost), and
  * loss keeps its relative precision where a token is certain: it is not formed
  * as a difference of lse and z.  Infinite logits give NaN.
  * Limits (MOE_ERR_SHAPE): 1 <= T, V <= 2^22, d a multiple of 64 up to 65536.
@@ -447,9 +448,11 @@ int moe_xent_fwd(int T, int V, int d, const uint16_t* x, const uint16_t* W, cons
  *   dx [T, d] = D W,  dW [V, d] = D^T x
  * each fp32 or bf16 (MOE_Y_F32, MOE_Y_BF16), either NULL if not wanted.  D is
  * formed from the logits again, in pieces of the vocabulary, and enters the
- * products in bf16 (2^-8 of each value, beside the final rounding) for bf16
- * results and as the sum of three bf16 values (24 bits) for fp32 ones, whose runs of
- * sums are kept short as the logits' are.  A token whose dloss and dlse are 0 or
+ * products as the sum of three bf16 values (24 bits) for fp32 results, whose runs of
+ * sums are kept short as the logits' are, and for bf16 results as the sum of two
+ * (16 bits) up to 256 tokens and as one (2^-8 of each value, beside the final
+ * rounding) beyond; dx is then still within its own rounding where the target's
+ * term is the largest (its rows are kept in units that make that term exact).  A token whose dloss and dlse are 0 or
  * that has neither target nor dlse adds nothing, whatever x holds. */
 int moe_xent_bwd(int T, int V, int d, const uint16_t* x, const uint16_t* W, const void* target, int target_type,
                  const float* loss, const float* lse, const float* dloss, const float* dlse, void* dx, int dx_type,
@@ -463,7 +466,8 @@ int moe_xent_bwd(int T, int V, int d, const uint16_t* x, const uint16_t* W, cons
  *   A = X X^T,  X <- 3.4445 X + (-4.7750 A + 2.0315 A A) X
  * (for rows > cols the same with X^T).  Between the products X, A and the
  * polynomial are held in fp16, sums in fp32: O differs from the formula by about
- * 1.2e-3 of its norm, and its rounding to bf16 by 1.7e-3.  A matrix of zeros (an
+ * 1e-3 of its norm (up to 1.5e-3 where one side is much the longer), and its
+ * rounding to bf16 by 1.7e-3.  A matrix of zeros (an
  * expert that saw no token) gives zeros; one that holds a NaN or an Inf, or whose
  * sum of squares passes fp32's range, gives NaN everywhere; norms below 1e-10
  * lose bits.  rows, cols any from 1 to 32768 (MOE_ERR_SHAPE otherwise).  O may not

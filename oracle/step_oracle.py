@@ -122,8 +122,8 @@ def orthogonalize_spread(G, steps, unit=2.0 ** -11, eps=1e-7):
 
 
 def orthogonalize_rounded(G, steps, eps=1e-7):
-    """The same with the library's roundings: X times 2^10, A times 2^12 and the polynomial times 2^11 to fp16 after each
-    product, the result to bf16 (sums in fp64, where the library's are fp32)."""
+    """The same with the library's roundings: X times 2^10, A times 2^12 and the polynomial plus 2.5 I times 2^11 to fp16
+    after each product, the result to bf16 (sums in fp64, where the library's are fp32)."""
     def f16(v):
         return v.astype(np.float16).astype(np.float64)
 
@@ -139,7 +139,7 @@ def orthogonalize_rounded(G, steps, eps=1e-7):
     wide = X.shape[0] <= X.shape[1]
     for i in range(steps):
         A = f16((X @ X.T if wide else X.T @ X) * r * r * 4096)
-        B = f16(b * 2048 / 4096 * A + c * 2048 / 4096 ** 2 * (A @ A))
-        Y = a * r * X + r / 2048 * (B @ X if wide else X @ B)
+        B = f16(b * 2048 / 4096 * A + c * 2048 / 4096 ** 2 * (A @ A) + 2.5 * 2048 * np.eye(len(A)))
+        Y = (a - 2.5) * r * X + r / 2048 * (B @ X if wide else X @ B)
         X, r = (bf16(Y), 1.0) if i == steps - 1 else (f16(Y * 1024), 1.0 / 1024)
     return X
