@@ -182,7 +182,12 @@ int check_ortho(int mats, int rows, int cols) {
   constexpr int kMax = 32768;
   if (mats < 1 || mats > 65536 || rows < 1 || rows > kMax || cols < 1 || cols > kMax) return MOE_ERR_SHAPE;
   // tiles of one launch
-  return static_cast<long long>(mats) * ceil_div(rows, kBM) * ceil_div(cols, kBM) < (1ll << 30) ? MOE_OK : MOE_ERR_SHAPE;
+  return static_cast<long long>(mats) * ceil_div(rows, kBM) * ceil_div(cols, 64) < (1ll << 30) ? MOE_OK : MOE_ERR_SHAPE;
+}
+// Two arrays of a call that may not share memory.
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + nb && y < x + na;
 }
 // Sequences of the balance loss: all of one length.
 int check_seqs(const moe_cfg& c, int seqs) { return seqs < 1 || c.T % seqs ? MOE_ERR_SHAPE : MOE_OK; }
@@ -693,6 +698,12 @@ int moe_xent_bwd(int T, int V, int d, const uint16_t* x, const uint16_t* W, cons
   if ((target_type != MOE_I32 && target_type != MOE_I64) || (!dx && !dW)) return MOE_ERR_ARG;
   if ((dx && !y_type_ok(dx_type)) || (dW && !y_type_ok(dW_type))) return MOE_ERR_ARG;
   MOE_TRY(check_ptrs({x, W, target, loss, lse, dloss}, {dlse, dx, dW}, ws));
+  // x and W are read for every piece of the vocabulary, after the first results are written
+  const size_t nx = static_cast<size_t>(T) * d, nw = static_cast<size_t>(V) * d;
+  const size_t bx = nx * (dx_type == MOE_Y_F32 ? 4 : 2), bw = nw * (dW_type == MOE_Y_F32 ? 4 : 2);
+  if (overlap(dx, bx, x, 2 * nx) || overlap(dx, bx, W, 2 * nw) || overlap(dW, bw, x, 2 * nx) || overlap(dW, bw, W, 2 * nw) ||
+      overlap(dx, bx, dW, bw))
+    return MOE_ERR_ARG;
   XentArgs a{T, V, d, x, W, target, target_type, const_cast<float*>(loss), const_cast<float*>(lse), dloss, dlse, dx, dW,
              dx_type, dW_type, ws, g_grid_limit};
   return launch_xent_bwd(a, static_cast<cudaStream_t>(stream));
@@ -710,7 +721,8 @@ int moe_orthogonalize(int mats, int rows, int cols, const void* G, int g_type, u
   if (steps < 1 || steps > MOE_ORTHOGONALIZE_MAX_STEPS) return MOE_ERR_SHAPE;
   if (!y_type_ok(g_type)) return MOE_ERR_ARG;
   MOE_TRY(check_ptrs({G, O}, {}, ws));
-  if (static_cast<const void*>(O) == G) return MOE_ERR_ARG;
+  const size_t n = static_cast<size_t>(mats) * rows * cols;
+  if (overlap(O, 2 * n, G, n * (g_type == MOE_Y_F32 ? 4 : 2))) return MOE_ERR_ARG;
   return launch_ortho(OrthoArgs{mats, rows, cols, G, g_type, O, steps, ws, g_grid_limit},
                       static_cast<cudaStream_t>(stream));
 }

@@ -36,10 +36,11 @@ constexpr int kThreads = 512, kBwdThreads = 256;
 constexpr int kUnits = 152 * 2;
 
 // Blocks of a sequence: at least 32 tokens each, so that all blocks' sums fit in
-// the E ceil(T / 32) words of the histogram regions of the workspace.
+// the E ceil(T / 32) words of the histogram regions of the workspace, and 4096 at
+// most or not much more, so that fp32 sums stay short.
 int seq_parts(int T, int B) {
   const int L = T / B;
-  const long long each = std::max<long long>(32, ceil_div(T, kUnits));
+  const long long each = std::clamp<long long>(ceil_div(T, kUnits), 32, 4096);
   return static_cast<int>(std::max(1ll, L / each));
 }
 

@@ -15,7 +15,8 @@
 // additions cut off what a sum has no room for, and an operation whose results
 // are kept in fp32 keeps those runs short (the other accumulator fills
 // meanwhile, so this costs the tensor core nothing).  An operation whose
-// results are rounded to 16 bits takes one run.
+// results are rounded to 16 bits takes one run, and may have its sums 32 columns
+// at a time (CHUNKS), which leaves it registers for what it reads beside them.
 //
 // Matrices are seen by TMA as [matrix][row][column] with the exact number of
 // rows, so tiles that reach past an end read zeros and their stores are cut:
@@ -50,7 +51,7 @@ struct DenseParams {
   CUtensorMap tmA, tmB;  // operands
   CUtensorMap tmT;       // a symmetric operand's MN-major view (see dense_flip)
   int M, N;              // rows and columns of C
-  int mt, nt;            // tiles of its rows (of TILE_M) and columns (of tn)
+  int mt, nt;            // tiles of its rows (128 for each CTA) and columns (of tn)
   int tn;                // columns of a tile: 256, on single CTAs also fewer (a multiple of 16)
   int half;              // columns of a tile that the first half of the epilogue's warps takes, a multiple of 32
   int a_bytes, b_bytes;  // of A and B in one CTA's part of a stage
@@ -393,6 +394,44 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_kernel(const __grid_co
       const DenseTile t = walk.next(p, i);
       const bool active = t.m0 + 32 * e.q < p.M;
       const auto pre = Op::pre(p, t, e);
+      auto release = [&](int buf) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (CG == 2 && rank == 1)
+            mbar_arrive_rank(&ss.tempty[buf], 0);
+          else
+            mbar_arrive(&ss.tempty[buf]);
+        }
+      };
+      if constexpr (Op::CHUNKS) {
+        // one run: 32 columns at a time, the next ones on their way meanwhile
+        if (t.kb1 == t.kb0) continue;
+        const int buf = it & 1;
+        if (!mbar_wait_inline(&ss.tfull[buf], (it >> 1) & 1, abort, p.err, where(4, i))) break;
+        ++it;
+        tc_fence_after();
+        const uint32_t ta = tmem + (static_cast<uint32_t>(e.q * 32) << 16) + buf * kBN + e.part * p.half;
+        const int chunks = active ? (dense_width(p, t, e) + 31) / 32 : 0;
+        uint32_t v[2][32];
+        if (chunks > 0) {
+          tmem_ld_32x32(ta, v[0]);
+          tmem_ld_wait();
+        } else {
+          release(buf);
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (c >= chunks) break;
+          if (c + 1 < chunks)
+            tmem_ld_32x32(ta + 32 * (c + 1), v[(c + 1) & 1]);
+          else
+            release(buf);
+          Op::chunk(p, t, e, pre, c, v[c & 1]);
+          if (c + 1 < chunks) tmem_ld_wait();
+        }
+        continue;
+      }
       uint32_t acc[4][32];
       const int runs = (t.kb1 - t.kb0 + p.run_kb - 1) / p.run_kb;
       if (runs == 0) {
@@ -432,16 +471,10 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_kernel(const __grid_co
                 acc[c + h][j] = __float_as_uint(__uint_as_float(acc[c + h][j]) + __uint_as_float(v[h][j]));
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if (CG == 2 && rank == 1)
-            mbar_arrive_rank(&ss.tempty[buf], 0);
-          else
-            mbar_arrive(&ss.tempty[buf]);
-        }
+        release(buf);
       }
-      if (ok && active) Op::epilogue(p, t, e, pre, acc);
+      if constexpr (!Op::CHUNKS)
+        if (ok && active) Op::epilogue(p, t, e, pre, acc);
     }
   }
 

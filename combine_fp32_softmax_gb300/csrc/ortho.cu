@@ -7,12 +7,12 @@
 // always the smaller of the two and nothing is transposed in memory.
 //
 // X, A and B are kept in fp16 between the products, scaled by powers of two so
-// that their whole range is normal numbers: a rounding is at most 2^-11 of a value, eight
-// times finer than bf16's at the same tensor-core rate.  Five steps multiply
-// what is rounded away of a small singular value by 485 as they do the value,
-// and with bf16 the result would be off by six times its own final rounding; with
-// fp16 by less than that rounding.  The norm itself enters as an fp32 factor of
-// the first step, so a bf16 G is taken exactly.
+// that their whole range is normal numbers: a rounding is at most 2^-11 of a value,
+// eight times finer than bf16's at the same tensor-core rate.  Beside X there are 8
+// bits of what its rounding leaves, for the a X of a step, and B's diagonal is
+// shifted in the last steps (ortho.cuh says why and what that measured): the result
+// is then off by less than its own final rounding to bf16.  The norm itself enters
+// as an fp32 factor of the first step, so a bf16 G is taken exactly.
 //
 // A and A A are symmetric: only the tiles on and above the diagonal are computed.
 // Where the products run on CTA pairs only those are stored, and the products that
@@ -41,7 +41,7 @@ struct OrthoOp {
   static constexpr bool SYM = KIND == kGramWide || KIND == kGramTall || KIND == kSquare;
   static constexpr bool A_MN = KIND == kGramTall;
   static constexpr bool B_MN = KIND == kGramTall || KIND == kUpdateWide;
-  static constexpr bool F16 = true, ONE = false;
+  static constexpr bool F16 = true, ONE = false, CHUNKS = true;
   // which operands are symmetric matrices
   static constexpr bool FLIP_A = KIND == kSquare || KIND == kUpdateWide, FLIP_B = KIND == kSquare || KIND == kUpdateTall;
   struct Params : DenseParams {
@@ -49,6 +49,9 @@ struct OrthoOp {
     int first;           // the first step
     const __half* old;   // square: A; update: X, laid out as the result
     int pitch;           // of old
+    uint8_t* lo;         // update: what rounding left of X, laid out as old; that of the result takes its place
+    int lo_in, lo_out;   // whether it is there and wanted
+    float shift;         // square, update: the polynomial is kept plus so many I
     void* out;           // [mats][M] rows
     int out_pitch;       // of out, a multiple of 16
     int bf16;            // last update: bf16 results
@@ -81,6 +84,7 @@ struct OrthoOp {
   struct Pre {
     float r;
     uint32_t old[SYM && KIND != kSquare ? 1 : 64];
+    uint32_t lo[SYM ? 1 : 32];
   };
   static __device__ __forceinline__ Pre pre(const Params& p, const DenseTile& t, const DenseEpi& e) {
     Pre o;
@@ -91,76 +95,103 @@ struct OrthoOp {
       const __half* from = p.old + (static_cast<size_t>(t.mat) * p.M + row) * p.pitch + x;
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        if (row < p.M && 16 * u < w && t.kb1 > t.kb0) {
+        if (row < p.M && 16 * u < w) {
           ld_32(from + 16 * u, &o.old[8 * u]);
         } else {
 #pragma unroll
           for (int k = 0; k < 8; ++k) o.old[8 * u + k] = 0u;
         }
       }
+      if constexpr (!SYM) {
+        const uint8_t* lo = p.lo + (static_cast<size_t>(t.mat) * p.M + row) * p.pitch + x;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (p.lo_in && row < p.M && 32 * c < w) {
+            ld_32(lo + 32 * c, &o.lo[8 * c]);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o.lo[8 * c + k] = 0u;
+          }
+        }
+      }
     }
     return o;
   }
-  static __device__ __forceinline__ void epilogue(const Params& p, const DenseTile& t, DenseEpi& e, const Pre& pre,
-                                                  uint32_t (&acc)[4][32]) {
+  static __device__ __forceinline__ void chunk(const Params& p, const DenseTile& t, const DenseEpi& e, const Pre& pre, int c,
+                                               const uint32_t (&acc)[32]) {
     if (pre.r == 0.f) return;  // no products for this matrix
     const float r = p.first ? pre.r : 1.f / kSX;
-    const int x0 = dense_col(p, t, e), x1 = x0 + dense_width(p, t, e), y = t.m0 + 32 * e.q;
-    // gram: A = r^2 sums; square: B + 2.5 I = b A + c sums + 2.5 I; update: X' =
-    // (a - 2.5) r X + r sums
+    const int x = dense_col(p, t, e) + 32 * c, y = t.m0 + 32 * e.q;
+    // gram: A = r^2 sums; square: B + s I = b A + c sums + s I; update: X' =
+    // (a - s) r X + r sums
     const float fs = KIND == kSquare                         ? kNsC * (kSB / (kSA * kSA))
                      : (KIND == kGramWide || KIND == kGramTall) ? r * r * kSA
                                                              : r * ((p.bf16 ? 1.f : kSX) / kSB);
-    const float fo = KIND == kSquare ? kNsB * (kSB / kSA) : (kNsA - kNsShift) * r * (p.bf16 ? 1.f : kSX);
+    const float fo = KIND == kSquare ? kNsB * (kSB / kSA) : (kNsA - p.shift) * r * (p.bf16 ? 1.f : kSX);
+    float v[32];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int x = x0 + 32 * c;
-      if (x >= x1) break;
-      float v[32];
+    for (int j = 0; j < 32; ++j) v[j] = fs * __uint_as_float(acc[j]);
+    if constexpr (KIND == kSquare || !SYM) {
 #pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = fs * __uint_as_float(acc[c][j]);
-      if constexpr (KIND == kSquare || !SYM) {
+      for (int u = 0; u < 16; ++u) {
+        const float2 o = unpack_f16(pre.old[16 * c + u]);
+        v[2 * u] = fmaf(fo, o.x, v[2 * u]);
+        v[2 * u + 1] = fmaf(fo, o.y, v[2 * u + 1]);
+      }
+    }
+    if constexpr (!SYM) {
+      if (p.lo_in) {
+        const float fl = fo * (1.f / kLo);
 #pragma unroll
         for (int u = 0; u < 16; ++u) {
-          const float2 o = unpack_f16(pre.old[16 * c + u]);
-          v[2 * u] = fmaf(fo, o.x, v[2 * u]);
-          v[2 * u + 1] = fmaf(fo, o.y, v[2 * u + 1]);
+          const float2 o = unpack_e4m3(pre.lo[8 * c + u / 2] >> (16 * (u & 1)));
+          v[2 * u] = fmaf(fl, o.x, v[2 * u]);
+          v[2 * u + 1] = fmaf(fl, o.y, v[2 * u + 1]);
         }
       }
-      if (KIND == kSquare && x == y) {  // the chunk on the diagonal: column lane of a lane's row
+    }
+    if (KIND == kSquare && x == y) {  // the chunk on the diagonal: column lane of a lane's row
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (j == e.lane) v[j] += kNsShift * kSB;
+      for (int j = 0; j < 32; ++j)
+        if (j == e.lane) v[j] += p.shift * kSB;
+    }
+    uint32_t w[16];
+#pragma unroll
+    for (int u = 0; u < 16; ++u)
+      w[u] = !SYM && p.bf16 ? pack_bf16(v[2 * u], v[2 * u + 1]) : pack_f16(v[2 * u], v[2 * u + 1]);
+    uint16_t* mat = static_cast<uint16_t*>(p.out) + static_cast<size_t>(t.mat) * p.M * p.out_pitch;
+    if (y + e.lane < p.M) {
+      uint16_t* to = mat + static_cast<size_t>(y + e.lane) * p.out_pitch + x;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)  // columns between the last and the pitch may hold anything
+        if (x + 16 * h < p.out_pitch) {
+          if (!SYM && p.apart)
+            st_2x16(to + 16 * h, w + 8 * h);
+          else
+            st_32(to + 16 * h, w + 8 * h);
+        }
+      if constexpr (!SYM) {
+        if (p.lo_out) {
+          uint32_t l[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            l[u] = rest_e4m3(v[4 * u], v[4 * u + 1], w[2 * u]) | rest_e4m3(v[4 * u + 2], v[4 * u + 3], w[2 * u + 1]) << 16;
+          st_32(p.lo + (static_cast<size_t>(t.mat) * p.M + y + e.lane) * p.pitch + x, l);
+        }
       }
-      uint32_t w[16];
+    }
+    if constexpr (SYM) {
+      if (!p.upper && t.n0 / p.tn > t.m0 / p.tn) {  // a tile off the diagonal: also to the other side
+        // neighbouring lanes' rows side by side: even lanes take the even columns,
+        // odd ones the odd, and a store covers 32 rows of two columns
+        const bool odd = e.lane & 1;
+        uint16_t* to = mat + static_cast<size_t>(x + odd) * p.out_pitch + y + (e.lane & ~1);
 #pragma unroll
-      for (int u = 0; u < 16; ++u)
-        w[u] = !SYM && p.bf16 ? pack_bf16(v[2 * u], v[2 * u + 1]) : pack_f16(v[2 * u], v[2 * u + 1]);
-      uint16_t* mat = static_cast<uint16_t*>(p.out) + static_cast<size_t>(t.mat) * p.M * p.out_pitch;
-      if (y + e.lane < p.M) {
-        uint16_t* to = mat + static_cast<size_t>(y + e.lane) * p.out_pitch + x;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)  // columns between the last and the pitch may hold anything
-          if (x + 16 * h < p.out_pitch) {
-            if (!SYM && p.apart)
-              st_2x16(to + 16 * h, w + 8 * h);
-            else
-              st_32(to + 16 * h, w + 8 * h);
-          }
-      }
-      if constexpr (SYM) {
-        if (!p.upper && t.n0 / p.tn > t.m0 / p.tn) {  // a tile off the diagonal: also to the other side
-          // neighbouring lanes' rows side by side: even lanes take the even columns,
-          // odd ones the odd, and a store covers 32 rows of two columns
-          const bool odd = e.lane & 1;
-          uint16_t* to = mat + static_cast<size_t>(x + odd) * p.out_pitch + y + (e.lane & ~1);
-#pragma unroll
-          for (int u = 0; u < 16; ++u) {
-            const uint32_t other = __shfl_xor_sync(0xffffffffu, w[u], 1);
-            const uint32_t both = odd ? __byte_perm(other, w[u], 0x7632) : __byte_perm(w[u], other, 0x5410);
-            if (x + 2 * u + odd < p.N)  // rows past the last one end before the pitch
-              *reinterpret_cast<uint32_t*>(to + static_cast<size_t>(2 * u) * p.out_pitch) = both;
-          }
+        for (int u = 0; u < 16; ++u) {
+          const uint32_t other = __shfl_xor_sync(0xffffffffu, w[u], 1);
+          const uint32_t both = odd ? __byte_perm(other, w[u], 0x7632) : __byte_perm(w[u], other, 0x5410);
+          if (x + 2 * u + odd < p.N)  // rows past the last one end before the pitch
+            *reinterpret_cast<uint32_t*>(to + static_cast<size_t>(2 * u) * p.out_pitch) = both;
         }
       }
     }
@@ -236,7 +267,7 @@ __global__ void __launch_bounds__(256) ortho_norm_kernel(const void* __restrict_
 template <bool BF16>
 __global__ void __launch_bounds__(256)
     ortho_cast_kernel(const void* __restrict__ G, int rows, int cols, int pitch, int mats, const double* __restrict__ sums,
-                      int steps, float* __restrict__ scal, __half* __restrict__ X, uint16_t* __restrict__ O) {
+                      int steps, float* __restrict__ scal, __half* __restrict__ X, uint8_t* __restrict__ rest, uint16_t* __restrict__ O) {
   griddep_wait();
   griddep_launch_dependents();
   __shared__ float shared_norm;
@@ -274,6 +305,7 @@ __global__ void __launch_bounds__(256)
     if (blockIdx.x == 0 && threadIdx.x == 0) scal[mat] = ldexpf(inv, -k);
     const float up = ldexpf(1.f, k);  // the norm is between 2^-41 and 2^64 here: 2^k is a normal number
     __half* Xm = X + static_cast<size_t>(mat) * rows * pitch;
+    uint8_t* Lm = rest + static_cast<size_t>(mat) * rows * pitch;  // a bf16 G is fp16 exactly
     constexpr int VE = BF16 ? 8 : 4;
     if (cols % VE == 0) {  // whole 16-byte pieces of G in a row: one place for each
       const uint32_t v0 = static_cast<uint32_t>((lo - at + VE - 1) / VE), v1 = static_cast<uint32_t>((hi - at + VE - 1) / VE);
@@ -288,14 +320,21 @@ __global__ void __launch_bounds__(256)
               make_uint4(pack_f16(up * bf16_lo(w.x), up * bf16_hi(w.x)), pack_f16(up * bf16_lo(w.y), up * bf16_hi(w.y)),
                          pack_f16(up * bf16_lo(w.z), up * bf16_hi(w.z)), pack_f16(up * bf16_lo(w.w), up * bf16_hi(w.w)));
         } else {
-          *reinterpret_cast<uint2*>(to) = make_uint2(pack_f16(up * __uint_as_float(w.x), up * __uint_as_float(w.y)),
-                                                     pack_f16(up * __uint_as_float(w.z), up * __uint_as_float(w.w)));
+          const float x0 = up * __uint_as_float(w.x), x1 = up * __uint_as_float(w.y);
+          const float x2 = up * __uint_as_float(w.z), x3 = up * __uint_as_float(w.w);
+          const uint32_t h0 = pack_f16(x0, x1), h1 = pack_f16(x2, x3);
+          *reinterpret_cast<uint2*>(to) = make_uint2(h0, h1);
+          *reinterpret_cast<uint32_t*>(Lm + (to - Xm)) = rest_e4m3(x0, x1, h0) | rest_e4m3(x2, x3, h1) << 16;
         }
       }
     } else {
       auto put = [&](size_t i, float v) {
         const uint32_t j = static_cast<uint32_t>(i - at), row = j / cols;
-        Xm[static_cast<size_t>(row) * pitch + (j - row * cols)] = __float2half_rn(up * v);
+        const size_t to = static_cast<size_t>(row) * pitch + (j - row * cols);
+        const float x = up * v;
+        const uint32_t h = pack_f16(x, 0.f);
+        reinterpret_cast<uint16_t*>(Xm)[to] = static_cast<uint16_t>(h);
+        if constexpr (!BF16) Lm[to] = static_cast<uint8_t>(rest_e4m3(x, 0.f, h));
       };
       for_elements<decltype(put), BF16>(G, lo, hi, threadIdx.x, 256, put);
     }
@@ -319,7 +358,7 @@ __global__ void __launch_bounds__(256) ortho_rows_kernel(const uint16_t* __restr
 // ------------------------------------------------------------------ host
 struct Plan {
   int small, pitch, spitch, parts;
-  size_t err, sums, scal, X[2], A, B, total;
+  size_t err, sums, scal, X[2], lo, A, B, total;
 };
 Plan plan(int mats, int rows, int cols) {
   Plan p{};
@@ -340,6 +379,7 @@ Plan plan(int mats, int rows, int cols) {
   p.sums = take(sizeof(double) * p.parts * mats);
   p.scal = take(sizeof(float) * mats);
   for (int i = 0; i < 2; ++i) p.X[i] = take(size_t(2) * mats * rows * p.pitch);
+  p.lo = take(size_t(1) * mats * rows * p.pitch);
   p.A = take(size_t(2) * mats * p.small * p.spitch);
   p.B = take(size_t(2) * mats * p.small * p.spitch);
   p.total = o;
@@ -358,6 +398,7 @@ int launch_ortho(const OrthoArgs& a, cudaStream_t s) {
   double* sums = reinterpret_cast<double*>(ws + L.sums);
   float* scal = reinterpret_cast<float*>(ws + L.scal);
   __half* X[2] = {reinterpret_cast<__half*>(ws + L.X[0]), reinterpret_cast<__half*>(ws + L.X[1])};
+  uint8_t* lo = ws + L.lo;
   __half* A = reinterpret_cast<__half*>(ws + L.A);
   __half* B = reinterpret_cast<__half*>(ws + L.B);
   const bool bf = a.g_type == MOE_Y_BF16, wide = a.rows <= a.cols;
@@ -369,9 +410,9 @@ int launch_ortho(const OrthoArgs& a, cudaStream_t s) {
                        : launch_pdl(ortho_norm_kernel<false>, grid, dim3(256), 0, s, a.G, n, a.mats, sums);
     if (e == cudaSuccess)
       e = bf ? launch_pdl(ortho_cast_kernel<true>, grid, dim3(256), 0, s, a.G, a.rows, a.cols, L.pitch, a.mats, sums, a.steps,
-                          scal, X[0], a.O)
+                          scal, X[0], lo, a.O)
              : launch_pdl(ortho_cast_kernel<false>, grid, dim3(256), 0, s, a.G, a.rows, a.cols, L.pitch, a.mats, sums,
-                          a.steps, scal, X[0], a.O);
+                          a.steps, scal, X[0], lo, a.O);
     if (e != cudaSuccess) return MOE_ERR_CUDA;
   }
   const int m = L.small;
@@ -394,6 +435,7 @@ int launch_ortho(const OrthoArgs& a, cudaStream_t s) {
     const __half* Xi = X[it & 1];
     __half* Xo = X[(it + 1) & 1];
     const bool last = it + 1 == a.steps;
+    const float shift = it >= a.steps - kShiftSteps ? kNsShift : 0.f;
     auto gram = [&](auto& p) {
       std::memset(&p, 0, sizeof(p));
       base(p, 0, m, m, wide ? a.cols : a.rows);
@@ -428,6 +470,7 @@ int launch_ortho(const OrthoArgs& a, cudaStream_t s) {
       p.scal = scal;
       p.upper = upper;
       p.old = A;
+      p.shift = shift;
       p.pitch = L.spitch;
       if (!dense_map_k(&p.tmA, A, true, m, m, a.mats, L.spitch, 128) ||
           !dense_map_k(&p.tmB, A, true, m, m, a.mats, L.spitch, p.b_bytes / 128) ||
@@ -445,6 +488,10 @@ int launch_ortho(const OrthoArgs& a, cudaStream_t s) {
       p.first = it == 0;
       p.upper = upper;
       p.old = Xi;
+      p.lo = lo;
+      p.lo_in = !last && (it > 0 || !bf);  // a bf16 G is fp16 exactly
+      p.lo_out = it + 2 < a.steps;
+      p.shift = shift;
       p.pitch = L.pitch;
       p.bf16 = last;
       p.out = last && !copy ? a.O : reinterpret_cast<uint16_t*>(Xo);

@@ -73,7 +73,7 @@ struct SmallShape {
   int C;       // CTAs of a cluster
 };
 int small_smem(int sp, int nc) {
-  return 256 + 2 * sp * half_stride(nc) + 2 * 2 * sp * half_stride(sp) + 4 * sp * sum_stride(sp);
+  return 256 + 2 * sp * half_stride(nc) + 2 * 2 * sp * half_stride(sp) + 4 * sp * sum_stride(sp) + sp * nc;
 }
 
 // C = M . M^T (16 x 16 pieces on and above the diagonal, spread over the warps) for
@@ -118,6 +118,7 @@ __global__ void __launch_bounds__(kSmallThreads)
   __half* A = X + sp * xs;
   __half* B = A + sp * as;
   float* P = reinterpret_cast<float*>(B + sp * as);
+  uint8_t* lo = reinterpret_cast<uint8_t*>(P + sp * ps);  // what rounding left of X
   __shared__ double wsum[kSmallThreads / 32];
   const size_t base = static_cast<size_t>(blockIdx.x / C) * rows * cols;
   const bool wide = rows <= cols;
@@ -153,6 +154,7 @@ __global__ void __launch_bounds__(kSmallThreads)
   for (int off = 16; off; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
   if (lane == 0) wsum[warp] = d;
   for (int i = tid; i < sp * xs / 2; i += kSmallThreads) reinterpret_cast<uint32_t*>(X)[i] = 0u;  // padding too
+  for (int i = tid; i < sp * nc / 4; i += kSmallThreads) reinterpret_cast<uint32_t*>(lo)[i] = 0u;
   __syncthreads();
   if (tid < C) {
     d = 0.;
@@ -174,11 +176,17 @@ __global__ void __launch_bounds__(kSmallThreads)
   int ex;
   frexpf(norm, &ex);
   const float up = ldexpf(1.f, kSXLog2 - ex);
-  each([&](int i, int j) { X[i * xs + j - c0] = __float2half_rn(up * load(at(i, j))); });
+  each([&](int i, int j) {
+    const float x = up * load(at(i, j));
+    const uint32_t h = pack_f16(x, 0.f);
+    reinterpret_cast<uint16_t*>(X)[i * xs + j - c0] = static_cast<uint16_t>(h);
+    lo[i * nc + j - c0] = static_cast<uint8_t>(rest_e4m3(x, 0.f, h));
+  });
   __syncthreads();
 
   for (int step = 0; step < steps; ++step) {
     const float r = step == 0 ? ldexpf(inv, ex - kSXLog2) : 1.f / kSX;
+    const float shift = step >= steps - kShiftSteps ? kNsShift : 0.f;
     gram_pieces(X, xs, sp, nc, warp, lane, [&](int i, int j, float a, float b, bool off) {
       *reinterpret_cast<float2*>(P + i * ps + j) = make_float2(a, b);
       if (off) {
@@ -205,7 +213,7 @@ __global__ void __launch_bounds__(kSmallThreads)
     constexpr float fs2 = kNsC * (kSB / (kSA * kSA)), fo2 = kNsB * (kSB / kSA);
     gram_pieces(A, as, sp, sp, warp, lane, [&](int i, int j, float a, float b, bool off) {
       const float2 o = __half22float2(*reinterpret_cast<const __half2*>(A + i * as + j));
-      const float di = i == j ? kNsShift * kSB : 0.f, dj = i == j + 1 ? kNsShift * kSB : 0.f;
+      const float di = i == j ? shift * kSB : 0.f, dj = i == j + 1 ? shift * kSB : 0.f;
       const __half2 v = __floats2half2_rn(fmaf(fo2, o.x, fmaf(fs2, a, di)), fmaf(fo2, o.y, fmaf(fs2, b, dj)));
       *reinterpret_cast<__half2*>(B + i * as + j) = v;
       if (off) {
@@ -215,7 +223,7 @@ __global__ void __launch_bounds__(kSmallThreads)
     });
     __syncthreads();
     const bool last = step + 1 == steps;
-    const float fs = r * ((last ? 1.f : kSX) / kSB), fo = (kNsA - kNsShift) * r * (last ? 1.f : kSX);
+    const float fs = r * ((last ? 1.f : kSX) / kSB), fo = (kNsA - shift) * r * (last ? 1.f : kSX);
     // a warp takes 16 columns: it reads all of theirs before it writes any
     for (int slab = warp; slab < nc / 16; slab += kSmallThreads / 32) {
       float c[8][2][4] = {};
@@ -241,10 +249,18 @@ __global__ void __launch_bounds__(kSmallThreads)
             for (int v = 0; v < 2; ++v) {
               const int i = 16 * mi + (lane >> 2) + 8 * v, j = 16 * slab + 8 * h + 2 * (lane & 3);
               __half2* x = reinterpret_cast<__half2*>(X + i * xs + j);
-              const float2 o = __half22float2(*x);
+              float2 o = __half22float2(*x);
+              uint16_t* l = reinterpret_cast<uint16_t*>(lo + i * nc + j);
+              if (!last) {
+                const float2 more = unpack_e4m3(*l);
+                o.x = fmaf(1.f / kLo, more.x, o.x);
+                o.y = fmaf(1.f / kLo, more.y, o.y);
+              }
               const float y0 = fmaf(fo, o.x, fs * c[mi][h][2 * v]), y1 = fmaf(fo, o.y, fs * c[mi][h][2 * v + 1]);
               if (!last) {
-                *x = __floats2half2_rn(y0, y1);
+                const uint32_t h = pack_f16(y0, y1);
+                *reinterpret_cast<uint32_t*>(x) = h;
+                *l = static_cast<uint16_t>(rest_e4m3(y0, y1, h));
               } else if (i < sh.s) {
                 const uint32_t w = pack_bf16(y0, y1);
                 if (c0 + j < c1) O[at(i, c0 + j)] = static_cast<uint16_t>(w);

@@ -11,8 +11,10 @@
 // token's small loss does not come out of the difference of two large numbers.
 //
 // The backward takes the vocabulary in pieces: the product again, with an
-// epilogue that turns logits into D (bf16, or the sum of three bf16 values where a
-// gradient is kept in fp32), then the two products that read D.
+// epilogue that turns logits into D (one to three bf16 values, see terms_of), then
+// the two products that read D.  A piece's D takes 512 MB at most unless there are
+// more than 32,768 tokens; what it costs in memory traffic hides behind the
+// products.
 #include <algorithm>
 #include <cstring>
 
@@ -64,7 +66,7 @@ __device__ __forceinline__ DenseTile rows_first(const DenseParams& p, int i, int
 
 // ------------------------------------------------------------- forward
 struct StatsOp {
-  static constexpr bool A_MN = false, B_MN = false, F16 = false, ONE = true, FLIP_A = false, FLIP_B = false;
+  static constexpr bool A_MN = false, B_MN = false, F16 = false, ONE = true, FLIP_A = false, FLIP_B = false, CHUNKS = false;
   struct Params : DenseParams {
     Target target;
     float2* part;  // [T][2 nt]: maximum and sum of exp of half a tile's logits
@@ -205,7 +207,7 @@ __device__ __forceinline__ float row_unit(float at) {
 }
 
 struct GradOp {
-  static constexpr bool A_MN = false, B_MN = false, F16 = false, ONE = true, FLIP_A = false, FLIP_B = false;
+  static constexpr bool A_MN = false, B_MN = false, F16 = false, ONE = true, FLIP_A = false, FLIP_B = false, CHUNKS = false;
   struct Params : DenseParams {
     RowGrads rows;
     const float* lse;
@@ -291,14 +293,14 @@ struct GradOp {
 // D^T, B = x, K runs over the tokens, likewise.
 template <bool DX>
 struct ProdOp {
-  static constexpr bool A_MN = !DX, B_MN = true, F16 = false, ONE = true, FLIP_A = false, FLIP_B = false;
+  static constexpr bool A_MN = !DX, B_MN = true, F16 = false, ONE = true, FLIP_A = false, FLIP_B = false, CHUNKS = false;
   struct Params : DenseParams {
     int v0;           // DX: the piece's first column of the vocabulary
     int once;         // K blocks of one of D's bf16 terms
     int cols;         // columns of the piece: from one term of D to the next
     int per_split;    // K blocks of a split; each has a matrix of its own in out
-    RowGrads rows;      // DX
-    int unit;           // DX: rows of D are kept divided by row_unit
+    RowGrads rows;    // DX
+    int unit;         // DX: rows of D are kept divided by row_unit
     const float* prev;  // added to the products, laid out as out is in fp32
     void* out;        // [splits][M][N]
     int bf16;         // type of out

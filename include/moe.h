@@ -396,16 +396,18 @@ int moe_q4_dequantize(const uint8_t* codes, const uint16_t* scales, uint16_t* W,
  * do not count, whatever their logits and picks hold.  Over the n tokens of a
  * sequence that count:
  *   counts [seqs, E]   c_e = picks of expert e (exact)
- *   mean_p [seqs, E]   P_e = mean of p_te, p as moe_route computes it
+ *   mean_p [seqs, E]   P_e = mean of p_te, the softmax in fp32
  *   loss   [seqs]      E / (k n) * sum_e c_e P_e   (1 for an even spread)
  *   zloss  [seqs]      mean of lse_t^2, lse_t = log sum_e exp(logits_te)
- * (all 0 where n = 0).  Sums over tokens are fp64 beyond a block's.  cfg and ws
- * are the layer's; ws lends its histogram and partial-dot scratch, so the calls
- * may stand anywhere between and after moe_layer_fwd and moe_layer_bwd.  d_model,
- * d_ff, n_shared and renorm do not matter.  A non-finite logit of a token that
- * counts sets MOE_ERR_NONFINITE (its sequence's mean_p, loss and zloss are then
- * unspecified and its gradient 0), a pick outside [0, E) MOE_ERR_ARG (it is not
- * counted).  MOE_ERR_SHAPE unless seqs >= 1 divides T. */
+ * (all 0 where n = 0).  Sums are fp32 over a block's tokens, and over the blocks
+ * fp32 with the roundings kept; p is off by at most 2^-21 + |z - max| 2^-23 of
+ * itself.  cfg and ws are the layer's (ws cleared once with moe_ws_init); ws lends
+ * its histogram and partial-dot scratch, which nothing keeps from one call to the
+ * next, so the calls may stand anywhere beside moe_layer_fwd and moe_layer_bwd on
+ * their stream.  d_model, d_ff, n_shared and renorm do not matter.  A non-finite
+ * logit of a token that counts sets MOE_ERR_NONFINITE (its sequence's mean_p, loss
+ * and zloss are then unspecified and its gradient 0), a pick outside [0, E)
+ * MOE_ERR_ARG (it is not counted).  MOE_ERR_SHAPE unless seqs >= 1 divides T. */
 int moe_balance_fwd(const moe_cfg* cfg, const float* logits, const int32_t* topk_idx, const uint8_t* mask, int seqs,
                     int32_t* counts, float* mean_p, float* loss, float* zloss, void* ws, void* stream);
 /* Its gradient for the logits, dloss and dzloss [seqs] being those of loss and
@@ -425,10 +427,9 @@ int moe_balance_bwd(const moe_cfg* cfg, const float* logits, const int32_t* coun
  * target [T] int32 or int64 (target_type).  A target >= V counts as none and sets
  * MOE_ERR_ARG (info: the token).  The logits are never in memory.  They are fp32
  * sums whose tensor-core runs are 512 columns long (64 up to 128 tokens) and are
- * added up rounded to nearest (so at most 2^-18 of the sum of the terms'
- * magnitudes is lost), and
- * loss keeps its relative precision where a token is certain: it is not formed
- * as a difference of lse and z.  Infinite logits give NaN.
+ * added up rounded to nearest, so that at most 2^-18 of the sum of the terms'
+ * magnitudes is lost, and loss keeps its relative precision where a token is
+ * certain: it is not formed as a difference of lse and z.  Infinite logits give NaN.
  * Limits (MOE_ERR_SHAPE): 1 <= T, V <= 2^22, d a multiple of 64 up to 65536.
  * Workspace: moe_xent_workspace_bytes (0 outside the limits; backward = 0: only
  * for the forward), its first bytes cleared once with moe_xent_ws_init; it keeps
@@ -446,14 +447,16 @@ int moe_xent_fwd(int T, int V, int d, const uint16_t* x, const uint16_t* W, cons
  *   D_tv = (g_t + dlse_t) exp(z_tv - lse_t) - [v = target(t)] g_t,
  *   g_t = dloss_t, 0 for a token without target
  *   dx [T, d] = D W,  dW [V, d] = D^T x
- * each fp32 or bf16 (MOE_Y_F32, MOE_Y_BF16), either NULL if not wanted.  D is
+ * each fp32 or bf16 (MOE_Y_F32, MOE_Y_BF16), either NULL if not wanted, neither
+ * sharing memory with x, W or the other (MOE_ERR_ARG).  D is
  * formed from the logits again, in pieces of the vocabulary, and enters the
- * products as the sum of three bf16 values (24 bits) for fp32 results, whose runs of
- * sums are kept short as the logits' are, and for bf16 results as the sum of two
+ * products as the sum of three bf16 values (24 bits) for fp32 results, whose runs
+ * of sums are kept short as the logits' are, and for bf16 results as the sum of two
  * (16 bits) up to 256 tokens and as one (2^-8 of each value, beside the final
- * rounding) beyond; dx is then still within its own rounding where the target's
- * term is the largest (its rows are kept in units that make that term exact).  A token whose dloss and dlse are 0 or
- * that has neither target nor dlse adds nothing, whatever x holds. */
+ * rounding) beyond.  dx then still stays within its own rounding where the
+ * target's term is the largest: rows of D are kept in units that make it exact.  A
+ * token whose dloss and dlse are 0, or that has neither target nor dlse, adds
+ * nothing, whatever x holds. */
 int moe_xent_bwd(int T, int V, int d, const uint16_t* x, const uint16_t* W, const void* target, int target_type,
                  const float* loss, const float* lse, const float* dloss, const float* dlse, void* dx, int dx_type,
                  void* dW, int dW_type, void* ws, void* stream);
@@ -464,14 +467,15 @@ int moe_xent_bwd(int T, int V, int d, const uint16_t* x, const uint16_t* W, cons
  * the Frobenius norm, then `steps` (1 to MOE_ORTHOGONALIZE_MAX_STEPS; 5 is usual)
  * times
  *   A = X X^T,  X <- 3.4445 X + (-4.7750 A + 2.0315 A A) X
- * (for rows > cols the same with X^T).  Between the products X, A and the
- * polynomial are held in fp16, sums in fp32: O differs from the formula by about
- * 1e-3 of its norm (up to 1.5e-3 where one side is much the longer), and its
- * rounding to bf16 by 1.7e-3.  A matrix of zeros (an
- * expert that saw no token) gives zeros; one that holds a NaN or an Inf, or whose
- * sum of squares passes fp32's range, gives NaN everywhere; norms below 1e-10
- * lose bits.  rows, cols any from 1 to 32768 (MOE_ERR_SHAPE otherwise).  O may not
- * be G.  Workspace as above: moe_orthogonalize_workspace_bytes, cleared once with
+ * (for rows > cols the same with X^T).  Between the products A and the polynomial
+ * are held in fp16 and X in fp16 with 8 more bits beside it, sums in fp32: O
+ * differs from the formula by 0.6e-3 of its norm, by up to 1.5e-3 where one side is
+ * much the longer and 2.5e-3 where the rank is a fraction of the smaller side, and
+ * by its rounding to bf16, 1.7e-3.  A matrix of zeros (an expert that saw no token) gives
+ * zeros; one that holds a NaN or an Inf, or whose sum of squares passes fp32's
+ * range, gives NaN everywhere; norms below 1e-10 lose bits.  rows, cols any from 1
+ * to 32768 (MOE_ERR_SHAPE otherwise).  O and G may not share memory (MOE_ERR_ARG).
+ * Workspace as above: moe_orthogonalize_workspace_bytes, cleared once with
  * moe_orthogonalize_ws_init. */
 #define MOE_ORTHOGONALIZE_MAX_STEPS 16
 size_t moe_orthogonalize_workspace_bytes(int mats, int rows, int cols);

@@ -122,24 +122,35 @@ def orthogonalize_spread(G, steps, unit=2.0 ** -11, eps=1e-7):
 
 
 def orthogonalize_rounded(G, steps, eps=1e-7):
-    """The same with the library's roundings: X times 2^10, A times 2^12 and the polynomial plus 2.5 I times 2^11 to fp16
-    after each product, the result to bf16 (sums in fp64, where the library's are fp32)."""
+    """The same with the library's roundings: X times 2^10 to fp16, with what that leaves times 2^9 in e4m3 beside it for
+    the first term of all steps but the last; A times 2^12 and the polynomial (plus 2.5 I in the last two steps) times
+    2^11 to fp16 after each product; the result to bf16 (sums in fp64, where the library's are fp32)."""
     def f16(v):
         return v.astype(np.float16).astype(np.float64)
+
+    def e4m3(v):
+        step = 2.0 ** (np.maximum(np.floor(np.log2(np.maximum(np.abs(v), 1e-300))), -6) - 3)
+        return np.clip(np.rint(v / step) * step, -448, 448)
 
     def bf16(v):
         u = v.astype(np.float32).view(np.uint32).astype(np.uint64)
         return ((u + 0x7FFF + ((u >> 16) & 1)) & 0xFFFF0000).astype(np.uint32).view(np.float32).astype(np.float64)
 
+    def parts(v):
+        hi = f16(v)
+        return hi, e4m3((v - hi) * 512) / 512
+
     G = G.astype(np.float64)
     norm = np.sqrt((G ** 2).sum())
     up = 2.0 ** (10 - np.frexp(norm)[1])
     a, b, c = NS
-    X, r = f16(G * up), 1.0 / (norm + eps) / up
+    (X, lo), r = parts(G * up), 1.0 / (norm + eps) / up
     wide = X.shape[0] <= X.shape[1]
     for i in range(steps):
+        s = 2.5 if i >= steps - 2 else 0.0
         A = f16((X @ X.T if wide else X.T @ X) * r * r * 4096)
-        B = f16(b * 2048 / 4096 * A + c * 2048 / 4096 ** 2 * (A @ A) + 2.5 * 2048 * np.eye(len(A)))
-        Y = (a - 2.5) * r * X + r / 2048 * (B @ X if wide else X @ B)
-        X, r = (bf16(Y), 1.0) if i == steps - 1 else (f16(Y * 1024), 1.0 / 1024)
-    return X
+        B = f16(b * 2048 / 4096 * A + c * 2048 / 4096 ** 2 * (A @ A) + s * 2048 * np.eye(len(A)))
+        Y = (a - s) * r * (X + (lo if i < steps - 1 else 0)) + r / 2048 * (B @ X if wide else X @ B)
+        if i == steps - 1:
+            return bf16(Y)
+        (X, lo), r = parts(Y * 1024), 1.0 / 1024

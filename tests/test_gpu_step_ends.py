@@ -459,6 +459,21 @@ def test_orthogonalize_many_large(rows, cols):
     assert torch.equal(got[:7], again[:7]) and torch.equal(got[8:], again[8:])
 
 
+@pytest.mark.parametrize("mats,rows,cols,rank", [(1, 64, 2048, 5), (2, 300, 128, 9), (1, 500, 700, 20), (1, 700, 500, 100),
+                                                 (9, 1300, 1400, 60)])
+def test_orthogonalize_of_low_rank(mats, rows, cols, rank):
+    """Gradients of an expert that saw few tokens: the steps raise what rounding leaves beside them 485-fold, so X carries
+    the bits below fp16's too.  With fp16 alone these come out up to 4e-2 of their norm off."""
+    G = (torch.randn(mats, rows, rank, generator=gen(1)) @ torch.randn(mats, rank, cols, generator=gen(2))) * 1e-4
+    got, ws = run_ortho(G)
+    for i in {0, mats - 1}:
+        g = U.np64(G[i])
+        ref = S.orthogonalize(g, 5)
+        like = U.relf(S.orthogonalize_rounded(g, 5), ref)
+        assert like <= 4e-3 and U.relf(U.np64(got[i]), ref) <= 1.25 * like + 2.0 ** -12
+    assert U.device_error(ws) == (0, 0)
+
+
 def test_orthogonalize_offsets_past_32_bits():
     mats, m = 8300, 512
     assert mats * m * m > 2 ** 31
@@ -601,3 +616,46 @@ def test_balance_more_sequences_than_counters():
     counts, mean_p, loss, *_ = run_balance(z, idx, mask, 70, d, d, None)
     rc, rp, rl, _ = S.balance_fwd(np.nan_to_num(z.numpy()), np.where(idx.numpy() < 32, idx.numpy(), 0), 70, mask.numpy())
     assert np.array_equal(counts.cpu().numpy(), rc) and np.allclose(U.np64(loss), rl, rtol=1e-5)
+
+
+def test_balance_of_millions_of_tokens():
+    """A block's sums stay short however many tokens there are."""
+    T, E, k = 2_000_003, 8, 2
+    z, idx, _ = balance_inputs(T, E, k, 1, None, scale=2.0)
+    d = torch.ones(1)
+    counts, mean_p, loss, zloss, out, ws = run_balance(z, idx, None, 1, d, d, None)
+    rc, rp, rl, rz = S.balance_fwd(z.numpy(), idx.numpy(), 1)
+    assert np.array_equal(counts.cpu().numpy(), rc)
+    # p to 4e-6, at most 4096 / 16 / 32 of them on a lane and 16 warps added in fp32
+    assert np.abs(U.np64(mean_p) - rp).max() <= (4e-6 + 24 * 2.0 ** -24) * rp.max()
+    assert np.allclose(U.np64(loss), rl, rtol=1e-5) and np.allclose(U.np64(zloss), rz, rtol=1e-5)
+    assert U.device_error(ws) == (0, 0)
+
+
+def test_two_graphs_share_a_workspace():
+    """Replayed in turn on one stream: nothing is kept in a workspace from one call to the next."""
+    cases = []
+    ws = moe.alloc_xent_workspace(700, 3000, 256)
+    for T, V, d in ((700, 3000, 256), (40, 2999, 128)):
+        x, W, target = xent_inputs(T, V, d, 0.2, seed=T)
+        dloss = torch.ones(T) / T
+        ref = run_xent(x, W, target, True, dloss, None, BF16, F32)[:4]
+        g, dl, out = [t.to(U.DEV) for t in (x, W, target)], dloss.to(U.DEV), [torch.empty_like(t) for t in ref]
+        assert moe.moe_xent_workspace_bytes(T, V, d) <= ws.nbytes
+
+        def step(g=g, dl=dl, out=out):
+            moe.moe_xent_fwd(*g, out[0], out[1], ws)
+            moe.moe_xent_bwd(*g, out[0], out[1], dl, None, out[2], out[3], ws)
+
+        step()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+        cases.append((graph, ref, out, g, dl))  # a graph does not keep its inputs alive
+    for _ in range(3):
+        for graph, ref, out, *_ in cases:
+            for t in out:
+                t.fill_(float("nan"))
+            graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for _, ref, out, *_ in cases for a, b in zip(ref, out))

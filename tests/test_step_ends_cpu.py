@@ -131,7 +131,8 @@ def test_xent_refuses_pointers_and_types(lib):
         assert lib.moe_xent_fwd(*fwd[:i], ODD if i < 9 else WS_ODD, *fwd[i + 1:]) == moe.MOE_ERR_ALIGN
     for tt in (2, -1):
         assert lib.moe_xent_fwd(*fwd[:6], tt, *fwd[7:]) == moe.MOE_ERR_ARG
-    bwd = [10, 20, 64, OK, OK, OK, 1, OK, OK, OK, OK, OK, 0, OK, 1, OK, None]
+    A, C = ctypes.c_void_p(1 << 21), ctypes.c_void_p(1 << 22)
+    bwd = [10, 20, 64, OK, OK, OK, 1, OK, OK, OK, OK, A, 0, C, 1, OK, None]
     for i in (3, 4, 5, 7, 8, 9, 15):
         assert lib.moe_xent_bwd(*bwd[:i], None, *bwd[i + 1:]) == moe.MOE_ERR_ARG
     for i in (3, 4, 5, 7, 8, 9, 10, 11, 13):
@@ -139,6 +140,10 @@ def test_xent_refuses_pointers_and_types(lib):
     assert lib.moe_xent_bwd(*bwd[:15], WS_ODD, None) == moe.MOE_ERR_ALIGN
     for i in (12, 14):
         assert lib.moe_xent_bwd(*bwd[:i], 2, *bwd[i + 1:]) == moe.MOE_ERR_ARG
+    for i, at in ((11, (1 << 20) + 1024), (13, (1 << 20) + 1024), (11, (1 << 20) - 2048), (13, (1 << 21) + 2048)):
+        shared = list(bwd)                            # with x and W, or with each other
+        shared[i] = ctypes.c_void_p(at)
+        assert lib.moe_xent_bwd(*shared) == moe.MOE_ERR_ARG
     none = list(bwd)
     none[11] = none[13] = None                        # nothing to compute
     assert lib.moe_xent_bwd(*none) == moe.MOE_ERR_ARG
@@ -172,7 +177,8 @@ def test_orthogonalize_refuses_arguments(lib):
     for i in (3, 5, 7):
         assert lib.moe_orthogonalize(*good[:i], None, *good[i + 1:]) == moe.MOE_ERR_ARG
         assert lib.moe_orthogonalize(*good[:i], ODD if i < 7 else WS_ODD, *good[i + 1:]) == moe.MOE_ERR_ALIGN
-    assert lib.moe_orthogonalize(*good[:5], OK, *good[6:]) == moe.MOE_ERR_ARG  # in place
+    for at in (1 << 20, (1 << 20) + 240, (1 << 20) - 112):  # in place, or sharing its end or beginning
+        assert lib.moe_orthogonalize(*good[:5], ctypes.c_void_p(at), *good[6:]) == moe.MOE_ERR_ARG
 
 
 # ----------------------------------------------------------------- binding
