@@ -2,7 +2,7 @@
 // then a number of steps of
 //   A = X X^T,  B = b A + c A A,  X <- a X + B X
 // with (a, b, c) = (3.4445, -4.7750, 2.0315), which bring every singular value of
-// X near 1 (between 0.7 and 1.2 after five steps for those above 0.002).  Where
+// X near 1 (between 0.7 and 1.2 after five steps for those above 0.0016).  Where
 // there are more rows than columns the products are X^T X and X B, so that A is
 // always the smaller of the two and nothing is transposed in memory.
 //
@@ -19,6 +19,7 @@
 // read them take the others transposed (dense_flip); on single CTAs, whose tiles
 // are smaller, the epilogue stores both halves.
 #include <algorithm>
+#include <cmath>
 #include <cstring>
 
 #include <cuda_fp16.h>
@@ -47,6 +48,7 @@ struct OrthoOp {
   struct Params : DenseParams {
     const float* scal;   // [mats]: X of the first step is scal times what is stored; 0: matrix needs no products
     int first;           // the first step
+    float grown, grows;  // kNsA to the power of the step, and of the next (see step_scale)
     const __half* old;   // square: A; update: X, laid out as the result
     int pitch;           // of old
     uint8_t* lo;         // update: what rounding left of X, laid out as old; that of the result takes its place
@@ -120,14 +122,15 @@ struct OrthoOp {
   static __device__ __forceinline__ void chunk(const Params& p, const DenseTile& t, const DenseEpi& e, const Pre& pre, int c,
                                                const uint32_t (&acc)[32]) {
     if (pre.r == 0.f) return;  // no products for this matrix
-    const float r = p.first ? pre.r : 1.f / kSX;
+    const float r = p.first ? pre.r : step_scale(pre.r, p.grown);
+    const float out = p.bf16 ? 1.f : 1.f / step_scale(pre.r, p.grows);  // update: of X' in what is stored
     const int x = dense_col(p, t, e) + 32 * c, y = t.m0 + 32 * e.q;
     // gram: A = r^2 sums; square: B + s I = b A + c sums + s I; update: X' =
     // (a - s) r X + r sums
     const float fs = KIND == kSquare                         ? kNsC * (kSB / (kSA * kSA))
                      : (KIND == kGramWide || KIND == kGramTall) ? r * r * kSA
-                                                             : r * ((p.bf16 ? 1.f : kSX) / kSB);
-    const float fo = KIND == kSquare ? kNsB * (kSB / kSA) : (kNsA - p.shift) * r * (p.bf16 ? 1.f : kSX);
+                                                             : (r * out) / kSB;
+    const float fo = KIND == kSquare ? kNsB * (kSB / kSA) : (kNsA - p.shift) * (r * out);
     float v[32];
 #pragma unroll
     for (int j = 0; j < 32; ++j) v[j] = fs * __uint_as_float(acc[j]);
@@ -303,7 +306,7 @@ __global__ void __launch_bounds__(256)
     frexpf(norm, &ex);
     const int k = kSXLog2 - ex;
     if (blockIdx.x == 0 && threadIdx.x == 0) scal[mat] = ldexpf(inv, -k);
-    const float up = ldexpf(1.f, k);  // the norm is between 2^-41 and 2^64 here: 2^k is a normal number
+    const float up = ldexpf(1.f, k);  // the norm is between 2^-104 and 2^64 here: 2^k is a normal number
     __half* Xm = X + static_cast<size_t>(mat) * rows * pitch;
     uint8_t* Lm = rest + static_cast<size_t>(mat) * rows * pitch;  // a bf16 G is fp16 exactly
     constexpr int VE = BF16 ? 8 : 4;
@@ -436,12 +439,15 @@ int launch_ortho(const OrthoArgs& a, cudaStream_t s) {
     __half* Xo = X[(it + 1) & 1];
     const bool last = it + 1 == a.steps;
     const float shift = it >= a.steps - kShiftSteps ? kNsShift : 0.f;
+    const float grown = std::pow(kNsA, static_cast<float>(it)), grows = grown * kNsA;
     auto gram = [&](auto& p) {
       std::memset(&p, 0, sizeof(p));
       base(p, 0, m, m, wide ? a.cols : a.rows);
       dense_shape(p, gram_shape.cg, gram_shape.tn, a.mats, true);
       p.scal = scal;
       p.first = it == 0;
+      p.grown = grown;
+      p.grows = grows;
       p.upper = upper;
       p.out = A;
       p.out_pitch = L.spitch;
@@ -486,6 +492,8 @@ int launch_ortho(const OrthoArgs& a, cudaStream_t s) {
       dense_shape(p, update_shape.cg, update_shape.tn, a.mats, false);
       p.scal = scal;
       p.first = it == 0;
+      p.grown = grown;
+      p.grows = grows;
       p.upper = upper;
       p.old = Xi;
       p.lo = lo;

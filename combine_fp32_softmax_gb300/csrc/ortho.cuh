@@ -27,9 +27,13 @@ constexpr float kNsEps = 1e-7f;
 // stay below fp16's 65504, and entries 2^-24, 2^-26, 2^-25 are still normal.
 constexpr float kSX = 1024.f, kSA = 4096.f, kSB = 2048.f;
 constexpr int kSXLog2 = 10;
-// Below this norm of X the cubic term of a step is under 2^-19 of the linear one
-// for five steps on: the result is a^steps X.
-constexpr float kTiny = 0x1p-17f;
+// X of step i is step_scale(...) times what is stored.  A matrix whose norm is small
+// beside eps grows by kNsA a step at first and is stored in units that grow with it,
+// so it loses nothing to fp16's range.
+__device__ __forceinline__ float step_scale(float scal, float grown) { return fminf(1.f / kSX, scal * grown); }
+// Below this norm of X the steps are linear for all of the most there may be (kNsA^16
+// is 2^28.6): the result is a^steps X.
+constexpr float kTiny = 0x1p-80f;
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);

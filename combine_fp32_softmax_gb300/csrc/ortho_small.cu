@@ -184,8 +184,11 @@ __global__ void __launch_bounds__(kSmallThreads)
   });
   __syncthreads();
 
+  const float scal = ldexpf(inv, ex - kSXLog2);
+  float grown = 1.f;  // kNsA to the power of the step
   for (int step = 0; step < steps; ++step) {
-    const float r = step == 0 ? ldexpf(inv, ex - kSXLog2) : 1.f / kSX;
+    const float r = step == 0 ? scal : step_scale(scal, grown);
+    grown *= kNsA;
     const float shift = step >= steps - kShiftSteps ? kNsShift : 0.f;
     gram_pieces(X, xs, sp, nc, warp, lane, [&](int i, int j, float a, float b, bool off) {
       *reinterpret_cast<float2*>(P + i * ps + j) = make_float2(a, b);
@@ -223,7 +226,7 @@ __global__ void __launch_bounds__(kSmallThreads)
     });
     __syncthreads();
     const bool last = step + 1 == steps;
-    const float fs = r * ((last ? 1.f : kSX) / kSB), fo = (kNsA - shift) * r * (last ? 1.f : kSX);
+    const float ro = last ? r : r / step_scale(scal, grown), fs = ro / kSB, fo = (kNsA - shift) * ro;
     // a warp takes 16 columns: it reads all of theirs before it writes any
     for (int slab = warp; slab < nc / 16; slab += kSmallThreads / 32) {
       float c[8][2][4] = {};

@@ -464,8 +464,9 @@ int moe_xent_bwd(int T, int V, int d, const uint16_t* x, const uint16_t* W, cons
 /* Matrices G [mats, rows, cols] (fp32 or bf16: g_type MOE_Y_F32 or MOE_Y_BF16; the
  * weight gradients of the experts, or a mean of them over steps) to nearly
  * orthogonal ones O [mats, rows, cols] bf16, each by itself: X = G / (|G| + 1e-7) in
- * the Frobenius norm, then `steps` (1 to MOE_ORTHOGONALIZE_MAX_STEPS; 5 is usual)
- * times
+ * the Frobenius norm, then `steps` (1 to MOE_ORTHOGONALIZE_MAX_STEPS; 5 is usual;
+ * steps past those that bring the singular values near 1 only move them about in
+ * [0.7, 1.2]) times
  *   A = X X^T,  X <- 3.4445 X + (-4.7750 A + 2.0315 A A) X
  * (for rows > cols the same with X^T).  Between the products A and the polynomial
  * are held in fp16 and X in fp16 with 8 more bits beside it, sums in fp32: O
@@ -473,7 +474,7 @@ int moe_xent_bwd(int T, int V, int d, const uint16_t* x, const uint16_t* W, cons
  * much the longer and 2.5e-3 where the rank is a fraction of the smaller side, and
  * by its rounding to bf16, 1.7e-3.  A matrix of zeros (an expert that saw no token) gives
  * zeros; one that holds a NaN or an Inf, or whose sum of squares passes fp32's
- * range, gives NaN everywhere; norms below 1e-10 lose bits.  rows, cols any from 1
+ * range, gives NaN everywhere.  rows, cols any from 1
  * to 32768 (MOE_ERR_SHAPE otherwise).  O and G may not share memory (MOE_ERR_ARG).
  * Workspace as above: moe_orthogonalize_workspace_bytes, cleared once with
  * moe_orthogonalize_ws_init. */

@@ -418,6 +418,20 @@ def test_orthogonalize_scales_zeros_and_bad_matrices():
     assert U.device_error(ws) == (0, 0)
 
 
+@pytest.mark.parametrize("rows,cols", [(96, 160), (300, 200)])
+@pytest.mark.parametrize("steps,top", [(1, 1e-9), (5, 1e-9), (10, 2e-14), (16, 1e-17)])
+def test_orthogonalize_small_norms(rows, cols, steps, top):
+    """Norms far below eps: X starts small and grows 3.4-fold a step, through all of fp16's range.  (Scales at which the
+    last step just comes near 1: further steps map [0.7, 1.2] into itself with slopes above 1 and amplify any error.)"""
+    scales = [top, top / 30, top / 1000, top * 1e-6]
+    base = torch.randn(rows, cols, generator=gen(7))
+    got, ws = run_ortho(torch.stack([base * s for s in scales]), steps)
+    for i, s in enumerate(scales):
+        g = U.np64(base * s)
+        assert U.relf(U.np64(got[i]), S.orthogonalize(g, steps)) <= 2.0 ** -8, s  # bf16's rounding and fp16's
+    assert U.device_error(ws) == (0, 0)
+
+
 def test_orthogonalize_same_bits_grid_graph():
     G = torch.randn(3, 300, 500, generator=gen(5))
     ref, _ = run_ortho(G)
