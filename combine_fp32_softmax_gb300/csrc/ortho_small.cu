@@ -24,6 +24,12 @@ namespace {
 constexpr int kSmallThreads = 256;
 constexpr int kMaxCluster = 16;
 
+// A CTA's shared memory may be written from its cluster once it has started: every
+// CTA arrives first of all and waits, the norm's reads later, before it writes.
+__device__ __forceinline__ void cluster_arrive_started() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait_started() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
   uint32_t a;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
@@ -107,6 +113,7 @@ __device__ __forceinline__ void gram_pieces(const __half* M, int stride, int sp,
 template <bool BF16>
 __global__ void __launch_bounds__(kSmallThreads)
     ortho_small_kernel(const void* __restrict__ G, uint16_t* __restrict__ O, int rows, int cols, SmallShape sh, int steps) {
+  cluster_arrive_started();
   griddep_wait();
   griddep_launch_dependents();
   extern __shared__ __align__(16) uint8_t smem[];
@@ -156,6 +163,7 @@ __global__ void __launch_bounds__(kSmallThreads)
   for (int i = tid; i < sp * xs / 2; i += kSmallThreads) reinterpret_cast<uint32_t*>(X)[i] = 0u;  // padding too
   for (int i = tid; i < sp * nc / 4; i += kSmallThreads) reinterpret_cast<uint32_t*>(lo)[i] = 0u;
   __syncthreads();
+  cluster_wait_started();
   if (tid < C) {
     d = 0.;
     for (int w = 0; w < kSmallThreads / 32; ++w) d += wsum[w];
