@@ -656,6 +656,8 @@ int moe_balance_bwd(const moe_cfg* cfg, const float* logits, const int32_t* coun
   MOE_TRY(check_seqs(*cfg, seqs));
   MOE_TRY(check_ptrs({logits, counts, dloss, dzloss, dlogits}, {mask, dlogits_in}, ws));
   const moe_cfg& c = *cfg;
+  const size_t n = sizeof(float) * c.T * c.E;
+  if (overlap(dlogits, n, logits, n) || (dlogits_in != dlogits && overlap(dlogits, n, dlogits_in, n))) return MOE_ERR_ARG;
   MOE_TRY_CUDA(launch_balance_bwd(logits, counts, mask, dloss, dzloss, c.T, seqs, c.E, c.k, dlogits_in, dlogits,
                                   static_cast<cudaStream_t>(stream)));
   return MOE_OK;

@@ -437,10 +437,10 @@ __global__ void __launch_bounds__(kBwdThreads, 4)
 #pragma unroll
     for (int i = 0; i < Y::E; ++i) dot = fmaf(a[i], v[i], dot);
     dot = lanes_reduce<Y>(dot, [](float x, float y) { return x + y; });
-    const float use = on ? inv : 0.f, shift = fmaf(hz, lse, -dot * inv);
-    if (ok)  // a row that is not there is: zeros' exponentials, times 0
+    const float shift = fmaf(hz, lse, -dot * inv);
+    if (ok && on)
 #pragma unroll
-      for (int i = 0; i < Y::E; ++i) in[i] = fmaf(v[i] * use, a[i] + shift, in[i]);
+      for (int i = 0; i < Y::E; ++i) in[i] = fmaf(v[i] * inv, a[i] + shift, in[i]);
     if (t < T) {
       float* to = dlogits + static_cast<size_t>(t) * E;
 #pragma unroll

@@ -415,7 +415,9 @@ int moe_balance_fwd(const moe_cfg* cfg, const float* logits, const int32_t* topk
  *   dlogits_te = dlogits_in_te + p_te (a_e - sum_j a_j p_tj) + 2 dzloss / n lse_t p_te,
  *   a_e = dloss E c_e / (k n^2)
  * dlogits_in [T, E]: the gradient of moe_layer_bwd, to which it is added; it may be
- * dlogits itself, or NULL for none.  Tokens that do not count get dlogits_in. */
+ * dlogits itself, or NULL for none; otherwise dlogits shares no memory with it or
+ * with logits (MOE_ERR_ARG).  Tokens that do not count get dlogits_in, whatever
+ * dloss and dzloss are. */
 int moe_balance_bwd(const moe_cfg* cfg, const float* logits, const int32_t* counts, const uint8_t* mask, int seqs,
                     const float* dloss, const float* dzloss, const float* dlogits_in, float* dlogits, void* ws,
                     void* stream);
@@ -434,7 +436,7 @@ int moe_balance_bwd(const moe_cfg* cfg, const float* logits, const int32_t* coun
  * Workspace: moe_xent_workspace_bytes (0 outside the limits; backward = 0: only
  * for the forward), its first bytes cleared once with moe_xent_ws_init; it keeps
  * nothing between calls, and calls that share it must not overlap on the GPU.
- * The forward is two launches, the backward at most 2 and three for each piece
+ * The forward is two launches, the backward at most three and three for each piece
  * of the vocabulary; all may be captured into a CUDA graph. */
 enum { MOE_I32 = 0, MOE_I64 = 1 }; /* type of target */
 size_t moe_xent_workspace_bytes(int T, int V, int d, int backward);

@@ -112,6 +112,14 @@ def test_balance_adds_in_place_and_without():
     assert torch.equal(a[~mask.to(a.device)].cpu(), add[~mask])  # tokens that do not count: as they were
 
 
+def test_balance_gradient_that_is_not_finite_leaves_padding_alone():
+    z, idx, mask = balance_inputs(300, 64, 6, 3, "random")
+    d, add = torch.tensor([float("nan"), 1.0, float("inf")]), torch.randn(300, 64, generator=gen(1))
+    out = run_balance(z, idx, mask, 3, d, d, add)[4].cpu()
+    assert torch.equal(out[~mask], add[~mask])
+    assert out[:100][mask[:100]].isnan().all() and out[100:200].isfinite().all()
+
+
 def test_balance_same_bits_and_grid():
     z, idx, mask = balance_inputs(30000, 64, 6, 2, "random")
     d = torch.ones(2)

@@ -114,6 +114,11 @@ def test_balance_refuses(lib):
             assert call(fn, args, 3, seqs) == moe.MOE_ERR_SHAPE
         for bad in (cfg(T=0), cfg(E=257), cfg(E=0), cfg(k=9, E=16), cfg(k=3, E=2)):
             assert call(fn, args, cc=bad) == moe.MOE_ERR_SHAPE
+    bwd[0] = ctypes.c_void_p(1 << 22)
+    size = 4 * c.T * c.E
+    for at in ((1 << 22), (1 << 22) + size - 16, (1 << 22) - size + 16,   # the logits, or a part of them
+               (1 << 20) + size - 16, (1 << 20) - size + 16):             # a part of the gradient to add to
+        assert call(lib.moe_balance_bwd, bwd, 7, ctypes.c_void_p(at)) == moe.MOE_ERR_ARG
 
 
 @pytest.mark.parametrize("T,V,d", [(0, 10, 64), (10, 0, 64), (10, 10, 0), (10, 10, 32), (10, 10, 96), ((1 << 22) + 1, 10, 64),
