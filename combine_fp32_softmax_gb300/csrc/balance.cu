@@ -91,7 +91,7 @@ __device__ __forceinline__ bool softmax_values(float (&v)[Y::E], int E, int l, f
   float s = bad;
 #pragma unroll
   for (int i = 0; i < Y::E; ++i) {
-    v[i] = __expf(v[i] - m);  // 0 beyond E
+    v[i] = exp_short(v[i] - m);  // 0 beyond E
     s += v[i];
   }
   s = lanes_reduce<Y>(s, [](float a, float b) { return a + b; });

@@ -393,7 +393,6 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_kernel(const __grid_co
     for (int i = first; ok && i < p.total && !*abort; i += step) {
       const DenseTile t = walk.next(p, i);
       const bool active = t.m0 + 32 * e.q < p.M;
-      const auto pre = Op::pre(p, t, e);
       auto release = [&](int buf) {
         tc_fence_before();
         __syncwarp();
@@ -407,6 +406,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_kernel(const __grid_co
       if constexpr (Op::CHUNKS) {
         // one run: 32 columns at a time, the next ones on their way meanwhile
         if (t.kb1 == t.kb0) continue;
+        const auto pre = Op::pre(p, t, e);
         const int buf = it & 1;
         if (!mbar_wait_inline(&ss.tfull[buf], (it >> 1) & 1, abort, p.err, where(4, i))) break;
         ++it;
@@ -432,6 +432,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_kernel(const __grid_co
         }
         continue;
       }
+      decltype(Op::pre(p, t, e)) pre{};
       uint32_t acc[4][32];
       const int runs = (t.kb1 - t.kb0 + p.run_kb - 1) / p.run_kb;
       if (runs == 0) {
@@ -443,6 +444,8 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_kernel(const __grid_co
 #pragma unroll 1
       for (int r = 0; r < runs; ++r) {
         const int buf = it & 1;
+        // in the first pause: the products of the run after next wait for the first run's buffer
+        if (r == min(1, runs - 1)) pre = Op::pre(p, t, e);
         if (!mbar_wait_inline(&ss.tfull[buf], (it >> 1) & 1, abort, p.err, where(4, i))) {
           ok = false;
           break;

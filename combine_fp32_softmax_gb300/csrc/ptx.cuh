@@ -270,11 +270,12 @@ __device__ __forceinline__ void tma_store_2d(const void* map, const void* src_sm
                "r"(smem_u32(src_smem)), "r"(c0), "r"(c1)
                : "memory");
 }
-__device__ __forceinline__ void tma_store_3d(const void* map, const void* src_smem, int c0, int c1, int c2) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(smem_u32(src_smem)), "r"(c0), "r"(c1), "r"(c2)
-               : "memory");
+// exp(x) = 2^(x log2 e): off by at most 2^-22 + |x| 2^-23 of itself; results below
+// 2^-126 are 0 (__expf's are not, at three more instructions a value).
+__device__ __forceinline__ float exp_short(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.44269504f));
+  return r;
 }
 // 1D bulk copies (16-byte aligned addresses, size a multiple of 16).
 __device__ __forceinline__ void bulk_load(void* dst_smem, const void* src, uint32_t bytes, uint64_t* bar) {

@@ -26,15 +26,21 @@ namespace {
 
 constexpr int kCodeXent = 0x11;  // + operation, in the error word of a wait that ran out
 
-// K blocks of a run of sums where fp32 results come out.
-// Short ones leave the epilogue less time beside the products (two runs wait at
-// most): at 8192 tokens of d = 2048 and V = 100000 the forward takes 2.37, 2.22 and
-// 2.20 ms with runs of 4, 8 and 16 blocks, the pieces' D 2.74, 2.40 and 2.38 ms.
+// K blocks of a run of sums of fp32 gradients.
 constexpr int kExactRun = 8;
+// K blocks of a run of a logit's sums: as even runs as there are of 12 at most.  Taking
+// out a run costs the epilogue 0.3 us, and at a tile's end two runs of the next one
+// are all that the products have room for: with runs of 4, 8, 11 and 16 of the 32
+// blocks of d = 2048, 2000 tokens of V = 32001 take 185, 149, 146 and 145 us forward
+// and 205, 168, 157 and 152 us for D, and lose 2^-19, 2^-18, 2^-17.5 and 2^-17 of the
+// terms' magnitudes at most.
 // Few tokens' time is their weights' bytes: runs of one block, whose losses nearly
 // vanish (loss off by 1e-7 of itself, as a plain fp32 product's; 1e-6 with 8), cost
 // 3 % there (37 tokens of d = 4096 and V = 50257: 76.8 against 74 us).
-int logit_run(int T) { return T <= kBM ? 1 : kExactRun; }
+int logit_run(int T, int d) {
+  const int blocks = d / kBK;
+  return T <= kBM ? 1 : ceil_div(blocks, ceil_div(blocks, 12));
+}
 // Bytes of D that a piece of the vocabulary takes at least, and its columns at least.
 constexpr size_t kPieceBytes = size_t(512) << 20;
 constexpr int kPieceCols = 8192;
@@ -111,7 +117,7 @@ struct StatsOp {
 #pragma unroll
     for (int c = 0; c < 4; ++c)
 #pragma unroll
-      for (int j = 0; j < 32; ++j) s4[j & 3] += __expf(__uint_as_float(acc[c][j]) - base);
+      for (int j = 0; j < 32; ++j) s4[j & 3] += exp_short(__uint_as_float(acc[c][j]) - base);
     if (row < p.M)
       p.part[static_cast<size_t>(row) * (2 * p.nt) + 2 * (t.n0 / p.tn) + e.part] =
           make_float2(m, (s4[0] + s4[1]) + (s4[2] + s4[3]));
@@ -262,7 +268,7 @@ struct GradOp {
       float f[32];
 #pragma unroll
       for (int j = 0; j < 32; ++j) {
-        const float v = r.w * __expf(__uint_as_float(acc[c][j]) - r.lse);
+        const float v = r.w * exp_short(__uint_as_float(acc[c][j]) - r.lse);
         // a row that no gradient reaches adds nothing, whatever its logits are
         f[j] = (r.w != 0.f && 32 * c + j < n) ? v : 0.f;
         if (32 * c + j == r.rel) f[j] = r.at;
@@ -526,7 +532,7 @@ int launch_xent_fwd(const XentArgs& a, cudaStream_t s) {
       !dense_map_k(&p.tmB, a.W, false, a.d, a.V, 1, a.d, p.b_bytes / 128))
     return MOE_ERR_CUDA;
   p.nkb = a.d / kBK;
-  p.run_kb = logit_run(a.T);
+  p.run_kb = logit_run(a.T, a.d);
   p.code = kCodeXent;
   p.err = err;
   p.target = {a.target, a.target_type};
@@ -580,7 +586,7 @@ int launch_xent_bwd(const XentArgs& a, cudaStream_t s) {
         return MOE_ERR_CUDA;
       p.D = static_cast<uint16_t*>(D);
       p.nkb = a.d / kBK;
-      p.run_kb = logit_run(a.T);  // the forward's logits, bit for bit
+      p.run_kb = logit_run(a.T, a.d);  // the forward's logits, bit for bit
       p.code = kCodeXent + 1;
       p.err = err;
       p.rows = rows;

@@ -428,8 +428,8 @@ int moe_balance_bwd(const moe_cfg* cfg, const float* logits, const int32_t* coun
  *   loss [T] fp32 = lse_t - z_t,target(t); 0 where target(t) < 0 (no target)
  * target [T] int32 or int64 (target_type).  A target >= V counts as none and sets
  * MOE_ERR_ARG (info: the token).  The logits are never in memory.  They are fp32
- * sums whose tensor-core runs are 512 columns long (64 up to 128 tokens) and are
- * added up rounded to nearest, so that at most 2^-18 of the sum of the terms'
+ * sums whose tensor-core runs are 768 columns long at most (64 up to 128 tokens) and
+ * are added up rounded to nearest, so that at most 2^-17.4 of the sum of the terms'
  * magnitudes is lost, and loss keeps its relative precision where a token is
  * certain: it is not formed as a difference of lse and z.  Infinite logits give NaN.
  * Limits (MOE_ERR_SHAPE): 1 <= T, V <= 2^22, d a multiple of 64 up to 65536.

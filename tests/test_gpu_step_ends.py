@@ -2,9 +2,10 @@
 orthogonalised matrices.
 
 Tolerances, derived from the kernels' stated roundings:
-  * a logit: its sum loses at most 2^-18 of S = sum |x||W| in the tensor core's runs of 512 columns and 2^-24 of S for each
-    of the d / 512 additions of runs: dz = (2^-18 + d 2^-33) max S;
-  * lse: dz, the error of the exponentials, sum and log (2^-20 together: __expf is within 2 + |z| ulp of terms that
+  * a logit: its sum loses at most 2^-23 of S = sum |x||W| for each 16 columns of a tensor core's run, and 2^-24 of S for
+    each addition of runs; runs are held to the bound of 512 columns (they have up to 768, whose last thirds' losses
+    do not all come to half a step): dz = (2^-18 + d 2^-33) max S;
+  * lse: dz, the error of the exponentials, sum and log (2^-20 together: the exponential is within 2 + |z| ulp of terms that
     add up to the sum), and its own rounding; loss: 2 dz and the same;
   * D: relative 2 dz + 2^-20 + 2^-23 |lse| for the exponential, plus its rounding, 2^-8 in bf16 and 2^-24 as three
     bf16 values; a product of it: that part of sum |D||W|, the tensor core's loss over the K of one run (2^-23 for each 16
