@@ -9,7 +9,17 @@
 // barriers a step and the shared-memory passes between them.  The matrices are far
 // too small for tcgen05's 128-row tiles and TMEM round trips (launched one by one
 // the products of a 64 x 2048 matrix took 91 us); 16 x 16 pieces of mma.sync spread
-// over eight warps fit them.  fp16 values and their scales are those of ortho.cu.
+// over eight warps fit them: it takes 40 us in this form.  fp16 values and their
+// scales are those of ortho.cu.
+//
+// Up to a side of 48 (FINE) there is no averaging over many roundings, and a random
+// square matrix has a singular value near 0 that the steps raise 485-fold: with fp16
+// values a 4 x 4 matrix comes out off by 3e-3 of its norm in the middle and 6e-3 at
+// the worst of 40.  X, A and B are then kept in two fp16 values each (22 bits) and every
+// product has its two cross terms, on tensor cores that are idle otherwise: 1.6e-3,
+// bf16's rounding, in the same 14 us; 32 x 2048 3.7e-3 -> 1.7e-3 in 27 us, 48 x 2048
+// 2.7e-3 -> 1.7e-3 in 35 instead of 32 us.  (64 x 2048 would take 47 instead of 41 us for
+// 2.2e-3 -> 1.7e-3, 112 x 2048 101 instead of 76.)
 #include <algorithm>
 
 #include <cuda_fp16.h>
@@ -77,22 +87,33 @@ struct SmallShape {
   int s, n;    // smaller and larger side
   int sp, nc;  // s rounded up to 16; columns of a slice, a multiple of 16
   int C;       // CTAs of a cluster
+  int fine;    // two fp16 values each
 };
-int small_smem(int sp, int nc) {
-  return 256 + 2 * sp * half_stride(nc) + 2 * 2 * sp * half_stride(sp) + 4 * sp * sum_stride(sp) + sp * nc;
+constexpr int kFineSide = 48;
+constexpr float kFineLo = 2048.f;  // scale of the second value beside the first
+int small_smem(int sp, int nc, bool fine) {
+  const int x = 2 * sp * half_stride(nc), ab = 2 * 2 * sp * half_stride(sp);
+  return 256 + x + ab + 4 * sp * sum_stride(sp) + (fine ? x + ab : sp * nc);
+}
+// x to the two fp16 values of a pair each.
+__device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  hi = pack_f16(x0, x1);
+  const float2 h = unpack_f16(hi);
+  lo = pack_f16(kFineLo * (x0 - h.x), kFineLo * (x1 - h.y));
 }
 
 // C = M . M^T (16 x 16 pieces on and above the diagonal, spread over the warps) for
-// M [sp][k] with rows `stride` apart; put(row, column, value pair) gets columns
-// j and j + 1 of a row, and each piece's transposed ones by put1.
-template <typename F>
-__device__ __forceinline__ void gram_pieces(const __half* M, int stride, int sp, int k, int warp, int lane, F put) {
+// M [sp][k] with rows `stride` apart (FINE: and what it leaves, `low` elements
+// further); put gets columns j and j + 1 of a row and whether its piece lies off the
+// diagonal, so that the transposed entries are wanted too.
+template <bool FINE, typename F>
+__device__ __forceinline__ void gram_pieces(const __half* M, int low, int stride, int sp, int k, int warp, int lane, F put) {
   const int mt = sp / 16, pieces = mt * (mt + 1) / 2;
   for (int piece = warp; piece < pieces; piece += kSmallThreads / 32) {
     int mi = 0, j = piece;
     while (j >= mt - mi) j -= mt - mi++;
     const int ni = mi + j;
-    float c[2][4] = {};
+    float c[2][4] = {}, cross[2][4] = {};
     const __half* pa = M + (16 * mi + (lane & 15)) * stride + 8 * (lane >> 4);
     const __half* pb = M + (16 * ni + (lane & 7) + 8 * (lane >> 4)) * stride + 8 * ((lane >> 3) & 1);
     for (int kk = 0; kk < k; kk += 16) {
@@ -101,7 +122,21 @@ __device__ __forceinline__ void gram_pieces(const __half* M, int stride, int sp,
       ldmatrix4<false>(b, pb + kk);
       mma16816(c[0], a, b[0], b[1]);
       mma16816(c[1], a, b[2], b[3]);
+      if constexpr (FINE) {
+        uint32_t al[4], bl[4];
+        ldmatrix4<false>(al, pa + low + kk);
+        ldmatrix4<false>(bl, pb + low + kk);
+        mma16816(cross[0], a, bl[0], bl[1]);
+        mma16816(cross[1], a, bl[2], bl[3]);
+        mma16816(cross[0], al, b[0], b[1]);
+        mma16816(cross[1], al, b[2], b[3]);
+      }
     }
+    if constexpr (FINE)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) c[h][v] = fmaf(1.f / kFineLo, cross[h][v], c[h][v]);
     const int r = 16 * mi + (lane >> 2), col = 16 * ni + 2 * (lane & 3);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -110,7 +145,7 @@ __device__ __forceinline__ void gram_pieces(const __half* M, int stride, int sp,
   }
 }
 
-template <bool BF16>
+template <bool BF16, bool FINE>
 __global__ void __launch_bounds__(kSmallThreads)
     ortho_small_kernel(const void* __restrict__ G, uint16_t* __restrict__ O, int rows, int cols, SmallShape sh, int steps) {
   cluster_arrive_started();
@@ -122,10 +157,11 @@ __global__ void __launch_bounds__(kSmallThreads)
   const int xs = half_stride(nc), as = half_stride(sp), ps = sum_stride(sp);
   double* norms = reinterpret_cast<double*>(smem);  // one of each CTA
   __half* X = reinterpret_cast<__half*>(smem + 256);
-  __half* A = X + sp * xs;
-  __half* B = A + sp * as;
-  float* P = reinterpret_cast<float*>(B + sp * as);
-  uint8_t* lo = reinterpret_cast<uint8_t*>(P + sp * ps);  // what rounding left of X
+  const int xlow = sp * xs, alow = sp * as;  // FINE: from a first value to the second
+  __half* A = X + (FINE ? 2 : 1) * xlow;
+  __half* B = A + (FINE ? 2 : 1) * alow;
+  float* P = reinterpret_cast<float*>(B + (FINE ? 2 : 1) * alow);
+  uint8_t* lo = reinterpret_cast<uint8_t*>(P + sp * ps);  // else: what rounding left of X
   __shared__ double wsum[kSmallThreads / 32];
   const size_t base = static_cast<size_t>(blockIdx.x / C) * rows * cols;
   const bool wide = rows <= cols;
@@ -160,8 +196,9 @@ __global__ void __launch_bounds__(kSmallThreads)
 #pragma unroll
   for (int off = 16; off; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
   if (lane == 0) wsum[warp] = d;
-  for (int i = tid; i < sp * xs / 2; i += kSmallThreads) reinterpret_cast<uint32_t*>(X)[i] = 0u;  // padding too
-  for (int i = tid; i < sp * nc / 4; i += kSmallThreads) reinterpret_cast<uint32_t*>(lo)[i] = 0u;
+  for (int i = tid; i < (FINE ? 2 : 1) * xlow / 2; i += kSmallThreads) reinterpret_cast<uint32_t*>(X)[i] = 0u;  // padding too
+  if (!FINE)
+    for (int i = tid; i < sp * nc / 4; i += kSmallThreads) reinterpret_cast<uint32_t*>(lo)[i] = 0u;
   __syncthreads();
   cluster_wait_started();
   if (tid < C) {
@@ -186,9 +223,14 @@ __global__ void __launch_bounds__(kSmallThreads)
   const float up = ldexpf(1.f, kSXLog2 - ex);
   each([&](int i, int j) {
     const float x = up * load(at(i, j));
-    const uint32_t h = pack_f16(x, 0.f);
-    reinterpret_cast<uint16_t*>(X)[i * xs + j - c0] = static_cast<uint16_t>(h);
-    lo[i * nc + j - c0] = static_cast<uint8_t>(rest_e4m3(x, 0.f, h));
+    uint32_t h, l;
+    split2(x, 0.f, h, l);
+    uint16_t* to = reinterpret_cast<uint16_t*>(X) + i * xs + j - c0;
+    to[0] = static_cast<uint16_t>(h);
+    if constexpr (FINE)
+      to[xlow] = static_cast<uint16_t>(l);
+    else
+      lo[i * nc + j - c0] = static_cast<uint8_t>(rest_e4m3(x, 0.f, h));
   });
   __syncthreads();
 
@@ -198,7 +240,7 @@ __global__ void __launch_bounds__(kSmallThreads)
     const float r = step == 0 ? scal : step_scale(scal, grown);
     grown *= kNsA;
     const float shift = step >= steps - kShiftSteps ? kNsShift : 0.f;
-    gram_pieces(X, xs, sp, nc, warp, lane, [&](int i, int j, float a, float b, bool off) {
+    gram_pieces<FINE>(X, xlow, xs, sp, nc, warp, lane, [&](int i, int j, float a, float b, bool off) {
       *reinterpret_cast<float2*>(P + i * ps + j) = make_float2(a, b);
       if (off) {
         P[j * ps + i] = a;
@@ -217,19 +259,33 @@ __global__ void __launch_bounds__(kSmallThreads)
         sum.x += v.x;
         sum.y += v.y;
       }
-      const uint32_t w = pack_f16(fa * sum.x, fa * sum.y);
-      for (int c = 0; c < C; ++c) st_cluster(cluster_addr(A + i * as + j, c), w);
+      uint32_t w, l;
+      split2(fa * sum.x, fa * sum.y, w, l);
+      for (int c = 0; c < C; ++c) {
+        st_cluster(cluster_addr(A + i * as + j, c), w);
+        if (FINE) st_cluster(cluster_addr(A + alow + i * as + j, c), l);
+      }
     }
     cluster_sync();
     constexpr float fs2 = kNsC * (kSB / (kSA * kSA)), fo2 = kNsB * (kSB / kSA);
-    gram_pieces(A, as, sp, sp, warp, lane, [&](int i, int j, float a, float b, bool off) {
-      const float2 o = __half22float2(*reinterpret_cast<const __half2*>(A + i * as + j));
+    gram_pieces<FINE>(A, alow, as, sp, sp, warp, lane, [&](int i, int j, float a, float b, bool off) {
+      float2 o = unpack_f16(*reinterpret_cast<const uint32_t*>(A + i * as + j));
+      if constexpr (FINE) {
+        const float2 l = unpack_f16(*reinterpret_cast<const uint32_t*>(A + alow + i * as + j));
+        o.x = fmaf(1.f / kFineLo, l.x, o.x);
+        o.y = fmaf(1.f / kFineLo, l.y, o.y);
+      }
       const float di = i == j ? shift * kSB : 0.f, dj = i == j + 1 ? shift * kSB : 0.f;
-      const __half2 v = __floats2half2_rn(fmaf(fo2, o.x, fmaf(fs2, a, di)), fmaf(fo2, o.y, fmaf(fs2, b, dj)));
-      *reinterpret_cast<__half2*>(B + i * as + j) = v;
-      if (off) {
-        B[j * as + i] = __low2half(v);
-        B[(j + 1) * as + i] = __high2half(v);
+      uint32_t w[2];
+      split2(fmaf(fo2, o.x, fmaf(fs2, a, di)), fmaf(fo2, o.y, fmaf(fs2, b, dj)), w[0], w[1]);
+#pragma unroll
+      for (int k = 0; k < (FINE ? 2 : 1); ++k) {
+        uint16_t* to = reinterpret_cast<uint16_t*>(B) + k * alow;
+        *reinterpret_cast<uint32_t*>(to + i * as + j) = w[k];
+        if (off) {
+          to[j * as + i] = static_cast<uint16_t>(w[k]);
+          to[(j + 1) * as + i] = static_cast<uint16_t>(w[k] >> 16);
+        }
       }
     });
     __syncthreads();
@@ -237,41 +293,64 @@ __global__ void __launch_bounds__(kSmallThreads)
     const float ro = last ? r : r / step_scale(scal, grown), fs = ro / kSB, fo = (kNsA - shift) * ro;
     // a warp takes 16 columns: it reads all of theirs before it writes any
     for (int slab = warp; slab < nc / 16; slab += kSmallThreads / 32) {
-      float c[8][2][4] = {};
+      constexpr int MI = (FINE ? kFineSide : 128) / 16;
+      float c[MI][2][4] = {}, cross[FINE ? MI : 1][2][4] = {};
       for (int kk = 0; kk < sp; kk += 16) {
-        uint32_t b[4];
-        ldmatrix4<true>(b, X + (kk + (lane & 15)) * xs + 16 * slab + 8 * (lane >> 4));
+        uint32_t b[4], bl[4];
+        const __half* pb = X + (kk + (lane & 15)) * xs + 16 * slab + 8 * (lane >> 4);
+        ldmatrix4<true>(b, pb);
+        if constexpr (FINE) ldmatrix4<true>(bl, pb + xlow);
 #pragma unroll
-        for (int mi = 0; mi < 8; ++mi)
+        for (int mi = 0; mi < MI; ++mi)
           if (16 * mi < sp) {
             uint32_t a[4];
-            ldmatrix4<false>(a, B + (16 * mi + (lane & 15)) * as + kk + 8 * (lane >> 4));
+            const __half* pa = B + (16 * mi + (lane & 15)) * as + kk + 8 * (lane >> 4);
+            ldmatrix4<false>(a, pa);
             mma16816(c[mi][0], a, b[0], b[1]);
             mma16816(c[mi][1], a, b[2], b[3]);
+            if constexpr (FINE) {
+              mma16816(cross[mi][0], a, bl[0], bl[1]);
+              mma16816(cross[mi][1], a, bl[2], bl[3]);
+              ldmatrix4<false>(a, pa + alow);
+              mma16816(cross[mi][0], a, b[0], b[1]);
+              mma16816(cross[mi][1], a, b[2], b[3]);
+            }
           }
       }
       __syncwarp();
 #pragma unroll
-      for (int mi = 0; mi < 8; ++mi)
+      for (int mi = 0; mi < MI; ++mi)
         if (16 * mi < sp)
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int v = 0; v < 2; ++v) {
               const int i = 16 * mi + (lane >> 2) + 8 * v, j = 16 * slab + 8 * h + 2 * (lane & 3);
-              __half2* x = reinterpret_cast<__half2*>(X + i * xs + j);
-              float2 o = __half22float2(*x);
+              uint32_t* x = reinterpret_cast<uint32_t*>(X + i * xs + j);
+              float2 o = unpack_f16(*x);
+              uint32_t* xl = reinterpret_cast<uint32_t*>(X + (FINE ? xlow : 0) + i * xs + j);
               uint16_t* l = reinterpret_cast<uint16_t*>(lo + i * nc + j);
-              if (!last) {
+              float s0 = c[mi][h][2 * v], s1 = c[mi][h][2 * v + 1];
+              if constexpr (FINE) {
+                const float2 more = unpack_f16(*xl);
+                o.x = fmaf(1.f / kFineLo, more.x, o.x);
+                o.y = fmaf(1.f / kFineLo, more.y, o.y);
+                s0 = fmaf(1.f / kFineLo, cross[mi][h][2 * v], s0);
+                s1 = fmaf(1.f / kFineLo, cross[mi][h][2 * v + 1], s1);
+              } else if (!last) {
                 const float2 more = unpack_e4m3(*l);
                 o.x = fmaf(1.f / kLo, more.x, o.x);
                 o.y = fmaf(1.f / kLo, more.y, o.y);
               }
-              const float y0 = fmaf(fo, o.x, fs * c[mi][h][2 * v]), y1 = fmaf(fo, o.y, fs * c[mi][h][2 * v + 1]);
+              const float y0 = fmaf(fo, o.x, fs * s0), y1 = fmaf(fo, o.y, fs * s1);
               if (!last) {
-                const uint32_t h = pack_f16(y0, y1);
-                *reinterpret_cast<uint32_t*>(x) = h;
-                *l = static_cast<uint16_t>(rest_e4m3(y0, y1, h));
+                uint32_t hi, low;
+                split2(y0, y1, hi, low);
+                *x = hi;
+                if constexpr (FINE)
+                  *xl = low;
+                else
+                  *l = static_cast<uint16_t>(rest_e4m3(y0, y1, hi));
               } else if (i < sh.s) {
                 const uint32_t w = pack_bf16(y0, y1);
                 if (c0 + j < c1) O[at(i, c0 + j)] = static_cast<uint16_t>(w);
@@ -284,25 +363,27 @@ __global__ void __launch_bounds__(kSmallThreads)
 }
 
 // The cluster's size: as many CTAs as have at least 64 columns each, while all
-// matrices' clusters run at one time; 0 where the slices do not fit or there are
-// more matrices than that.
+// matrices' clusters run at one time.  Sides up to kFineSide take this form for any
+// number of matrices, a CTA each if need be.  False where the slices do not fit.
 bool small_shape(int mats, int rows, int cols, SmallShape& sh) {
   sh.s = std::min(rows, cols);
   sh.n = std::max(rows, cols);
   if (sh.s > 128) return false;
   sh.sp = ceil_div(sh.s, 16) * 16;
   for (sh.C = kMaxCluster; sh.C >= 1; sh.C /= 2) {
-    if (static_cast<long long>(mats) * sh.C > 128 || (sh.C > 1 && sh.n < 64 * sh.C)) continue;
+    const bool wave = static_cast<long long>(mats) * sh.C <= 128 || (sh.C == 1 && sh.sp <= kFineSide);
+    if (!wave || (sh.C > 1 && sh.n < 64 * sh.C)) continue;
     sh.nc = ceil_div(ceil_div(sh.n, sh.C), 16) * 16;
-    return small_smem(sh.sp, sh.nc) <= kSmemBudget - 1024;
+    sh.fine = sh.sp <= kFineSide && small_smem(sh.sp, sh.nc, true) <= kSmemBudget - 1024;
+    return small_smem(sh.sp, sh.nc, sh.fine) <= kSmemBudget - 1024;
   }
   return false;
 }
 
-template <bool BF16>
+template <bool BF16, bool FINE>
 int launch_small(const OrthoArgs& a, const SmallShape& sh, cudaStream_t s) {
-  auto kern = ortho_small_kernel<BF16>;
-  const int smem = small_smem(sh.sp, sh.nc);
+  auto kern = ortho_small_kernel<BF16, FINE>;
+  const int smem = small_smem(sh.sp, sh.nc, FINE);
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget - 1024) != cudaSuccess ||
       cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
     return MOE_ERR_CUDA;
@@ -331,7 +412,9 @@ bool ortho_small(int mats, int rows, int cols) {
 int launch_ortho_small(const OrthoArgs& a, cudaStream_t s) {
   SmallShape sh;
   if (!small_shape(a.mats, a.rows, a.cols, sh)) return MOE_ERR_SHAPE;
-  return a.g_type == MOE_Y_BF16 ? launch_small<true>(a, sh, s) : launch_small<false>(a, sh, s);
+  const bool bf = a.g_type == MOE_Y_BF16;
+  if (sh.fine) return bf ? launch_small<true, true>(a, sh, s) : launch_small<false, true>(a, sh, s);
+  return bf ? launch_small<true, false>(a, sh, s) : launch_small<false, false>(a, sh, s);
 }
 
 }  // namespace moe

@@ -474,10 +474,11 @@ int moe_xent_bwd(int T, int V, int d, const uint16_t* x, const uint16_t* W, cons
  * are held in fp16 and X in fp16 with 8 more bits beside it, sums in fp32: O
  * differs from the formula by 0.6e-3 of its norm, by up to 1.5e-3 where one side is
  * much the longer and 2.5e-3 where the rank is a fraction of the smaller side, and
- * by its rounding to bf16, 1.7e-3.  A matrix of zeros (an expert that saw no token) gives
- * zeros; one that holds a NaN or an Inf, or whose sum of squares passes fp32's
- * range, gives NaN everywhere.  rows, cols any from 1
- * to 32768 (MOE_ERR_SHAPE otherwise).  O and G may not share memory (MOE_ERR_ARG).
+ * by its rounding to bf16, 1.7e-3.  Where the smaller side is at most 48 all three
+ * have 22 bits, as long as they fit on chip, and only that rounding is left.
+ * A matrix of zeros (an expert that saw no token) gives zeros; one that holds a NaN
+ * or an Inf, or whose sum of squares passes fp32's range, gives NaN everywhere.
+ * rows, cols any from 1 to 32768 (MOE_ERR_SHAPE otherwise).  O and G may not share memory (MOE_ERR_ARG).
  * Workspace as above: moe_orthogonalize_workspace_bytes, cleared once with
  * moe_orthogonalize_ws_init. */
 #define MOE_ORTHOGONALIZE_MAX_STEPS 16

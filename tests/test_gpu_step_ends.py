@@ -3,8 +3,7 @@ orthogonalised matrices.
 
 Tolerances, derived from the kernels' stated roundings:
   * a logit: its sum loses at most 2^-23 of S = sum |x||W| for each 16 columns of a tensor core's run, and 2^-24 of S for
-    each addition of runs; runs are held to the bound of 512 columns (they have up to 768, whose last thirds' losses
-    do not all come to half a step): dz = (2^-18 + d 2^-33) max S;
+    each addition of runs; runs have up to 768 columns and are held to the bound of 512, the stricter one: dz = (2^-18 + d 2^-33) max S;
   * lse: dz, the error of the exponentials, sum and log (2^-20 together: the exponential is within 2 + |z| ulp of terms that
     add up to the sum), and its own rounding; loss: 2 dz and the same;
   * D: relative 2 dz + 2^-20 + 2^-23 |lse| for the exponential, plus its rounding, 2^-8 in bf16 and 2^-24 as three
@@ -495,6 +494,20 @@ def test_orthogonalize_of_low_rank(mats, rows, cols, rank):
         like = U.relf(S.orthogonalize_rounded(g, 5), ref)
         assert like <= 4e-3 and U.relf(U.np64(got[i]), ref) <= 1.25 * like + 2.0 ** -12
     assert U.device_error(ws) == (0, 0)
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("mats,rows,cols", [(40, 2, 2), (40, 4, 4), (300, 8, 8), (40, 17, 16), (40, 32, 32), (3, 5, 700),
+                                            (2, 2500, 32), (1000, 31, 64), (20, 30, 1500), (1, 16, 20000), (7, 48, 600), (200, 45, 47)])
+def test_orthogonalize_small_sides_keep_two_values(mats, rows, cols, dt):
+    """Sides up to 48, many of them with a singular value near 0: X, A and the polynomial have 22 bits and their sums 24
+    (2^-21 together), so the result is off by little more than its own rounding, half a step of bf16 at most."""
+    G = (torch.randn(mats, rows, cols, generator=gen(8)) * 1e-3).to(dt)
+    got, ws = run_ortho(G)
+    assert U.device_error(ws) == (0, 0)
+    for i in range(0, mats, max(1, mats // 40)):
+        g = U.np64(G[i])
+        assert U.relf(U.np64(got[i]), S.orthogonalize(g, 5)) <= S.orthogonalize_spread(g, 5, unit=2.0 ** -21) + 2.0 ** -9
 
 
 def test_orthogonalize_offsets_past_32_bits():
