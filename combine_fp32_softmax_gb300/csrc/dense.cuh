@@ -5,9 +5,10 @@
 // tile of C for each pair, tcgen05 MMAs of the CTA group of two), CG = 1 on
 // single CTAs (128 rows x up to 256 columns), for products that would leave
 // pairs without work (dense_pick).  384 threads:
-//   warp 0      TMA producer, 64-deep K blocks through a ring of 224 KB;
-//   warp 1      issues the MMAs (warps 2 and 3 fill up their warpgroup, whose
-//               registers go to the other two);
+//   warp 0      loads A by TMA, 64-deep K blocks through a ring of 224 KB;
+//   warp 1      issues the MMAs;
+//   warp 2      loads B (warp 3 fills up the warpgroup, whose registers go to the
+//               other two);
 //   warps 4-11  epilogue: two warps for each TMEM lane quadrant, so a thread has
 //               one row and 128 of its 256 columns, all of them in registers.
 // The sums of a tile are taken out of TMEM in runs of run_kb K blocks and
@@ -23,6 +24,8 @@
 // no tail code.  Rows are padded to 64 columns in the library's own buffers;
 // the callers' have widths that are multiples of 64.
 #pragma once
+#include <type_traits>
+
 #include "gemm_tiles.cuh"
 
 namespace moe {
@@ -38,6 +41,7 @@ static_assert(kIssueRegs + 2 * kEpiRegs == 3 * kDenseRegs && kDenseRegs * kDense
 // CTAs.
 constexpr int kDenseRing = 7 * (kABytes + kBBytes / 2);
 constexpr int kDenseMaxStages = 14;
+constexpr uint64_t kDrainNs = 2000000;  // after a wait that ran out
 struct DenseState {
   uint64_t full[kDenseMaxStages], empty[kDenseMaxStages], tfull[2], tempty[2], drain;
   uint32_t tmem_base;
@@ -191,39 +195,28 @@ __device__ __forceinline__ bool mbar_wait_inline(uint64_t* bar, uint32_t parity,
   return true;
 }
 
-// One stage of loads.
-template <class Op, int CG>
-__device__ __forceinline__ void dense_loads(const typename Op::Params& p, const DenseTile& t, int kb, int b_off,
-                                            uint8_t* sA, uint8_t* sB, uint64_t* bar, int rank) {
+// A's (B's) part of a stage.
+template <class Op, int CG, bool IS_B>
+__device__ __forceinline__ void dense_load(const typename Op::Params& p, const DenseTile& t, int kb, int b_off, uint8_t* to,
+                                           uint64_t* bar, int rank) {
   int ak, am, bk, bn;
   Op::coords(p, t, kb, ak, am, bk, bn);
-  bn += b_off;
+  const int k = IS_B ? bk : ak, x = IS_B ? bn + b_off : am;
   const bool to_even = CG == 2 && rank == 1;
   const int mat = Op::ONE ? 0 : t.mat;  // ONE: a single A and B, t.mat tells results apart
-  const bool flip_a = Op::FLIP_A && dense_flip(p, kb, t.m0), flip_b = Op::FLIP_B && dense_flip(p, kb, t.n0);
-  if (Op::A_MN || flip_a) {
-    const CUtensorMap* map = flip_a ? &p.tmT : &p.tmA;
+  const bool flip = (IS_B ? Op::FLIP_B : Op::FLIP_A) && dense_flip(p, kb, IS_B ? t.n0 : t.m0);
+  const CUtensorMap* own = IS_B ? &p.tmB : &p.tmA;
+  if ((IS_B ? Op::B_MN : Op::A_MN) || flip) {
+    const CUtensorMap* map = flip ? &p.tmT : own;
     if (to_even)
-      tma_load_4d_to_even(sA, map, bar, 0, ak, am / 64, mat);
+      tma_load_4d_to_even(to, map, bar, 0, k, x / 64, mat);
     else
-      tma_load_4d(sA, map, bar, 0, ak, am / 64, mat);
+      tma_load_4d(to, map, bar, 0, k, x / 64, mat);
   } else {
     if (to_even)
-      tma_load_3d_to_even(sA, &p.tmA, bar, ak, am, mat);
+      tma_load_3d_to_even(to, own, bar, k, x, mat);
     else
-      tma_load_3d(sA, &p.tmA, bar, ak, am, mat);
-  }
-  if (Op::B_MN || flip_b) {
-    const CUtensorMap* map = flip_b ? &p.tmT : &p.tmB;
-    if (to_even)
-      tma_load_4d_to_even(sB, map, bar, 0, bk, bn / 64, mat);
-    else
-      tma_load_4d(sB, map, bar, 0, bk, bn / 64, mat);
-  } else {
-    if (to_even)
-      tma_load_3d_to_even(sB, &p.tmB, bar, bk, bn, mat);
-    else
-      tma_load_3d(sB, &p.tmB, bar, bk, bn, mat);
+      tma_load_3d(to, own, bar, k, x, mat);
   }
 }
 
@@ -293,7 +286,11 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_kernel(const __grid_co
 
   if (warp < 4) {
     regs_give<kIssueRegs>();
-    if (warp == 0 && lane == 0) {
+    // A's loads from one warp, B's from another: one thread took 365 to 590 cycles
+    // from one K block's two loads to the next, a pair's MMAs take 512 (b A + c A A of
+    // 66 x 1408 x 1408 1040 -> 845 us, dx and dW of 2000 tokens 158 -> 147 and 152 -> 137).
+    auto load = [&](auto is_b) {
+      constexpr bool IS_B = decltype(is_b)::value;
       int stage = 0;
       uint32_t phase = 0, filled = 0, fill_par = 0;
       bool ok = true;
@@ -302,28 +299,33 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_kernel(const __grid_co
         const DenseTile t = walk.next(p, i);
         const int b_off = CG == 2 ? rank * dense_mma_n<CG, Op::B_MN || Op::FLIP_B>(p, t) / 2 : 0;
         for (int kb = t.kb0; kb < t.kb1; ++kb) {
-          if (!mbar_wait(&ss.empty[stage], phase ^ 1, abort, p.err, where(0, i))) {
+          if (!mbar_wait(&ss.empty[stage], phase ^ 1, abort, p.err, where(IS_B, i))) {
             ok = false;
             break;
           }
-          uint8_t* sA = smem + stage * SB;
-          // a pair's loads are all counted on the even CTA's barrier
-          if (rank == 0) {
+          // a pair's loads are all counted on the even CTA's barrier (B's may be there
+          // before the bytes are announced: the phase waits for the announcement)
+          if (!IS_B && rank == 0) {
             mbar_arrive_expect_tx(&ss.full[stage], CG * SB);
             filled |= 1u << stage;
             fill_par = (fill_par & ~(1u << stage)) | phase << stage;
           }
-          dense_loads<Op, CG>(p, t, kb, b_off, sA, sA + p.a_bytes, &ss.full[stage], rank);
+          dense_load<Op, CG, IS_B>(p, t, kb, b_off, smem + stage * SB + (IS_B ? p.a_bytes : 0), &ss.full[stage], rank);
           if (++stage == NST) {
             stage = 0;
             phase ^= 1;
           }
         }
       }
-      if (*abort)
+      if (*abort) {
         for (int s = 0; s < NST; ++s)
           if (filled & (1u << s)) mbar_wait_drain(&ss.full[s], (fill_par >> s) & 1);
-    }
+        // copies whose bytes the other role no longer announced: long done by then
+        for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < kDrainNs;) __nanosleep(1000);
+      }
+    };
+    if (lane == 0 && warp == 0) load(std::false_type{});
+    if (lane == 0 && warp == 2) load(std::true_type{});
     __syncwarp();
     if (warp == 1 && rank == 0) {
       // The warp stays together: one lane issues by predicate, everything it needs

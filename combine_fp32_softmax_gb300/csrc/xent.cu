@@ -324,7 +324,7 @@ struct ProdOp {
   }
   static __device__ __forceinline__ void coords(const Params& p, const DenseTile& t, int kb, int& ak, int& am, int& bk,
                                                 int& bn) {
-    const int term = kb / p.once, k = (kb - term * p.once) * kBK;
+    const int term = (kb >= p.once) + (kb >= 2 * p.once), k = (kb - term * p.once) * kBK;  // three terms at most
     if constexpr (DX) {
       ak = kb * kBK;  // the terms follow one another in a row of D
       am = t.m0;
