@@ -277,6 +277,21 @@ def test_xent_pieces_of_the_vocabulary():
         assert U.device_error(ws) == (0, 0)
 
 
+@pytest.mark.parametrize("weight", [1 + 2.0 ** -8 * 0.999, 1 / 900])
+def test_xent_even_weights_add_no_common_error(weight):
+    """More tokens than D is kept in two values for, all of one weight: its rounding (half a step at worst, 2^-8) would be
+    the error of every target's entry.  The entries beside them are small (V = 6000), so both gradients are off by
+    little more than their own rounding, spread evenly up to half a step."""
+    T, V, d = 900, 6000, 64
+    x, W, target = xent_inputs(T, V, d, 0.1, sure=0.0)
+    dloss = torch.full((T,), weight)
+    loss, lse, dx, dW, ws = run_xent(x, W, target, True, dloss, None, BF16, BF16)
+    D = S.xent_grad(U.np64(x), U.np64(W), target.numpy().astype(np.int64), dloss.double().numpy(), None)
+    for got, exact in ((dx, D @ U.np64(W)), (dW, D.T @ U.np64(x))):
+        assert U.relf(U.np64(got), exact) <= 2.0 ** -8 / 3 ** 0.5
+    assert U.device_error(ws) == (0, 0)
+
+
 def test_xent_certain_tokens_keep_their_precision():
     """Targets so likely that lse and the logit agree to many digits: loss and gradient are those of the rest."""
     T, V, d = 16, 700, 256
