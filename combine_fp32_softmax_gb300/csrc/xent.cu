@@ -209,9 +209,8 @@ struct RowGrads {
   const float* units;  // what the units are near, and their mean; null: 1
   // D at the target: (g + h) p - g with p = exp(-loss), so that what is left of a
   // certain token's gradient is not the difference of two numbers near g.
-  __device__ __forceinline__ float at_target(int row, float g, float h) const {
-    const float l = -loss[row];
-    return h * expf(l) + g * expm1f(l);
+  static __device__ __forceinline__ float at_target(float loss, float g, float h) {
+    return h * expf(-loss) + g * expm1f(-loss);
   }
   static __device__ __forceinline__ float unit_near(float at, float near) {
     return at / bf16_lo(pack_bf16(at / near, 0.f));
@@ -256,7 +255,7 @@ struct GradOp {
       r.w = g + h;
       r.lse = p.lse[row];
       if (g != 0.f) {
-        r.at = p.rows.at_target(row, g, h);
+        r.at = p.rows.at_target(p.rows.loss[row], g, h);
         r.rel = target - (p.v0 + dense_col(p, t, e));
       }
       if (p.terms == 1) {
@@ -352,7 +351,7 @@ struct ProdOp {
     if (!p.unit || row >= p.M) return 1.f;
     const float g = load_target(p.rows.target, row, p.rows.V) >= 0 ? p.rows.dloss[row] : 0.f;
     const float h = p.rows.dlse ? p.rows.dlse[row] : 0.f;
-    return p.rows.unit(g != 0.f ? p.rows.at_target(row, g, h) : 0.f);
+    return p.rows.unit(g != 0.f ? p.rows.at_target(p.rows.loss[row], g, h) : 0.f);
   }
   static __device__ __forceinline__ void epilogue(const Params& p, const DenseTile& t, DenseEpi& e, float unit,
                                                   uint32_t (&acc)[4][32]) {
@@ -417,17 +416,22 @@ __device__ __forceinline__ void common_units(const RowGrads& rows, int T, float*
   constexpr int EACH = 4;
   const int n = min(T, 256 * EACH), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float at[EACH], most = 0.f;
+  float g[EACH], h[EACH], loss[EACH];  // all asked for before any is used
+  int target[EACH];
 #pragma unroll
   for (int i = 0; i < EACH; ++i) {
-    const int j = threadIdx.x + 256 * i;
-    at[i] = 0.f;
-    if (j >= n) continue;
+    const int j = min(static_cast<int>(threadIdx.x) + 256 * i, n - 1);
     const int t = static_cast<int>(static_cast<long long>(j) * T / n);
-    if (load_target(rows.target, t, rows.V) < 0) continue;
-    const float g = rows.dloss[t];
-    if (g == 0.f) continue;
-    const float v = rows.at_target(t, g, rows.dlse ? rows.dlse[t] : 0.f);
-    if (isfinite(v)) at[i] = v;
+    target[i] = load_target(rows.target, t, rows.V);
+    g[i] = rows.dloss[t];
+    h[i] = rows.dlse ? rows.dlse[t] : 0.f;
+    loss[i] = rows.loss[t];
+  }
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) {
+    const bool here = static_cast<int>(threadIdx.x) + 256 * i < n && target[i] >= 0 && g[i] != 0.f;
+    const float v = RowGrads::at_target(loss[i], g[i], h[i]);
+    at[i] = here && isfinite(v) ? v : 0.f;
     most = fmaxf(most, fabsf(at[i]));
   }
 #pragma unroll
