@@ -75,7 +75,10 @@ struct StatsOp {
   static constexpr bool A_MN = false, B_MN = false, F16 = false, ONE = true, FLIP_A = false, FLIP_B = false, CHUNKS = false;
   struct Params : DenseParams {
     Target target;
-    float2* part;  // [T][2 nt]: maximum and sum of exp of half a tile's logits
+    // [T][2 nt]: of half a tile's logits the maximum m and the sum s of exp(z - m) less
+    // 1, the largest term's: a certain token's loss, log1p(s - 1), is not what the
+    // roundings of sums near 1 leave (it was off by up to 6 2^-24 of 1)
+    float2* part;
     float* zt;     // [T] the target's logit
   };
   static __device__ __forceinline__ float flag(const Params&, int) { return 1.f; }
@@ -114,13 +117,19 @@ struct StatsOp {
     const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
     const float base = m == -INFINITY ? 0.f : m;  // nothing but -inf: the sum is 0
     float s4[4] = {0.f, 0.f, 0.f, 0.f};
+    int ones[4] = {-1, 0, 0, 0};  // terms that are 1, but for the largest
 #pragma unroll
     for (int c = 0; c < 4; ++c)
 #pragma unroll
-      for (int j = 0; j < 32; ++j) s4[j & 3] += exp_short(__uint_as_float(acc[c][j]) - base);
+      for (int j = 0; j < 32; ++j) {
+        const float v = exp_short(__uint_as_float(acc[c][j]) - base);
+        const bool one = v >= 1.f;  // not where v is NaN
+        s4[j & 3] += one ? 0.f : v;
+        ones[j & 3] += one;
+      }
     if (row < p.M)
       p.part[static_cast<size_t>(row) * (2 * p.nt) + 2 * (t.n0 / p.tn) + e.part] =
-          make_float2(m, (s4[0] + s4[1]) + (s4[2] + s4[3]));
+          make_float2(m, ((s4[0] + s4[1]) + (s4[2] + s4[3])) + ((ones[0] + ones[1]) + (ones[2] + ones[3])));
     const int rel = target - col;
     const bool here = target >= 0 && rel >= 0 && rel < min(n, 128);
     if (__any_sync(0xffffffffu, here)) {
@@ -137,12 +146,15 @@ struct StatsOp {
 
 // Joins the pairs of a row, WARPS warps a row (eight where there are few rows), the
 // pairs in a fixed order.
+// What the sum y + 1 of a pair with the maximum x adds to one with the maximum m.
+// A pair without a finite logit (y = -1) adds nothing.
+__device__ __forceinline__ float pair_adds(float2 a, float m) {
+  const float s = 1.f + a.y;
+  return s == 0.f ? 0.f : s * (a.x == m ? 1.f : expf(a.x - m));
+}
 __device__ __forceinline__ float2 join_pairs(float2 a, float2 b) {
   const float m = fmaxf(a.x, b.x);
-  // a pair without a finite logit has sum 0 and adds nothing
-  const float x = a.y == 0.f ? 0.f : a.y * (a.x == m ? 1.f : expf(a.x - m));
-  const float y = b.y == 0.f ? 0.f : b.y * (b.x == m ? 1.f : expf(b.x - m));
-  return make_float2(m, x + y);
+  return make_float2(m, a.x == m ? a.y + pair_adds(b, m) : b.y + pair_adds(a, m));
 }
 template <int WARPS>
 __global__ void __launch_bounds__(256) xent_join_kernel(const float2* __restrict__ part, const float* __restrict__ zt,
@@ -155,16 +167,21 @@ __global__ void __launch_bounds__(256) xent_join_kernel(const float2* __restrict
   const int t = WARPS == 1 ? blockIdx.x * 8 + warp : blockIdx.x;
   if (t >= T) return;
   const float2* row = part + static_cast<size_t>(t) * np;
-  float2 v = make_float2(-INFINITY, 0.f);
+  float2 v = make_float2(-INFINITY, -1.f);
   constexpr int STEP = 32 * WARPS;
   for (int i = WARPS == 1 ? lane : static_cast<int>(threadIdx.x); i < np; i += 4 * STEP) {
     float2 w[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = i + j * STEP < np ? row[i + j * STEP] : make_float2(-INFINITY, 0.f);
+    for (int j = 0; j < 4; ++j) w[j] = i + j * STEP < np ? row[i + j * STEP] : make_float2(-INFINITY, -1.f);
     const float m = fmaxf(fmaxf(fmaxf(v.x, w[0].x), fmaxf(w[1].x, w[2].x)), w[3].x);
-    float s = v.y == 0.f ? 0.f : v.y * (v.x == m ? 1.f : expf(v.x - m));
+    bool less = v.x == m;  // the largest term's 1 is out
+    float s = less ? v.y : pair_adds(v, m);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s += w[j].y == 0.f ? 0.f : w[j].y * (w[j].x == m ? 1.f : expf(w[j].x - m));
+    for (int j = 0; j < 4; ++j) {
+      const bool out = !less && w[j].x == m;
+      s += out ? w[j].y : pair_adds(w[j], m);
+      less |= out;
+    }
     v = make_float2(m, s);
   }
 #pragma unroll
@@ -180,7 +197,7 @@ __global__ void __launch_bounds__(256) xent_join_kernel(const float2* __restrict
       v = join_pairs(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, off), __shfl_xor_sync(0xffffffffu, v.y, off)));
   }
   if (lane == 0) {
-    const float ls = logf(v.y);
+    const float ls = log1pf(v.y);
     lse[t] = v.x + ls;
     const long long g = target.wide ? static_cast<const long long*>(target.p)[t] : static_cast<const int*>(target.p)[t];
     if (g >= V) record_error(err, MOE_ERR_ARG, t);

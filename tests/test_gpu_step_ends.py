@@ -292,6 +292,43 @@ def test_xent_even_weights_add_no_common_error(weight):
     assert U.device_error(ws) == (0, 0)
 
 
+def test_xent_loss_of_nearly_certain_tokens():
+    """Losses of 1e-7 to 1 keep their relative precision: s - 1 is summed without the largest term's 1.  Off by 2 dz of
+    itself for the logits, the exponentials' 2^-19 (2 + |z| ulp of small terms, |z| below 24) and 2^-24 for each of at most
+    128 additions."""
+    T, V, d = 2100, 500, 64
+    x, W, target = xent_inputs(T, V, d, sure=30.0)
+    loss, lse, ws = run_xent(x, W, target)
+    rl, _ = S.xent_fwd(U.np64(x), U.np64(W), target.numpy())
+    dz = logit_error(U.np64(x), U.np64(W))
+    some = (rl > 1e-7) & (rl < 1)
+    assert some.sum() > 500
+    assert np.all(np.abs(U.np64(loss) - rl)[some] <= ((2 * dz + 2.0 ** -19 + 2.0 ** -17) * rl)[some])
+
+
+@pytest.mark.parametrize("kind", ["none of the sample", "lse alone", "far apart", "tiny", "signs"])
+def test_xent_units_of_odd_weights(kind):
+    """D's rows are kept in units near one number that a sample of tokens sets: it may find nothing, or numbers whose
+    squares fp32 does not hold."""
+    T, V, d = 2100, 500, 64
+    x, W, target = xent_inputs(T, V, d, 0.1)
+    dloss, dlse = torch.rand(T, generator=gen(9)) + 0.5, None
+    if kind == "none of the sample":  # tokens spread evenly over all are looked at
+        target[(torch.arange(1024) * T) // 1024] = -1
+    elif kind == "lse alone":
+        dloss, dlse = torch.zeros(T), torch.randn(T, generator=gen(10))
+    elif kind == "far apart":
+        dloss *= 10.0 ** torch.randint(-25, 26, (T,), generator=gen(11)).float()
+    elif kind == "tiny":
+        dloss *= 1e-30
+    else:
+        dloss *= torch.randint(0, 2, (T,), generator=gen(11)) * 2.0 - 1.0
+    loss, lse, dx, dW, ws = run_xent(x, W, target, True, dloss, dlse, BF16, BF16)
+    dz, rs = check_fwd(x, W, target, loss, lse)
+    check_bwd(x, W, target, dloss, dlse, rs, dz, dx, dW, T, V)
+    assert U.device_error(ws) == (0, 0)
+
+
 def test_xent_certain_tokens_keep_their_precision():
     """Targets so likely that lse and the logit agree to many digits: loss and gradient are those of the rest."""
     T, V, d = 16, 700, 256
@@ -516,13 +553,46 @@ def test_orthogonalize_of_low_rank(mats, rows, cols, rank):
                                             (2, 2500, 32), (1000, 31, 64), (20, 30, 1500), (1, 16, 20000), (7, 48, 600), (200, 45, 47)])
 def test_orthogonalize_small_sides_keep_two_values(mats, rows, cols, dt):
     """Sides up to 48, many of them with a singular value near 0: X, A and the polynomial have 22 bits and their sums 24
-    (2^-21 together), so the result is off by little more than its own rounding, half a step of bf16 at most."""
+    (2^-21 together), so the result is off by little more than its own rounding: half a step of bf16 at most, 2^-8, and
+    2^-8 / sqrt(3) where it is spread evenly."""
     G = (torch.randn(mats, rows, cols, generator=gen(8)) * 1e-3).to(dt)
     got, ws = run_ortho(G)
     assert U.device_error(ws) == (0, 0)
+    errs = []
     for i in range(0, mats, max(1, mats // 40)):
         g = U.np64(G[i])
-        assert U.relf(U.np64(got[i]), S.orthogonalize(g, 5)) <= S.orthogonalize_spread(g, 5, unit=2.0 ** -21) + 2.0 ** -9
+        errs.append(U.relf(U.np64(got[i]), S.orthogonalize(g, 5)))
+        assert errs[-1] <= S.orthogonalize_spread(g, 5, unit=2.0 ** -21) + 2.0 ** -8
+    assert np.median(errs) <= 2.0 ** -8 / 3 ** 0.5
+
+
+@pytest.mark.parametrize("rows,cols", [(6, 20), (33, 40), (700, 12), (1, 5)])
+@pytest.mark.parametrize("steps", [1, 5])
+def test_orthogonalize_small_sides_scales_zeros_and_bad_matrices(rows, cols, steps):
+    base = torch.randn(rows, cols, generator=gen(4))
+    scales = [1.0, 0.0, 1e-20, 1e15, 1e-9, 1e-4, 3e-17]
+    G = torch.stack([base * s for s in scales] + [base.clone(), base.clone()])
+    G[-2, 0, 3] = float("nan")
+    G[-1, rows - 1, cols - 1] = -float("inf")
+    got, ws = run_ortho(G, steps)
+    for i, s in enumerate(scales):
+        g = U.np64(G[i])
+        if s == 0.0:
+            assert not got[i].any()
+        else:
+            assert U.relf(U.np64(got[i]), S.orthogonalize(g, steps)) <= S.orthogonalize_spread(g, steps, unit=2.0 ** -21) + 2.0 ** -8, s
+    assert got[-2:].isnan().all()
+    again, _ = run_ortho(G[2:4], steps)  # other matrices, another workspace: the same bits
+    assert torch.equal(got[2:4], again)
+    g, out = put(G), torch.empty_like(got)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moe.moe_orthogonalize(g, out, steps, ws)
+    for _ in range(2):
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got[:-2], out[:-2]) and out[-2:].isnan().all()
 
 
 def test_orthogonalize_offsets_past_32_bits():
