@@ -9,6 +9,10 @@ Tolerances, derived from the kernels' stated roundings:
   * D: relative 2 dz + 2^-20 + 2^-23 |lse| for the exponential, plus its rounding, 2^-8 in bf16 and 2^-24 as three
     bf16 values; a product of it: that part of sum |D||W|, the tensor core's loss over the K of one run (2^-23 for each 16
     terms), and the result's own rounding, 2^-8 or 2^-24."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -751,6 +755,43 @@ def test_balance_of_millions_of_tokens():
     assert np.abs(U.np64(mean_p) - rp).max() <= (4e-6 + 24 * 2.0 ** -24) * rp.max()
     assert np.allclose(U.np64(loss), rl, rtol=1e-5) and np.allclose(U.np64(zloss), rz, rtol=1e-5)
     assert U.device_error(ws) == (0, 0)
+
+
+FIRST_CALLS = """
+import torch
+from combine_fp32_softmax_gb300 import moe
+dev, bf, f = "cuda", torch.bfloat16, torch.float32
+T, V, d = 300, 700, 128
+x, W = torch.randn(T, d, device=dev).to(bf), torch.randn(V, d, device=dev).to(bf)
+t, g = torch.randint(V, (T,), device=dev), torch.ones(T, device=dev)
+loss, lse = torch.zeros(T, device=dev), torch.zeros(T, device=dev)
+dx, dW = torch.zeros(T, d, device=dev), torch.zeros(V, d, dtype=bf, device=dev)
+G = [torch.randn(2, n, 200, device=dev) for n in (40, 300)]
+O = [torch.zeros_like(m, dtype=bf) for m in G]
+xws, ows = moe.alloc_xent_workspace(T, V, d), [moe.alloc_orthogonalize_workspace(*m.shape) for m in G]
+def step():
+    moe.moe_xent_fwd(x, W, t, loss, lse, xws)
+    moe.moe_xent_bwd(x, W, t, loss, lse, g, None, dx, dW, xws)
+    for m, o, w in zip(G, O, ows):
+        moe.moe_orthogonalize(m, o, 5, w)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    step()
+graph.replay()
+torch.cuda.synchronize()
+got = [v.clone() for v in (loss, lse, dx, dW, *O)]
+step()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) and a.isfinite().all() and a.any() for a, b in zip(got, (loss, lse, dx, dW, *O)))
+print("same")
+"""
+
+
+def test_the_first_calls_of_a_process_may_be_captured():
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and r.stdout.strip() == "same", r.stderr[-2000:]
 
 
 def test_two_graphs_share_a_workspace():
