@@ -15,7 +15,7 @@
 // added up in registers, rounded to nearest: the tensor core's own fp32
 // additions cut off what a sum has no room for, and an operation whose results
 // are kept in fp32 keeps those runs short (the other accumulator fills
-// meanwhile, so this costs the tensor core nothing).  An operation whose
+// meanwhile; what it costs stands at the operations).  An operation whose
 // results are rounded to 16 bits takes one run, and may have its sums 32 columns
 // at a time (CHUNKS), which leaves it registers for what it reads beside them.
 //
