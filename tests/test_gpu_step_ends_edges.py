@@ -1,0 +1,149 @@
+"""The ends of a training step on the GPU, beside test_gpu_step_ends.py: the forms that only large products take, types that
+differ, long sums, limits that a result may not depend on.
+
+Tolerances are those of test_gpu_step_ends.py, or are derived at the test."""
+import functools
+import json
+import os
+import re
+import tempfile
+
+import numpy as np
+import pytest
+import torch
+
+from combine_fp32_softmax_gb300 import moe
+from oracle import step_oracle as S
+from tests import gpu_util as U
+from tests import test_gpu_step_ends as E
+
+pytestmark = pytest.mark.gpu
+F32, BF16, I32 = torch.float32, torch.bfloat16, torch.int32
+
+
+def profiled(fn):
+    with torch.profiler.profile(activities=[torch.profiler.ProfilerActivity.CPU, torch.profiler.ProfilerActivity.CUDA]) as p:
+        fn()
+        torch.cuda.synchronize()
+    with tempfile.TemporaryDirectory() as d:
+        path = os.path.join(d, "trace.json")
+        p.export_chrome_trace(path)
+        with open(path) as f:
+            events = json.load(f)["traceEvents"]
+    return [(e["name"], int(np.prod(e["args"]["grid"]))) for e in events if e.get("cat") == "kernel"]
+
+
+@functools.cache
+def profiler_works():
+    """The first time it is used it may see nothing."""
+    return any(profiled(lambda: torch.ones(4, device=U.DEV) + 1) for _ in range(3))
+
+
+def launches(fn):
+    """(name, CTAs) of the kernels that fn launches; None where they cannot be listed."""
+    if profiler_works():
+        return profiled(fn)
+    fn()
+    return None
+
+
+def forms(seen, op):
+    """How many CTAs share a tile in the launches of an operation of the dense products."""
+    return [int(m.group(1)) for n, _ in seen if (m := re.search(rf"dense_kernel<.*{op}, ?(?:\(int\))?([12])>", n))]
+
+
+def product(kind, number):
+    return rf"{kind}<(?:\((?:bool|int)\))?{number}>"
+
+
+DX, DW = product("ProdOp", "(?:true|1)"), product("ProdOp", "(?:false|0)")
+
+
+# ----------------------------------------------------------- cross entropy
+def check_xent(x, W, target, dloss, dlse, loss, lse, dx, dW):
+    """The bounds of test_gpu_step_ends.check_fwd and check_bwd, in fp64 on the GPU."""
+    xd, Wd, tg = x.to(U.DEV).double(), W.to(U.DEV).double(), target.to(U.DEV).long()
+    T, V, d = len(xd), len(Wd), xd.shape[1]
+    dz = (2.0 ** -18 + d * 2.0 ** -33) * (xd.abs() @ Wd.abs().t()).amax(1)
+    z = xd @ Wd.t()
+    rs = torch.logsumexp(z, 1)
+    rows = (tg >= 0).nonzero()[:, 0]
+    at = (rows, tg[rows])
+    p = z.sub_(rs[:, None]).exp_()
+    others = (p[rows].sum(1) - p[at]) if V * T < 2 ** 27 else 1 - p[at]
+    rl = torch.zeros(T, dtype=torch.float64, device=U.DEV)
+    rl[rows] = -torch.log(p[at])
+    assert ((lse.double() - rs).abs() <= dz + 2.0 ** -20 + 2.0 ** -23 * rs.abs()).all()
+    assert not loss[tg < 0].any()
+    assert ((loss.double() - rl).abs()[rows] <= (2 * dz * rl.clamp(max=1) + 2.0 ** -20 * rl + 2.0 ** -22)[rows]).all()
+    g = torch.where(tg >= 0, dloss.to(U.DEV).double(), 0.0)
+    h = torch.zeros_like(g) if dlse is None else dlse.to(U.DEV).double()
+    pt = p[at].clone()
+    D = p.mul_((g + h)[:, None])
+    D[at] = h[rows] * pt - g[rows] * others
+    rel = 2 * dz + 2.0 ** -20 + 2.0 ** -23 * rs.abs()
+    for name, got, K in (("dx", dx, V), ("dW", dW, T)):
+        if got is None:
+            continue
+        half = got.dtype == BF16
+        run = 2.0 ** -23 * (-(-K // 16)) if half else 2.0 ** -18 + 3 * K * 2.0 ** -33
+        exact = D @ Wd if name == "dx" else D.t() @ xd
+        B = D.abs().mul_((rel + (2.0 ** -8 if half else 2.0 ** -24) + run)[:, None])
+        B[at] += 2.0 ** -22 * (g.abs() + h.abs())[rows]
+        bound = (B @ Wd.abs() if name == "dx" else B.t() @ xd.abs()) + (2.0 ** -8 if half else 2.0 ** -24) * exact.abs()
+        del B
+        err = (got.double() - exact).abs()
+        assert (err <= bound + 1e-30).all(), (name, float((err / (bound + 1e-30)).max()))
+
+
+@pytest.mark.parametrize("types", [(BF16, BF16), (F32, F32), (BF16, F32), (F32, BF16)], ids=lambda t: "/".join(str(x)[6:] for x in t))
+@pytest.mark.parametrize("T,V,d", [(1300, 6000, 832), (2500, 9001, 1024)])
+def test_xent_on_cta_pairs(T, V, d, types):
+    """Logits in several runs of sums, uneven ones among them, and both products on pairs of CTAs, a ring that goes round
+    many times, ends that are no whole tiles; dx of the smaller case with its K split."""
+    x, W, target = E.xent_inputs(T, V, d, 0.2, seed=T)
+    dloss, dlse = torch.rand(T, generator=E.gen(9)) / T, torch.randn(T, generator=E.gen(10)) * 1e-5
+    out = []
+    seen = launches(lambda: out.extend(E.run_xent(x, W, target, True, dloss, dlse, *types)))
+    for op in ("StatsOp", "GradOp", DX, DW):
+        assert seen is None or set(forms(seen, op)) == {2}, (op, seen)
+    loss, lse, dx, dW, ws = out
+    check_xent(x, W, target, dloss, dlse, loss, lse, dx, dW)
+    assert U.device_error(ws) == (0, 0)
+
+
+@pytest.mark.parametrize("types", [(BF16, BF16), (F32, F32), (BF16, F32)], ids=lambda t: "/".join(str(x)[6:] for x in t))
+def test_xent_pieces_on_cta_pairs(types):
+    """More columns than a piece holds, each piece's products with a long K."""
+    T, V, d = 33000, 8449, 832
+    x, W, target = E.xent_inputs(T, V, d, 0.1)
+    dloss = torch.rand(T, generator=E.gen(9)) / T
+    out = []
+    seen = launches(lambda: out.extend(E.run_xent(x, W, target, True, dloss, None, *types)))
+    for op in ("GradOp", DX, DW):
+        assert seen is None or (len(forms(seen, op)) > 1 and 2 in forms(seen, op)), (op, seen)
+    loss, lse, dx, dW, ws = out
+    check_xent(x, W, target, dloss, None, loss, lse, dx, dW)
+    assert U.device_error(ws) == (0, 0)
+
+
+# --------------------------------------------------------- orthogonalised
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("mats,rows,cols,pairs", [
+    (22, 541, 1021, {"gram": 2, "square": 2, "update": 1}),   # halves on pairs, read by single CTAs
+    (87, 623, 580, {"gram": 2, "square": 2, "update": 1}),    # the same where the products are tall
+    (70, 1146, 636, {"gram": 2, "square": 1, "update": 2})])  # pairs store both halves for the square
+def test_orthogonalize_forms_of_its_products(mats, rows, cols, pairs, dt):
+    G = torch.empty(mats, rows, cols, device=U.DEV).normal_(0, 1e-3, generator=torch.Generator(device=U.DEV).manual_seed(1)).to(dt)
+    G[1] = 0
+    out = []
+    seen = launches(lambda: out.extend(E.run_ortho(G)))
+    tall = rows > cols
+    for name, kind in (("gram", 1 if tall else 0), ("square", 2), ("update", 4 if tall else 3)):
+        assert seen is None or set(forms(seen, product("OrthoOp", kind))) == {pairs[name]}, (name, seen)
+    got, ws = out
+    assert U.device_error(ws) == (0, 0) and not got[1].any()
+    for i in (0, mats // 2, mats - 1):
+        g = U.np64(G[i])
+        ref = S.orthogonalize(g, 5)
+        assert U.relf(U.np64(got[i]), ref) <= 1.25 * U.relf(S.orthogonalize_rounded(g, 5), ref) + 2.0 ** -12
