@@ -48,7 +48,12 @@ constexpr int kPieceCols = 8192;
 // bf16 one of up to 256 tokens, where bytes and latency count more than the
 // products: a row of a gradient is then little more than its target's term, whose
 // rounding would be as large again as the result's own (2.4e-3 of the norm against
-// 1.7e-3); one for more tokens.
+// 1.7e-3); one for more tokens.  Where only one of the two gradients is bf16 then, the
+// products of the other take three values, and its own take a fourth, D rounded in
+// units as it is alone (the first of three is no such value: dx was off by 3.1e-3 to 4.1e-3
+// of its norm).  That costs 2 bytes of D (2000 tokens of V = 32001, d = 2048, bf16 dx and
+// fp32 dW: 1025 -> 1065 us), where a second value in the product would cost another
+// 2 T V d operations.
 constexpr int kTerms = 3;
 int terms_of(int T, bool f32) { return f32 ? kTerms : T <= 256 ? 2 : 1; }
 
@@ -208,7 +213,7 @@ __global__ void __launch_bounds__(256) xent_join_kernel(const float2* __restrict
 // ------------------------------------------------------------ backward: D
 // What the backward needs of a row.
 //
-// Where D is kept in one bf16 value, a row of it is kept divided by its unit, that
+// Where D enters a product in one bf16 value, a row of it is kept divided by its unit, that
 // number which makes its target's entry, the largest as a rule, a bf16 value exactly.
 // dx, whose rows are sums over a row of D, is multiplied by it again in fp32.  dW's
 // sums have a part of every row: they are multiplied by the rows' mean unit
@@ -246,10 +251,12 @@ struct GradOp {
     const float* lse;
     int v0;             // the piece is columns [v0, v0 + N) of V; columns from V on are zeros
     int terms;          // D is the sum of so many bf16 values, each N columns further
-    uint16_t* D;        // [T, terms N]
+    int rounded;        // 1: another N columns with D in one bf16 value, divided by its unit
+    uint16_t* D;        // [T, (terms + rounded) N]
   };
   struct Pre {
     float w, lse, at;  // of exp(z - lse); log of the sum; D at the target
+    float by;          // 1 / unit
     int rel;           // the target's column among this thread's, or another number
   };
   static __device__ __forceinline__ float flag(const Params&, int) { return 1.f; }
@@ -265,7 +272,7 @@ struct GradOp {
   }
   static __device__ __forceinline__ Pre pre(const Params& p, const DenseTile& t, const DenseEpi& e) {
     const int row = t.m0 + 32 * e.q + e.lane;
-    Pre r{0.f, 0.f, 0.f, -1};
+    Pre r{0.f, 0.f, 0.f, 1.f, -1};
     if (row < p.M) {
       const int target = load_target(p.rows.target, row, p.rows.V);
       const float g = target >= 0 ? p.rows.dloss[row] : 0.f, h = p.rows.dlse ? p.rows.dlse[row] : 0.f;
@@ -279,6 +286,8 @@ struct GradOp {
         const float s = p.rows.unit(r.at);
         r.w /= s;
         r.at /= s;
+      } else if (p.rounded) {
+        r.by = 1.f / p.rows.unit(r.at);
       }
     }
     return r;
@@ -300,15 +309,24 @@ struct GradOp {
         f[j] = (r.w != 0.f && 32 * c + j < n) ? v : 0.f;
         if (32 * c + j == r.rel) f[j] = r.at;
       }
+      uint16_t* to = p.D + static_cast<size_t>(y + e.lane) * ((p.terms + p.rounded) * p.N) + col + 32 * c;
+      auto put = [&](int k, const uint32_t* w) {
+        if (y + e.lane < p.M) {
+          st_32(to + k * p.N, w);
+          st_32(to + k * p.N + 16, w + 8);
+        }
+      };
+      if (p.rounded) {
+        uint32_t w[16];
+#pragma unroll
+        for (int u = 0; u < 16; ++u) w[u] = pack_bf16(r.by * f[2 * u], r.by * f[2 * u + 1]);
+        put(p.terms, w);
+      }
       for (int k = 0;; ++k) {
         uint32_t w[16];
 #pragma unroll
         for (int u = 0; u < 16; ++u) w[u] = pack_bf16(f[2 * u], f[2 * u + 1]);
-        if (y + e.lane < p.M) {
-          uint16_t* to = p.D + static_cast<size_t>(y + e.lane) * (p.terms * p.N) + k * p.N + col + 32 * c;
-          st_32(to, w);
-          st_32(to + 16, w + 8);
-        }
+        put(k, w);
         if (k + 1 == p.terms) break;
 #pragma unroll
         for (int u = 0; u < 16; ++u) {  // what the value so far leaves, exactly
@@ -323,7 +341,7 @@ struct GradOp {
 // ----------------------------------------------- backward: products of D
 // out (+)= A . B with 16-bit or fp32 results.  DX: A = D [T, terms N], B = rows
 // [v0, ..) of W, K runs over the piece, once for each bf16 term of D.  DW: A =
-// D^T, B = x, K runs over the tokens, likewise.
+// D^T, B = x, K runs over the tokens, likewise.  Either may take one of D's values alone.
 template <bool DX>
 struct ProdOp {
   static constexpr bool A_MN = !DX, B_MN = true, F16 = false, ONE = true, FLIP_A = false, FLIP_B = false, CHUNKS = false;
@@ -331,9 +349,10 @@ struct ProdOp {
     int v0;           // DX: the piece's first column of the vocabulary
     int once;         // K blocks of one of D's bf16 terms
     int cols;         // columns of the piece: from one term of D to the next
+    int d0;           // first column in D of the first term
     int per_split;    // K blocks of a split; each has a matrix of its own in out
     RowGrads rows;    // DX; units also else
-    int unit;         // rows of D are kept divided by their units
+    int unit;         // the rows of D that it takes are divided by their units
     const float* prev;  // added to the products, laid out as out is in fp32
     void* out;        // [splits][M][N]
     int bf16;         // type of out
@@ -353,12 +372,12 @@ struct ProdOp {
                                                 int& bn) {
     const int term = (kb >= p.once) + (kb >= 2 * p.once), k = (kb - term * p.once) * kBK;  // three terms at most
     if constexpr (DX) {
-      ak = kb * kBK;  // the terms follow one another in a row of D
+      ak = p.d0 + kb * kBK;  // the terms follow one another in a row of D
       am = t.m0;
       bk = p.v0 + k;
     } else {
       ak = bk = k;
-      am = t.m0 + term * p.cols;
+      am = p.d0 + t.m0 + term * p.cols;
     }
     bn = t.n0;
   }
@@ -527,6 +546,17 @@ __global__ void __launch_bounds__(256) xent_sum_kernel(const float4* __restrict_
 // ------------------------------------------------------------------ host
 constexpr int kMaxSplits = 64;
 
+// How D enters the products: as so many bf16 values for dx and for dW, the first of so
+// many; behind these (rounded) in one value for the gradient that takes one alone.
+struct Terms {
+  int dx, dW, first, rounded;
+};
+Terms terms_for(int T, bool want_dx, bool dx_f32, bool want_dW, bool dW_f32) {
+  const int x = want_dx ? terms_of(T, dx_f32) : 1, w = want_dW ? terms_of(T, dW_f32) : 1;
+  const int first = std::max(x, w), rounded = first > 1 && ((want_dx && x == 1) || (want_dW && w == 1));
+  return {x, w, first, rounded};
+}
+
 struct Plan {
   int cols;    // most columns of a piece, a multiple of 256, counted in bf16 values of a row of D
   DenseShape dx, dW;
@@ -549,7 +579,7 @@ void logit_tiles(DenseParams& p, int T, int cols, int unit) {
 }
 int logit_cg(const DenseParams& p, int T) { return p.mt == ceil_div(T, kBM) ? 1 : 2; }
 
-Plan plan(int T, int V, int d, int backward, int terms) {
+Plan plan(int T, int V, int d, int backward, const Terms& h) {
   Plan p{};
   DenseParams tiles{};
   tiles.M = T;
@@ -557,12 +587,12 @@ Plan plan(int T, int V, int d, int backward, int terms) {
   logit_tiles(tiles, T, V, 16);
   const int all = ceil_div(V, kBN) * kBN;
   const long long want = std::max<long long>(kPieceBytes / 2 / T / kBN * kBN, kPieceCols);
-  // every term of D for the whole vocabulary at most
-  p.cols = static_cast<int>(std::min<long long>(want, 1ll * kTerms * all));
+  // every value of D for the whole vocabulary at most
+  p.cols = static_cast<int>(std::min<long long>(want, 1ll * (kTerms + 1) * all));
   if (backward) {
-    const int width = std::min(V, p.cols / terms);
-    p.dx = dense_pick(T, d, 1, terms * ceil_div(width, kBK), false, kMaxSplits);
-    p.dW = dense_pick(width, d, 1, terms * ceil_div(T, kBK), false, width == V ? kMaxSplits : 1);
+    const int width = std::min(V, p.cols / (h.first + h.rounded));
+    p.dx = dense_pick(T, d, 1, (h.rounded ? h.dx : h.first) * ceil_div(width, kBK), false, kMaxSplits);
+    p.dW = dense_pick(width, d, 1, (h.rounded ? h.dW : h.first) * ceil_div(T, kBK), false, width == V ? kMaxSplits : 1);
   }
   size_t o = 0;
   auto take = [&](size_t bytes) {
@@ -606,11 +636,14 @@ int launch_sum(const float* part, int splits, size_t n, bool bf16, void* out, cu
 }  // namespace
 
 size_t xent_workspace_bytes(int T, int V, int d, int backward) {
-  return std::max(plan(T, V, d, backward, terms_of(T, false)).total, backward ? plan(T, V, d, 1, kTerms).total : 0);
+  size_t most = 0;
+  for (int types = 0; types < (backward ? 4 : 1); ++types)  // of dx and dW; one alone takes what both of its type do
+    most = std::max(most, plan(T, V, d, backward, terms_for(T, true, types & 1, true, types & 2)).total);
+  return most;
 }
 
 int launch_xent_fwd(const XentArgs& a, cudaStream_t s) {
-  const Plan L = plan(a.T, a.V, a.d, 0, 1);
+  const Plan L = plan(a.T, a.V, a.d, 0, {});
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
   int* err = reinterpret_cast<int*>(ws + L.err);
   StatsOp::Params p;
@@ -639,18 +672,19 @@ int launch_xent_fwd(const XentArgs& a, cudaStream_t s) {
 }
 
 int launch_xent_bwd(const XentArgs& a, cudaStream_t s) {
-  const int h = std::max(a.dx ? terms_of(a.T, a.dx_type == MOE_Y_F32) : 1, a.dW ? terms_of(a.T, a.dW_type == MOE_Y_F32) : 1);
+  const Terms h = terms_for(a.T, a.dx, a.dx_type == MOE_Y_F32, a.dW, a.dW_type == MOE_Y_F32);
+  const int values = h.first + h.rounded;  // of D
   const Plan L = plan(a.T, a.V, a.d, 1, h);
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
   int* err = reinterpret_cast<int*>(ws + L.err);
   void* D = ws + L.D;
   float* accbuf = reinterpret_cast<float*>(ws + L.acc);
   uint16_t* xz = reinterpret_cast<uint16_t*>(ws + L.xz);
-  float* units = a.dW && h == 1 ? reinterpret_cast<float*>(ws + L.units) : nullptr;
+  float* units = a.dW && h.dW == 1 ? reinterpret_cast<float*>(ws + L.units) : nullptr;
   const Target target{a.target, a.target_type};
   const RowGrads rows{target, a.loss, a.dloss, a.dlse, a.V, units};
   // pieces of about equal size, whole tiles wide
-  const int most = L.cols / h / kBN * kBN;
+  const int most = L.cols / values / kBN * kBN;
   const int pieces = ceil_div(a.V, most);
   const int width = ceil_div(ceil_div(a.V, pieces), kBN) * kBN;
   int rc;
@@ -683,7 +717,8 @@ int launch_xent_bwd(const XentArgs& a, cudaStream_t s) {
       p.rows = rows;
       p.lse = a.lse;
       p.v0 = v0;
-      p.terms = h;
+      p.terms = h.first;
+      p.rounded = h.rounded;
       if ((rc = launch_logits<GradOp>(p, a, MOE_K_XENT_GRAD, s)) != MOE_OK) return rc;
     }
     if (a.dx) {
@@ -694,10 +729,11 @@ int launch_xent_bwd(const XentArgs& a, cudaStream_t s) {
       p.M = a.T;
       p.N = a.d;
       p.once = cols / kBK;
-      p.nkb = terms_of(a.T, f32) * p.once;
+      p.nkb = h.dx * p.once;
       p.run_kb = f32 ? kExactRun : p.nkb;
       p.rows = rows;
-      p.unit = h == 1;
+      p.unit = h.dx == 1;
+      p.d0 = p.unit && h.rounded ? h.first * cols : 0;
       p.code = kCodeXent + 2;
       p.err = err;
       p.v0 = v0;
@@ -712,7 +748,7 @@ int launch_xent_bwd(const XentArgs& a, cudaStream_t s) {
       p.out = splits == 1 && last ? a.dx : sums;
       p.bf16 = splits == 1 && last && !f32;
       p.apart = (reinterpret_cast<uintptr_t>(p.out) & 31) != 0;
-      if (!dense_map_k(&p.tmA, D, false, size_t(cols) * h, a.T, 1, size_t(cols) * h, 128) ||
+      if (!dense_map_k(&p.tmA, D, false, size_t(cols) * values, a.T, 1, size_t(cols) * values, 128) ||
           !dense_map_mn(&p.tmB, a.W, false, a.d, a.V, 1, p.b_bytes / kBoxBytes))
         return MOE_ERR_CUDA;
       if ((rc = dense_launch<ProdOp<true>>(L.dx.cg, p, a.grid_limit, MOE_K_XENT_DX, s)) != MOE_OK) return rc;
@@ -726,10 +762,11 @@ int launch_xent_bwd(const XentArgs& a, cudaStream_t s) {
       p.M = real;
       p.N = a.d;
       p.once = ceil_div(a.T, kBK);
-      p.nkb = terms_of(a.T, f32) * p.once;
+      p.nkb = h.dW * p.once;
       p.run_kb = f32 ? kExactRun : p.nkb;
       p.rows = rows;
-      p.unit = h == 1;
+      p.unit = h.dW == 1;
+      p.d0 = p.unit && h.rounded ? h.first * cols : 0;
       p.code = kCodeXent + 3;
       p.err = err;
       p.cols = cols;
@@ -738,7 +775,7 @@ int launch_xent_bwd(const XentArgs& a, cudaStream_t s) {
       p.bf16 = splits == 1 && !f32;
       p.out = splits > 1 ? static_cast<void*>(accbuf) : static_cast<uint8_t*>(a.dW) + size_t(v0) * a.d * (f32 ? 4 : 2);
       p.apart = (reinterpret_cast<uintptr_t>(p.out) & 31) != 0;
-      if (!dense_map_mn(&p.tmA, D, false, size_t(cols) * h, a.T, 1, 2) ||
+      if (!dense_map_mn(&p.tmA, D, false, size_t(cols) * values, a.T, 1, 2) ||
           !dense_map_mn(&p.tmB, xz, false, a.d, a.T, 1, p.b_bytes / kBoxBytes))
         return MOE_ERR_CUDA;
       if ((rc = dense_launch<ProdOp<false>>(L.dW.cg, p, a.grid_limit, MOE_K_XENT_DW, s)) != MOE_OK) return rc;
