@@ -16,8 +16,9 @@
 // additions cut off what a sum has no room for, and an operation whose results
 // are kept in fp32 keeps those runs short (the other accumulator fills
 // meanwhile; what it costs stands at the operations).  An operation whose
-// results are rounded to 16 bits takes one run, and may have its sums 32 columns
-// at a time (CHUNKS), which leaves it registers for what it reads beside them.
+// results are rounded to 16 bits takes one run or a few long ones, and with one may
+// have its sums 32 columns at a time (CHUNKS), which leaves it registers for what it
+// reads beside them.
 //
 // Matrices are seen by TMA as [matrix][row][column] with the exact number of
 // rows, so tiles that reach past an end read zeros and their stores are cut:

@@ -28,6 +28,10 @@ constexpr int kCodeXent = 0x11;  // + operation, in the error word of a wait tha
 
 // K blocks of a run of sums of fp32 gradients.
 constexpr int kExactRun = 8;
+// And of bf16 ones at most, 131,072 terms: each 16 lose up to 2^-23 of the sum, always
+// towards zero, so a run 2^-10 of its terms' magnitudes, a quarter of the result's own
+// rounding.  (2^22 tokens alike in one run: dW short by 2.0e-2 of itself.)
+constexpr int kRoundedRun = 2048;
 // K blocks of a run of a logit's sums: as even runs as there are of 12 at most.  Taking
 // out a run costs the epilogue 0.3 us, and at a tile's end two runs of the next one
 // are all that the products have room for: with runs of 4, 8, 11 and 16 of the 32
@@ -730,7 +734,7 @@ int launch_xent_bwd(const XentArgs& a, cudaStream_t s) {
       p.N = a.d;
       p.once = cols / kBK;
       p.nkb = h.dx * p.once;
-      p.run_kb = f32 ? kExactRun : p.nkb;
+      p.run_kb = f32 ? kExactRun : kRoundedRun;
       p.rows = rows;
       p.unit = h.dx == 1;
       p.d0 = p.unit && h.rounded ? h.first * cols : 0;
@@ -763,7 +767,7 @@ int launch_xent_bwd(const XentArgs& a, cudaStream_t s) {
       p.N = a.d;
       p.once = ceil_div(a.T, kBK);
       p.nkb = h.dW * p.once;
-      p.run_kb = f32 ? kExactRun : p.nkb;
+      p.run_kb = f32 ? kExactRun : kRoundedRun;
       p.rows = rows;
       p.unit = h.dW == 1;
       p.d0 = p.unit && h.rounded ? h.first * cols : 0;

@@ -455,7 +455,8 @@ int moe_xent_fwd(int T, int V, int d, const uint16_t* x, const uint16_t* W, cons
  * products as the sum of three bf16 values (24 bits) for fp32 results, whose runs
  * of sums are kept short as the logits' are, and for bf16 results, whatever the
  * other's type, as the sum of two (16 bits) up to 256 tokens and as one (2^-8 of each
- * value, beside the final rounding) beyond.  dx then still stays within its own
+ * value, beside the final rounding) beyond, in runs of 131,072 terms at most (2^-10 of
+ * the terms' magnitudes).  dx then still stays within its own
  * rounding where the target's term is the largest: rows of D are kept in units that
  * make it exact.  dW
  * takes the mean of the rows' units for each (2^-7 from a row's own at most, 2^-8

@@ -145,6 +145,31 @@ def test_xent_even_weights_with_types_that_differ(weight, types):
     assert U.device_error(ws) == (0, 0)
 
 
+def test_xent_long_sums_in_bf16():
+    """2^22 tokens, all alike, so every term of a sum has one sign and what the tensor core's additions cut off adds up.
+    What is left is the rounding of the result, half a step of bf16 at most and 2^-8 / sqrt(3) where it is spread evenly,
+    at the target (whose entry in D is exact) and that of D's entry (2^-8 at most) elsewhere; and 2^-10 for the sums, which
+    end after 131,072 terms."""
+    T, V, d = 1 << 22, 8448, 64
+    gd = torch.Generator(device=U.DEV).manual_seed(3)
+    x = torch.empty(1, d, dtype=BF16, device=U.DEV).normal_(generator=gd).expand(T, d).contiguous()
+    W = torch.empty(V, d, dtype=BF16, device=U.DEV).normal_(0, 0.05, generator=gd)
+    target = torch.full((T,), 5, dtype=I32, device=U.DEV)
+    dloss = torch.full((T,), 1.0, device=U.DEV)
+    loss, lse = (torch.empty(T, device=U.DEV) for _ in range(2))
+    dW = torch.empty_like(W)
+    ws = moe.alloc_xent_workspace(T, V, d)
+    moe.moe_xent_fwd(x, W, target, loss, lse, ws)
+    moe.moe_xent_bwd(x, W, target, loss, lse, dloss, None, None, dW, ws)
+    assert moe.moe_get_device_error(ws) == (0, 0)
+    D = torch.softmax(x[0].double() @ W.double().t(), 0)
+    D[5] -= 1.0
+    ref = T * D[:, None] * x[:1].double()
+    err = (dW.double() - ref).norm(dim=1) / ref.norm(dim=1)
+    assert err[5].item() <= 2.0 ** -8 / 3 ** 0.5 + 2.0 ** -10
+    assert err.max().item() <= 2.0 ** -8 * (1 + 1 / 3 ** 0.5) + 2.0 ** -10
+
+
 # --------------------------------------------------------- orthogonalised
 @pytest.mark.parametrize("dt", [F32, BF16])
 @pytest.mark.parametrize("mats,rows,cols,pairs", [
