@@ -234,9 +234,11 @@ struct RowGrads {
   int V;
   const float* units;  // what the units are near, and their mean; null: 1
   // D at the target: (g + h) p - g with p = exp(-loss), so that what is left of a
-  // certain token's gradient is not the difference of two numbers near g.
+  // certain token's gradient is not the difference of two numbers near g.  One fma in
+  // every kernel: a unit comes of rounding this to bf16, and where the kernels that divide
+  // and multiply by it had another last bit, a row could be off by a step of bf16.
   static __device__ __forceinline__ float at_target(float loss, float g, float h) {
-    return h * expf(-loss) + g * expm1f(-loss);
+    return __fmaf_rn(h, expf(-loss), __fmul_rn(g, expm1f(-loss)));
   }
   static __device__ __forceinline__ float unit_near(float at, float near) {
     return at / bf16_lo(pack_bf16(at / near, 0.f));

@@ -170,6 +170,34 @@ def test_xent_long_sums_in_bf16():
     assert err.max().item() <= 2.0 ** -8 * (1 + 1 / 3 ** 0.5) + 2.0 ** -10
 
 
+def test_xent_units_are_the_same_in_both_kernels():
+    """A row of D is divided by its unit in one kernel and dx multiplied by it in another.  The unit comes of a rounding
+    to bf16, so where the two differ in a last bit a whole row of dx is off by up to 2^-7; with a gradient of lse beside the
+    loss's, over enough rows that some lie near the middle of two bf16 values.  Every row: its own rounding (half a step of
+    bf16 at most) and D's, 2^-8 of each value against the row's sum of magnitudes."""
+    T, V, d = 1 << 20, 256, 64
+    gd = torch.Generator(device=U.DEV).manual_seed(4)
+    x = torch.empty(T, d, dtype=BF16, device=U.DEV).normal_(generator=gd)
+    W = torch.empty(V, d, dtype=BF16, device=U.DEV).normal_(0, 0.05, generator=gd)
+    target = torch.randint(V, (T,), generator=gd, device=U.DEV)
+    dloss = torch.rand(T, generator=gd, device=U.DEV) + 0.5
+    dlse = torch.randn(T, generator=gd, device=U.DEV) * 0.3
+    loss, lse = (torch.empty(T, device=U.DEV) for _ in range(2))
+    dx = torch.empty_like(x)
+    ws = moe.alloc_xent_workspace(T, V, d)
+    moe.moe_xent_fwd(x, W, target, loss, lse, ws)
+    moe.moe_xent_bwd(x, W, target, loss, lse, dloss, dlse, dx, None, ws)
+    Wd = W.double()
+    D = torch.softmax(x.double() @ Wd.t(), 1).mul_((dloss + dlse).double()[:, None])
+    D[torch.arange(T, device=U.DEV), target] -= dloss.double()
+    ref = D @ Wd
+    # the target's entry in D is exact: its part of the row is off by the result's rounding alone
+    D[torch.arange(T, device=U.DEV), target] = 0
+    bound = 2.0 ** -8 * ref.norm(dim=1) + (2.0 ** -8 + 1e-4) * D.abs() @ Wd.norm(dim=1) + 1e-4 * ref.norm(dim=1)
+    err = (dx.double() - ref).norm(dim=1)
+    assert (err <= bound).all(), float((err / bound).max())
+
+
 # --------------------------------------------------------- orthogonalised
 @pytest.mark.parametrize("dt", [F32, BF16])
 @pytest.mark.parametrize("mats,rows,cols,pairs", [
