@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(256)
       for (int i = threadIdx.x; i < parts; i += 32) d += sums[static_cast<size_t>(mat) * parts + i];
 #pragma unroll
       for (int off = 16; off; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
-      if (threadIdx.x == 0) shared_norm = static_cast<float>(sqrt(d));
+      if (threadIdx.x == 0) shared_norm = norm_of(d);
     }
     __syncthreads();
     const float norm = shared_norm;

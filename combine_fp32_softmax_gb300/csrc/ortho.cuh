@@ -34,6 +34,12 @@ __device__ __forceinline__ float step_scale(float scal, float grown) { return fm
 // Below this norm of X the steps are linear for all of the most there may be (kNsA^16
 // is 2^28.6): the result is a^steps X.
 constexpr float kTiny = 0x1p-80f;
+// The norm from the whole sum of squares: infinite past fp32's range.  A part of the sum
+// may leave that range only where the whole does, so what counts as infinite does not
+// depend on how the parts are shared out.
+__device__ __forceinline__ float norm_of(double squares) {
+  return squares > 0x1.fffffep127 ? INFINITY : static_cast<float>(sqrt(squares));
+}
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);

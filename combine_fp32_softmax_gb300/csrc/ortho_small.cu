@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kSmallThreads)
   cluster_sync();
   d = 0.;
   for (int r = 0; r < C; ++r) d += norms[r];
-  const float norm = static_cast<float>(sqrt(d)), inv = 1.f / (norm + kNsEps);
+  const float norm = norm_of(d), inv = 1.f / (norm + kNsEps);
   if (!(norm * inv >= kTiny) || isinf(norm)) {  // the same in every CTA of the cluster
     float f = isfinite(norm) ? inv : __uint_as_float(0x7fc00000u);
     for (int i = 0; i < steps; ++i) f *= kNsA;

@@ -218,3 +218,25 @@ def test_orthogonalize_forms_of_its_products(mats, rows, cols, pairs, dt):
         g = U.np64(G[i])
         ref = S.orthogonalize(g, 5)
         assert U.relf(U.np64(got[i]), ref) <= 1.25 * U.relf(S.orthogonalize_rounded(g, 5), ref) + 2.0 ** -12
+
+
+@pytest.mark.parametrize("rows,cols", [(6, 2000), (96, 160), (300, 200), (700, 900)])
+def test_orthogonalize_of_sums_of_squares_past_fp32(rows, cols):
+    """Whether a matrix counts as finite does not depend on how its sum of squares is shared: alone and among others."""
+    base = torch.randn(rows, cols, generator=E.gen(4))
+    top = 3.4e38 / float(base.double().square().sum())
+    over, under = base * (1.01 * top) ** 0.5, base * (0.98 * top) ** 0.5
+    G = torch.stack([over, under] + [base] * 20 + [over, under])
+    finite = {}
+    for name, m in (("under", under), ("base", base)):
+        g = U.np64(m)
+        finite[name] = (S.orthogonalize(g, 5), S.orthogonalize_spread(g, 5) + 2.0 ** -8)
+    for m in (G, G[:2], G[:1], G[1:2]):
+        got, ws = E.run_ortho(m)
+        for i in range(len(m)):
+            if torch.equal(m[i], over):
+                assert got[i].isnan().all()
+            else:
+                ref, bar = finite["under" if torch.equal(m[i], under) else "base"]
+                assert U.relf(U.np64(got[i]), ref) <= bar
+        assert U.device_error(ws) == (0, 0)
