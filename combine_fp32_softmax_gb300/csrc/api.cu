@@ -644,7 +644,7 @@ int moe_balance_fwd(const moe_cfg* cfg, const float* logits, const int32_t* topk
   const moe_cfg& c = *cfg;
   MOE_TRY_CUDA(launch_balance(logits, topk_idx, mask, c.T, seqs, c.E, c.k, counts, mean_p, loss, zloss,
                               at<int32_t>(ws, L.hist), at<float>(ws, L.base), at<float>(ws, L.partial),
-                              at<int>(ws, L.err) + kErrBalanceWord, at<int>(ws, L.err),
+                              at<int>(ws, L.err) + kErrBalanceWord, at<int>(ws, L.err), g_grid_limit,
                               static_cast<cudaStream_t>(stream)));
   return MOE_OK;
 }
@@ -659,7 +659,7 @@ int moe_balance_bwd(const moe_cfg* cfg, const float* logits, const int32_t* coun
   const size_t n = sizeof(float) * c.T * c.E;
   if (overlap(dlogits, n, logits, n) || (dlogits_in != dlogits && overlap(dlogits, n, dlogits_in, n))) return MOE_ERR_ARG;
   MOE_TRY_CUDA(launch_balance_bwd(logits, counts, mask, dloss, dzloss, c.T, seqs, c.E, c.k, dlogits_in, dlogits,
-                                  static_cast<cudaStream_t>(stream)));
+                                  g_grid_limit, static_cast<cudaStream_t>(stream)));
   return MOE_OK;
 }
 

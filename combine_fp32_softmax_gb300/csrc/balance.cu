@@ -463,6 +463,11 @@ __global__ void __launch_bounds__(kBwdThreads, 4)
   }
 }
 
+// Blocks for so much work, as many as fit, or as the caller allows.
+int blocks_of(long long work, int fit, int max_grid) {
+  return static_cast<int>(std::min<long long>(work, max_grid > 0 ? std::min(fit, max_grid) : fit));
+}
+
 template <typename F>
 cudaError_t with_layout(int E, F f) {
   if (E % 4 == 0) {  // whole 16-byte pieces
@@ -483,11 +488,11 @@ cudaError_t with_layout(int E, F f) {
 
 cudaError_t launch_balance(const float* logits, const int32_t* topk_idx, const uint8_t* mask, int T, int B, int E, int k,
                            int32_t* counts, float* mean_p, float* loss, float* zloss, int32_t* part_counts, float* part_p,
-                           float* part_zn, int* arrived, int* err, cudaStream_t s) {
+                           float* part_zn, int* arrived, int* err, int max_grid, cudaStream_t s) {
   TraceScope trace_scope(MOE_K_BALANCE, s);
   const int parts = seq_parts(T, B);
   const BalanceOut out{counts, mean_p, loss, zloss};
-  const int units = static_cast<int>(std::min<long long>(static_cast<long long>(B) * parts, num_sms() * 2));
+  const int units = blocks_of(static_cast<long long>(B) * parts, num_sms() * 2, max_grid);
   float2* zn = reinterpret_cast<float2*>(part_zn);
   int* counters = B <= kBalanceCounters ? arrived : nullptr;
   cudaError_t e = with_layout(E, [&](auto y) {
@@ -495,18 +500,18 @@ cudaError_t launch_balance(const float* logits, const int32_t* topk_idx, const u
                       parts, E, k, part_counts, part_p, zn, counters, out, err);
   });
   if (e == cudaSuccess && parts > 1 && !counters)
-    e = launch_pdl(E % 4 ? balance_join_kernel<1> : balance_join_kernel<4>, dim3(std::min(B, 65535)), dim3(kThreads), 0, s,
+    e = launch_pdl(E % 4 ? balance_join_kernel<1> : balance_join_kernel<4>, dim3(blocks_of(B, 65535, max_grid)), dim3(kThreads), 0, s,
                    part_counts, part_p, zn, B, parts, E, k, out);
   return e;
 }
 
 cudaError_t launch_balance_bwd(const float* logits, const int32_t* counts, const uint8_t* mask, const float* dloss,
                                const float* dz, int T, int B, int E, int k, const float* add, float* dlogits,
-                               cudaStream_t s) {
+                               int max_grid, cudaStream_t s) {
   TraceScope trace_scope(MOE_K_BALANCE_BWD, s);
   return with_layout(E, [&](auto y) {
     const long long warps = ceil_div(T, 32 / decltype(y)::LANES);
-    const int blocks = static_cast<int>(std::min<long long>(ceil_div(warps, kBwdThreads / 32), num_sms() * 4));
+    const int blocks = blocks_of(ceil_div(warps, kBwdThreads / 32), num_sms() * 4, max_grid);
     return launch_pdl(balance_bwd_kernel<decltype(y)>, dim3(blocks), dim3(kBwdThreads), 0, s, logits, counts, mask, dloss, dz, T,
                       T / B, E, k, add, dlogits);
   });

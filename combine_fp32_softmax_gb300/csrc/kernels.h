@@ -50,13 +50,14 @@ cudaError_t launch_route_bwd(const float* logits, const int32_t* topk_idx, const
 // Balance of the routing over B sequences of T / B tokens (balance.cu), and its
 // gradient added to `add` (which may be dlogits or null).  part_*: scratch of
 // E ceil(T / 32) ints, as many floats, and 2 ceil(T / 32) floats; arrived:
-// kBalanceCounters ints that are 0 before and after the call.
+// kBalanceCounters ints that are 0 before and after the call.  max_grid: blocks at most (0:
+// as many as fit).
 cudaError_t launch_balance(const float* logits, const int32_t* topk_idx, const uint8_t* mask, int T, int B, int E, int k,
                            int32_t* counts, float* mean_p, float* loss, float* zloss, int32_t* part_counts, float* part_p,
-                           float* part_zn, int* arrived, int* err, cudaStream_t s);
+                           float* part_zn, int* arrived, int* err, int max_grid, cudaStream_t s);
 cudaError_t launch_balance_bwd(const float* logits, const int32_t* counts, const uint8_t* mask, const float* dloss,
                                const float* dz, int T, int B, int E, int k, const float* add, float* dlogits,
-                               cudaStream_t s);
+                               int max_grid, cudaStream_t s);
 // bf16 matrices [mats][rows][cols] to 4-bit codes and group scales (q4.cuh), and back.
 cudaError_t launch_q4_quantize(const uint16_t* W, uint8_t* codes, uint16_t* scales, int mats, int rows, int cols,
                                int group, cudaStream_t s);

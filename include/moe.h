@@ -503,7 +503,9 @@ int moe_get_device_error(const void* ws, void* stream, int* code, int* info);
 int moe_num_sms(void);
 
 /* Caps the number of CTAs of the persistent kernels (grouped GEMMs, the
- * MegaKernel and the fused routing launch) at n; n <= 0 restores one CTA per SM.  Results never depend
+ * MegaKernel, the fused routing launch, the calls for a few tokens, the products of the
+ * cross entropy and of the orthogonalised matrices, which take a pair at least, and the
+ * balance loss) at n; n <= 0 restores as many as fit.  Results never depend
  * on it (each output element has one fixed producer and reduction order);
  * it exists to test exactly that.  Process-wide, not thread-safe. */
 int moe_set_grid_limit(int n);

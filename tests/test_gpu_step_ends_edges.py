@@ -240,3 +240,23 @@ def test_orthogonalize_of_sums_of_squares_past_fp32(rows, cols):
                 ref, bar = finite["under" if torch.equal(m[i], under) else "base"]
                 assert U.relf(U.np64(got[i]), ref) <= bar
         assert U.device_error(ws) == (0, 0)
+
+
+# ----------------------------------------------------------------- balance
+@pytest.mark.parametrize("T,E_,k,B,masked", [(30000, 64, 6, 2, "random"), (5000, 33, 3, 1, None), (9000, 8, 2, 3, "tail"),
+                                             (7000, 256, 8, 70, "random")])
+def test_balance_keeps_to_a_grid_limit(T, E_, k, B, masked):
+    """A block that takes several parts of one sequence, and of several, in turn: the same bits."""
+    z, idx, mask = E.balance_inputs(T, E_, k, B, masked)
+    d, add = torch.ones(B), torch.randn(T, E_, generator=E.gen(7))
+    ref = E.run_balance(z, idx, mask, B, d, d, add)
+    for limit in (1, 5):
+        out = []
+        moe.moe_set_grid_limit(limit)
+        try:
+            seen = launches(lambda: out.extend(E.run_balance(z, idx, mask, B, d, d, add)))
+        finally:
+            moe.moe_set_grid_limit(0)
+        assert all(torch.equal(a, b) for a, b in zip(ref[:5], out[:5]))
+        grids = [g for n, g in seen or () if "balance_" in n]
+        assert seen is None or (len(grids) >= 2 and max(grids) <= limit)
