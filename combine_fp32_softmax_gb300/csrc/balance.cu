@@ -36,8 +36,8 @@ constexpr int kThreads = 512, kBwdThreads = 256;
 constexpr int kUnits = 152 * 2;
 
 // Blocks of a sequence: at least 32 tokens each, so that all blocks' sums fit in
-// the E ceil(T / 32) words of the histogram regions of the workspace, and 4096 at
-// most or not much more, so that fp32 sums stay short.
+// the E ceil(T / 32) words of the histogram regions of the workspace, and below 8192
+// (4096 as a rule), so that fp32 sums stay short.
 int seq_parts(int T, int B) {
   const int L = T / B;
   const long long each = std::clamp<long long>(ceil_div(T, kUnits), 32, 4096);
@@ -77,8 +77,11 @@ __device__ __forceinline__ float lanes_reduce(float v, F f) {
   return v;
 }
 // exp(v - max) of the row in v, in place, 1 / their sum and lse; false where a
-// logit is not finite.  The instructions are what bounds a token here, so exp and
-// log are the short forms: p is off by at most 2^-21 + |z - max| 2^-23 of itself.
+// logit is not finite.  The instructions are most of a token's time here, so exp and
+// log are the short forms.  In units of 2^-22 of itself p is off by |z - max| + 1 for its
+// exponential (with the rounding of z - max), in the sum by log E + 1 (|z_j - max| weighted
+// by p_j is at most log E) and 4 for its up to 16 additions, by 1 for the quotient and less
+// for the product: |z - max| 2^-22 + 2^-18 for up to 256 experts.
 template <class Y>
 __device__ __forceinline__ bool softmax_values(float (&v)[Y::E], int E, int l, float& inv, float& lse) {
   float m = v[0], bad = 0.f;

@@ -260,3 +260,19 @@ def test_balance_keeps_to_a_grid_limit(T, E_, k, B, masked):
         assert all(torch.equal(a, b) for a, b in zip(ref[:5], out[:5]))
         grids = [g for n, g in seen or () if "balance_" in n]
         assert seen is None or (len(grids) >= 2 and max(grids) <= limit)
+
+
+@pytest.mark.parametrize("E_", [3, 8, 33, 64, 129, 256])
+@pytest.mark.parametrize("scale", [1.0, 8.0, 25.0])
+def test_balance_probabilities(E_, scale):
+    """Sequences of one token: mean_p is that token's p, to the bound that the header states."""
+    T = 512
+    z, idx, _ = E.balance_inputs(T, E_, 1, T, None, scale=scale)
+    d = torch.ones(T)
+    _, mean_p, *_, ws = E.run_balance(z, idx, None, T, d, d, None)
+    assert U.device_error(ws) == (0, 0)
+    zn = z.double().numpy()
+    p = S.softmax(zn)
+    below = zn.max(1, keepdims=True) - zn
+    # results below 2^-126 are 0
+    assert np.all(np.abs(U.np64(mean_p) - p) <= (2.0 ** -18 + below * 2.0 ** -22) * p + 2.0 ** -125)
