@@ -457,6 +457,13 @@ def _typed(name, t, dtypes, shape):
         raise ValueError(f"{name}: {tuple(shape)} of {' or '.join(map(str, dtypes))} expected, got {got}")
 
 
+def _given(**tensors):
+    """Tensors whose shape says what the others' must be."""
+    for name, t in tensors.items():
+        if t is None:
+            raise ValueError(f"{name}: a tensor expected, got None")
+
+
 def _room(ws, nbytes):
     """A workspace must have nbytes."""
     if ws is None or ws.nbytes < nbytes:
@@ -492,6 +499,7 @@ def _balance_sizes(key, B):
 def moe_balance_fwd(cfg, logits, topk_idx, mask, counts, mean_p, loss, zloss, ws, stream=None):
     """Picks and mean probabilities of each expert, counts int32 and mean_p fp32 [B, E], and the balance and z losses
     [B] of B sequences of T / B tokens; mask [T] bool (None: every token counts)."""
+    _given(loss=loss)
     B = loss.numel()
     c, nbytes, TE, Tk, BE, B_, T_ = _balance_sizes(_key(cfg), B)
     try:
@@ -516,6 +524,7 @@ def moe_balance_fwd(cfg, logits, topk_idx, mask, counts, mean_p, loss, zloss, ws
 
 def moe_balance_bwd(cfg, logits, counts, mask, dloss, dzloss, dlogits_in, dlogits, ws, stream=None):
     """dlogits [T, E] = dlogits_in (None: 0; may be dlogits) + the gradient of dloss . loss + dzloss . zloss."""
+    _given(dloss=dloss)
     B = dloss.numel()
     c, nbytes, TE, Tk, BE, B_, T_ = _balance_sizes(_key(cfg), B)
     try:
@@ -557,6 +566,7 @@ def moe_xent_ws_init(ws, stream=None):
 
 def _xent_shape(x, W, target, *rows):
     """(T, V, d, type of target) of x [T, d], W [V, d], target [T] and fp32 tensors [T]."""
+    _given(x=x, W=W)
     if x.dim() != 2 or W.dim() != 2 or x.shape[1] != W.shape[1]:
         raise ValueError(f"x [T, d] and W [V, d] expected, got {tuple(x.shape)} and {tuple(W.shape)}")
     (T, d), V = x.shape, W.shape[0]
@@ -611,6 +621,7 @@ def moe_orthogonalize_ws_init(ws, stream=None):
 def moe_orthogonalize(G, O, steps, ws, stream=None):
     """O bf16 = G (fp32 or bf16) made nearly orthogonal, each of [mats, rows, cols] matrices (or one [rows, cols]) by
     itself, in `steps` steps (5 is usual)."""
+    _given(G=G)
     if G.dim() not in (2, 3):
         raise ValueError(f"G [mats, rows, cols] or [rows, cols] expected, got {tuple(G.shape)}")
     _typed("G", G, _FLOATS, G.shape)
