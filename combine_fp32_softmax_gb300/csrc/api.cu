@@ -189,6 +189,21 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return a && b && x < y + nb && y < x + na;
 }
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+// Results of a call may share memory neither with what it reads, which is read after
+// the first of them are written, nor with one another.
+int check_apart(std::initializer_list<Span> results, std::initializer_list<Span> inputs) {
+  for (const Span* r = results.begin(); r != results.end(); ++r) {
+    for (const Span& i : inputs)
+      if (overlap(r->p, r->bytes, i.p, i.bytes)) return MOE_ERR_ARG;
+    for (const Span* o = results.begin(); o != r; ++o)
+      if (overlap(r->p, r->bytes, o->p, o->bytes)) return MOE_ERR_ARG;
+  }
+  return MOE_OK;
+}
 // Sequences of the balance loss: all of one length.
 int check_seqs(const moe_cfg& c, int seqs) { return seqs < 1 || c.T % seqs ? MOE_ERR_SHAPE : MOE_OK; }
 
@@ -642,6 +657,9 @@ int moe_balance_fwd(const moe_cfg* cfg, const float* logits, const int32_t* topk
   MOE_TRY(check_ptrs({logits, topk_idx, counts, mean_p, loss, zloss}, {mask}, ws));
   const WsLayout L = ws_layout(*cfg);
   const moe_cfg& c = *cfg;
+  const size_t T = c.T, B = seqs;
+  MOE_TRY(check_apart({{counts, 4 * B * c.E}, {mean_p, 4 * B * c.E}, {loss, 4 * B}, {zloss, 4 * B}},
+                      {{logits, 4 * T * c.E}, {topk_idx, 4 * T * c.k}, {mask, T}}));
   MOE_TRY_CUDA(launch_balance(logits, topk_idx, mask, c.T, seqs, c.E, c.k, counts, mean_p, loss, zloss,
                               at<int32_t>(ws, L.hist), at<float>(ws, L.base), at<float>(ws, L.partial),
                               at<int>(ws, L.err) + kErrBalanceWord, at<int>(ws, L.err), g_grid_limit,
@@ -656,8 +674,9 @@ int moe_balance_bwd(const moe_cfg* cfg, const float* logits, const int32_t* coun
   MOE_TRY(check_seqs(*cfg, seqs));
   MOE_TRY(check_ptrs({logits, counts, dloss, dzloss, dlogits}, {mask, dlogits_in}, ws));
   const moe_cfg& c = *cfg;
-  const size_t n = sizeof(float) * c.T * c.E;
-  if (overlap(dlogits, n, logits, n) || (dlogits_in != dlogits && overlap(dlogits, n, dlogits_in, n))) return MOE_ERR_ARG;
+  const size_t n = sizeof(float) * c.T * c.E, B = seqs;
+  MOE_TRY(check_apart({{dlogits, n}}, {{logits, n}, {counts, 4 * B * c.E}, {mask, size_t(c.T)}, {dloss, 4 * B}, {dzloss, 4 * B},
+                                       {dlogits_in != dlogits ? dlogits_in : nullptr, n}}));
   MOE_TRY_CUDA(launch_balance_bwd(logits, counts, mask, dloss, dzloss, c.T, seqs, c.E, c.k, dlogits_in, dlogits,
                                   g_grid_limit, static_cast<cudaStream_t>(stream)));
   return MOE_OK;
@@ -678,6 +697,9 @@ int moe_xent_fwd(int T, int V, int d, const uint16_t* x, const uint16_t* W, cons
   MOE_TRY(check_xent(T, V, d));
   if (target_type != MOE_I32 && target_type != MOE_I64) return MOE_ERR_ARG;
   MOE_TRY(check_ptrs({x, W, target, loss, lse}, {}, ws));
+  const size_t t = T;
+  MOE_TRY(check_apart({{loss, 4 * t}, {lse, 4 * t}},
+                      {{x, 2 * t * d}, {W, size_t(2) * V * d}, {target, t * (target_type == MOE_I64 ? 8 : 4)}}));
   XentArgs a{};
   a.T = T;
   a.V = V;
@@ -700,12 +722,10 @@ int moe_xent_bwd(int T, int V, int d, const uint16_t* x, const uint16_t* W, cons
   if ((target_type != MOE_I32 && target_type != MOE_I64) || (!dx && !dW)) return MOE_ERR_ARG;
   if ((dx && !y_type_ok(dx_type)) || (dW && !y_type_ok(dW_type))) return MOE_ERR_ARG;
   MOE_TRY(check_ptrs({x, W, target, loss, lse, dloss}, {dlse, dx, dW}, ws));
-  // x and W are read for every piece of the vocabulary, after the first results are written
-  const size_t nx = static_cast<size_t>(T) * d, nw = static_cast<size_t>(V) * d;
-  const size_t bx = nx * (dx_type == MOE_Y_F32 ? 4 : 2), bw = nw * (dW_type == MOE_Y_F32 ? 4 : 2);
-  if (overlap(dx, bx, x, 2 * nx) || overlap(dx, bx, W, 2 * nw) || overlap(dW, bw, x, 2 * nx) || overlap(dW, bw, W, 2 * nw) ||
-      overlap(dx, bx, dW, bw))
-    return MOE_ERR_ARG;
+  const size_t t = T, nx = t * d, nw = static_cast<size_t>(V) * d;
+  MOE_TRY(check_apart({{dx, nx * (dx_type == MOE_Y_F32 ? 4 : 2)}, {dW, nw * (dW_type == MOE_Y_F32 ? 4 : 2)}},
+                      {{x, 2 * nx}, {W, 2 * nw}, {target, t * (target_type == MOE_I64 ? 8 : 4)}, {loss, 4 * t}, {lse, 4 * t},
+                       {dloss, 4 * t}, {dlse, 4 * t}}));
   XentArgs a{T, V, d, x, W, target, target_type, const_cast<float*>(loss), const_cast<float*>(lse), dloss, dlse, dx, dW,
              dx_type, dW_type, ws, g_grid_limit};
   return launch_xent_bwd(a, static_cast<cudaStream_t>(stream));

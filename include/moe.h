@@ -407,7 +407,9 @@ int moe_q4_dequantize(const uint8_t* codes, const uint16_t* scales, uint16_t* W,
  * their stream.  d_model, d_ff, n_shared and renorm do not matter.  A non-finite
  * logit of a token that counts sets MOE_ERR_NONFINITE (its sequence's mean_p, loss
  * and zloss are then unspecified and its gradient 0), a pick outside [0, E)
- * MOE_ERR_ARG (it is not counted).  MOE_ERR_SHAPE unless seqs >= 1 divides T. */
+ * MOE_ERR_ARG (it is not counted, and moe_balance_bwd, which has n from the counts,
+ * then takes n for less).  No result may share memory with an input or another result
+ * (MOE_ERR_ARG).  MOE_ERR_SHAPE unless seqs >= 1 divides T. */
 int moe_balance_fwd(const moe_cfg* cfg, const float* logits, const int32_t* topk_idx, const uint8_t* mask, int seqs,
                     int32_t* counts, float* mean_p, float* loss, float* zloss, void* ws, void* stream);
 /* Its gradient for the logits, dloss and dzloss [seqs] being those of loss and
@@ -415,8 +417,8 @@ int moe_balance_fwd(const moe_cfg* cfg, const float* logits, const int32_t* topk
  *   dlogits_te = dlogits_in_te + p_te (a_e - sum_j a_j p_tj) + 2 dzloss / n lse_t p_te,
  *   a_e = dloss E c_e / (k n^2)
  * dlogits_in [T, E]: the gradient of moe_layer_bwd, to which it is added; it may be
- * dlogits itself, or NULL for none; otherwise dlogits shares no memory with it or
- * with logits (MOE_ERR_ARG).  Tokens that do not count get dlogits_in, whatever
+ * dlogits itself, or NULL for none; otherwise dlogits shares no memory with it, nor
+ * with any other input (MOE_ERR_ARG).  Tokens that do not count get dlogits_in, whatever
  * dloss and dzloss are. */
 int moe_balance_bwd(const moe_cfg* cfg, const float* logits, const int32_t* counts, const uint8_t* mask, int seqs,
                     const float* dloss, const float* dzloss, const float* dlogits_in, float* dlogits, void* ws,
@@ -432,6 +434,7 @@ int moe_balance_bwd(const moe_cfg* cfg, const float* logits, const int32_t* coun
  * are added up rounded to nearest, so that at most 2^-17.4 of the sum of the terms'
  * magnitudes is lost, and loss keeps its relative precision where a token is
  * certain: it is not formed as a difference of lse and z.  Infinite logits give NaN.
+ * loss and lse share no memory with the inputs or with each other (MOE_ERR_ARG).
  * Limits (MOE_ERR_SHAPE): 1 <= T, V <= 2^22, d a multiple of 64 up to 65536.
  * Workspace: moe_xent_workspace_bytes (0 outside the limits; backward = 0: only
  * for the forward), its first bytes cleared once with moe_xent_ws_init; it keeps
@@ -450,7 +453,7 @@ int moe_xent_fwd(int T, int V, int d, const uint16_t* x, const uint16_t* W, cons
  *   g_t = dloss_t, 0 for a token without target
  *   dx [T, d] = D W,  dW [V, d] = D^T x
  * each fp32 or bf16 (MOE_Y_F32, MOE_Y_BF16), either NULL if not wanted, neither
- * sharing memory with x, W or the other (MOE_ERR_ARG).  D is
+ * sharing memory with an input or the other (MOE_ERR_ARG).  D is
  * formed from the logits again, in pieces of the vocabulary, and enters the
  * products as the sum of three bf16 values (24 bits) for fp32 results, whose runs
  * of sums are kept short as the logits' are, and for bf16 results, whatever the
