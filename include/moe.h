@@ -433,7 +433,8 @@ int moe_balance_bwd(const moe_cfg* cfg, const float* logits, const int32_t* coun
  * sums whose tensor-core runs are 768 columns long at most (64 up to 128 tokens) and
  * are added up rounded to nearest, so that at most 2^-17.4 of the sum of the terms'
  * magnitudes is lost, and loss keeps its relative precision where a token is
- * certain: it is not formed as a difference of lse and z.  Infinite logits give NaN.
+ * certain: it is not formed as a difference of lse and z.  A logit of -Inf counts as a
+ * probability of 0; one of +Inf or NaN, or none but -Inf, give their token NaN.
  * loss and lse share no memory with the inputs or with each other (MOE_ERR_ARG).
  * Limits (MOE_ERR_SHAPE): 1 <= T, V <= 2^22, d a multiple of 64 up to 65536.
  * Workspace: moe_xent_workspace_bytes (0 outside the limits; backward = 0: only

@@ -198,6 +198,38 @@ def test_xent_units_are_the_same_in_both_kernels():
     assert (err <= bound).all(), float((err / bound).max())
 
 
+@pytest.mark.parametrize("T,V,d", [(5, 300, 64), (300, 1000, 832)])
+def test_xent_infinite_logits(T, V, d):
+    """A logit of -Inf is a probability of 0; one of +Inf, a NaN, or nothing but -Inf gives NaN to its token alone."""
+    x, W, target = E.xent_inputs(T, V, d, 0.0)
+    x[:, 0] = x[:, 0].abs() + 0.5
+    target[target == 7] = 8
+    target[1] = 7
+    W[7, 0] = -float("inf")
+    loss, lse, ws = E.run_xent(x, W, target)
+    z = U.np64(x)[:, 1:] @ U.np64(W)[:, 1:].T + U.np64(x)[:, :1] * U.np64(W)[:, 0]
+    rs = S.logsumexp(z)
+    rl = rs - z[np.arange(T), target.numpy()]
+    Wf = U.np64(W)
+    Wf[7] = 0
+    dz = E.logit_error(U.np64(x), Wf)
+    assert loss[1] == float("inf") and rl[1] == np.inf
+    rest = np.arange(T) != 1
+    assert np.all(np.abs(U.np64(lse) - rs) <= dz + 2.0 ** -20 + 2.0 ** -23 * np.abs(rs))
+    assert np.all((np.abs(U.np64(loss) - rl) <= 2 * dz + 2.0 ** -20 * rl + 2.0 ** -22)[rest])
+    assert U.device_error(ws) == (0, 0)
+    x[2, 0] = -x[2, 0]                     # its logit is +Inf
+    x[3, 5] = float("nan")
+    loss, lse, ws = E.run_xent(x, W, target)
+    bad = torch.zeros(T, dtype=torch.bool)
+    bad[2] = bad[3] = True
+    assert torch.equal(loss.isnan().cpu(), bad) and torch.equal(lse.isnan().cpu(), bad)
+    W[:, 0] = -float("inf")
+    x[2, 0] = 1.0
+    loss, lse, ws = E.run_xent(x, W, target)
+    assert loss.isnan().all() and (lse.isnan() | (lse == -float("inf"))).all()
+
+
 # --------------------------------------------------------- orthogonalised
 @pytest.mark.parametrize("dt", [F32, BF16])
 @pytest.mark.parametrize("mats,rows,cols,pairs", [
@@ -218,6 +250,24 @@ def test_orthogonalize_forms_of_its_products(mats, rows, cols, pairs, dt):
         g = U.np64(G[i])
         ref = S.orthogonalize(g, 5)
         assert U.relf(U.np64(got[i]), ref) <= 1.25 * U.relf(S.orthogonalize_rounded(g, 5), ref) + 2.0 ** -12
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("mats,rows,cols", [(300, 60, 200), (300, 200, 60), (200, 100, 300), (150, 49, 50), (140, 130, 64), (1, 40, 32768),
+                                            (3, 1, 32768), (1, 32768, 47)])
+def test_orthogonalize_small_sides_of_many_or_long_matrices(mats, rows, cols, dt):
+    """Too many of them for a cluster each, or too long for what is on chip: the products one by one, on tiles that are
+    mostly not there."""
+    G = torch.empty(mats, rows, cols, device=U.DEV).normal_(0, 1e-3, generator=torch.Generator(device=U.DEV).manual_seed(2)).to(dt)
+    if mats > 2:
+        G[1] = 0
+        G[2, 0, 0] = float("nan")
+    got, ws = E.run_ortho(G)
+    assert U.device_error(ws) == (0, 0)
+    assert mats <= 2 or (not got[1].any() and got[2].isnan().all())
+    for i in sorted({0, mats // 2, mats - 1} - ({1, 2} if mats > 2 else set())):
+        g = U.np64(G[i])
+        assert U.relf(U.np64(got[i]), S.orthogonalize(g, 5)) <= S.orthogonalize_spread(g, 5) + 2.0 ** -8
 
 
 @pytest.mark.parametrize("rows,cols", [(6, 2000), (96, 160), (300, 200), (700, 900)])
