@@ -456,18 +456,18 @@ int moe_xent_fwd(int T, int V, int d, const uint16_t* x, const uint16_t* W, cons
  * each fp32 or bf16 (MOE_Y_F32, MOE_Y_BF16), either NULL if not wanted, neither
  * sharing memory with an input or the other (MOE_ERR_ARG).  D is
  * formed from the logits again, in pieces of the vocabulary, and enters the
- * products as the sum of three bf16 values (24 bits) for fp32 results, whose runs
- * of sums are kept short as the logits' are, and for bf16 results, whatever the
- * other's type, as the sum of two (16 bits) up to 256 tokens and as one (2^-8 of each
- * value, beside the final rounding) beyond, in runs of 131,072 terms at most (2^-10 of
- * the terms' magnitudes).  dx then still stays within its own
+ * products as the sum of three bf16 values (24 bits) for fp32 results, in runs of 512
+ * terms (2^-18 of their magnitudes), and for bf16 results, whatever the other's type,
+ * as the sum of two (16 bits) up to 256 tokens and as one (2^-8 of each value, beside
+ * the final rounding) beyond, in runs of 131,072 terms at most (2^-10 of their
+ * magnitudes).  D itself is off by up to 2^-20 + |lse| 2^-23 + |z - lse| 2^-22 of each
+ * value, and by what the logits are.  With one value dx still stays within its own
  * rounding where the target's term is the largest: rows of D are kept in units that
- * make it exact.  dW
- * takes the mean of the rows' units for each (2^-7 from a row's own at most, 2^-8
- * near the largest, and the same where all tokens have one weight and small
- * probabilities).  A
- * token whose dloss and dlse are 0, or that has neither target nor dlse, adds
- * nothing, whatever x holds. */
+ * make it exact.  dW takes the mean of the rows' units for each (2^-7 from a row's own
+ * at most, 2^-8 near the largest, and the same where all tokens have one weight and
+ * small probabilities).  A token whose dloss and dlse are 0, or that has neither target
+ * nor dlse, adds nothing, whatever x holds; a dlse formed from lse is NaN where lse is,
+ * so a token that is not to count needs one that is 0. */
 int moe_xent_bwd(int T, int V, int d, const uint16_t* x, const uint16_t* W, const void* target, int target_type,
                  const float* loss, const float* lse, const float* dloss, const float* dlse, void* dx, int dx_type,
                  void* dW, int dW_type, void* ws, void* stream);
