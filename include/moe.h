@@ -401,7 +401,8 @@ int moe_q4_dequantize(const uint8_t* codes, const uint16_t* scales, uint16_t* W,
  *   zloss  [seqs]      mean of lse_t^2, lse_t = log sum_e exp(logits_te)
  * (all 0 where n = 0).  Sums are fp32 over a block's tokens, and over the blocks
  * fp32 with the roundings kept; p is off by at most 2^-18 + |z - max| 2^-22 of
- * itself (below 2^-126 of the largest it is 0).  cfg and ws are the layer's (ws cleared once with moe_ws_init); ws lends
+ * itself (below 2^-126 of the largest it is 0).  cfg and ws are the layer's (ws
+ * cleared once with moe_ws_init); ws lends
  * its histogram and partial-dot scratch, which nothing keeps from one call to the
  * next, so the calls may stand anywhere beside moe_layer_fwd and moe_layer_bwd on
  * their stream.  d_model, d_ff, n_shared and renorm do not matter.  A non-finite

@@ -230,6 +230,20 @@ def test_xent_infinite_logits(T, V, d):
     assert loss.isnan().all() and (lse.isnan() | (lse == -float("inf"))).all()
 
 
+@pytest.mark.parametrize("types", [(BF16, BF16), (F32, F32), (BF16, F32)], ids=lambda t: "/".join(str(x)[6:] for x in t))
+@pytest.mark.parametrize("T,V,d", [(3, 1 << 22, 64), (5, 300, 65536), (300, 200, 65536)])
+def test_xent_largest_sizes(T, V, d, types):
+    gd = torch.Generator(device=U.DEV).manual_seed(5)
+    W = torch.empty(V, d, dtype=BF16, device=U.DEV).normal_(0, d ** -0.5, generator=gd)
+    x = torch.empty(T, d, dtype=BF16, device=U.DEV).normal_(generator=gd)
+    target = torch.randint(V, (T,), generator=gd, device=U.DEV)
+    target[0] = V - 1
+    dloss = torch.rand(T, generator=gd, device=U.DEV)
+    loss, lse, dx, dW, ws = E.run_xent(x, W, target, True, dloss, None, *types)
+    check_xent(x, W, target, dloss, None, loss, lse, dx, dW)
+    assert U.device_error(ws) == (0, 0)
+
+
 # --------------------------------------------------------- orthogonalised
 @pytest.mark.parametrize("dt", [F32, BF16])
 @pytest.mark.parametrize("mats,rows,cols,pairs", [
@@ -266,6 +280,18 @@ def test_orthogonalize_small_sides_of_many_or_long_matrices(mats, rows, cols, dt
     assert U.device_error(ws) == (0, 0)
     assert mats <= 2 or (not got[1].any() and got[2].isnan().all())
     for i in sorted({0, mats // 2, mats - 1} - ({1, 2} if mats > 2 else set())):
+        g = U.np64(G[i])
+        assert U.relf(U.np64(got[i]), S.orthogonalize(g, 5)) <= S.orthogonalize_spread(g, 5) + 2.0 ** -8
+
+
+@pytest.mark.parametrize("rows,cols", [(4, 4), (49, 51)])
+def test_orthogonalize_most_matrices(rows, cols):
+    """More than a grid has rows."""
+    mats = 65536
+    G = torch.empty(mats, rows, cols, device=U.DEV).normal_(generator=torch.Generator(device=U.DEV).manual_seed(3))
+    got, ws = E.run_ortho(G)
+    assert U.device_error(ws) == (0, 0)
+    for i in (0, 40000, 65534, 65535):
         g = U.np64(G[i])
         assert U.relf(U.np64(got[i]), S.orthogonalize(g, 5)) <= S.orthogonalize_spread(g, 5) + 2.0 ** -8
 
@@ -310,6 +336,37 @@ def test_balance_keeps_to_a_grid_limit(T, E_, k, B, masked):
         assert all(torch.equal(a, b) for a, b in zip(ref[:5], out[:5]))
         grids = [g for n, g in seen or () if "balance_" in n]
         assert seen is None or (len(grids) >= 2 and max(grids) <= limit)
+
+
+def test_balance_counts_an_expert_picked_twice():
+    z, idx, mask = E.balance_inputs(400, 12, 3, 2, "random")
+    idx[mask, 2] = idx[mask, 0]
+    d = torch.ones(2)
+    counts, mean_p, loss, zloss, out, ws = E.run_balance(z, idx, mask, 2, d, d, None)
+    zn, idn = np.nan_to_num(z.numpy()), np.where(idx.numpy() < 12, idx.numpy(), 0)
+    rc, _, rl, _ = S.balance_fwd(zn, idn, 2, mask.numpy())
+    assert np.array_equal(counts.cpu().numpy(), rc) and np.allclose(U.np64(loss), rl, rtol=1e-5)
+    ref = S.balance_bwd(zn, idn, 2, np.ones(2), np.ones(2), None, mask.numpy())
+    assert np.allclose(U.np64(out), ref, rtol=1e-4, atol=1e-5 * np.abs(ref).max())
+    assert U.device_error(ws) == (0, 0)
+
+
+def test_balance_two_calls_at_once_on_their_own_workspaces():
+    cases = []
+    for T, E_, B, seed in ((20000, 64, 2, 1), (30000, 33, 3, 2)):
+        z, idx, mask = E.balance_inputs(T, E_, 4, B, "random", seed=seed)
+        cfg = moe.moe_cfg(T, 64, 64, E_, 4, 0, 0)
+        g = [t.to(U.DEV) for t in (z, idx, mask)]
+        d = torch.ones(B, device=U.DEV)
+        ref = E.run_balance(z, idx, mask, B, torch.ones(B), torch.ones(B), None)[:5]
+        cases.append((cfg, g, d, ref, [torch.empty_like(t) for t in ref], moe.alloc_workspace(cfg), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for cfg, (z, idx, mask), d, _, (counts, mean_p, loss, zloss, out), ws, s in cases:
+            moe.moe_balance_fwd(cfg, z, idx, mask, counts, mean_p, loss, zloss, ws, stream=s)
+            moe.moe_balance_bwd(cfg, z, counts, mask, d, d, None, out, ws, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for _, _, _, ref, got, _, _ in cases for a, b in zip(ref, got))
 
 
 @pytest.mark.parametrize("E_", [3, 8, 33, 64, 129, 256])
